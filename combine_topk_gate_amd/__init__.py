@@ -9,8 +9,8 @@ missing, loading it raises.
 
 The entry points keep the C names: ``moe_route``, ``moe_dispatch``,
 ``moe_dispatch_noalloc``, ``moe_grouped_gemm``, ``moe_combine``, ``moe_combine_ex``, ``moe_layer``,
-``moe_layer_ex`` (plus
-``moe_workspace_bytes``, ``moe_layer_default_movers``,
+``moe_layer_ex``, ``moe_layer_decode``, ``moe_adapter_linear`` (plus
+``moe_workspace_bytes``, ``moe_adapter_workspace_bytes``, ``moe_layer_default_movers``,
 ``moe_debug_device_status``, ``moe_status_string``, ``moe_abi_version``).
 """
 from __future__ import annotations
@@ -35,11 +35,15 @@ MOE_DTYPE_BF16_MXFP8 = 2
 MOE_OP_DISPATCH = 0
 MOE_OP_GROUPED_GEMM = 1
 MOE_OP_LAYER = 2
+MOE_OP_LAYER_DECODE = 3
+
+MOE_DECODE_MAX_TOKENS = 256
 
 MOE_NOALLOC_SCRATCH_BYTES = 1 << 20
 
 EXPORTED = ("moe_workspace_bytes", "moe_route", "moe_dispatch", "moe_dispatch_noalloc", "moe_grouped_gemm", "moe_combine", "moe_combine_ex",
-            "moe_layer", "moe_layer_ex", "moe_quantize_mxfp8", "moe_transpose_weights", "moe_layer_default_movers",
+            "moe_layer", "moe_layer_ex", "moe_layer_decode", "moe_adapter_linear", "moe_adapter_workspace_bytes",
+            "moe_quantize_mxfp8", "moe_transpose_weights", "moe_layer_default_movers",
             "moe_debug_device_status",
             "moe_status_string", "moe_abi_version")
 
@@ -54,6 +58,11 @@ class Problem(ctypes.Structure):
     _fields_ = [("num_tokens", ctypes.c_int64), ("hidden", ctypes.c_int32), ("ffn", ctypes.c_int32),
                 ("num_experts", ctypes.c_int32), ("topk", ctypes.c_int32), ("num_src_blocks", ctypes.c_int32),
                 ("dtype", ctypes.c_int32), ("expert_base", ctypes.c_int32), ("local_experts", ctypes.c_int32)]
+
+
+class AdapterProblem(ctypes.Structure):
+    _fields_ = [("num_tokens", ctypes.c_int64), ("in_features", ctypes.c_int32), ("out_features", ctypes.c_int32),
+                ("rank", ctypes.c_int32), ("num_adapters", ctypes.c_int32), ("dtype", ctypes.c_int32)]
 
 
 class Epilogue(ctypes.Structure):
@@ -84,6 +93,7 @@ def load_library(path: str = LIB_PATH):
     lib = ctypes.CDLL(path)
     P, I32, SZ = ctypes.c_void_p, ctypes.c_int32, ctypes.c_size_t
     PP = ctypes.POINTER(Problem)
+    PA = ctypes.POINTER(AdapterProblem)
     sig = {
         "moe_workspace_bytes": ([PP, I32], SZ),
         "moe_route": ([PP, P, P, P, P], I32),
@@ -95,6 +105,9 @@ def load_library(path: str = LIB_PATH):
         "moe_layer": ([PP, P, P, P, P, P, P, P, ctypes.POINTER(LayerAux), ctypes.POINTER(LayerOpts), P, SZ, P], I32),
         "moe_layer_ex": ([PP, P, P, P, P, P, P, ctypes.POINTER(Epilogue), P, ctypes.POINTER(LayerAux),
                           ctypes.POINTER(LayerOpts), P, SZ, P], I32),
+        "moe_layer_decode": ([PP, P, P, P, P, P, ctypes.POINTER(Epilogue), P, P, SZ, P], I32),
+        "moe_adapter_workspace_bytes": ([PA], SZ),
+        "moe_adapter_linear": ([PA, P, P, P, P, P, P, ctypes.POINTER(Epilogue), P, P, SZ, P], I32),
         "moe_quantize_mxfp8": ([ctypes.c_int64, I32, I32, P, P, P], I32),
         "moe_transpose_weights": ([ctypes.c_int64, I32, I32, I32, P, P, P], I32),
         "moe_layer_default_movers": ([PP], I32),
@@ -131,6 +144,10 @@ def mx_bytes(rows: int, cols: int) -> int:
 def problem(M, H, F, E, k, S=1, dtype="bf16", expert_base=0, local_experts=0) -> Problem:
     return Problem(int(M), int(H), int(F), int(E), int(k), int(S), _DTYPES[dtype], int(expert_base),
                    int(local_experts))
+
+
+def adapter_problem(M, H, N, rank, num_adapters, dtype="bf16") -> AdapterProblem:
+    return AdapterProblem(int(M), int(H), int(N), int(rank), int(num_adapters), _DTYPES[dtype])
 
 
 def epilogue(residual=None, out_dtype="f32") -> Epilogue:
@@ -257,6 +274,75 @@ def moe_layer_ex(p, x, logits, src_block, w_gate, w_up, w_down, epi, out, ws, au
                                        _ptr(w_up), _ptr(w_down), ctypes.byref(epi) if epi is not None else None,
                                        _ptr(out), ctypes.byref(a) if a else None, ctypes.byref(o), _ptr(ws),
                                        _nbytes(ws), _stream(stream)), "moe_layer_ex")
+
+
+def _operands(what, device, **given):
+    """Refuses (MOE_ERR_INVALID_ARGUMENT) a tensor that is not on `device` (a
+    GPU), not contiguous, or not of the shape and type the call reads.  given: name
+    = (tensor, type, shape); the tensor or a part of its shape may be None."""
+    for name, (t, dtype, shape) in given.items():
+        if t is None:
+            continue
+        if t.device != device or device.type != "cuda" or not t.is_contiguous() or t.dtype != dtype or \
+                (shape is not None and tuple(t.shape) != tuple(shape)):
+            raise MoeError(MOE_ERR_INVALID_ARGUMENT,
+                           f"{what}: {name} must be a contiguous {dtype} tensor of shape {shape} on {device}, "
+                           f"got {t.dtype} {tuple(t.shape)} strides {t.stride()} on {t.device}")
+
+
+def _call_on(x, stream, call):
+    """call(stream) with x's device current: a stream given is used as it is,
+    otherwise torch's current stream of that device."""
+    import torch
+    with torch.cuda.device(x.device):
+        return call(_stream(stream))
+
+
+def _epilogue_types(epi):
+    import torch
+    return torch.bfloat16 if epi is not None and epi.out_dtype == MOE_DTYPE_BF16 else torch.float32
+
+
+def moe_layer_decode(p, x, logits, w_gate, w_up, w_down, epi, out, ws, stream=None):
+    """The layer for at most MOE_DECODE_MAX_TOKENS tokens (a decode step): out
+    [M, H] of x [M, H] and logits [M, E] (-inf: an expert the token may not
+    choose; an all -inf row is idle), epi as in moe_layer_ex or None, ws
+    moe_workspace_bytes(p, MOE_OP_LAYER_DECODE) bytes."""
+    import torch
+    M, H, F, EL = p.num_tokens, p.hidden, p.ffn, p.local_experts or p.num_experts
+    act = torch.float32 if p.dtype == MOE_DTYPE_F32 else torch.bfloat16
+    mx = p.dtype == MOE_DTYPE_BF16_MXFP8
+    _operands("moe_layer_decode", x.device, x=(x, act, (M, H)), logits=(logits, torch.float32, (M, p.num_experts)),
+              w_gate=(w_gate, act, (EL, F, H)), w_up=(w_up, act, (EL, F, H)),
+              w_down=(w_down, torch.uint8, (mx_bytes(EL * H, F),)) if mx else (w_down, act, (EL, H, F)),
+              out=(out, _epilogue_types(epi), (M, H)), ws=(ws, torch.uint8, None))
+    lib = load_library()
+    _check(_call_on(x, stream, lambda s: lib.moe_layer_decode(
+        ctypes.byref(p), _ptr(x), _ptr(logits), _ptr(w_gate), _ptr(w_up), _ptr(w_down),
+        ctypes.byref(epi) if epi is not None else None, _ptr(out), _ptr(ws), _nbytes(ws), s)), "moe_layer_decode")
+
+
+def moe_adapter_workspace_bytes(q: AdapterProblem) -> int:
+    return load_library().moe_adapter_workspace_bytes(ctypes.byref(q))
+
+
+def moe_adapter_linear(q, x, w, a, b, scale, adapter_idx, epi, out, ws, stream=None):
+    """out[m] = x[m] W^T + scale[a] (x[m] A[a]^T) B[a]^T (+ residual) with a =
+    adapter_idx[m] (-1: none): x [M, H], w [N, H], a [P, rank, H], b [P, N,
+    rank], scale [P] f32, adapter_idx [M] int32, out [M, N]; epi as in
+    moe_combine_ex or None; ws moe_adapter_workspace_bytes(q) bytes.  With
+    num_adapters 0: a, b, scale, adapter_idx and ws may be None."""
+    import torch
+    M, H, N, r, P = q.num_tokens, q.in_features, q.out_features, q.rank, q.num_adapters
+    act = torch.float32 if q.dtype == MOE_DTYPE_F32 else torch.bfloat16
+    _operands("moe_adapter_linear", x.device, x=(x, act, (M, H)), w=(w, act, (N, H)), a=(a, act, (P, r, H)),
+              b=(b, act, (P, N, r)), scale=(scale, torch.float32, (P,)),
+              adapter_idx=(adapter_idx, torch.int32, (M,)), out=(out, _epilogue_types(epi), (M, N)),
+              ws=(ws, torch.uint8, None))
+    lib = load_library()
+    _check(_call_on(x, stream, lambda s: lib.moe_adapter_linear(
+        ctypes.byref(q), _ptr(x), _ptr(w), _ptr(a), _ptr(b), _ptr(scale), _ptr(adapter_idx),
+        ctypes.byref(epi) if epi is not None else None, _ptr(out), _ptr(ws), _nbytes(ws), s)), "moe_adapter_linear")
 
 
 def moe_debug_device_status(p, ws, stream=None) -> int:

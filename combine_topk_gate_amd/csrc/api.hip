@@ -5,6 +5,7 @@
 #include <stdlib.h>
 #include <string.h>
 
+#include <exception>
 #include <vector>
 
 #include "common.hpp"
@@ -124,7 +125,11 @@ uint32_t debug_shuffle() {
 
 template <typename T>
 bool fetch(std::vector<T>& h, const T* d, int64_t n, hipStream_t s) {
-  h.resize(n > 0 ? (size_t)n : 0);
+  try {
+    h.resize(n > 0 ? (size_t)n : 0);
+  } catch (const std::exception&) {  // no host memory for the copy: no exception leaves the C ABI
+    return false;
+  }
   if (n <= 0) return true;
   if (hipMemcpyAsync(h.data(), d, (size_t)n * sizeof(T), hipMemcpyDeviceToHost, s) != hipSuccess) return false;
   return hipStreamSynchronize(s) == hipSuccess;
@@ -223,6 +228,71 @@ LayerWs layer_ws(const moe_problem_t* p) {
   return w;
 }
 
+// ------------------------------------------------------- decode layer ----
+// bf16 planes of h (0: f32): three hold the f32 value exactly, two hold it
+// to 2^-17, for a bf16 output.
+int decode_planes(const moe_problem_t* p, const OutEpilogue& ep) {
+  return p->dtype == MOE_DTYPE_F32 ? 0 : ep.out_bf16 ? 2 : 3;
+}
+
+struct DecodeWs {
+  size_t hdr, entries, list, f2s, w, hact, y, total;
+};
+
+// The workspace does not depend on the output's type (three planes).
+DecodeWs decode_ws(const moe_problem_t* p) {
+  const int M = (int)p->num_tokens, R = M * p->topk;
+  DecodeWs w;
+  size_t o = 0;
+  w.hdr = o; o += align_up(16);
+  w.entries = o; o += align_up(16 * (size_t)decode_max_entries(M, p->topk, held(p), is_mx(p)));
+  w.list = o; o += align_up((size_t)R * 4);
+  w.f2s = o; o += align_up((size_t)R * 4);
+  w.w = o; o += align_up((size_t)R * 4);
+  w.hact = o; o += align_up((size_t)R * p->ffn * (p->dtype == MOE_DTYPE_F32 ? 4 : 6));
+  w.y = o; o += align_up((size_t)R * p->hidden * 4);
+  w.total = o;
+  return w;
+}
+
+moe_status_t check_decode(const moe_problem_t* p) {
+  const moe_status_t st = check_problem(p);
+  if (st != MOE_OK) return st;
+  return p->num_tokens > MOE_DECODE_MAX_TOKENS ? MOE_ERR_UNSUPPORTED : MOE_OK;
+}
+
+bool overlap(const void* a, size_t na, const void* b, size_t nb) {
+  const uintptr_t x = (uintptr_t)a, y = (uintptr_t)b;
+  return a && b && na && nb && x < y + nb && y < x + na;
+}
+
+// out may be the residual itself (same place, same type: every element is
+// read by the thread that writes it); any other overlap is an error.
+bool residual_clash(const OutEpilogue& ep, int64_t n) {
+  if (!ep.residual) return false;
+  const size_t nr = (size_t)n * (ep.res_bf16 ? 2 : 4), no = (size_t)n * (ep.out_bf16 ? 2 : 4);
+  if (ep.residual == ep.out && nr == no) return false;
+  return overlap(ep.residual, nr, ep.out, no);
+}
+
+// ------------------------------------------------- adapter projection ----
+moe_status_t check_adapter(const moe_adapter_problem_t* q) {
+  if (!q) return MOE_ERR_INVALID_ARGUMENT;
+  if (q->num_tokens < 0) return MOE_ERR_INVALID_ARGUMENT;
+  if (q->in_features < 64 || q->in_features > 65536 || q->in_features % 64) return MOE_ERR_INVALID_ARGUMENT;
+  if (q->out_features < 1 || q->out_features > 65536) return MOE_ERR_INVALID_ARGUMENT;
+  if (q->num_adapters < 0 || q->num_adapters > 65536) return MOE_ERR_INVALID_ARGUMENT;
+  if (q->num_adapters > 0 && (q->rank < 8 || q->rank > 256 || q->rank % 8)) return MOE_ERR_INVALID_ARGUMENT;
+  if (q->dtype != MOE_DTYPE_F32 && q->dtype != MOE_DTYPE_BF16)
+    return q->dtype == MOE_DTYPE_BF16_MXFP8 ? MOE_ERR_UNSUPPORTED : MOE_ERR_INVALID_ARGUMENT;
+  if (q->num_tokens >= (1ll << 31)) return MOE_ERR_UNSUPPORTED;
+  return MOE_OK;
+}
+
+size_t adapter_ws(const moe_adapter_problem_t* q) {
+  return q->num_adapters > 0 ? align_up((size_t)q->num_tokens * q->rank * 4) : 0;
+}
+
 template <typename T>
 T* at(void* ws, size_t off) {
   return reinterpret_cast<T*>(reinterpret_cast<char*>(ws) + off);
@@ -232,7 +302,7 @@ T* at(void* ws, size_t off) {
 
 extern "C" {
 
-int32_t moe_abi_version(void) { return (2 << 16) | 0; }
+int32_t moe_abi_version(void) { return (2 << 16) | 1; }
 
 const char* moe_status_string(moe_status_t s) {
   switch (s) {
@@ -252,6 +322,7 @@ size_t moe_workspace_bytes(const moe_problem_t* p, int32_t op) {
     case MOE_OP_DISPATCH: return permute_ws_bytes(plan_of(p));
     case MOE_OP_GROUPED_GEMM: return p->dtype == MOE_DTYPE_BF16 ? gemm_split_ws_bytes() : 0;
     case MOE_OP_LAYER: return layer_ws(p).total;
+    case MOE_OP_LAYER_DECODE: return check_decode(p) == MOE_OK ? decode_ws(p).total : 0;
   }
   return 0;
 }
@@ -514,6 +585,116 @@ moe_status_t moe_layer(const moe_problem_t* p, const void* x, const float* logit
                        const moe_layer_aux_t* aux, const moe_layer_opts_t* opts, void* ws, size_t ws_bytes,
                        void* stream) {
   return moe_layer_ex(p, x, logits, src_block, w_gate, w_up, w_down, nullptr, out, aux, opts, ws, ws_bytes, stream);
+}
+
+moe_status_t moe_layer_decode(const moe_problem_t* p, const void* x, const float* logits, const void* w_gate,
+                              const void* w_up, const void* w_down, const moe_epilogue_t* epi, void* out, void* ws,
+                              size_t ws_bytes, void* stream) {
+  moe_status_t st = check_decode(p);
+  if (st != MOE_OK) return st;
+  if (!w_gate || !w_up || !w_down) return MOE_ERR_INVALID_ARGUMENT;
+  if (!aligned(w_gate, 16) || !aligned(w_up, 16) || !aligned(w_down, 16)) return MOE_ERR_INVALID_ARGUMENT;
+  OutEpilogue ep;
+  st = epilogue_of(p, epi, out, &ep);
+  if (st != MOE_OK) return st;
+  if (p->num_tokens == 0) return MOE_OK;
+  if (!x || !logits || !out) return MOE_ERR_INVALID_ARGUMENT;
+  if (!aligned(x, 16) || !aligned(logits, 4)) return MOE_ERR_INVALID_ARGUMENT;
+  const int64_t n = p->num_tokens * p->hidden;
+  const DecodeWs L = decode_ws(p);
+  if (!ws || ws_bytes < L.total) return MOE_ERR_WORKSPACE_TOO_SMALL;
+  if (!aligned(ws, kAlign)) return MOE_ERR_INVALID_ARGUMENT;
+  const size_t nout = (size_t)n * (ep.out_bf16 ? 2 : 4);
+  if (overlap(out, nout, x, (size_t)n * elem_bytes(p)) || overlap(out, nout, ws, L.total) || residual_clash(ep, n) ||
+      overlap(out, nout, logits, (size_t)p->num_tokens * p->num_experts * 4))
+    return MOE_ERR_INVALID_ARGUMENT;
+  hipStream_t s = (hipStream_t)stream;
+  if (debug_validate()) {
+    // -inf is an expert the token may not choose; NaN and +inf are errors
+    std::vector<float> h;
+    if (!fetch(h, logits, p->num_tokens * (int64_t)p->num_experts, s)) return MOE_ERR_HIP;
+    for (float v : h)
+      if (!(v < INFINITY)) return MOE_ERR_INVALID_ARGUMENT;
+  }
+  const bool mx = is_mx(p);
+  const int planes = decode_planes(p, ep);
+  DecodeArgs a;
+  a.plan.M = (int)p->num_tokens;
+  a.plan.k = p->topk;
+  a.plan.E = p->num_experts;
+  a.plan.EL = held(p);
+  a.plan.base = held_base(p);
+  a.plan.rows = decode_entry_rows(a.plan.M, mx);
+  a.plan.hdr = at<int32_t>(ws, L.hdr);
+  a.plan.entries = at<int4>(ws, L.entries);
+  a.plan.list = at<int32_t>(ws, L.list);
+  a.plan.f2s = at<int32_t>(ws, L.f2s);
+  a.plan.w = at<float>(ws, L.w);
+  a.x = x;
+  a.w_gate = w_gate;
+  a.w_up = w_up;
+  a.w_down = w_down;
+  a.wd_scale = mx ? reinterpret_cast<const uint8_t*>(w_down) + (int64_t)held(p) * p->hidden * p->ffn : nullptr;
+  a.hact = at<void>(ws, L.hact);
+  a.y = at<float>(ws, L.y);
+  a.H = p->hidden;
+  a.F = p->ffn;
+  a.x_pitch = (uint32_t)(p->hidden * elem_bytes(p));
+  a.h_pitch = (uint32_t)p->ffn * (planes ? 2u * planes : 4u);
+  a.wd_pitch = (uint32_t)p->ffn * (mx ? 1u : (uint32_t)elem_bytes(p));
+  return hip_status(launch_decode(a, logits, p->dtype, planes, ep, s));
+}
+
+size_t moe_adapter_workspace_bytes(const moe_adapter_problem_t* q) {
+  return check_adapter(q) == MOE_OK ? adapter_ws(q) : 0;
+}
+
+moe_status_t moe_adapter_linear(const moe_adapter_problem_t* q, const void* x, const void* w, const void* a,
+                                const void* b, const float* scale, const int32_t* adapter_idx,
+                                const moe_epilogue_t* epi, void* out, void* ws, size_t ws_bytes, void* stream) {
+  const moe_status_t st = check_adapter(q);
+  if (st != MOE_OK) return st;
+  const bool f32 = q->dtype == MOE_DTYPE_F32;
+  const size_t eb = f32 ? 4 : 2;
+  AdapterArgs g;
+  g.M = q->num_tokens;
+  g.H = q->in_features;
+  g.N = q->out_features;
+  g.P = q->num_adapters;
+  g.r = g.P > 0 ? q->rank : 0;
+  g.out.out = out;
+  g.out.residual = epi ? epi->residual : nullptr;
+  g.out.res_bf16 = !f32;
+  g.out.out_bf16 = epi && epi->out_dtype == MOE_DTYPE_BF16;
+  if (epi && epi->out_dtype != MOE_DTYPE_F32 && epi->out_dtype != MOE_DTYPE_BF16) return MOE_ERR_INVALID_ARGUMENT;
+  if (!w || (g.P > 0 && (!a || !b || !scale))) return MOE_ERR_INVALID_ARGUMENT;
+  if (!aligned(x, 16) || !aligned(w, 16) || !aligned(a, 16) || !aligned(b, 16) || !aligned(out, 16) ||
+      !aligned(g.out.residual, 16) || !aligned(scale, 4) || !aligned(adapter_idx, 4))
+    return MOE_ERR_INVALID_ARGUMENT;
+  if (g.M == 0) return MOE_OK;
+  if (!x || !out || (g.P > 0 && !adapter_idx)) return MOE_ERR_INVALID_ARGUMENT;
+  const size_t need = adapter_ws(q);
+  if (need > 0) {
+    if (!ws || ws_bytes < need) return MOE_ERR_WORKSPACE_TOO_SMALL;
+    if (!aligned(ws, kAlign)) return MOE_ERR_INVALID_ARGUMENT;
+  }
+  const size_t nout = (size_t)g.M * g.N * (g.out.out_bf16 ? 2 : 4);
+  if (overlap(out, nout, x, (size_t)g.M * g.H * eb) || overlap(out, nout, w, (size_t)g.N * g.H * eb) ||
+      (need > 0 && overlap(out, nout, ws, need)) || residual_clash(g.out, g.M * g.N))
+    return MOE_ERR_INVALID_ARGUMENT;
+  if (debug_validate() && g.P > 0) {
+    const moe_status_t sv = check_range(adapter_idx, g.M, -1, g.P, (hipStream_t)stream);
+    if (sv != MOE_OK) return sv;
+  }
+  g.x = x;
+  g.w = w;
+  g.a = a;
+  g.b = b;
+  g.scale = scale;
+  g.idx = adapter_idx;
+  g.t = need > 0 ? at<float>(ws, 0) : nullptr;
+  g.row_bytes = (uint32_t)(g.H * eb);
+  return hip_status(launch_adapter_linear(g, f32, (hipStream_t)stream));
 }
 
 moe_status_t moe_quantize_mxfp8(int64_t rows, int32_t cols, int32_t src_dtype, const void* src, void* dst,

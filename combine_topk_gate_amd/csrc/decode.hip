@@ -1,0 +1,296 @@
+// The MoE layer for a few tokens (a decode step): moe_layer_decode.
+//
+// The same layer as the kernel chain (COMET paper review §3.2: Layer0 = gate
+// and up products with SwiGLU, Layer1 = down product; §4.1.1: the Top-K
+// reduction), for at most MOE_DECODE_MAX_TOKENS tokens:
+//   h[t,j,f] = silu(x[t].Wg[e,f]) * (x[t].Wu[e,f])         e = expert j of token t
+//   out[t,n] = cast(sum_j w[t,j] (h[t,j].Wd[e,n]) + residual[t,n])
+// What bounds it is reading the chosen experts' weights once from HBM (3 H F
+// elements an expert; with r rows an expert there are r multiply-adds per
+// weight, and the matrix cores only catch up with HBM at about 150 rows).
+// So nothing is dispatched: a plan kernel routes and lists each held
+// expert's pairs, and the two product kernels stream weight rows past the
+// listed token rows (stream.hpp), reading x through the list.
+//
+// h is not rounded to the layer's type between the products as in the chain
+// (there it halves the traffic of R x F values; here R is small): it is kept
+// in f32, for bf16 weights as bf16 planes whose sum is the f32 value (three,
+// exact, for an f32 output; two, 2^-17 of the value, for a bf16 output, whose
+// own rounding is 2^-9).
+#include "common.hpp"
+#include "launch.hpp"
+#include "stream.hpp"
+#include "topk.hpp"
+
+namespace moe {
+
+constexpr int kPlanThreads = 1024;
+constexpr int kPlanMaxPairs = 256 * 16;
+constexpr int kPlanMaxExperts = 512;
+
+// ------------------------------------------------------------------ plan ---
+// One workgroup: the tokens' experts and weights, and per held expert the
+// list of its pairs f = t k + j, cut into entries of at most `rows` rows.
+// (Which place of an expert's list a pair gets is decided by an LDS atomic;
+// a row's result does not depend on its place.)
+template <int KMAX>
+__global__ __launch_bounds__(kPlanThreads) void decode_plan_kernel(const float* __restrict__ logits, DecodePlan p) {
+  __shared__ int cnt[kPlanMaxExperts], scan[kPlanMaxExperts], cur[kPlanMaxExperts];
+  __shared__ short slot[kPlanMaxPairs];
+  const int tid = threadIdx.x;
+  for (int e = tid; e < p.EL; e += kPlanThreads) cnt[e] = 0;
+  __syncthreads();
+  const int q = tid % kLanesPerToken;
+  for (int t0 = 0; t0 < p.M; t0 += kPlanThreads / kLanesPerToken) {
+    const int t = t0 + tid / kLanesPerToken;
+    const bool valid = t < p.M;
+    float vals[KMAX];
+    int ids[KMAX];
+    topk_row<KMAX>(logits + (int64_t)(valid ? t : 0) * p.E, p.E, q, valid, vals, ids);
+    if (!valid) continue;
+    // softmax over the chosen logits, shifted by the largest, summed in slot
+    // order; a place left over (fewer than k logits above -inf) has weight 0
+    // and belongs to no expert
+    const float l0 = vals[0];
+    float denom = 0.0f;
+#pragma unroll
+    for (int j = 0; j < KMAX; ++j)
+      if (j < p.k && ids[j] < p.E) denom += expf(vals[j] - l0);
+#pragma unroll
+    for (int j = 0; j < KMAX; ++j) {
+      if (j < p.k && j == q) {
+        const int f = t * p.k + j;
+        const bool chosen = ids[j] < p.E;
+        int e = chosen ? ids[j] - p.base : -1;
+        if (e >= p.EL) e = -1;
+        p.w[f] = chosen ? expf(vals[j] - l0) / denom : 0.0f;
+        p.f2s[f] = e >= 0 ? f : -1;
+        slot[f] = (short)e;
+        if (e >= 0) atomicAdd(&cnt[e], 1);
+      }
+    }
+  }
+  __syncthreads();
+  // exclusive prefix over the experts of (pairs, entries), 16 bits each
+  const int rows = p.rows;
+  int c = 0, mine = 0;
+  if (tid < p.EL) {
+    c = cnt[tid];
+    mine = c | (((c + rows - 1) / rows) << 16);
+    scan[tid] = mine;
+  }
+  __syncthreads();
+  for (int off = 1; off < p.EL; off <<= 1) {
+    const int v = tid >= off && tid < p.EL ? scan[tid - off] : 0;
+    __syncthreads();
+    if (tid < p.EL) scan[tid] += v;
+    __syncthreads();
+  }
+  if (tid < p.EL) {
+    const int ex = scan[tid] - mine;
+    const int start = ex & 0xFFFF, entry = ex >> 16;
+    cur[tid] = start;
+    for (int b = 0; b * rows < c; ++b) {
+      int4 v;
+      v.x = tid;
+      v.y = start + b * rows;
+      v.z = min(rows, c - b * rows);
+      v.w = 0;
+      p.entries[entry + b] = v;
+    }
+  }
+  if (tid == 0) p.hdr[0] = scan[p.EL - 1] >> 16;
+  __syncthreads();
+  for (int f = tid; f < p.M * p.k; f += kPlanThreads)
+    if (slot[f] >= 0) p.list[atomicAdd(&cur[slot[f]], 1)] = f;
+}
+
+// --------------------------------------------------------------- products ---
+// Chunk depth: both chunks of a wave's loads fit about 128 registers.
+template <class Op, int NW, int NT>
+constexpr int stream_depth() {
+  constexpr int u = 16 / (NW + NT * Op::kX);
+  return u > 4 ? 4 : u < 1 ? 1 : u;
+}
+
+// Offsets of this lane's token rows: row i of the entry is pair list[i], at
+// (pair / div) * pitch.
+template <int NT>
+__device__ __forceinline__ void decode_rows(const DecodePlan& p, int4 ent, int div, uint32_t pitch,
+                                            uint32_t (&xoff)[NT]) {
+#pragma unroll
+  for (int j = 0; j < NT; ++j) {
+    const int i = 16 * j + (threadIdx.x & 15);
+    xoff[j] = i < ent.z ? (uint32_t)(p.list[ent.y + i] / div) * pitch : kNoRow;
+  }
+}
+
+// Layer0 of one entry: 16 NF columns of h for its rows.  NP: bf16 planes of
+// h (0: f32).
+template <class Op, int NF, int NT, int NP>
+__device__ __forceinline__ void decode_l0_tile(const DecodeArgs& a, int4 ent, f32x4_t* lds) {
+  const int f0 = blockIdx.x * 16 * NF;
+  uint32_t xoff[NT];
+  decode_rows<NT>(a.plan, ent, a.plan.k, a.x_pitch, xoff);
+  StreamArgs s{};
+  s.row_bytes = a.x_pitch;  // a gate or up row is as long as a row of x, in the same type
+  const int64_t at = ((int64_t)ent.x * a.F + f0) * (int64_t)s.row_bytes;
+  s.w0 = reinterpret_cast<const char*>(a.w_gate) + at;
+  s.w1 = reinterpret_cast<const char*>(a.w_up) + at;
+  s.w_bytes = 16u * NF * s.row_bytes;
+  s.x = a.x;
+  s.x_bytes = (uint32_t)a.plan.M * a.x_pitch;
+  s.steps = a.H / Op::kStep;
+  f32x4_t acc[2 * NF][NT];
+  stream_tile<Op, 2 * NF, NF, NT, stream_depth<Op, 2 * NF, NT>()>(s, xoff, acc);
+  stream_put<2 * NF, NT>(acc, lds);
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  for (int t = wave; t < NF * NT; t += kStreamWaves) {
+    const f32x4_t g = stream_sum(lds, t), u = stream_sum(lds, t + NF * NT);
+    const int i = 16 * (t % NT) + (lane & 15);
+    if (i >= ent.z) continue;
+    const int64_t pair = a.plan.list[ent.y + i];
+    const int col = f0 + 16 * (t / NT) + 4 * (lane >> 4);
+    f32x4_t h;
+#pragma unroll
+    for (int v = 0; v < 4; ++v) h[v] = silu_f32(g[v]) * u[v];
+    if constexpr (NP == 0) {
+      *reinterpret_cast<f32x4_t*>(reinterpret_cast<float*>(a.hact) + pair * a.F + col) = h;
+    } else {
+      __bf16 pl[4][NP];
+#pragma unroll
+      for (int v = 0; v < 4; ++v) split_bf16<NP>(h[v], pl[v]);
+#pragma unroll
+      for (int p = 0; p < NP; ++p) {
+        const bf16x4_t o = {pl[0][p], pl[1][p], pl[2][p], pl[3][p]};
+        *reinterpret_cast<bf16x4_t*>(reinterpret_cast<__bf16*>(a.hact) + (pair * NP + p) * a.F + col) = o;
+      }
+    }
+  }
+}
+
+template <class Op, int NF, int MAXNT, int NP>
+__global__ __launch_bounds__(kStreamThreads) void decode_l0_kernel(DecodeArgs a) {
+  __shared__ f32x4_t lds[kStreamWaves * 2 * NF * MAXNT * 64];
+  if ((int)blockIdx.y >= a.plan.hdr[0]) return;
+  const int4 ent = a.plan.entries[blockIdx.y];
+  if (MAXNT == 1 || ent.z <= 16)
+    decode_l0_tile<Op, NF, 1, NP>(a, ent, lds);
+  else if (MAXNT == 2 || ent.z <= 32)
+    decode_l0_tile<Op, NF, MAXNT < 2 ? 1 : 2, NP>(a, ent, lds);
+  else
+    decode_l0_tile<Op, NF, MAXNT, NP>(a, ent, lds);
+}
+
+// Layer1 of one entry: 16 NF columns of y for its rows (f32, at the pair's
+// own row).
+template <class Op, int NF, int NT, bool MX>
+__device__ __forceinline__ void decode_l1_tile(const DecodeArgs& a, int4 ent, f32x4_t* lds) {
+  const int n0 = blockIdx.x * 16 * NF;
+  uint32_t xoff[NT];
+  decode_rows<NT>(a.plan, ent, 1, a.h_pitch, xoff);
+  StreamArgs s{};
+  const int64_t row0 = (int64_t)ent.x * a.H + n0;
+  s.row_bytes = a.wd_pitch;
+  s.w0 = s.w1 = reinterpret_cast<const char*>(a.w_down) + row0 * s.row_bytes;
+  s.w_bytes = 16u * NF * s.row_bytes;
+  s.x = a.hact;
+  s.x_bytes = (uint32_t)a.plan.M * a.plan.k * a.h_pitch;
+  s.plane = 2u * a.F;
+  s.steps = a.F / Op::kStep;
+  if constexpr (MX) {
+    s.scale = a.wd_scale + (row0 >> 5) * (int64_t)a.F;
+    s.scale_row = (int)(row0 & 31);
+    s.scale_bytes = (uint32_t)((s.scale_row + 16 * NF + 31) / 32) * a.F;
+    s.scale_pitch = a.F;
+  }
+  f32x4_t acc[NF][NT];
+  stream_tile<Op, NF, NF, NT, stream_depth<Op, NF, NT>()>(s, xoff, acc);
+  stream_put<NF, NT>(acc, lds);
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  for (int t = wave; t < NF * NT; t += kStreamWaves) {
+    const f32x4_t y = stream_sum(lds, t);
+    const int i = 16 * (t % NT) + (lane & 15);
+    if (i >= ent.z) continue;
+    const int64_t pair = a.plan.list[ent.y + i];
+    *reinterpret_cast<f32x4_t*>(a.y + pair * a.H + n0 + 16 * (t / NT) + 4 * (lane >> 4)) = y;
+  }
+}
+
+template <class Op, int NF, int MAXNT, bool MX>
+__global__ __launch_bounds__(kStreamThreads) void decode_l1_kernel(DecodeArgs a) {
+  __shared__ f32x4_t lds[kStreamWaves * NF * MAXNT * 64];
+  if ((int)blockIdx.y >= a.plan.hdr[0]) return;
+  const int4 ent = a.plan.entries[blockIdx.y];
+  if (MAXNT == 1 || ent.z <= 16)
+    decode_l1_tile<Op, NF, 1, MX>(a, ent, lds);
+  else if (MAXNT == 2 || ent.z <= 32)
+    decode_l1_tile<Op, NF, MAXNT < 2 ? 1 : 2, MX>(a, ent, lds);
+  else
+    decode_l1_tile<Op, NF, MAXNT, MX>(a, ent, lds);
+}
+
+// ---------------------------------------------------------------- launch ---
+// Rows an entry may hold, by the token count (an expert gets at most one row
+// of every token): 16, 32, or blocks of 64 (32 for MXFP8, whose converted
+// weights and planes need more registers).
+static int decode_max_nt(int M, bool mx) { return M <= 16 ? 1 : (M <= 32 || mx) ? 2 : 4; }
+
+int decode_entry_rows(int M, bool mx) { return 16 * decode_max_nt(M, mx); }
+
+int decode_max_entries(int M, int k, int EL, bool mx) {
+  const int R = M * k;
+  return (EL < R ? EL : R) + R / decode_entry_rows(M, mx);
+}
+
+template <class Op0, class Op1, int NP, bool MX>
+static void launch_products(const DecodeArgs& a, int entries, hipStream_t s) {
+  const int nt = decode_max_nt(a.plan.M, MX);
+  auto grid = [&](int n, int nf) { return dim3((unsigned)(n / (16 * nf)), (unsigned)entries); };
+  if (nt == 1) {
+    decode_l0_kernel<Op0, 1, 1, NP><<<grid(a.F, 1), kStreamThreads, 0, s>>>(a);
+    decode_l1_kernel<Op1, 1, 1, MX><<<grid(a.H, 1), kStreamThreads, 0, s>>>(a);
+  } else if (nt == 2) {
+    decode_l0_kernel<Op0, 1, 2, NP><<<grid(a.F, 1), kStreamThreads, 0, s>>>(a);
+    decode_l1_kernel<Op1, 2, 2, MX><<<grid(a.H, 2), kStreamThreads, 0, s>>>(a);
+  } else {
+    if constexpr (!MX) {
+      decode_l0_kernel<Op0, 2, 4, NP><<<grid(a.F, 2), kStreamThreads, 0, s>>>(a);
+      decode_l1_kernel<Op1, 4, 4, MX><<<grid(a.H, 4), kStreamThreads, 0, s>>>(a);
+    }
+  }
+}
+
+hipError_t launch_decode(const DecodeArgs& a, const float* logits, int dtype, int planes, const OutEpilogue& ep,
+                         hipStream_t s) {
+  const DecodePlan& p = a.plan;
+  const dim3 block(kPlanThreads);
+  if (p.k <= 1)
+    decode_plan_kernel<1><<<1, block, 0, s>>>(logits, p);
+  else if (p.k <= 2)
+    decode_plan_kernel<2><<<1, block, 0, s>>>(logits, p);
+  else if (p.k <= 4)
+    decode_plan_kernel<4><<<1, block, 0, s>>>(logits, p);
+  else if (p.k <= 8)
+    decode_plan_kernel<8><<<1, block, 0, s>>>(logits, p);
+  else
+    decode_plan_kernel<16><<<1, block, 0, s>>>(logits, p);
+  hipError_t e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  const int entries = decode_max_entries(p.M, p.k, p.EL, dtype == MOE_DTYPE_BF16_MXFP8);
+  if (dtype == MOE_DTYPE_F32)
+    launch_products<StreamF32, StreamF32, 0, false>(a, entries, s);
+  else if (dtype == MOE_DTYPE_BF16 && planes == 3)
+    launch_products<StreamBf16<1>, StreamBf16<3>, 3, false>(a, entries, s);
+  else if (dtype == MOE_DTYPE_BF16)
+    launch_products<StreamBf16<1>, StreamBf16<2>, 2, false>(a, entries, s);
+  else if (planes == 3)
+    launch_products<StreamBf16<1>, StreamMx<3>, 3, true>(a, entries, s);
+  else
+    launch_products<StreamBf16<1>, StreamMx<2>, 2, true>(a, entries, s);
+  e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  return launch_combine(a.y, p.w, p.f2s, p.M, a.H, p.k, ep, s);
+}
+
+}  // namespace moe

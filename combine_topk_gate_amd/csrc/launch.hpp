@@ -82,6 +82,49 @@ hipError_t launch_transpose(const void* src, void* dst, int64_t batch, int rows,
 hipError_t launch_combine(const float* y, const float* topk_w, const int32_t* flat_to_sorted, int64_t M, int H,
                           int k, const OutEpilogue& ep, hipStream_t s);
 
+// Decode layer (at most MOE_DECODE_MAX_TOKENS tokens).
+struct DecodePlan {
+  int M, k, E, EL, base;
+  int rows;       // rows an entry may hold (decode_entry_rows)
+  int32_t* hdr;   // [0]: number of entries
+  int4* entries;  // {held expert, first place in list, rows, 0}
+  int32_t* list;  // pairs f = t k + j, expert by expert
+  int32_t* f2s;   // [M k] f, or -1 for a pair of no held expert
+  float* w;       // [M k] combine weights
+};
+struct DecodeArgs {
+  DecodePlan plan;
+  const void* x;
+  const void* w_gate;
+  const void* w_up;
+  const void* w_down;
+  const uint8_t* wd_scale;  // MXFP8: the scale bytes of W_down
+  void* hact;               // [M k][planes][F] bf16, or [M k][F] f32
+  float* y;                 // [M k][H]
+  int H, F;
+  uint32_t x_pitch, h_pitch, wd_pitch;  // bytes of a row of x (and of the gate and up weights), h, W_down
+};
+int decode_entry_rows(int M, bool mx);
+int decode_max_entries(int M, int k, int EL, bool mx);
+hipError_t launch_decode(const DecodeArgs& a, const float* logits, int dtype, int planes, const OutEpilogue& ep,
+                         hipStream_t s);
+
+// Projection with low-rank adapters.
+struct AdapterArgs {
+  int64_t M;
+  int H, N, r, P;  // P = 0: no adapters
+  const void* x;
+  const void* w;
+  const void* a;
+  const void* b;
+  const float* scale;
+  const int32_t* idx;
+  float* t;            // [M, r] workspace
+  OutEpilogue out;
+  uint32_t row_bytes;  // bytes of a row of x, W and A
+};
+hipError_t launch_adapter_linear(const AdapterArgs& a, bool f32, hipStream_t s);
+
 int device_cu_count();
 
 }  // namespace moe

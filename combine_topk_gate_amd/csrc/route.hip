@@ -16,74 +16,11 @@
 // token ends with the same one.
 #include "common.hpp"
 #include "launch.hpp"
+#include "topk.hpp"
 
 namespace moe {
 
 constexpr int kRouteThreads = 256;
-constexpr int kLanesPerToken = 16;
-
-// a ahead of b: larger value, or equal value and lower index
-__device__ __forceinline__ bool route_before(float va, int ia, float vb, int ib) {
-  return va > vb || (va == vb && ia < ib);
-}
-
-template <int KMAX>
-__device__ __forceinline__ void topk_insert(float (&vals)[KMAX], int (&ids)[KMAX], float v, int e) {
-  // e exceeds every index kept so far, so v enters only if strictly larger
-  // than the last kept value, behind every kept value it does not exceed
-  if (!(v > vals[KMAX - 1])) return;
-#pragma unroll
-  for (int i = KMAX - 1; i >= 0; --i) {
-    if (vals[i] >= v) continue;
-    const bool above_ge = (i == 0) ? true : (vals[i - 1] >= v);
-    if (above_ge) {
-      vals[i] = v;
-      ids[i] = e;
-    } else {
-      vals[i] = vals[i - 1];
-      ids[i] = ids[i - 1];
-    }
-  }
-}
-
-// Keep the KMAX best of two sorted lists (own and the partner lane's):
-// pairing own[i] with partner[KMAX-1-i] and keeping the better of each pair
-// leaves the KMAX best as a bitonic sequence, which a bitonic merger sorts.
-template <int KMAX>
-__device__ __forceinline__ void topk_merge_partner(float (&vals)[KMAX], int (&ids)[KMAX], int off) {
-  float pv[KMAX];
-  int pi[KMAX];
-#pragma unroll
-  for (int i = 0; i < KMAX; ++i) {
-    pv[i] = __shfl_xor(vals[i], off);
-    pi[i] = __shfl_xor(ids[i], off);
-  }
-#pragma unroll
-  for (int i = 0; i < KMAX; ++i) {
-    const float bv = pv[KMAX - 1 - i];
-    const int bi = pi[KMAX - 1 - i];
-    if (!route_before(vals[i], ids[i], bv, bi)) {
-      vals[i] = bv;
-      ids[i] = bi;
-    }
-  }
-#pragma unroll
-  for (int half = KMAX / 2; half >= 1; half >>= 1) {
-#pragma unroll
-    for (int i = 0; i < KMAX; ++i) {
-      if (i & half) continue;
-      const int j = i + half;
-      if (!route_before(vals[i], ids[i], vals[j], ids[j])) {
-        const float tv = vals[i];
-        const int ti = ids[i];
-        vals[i] = vals[j];
-        ids[i] = ids[j];
-        vals[j] = tv;
-        ids[j] = ti;
-      }
-    }
-  }
-}
 
 // Words the caller needs zero before the kernels that follow (the layer
 // call's status word and the fused kernel's ready counters): block 0 clears
@@ -108,26 +45,7 @@ __global__ __launch_bounds__(kRouteThreads) void route_topk_kernel(const float* 
   const bool valid = t < M;  // whole 16-lane groups share `valid`
   float vals[KMAX];
   int ids[KMAX];
-#pragma unroll
-  for (int i = 0; i < KMAX; ++i) {
-    vals[i] = -__builtin_inff();
-    ids[i] = 0x7fffffff;  // behind every real expert (logits are finite)
-  }
-  if (valid) {
-    const float* row = logits + t * (int64_t)E;
-    // 4 loads in flight per lane, then insertion in increasing expert order
-    int e = q;
-    for (; e + 3 * kLanesPerToken < E; e += 4 * kLanesPerToken) {
-      float v[4];
-#pragma unroll
-      for (int u = 0; u < 4; ++u) v[u] = row[e + u * kLanesPerToken];
-#pragma unroll
-      for (int u = 0; u < 4; ++u) topk_insert<KMAX>(vals, ids, v[u], e + u * kLanesPerToken);
-    }
-    for (; e < E; e += kLanesPerToken) topk_insert<KMAX>(vals, ids, row[e], e);
-  }
-#pragma unroll
-  for (int off = 1; off < kLanesPerToken; off <<= 1) topk_merge_partner<KMAX>(vals, ids, off);
+  topk_row<KMAX>(logits + (valid ? t : 0) * (int64_t)E, E, q, valid, vals, ids);
   if (!valid) return;
 
   // weights: softmax over the k chosen logits, shifted by the largest,

@@ -120,7 +120,7 @@ typedef enum {
 typedef enum { MOE_DTYPE_F32 = 0, MOE_DTYPE_BF16 = 1, MOE_DTYPE_BF16_MXFP8 = 2 } moe_dtype_t;
 
 /* Operation whose workspace moe_workspace_bytes sizes. */
-typedef enum { MOE_OP_DISPATCH = 0, MOE_OP_GROUPED_GEMM = 1, MOE_OP_LAYER = 2 } moe_op_t;
+typedef enum { MOE_OP_DISPATCH = 0, MOE_OP_GROUPED_GEMM = 1, MOE_OP_LAYER = 2, MOE_OP_LAYER_DECODE = 3 } moe_op_t;
 
 /*
  * Problem shape.  Limits: 0 <= M, M*k < 2^31; H and F multiples of 64 in
@@ -380,6 +380,73 @@ moe_status_t moe_layer_ex(const moe_problem_t* p, const void* x, const float* lo
                           const void* w_gate, const void* w_up, const void* w_down, const moe_epilogue_t* epi,
                           void* out, const moe_layer_aux_t* aux, const moe_layer_opts_t* opts, void* ws,
                           size_t ws_bytes, void* stream);
+
+/*
+ * The layer for a few tokens (a decode step; [COMET] §3.2 the two products,
+ * §4.1.1 the Top-K reduction): M <= MOE_DECODE_MAX_TOKENS, else
+ * MOE_ERR_UNSUPPORTED.  Routing, products and combine of moe_layer_ex, with
+ * nothing dispatched: the weights of the experts that the tokens choose are
+ * read once, past the token rows.  It differs from moe_layer_ex in that
+ *   - a logit of -inf is an expert the token may not choose: it is never
+ *     chosen, a token with fewer than k others uses those, and a row with
+ *     none (an idle row of a fixed batch) gives 0 (plus the residual);
+ *   - the activation between the products is kept in f32 (to 2^-17 when the
+ *     output is bf16), not rounded to the dtype.  MOE_DTYPE_BF16_MXFP8 takes
+ *     W_down in MXFP8 as moe_layer does, and its activation is not quantised
+ *     (the products are bound by reading the weights);
+ *   - num_src_blocks has no effect on the result: there are no segments, and
+ *     no src_block argument.
+ *   x [M,H] dtype; logits [M,E] f32 (finite or -inf); w_gate, w_up [EL,F,H];
+ *   w_down [EL,H,F]; out [M,H] in epi->out_dtype (NULL epi: f32), the
+ *   partial combine when EL < E.  out may be the residual itself (same type),
+ *   and otherwise overlaps no input and not ws.
+ *   ws: moe_workspace_bytes(p, MOE_OP_LAYER_DECODE) bytes, 256-byte aligned,
+ *   for this call alone while it runs (its contents need no clearing).
+ * MOE_DEBUG_VALIDATE=1 refuses logits that are NaN or +inf.
+ */
+#define MOE_DECODE_MAX_TOKENS 256
+moe_status_t moe_layer_decode(const moe_problem_t* p, const void* x, const float* logits, const void* w_gate,
+                              const void* w_up, const void* w_down, const moe_epilogue_t* epi, void* out, void* ws,
+                              size_t ws_bytes, void* stream);
+
+/*
+ * A shared projection with the low-rank adapters of many requests ([GGEMM]
+ * many small products beside a large one): for every row m with adapter a =
+ * adapter_idx[m],
+ *   t[m]     = scale[a] * sum_h x[m,h] A[a,:,h]             (f32, rank values)
+ *   out[m,n] = cast(sum_h x[m,h] W[n,h] + sum_j t[m,j] B[a,n,j] + residual[m,n])
+ * accumulated in f32; a row whose adapter_idx is -1 (or outside [0,
+ * num_adapters)) uses no adapter.  It gives the gate logits of moe_route and
+ * moe_layer from the hidden state (W the router, out f32), and the dense
+ * projections around the layer.
+ *   x [M,H]; w [N,H]; a [P,rank,H]; b [P,N,rank]: dtype, bf16 or f32
+ *   (MOE_DTYPE_BF16_MXFP8: MOE_ERR_UNSUPPORTED); scale [P] f32;
+ *   adapter_idx [M] int32; epi as in moe_combine_ex, with residual and out
+ *   [M,N] (NULL: f32 out, no residual).  out may be the residual itself
+ *   (same type), and otherwise overlaps neither x, w, residual nor ws.
+ *   P = 0: the projection alone (a, b, scale, adapter_idx and ws unused).
+ * Limits: 0 <= M < 2^31; H a multiple of 64 in [64, 65536]; 1 <= N <= 65536;
+ * rank a multiple of 8 in [8, 256] (smaller ranks: pad with zeros); 0 <= P
+ * <= 65536.
+ *   ws: moe_adapter_workspace_bytes(q) bytes, 256-byte aligned, for this call
+ *   alone while it runs (its contents need no clearing).
+ * MOE_DEBUG_VALIDATE=1 refuses an adapter_idx outside [-1, P).
+ */
+typedef struct {
+  int64_t num_tokens;   /* M */
+  int32_t in_features;  /* H */
+  int32_t out_features; /* N */
+  int32_t rank;         /* of every adapter */
+  int32_t num_adapters; /* P */
+  int32_t dtype;        /* moe_dtype_t: F32 or BF16 */
+} moe_adapter_problem_t;
+
+/* Bytes of device workspace (0 if none, or for an invalid problem). */
+size_t moe_adapter_workspace_bytes(const moe_adapter_problem_t* q);
+
+moe_status_t moe_adapter_linear(const moe_adapter_problem_t* q, const void* x, const void* w, const void* a,
+                                const void* b, const float* scale, const int32_t* adapter_idx,
+                                const moe_epilogue_t* epi, void* out, void* ws, size_t ws_bytes, void* stream);
 
 /* The plan the profiled split table picks for this problem (what moe_layer
  * does when opts->n_mover < 0): the number of dedicated combine workgroups
