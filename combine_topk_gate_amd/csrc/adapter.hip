@@ -10,6 +10,9 @@
 // projection with the adapters' part, the residual and the cast in its
 // epilogue, so out is written once and nothing of the size of out is read
 // back.
+#include <math.h>
+
+#include "adapter_gemm.hpp"
 #include "common.hpp"
 #include "launch.hpp"
 #include "stream.hpp"
@@ -17,49 +20,62 @@
 namespace moe {
 
 // -------------------------------------------------------------- t = x A^T ---
-// Workgroup (b, s, z): the s-th distinct adapter among the 16 rows of block b
-// (none: it exits), its rank rows 16 NW z .. + 16 NW - 1.  Rows of other
-// adapters read zeros and store nothing.
-template <class Op, int NW>
-__global__ __launch_bounds__(kStreamThreads) void adapter_shrink_kernel(AdapterArgs a) {
-  __shared__ f32x4_t lds[kStreamWaves * NW * 64];
-  const int64_t m0 = (int64_t)blockIdx.x * 16;
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, i = lane & 15;
-  const int rows = (int)min((int64_t)16, a.M - m0);
-  int id = -1;
-  if (i < rows) {
-    id = a.idx[m0 + i];
+// Block (b, s, z): of the distinct adapters among the 16 NT rows of block b,
+// those number s, s + gridDim.y, ... (none: it exits), rank rows 16 NW z .. +
+// 16 NW - 1.  The waves split the reduction.  Bound by latency for short
+// batches, by reading x for long ones (launch_shrink).
+template <class Op, int WAVES, int NW, int NT>
+__global__ __launch_bounds__(64 * WAVES) void adapter_shrink_kernel(AdapterArgs a) {
+  constexpr int kLds = WAVES * imax(stream_line_bytes<Op, NW, NT>(), NW * NT * 1024);
+  __shared__ __attribute__((aligned(16))) char lds[kLds];
+  const int64_t m0 = (int64_t)blockIdx.x * 16 * NT;
+  const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
+  const int rows = (int)min((int64_t)16 * NT, a.M - m0);
+  int id = -1;  // lane's row: m0 + lane
+  if (lane < rows) {
+    id = a.idx[m0 + lane];
     if ((uint32_t)id >= (uint32_t)a.P) id = -1;
   }
-  bool first = id >= 0;
-  for (int j = 0; j < 15; ++j) {
-    const int other = __shfl(id, j);  // by every lane, those that do not use it too
-    if (j < i && other == id) first = false;
-  }
-  uint64_t firsts = __ballot(first) & 0xFFFFull;
-  for (unsigned s = 0; s < blockIdx.y && firsts; ++s) firsts &= firsts - 1;
-  if (!firsts) return;
-  const int mine = uniform(__shfl(id, __ffsll((unsigned long long)firsts) - 1));
   const int j0 = blockIdx.z * 16 * NW;
-  uint32_t xoff[1] = {id == mine ? (uint32_t)i * a.row_bytes : kNoRow};
   StreamArgs s{};
   s.row_bytes = a.row_bytes;
-  s.w0 = s.w1 = reinterpret_cast<const char*>(a.a) + ((int64_t)mine * a.r + j0) * a.row_bytes;
-  s.w_bytes = (uint32_t)min(16 * NW, a.r - j0) * a.row_bytes;
+  s.w_rows = min(16 * NW, a.r - j0);
   s.x = reinterpret_cast<const char*>(a.x) + m0 * a.row_bytes;
   s.x_bytes = (uint32_t)rows * a.row_bytes;
-  s.steps = a.H / Op::kStep;
-  f32x4_t acc[NW][1];
-  stream_tile<Op, NW, NW, 1, 4>(s, xoff, acc);
-  stream_put<NW, 1>(acc, lds);
-  const float sc = a.scale[mine];
-  for (int t = wave; t < NW; t += kStreamWaves) {
-    f32x4_t v = stream_sum(lds, t);
-    const int j = j0 + 16 * t + 4 * (lane >> 4);
-    if (id != mine || j >= a.r) continue;  // r is a multiple of 8
+  s.lines = a.H / Op::kLine;
+  uint64_t left = __ballot(id >= 0);
+  for (int n = 0; left; ++n) {
+    const int mine = __builtin_amdgcn_readlane(id, __ffsll((unsigned long long)left) - 1);
+    left &= ~__ballot(id == mine);
+    if (n % (int)gridDim.y != (int)blockIdx.y) continue;
+    // (rows of other adapters are computed too, and not stored)
+    s.w0 = reinterpret_cast<const char*>(a.a) + ((int64_t)mine * a.r + j0) * a.row_bytes;
+    f32x4_t acc[NW][NT];
+    stream_tile<Op, WAVES, NW, false, NT>(s, [&](int m) { return (uint32_t)min(m, rows - 1) * a.row_bytes; },
+                                          lds + wave * stream_line_bytes<Op, NW, NT>(), acc);
+    const float sc = a.scale[mine];
+    stream_reduce<WAVES, NW, NT, NW, 1>(acc, reinterpret_cast<f32x4_t*>(lds), [&](int g, int jt, const f32x4_t (&t)[1]) {
+      f32x4_t v = t[0];
+      const int i = 16 * jt + (lane & 15), j = j0 + 16 * g + 4 * (lane >> 4);
+      if (__shfl(id, i) != mine || j >= a.r) return;  // r is a multiple of 8
 #pragma unroll
-    for (int c = 0; c < 4; ++c) v[c] *= sc;
-    *reinterpret_cast<f32x4_t*>(a.t + (m0 + i) * a.r + j) = v;
+      for (int c = 0; c < 4; ++c) v[c] *= sc;
+      if (a.planes == 0) {
+        *reinterpret_cast<f32x4_t*>(reinterpret_cast<float*>(a.t) + (m0 + i) * a.r + j) = v;
+        return;
+      }
+      __bf16 pl[4][3];
+#pragma unroll
+      for (int c = 0; c < 4; ++c) split_bf16<3>(v[c], pl[c]);
+      __bf16* t16 = reinterpret_cast<__bf16*>(a.t) + (m0 + i) * a.planes * a.r + j;
+#pragma unroll
+      for (int p = 0; p < 3; ++p) {
+        if (p >= a.planes) break;
+        const bf16x4_t o = {pl[0][p], pl[1][p], pl[2][p], pl[3][p]};
+        *reinterpret_cast<bf16x4_t*>(t16 + p * a.r) = o;
+      }
+    });
+    __syncthreads();  // the sums are read before the next adapter's lines come
   }
 }
 
@@ -72,7 +88,7 @@ __device__ __forceinline__ float to_f32(T v) {
 // acc[c] += t . B[id, n + c] for the columns that exist, in increasing rank.
 template <class T>
 __device__ __forceinline__ void add_adapter(const AdapterArgs& a, int64_t m, int id, int n, f32x4_t& acc) {
-  const float* t = a.t + m * a.r;
+  const float* t = reinterpret_cast<const float*>(a.t) + m * a.r;
   const T* b = reinterpret_cast<const T*>(a.b) + ((int64_t)id * a.N + n) * a.r;
   constexpr int V = 16 / sizeof(T);  // elements per vector; r is a multiple of 8
   typedef T vec_t __attribute__((ext_vector_type(V)));
@@ -91,98 +107,142 @@ __device__ __forceinline__ void add_adapter(const AdapterArgs& a, int64_t m, int
   }
 }
 
-// Stores 4 columns (those below N) of row m: residual, cast.
-__device__ __forceinline__ void adapter_store(const AdapterArgs& a, int64_t m, int n, f32x4_t acc) {
-  const int64_t i = m * a.N + n;
-  if ((a.N & 3) == 0) {
-    store_out(a.out, i, make_float4(acc[0], acc[1], acc[2], acc[3]));
-    return;
-  }
-#pragma unroll
-  for (int c = 0; c < 4; ++c) {
-    if (n + c >= a.N) break;
-    float v = acc[c];
-    if (a.out.residual)
-      v += a.out.res_bf16 ? (float)reinterpret_cast<const __bf16*>(a.out.residual)[i + c]
-                          : reinterpret_cast<const float*>(a.out.residual)[i + c];
-    if (a.out.out_bf16)
-      reinterpret_cast<__bf16*>(a.out.out)[i + c] = (__bf16)v;
-    else
-      reinterpret_cast<float*>(a.out.out)[i + c] = v;
-  }
-}
-
 // 16 NW columns of 16 NT rows: the weight rows stream past the token rows
 // (stream.hpp).  T: the type of x, W, A and B.
-template <class Op, class T, int NW, int NT, int U>
-__global__ __launch_bounds__(kStreamThreads) void adapter_stream_kernel(AdapterArgs a) {
-  __shared__ f32x4_t lds[kStreamWaves * NW * NT * 64];
-  const int64_t m0 = (int64_t)blockIdx.x * 16 * NT;
-  const int n0 = blockIdx.y * 16 * NW;
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+template <class Op, class T, int WAVES, int NW, int NT>
+__global__ __launch_bounds__(64 * WAVES) void adapter_stream_kernel(AdapterArgs a, int mb, int nb) {
+  constexpr int G = NW * NT * WAVES <= 64 ? NW : NW * NT * WAVES <= 128 && NW % 2 == 0 ? NW / 2 : 1;
+  constexpr int kLds = WAVES * imax(stream_line_bytes<Op, NW, NT>(), G * NT * 1024);
+  __shared__ __attribute__((aligned(16))) char lds[kLds];
+  // the row blocks of one weight block run next to each other on one XCD (whose
+  // workgroups come 8 apart), so its L2 reads the weights once
+  const int64_t per = ((int64_t)mb * nb + 7) / 8, v0 = (int64_t)(blockIdx.x & 7) * per + (blockIdx.x >> 3);
+  if (v0 >= (int64_t)mb * nb) return;
+  const int64_t m0 = v0 % mb * 16 * NT;
+  const int n0 = (int)(v0 / mb) * 16 * NW;
+  const int lane = threadIdx.x & 63;
   const int rows = (int)min((int64_t)16 * NT, a.M - m0);
-  uint32_t xoff[NT];
-#pragma unroll
-  for (int j = 0; j < NT; ++j) {
-    const int i = 16 * j + (lane & 15);
-    xoff[j] = i < rows ? (uint32_t)i * a.row_bytes : kNoRow;
-  }
   StreamArgs s{};
   s.row_bytes = a.row_bytes;
-  s.w0 = s.w1 = reinterpret_cast<const char*>(a.w) + (int64_t)n0 * a.row_bytes;
-  s.w_bytes = (uint32_t)min(16 * NW, a.N - n0) * a.row_bytes;
+  s.w0 = reinterpret_cast<const char*>(a.w) + (int64_t)n0 * a.row_bytes;
+  s.w_rows = min(16 * NW, a.N - n0);
   s.x = reinterpret_cast<const char*>(a.x) + m0 * a.row_bytes;
   s.x_bytes = (uint32_t)rows * a.row_bytes;
-  s.steps = a.H / Op::kStep;
+  s.lines = a.H / Op::kLine;
   f32x4_t acc[NW][NT];
-  stream_tile<Op, NW, NW, NT, U>(s, xoff, acc);
-  stream_put<NW, NT>(acc, lds);
-  for (int t = wave; t < NW * NT; t += kStreamWaves) {
-    f32x4_t v = stream_sum(lds, t);
-    const int i = 16 * (t % NT) + (lane & 15);
-    const int n = n0 + 16 * (t / NT) + 4 * (lane >> 4);
-    if (i >= rows || n >= a.N) continue;
+  stream_tile<Op, WAVES, NW, false, NT>(s, [&](int m) { return (uint32_t)min(m, rows - 1) * a.row_bytes; },
+                                        lds + uniform(threadIdx.x >> 6) * stream_line_bytes<Op, NW, NT>(), acc);
+  stream_reduce<WAVES, NW, NT, G, 1>(acc, reinterpret_cast<f32x4_t*>(lds), [&](int g, int j, const f32x4_t (&sum)[1]) {
+    f32x4_t v = sum[0];
+    const int i = 16 * j + (lane & 15);
+    const int n = n0 + 16 * g + 4 * (lane >> 4);
+    if (i >= rows || n >= a.N) return;
     const int id = a.P > 0 ? a.idx[m0 + i] : -1;
     if ((uint32_t)id < (uint32_t)a.P) add_adapter<T>(a, m0 + i, id, n, v);
     adapter_store(a, m0 + i, n, v);
-  }
+  });
 }
 
 // ----------------------------------------------------------------- launch ---
+template <class Op, int WAVES, int NW, int NT>
+static void launch_shrink_as(const AdapterArgs& a, unsigned slots, hipStream_t s) {
+  const dim3 grid((unsigned)((a.M + 16 * NT - 1) / (16 * NT)), slots, (unsigned)((a.r + 16 * NW - 1) / (16 * NW)));
+  adapter_shrink_kernel<Op, WAVES, NW, NT><<<grid, 64 * WAVES, 0, s>>>(a);
+}
+
+// Short batches: a block of 16 waves for every adapter that 16 rows can have.
+// Long ones: the largest tile that still gives a block for every CU (x is
+// read once per 16 NW of the rank, A once per 16 NT rows), which takes its
+// rows' adapters in turn.
 template <class Op>
 static void launch_shrink(const AdapterArgs& a, hipStream_t s) {
-  const unsigned blocks = (unsigned)((a.M + 15) / 16);
-  if (a.r <= 16)
-    adapter_shrink_kernel<Op, 1><<<dim3(blocks, 16, 1), kStreamThreads, 0, s>>>(a);
-  else
-    adapter_shrink_kernel<Op, 2><<<dim3(blocks, 16, (unsigned)((a.r + 31) / 32)), kStreamThreads, 0, s>>>(a);
+  const int64_t cus = device_cu_count();
+  auto blocks = [&](int nw, int nt) {
+    return ((a.M + 16 * nt - 1) / (16 * nt)) * ((a.r + 16 * nw - 1) / (16 * nw));
+  };
+  if (a.M <= 256) {
+    if (a.r <= 16)
+      launch_shrink_as<Op, 16, 1, 1>(a, 16, s);
+    else
+      launch_shrink_as<Op, 16, 2, 1>(a, 16, s);
+  } else if (a.r > 32 && blocks(4, 2) >= cus) {
+    launch_shrink_as<Op, 8, 4, 2>(a, 1, s);
+  } else if (a.r > 16 && blocks(2, 2) >= cus) {
+    launch_shrink_as<Op, 8, 2, 2>(a, 1, s);
+  } else if (blocks(1, 2) >= cus) {
+    launch_shrink_as<Op, 8, 1, 2>(a, 1, s);
+  } else {
+    launch_shrink_as<Op, 8, 1, 1>(a, 1, s);
+  }
+}
+
+template <class Op, class T, int WAVES, int NW, int NT>
+static void launch_stream_as(const AdapterArgs& a, hipStream_t s) {
+  const int mb = (int)((a.M + 16 * NT - 1) / (16 * NT)), nb = (a.N + 16 * NW - 1) / (16 * NW);
+  const unsigned grid = (unsigned)(((int64_t)mb * nb + 7) / 8 * 8);
+  adapter_stream_kernel<Op, T, WAVES, NW, NT><<<grid, 64 * WAVES, 0, s>>>(a, mb, nb);
+}
+
+// Which kernel: the tiles of each differ in how long a round of them (one
+// per CU) takes, and the rule takes the fewest rounds times that.  Measured
+// at H = 4096, in us a round: bf16 stream tiles of 64 x 64, 32 x 32 and 16 x
+// 16 outputs 17.5, 7 and 4; the matrix-core tiles of 128 x 256 and 256 x 256
+// 57 and 105 (they keep more of the operands in LDS, but one of them alone on
+// a CU waits longer for its loads).  E.g. 1024 x 4096 x 2048: 64 x 64 tiles 34
+// us, 128 x 256 tiles 55; 2048 x 4096 x 4096: 168 and 72.  f32 (the matrix
+// cores bound it): 77, 21 and 7.
+static float tile_cost(const AdapterArgs& a, int rows, int cols, float us) {
+  const float tiles = (float)((a.M + rows - 1) / rows) * (float)((a.N + cols - 1) / cols);
+  return ceilf(tiles / (float)device_cu_count()) * us;
+}
+
+struct StreamCost {
+  float c4, c2, c1;
+  float least() const { return fminf(c4, fminf(c2, c1)); }
+};
+static StreamCost stream_cost(const AdapterArgs& a, float us4, float us2, float us1) {
+  return {tile_cost(a, 64, 64, us4), tile_cost(a, 32, 32, us2), tile_cost(a, 16, 16, us1)};
 }
 
 template <class Op, class T>
-static void launch_stream(const AdapterArgs& a, hipStream_t s) {
-  auto grid = [&](int nt, int nw) {
-    return dim3((unsigned)((a.M + 16 * nt - 1) / (16 * nt)), (unsigned)((a.N + 16 * nw - 1) / (16 * nw)));
-  };
-  if (a.M <= 16)
-    adapter_stream_kernel<Op, T, 1, 1, 4><<<grid(1, 1), kStreamThreads, 0, s>>>(a);
+static void launch_stream(const AdapterArgs& a, const StreamCost& c, hipStream_t s) {
+  if (c.c4 <= c.c2 && c.c4 <= c.c1)
+    launch_stream_as<Op, T, 8, 4, 4>(a, s);
+  else if (c.c2 <= c.c1)
+    launch_stream_as<Op, T, 8, 2, 2>(a, s);
   else
-    adapter_stream_kernel<Op, T, 4, 4, 2><<<grid(4, 4), kStreamThreads, 0, s>>>(a);
+    launch_stream_as<Op, T, 8, 1, 1>(a, s);
 }
 
-hipError_t launch_adapter_linear(const AdapterArgs& a, bool f32, hipStream_t s) {
+hipError_t launch_adapter_linear(AdapterArgs a, bool f32, hipStream_t s) {
   if (a.M == 0) return hipSuccess;
-  if (a.P > 0) {
+  const float g128 = tile_cost(a, 128, 256, 57.0f), g256 = tile_cost(a, 256, 256, 105.0f);
+  const StreamCost sc = f32 ? stream_cost(a, 77.0f, 21.0f, 7.0f) : stream_cost(a, 17.5f, 7.0f, 4.0f);
+  auto shrink = [&](int planes) {
+    a.planes = planes;
+    if (a.P == 0) return hipSuccess;
     if (f32)
       launch_shrink<StreamF32>(a, s);
     else
       launch_shrink<StreamBf16<1>>(a, s);
-    const hipError_t e = hipGetLastError();
-    if (e != hipSuccess) return e;
+    return hipGetLastError();
+  };
+  hipError_t e;
+  if (f32 || a.H < 128 || sc.least() <= fminf(g128, g256)) {
+    if ((e = shrink(0)) != hipSuccess) return e;
+    if (f32)
+      launch_stream<StreamF32, float>(a, sc, s);
+    else
+      launch_stream<StreamBf16<1>, __bf16>(a, sc, s);
+  } else {
+    if ((e = shrink(a.out.out_bf16 ? 2 : 3)) != hipSuccess) return e;
+    const int64_t rows = g256 < g128 ? 256 : 128, mt = (a.M + rows - 1) / rows, nt = (a.N + 255) / 256;
+    const dim3 grid((unsigned)((mt * nt + 7) / 8 * 8));
+    if (g256 < g128)
+      adapter_gemm_kernel<256><<<grid, kGemmThreads, 0, s>>>(a, (int)mt, (int)nt);
+    else
+      adapter_gemm_kernel<128><<<grid, kGemmThreads, 0, s>>>(a, (int)mt, (int)nt);
   }
-  if (f32)
-    launch_stream<StreamF32, float>(a, s);
-  else
-    launch_stream<StreamBf16<1>, __bf16>(a, s);
   return hipGetLastError();
 }
 

@@ -290,7 +290,7 @@ moe_status_t check_adapter(const moe_adapter_problem_t* q) {
 }
 
 size_t adapter_ws(const moe_adapter_problem_t* q) {
-  return q->num_adapters > 0 ? align_up((size_t)q->num_tokens * q->rank * 4) : 0;
+  return q->num_adapters > 0 ? align_up((size_t)q->num_tokens * q->rank * 6) : 0;  // f32, or three bf16 planes
 }
 
 template <typename T>
@@ -692,7 +692,8 @@ moe_status_t moe_adapter_linear(const moe_adapter_problem_t* q, const void* x, c
   g.b = b;
   g.scale = scale;
   g.idx = adapter_idx;
-  g.t = need > 0 ? at<float>(ws, 0) : nullptr;
+  g.t = need > 0 ? ws : nullptr;
+  g.planes = 0;  // set by the launcher
   g.row_bytes = (uint32_t)(g.H * eb);
   return hip_status(launch_adapter_linear(g, f32, (hipStream_t)stream));
 }

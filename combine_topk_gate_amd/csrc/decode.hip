@@ -24,6 +24,8 @@
 
 namespace moe {
 
+constexpr int kStreamWaves = 4;
+constexpr int kStreamThreads = 64 * kStreamWaves;
 constexpr int kPlanThreads = 1024;
 constexpr int kPlanMaxPairs = 256 * 16;
 constexpr int kPlanMaxExperts = 512;
@@ -106,54 +108,46 @@ __global__ __launch_bounds__(kPlanThreads) void decode_plan_kernel(const float* 
 }
 
 // --------------------------------------------------------------- products ---
-// Chunk depth: both chunks of a wave's loads fit about 128 registers.
-template <class Op, int NW, int NT>
-constexpr int stream_depth() {
-  constexpr int u = 16 / (NW + NT * Op::kX);
-  return u > 4 ? 4 : u < 1 ? 1 : u;
+// Byte offset of the entry's token row i (a row past its end: its last one):
+// pair list[i], at (pair / div) * pitch.
+__device__ __forceinline__ uint32_t decode_row(const DecodePlan& p, int4 ent, int i, int div, uint32_t pitch) {
+  return (uint32_t)(p.list[ent.y + min(i, ent.z - 1)] / div) * pitch;
 }
 
-// Offsets of this lane's token rows: row i of the entry is pair list[i], at
-// (pair / div) * pitch.
-template <int NT>
-__device__ __forceinline__ void decode_rows(const DecodePlan& p, int4 ent, int div, uint32_t pitch,
-                                            uint32_t (&xoff)[NT]) {
-#pragma unroll
-  for (int j = 0; j < NT; ++j) {
-    const int i = 16 * j + (threadIdx.x & 15);
-    xoff[j] = i < ent.z ? (uint32_t)(p.list[ent.y + i] / div) * pitch : kNoRow;
-  }
+// LDS of a product kernel: the waves' lines, then the sums of G groups.
+template <class Op, int NW, int NT, int G>
+constexpr int product_lds() {
+  return kStreamWaves * imax(stream_line_bytes<Op, NW, NT>(), G * NT * 1024);
 }
 
 // Layer0 of one entry: 16 NF columns of h for its rows.  NP: bf16 planes of
 // h (0: f32).
 template <class Op, int NF, int NT, int NP>
-__device__ __forceinline__ void decode_l0_tile(const DecodeArgs& a, int4 ent, f32x4_t* lds) {
+__device__ __forceinline__ void decode_l0_tile(const DecodeArgs& a, int4 ent, char* lds) {
   const int f0 = blockIdx.x * 16 * NF;
-  uint32_t xoff[NT];
-  decode_rows<NT>(a.plan, ent, a.plan.k, a.x_pitch, xoff);
   StreamArgs s{};
   s.row_bytes = a.x_pitch;  // a gate or up row is as long as a row of x, in the same type
   const int64_t at = ((int64_t)ent.x * a.F + f0) * (int64_t)s.row_bytes;
   s.w0 = reinterpret_cast<const char*>(a.w_gate) + at;
   s.w1 = reinterpret_cast<const char*>(a.w_up) + at;
-  s.w_bytes = 16u * NF * s.row_bytes;
+  s.w_rows = 16 * NF;
   s.x = a.x;
   s.x_bytes = (uint32_t)a.plan.M * a.x_pitch;
-  s.steps = a.H / Op::kStep;
+  s.lines = a.H / Op::kLine;
   f32x4_t acc[2 * NF][NT];
-  stream_tile<Op, 2 * NF, NF, NT, stream_depth<Op, 2 * NF, NT>()>(s, xoff, acc);
-  stream_put<2 * NF, NT>(acc, lds);
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  for (int t = wave; t < NF * NT; t += kStreamWaves) {
-    const f32x4_t g = stream_sum(lds, t), u = stream_sum(lds, t + NF * NT);
-    const int i = 16 * (t % NT) + (lane & 15);
-    if (i >= ent.z) continue;
+  const int wave = uniform(threadIdx.x >> 6);
+  stream_tile<Op, kStreamWaves, 2 * NF, true, NT>(
+      s, [&](int i) { return decode_row(a.plan, ent, i, a.plan.k, a.x_pitch); },
+      lds + wave * stream_line_bytes<Op, 2 * NF, NT>(), acc);
+  const int lane = threadIdx.x & 63;
+  stream_reduce<kStreamWaves, 2 * NF, NT, 2, 2>(acc, reinterpret_cast<f32x4_t*>(lds), [&](int grp, int j, const f32x4_t (&gu)[2]) {
+    const int i = 16 * j + (lane & 15);
+    if (i >= ent.z) return;
     const int64_t pair = a.plan.list[ent.y + i];
-    const int col = f0 + 16 * (t / NT) + 4 * (lane >> 4);
+    const int col = f0 + 8 * grp + 4 * (lane >> 4);
     f32x4_t h;
 #pragma unroll
-    for (int v = 0; v < 4; ++v) h[v] = silu_f32(g[v]) * u[v];
+    for (int v = 0; v < 4; ++v) h[v] = silu_f32(gu[0][v]) * gu[1][v];
     if constexpr (NP == 0) {
       *reinterpret_cast<f32x4_t*>(reinterpret_cast<float*>(a.hact) + pair * a.F + col) = h;
     } else {
@@ -166,12 +160,12 @@ __device__ __forceinline__ void decode_l0_tile(const DecodeArgs& a, int4 ent, f3
         *reinterpret_cast<bf16x4_t*>(reinterpret_cast<__bf16*>(a.hact) + (pair * NP + p) * a.F + col) = o;
       }
     }
-  }
+  });
 }
 
 template <class Op, int NF, int MAXNT, int NP>
 __global__ __launch_bounds__(kStreamThreads) void decode_l0_kernel(DecodeArgs a) {
-  __shared__ f32x4_t lds[kStreamWaves * 2 * NF * MAXNT * 64];
+  __shared__ __attribute__((aligned(16))) char lds[product_lds<Op, 2 * NF, MAXNT, 2>()];
   if ((int)blockIdx.y >= a.plan.hdr[0]) return;
   const int4 ent = a.plan.entries[blockIdx.y];
   if (MAXNT == 1 || ent.z <= 16)
@@ -185,41 +179,38 @@ __global__ __launch_bounds__(kStreamThreads) void decode_l0_kernel(DecodeArgs a)
 // Layer1 of one entry: 16 NF columns of y for its rows (f32, at the pair's
 // own row).
 template <class Op, int NF, int NT, bool MX>
-__device__ __forceinline__ void decode_l1_tile(const DecodeArgs& a, int4 ent, f32x4_t* lds) {
+__device__ __forceinline__ void decode_l1_tile(const DecodeArgs& a, int4 ent, char* lds) {
   const int n0 = blockIdx.x * 16 * NF;
-  uint32_t xoff[NT];
-  decode_rows<NT>(a.plan, ent, 1, a.h_pitch, xoff);
   StreamArgs s{};
   const int64_t row0 = (int64_t)ent.x * a.H + n0;
   s.row_bytes = a.wd_pitch;
-  s.w0 = s.w1 = reinterpret_cast<const char*>(a.w_down) + row0 * s.row_bytes;
-  s.w_bytes = 16u * NF * s.row_bytes;
+  s.w0 = reinterpret_cast<const char*>(a.w_down) + row0 * s.row_bytes;
+  s.w_rows = 16 * NF;
   s.x = a.hact;
   s.x_bytes = (uint32_t)a.plan.M * a.plan.k * a.h_pitch;
   s.plane = 2u * a.F;
-  s.steps = a.F / Op::kStep;
+  s.lines = a.F / Op::kLine;
   if constexpr (MX) {
     s.scale = a.wd_scale + (row0 >> 5) * (int64_t)a.F;
     s.scale_row = (int)(row0 & 31);
-    s.scale_bytes = (uint32_t)((s.scale_row + 16 * NF + 31) / 32) * a.F;
     s.scale_pitch = a.F;
   }
   f32x4_t acc[NF][NT];
-  stream_tile<Op, NF, NF, NT, stream_depth<Op, NF, NT>()>(s, xoff, acc);
-  stream_put<NF, NT>(acc, lds);
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  for (int t = wave; t < NF * NT; t += kStreamWaves) {
-    const f32x4_t y = stream_sum(lds, t);
-    const int i = 16 * (t % NT) + (lane & 15);
-    if (i >= ent.z) continue;
+  const int wave = uniform(threadIdx.x >> 6);
+  stream_tile<Op, kStreamWaves, NF, false, NT>(s, [&](int i) { return decode_row(a.plan, ent, i, 1, a.h_pitch); },
+                                               lds + wave * stream_line_bytes<Op, NF, NT>(), acc);
+  const int lane = threadIdx.x & 63;
+  stream_reduce<kStreamWaves, NF, NT, NF < 2 ? 1 : 2, 1>(acc, reinterpret_cast<f32x4_t*>(lds), [&](int g, int j, const f32x4_t (&y)[1]) {
+    const int i = 16 * j + (lane & 15);
+    if (i >= ent.z) return;
     const int64_t pair = a.plan.list[ent.y + i];
-    *reinterpret_cast<f32x4_t*>(a.y + pair * a.H + n0 + 16 * (t / NT) + 4 * (lane >> 4)) = y;
-  }
+    *reinterpret_cast<f32x4_t*>(a.y + pair * a.H + n0 + 16 * g + 4 * (lane >> 4)) = y[0];
+  });
 }
 
 template <class Op, int NF, int MAXNT, bool MX>
 __global__ __launch_bounds__(kStreamThreads) void decode_l1_kernel(DecodeArgs a) {
-  __shared__ f32x4_t lds[kStreamWaves * NF * MAXNT * 64];
+  __shared__ __attribute__((aligned(16))) char lds[product_lds<Op, NF, MAXNT, (NF < 2 ? 1 : 2)>()];
   if ((int)blockIdx.y >= a.plan.hdr[0]) return;
   const int4 ent = a.plan.entries[blockIdx.y];
   if (MAXNT == 1 || ent.z <= 16)

@@ -3,19 +3,21 @@
 //
 //   acc[i][j] = sum_k W[i, k] X[j, k]    i: 16 NW weight rows, j: 16 NT token rows
 //
-// With few token rows every weight is used once per call, so the tile has no
-// LDS staging: the weight rows are the MFMA "A" operand and go from HBM
-// straight into registers, 16 bytes per lane and load (a 16-row x 64-byte
-// block per wave), and the token rows, the "B" operand, come from the L2 the
-// same way.  The block's waves split the reduction: wave w takes chunks
-// w, w + waves, ... of U steps, so one weight row is read as a contiguous run
-// by the waves together, and the partial accumulators are added in LDS in
-// wave order at the end (a fixed order: the bits do not depend on timing).
-// Two chunks are in flight per wave (one computing, one loading).
-//
-// Token rows that do not exist (row offset kNoRow) and steps past the
-// reduction read zeros through the buffer range check, without touching
-// memory.
+// With few token rows every weight is used once per call, so what counts is
+// that the loads never pause.  The block's waves split the reduction: a line
+// is 128 bytes of every row, wave w takes lines w, w + waves, ...; the partial
+// accumulators are added in LDS in wave order at the end (a fixed order: the
+// bits do not depend on timing).  A wave loads a line of 8 rows with one
+// instruction, 8 lanes of 16 bytes beside each other in a row, keeps one line
+// in flight in registers while it works on the one before, and turns each
+// line to the matrix cores' layout (lane = row, then 16-byte chunk) through a
+// place in LDS of its own, without a barrier.
+//   Loading straight in the matrix cores' layout, where neighbouring lanes
+// are different rows, needs no LDS but gives 38 bytes per ns and CU from the
+// L2; 8 lanes to a row give 124 (measured; HBM gives 27).  With weights and
+// token rows on that path, 200 rows x 4096 x 4096 took 33 us.
+// Rows that do not exist read the last one that does (their sums are not
+// used).
 #pragma once
 
 #include "common.hpp"
@@ -23,9 +25,7 @@
 
 namespace moe {
 
-constexpr int kStreamThreads = 256;
-constexpr int kStreamWaves = kStreamThreads / 64;
-constexpr uint32_t kNoRow = 0x80000000u;  // row offset past every buffer range
+constexpr uint32_t kNoRow = 0x80000000u;  // offset past every buffer range
 
 // f32 value as NP bf16 values whose sum is the value (NP = 3: exactly, but
 // for magnitudes below 2^-110; NP = 2: to 2^-17 of it).
@@ -38,22 +38,21 @@ __device__ __forceinline__ void split_bf16(float v, __bf16 (&p)[NP]) {
   }
 }
 
-// ---- operand kinds: kStep reduction elements a step; a weight row takes 64
-// bytes of every step, 16 of them per lane group q = lane / 16; a token row
-// takes kX loads of 16 bytes per lane at kXBytes a step.
+// ---- operand kinds.  A line of a weight row is kW = 8 chunks of 16 bytes;
+// kLine elements.  A line of a token row is kXC chunks per plane, kP planes.
+// mma: half h (0, 1) of a line; w: the lane's chunk 4 h + q (q = lane / 16)
+// of its weight row; x(c): chunk c of plane p of its token row.
 
 // bf16 weights, token rows in NP bf16 planes (their sum is the row's value).
 template <int NP>
 struct StreamBf16 {
-  static constexpr int kStep = 32, kX = NP, kXBytes = 64, kXLane = 16;
-  static __device__ __forceinline__ void load_x(i32x4_t (&x)[kX], __amdgpu_buffer_rsrc_t r, uint32_t off,
-                                                uint32_t soff, uint32_t plane) {
-#pragma unroll
-    for (int p = 0; p < NP; ++p) x[p] = buf_load16(r, off + (uint32_t)p * plane, soff);
-  }
+  static constexpr int kLine = 64, kP = NP, kXC = 8;
+  static constexpr bool kMx = false;
+  // x chunks that go with half h: one per plane
+  static constexpr int kXH = 1;
+  static __device__ __forceinline__ int x_chunk(int h, int q, int) { return 4 * h + q; }
   template <int NT>
-  static __device__ __forceinline__ void mma(f32x4_t (&acc)[NT], const i32x4_t& w, uint32_t, int,
-                                             const i32x4_t (&x)[NT][kX]) {
+  static __device__ __forceinline__ void mma(f32x4_t (&acc)[NT], const i32x4_t& w, float, const i32x4_t (&x)[NT][NP]) {
     const bf16x8_t a = __builtin_bit_cast(bf16x8_t, w);
 #pragma unroll
     for (int p = 0; p < NP; ++p)
@@ -66,14 +65,12 @@ struct StreamBf16 {
 // f32 weights and token rows: a lane's 4 consecutive elements feed 4 MFMAs
 // of K = 4 (both operands in the same permuted order of k).
 struct StreamF32 {
-  static constexpr int kStep = 16, kX = 1, kXBytes = 64, kXLane = 16;
-  static __device__ __forceinline__ void load_x(i32x4_t (&x)[kX], __amdgpu_buffer_rsrc_t r, uint32_t off,
-                                                uint32_t soff, uint32_t) {
-    x[0] = buf_load16(r, off, soff);
-  }
+  static constexpr int kLine = 32, kP = 1, kXC = 8;
+  static constexpr bool kMx = false;
+  static constexpr int kXH = 1;
+  static __device__ __forceinline__ int x_chunk(int h, int q, int) { return 4 * h + q; }
   template <int NT>
-  static __device__ __forceinline__ void mma(f32x4_t (&acc)[NT], const i32x4_t& w, uint32_t, int,
-                                             const i32x4_t (&x)[NT][kX]) {
+  static __device__ __forceinline__ void mma(f32x4_t (&acc)[NT], const i32x4_t& w, float, const i32x4_t (&x)[NT][1]) {
     const f32x4_t a = __builtin_bit_cast(f32x4_t, w);
 #pragma unroll
     for (int i = 0; i < 4; ++i)
@@ -86,34 +83,25 @@ struct StreamF32 {
 // MXFP8 weights (e4m3 codes, one scale byte per 32), token rows in NP bf16
 // planes.  A lane's 16 codes are two bf16 fragments: the conversion applies
 // the block's power-of-two scale, and every e4m3 value times it is a bf16
-// value (3 bits of mantissa), so nothing is rounded.  Fragment s takes the
-// codes 8 s .. 8 s + 7 of every lane group; the token loads follow.
+// value (3 bits of mantissa), so nothing is rounded.
 template <int NP>
 struct StreamMx {
-  static constexpr int kStep = 64, kX = 2 * NP, kXBytes = 128, kXLane = 32;
-  static __device__ __forceinline__ void load_x(i32x4_t (&x)[kX], __amdgpu_buffer_rsrc_t r, uint32_t off,
-                                                uint32_t soff, uint32_t plane) {
-#pragma unroll
-    for (int p = 0; p < NP; ++p)
-#pragma unroll
-      for (int s = 0; s < 2; ++s) x[2 * p + s] = buf_load16(r, off + (uint32_t)p * plane + 16u * s, soff);
-  }
-  // scales: the 4 scale bytes of the lane's row for the 128 columns the step
-  // lies in; byte: which of them holds the lane's block
+  static constexpr int kLine = 128, kP = NP, kXC = 16;
+  static constexpr bool kMx = true;
+  static constexpr int kXH = 2;
+  static __device__ __forceinline__ int x_chunk(int h, int q, int s) { return 2 * (4 * h + q) + s; }
   template <int NT>
-  static __device__ __forceinline__ void mma(f32x4_t (&acc)[NT], const i32x4_t& w, uint32_t scales, int byte,
-                                             const i32x4_t (&x)[NT][kX]) {
+  static __device__ __forceinline__ void mma(f32x4_t (&acc)[NT], const i32x4_t& w, float scale,
+                                             const i32x4_t (&x)[NT][2 * NP]) {
     typedef __bf16 bf16x2_t __attribute__((ext_vector_type(2)));
-    const uint32_t e = (scales >> (8 * byte)) & 0xFFu;
-    const float sc = __builtin_bit_cast(float, e << 23);
 #pragma unroll
     for (int s = 0; s < 2; ++s) {
       bf16x8_t a;
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         const uint32_t c = (uint32_t)w[2 * s + h];
-        const bf16x2_t lo = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(c, sc, false);
-        const bf16x2_t hi = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(c, sc, true);
+        const bf16x2_t lo = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(c, scale, false);
+        const bf16x2_t hi = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(c, scale, true);
         a[4 * h] = lo[0];
         a[4 * h + 1] = lo[1];
         a[4 * h + 2] = hi[0];
@@ -123,132 +111,170 @@ struct StreamMx {
       for (int p = 0; p < NP; ++p)
 #pragma unroll
         for (int j = 0; j < NT; ++j)
-          acc[j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, __builtin_bit_cast(bf16x8_t, x[j][2 * p + s]), acc[j], 0,
+          acc[j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, __builtin_bit_cast(bf16x8_t, x[j][p * 2 + s]), acc[j], 0,
                                                            0, 0);
     }
   }
 };
 
-template <class Op>
-struct StreamTraits {
-  static constexpr bool kMx = Op::kXLane == 32;
-};
-
 // The rows a tile reads.
 struct StreamArgs {
-  const void* w0;        // first weight row of groups 0 .. NW0 - 1 (16 rows each)
-  const void* w1;        // first weight row of groups NW0 .. NW - 1
-  uint32_t w_bytes;      // bytes of the weight rows that exist at w0 and at w1
+  const void* w0;        // first weight row; PAIRED: of the even groups of 16 rows
+  const void* w1;        // PAIRED: first weight row of the odd groups
+  int w_rows;            // weight rows that exist there (>= 1)
   uint32_t row_bytes;    // bytes of a weight row
   const void* x;         // base of the token rows
-  uint32_t x_bytes;      // bytes that exist there (at most 2^31)
+  uint32_t x_bytes;      // bytes that exist there (below 2^31)
   uint32_t plane;        // bytes between the planes of a token row
-  int steps;             // K / Op::kStep
+  int lines;             // K / Op::kLine
   const uint8_t* scale;  // MXFP8: scale bytes of the 32-row group that holds weight row 0
-  uint32_t scale_bytes;
   int scale_row;         // row of that group which is weight row 0 (0 or 16)
   uint32_t scale_pitch;  // bytes of a 32-row group (= K)
 };
 
-// The wave's share of the tile.  xoff[j]: byte offset of this lane's token
-// row (row 16 j + lane % 16 of the tile) from a.x, or kNoRow.
-template <class Op, int NW, int NW0, int NT, int U>
-__device__ __forceinline__ void stream_tile(const StreamArgs& a, const uint32_t (&xoff)[NT], f32x4_t (&acc)[NW][NT]) {
-  constexpr bool MX = StreamTraits<Op>::kMx;
+// Bytes of LDS of one wave: a line of the weight rows and of the token rows.
+template <class Op, int NW, int NT>
+constexpr int stream_line_bytes() {
+  return 16 * (NW * 128 + NT * Op::kP * Op::kXC * 16);
+}
+
+// The share of the tile of one of WAVES waves (the block has WAVES).  Weight
+// group g is rows 16 g .. of w0, or, PAIRED, rows 16 (g / 2) .. of w0 (g even)
+// or w1 (g odd).  row_off(i): byte offset from a.x of token row i (0 <= i <
+// 16 NT), any row for one that does not exist.  lds: stream_line_bytes() of
+// the wave's own.
+template <class Op, int WAVES, int NW, bool PAIRED, int NT, class RowOff>
+__device__ __forceinline__ void stream_tile(const StreamArgs& a, RowOff row_off, char* __restrict__ lds,
+                                            f32x4_t (&acc)[NW][NT]) {
+  constexpr bool MX = Op::kMx;
+  constexpr int XC = Op::kXC, XR = 64 / XC;            // chunks of a token row; token rows per load
+  constexpr int XL = 16 / XR;                          // loads per 16 token rows and plane
+  constexpr int XPITCH = XC * 16;
   const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
   const int r = lane & 15, q = lane >> 4;
-  uint32_t woff[NW], xo[NT], so[NW];
+  // Chunk c of row i sits at place c ^ swz(i): 16 rows read at one chunk, and
+  // 8 (or 4) whole rows written, hit every bank once.
+  auto swz_w = [](int i) { return (i >> 1) & 7; };
+  auto swz_x = [](int i) { return XC == 8 ? (i >> 1) & 7 : i & 15; };
+  uint32_t woff[2 * NW], xo[XL * NT];
+#pragma unroll
+  for (int l = 0; l < 2 * NW; ++l) {
+    const int i = 8 * (l & 1) + (lane >> 3), grp = PAIRED ? l >> 2 : l >> 1;
+    woff[l] = (uint32_t)min(16 * grp + i, a.w_rows - 1) * a.row_bytes + 16u * ((lane & 7) ^ swz_w(i));
+  }
+#pragma unroll
+  for (int l = 0; l < XL * NT; ++l) {
+    const int i = XR * (l % XL) + lane / XC;
+    xo[l] = row_off(16 * (l / XL) + i) + 16u * ((lane % XC) ^ swz_x(i));
+  }
+  uint32_t so[NW];
 #pragma unroll
   for (int g = 0; g < NW; ++g) {
-    const int row = (g < NW0 ? g : g - NW0) * 16 + r;
-    woff[g] = (uint32_t)row * a.row_bytes + 16u * q;
     if (MX) {
-      const int sr = a.scale_row + row;
+      const int sr = a.scale_row + min(16 * g + r, a.w_rows - 1);
       so[g] = (uint32_t)(sr >> 5) * a.scale_pitch + 4u * (sr & 31);
     }
+#pragma unroll
+    for (int j = 0; j < NT; ++j) acc[g][j] = f32x4_t{0.f, 0.f, 0.f, 0.f};
   }
-#pragma unroll
-  for (int j = 0; j < NT; ++j) {
-    xo[j] = xoff[j] + (uint32_t)Op::kXLane * q;
-#pragma unroll
-    for (int g = 0; g < NW; ++g) acc[g][j] = f32x4_t{0.f, 0.f, 0.f, 0.f};
-  }
-  struct Chunk {
-    i32x4_t w[U][NW];
-    i32x4_t x[U][NT][Op::kX];
-    uint32_t s[MX ? U : 1][NW];
+  const uint32_t w_bytes = (uint32_t)a.w_rows * a.row_bytes;
+  const __amdgpu_buffer_rsrc_t r0 = make_rsrc(a.w0, w_bytes), r1 = make_rsrc(PAIRED ? a.w1 : a.w0, w_bytes);
+  const __amdgpu_buffer_rsrc_t rx = make_rsrc(a.x, a.x_bytes);
+  struct Line {
+    i32x4_t w[2 * NW];
+    i32x4_t x[Op::kP][XL * NT];
+    uint32_t s[MX ? NW : 1];
   };
-  auto load = [&](Chunk& c, int chunk) {
-    const int s0 = chunk * U;
+  auto load = [&](Line& c, int line) {
+    const uint32_t at = (uint32_t)min(line, a.lines - 1);  // past the last: any line, not used
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      // steps past the reduction read zeros: an empty range, at offset 0 (the
-      // range check may subtract the scalar offset from the range)
-      const bool live = s0 + u < a.steps;
-      const uint32_t soff = live ? (uint32_t)(s0 + u) * 64u : 0u;
-      const __amdgpu_buffer_rsrc_t r0 = make_rsrc(a.w0, live ? a.w_bytes : 0u);
-      const __amdgpu_buffer_rsrc_t r1 = make_rsrc(a.w1, live ? a.w_bytes : 0u);
-#pragma unroll
-      for (int g = 0; g < NW; ++g) c.w[u][g] = buf_load16(g < NW0 ? r0 : r1, woff[g], soff);
-      if constexpr (MX) {
-        // 4 scale bytes of a row per 128 columns, i.e. per two steps
-        const __amdgpu_buffer_rsrc_t rs = make_rsrc(a.scale, live ? a.scale_bytes : 0u);
-#pragma unroll
-        for (int g = 0; g < NW; ++g)
-          c.s[u][g] = __builtin_amdgcn_raw_buffer_load_b32(rs, (int)so[g], live ? ((s0 + u) >> 1) * 128 : 0, 0);
-      }
-    }
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const bool live = s0 + u < a.steps;
-      const uint32_t soff = live ? (uint32_t)(s0 + u) * (uint32_t)Op::kXBytes : 0u;
-      const __amdgpu_buffer_rsrc_t rx = make_rsrc(a.x, live ? a.x_bytes : 0u);
-#pragma unroll
-      for (int j = 0; j < NT; ++j) Op::load_x(c.x[u][j], rx, xo[j], soff, a.plane);
-    }
-  };
-  auto compute = [&](const Chunk& c, int chunk) {
-#pragma unroll
-    for (int u = 0; u < U; ++u)
+    for (int l = 0; l < 2 * NW; ++l) c.w[l] = buf_load16(PAIRED && (l & 2) ? r1 : r0, woff[l], at * 128u);
+    if constexpr (MX) {
 #pragma unroll
       for (int g = 0; g < NW; ++g)
-        Op::template mma<NT>(acc[g], c.w[u][g], MX ? c.s[u][g] : 0u, 2 * ((chunk * U + u) & 1) + (q >> 1), c.x[u]);
+        c.s[g] = *reinterpret_cast<const uint32_t*>(a.scale + so[g] + at * 128u);  // the row's 4 blocks of the line
+    }
+#pragma unroll
+    for (int p = 0; p < Op::kP; ++p)
+#pragma unroll
+      for (int l = 0; l < XL * NT; ++l) c.x[p][l] = buf_load16(rx, xo[l] + (uint32_t)p * a.plane, at * (uint32_t)XPITCH);
   };
-  const int chunks = (a.steps + U - 1) / U;
-  Chunk ca, cb;
+  char* const ldx = lds + NW * 2048;
+  auto compute = [&](const Line& c) {
+#pragma unroll
+    for (int l = 0; l < 2 * NW; ++l) *reinterpret_cast<i32x4_t*>(lds + l * 1024 + lane * 16) = c.w[l];
+#pragma unroll
+    for (int p = 0; p < Op::kP; ++p)
+#pragma unroll
+      for (int l = 0; l < XL * NT; ++l)
+        *reinterpret_cast<i32x4_t*>(ldx + (p * XL * NT + l) * 1024 + lane * 16) = c.x[p][l];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      i32x4_t x[NT][Op::kXH * Op::kP];
+#pragma unroll
+      for (int p = 0; p < Op::kP; ++p)
+#pragma unroll
+        for (int j = 0; j < NT; ++j)
+#pragma unroll
+          for (int t = 0; t < Op::kXH; ++t)
+            x[j][p * Op::kXH + t] = *reinterpret_cast<const i32x4_t*>(
+                ldx + ((p * NT + j) * 16 + r) * XPITCH + ((Op::x_chunk(h, q, t) ^ swz_x(r)) << 4));
+#pragma unroll
+      for (int g = 0; g < NW; ++g) {
+        const i32x4_t w = *reinterpret_cast<const i32x4_t*>(lds + (16 * g + r) * 128 + (((4 * h + q) ^ swz_w(r)) << 4));
+        // MXFP8: the scale byte of the lane's block of 32, as a power of two
+        const float sc = MX ? __builtin_bit_cast(float, ((c.s[MX ? g : 0] >> (8 * (2 * h + (q >> 1)))) & 0xFFu) << 23) : 0.f;
+        Op::template mma<NT>(acc[g], w, sc, x);
+      }
+    }
+  };
+  Line ca, cb;
   load(ca, wave);
-  for (int c = wave; c < chunks; c += 2 * kStreamWaves) {
-    load(cb, c + kStreamWaves);
+  for (int c = wave; c < a.lines; c += 2 * WAVES) {
+    load(cb, c + WAVES);
     __builtin_amdgcn_sched_barrier(0);
-    compute(ca, c);
+    compute(ca);
     __builtin_amdgcn_sched_barrier(0);
-    load(ca, c + 2 * kStreamWaves);
+    load(ca, c + 2 * WAVES);
     __builtin_amdgcn_sched_barrier(0);
-    compute(cb, c + kStreamWaves);
+    if (c + WAVES < a.lines) compute(cb);
     __builtin_amdgcn_sched_barrier(0);
   }
 }
 
-// The waves' accumulators, added in wave order in LDS: stream_put (all
-// threads, then a barrier), then stream_sum(t) for tile t = g * NT + j gives
-// the lane weight rows 16 g + 4 (lane / 16) + 0..3 of token row 16 j + lane
-// % 16.  lds: kStreamWaves * NW * NT KiB.
-template <int NW, int NT>
-__device__ __forceinline__ void stream_put(const f32x4_t (&acc)[NW][NT], f32x4_t* __restrict__ lds) {
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-#pragma unroll
-  for (int g = 0; g < NW; ++g)
-#pragma unroll
-    for (int j = 0; j < NT; ++j) lds[((g * NT + j) * kStreamWaves + wave) * 64 + lane] = acc[g][j];
-  __syncthreads();
-}
+constexpr int imax(int a, int b) { return a > b ? a : b; }
 
-__device__ __forceinline__ f32x4_t stream_sum(const f32x4_t* __restrict__ lds, int t) {
-  const int lane = threadIdx.x & 63;
-  f32x4_t s = lds[(t * kStreamWaves) * 64 + lane];
+// Adds the WAVES partial accumulators in wave order through LDS, G groups of
+// 16 weight rows at a time (lds: WAVES * G * NT KiB), and hands the sums out:
+// visit(g, j, s) with s[0 .. V - 1] the sums of groups g .. g + V - 1 (V = 2:
+// a gate group and its up group; lds may hold the waves' lines: a barrier
+// comes first), lane: weight rows 4 (lane / 16) + 0..3 of
+// the group, token row 16 j + lane % 16.  All threads of the block call it.
+template <int WAVES, int NW, int NT, int G, int V, class F>
+__device__ __forceinline__ void stream_reduce(const f32x4_t (&acc)[NW][NT], f32x4_t* __restrict__ lds, F visit) {
+  static_assert(NW % G == 0 && G % V == 0, "whole rounds");
+  const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
 #pragma unroll
-  for (int w = 1; w < kStreamWaves; ++w) s += lds[(t * kStreamWaves + w) * 64 + lane];
-  return s;
+  for (int g0 = 0; g0 < NW; g0 += G) {
+    __syncthreads();
+#pragma unroll
+    for (int g = 0; g < G; ++g)
+#pragma unroll
+      for (int j = 0; j < NT; ++j) lds[((g * NT + j) * WAVES + wave) * 64 + lane] = acc[g0 + g][j];
+    __syncthreads();
+    for (int t = wave; t < G / V * NT; t += WAVES) {
+      const int g = t / NT * V, j = t % NT;
+      f32x4_t s[V];
+#pragma unroll
+      for (int v = 0; v < V; ++v) {
+        const f32x4_t* at = lds + ((g + v) * NT + j) * WAVES * 64 + lane;
+        s[v] = at[0];
+#pragma unroll
+        for (int w = 1; w < WAVES; ++w) s[v] += at[w * 64];
+      }
+      visit(g0 + g, j, s);
+    }
+  }
 }
 
 }  // namespace moe

@@ -101,6 +101,8 @@ def linear(x, w, a, b, scale, idx, residual, f32, out_bf16):
         A, B, s = a[p].double(), b[p].double(), float(scale[p])
         t = s * (x[rows] @ A.T)
         et = (n + 1) * U * abs(s) * (x[rows].abs() @ A.abs().T)
+        if out_bf16 and not f32:  # long batches: two planes of t
+            et = et + BF16 * BF16 * t.abs()
         r = A.shape[0]
         at = t.abs() @ B.abs().T
         out[rows] += t @ B.T
