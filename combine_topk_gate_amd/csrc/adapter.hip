@@ -51,7 +51,7 @@ __global__ __launch_bounds__(64 * WAVES) void adapter_shrink_kernel(AdapterArgs 
     // (rows of other adapters are computed too, and not stored)
     s.w0 = reinterpret_cast<const char*>(a.a) + ((int64_t)mine * a.r + j0) * a.row_bytes;
     f32x4_t acc[NW][NT];
-    stream_tile<Op, WAVES, NW, false, NT>(s, [&](int m) { return (uint32_t)min(m, rows - 1) * a.row_bytes; },
+    stream_tile<Op, WAVES, NW, false, NT, 2>(s, [&](int m) { return (uint32_t)min(m, rows - 1) * a.row_bytes; },
                                           lds + wave * stream_line_bytes<Op, NW, NT>(), acc);
     const float sc = a.scale[mine];
     stream_reduce<WAVES, NW, NT, NW, 1>(acc, reinterpret_cast<f32x4_t*>(lds), [&](int g, int jt, const f32x4_t (&t)[1]) {
@@ -130,7 +130,7 @@ __global__ __launch_bounds__(64 * WAVES) void adapter_stream_kernel(AdapterArgs 
   s.x_bytes = (uint32_t)rows * a.row_bytes;
   s.lines = a.H / Op::kLine;
   f32x4_t acc[NW][NT];
-  stream_tile<Op, WAVES, NW, false, NT>(s, [&](int m) { return (uint32_t)min(m, rows - 1) * a.row_bytes; },
+  stream_tile<Op, WAVES, NW, false, NT, 2>(s, [&](int m) { return (uint32_t)min(m, rows - 1) * a.row_bytes; },
                                         lds + uniform(threadIdx.x >> 6) * stream_line_bytes<Op, NW, NT>(), acc);
   stream_reduce<WAVES, NW, NT, G, 1>(acc, reinterpret_cast<f32x4_t*>(lds), [&](int g, int j, const f32x4_t (&sum)[1]) {
     f32x4_t v = sum[0];
@@ -153,14 +153,14 @@ static void launch_shrink_as(const AdapterArgs& a, unsigned slots, hipStream_t s
 // Short batches: a block of 16 waves for every adapter that 16 rows can have.
 // Long ones: the largest tile that still gives a block for every CU (x is
 // read once per 16 NW of the rank, A once per 16 NT rows), which takes its
-// rows' adapters in turn.
+// rows' adapters in turn, half of them each where the blocks leave room.
 template <class Op>
 static void launch_shrink(const AdapterArgs& a, hipStream_t s) {
   const int64_t cus = device_cu_count();
   auto blocks = [&](int nw, int nt) {
     return ((a.M + 16 * nt - 1) / (16 * nt)) * ((a.r + 16 * nw - 1) / (16 * nw));
   };
-  if (a.M <= 256) {
+  if (a.M <= 512) {
     if (a.r <= 16)
       launch_shrink_as<Op, 16, 1, 1>(a, 16, s);
     else

@@ -136,7 +136,7 @@ __device__ __forceinline__ void decode_l0_tile(const DecodeArgs& a, int4 ent, ch
   s.lines = a.H / Op::kLine;
   f32x4_t acc[2 * NF][NT];
   const int wave = uniform(threadIdx.x >> 6);
-  stream_tile<Op, kStreamWaves, 2 * NF, true, NT>(
+  stream_tile<Op, kStreamWaves, 2 * NF, true, NT, 4>(
       s, [&](int i) { return decode_row(a.plan, ent, i, a.plan.k, a.x_pitch); },
       lds + wave * stream_line_bytes<Op, 2 * NF, NT>(), acc);
   const int lane = threadIdx.x & 63;
@@ -197,7 +197,7 @@ __device__ __forceinline__ void decode_l1_tile(const DecodeArgs& a, int4 ent, ch
   }
   f32x4_t acc[NF][NT];
   const int wave = uniform(threadIdx.x >> 6);
-  stream_tile<Op, kStreamWaves, NF, false, NT>(s, [&](int i) { return decode_row(a.plan, ent, i, 1, a.h_pitch); },
+  stream_tile<Op, kStreamWaves, NF, false, NT, 4>(s, [&](int i) { return decode_row(a.plan, ent, i, 1, a.h_pitch); },
                                                lds + wave * stream_line_bytes<Op, NF, NT>(), acc);
   const int lane = threadIdx.x & 63;
   stream_reduce<kStreamWaves, NF, NT, NF < 2 ? 1 : 2, 1>(acc, reinterpret_cast<f32x4_t*>(lds), [&](int g, int j, const f32x4_t (&y)[1]) {

@@ -8,10 +8,10 @@
 // is 128 bytes of every row, wave w takes lines w, w + waves, ...; the partial
 // accumulators are added in LDS in wave order at the end (a fixed order: the
 // bits do not depend on timing).  A wave loads a line of 8 rows with one
-// instruction, 8 lanes of 16 bytes beside each other in a row, keeps one line
-// in flight in registers while it works on the one before, and turns each
-// line to the matrix cores' layout (lane = row, then 16-byte chunk) through a
-// place in LDS of its own, without a barrier.
+// instruction, 8 lanes of 16 bytes beside each other in a row, keeps DEPTH
+// lines in flight in registers, and turns each to the matrix cores' layout
+// (lane = row, then 16-byte chunk) through a place in LDS of its own, without
+// a barrier.
 //   Loading straight in the matrix cores' layout, where neighbouring lanes
 // are different rows, needs no LDS but gives 38 bytes per ns and CU from the
 // L2; 8 lanes to a row give 124 (measured; HBM gives 27).  With weights and
@@ -142,8 +142,17 @@ constexpr int stream_line_bytes() {
 // group g is rows 16 g .. of w0, or, PAIRED, rows 16 (g / 2) .. of w0 (g even)
 // or w1 (g odd).  row_off(i): byte offset from a.x of token row i (0 <= i <
 // 16 NT), any row for one that does not exist.  lds: stream_line_bytes() of
-// the wave's own.
-template <class Op, int WAVES, int NW, bool PAIRED, int NT, class RowOff>
+// the wave's own.  DEPTH: lines in flight (as many as about 96 registers hold,
+// at most): 4 where the weights come from HBM for long (decode, 2 experts of
+// 4096 x 14336: 81 us for Layer0 instead of 84), 2 for short streams, where
+// filling and draining the pipe costs more (333 x 2048 x 1408: 13 us, 17).
+template <class Op, int NW, int NT, int DEPTH>
+constexpr int stream_depth() {
+  constexpr int regs = 4 * (2 * NW + Op::kP * (Op::kXC / 4) * NT), d = 96 / regs;
+  return d > DEPTH ? DEPTH : d < 1 ? 1 : d;
+}
+
+template <class Op, int WAVES, int NW, bool PAIRED, int NT, int DEPTH, class RowOff>
 __device__ __forceinline__ void stream_tile(const StreamArgs& a, RowOff row_off, char* __restrict__ lds,
                                             f32x4_t (&acc)[NW][NT]) {
   constexpr bool MX = Op::kMx;
@@ -178,15 +187,19 @@ __device__ __forceinline__ void stream_tile(const StreamArgs& a, RowOff row_off,
     for (int j = 0; j < NT; ++j) acc[g][j] = f32x4_t{0.f, 0.f, 0.f, 0.f};
   }
   const uint32_t w_bytes = (uint32_t)a.w_rows * a.row_bytes;
-  const __amdgpu_buffer_rsrc_t r0 = make_rsrc(a.w0, w_bytes), r1 = make_rsrc(PAIRED ? a.w1 : a.w0, w_bytes);
-  const __amdgpu_buffer_rsrc_t rx = make_rsrc(a.x, a.x_bytes);
   struct Line {
     i32x4_t w[2 * NW];
     i32x4_t x[Op::kP][XL * NT];
     uint32_t s[MX ? NW : 1];
   };
   auto load = [&](Line& c, int line) {
-    const uint32_t at = (uint32_t)min(line, a.lines - 1);  // past the last: any line, not used
+    // past the last line: nothing is read (an empty range, at offset 0: the
+    // range check may take the scalar offset from the range)
+    const bool live = line < a.lines;
+    const uint32_t at = live ? (uint32_t)line : 0u;
+    const __amdgpu_buffer_rsrc_t r0 = make_rsrc(a.w0, live ? w_bytes : 0u);
+    const __amdgpu_buffer_rsrc_t r1 = make_rsrc(PAIRED ? a.w1 : a.w0, live ? w_bytes : 0u);
+    const __amdgpu_buffer_rsrc_t rx = make_rsrc(a.x, live ? a.x_bytes : 0u);
 #pragma unroll
     for (int l = 0; l < 2 * NW; ++l) c.w[l] = buf_load16(PAIRED && (l & 2) ? r1 : r0, woff[l], at * 128u);
     if constexpr (MX) {
@@ -200,45 +213,56 @@ __device__ __forceinline__ void stream_tile(const StreamArgs& a, RowOff row_off,
       for (int l = 0; l < XL * NT; ++l) c.x[p][l] = buf_load16(rx, xo[l] + (uint32_t)p * a.plane, at * (uint32_t)XPITCH);
   };
   char* const ldx = lds + NW * 2048;
-  auto compute = [&](const Line& c) {
+  constexpr int D = stream_depth<Op, NW, NT, DEPTH>();
+  Line ring[D];
 #pragma unroll
-    for (int l = 0; l < 2 * NW; ++l) *reinterpret_cast<i32x4_t*>(lds + l * 1024 + lane * 16) = c.w[l];
+  for (int d = 0; d < D; ++d) {
+    load(ring[d], wave + d * WAVES);
+    __builtin_amdgcn_sched_barrier(0);
+  }
+  for (int c = wave; c < a.lines; c += D * WAVES) {
 #pragma unroll
-    for (int p = 0; p < Op::kP; ++p)
+    for (int d = 0; d < D; ++d) {
+      Line& n = ring[d];
 #pragma unroll
-      for (int l = 0; l < XL * NT; ++l)
-        *reinterpret_cast<i32x4_t*>(ldx + (p * XL * NT + l) * 1024 + lane * 16) = c.x[p][l];
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      i32x4_t x[NT][Op::kXH * Op::kP];
+      for (int l = 0; l < 2 * NW; ++l) *reinterpret_cast<i32x4_t*>(lds + l * 1024 + lane * 16) = n.w[l];
 #pragma unroll
       for (int p = 0; p < Op::kP; ++p)
 #pragma unroll
-        for (int j = 0; j < NT; ++j)
+        for (int l = 0; l < XL * NT; ++l)
+          *reinterpret_cast<i32x4_t*>(ldx + (p * XL * NT + l) * 1024 + lane * 16) = n.x[p][l];
+      uint32_t scales[MX ? NW : 1];
+      if constexpr (MX) {
 #pragma unroll
-          for (int t = 0; t < Op::kXH; ++t)
-            x[j][p * Op::kXH + t] = *reinterpret_cast<const i32x4_t*>(
-                ldx + ((p * NT + j) * 16 + r) * XPITCH + ((Op::x_chunk(h, q, t) ^ swz_x(r)) << 4));
-#pragma unroll
-      for (int g = 0; g < NW; ++g) {
-        const i32x4_t w = *reinterpret_cast<const i32x4_t*>(lds + (16 * g + r) * 128 + (((4 * h + q) ^ swz_w(r)) << 4));
-        // MXFP8: the scale byte of the lane's block of 32, as a power of two
-        const float sc = MX ? __builtin_bit_cast(float, ((c.s[MX ? g : 0] >> (8 * (2 * h + (q >> 1)))) & 0xFFu) << 23) : 0.f;
-        Op::template mma<NT>(acc[g], w, sc, x);
+        for (int g = 0; g < NW; ++g) scales[g] = n.s[g];
       }
+      __builtin_amdgcn_sched_barrier(0);
+      load(n, c + (d + D) * WAVES);
+      __builtin_amdgcn_sched_barrier(0);
+      // (a line past the last one is zeros: it adds nothing)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        i32x4_t x[NT][Op::kXH * Op::kP];
+#pragma unroll
+        for (int p = 0; p < Op::kP; ++p)
+#pragma unroll
+          for (int j = 0; j < NT; ++j)
+#pragma unroll
+            for (int t = 0; t < Op::kXH; ++t)
+              x[j][p * Op::kXH + t] = *reinterpret_cast<const i32x4_t*>(
+                  ldx + ((p * NT + j) * 16 + r) * XPITCH + ((Op::x_chunk(h, q, t) ^ swz_x(r)) << 4));
+#pragma unroll
+        for (int g = 0; g < NW; ++g) {
+          const i32x4_t w =
+              *reinterpret_cast<const i32x4_t*>(lds + (16 * g + r) * 128 + (((4 * h + q) ^ swz_w(r)) << 4));
+          // MXFP8: the scale byte of the lane's block of 32, as a power of two
+          const float sc =
+              MX ? __builtin_bit_cast(float, ((scales[MX ? g : 0] >> (8 * (2 * h + (q >> 1)))) & 0xFFu) << 23) : 0.f;
+          Op::template mma<NT>(acc[g], w, sc, x);
+        }
+      }
+      __builtin_amdgcn_sched_barrier(0);
     }
-  };
-  Line ca, cb;
-  load(ca, wave);
-  for (int c = wave; c < a.lines; c += 2 * WAVES) {
-    load(cb, c + WAVES);
-    __builtin_amdgcn_sched_barrier(0);
-    compute(ca);
-    __builtin_amdgcn_sched_barrier(0);
-    load(ca, c + 2 * WAVES);
-    __builtin_amdgcn_sched_barrier(0);
-    if (c + WAVES < a.lines) compute(cb);
-    __builtin_amdgcn_sched_barrier(0);
   }
 }
 
