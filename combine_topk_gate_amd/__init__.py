@@ -276,31 +276,47 @@ def moe_layer_ex(p, x, logits, src_block, w_gate, w_up, w_down, epi, out, ws, au
                                        _nbytes(ws), _stream(stream)), "moe_layer_ex")
 
 
-def _operands(what, device, **given):
-    """Refuses (MOE_ERR_INVALID_ARGUMENT) a tensor that is not on `device` (a
-    GPU), not contiguous, or not of the shape and type the call reads.  given: name
-    = (tensor, type, shape); the tensor or a part of its shape may be None."""
-    for name, (t, dtype, shape) in given.items():
-        if t is None:
-            continue
-        if t.device != device or device.type != "cuda" or not t.is_contiguous() or t.dtype != dtype or \
-                (shape is not None and tuple(t.shape) != tuple(shape)):
-            raise MoeError(MOE_ERR_INVALID_ARGUMENT,
-                           f"{what}: {name} must be a contiguous {dtype} tensor of shape {shape} on {device}, "
-                           f"got {t.dtype} {tuple(t.shape)} strides {t.stride()} on {t.device}")
+def _refuse(what, name, t, dtype, shape, device):
+    raise MoeError(MOE_ERR_INVALID_ARGUMENT,
+                   f"{what}: {name} must be a contiguous {dtype} tensor of shape {shape} on {device}, a GPU; "
+                   f"got {t.dtype} {tuple(t.shape)} strides {t.stride()} on {t.device}")
 
 
-def _call_on(x, stream, call):
-    """call(stream) with x's device current: a stream given is used as it is,
+def _operand(what, name, t, dtype, shape, device):
+    """The data pointer of t (None: NULL), which must be what the call reads:
+    contiguous, of this type and shape (None: any), on this GPU; otherwise
+    MoeError with MOE_ERR_INVALID_ARGUMENT, before the library sees it."""
+    if t is None:
+        return None
+    if t.dtype != dtype or (shape is not None and t.shape != shape) or not t.is_contiguous() or t.device != device:
+        _refuse(what, name, t, dtype, shape, device)
+    return t.data_ptr()
+
+
+def _call_on(device, stream, call):
+    """call(stream) with `device` current: a stream given is used as it is,
     otherwise torch's current stream of that device."""
     import torch
-    with torch.cuda.device(x.device):
-        return call(_stream(stream))
+    if stream is None:
+        raw = torch.cuda.current_stream(device).cuda_stream
+    else:
+        raw = stream if isinstance(stream, int) else stream.cuda_stream
+    if device.index == torch.cuda.current_device():
+        return call(raw)
+    with torch.cuda.device(device):
+        return call(raw)
 
 
-def _epilogue_types(epi):
+def _epilogue_type(epi):
     import torch
     return torch.bfloat16 if epi is not None and epi.out_dtype == MOE_DTYPE_BF16 else torch.float32
+
+
+def _activation_type(what, x, dtype):
+    import torch
+    if not x.is_cuda:
+        _refuse(what, "x", x, "floating", None, "cuda")
+    return torch.float32 if dtype == MOE_DTYPE_F32 else torch.bfloat16
 
 
 def moe_layer_decode(p, x, logits, w_gate, w_up, w_down, epi, out, ws, stream=None):
@@ -309,17 +325,18 @@ def moe_layer_decode(p, x, logits, w_gate, w_up, w_down, epi, out, ws, stream=No
     choose; an all -inf row is idle), epi as in moe_layer_ex or None, ws
     moe_workspace_bytes(p, MOE_OP_LAYER_DECODE) bytes."""
     import torch
-    M, H, F, EL = p.num_tokens, p.hidden, p.ffn, p.local_experts or p.num_experts
-    act = torch.float32 if p.dtype == MOE_DTYPE_F32 else torch.bfloat16
-    mx = p.dtype == MOE_DTYPE_BF16_MXFP8
-    _operands("moe_layer_decode", x.device, x=(x, act, (M, H)), logits=(logits, torch.float32, (M, p.num_experts)),
-              w_gate=(w_gate, act, (EL, F, H)), w_up=(w_up, act, (EL, F, H)),
-              w_down=(w_down, torch.uint8, (mx_bytes(EL * H, F),)) if mx else (w_down, act, (EL, H, F)),
-              out=(out, _epilogue_types(epi), (M, H)), ws=(ws, torch.uint8, None))
-    lib = load_library()
-    _check(_call_on(x, stream, lambda s: lib.moe_layer_decode(
-        ctypes.byref(p), _ptr(x), _ptr(logits), _ptr(w_gate), _ptr(w_up), _ptr(w_down),
-        ctypes.byref(epi) if epi is not None else None, _ptr(out), _ptr(ws), _nbytes(ws), s)), "moe_layer_decode")
+    what = "moe_layer_decode"
+    M, H, F, EL, dev = p.num_tokens, p.hidden, p.ffn, p.local_experts or p.num_experts, x.device
+    act = _activation_type(what, x, p.dtype)
+    down = (torch.uint8, (mx_bytes(EL * H, F),)) if p.dtype == MOE_DTYPE_BF16_MXFP8 else (act, (EL, H, F))
+    a = (_operand(what, "x", x, act, (M, H), dev),
+         _operand(what, "logits", logits, torch.float32, (M, p.num_experts), dev),
+         _operand(what, "w_gate", w_gate, act, (EL, F, H), dev), _operand(what, "w_up", w_up, act, (EL, F, H), dev),
+         _operand(what, "w_down", w_down, *down, dev), ctypes.byref(epi) if epi is not None else None,
+         _operand(what, "out", out, _epilogue_type(epi), (M, H), dev),
+         _operand(what, "ws", ws, torch.uint8, None, dev), 0 if ws is None else ws.numel())
+    f = load_library().moe_layer_decode
+    _check(_call_on(dev, stream, lambda s: f(ctypes.byref(p), *a, s)), what)
 
 
 def moe_adapter_workspace_bytes(q: AdapterProblem) -> int:
@@ -333,16 +350,18 @@ def moe_adapter_linear(q, x, w, a, b, scale, adapter_idx, epi, out, ws, stream=N
     moe_combine_ex or None; ws moe_adapter_workspace_bytes(q) bytes.  With
     num_adapters 0: a, b, scale, adapter_idx and ws may be None."""
     import torch
-    M, H, N, r, P = q.num_tokens, q.in_features, q.out_features, q.rank, q.num_adapters
-    act = torch.float32 if q.dtype == MOE_DTYPE_F32 else torch.bfloat16
-    _operands("moe_adapter_linear", x.device, x=(x, act, (M, H)), w=(w, act, (N, H)), a=(a, act, (P, r, H)),
-              b=(b, act, (P, N, r)), scale=(scale, torch.float32, (P,)),
-              adapter_idx=(adapter_idx, torch.int32, (M,)), out=(out, _epilogue_types(epi), (M, N)),
-              ws=(ws, torch.uint8, None))
-    lib = load_library()
-    _check(_call_on(x, stream, lambda s: lib.moe_adapter_linear(
-        ctypes.byref(q), _ptr(x), _ptr(w), _ptr(a), _ptr(b), _ptr(scale), _ptr(adapter_idx),
-        ctypes.byref(epi) if epi is not None else None, _ptr(out), _ptr(ws), _nbytes(ws), s)), "moe_adapter_linear")
+    what = "moe_adapter_linear"
+    M, H, N, r, P, dev = q.num_tokens, q.in_features, q.out_features, q.rank, q.num_adapters, x.device
+    act = _activation_type(what, x, q.dtype)
+    args = (_operand(what, "x", x, act, (M, H), dev), _operand(what, "w", w, act, (N, H), dev),
+            _operand(what, "a", a, act, (P, r, H), dev), _operand(what, "b", b, act, (P, N, r), dev),
+            _operand(what, "scale", scale, torch.float32, (P,), dev),
+            _operand(what, "adapter_idx", adapter_idx, torch.int32, (M,), dev),
+            ctypes.byref(epi) if epi is not None else None,
+            _operand(what, "out", out, _epilogue_type(epi), (M, N), dev),
+            _operand(what, "ws", ws, torch.uint8, None, dev), 0 if ws is None else ws.numel())
+    f = load_library().moe_adapter_linear
+    _check(_call_on(dev, stream, lambda s: f(ctypes.byref(q), *args, s)), what)
 
 
 def moe_debug_device_status(p, ws, stream=None) -> int:

@@ -236,7 +236,7 @@ int decode_planes(const moe_problem_t* p, const OutEpilogue& ep) {
 }
 
 struct DecodeWs {
-  size_t hdr, entries, list, f2s, w, hact, y, total;
+  size_t hdr, entries, list, f2s, w, arrived, hact, y, total;
 };
 
 // The workspace does not depend on the output's type (three planes).
@@ -245,10 +245,11 @@ DecodeWs decode_ws(const moe_problem_t* p) {
   DecodeWs w;
   size_t o = 0;
   w.hdr = o; o += align_up(16);
-  w.entries = o; o += align_up(16 * (size_t)decode_max_entries(M, p->topk, held(p), is_mx(p)));
+  w.entries = o; o += align_up(decode_entry_bytes(M, p->topk, held(p), is_mx(p)));
   w.list = o; o += align_up((size_t)R * 4);
   w.f2s = o; o += align_up((size_t)R * 4);
   w.w = o; o += align_up((size_t)R * 4);
+  w.arrived = o; o += align_up((size_t)p->hidden / 16 * 4);
   w.hact = o; o += align_up((size_t)R * p->ffn * (p->dtype == MOE_DTYPE_F32 ? 4 : 6));
   w.y = o; o += align_up((size_t)R * p->hidden * 4);
   w.total = o;
@@ -637,6 +638,7 @@ moe_status_t moe_layer_decode(const moe_problem_t* p, const void* x, const float
   a.wd_scale = mx ? reinterpret_cast<const uint8_t*>(w_down) + (int64_t)held(p) * p->hidden * p->ffn : nullptr;
   a.hact = at<void>(ws, L.hact);
   a.y = at<float>(ws, L.y);
+  a.arrived = at<int32_t>(ws, L.arrived);
   a.H = p->hidden;
   a.F = p->ffn;
   a.x_pitch = (uint32_t)(p->hidden * elem_bytes(p));

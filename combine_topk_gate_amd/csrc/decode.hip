@@ -120,6 +120,26 @@ constexpr int product_lds() {
   return kStreamWaves * imax(stream_line_bytes<Op, NW, NT>(), G * NT * 1024);
 }
 
+// h of one pair's 4 columns to its planes.
+template <int NP>
+__device__ __forceinline__ void store_h(const DecodeArgs& a, int64_t pair, int col, const f32x4_t& g, const f32x4_t& u) {
+  f32x4_t h;
+#pragma unroll
+  for (int v = 0; v < 4; ++v) h[v] = silu_f32(g[v]) * u[v];
+  if constexpr (NP == 0) {
+    *reinterpret_cast<f32x4_t*>(reinterpret_cast<float*>(a.hact) + pair * a.F + col) = h;
+  } else {
+    __bf16 pl[4][NP];
+#pragma unroll
+    for (int v = 0; v < 4; ++v) split_bf16<NP>(h[v], pl[v]);
+#pragma unroll
+    for (int p = 0; p < NP; ++p) {
+      const bf16x4_t o = {pl[0][p], pl[1][p], pl[2][p], pl[3][p]};
+      *reinterpret_cast<bf16x4_t*>(reinterpret_cast<__bf16*>(a.hact) + (pair * NP + p) * a.F + col) = o;
+    }
+  }
+}
+
 // Layer0 of one entry: 16 NF columns of h for its rows.  NP: bf16 planes of
 // h (0: f32).
 template <class Op, int NF, int NT, int NP>
@@ -143,23 +163,7 @@ __device__ __forceinline__ void decode_l0_tile(const DecodeArgs& a, int4 ent, ch
   stream_reduce<kStreamWaves, 2 * NF, NT, 2, 2>(acc, reinterpret_cast<f32x4_t*>(lds), [&](int grp, int j, const f32x4_t (&gu)[2]) {
     const int i = 16 * j + (lane & 15);
     if (i >= ent.z) return;
-    const int64_t pair = a.plan.list[ent.y + i];
-    const int col = f0 + 8 * grp + 4 * (lane >> 4);
-    f32x4_t h;
-#pragma unroll
-    for (int v = 0; v < 4; ++v) h[v] = silu_f32(gu[0][v]) * gu[1][v];
-    if constexpr (NP == 0) {
-      *reinterpret_cast<f32x4_t*>(reinterpret_cast<float*>(a.hact) + pair * a.F + col) = h;
-    } else {
-      __bf16 pl[4][NP];
-#pragma unroll
-      for (int v = 0; v < 4; ++v) split_bf16<NP>(h[v], pl[v]);
-#pragma unroll
-      for (int p = 0; p < NP; ++p) {
-        const bf16x4_t o = {pl[0][p], pl[1][p], pl[2][p], pl[3][p]};
-        *reinterpret_cast<bf16x4_t*>(reinterpret_cast<__bf16*>(a.hact) + (pair * NP + p) * a.F + col) = o;
-      }
-    }
+    store_h<NP>(a, a.plan.list[ent.y + i], f0 + 8 * grp + 4 * (lane >> 4), gu[0], gu[1]);
   });
 }
 
@@ -221,7 +225,224 @@ __global__ __launch_bounds__(kStreamThreads) void decode_l1_kernel(DecodeArgs a)
     decode_l1_tile<Op, NF, MAXNT, MX>(a, ent, lds);
 }
 
+// ------------------------------------------------------------ few tokens ---
+// At most 8 tokens and 64 pairs: two kernels.  Every Layer0 block routes the
+// tokens itself (a few us that the other blocks' loads hide; a plan kernel in
+// front takes 4 to 6 us alone) and its first blocks leave what Layer1 needs.
+// Of the Layer1 blocks of 16 columns the one that is done last combines them
+// (no block waits for another; the pairs are added in slot order whichever it
+// is).  Layer1 blocks of 16 waves that own 16 columns of every pair need no
+// such hand-over, but then each expert's stream starts when the one before
+// has ended: 73 us at 8 tokens, 64 experts of 2048 x 1408, instead of 43.
+constexpr int kFewTokens = 8;
+constexpr int kFewPairs = 64;
+constexpr int kFewRows = 8;  // rows of one expert: one a token
+
+// An expert and its pairs, past its rows the last one again; rows 0: none.
+struct FewEntry {
+  int expert, rows;
+  int pair[kFewRows];
+};
+
+// The n-th distinct expert among the pairs' (lane f: pair f's, -1 none), in
+// order of the first pair; rows 0: there are fewer.
+__device__ __forceinline__ FewEntry few_entry(int slot, int n) {
+  FewEntry e;
+  uint64_t left = __ballot(slot >= 0), m = 0;
+  e.expert = 0;
+  for (int i = 0; i <= n; ++i) {
+    if (left) e.expert = __builtin_amdgcn_readlane(slot, __ffsll((unsigned long long)left) - 1);
+    m = left & __ballot(slot == e.expert);
+    left &= ~m;
+  }
+  e.rows = __popcll(m);
+  int last = 0;
+#pragma unroll
+  for (int i = 0; i < kFewRows; ++i) {
+    if (m) last = __ffsll((unsigned long long)m) - 1;
+    e.pair[i] = last;
+    m &= m - 1;
+  }
+  return e;
+}
+
+template <class Op, int KMAX, int NP>
+__global__ __launch_bounds__(kStreamThreads) void decode_few_l0_kernel(const float* __restrict__ logits, DecodeArgs a) {
+  constexpr int kLine = stream_line_bytes<Op, 2, 1, kFewRows>();
+  __shared__ __attribute__((aligned(16))) char lds[kStreamWaves * imax(kLine, 2048)];
+  __shared__ int slots[kFewPairs];
+  __shared__ FewEntry ent;
+  const DecodePlan& p = a.plan;
+  const int tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6);
+  const int t = tid / kLanesPerToken, q = tid % kLanesPerToken;
+  if (blockIdx.x == 0 && blockIdx.y == 0)
+    for (int i = tid; i < a.H / 16; i += kStreamThreads) a.arrived[i] = 0;
+  float vals[KMAX];
+  int ids[KMAX];
+  if (wave * 64 < p.M * kLanesPerToken) {
+    const bool valid = t < p.M;
+    topk_row<KMAX>(logits + (int64_t)(valid ? t : 0) * p.E, p.E, q, valid, vals, ids);
+    int e = -1;
+#pragma unroll
+    for (int j = 0; j < KMAX; ++j)
+      if (j == q && ids[j] < p.E) e = ids[j] - p.base;
+    if (e >= p.EL) e = -1;
+    if (valid && q < p.k) slots[t * p.k + q] = e;
+    if (valid && blockIdx.x == 0 && blockIdx.y == 0) {
+      // softmax over the chosen logits (see the plan kernel)
+      const float l0 = vals[0];
+      float denom = 0.0f, mine = 0.0f;
+#pragma unroll
+      for (int j = 0; j < KMAX; ++j) {
+        if (j >= p.k || ids[j] >= p.E) continue;
+        const float v = expf(vals[j] - l0);
+        denom += v;
+        if (j == q) mine = v;
+      }
+      if (q < p.k) {
+        p.w[t * p.k + q] = mine > 0.0f ? mine / denom : 0.0f;
+        p.f2s[t * p.k + q] = e;
+      }
+    }
+  }
+  __syncthreads();
+  if (wave == 0) {
+    FewEntry e;
+    if (p.M == 1) {  // one token's experts are distinct
+      e.expert = slots[blockIdx.y];
+      e.rows = e.expert >= 0 ? 1 : 0;
+#pragma unroll
+      for (int i = 0; i < kFewRows; ++i) e.pair[i] = blockIdx.y;
+    } else {
+      e = few_entry(lane < p.M * p.k ? slots[lane] : -1, blockIdx.y);
+    }
+    if (lane == 0) {
+      ent = e;
+      if (blockIdx.x == 0) reinterpret_cast<FewEntry*>(p.entries)[blockIdx.y] = e;
+    }
+  }
+  __syncthreads();
+  const int rows = uniform(ent.rows);
+  if (rows == 0) return;
+  const int f0 = blockIdx.x * 16;
+  StreamArgs s{};
+  s.row_bytes = a.x_pitch;
+  const int64_t at = ((int64_t)uniform(ent.expert) * a.F + f0) * (int64_t)s.row_bytes;
+  s.w0 = reinterpret_cast<const char*>(a.w_gate) + at;
+  s.w1 = reinterpret_cast<const char*>(a.w_up) + at;
+  s.w_rows = 16;
+  s.x = a.x;
+  s.x_bytes = (uint32_t)p.M * a.x_pitch;
+  s.lines = a.H / Op::kLine;
+  f32x4_t acc[2][1];
+  stream_share<Op, 2, true, 1, 4, kFewRows>(
+      s, wave, kStreamWaves, [&](int i) { return (uint32_t)(ent.pair[i] / p.k) * a.x_pitch; }, lds + wave * kLine, acc);
+  stream_reduce<kStreamWaves, 2, 1, 2, 2>(acc, reinterpret_cast<f32x4_t*>(lds), [&](int, int, const f32x4_t (&gu)[2]) {
+    const int i = lane & 15;
+    if (i < rows) store_h<NP>(a, ent.pair[i], f0 + 4 * (lane >> 4), gu[0], gu[1]);
+  });
+}
+
+// 16 bytes of y between blocks: stored past the XCD's L2 and loaded past it
+// (agent-scope accesses).  Ordering them with the count by waiting for the
+// stores, instead of an agent-scope release, keeps the L2 from being written
+// back by every block: 44 us instead of 352 for Layer1 at 8 tokens, 64
+// experts of 2048 x 1408.
+__device__ __forceinline__ void put_y(float* p, f32x4_t v) {
+  typedef uint64_t u64x2_t __attribute__((ext_vector_type(2)));
+  const u64x2_t u = __builtin_bit_cast(u64x2_t, v);
+  __hip_atomic_store(reinterpret_cast<uint64_t*>(p), u[0], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  __hip_atomic_store(reinterpret_cast<uint64_t*>(p) + 1, u[1], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+__device__ __forceinline__ f32x4_t get_y(const float* p) {
+  typedef uint64_t u64x2_t __attribute__((ext_vector_type(2)));
+  u64x2_t u;
+  u[0] = __hip_atomic_load(reinterpret_cast<const uint64_t*>(p), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  u[1] = __hip_atomic_load(reinterpret_cast<const uint64_t*>(p) + 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  return __builtin_bit_cast(f32x4_t, u);
+}
+
+// Columns 16 x .. 16 x + 15 of entry y's pairs; the last block of the columns
+// combines.
+template <class Op, bool MX>
+__global__ __launch_bounds__(kStreamThreads) void decode_few_l1_kernel(DecodeArgs a, OutEpilogue ep) {
+  constexpr int kLine = stream_line_bytes<Op, 1, 1, kFewRows>();
+  __shared__ __attribute__((aligned(16))) char lds[kStreamWaves * imax(kLine, 1024)];
+  __shared__ int last;
+  const DecodePlan& p = a.plan;
+  const int tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6);
+  const int n0 = blockIdx.x * 16;
+  const FewEntry* __restrict__ ent = reinterpret_cast<const FewEntry*>(p.entries) + blockIdx.y;
+  const int rows = uniform(ent->rows), expert = uniform(ent->expert);
+  const int row_pair = ent->pair[lane >> 3], out_pair = ent->pair[lane & 7];  // (loaded together)
+  if (rows > 0) {
+    StreamArgs s{};
+    const int64_t row0 = (int64_t)expert * a.H + n0;
+    s.row_bytes = a.wd_pitch;
+    s.w0 = reinterpret_cast<const char*>(a.w_down) + row0 * s.row_bytes;
+    s.w_rows = 16;
+    s.x = a.hact;
+    s.x_bytes = (uint32_t)(p.M * p.k) * a.h_pitch;
+    s.plane = 2u * a.F;
+    s.lines = a.F / Op::kLine;
+    if constexpr (MX) {
+      s.scale = a.wd_scale + (row0 >> 5) * (int64_t)a.F;
+      s.scale_row = (int)(row0 & 31);
+      s.scale_pitch = a.F;
+    }
+    f32x4_t acc[1][1];
+    stream_share<Op, 1, false, 1, 4, kFewRows>(
+        s, wave, kStreamWaves, [&](int i) { return (uint32_t)(i == lane >> 3 ? row_pair : ent->pair[i]) * a.h_pitch; },
+        lds + wave * kLine, acc);
+    stream_reduce<kStreamWaves, 1, 1, 1, 1>(acc, reinterpret_cast<f32x4_t*>(lds), [&](int, int, const f32x4_t (&y)[1]) {
+      if ((lane & 15) < rows) put_y(a.y + (int64_t)out_pair * a.H + n0 + 4 * (lane >> 4), y[0]);
+    });
+  }
+  // wave 0 has stored the block's rows: it waits until they are at the point
+  // that every XCD sees, then counts the block
+  if (wave == 0) {
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+    if (lane == 0)
+      last = __hip_atomic_fetch_add(a.arrived + blockIdx.x, 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) ==
+             (int)gridDim.y - 1;
+  }
+  __syncthreads();
+  if (!last) return;
+  if (tid < p.M * 4) {
+    const int t = tid >> 2, n = n0 + 4 * (tid & 3);
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int f = t * p.k; f < (t + 1) * p.k; ++f) {
+      const float w = p.w[f];
+      if (p.f2s[f] < 0) continue;
+      const f32x4_t y = get_y(a.y + (int64_t)f * a.H + n);
+      o.x = fmaf(w, y[0], o.x);
+      o.y = fmaf(w, y[1], o.y);
+      o.z = fmaf(w, y[2], o.z);
+      o.w = fmaf(w, y[3], o.w);
+    }
+    store_out(ep, (int64_t)t * a.H + n, o);
+  }
+}
+
 // ---------------------------------------------------------------- launch ---
+template <class Op0, class Op1, int NP, bool MX>
+static void launch_few(const DecodeArgs& a, const float* logits, const OutEpilogue& ep, hipStream_t s) {
+  const DecodePlan& p = a.plan;
+  const int pairs = p.M * p.k;
+  // one token's entries are its slots, held or not
+  const int entries = p.M == 1 ? p.k : p.EL < pairs ? p.EL : pairs;
+  const dim3 grid((unsigned)(a.F / 16), (unsigned)entries);
+  if (p.k <= 2)
+    decode_few_l0_kernel<Op0, 2, NP><<<grid, kStreamThreads, 0, s>>>(logits, a);
+  else if (p.k <= 4)
+    decode_few_l0_kernel<Op0, 4, NP><<<grid, kStreamThreads, 0, s>>>(logits, a);
+  else if (p.k <= 8)
+    decode_few_l0_kernel<Op0, 8, NP><<<grid, kStreamThreads, 0, s>>>(logits, a);
+  else
+    decode_few_l0_kernel<Op0, 16, NP><<<grid, kStreamThreads, 0, s>>>(logits, a);
+  decode_few_l1_kernel<Op1, MX><<<dim3((unsigned)(a.H / 16), grid.y), kStreamThreads, 0, s>>>(a, ep);
+}
+
 // Rows an entry may hold, by the token count (an expert gets at most one row
 // of every token): 16, 32, or blocks of 64 (32 for MXFP8, whose converted
 // weights and planes need more registers).
@@ -229,9 +450,14 @@ static int decode_max_nt(int M, bool mx) { return M <= 16 ? 1 : (M <= 32 || mx) 
 
 int decode_entry_rows(int M, bool mx) { return 16 * decode_max_nt(M, mx); }
 
-int decode_max_entries(int M, int k, int EL, bool mx) {
+static int decode_max_entries(int M, int k, int EL, bool mx) {
   const int R = M * k;
   return (EL < R ? EL : R) + R / decode_entry_rows(M, mx);
+}
+
+size_t decode_entry_bytes(int M, int k, int EL, bool mx) {
+  const size_t many = sizeof(int4) * (size_t)decode_max_entries(M, k, EL, mx), few = sizeof(FewEntry) * kFewPairs;
+  return many > few ? many : few;
 }
 
 template <class Op0, class Op1, int NP, bool MX>
@@ -255,6 +481,19 @@ static void launch_products(const DecodeArgs& a, int entries, hipStream_t s) {
 hipError_t launch_decode(const DecodeArgs& a, const float* logits, int dtype, int planes, const OutEpilogue& ep,
                          hipStream_t s) {
   const DecodePlan& p = a.plan;
+  if (p.M <= kFewTokens && p.M * p.k <= kFewPairs) {
+    if (dtype == MOE_DTYPE_F32)
+      launch_few<StreamF32, StreamF32, 0, false>(a, logits, ep, s);
+    else if (dtype == MOE_DTYPE_BF16 && planes == 3)
+      launch_few<StreamBf16<1>, StreamBf16<3>, 3, false>(a, logits, ep, s);
+    else if (dtype == MOE_DTYPE_BF16)
+      launch_few<StreamBf16<1>, StreamBf16<2>, 2, false>(a, logits, ep, s);
+    else if (planes == 3)
+      launch_few<StreamBf16<1>, StreamMx<3>, 3, true>(a, logits, ep, s);
+    else
+      launch_few<StreamBf16<1>, StreamMx<2>, 2, true>(a, logits, ep, s);
+    return hipGetLastError();
+  }
   const dim3 block(kPlanThreads);
   if (p.k <= 1)
     decode_plan_kernel<1><<<1, block, 0, s>>>(logits, p);

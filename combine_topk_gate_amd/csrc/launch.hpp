@@ -101,11 +101,12 @@ struct DecodeArgs {
   const uint8_t* wd_scale;  // MXFP8: the scale bytes of W_down
   void* hact;               // [M k][planes][F] bf16, or [M k][F] f32
   float* y;                 // [M k][H]
+  int32_t* arrived;         // [H / 16] Layer1 blocks done per 16 columns (few tokens)
   int H, F;
   uint32_t x_pitch, h_pitch, wd_pitch;  // bytes of a row of x (and of the gate and up weights), h, W_down
 };
 int decode_entry_rows(int M, bool mx);
-int decode_max_entries(int M, int k, int EL, bool mx);
+size_t decode_entry_bytes(int M, int k, int EL, bool mx);  // of DecodePlan::entries
 hipError_t launch_decode(const DecodeArgs& a, const float* logits, int dtype, int planes, const OutEpilogue& ep,
                          hipStream_t s);
 

@@ -133,12 +133,13 @@ struct StreamArgs {
 };
 
 // Bytes of LDS of one wave: a line of the weight rows and of the token rows.
-template <class Op, int NW, int NT>
+// XG: token rows of a group that are loaded, 16, or 8 where there are no more.
+template <class Op, int NW, int NT, int XG = 16>
 constexpr int stream_line_bytes() {
-  return 16 * (NW * 128 + NT * Op::kP * Op::kXC * 16);
+  return 16 * NW * 128 + XG * NT * Op::kP * Op::kXC * 16;
 }
 
-// The share of the tile of one of WAVES waves (the block has WAVES).  Weight
+// One wave's share of the tile: lines first, first + stride, ....  Weight
 // group g is rows 16 g .. of w0, or, PAIRED, rows 16 (g / 2) .. of w0 (g even)
 // or w1 (g odd).  row_off(i): byte offset from a.x of token row i (0 <= i <
 // 16 NT), any row for one that does not exist.  lds: stream_line_bytes() of
@@ -146,21 +147,21 @@ constexpr int stream_line_bytes() {
 // at most): 4 where the weights come from HBM for long (decode, 2 experts of
 // 4096 x 14336: 81 us for Layer0 instead of 84), 2 for short streams, where
 // filling and draining the pipe costs more (333 x 2048 x 1408: 13 us, 17).
-template <class Op, int NW, int NT, int DEPTH>
+template <class Op, int NW, int NT, int DEPTH, int XG>
 constexpr int stream_depth() {
-  constexpr int regs = 4 * (2 * NW + Op::kP * (Op::kXC / 4) * NT), d = 96 / regs;
+  constexpr int regs = 4 * (2 * NW + Op::kP * (Op::kXC / 4) * NT * XG / 16), d = 96 / regs;
   return d > DEPTH ? DEPTH : d < 1 ? 1 : d;
 }
 
-template <class Op, int WAVES, int NW, bool PAIRED, int NT, int DEPTH, class RowOff>
-__device__ __forceinline__ void stream_tile(const StreamArgs& a, RowOff row_off, char* __restrict__ lds,
-                                            f32x4_t (&acc)[NW][NT]) {
+template <class Op, int NW, bool PAIRED, int NT, int DEPTH, int XG, class RowOff>
+__device__ __forceinline__ void stream_share(const StreamArgs& a, int first, int stride, RowOff row_off,
+                                             char* __restrict__ lds, f32x4_t (&acc)[NW][NT]) {
   constexpr bool MX = Op::kMx;
   constexpr int XC = Op::kXC, XR = 64 / XC;            // chunks of a token row; token rows per load
-  constexpr int XL = 16 / XR;                          // loads per 16 token rows and plane
+  constexpr int XL = XG / XR;                          // loads per group of token rows and plane
   constexpr int XPITCH = XC * 16;
-  const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
-  const int r = lane & 15, q = lane >> 4;
+  const int lane = threadIdx.x & 63;
+  const int r = lane & 15, q = lane >> 4, rx16 = r % XG;
   // Chunk c of row i sits at place c ^ swz(i): 16 rows read at one chunk, and
   // 8 (or 4) whole rows written, hit every bank once.
   auto swz_w = [](int i) { return (i >> 1) & 7; };
@@ -174,7 +175,7 @@ __device__ __forceinline__ void stream_tile(const StreamArgs& a, RowOff row_off,
 #pragma unroll
   for (int l = 0; l < XL * NT; ++l) {
     const int i = XR * (l % XL) + lane / XC;
-    xo[l] = row_off(16 * (l / XL) + i) + 16u * ((lane % XC) ^ swz_x(i));
+    xo[l] = row_off(XG * (l / XL) + i) + 16u * ((lane % XC) ^ swz_x(i));
   }
   uint32_t so[NW];
 #pragma unroll
@@ -213,14 +214,14 @@ __device__ __forceinline__ void stream_tile(const StreamArgs& a, RowOff row_off,
       for (int l = 0; l < XL * NT; ++l) c.x[p][l] = buf_load16(rx, xo[l] + (uint32_t)p * a.plane, at * (uint32_t)XPITCH);
   };
   char* const ldx = lds + NW * 2048;
-  constexpr int D = stream_depth<Op, NW, NT, DEPTH>();
+  constexpr int D = stream_depth<Op, NW, NT, DEPTH, XG>();
   Line ring[D];
 #pragma unroll
   for (int d = 0; d < D; ++d) {
-    load(ring[d], wave + d * WAVES);
+    load(ring[d], first + d * stride);
     __builtin_amdgcn_sched_barrier(0);
   }
-  for (int c = wave; c < a.lines; c += D * WAVES) {
+  for (int c = first; c < a.lines; c += D * stride) {
 #pragma unroll
     for (int d = 0; d < D; ++d) {
       Line& n = ring[d];
@@ -237,7 +238,7 @@ __device__ __forceinline__ void stream_tile(const StreamArgs& a, RowOff row_off,
         for (int g = 0; g < NW; ++g) scales[g] = n.s[g];
       }
       __builtin_amdgcn_sched_barrier(0);
-      load(n, c + (d + D) * WAVES);
+      load(n, c + (d + D) * stride);
       __builtin_amdgcn_sched_barrier(0);
       // (a line past the last one is zeros: it adds nothing)
 #pragma unroll
@@ -250,7 +251,7 @@ __device__ __forceinline__ void stream_tile(const StreamArgs& a, RowOff row_off,
 #pragma unroll
             for (int t = 0; t < Op::kXH; ++t)
               x[j][p * Op::kXH + t] = *reinterpret_cast<const i32x4_t*>(
-                  ldx + ((p * NT + j) * 16 + r) * XPITCH + ((Op::x_chunk(h, q, t) ^ swz_x(r)) << 4));
+                  ldx + ((p * NT + j) * XG + rx16) * XPITCH + ((Op::x_chunk(h, q, t) ^ swz_x(rx16)) << 4));
 #pragma unroll
         for (int g = 0; g < NW; ++g) {
           const i32x4_t w =
@@ -264,6 +265,13 @@ __device__ __forceinline__ void stream_tile(const StreamArgs& a, RowOff row_off,
       __builtin_amdgcn_sched_barrier(0);
     }
   }
+}
+
+// The whole tile by the WAVES waves of a block.
+template <class Op, int WAVES, int NW, bool PAIRED, int NT, int DEPTH, class RowOff>
+__device__ __forceinline__ void stream_tile(const StreamArgs& a, RowOff row_off, char* __restrict__ lds,
+                                            f32x4_t (&acc)[NW][NT]) {
+  stream_share<Op, NW, PAIRED, NT, DEPTH, 16>(a, uniform(threadIdx.x >> 6), WAVES, row_off, lds, acc);
 }
 
 constexpr int imax(int a, int b) { return a > b ? a : b; }
