@@ -51,7 +51,7 @@ __global__ __launch_bounds__(64 * WAVES) void adapter_shrink_kernel(AdapterArgs 
     // (rows of other adapters are computed too, and not stored)
     s.w0 = reinterpret_cast<const char*>(a.a) + ((int64_t)mine * a.r + j0) * a.row_bytes;
     f32x4_t acc[NW][NT];
-    stream_tile<Op, WAVES, NW, false, NT, 2>(s, [&](int m) { return (uint32_t)min(m, rows - 1) * a.row_bytes; },
+    stream_tile<Op, WAVES, NW, false, NT, 2, false>(s, [&](int m) { return (uint32_t)min(m, rows - 1) * a.row_bytes; },
                                           lds + wave * stream_line_bytes<Op, NW, NT>(), acc);
     const float sc = a.scale[mine];
     stream_reduce<WAVES, NW, NT, NW, 1>(acc, reinterpret_cast<f32x4_t*>(lds), [&](int g, int jt, const f32x4_t (&t)[1]) {
@@ -130,7 +130,7 @@ __global__ __launch_bounds__(64 * WAVES) void adapter_stream_kernel(AdapterArgs 
   s.x_bytes = (uint32_t)rows * a.row_bytes;
   s.lines = a.H / Op::kLine;
   f32x4_t acc[NW][NT];
-  stream_tile<Op, WAVES, NW, false, NT, 2>(s, [&](int m) { return (uint32_t)min(m, rows - 1) * a.row_bytes; },
+  stream_tile<Op, WAVES, NW, false, NT, 2, false>(s, [&](int m) { return (uint32_t)min(m, rows - 1) * a.row_bytes; },
                                         lds + uniform(threadIdx.x >> 6) * stream_line_bytes<Op, NW, NT>(), acc);
   stream_reduce<WAVES, NW, NT, G, 1>(acc, reinterpret_cast<f32x4_t*>(lds), [&](int g, int j, const f32x4_t (&sum)[1]) {
     f32x4_t v = sum[0];

@@ -156,7 +156,7 @@ __device__ __forceinline__ void decode_l0_tile(const DecodeArgs& a, int4 ent, ch
   s.lines = a.H / Op::kLine;
   f32x4_t acc[2 * NF][NT];
   const int wave = uniform(threadIdx.x >> 6);
-  stream_tile<Op, kStreamWaves, 2 * NF, true, NT, 4>(
+  stream_tile<Op, kStreamWaves, 2 * NF, true, NT, 4, true>(
       s, [&](int i) { return decode_row(a.plan, ent, i, a.plan.k, a.x_pitch); },
       lds + wave * stream_line_bytes<Op, 2 * NF, NT>(), acc);
   const int lane = threadIdx.x & 63;
@@ -174,24 +174,53 @@ __global__ __launch_bounds__(kStreamThreads) void decode_l0_kernel(DecodeArgs a)
   const int4 ent = a.plan.entries[blockIdx.y];
   if (MAXNT == 1 || ent.z <= 16)
     decode_l0_tile<Op, NF, 1, NP>(a, ent, lds);
-  else if (MAXNT == 2 || ent.z <= 32)
-    decode_l0_tile<Op, NF, MAXNT < 2 ? 1 : 2, NP>(a, ent, lds);
-  else
+  else if (ent.z <= 32)
     decode_l0_tile<Op, NF, MAXNT, NP>(a, ent, lds);
 }
 
-// Layer1 of one entry: 16 NF columns of y for its rows (f32, at the pair's
-// own row).
-template <class Op, int NF, int NT, bool MX>
+// Layer0 of an entry of more than 32 rows: the waves split the columns.
+constexpr int kWideL0 = 4;  // waves; 16 columns each
+
+template <class Op, int NP>
+__global__ __launch_bounds__(64 * kWideL0) void decode_l0_wide_kernel(DecodeArgs a) {
+  __shared__ __attribute__((aligned(16))) char lds[stream_wide_bytes<Op, kWideL0, 2, 4>()];
+  if ((int)blockIdx.y >= a.plan.hdr[0]) return;
+  const int4 ent = a.plan.entries[blockIdx.y];
+  if (ent.z <= 32) return;
+  const int f0 = blockIdx.x * 16 * kWideL0;
+  StreamArgs s{};
+  s.row_bytes = a.x_pitch;
+  const int64_t at = ((int64_t)ent.x * a.F + f0) * (int64_t)s.row_bytes;
+  s.w0 = reinterpret_cast<const char*>(a.w_gate) + at;
+  s.w1 = reinterpret_cast<const char*>(a.w_up) + at;
+  s.w_rows = 16 * kWideL0;
+  s.x = a.x;
+  s.x_bytes = (uint32_t)a.plan.M * a.x_pitch;
+  s.lines = a.H / Op::kLine;
+  f32x4_t acc[2][4];
+  stream_wide<Op, kWideL0, 2, true, 4, 3, true>(
+      s, [&](int i) { return decode_row(a.plan, ent, i, a.plan.k, a.x_pitch); }, lds, acc);
+  const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const int i = 16 * j + (lane & 15);
+    if (i < ent.z) store_h<NP>(a, a.plan.list[ent.y + i], f0 + 16 * wave + 4 * (lane >> 4), acc[0][j], acc[1][j]);
+  }
+}
+
+// Layer1 of one entry: 16 NW WAVES columns of y for its rows (f32, at the
+// pair's own row).  Waves split the columns: h is wider than a weight row (two
+// or three planes), so its lines are shared.
+template <class Op, int WAVES, int NW, int NT, bool MX>
 __device__ __forceinline__ void decode_l1_tile(const DecodeArgs& a, int4 ent, char* lds) {
-  const int n0 = blockIdx.x * 16 * NF;
+  const int n0 = blockIdx.x * 16 * NW * WAVES;
   StreamArgs s{};
   const int64_t row0 = (int64_t)ent.x * a.H + n0;
   s.row_bytes = a.wd_pitch;
   s.w0 = reinterpret_cast<const char*>(a.w_down) + row0 * s.row_bytes;
-  s.w_rows = 16 * NF;
+  s.w_rows = min(16 * NW * WAVES, a.H - n0);
   s.x = a.hact;
-  s.x_bytes = (uint32_t)a.plan.M * a.plan.k * a.h_pitch;
+  s.x_bytes = (uint32_t)(a.plan.M * a.plan.k) * a.h_pitch;
   s.plane = 2u * a.F;
   s.lines = a.F / Op::kLine;
   if constexpr (MX) {
@@ -199,30 +228,36 @@ __device__ __forceinline__ void decode_l1_tile(const DecodeArgs& a, int4 ent, ch
     s.scale_row = (int)(row0 & 31);
     s.scale_pitch = a.F;
   }
-  f32x4_t acc[NF][NT];
-  const int wave = uniform(threadIdx.x >> 6);
-  stream_tile<Op, kStreamWaves, NF, false, NT, 4>(s, [&](int i) { return decode_row(a.plan, ent, i, 1, a.h_pitch); },
-                                               lds + wave * stream_line_bytes<Op, NF, NT>(), acc);
-  const int lane = threadIdx.x & 63;
-  stream_reduce<kStreamWaves, NF, NT, NF < 2 ? 1 : 2, 1>(acc, reinterpret_cast<f32x4_t*>(lds), [&](int g, int j, const f32x4_t (&y)[1]) {
+  f32x4_t acc[NW][NT];
+  constexpr int kDepth = NT * Op::kP * Op::kXH > 8 ? 2 : 3;
+  stream_wide<Op, WAVES, NW, false, NT, kDepth, true>(
+      s, [&](int i) { return decode_row(a.plan, ent, i, 1, a.h_pitch); }, lds, acc);
+  const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
+#pragma unroll
+  for (int j = 0; j < NT; ++j) {
     const int i = 16 * j + (lane & 15);
-    if (i >= ent.z) return;
+    if (i >= ent.z) continue;
     const int64_t pair = a.plan.list[ent.y + i];
-    *reinterpret_cast<f32x4_t*>(a.y + pair * a.H + n0 + 16 * g + 4 * (lane >> 4)) = y[0];
-  });
+#pragma unroll
+    for (int g = 0; g < NW; ++g) {
+      const int n = n0 + 16 * (wave * NW + g) + 4 * (lane >> 4);
+      if (n < a.H) *reinterpret_cast<f32x4_t*>(a.y + pair * a.H + n) = acc[g][j];
+    }
+  }
 }
 
-template <class Op, int NF, int MAXNT, bool MX>
-__global__ __launch_bounds__(kStreamThreads) void decode_l1_kernel(DecodeArgs a) {
-  __shared__ __attribute__((aligned(16))) char lds[product_lds<Op, NF, MAXNT, (NF < 2 ? 1 : 2)>()];
+// Entries of LO < rows <= HI: one kernel for every range that a batch may
+// have, so that short entries do not pay for the registers of long ones.
+template <class Op, int WAVES, int NW, int LO, int HI, bool MX>
+__global__ __launch_bounds__(64 * WAVES) void decode_l1_kernel(DecodeArgs a) {
+  __shared__ __attribute__((aligned(16))) char lds[stream_wide_bytes<Op, WAVES, NW, HI / 16>()];
   if ((int)blockIdx.y >= a.plan.hdr[0]) return;
   const int4 ent = a.plan.entries[blockIdx.y];
-  if (MAXNT == 1 || ent.z <= 16)
-    decode_l1_tile<Op, NF, 1, MX>(a, ent, lds);
-  else if (MAXNT == 2 || ent.z <= 32)
-    decode_l1_tile<Op, NF, MAXNT < 2 ? 1 : 2, MX>(a, ent, lds);
+  if (ent.z <= LO || ent.z > HI) return;
+  if (HI > 16 && ent.z <= 16)
+    decode_l1_tile<Op, WAVES, NW, 1, MX>(a, ent, lds);
   else
-    decode_l1_tile<Op, NF, MAXNT, MX>(a, ent, lds);
+    decode_l1_tile<Op, WAVES, NW, HI / 16, MX>(a, ent, lds);
 }
 
 // ------------------------------------------------------------ few tokens ---
@@ -335,7 +370,7 @@ __global__ __launch_bounds__(kStreamThreads) void decode_few_l0_kernel(const flo
   s.x_bytes = (uint32_t)p.M * a.x_pitch;
   s.lines = a.H / Op::kLine;
   f32x4_t acc[2][1];
-  stream_share<Op, 2, true, 1, 4, kFewRows>(
+  stream_share<Op, 2, true, 1, 4, kFewRows, true>(
       s, wave, kStreamWaves, [&](int i) { return (uint32_t)(ent.pair[i] / p.k) * a.x_pitch; }, lds + wave * kLine, acc);
   stream_reduce<kStreamWaves, 2, 1, 2, 2>(acc, reinterpret_cast<f32x4_t*>(lds), [&](int, int, const f32x4_t (&gu)[2]) {
     const int i = lane & 15;
@@ -391,7 +426,7 @@ __global__ __launch_bounds__(kStreamThreads) void decode_few_l1_kernel(DecodeArg
       s.scale_pitch = a.F;
     }
     f32x4_t acc[1][1];
-    stream_share<Op, 1, false, 1, 4, kFewRows>(
+    stream_share<Op, 1, false, 1, 4, kFewRows, true>(
         s, wave, kStreamWaves, [&](int i) { return (uint32_t)(i == lane >> 3 ? row_pair : ent->pair[i]) * a.h_pitch; },
         lds + wave * kLine, acc);
     stream_reduce<kStreamWaves, 1, 1, 1, 1>(acc, reinterpret_cast<f32x4_t*>(lds), [&](int, int, const f32x4_t (&y)[1]) {
@@ -444,37 +479,33 @@ static void launch_few(const DecodeArgs& a, const float* logits, const OutEpilog
 }
 
 // Rows an entry may hold, by the token count (an expert gets at most one row
-// of every token): 16, 32, or blocks of 64 (32 for MXFP8, whose converted
-// weights and planes need more registers).
-static int decode_max_nt(int M, bool mx) { return M <= 16 ? 1 : (M <= 32 || mx) ? 2 : 4; }
+// of every token): 16, 32, or blocks of 64.
+static int decode_max_nt(int M) { return M <= 16 ? 1 : M <= 32 ? 2 : 4; }
 
-int decode_entry_rows(int M, bool mx) { return 16 * decode_max_nt(M, mx); }
+int decode_entry_rows(int M) { return 16 * decode_max_nt(M); }
 
-static int decode_max_entries(int M, int k, int EL, bool mx) {
+static int decode_max_entries(int M, int k, int EL) {
   const int R = M * k;
-  return (EL < R ? EL : R) + R / decode_entry_rows(M, mx);
+  return (EL < R ? EL : R) + R / decode_entry_rows(M);
 }
 
-size_t decode_entry_bytes(int M, int k, int EL, bool mx) {
-  const size_t many = sizeof(int4) * (size_t)decode_max_entries(M, k, EL, mx), few = sizeof(FewEntry) * kFewPairs;
+size_t decode_entry_bytes(int M, int k, int EL) {
+  const size_t many = sizeof(int4) * (size_t)decode_max_entries(M, k, EL), few = sizeof(FewEntry) * kFewPairs;
   return many > few ? many : few;
 }
 
 template <class Op0, class Op1, int NP, bool MX>
 static void launch_products(const DecodeArgs& a, int entries, hipStream_t s) {
-  const int nt = decode_max_nt(a.plan.M, MX);
-  auto grid = [&](int n, int nf) { return dim3((unsigned)(n / (16 * nf)), (unsigned)entries); };
+  const int nt = decode_max_nt(a.plan.M);
+  auto grid = [&](int n, int cols) { return dim3((unsigned)((n + cols - 1) / cols), (unsigned)entries); };
   if (nt == 1) {
-    decode_l0_kernel<Op0, 1, 1, NP><<<grid(a.F, 1), kStreamThreads, 0, s>>>(a);
-    decode_l1_kernel<Op1, 1, 1, MX><<<grid(a.H, 1), kStreamThreads, 0, s>>>(a);
-  } else if (nt == 2) {
-    decode_l0_kernel<Op0, 1, 2, NP><<<grid(a.F, 1), kStreamThreads, 0, s>>>(a);
-    decode_l1_kernel<Op1, 2, 2, MX><<<grid(a.H, 2), kStreamThreads, 0, s>>>(a);
+    decode_l0_kernel<Op0, 1, 1, NP><<<grid(a.F, 16), kStreamThreads, 0, s>>>(a);
+    decode_l1_kernel<Op1, 4, 1, 0, 16, MX><<<grid(a.H, 64), 256, 0, s>>>(a);
   } else {
-    if constexpr (!MX) {
-      decode_l0_kernel<Op0, 2, 4, NP><<<grid(a.F, 2), kStreamThreads, 0, s>>>(a);
-      decode_l1_kernel<Op1, 4, 4, MX><<<grid(a.H, 4), kStreamThreads, 0, s>>>(a);
-    }
+    decode_l0_kernel<Op0, 1, 2, NP><<<grid(a.F, 16), kStreamThreads, 0, s>>>(a);
+    if (nt == 4) decode_l0_wide_kernel<Op0, NP><<<grid(a.F, 16 * kWideL0), 64 * kWideL0, 0, s>>>(a);
+    decode_l1_kernel<Op1, 4, 1, 0, 32, MX><<<grid(a.H, 64), 256, 0, s>>>(a);
+    if (nt == 4) decode_l1_kernel<Op1, 8, 1, 32, 64, MX><<<grid(a.H, 128), 512, 0, s>>>(a);
   }
 }
 
@@ -507,7 +538,7 @@ hipError_t launch_decode(const DecodeArgs& a, const float* logits, int dtype, in
     decode_plan_kernel<16><<<1, block, 0, s>>>(logits, p);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  const int entries = decode_max_entries(p.M, p.k, p.EL, dtype == MOE_DTYPE_BF16_MXFP8);
+  const int entries = decode_max_entries(p.M, p.k, p.EL);
   if (dtype == MOE_DTYPE_F32)
     launch_products<StreamF32, StreamF32, 0, false>(a, entries, s);
   else if (dtype == MOE_DTYPE_BF16 && planes == 3)

@@ -27,6 +27,14 @@ namespace moe {
 
 constexpr uint32_t kNoRow = 0x80000000u;  // offset past every buffer range
 
+// A weight load: NT marks it as used once, so that it does not push the token
+// rows out of the caches (2 experts of 4096 x 14336, one token: 78 + 43 us
+// instead of 84 + 46; not for weights that the caches may keep between calls).
+template <bool NT>
+__device__ __forceinline__ i32x4_t load_weight(__amdgpu_buffer_rsrc_t r, uint32_t voff, uint32_t soff) {
+  return __builtin_bit_cast(i32x4_t, __builtin_amdgcn_raw_buffer_load_b128(r, (int)voff, (int)soff, NT ? 2 : 0));
+}
+
 // f32 value as NP bf16 values whose sum is the value (NP = 3: exactly, but
 // for magnitudes below 2^-110; NP = 2: to 2^-17 of it).
 template <int NP>
@@ -147,13 +155,14 @@ constexpr int stream_line_bytes() {
 // at most): 4 where the weights come from HBM for long (decode, 2 experts of
 // 4096 x 14336: 81 us for Layer0 instead of 84), 2 for short streams, where
 // filling and draining the pipe costs more (333 x 2048 x 1408: 13 us, 17).
+// ONCE: the weights are not used again soon (load_weight).
 template <class Op, int NW, int NT, int DEPTH, int XG>
 constexpr int stream_depth() {
   constexpr int regs = 4 * (2 * NW + Op::kP * (Op::kXC / 4) * NT * XG / 16), d = 96 / regs;
   return d > DEPTH ? DEPTH : d < 1 ? 1 : d;
 }
 
-template <class Op, int NW, bool PAIRED, int NT, int DEPTH, int XG, class RowOff>
+template <class Op, int NW, bool PAIRED, int NT, int DEPTH, int XG, bool ONCE, class RowOff>
 __device__ __forceinline__ void stream_share(const StreamArgs& a, int first, int stride, RowOff row_off,
                                              char* __restrict__ lds, f32x4_t (&acc)[NW][NT]) {
   constexpr bool MX = Op::kMx;
@@ -202,7 +211,7 @@ __device__ __forceinline__ void stream_share(const StreamArgs& a, int first, int
     const __amdgpu_buffer_rsrc_t r1 = make_rsrc(PAIRED ? a.w1 : a.w0, live ? w_bytes : 0u);
     const __amdgpu_buffer_rsrc_t rx = make_rsrc(a.x, live ? a.x_bytes : 0u);
 #pragma unroll
-    for (int l = 0; l < 2 * NW; ++l) c.w[l] = buf_load16(PAIRED && (l & 2) ? r1 : r0, woff[l], at * 128u);
+    for (int l = 0; l < 2 * NW; ++l) c.w[l] = load_weight<ONCE>(PAIRED && (l & 2) ? r1 : r0, woff[l], at * 128u);
     if constexpr (MX) {
 #pragma unroll
       for (int g = 0; g < NW; ++g)
@@ -268,13 +277,136 @@ __device__ __forceinline__ void stream_share(const StreamArgs& a, int first, int
 }
 
 // The whole tile by the WAVES waves of a block.
-template <class Op, int WAVES, int NW, bool PAIRED, int NT, int DEPTH, class RowOff>
+template <class Op, int WAVES, int NW, bool PAIRED, int NT, int DEPTH, bool ONCE, class RowOff>
 __device__ __forceinline__ void stream_tile(const StreamArgs& a, RowOff row_off, char* __restrict__ lds,
                                             f32x4_t (&acc)[NW][NT]) {
-  stream_share<Op, NW, PAIRED, NT, DEPTH, 16>(a, uniform(threadIdx.x >> 6), WAVES, row_off, lds, acc);
+  stream_share<Op, NW, PAIRED, NT, DEPTH, 16, ONCE>(a, uniform(threadIdx.x >> 6), WAVES, row_off, lds, acc);
 }
 
 constexpr int imax(int a, int b) { return a > b ? a : b; }
+
+// The same product with the weight rows, not the reduction, split over the
+// block's WAVES waves (16 NW rows each: group g of wave w is weight group w NW
+// + g), which share the lines of the token rows: every wave loads its part of
+// a line, and one barrier per line, over two places for it, hands them round.
+// For many or wide (several planes) token rows, whose lines would otherwise be
+// as much traffic as the weights'.  lds: stream_wide_bytes().  The sums are
+// complete: acc as in stream_share.
+template <class Op, int WAVES, int NW, int NT>
+constexpr int stream_wide_bytes() {
+  return WAVES * NW * 2048 + 2 * 16 * NT * Op::kP * Op::kXC * 16;
+}
+
+template <class Op, int WAVES, int NW, bool PAIRED, int NT, int DEPTH, bool ONCE, class RowOff>
+__device__ __forceinline__ void stream_wide(const StreamArgs& a, RowOff row_off, char* __restrict__ lds,
+                                            f32x4_t (&acc)[NW][NT]) {
+  constexpr bool MX = Op::kMx;
+  constexpr int XC = Op::kXC, XR = 64 / XC, XL = 16 / XR, XPITCH = XC * 16;
+  constexpr int kLoads = XL * NT * Op::kP, XW = (kLoads + WAVES - 1) / WAVES;  // a line's token loads; of one wave
+  constexpr int kX = 16 * NT * Op::kP * XPITCH;                              // bytes of a token line
+  const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
+  const int r = lane & 15, q = lane >> 4;
+  auto swz_w = [](int i) { return (i >> 1) & 7; };
+  auto swz_x = [](int i) { return XC == 8 ? (i >> 1) & 7 : i & 15; };
+  uint32_t woff[2 * NW], xo[XW], so[NW];
+#pragma unroll
+  for (int l = 0; l < 2 * NW; ++l) {
+    const int i = 8 * (l & 1) + (lane >> 3), grp = wave * NW + (l >> 1);
+    woff[l] = (uint32_t)min(16 * (PAIRED ? grp >> 1 : grp) + i, a.w_rows - 1) * a.row_bytes +
+              16u * ((lane & 7) ^ swz_w(i));
+  }
+  // token load l of a line: plane l / (XL NT), rows XR (l % (XL NT)) ..
+#pragma unroll
+  for (int v = 0; v < XW; ++v) {
+    const int l = min(wave + v * WAVES, kLoads - 1), p = l / (XL * NT), i = XR * (l % (XL * NT)) + lane / XC;
+    xo[v] = row_off(i) + (uint32_t)p * a.plane + 16u * ((lane % XC) ^ swz_x(i & 15));
+  }
+#pragma unroll
+  for (int g = 0; g < NW; ++g) {
+    if (MX) {
+      const int sr = a.scale_row + min(16 * (wave * NW + g) + r, a.w_rows - 1);
+      so[g] = (uint32_t)(sr >> 5) * a.scale_pitch + 4u * (sr & 31);
+    }
+#pragma unroll
+    for (int j = 0; j < NT; ++j) acc[g][j] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+  }
+  const uint32_t w_bytes = (uint32_t)a.w_rows * a.row_bytes;
+  struct Line {
+    i32x4_t w[2 * NW];
+    i32x4_t x[XW];
+    uint32_t s[MX ? NW : 1];
+  };
+  static_assert(!PAIRED || NW % 2 == 0, "a wave's pairs are its own");
+  auto load = [&](Line& c, int line) {
+    const bool live = line < a.lines;  // else nothing is read (see stream_share)
+    const uint32_t at = live ? (uint32_t)line : 0u;
+    const __amdgpu_buffer_rsrc_t r0 = make_rsrc(a.w0, live ? w_bytes : 0u);
+    const __amdgpu_buffer_rsrc_t r1 = make_rsrc(PAIRED ? a.w1 : a.w0, live ? w_bytes : 0u);
+    const __amdgpu_buffer_rsrc_t rx = make_rsrc(a.x, live ? a.x_bytes : 0u);
+#pragma unroll
+    for (int l = 0; l < 2 * NW; ++l) c.w[l] = load_weight<ONCE>(PAIRED && (l & 2) ? r1 : r0, woff[l], at * 128u);
+    if constexpr (MX) {
+#pragma unroll
+      for (int g = 0; g < NW; ++g) c.s[g] = *reinterpret_cast<const uint32_t*>(a.scale + so[g] + at * 128u);
+    }
+#pragma unroll
+    for (int v = 0; v < XW; ++v) c.x[v] = buf_load16(rx, xo[v], at * (uint32_t)XPITCH);
+  };
+  char* const ldw = lds + wave * NW * 2048;
+  char* const ldx = lds + WAVES * NW * 2048;
+  constexpr int D = DEPTH;
+  Line ring[D];
+#pragma unroll
+  for (int d = 0; d < D; ++d) {
+    load(ring[d], d);
+    __builtin_amdgcn_sched_barrier(0);
+  }
+  for (int c = 0; c < a.lines; c += D) {
+#pragma unroll
+    for (int d = 0; d < D; ++d) {
+      Line& n = ring[d];
+      char* const xb = ldx + ((D % 2 == 0 ? d : c + d) & 1) * kX;
+#pragma unroll
+      for (int l = 0; l < 2 * NW; ++l) *reinterpret_cast<i32x4_t*>(ldw + l * 1024 + lane * 16) = n.w[l];
+#pragma unroll
+      for (int v = 0; v < XW; ++v)
+        if (kLoads % WAVES == 0 || wave + v * WAVES < kLoads)
+          *reinterpret_cast<i32x4_t*>(xb + (wave + v * WAVES) * 1024 + lane * 16) = n.x[v];
+      uint32_t scales[MX ? NW : 1];
+      if constexpr (MX) {
+#pragma unroll
+        for (int g = 0; g < NW; ++g) scales[g] = n.s[g];
+      }
+      __builtin_amdgcn_sched_barrier(0);
+      load(n, c + d + D);
+      __builtin_amdgcn_sched_barrier(0);
+      __syncthreads();
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        i32x4_t w[NW];
+#pragma unroll
+        for (int g = 0; g < NW; ++g)
+          w[g] = *reinterpret_cast<const i32x4_t*>(ldw + (16 * g + r) * 128 + (((4 * h + q) ^ swz_w(r)) << 4));
+        i32x4_t x[NT][Op::kXH * Op::kP];
+#pragma unroll
+        for (int p = 0; p < Op::kP; ++p)
+#pragma unroll
+          for (int j = 0; j < NT; ++j)
+#pragma unroll
+            for (int t = 0; t < Op::kXH; ++t)
+              x[j][p * Op::kXH + t] = *reinterpret_cast<const i32x4_t*>(
+                  xb + ((p * NT + j) * 16 + r) * XPITCH + ((Op::x_chunk(h, q, t) ^ swz_x(r)) << 4));
+#pragma unroll
+        for (int g = 0; g < NW; ++g) {
+          const float sc =
+              MX ? __builtin_bit_cast(float, ((scales[MX ? g : 0] >> (8 * (2 * h + (q >> 1)))) & 0xFFu) << 23) : 0.f;
+          Op::template mma<NT>(acc[g], w[g], sc, x);
+        }
+      }
+      __builtin_amdgcn_sched_barrier(0);
+    }
+  }
+}
 
 // Adds the WAVES partial accumulators in wave order through LDS, G groups of
 // 16 weight rows at a time (lds: WAVES * G * NT KiB), and hands the sums out:
