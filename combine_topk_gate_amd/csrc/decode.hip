@@ -31,10 +31,53 @@ constexpr int kPlanMaxPairs = 256 * 16;
 constexpr int kPlanMaxExperts = 512;
 
 // ------------------------------------------------------------------ plan ---
-// One workgroup: the tokens' experts and weights, and per held expert the
-// list of its pairs f = t k + j, cut into entries of at most `rows` rows.
-// (Which place of an expert's list a pair gets is decided by an LDS atomic;
-// a row's result does not depend on its place.)
+// A token's experts and weights by its 16 lanes: softmax over the chosen
+// logits, shifted by the largest, summed in slot order; a place left over
+// (fewer than k logits above -inf) has weight 0 and belongs to no expert.
+// Returns the held expert of slot q (-1: none).
+template <int KMAX>
+__device__ __forceinline__ int route_token(const float* __restrict__ logits, const DecodePlan& p, int t, int q,
+                                           bool valid, bool store) {
+  float vals[KMAX];
+  int ids[KMAX];
+  topk_row<KMAX>(logits + (int64_t)(valid ? t : 0) * p.E, p.E, q, valid, vals, ids);
+  int e = -1;
+#pragma unroll
+  for (int j = 0; j < KMAX; ++j)
+    if (j == q && ids[j] < p.E) e = ids[j] - p.base;
+  if (e >= p.EL || q >= p.k || !valid) e = -1;
+  if (store && valid) {
+    const float l0 = vals[0];
+    float denom = 0.0f, mine = 0.0f;
+#pragma unroll
+    for (int j = 0; j < KMAX; ++j) {
+      if (j >= p.k || ids[j] >= p.E) continue;
+      const float v = expf(vals[j] - l0);
+      denom += v;
+      if (j == q) mine = v;
+    }
+    if (q < p.k) {
+      const int f = t * p.k + q;
+      p.w[f] = mine > 0.0f ? mine / denom : 0.0f;
+      p.f2s[f] = e >= 0 ? f : -1;
+    }
+  }
+  return e;
+}
+
+// 16 tokens a block: their weights and (in list) their pairs' experts.
+template <int KMAX>
+__global__ __launch_bounds__(256) void decode_route_kernel(const float* __restrict__ logits, DecodePlan p) {
+  const int q = threadIdx.x % kLanesPerToken, t = blockIdx.x * 16 + threadIdx.x / kLanesPerToken;
+  const int e = route_token<KMAX>(logits, p, t, q, t < p.M, true);
+  if (t < p.M && q < p.k) p.list[t * p.k + q] = e;
+}
+
+// One workgroup: per held expert the list of its pairs f = t k + j, cut into
+// entries of at most `rows` rows.  (Which place of an expert's list a pair
+// gets is decided by an LDS atomic; a row's result does not depend on its
+// place.)  KMAX 0: the route kernel has left the pairs' experts in list;
+// otherwise the tokens are routed here.
 template <int KMAX>
 __global__ __launch_bounds__(kPlanThreads) void decode_plan_kernel(const float* __restrict__ logits, DecodePlan p) {
   __shared__ int cnt[kPlanMaxExperts], scan[kPlanMaxExperts], cur[kPlanMaxExperts];
@@ -42,34 +85,19 @@ __global__ __launch_bounds__(kPlanThreads) void decode_plan_kernel(const float* 
   const int tid = threadIdx.x;
   for (int e = tid; e < p.EL; e += kPlanThreads) cnt[e] = 0;
   __syncthreads();
-  const int q = tid % kLanesPerToken;
-  for (int t0 = 0; t0 < p.M; t0 += kPlanThreads / kLanesPerToken) {
-    const int t = t0 + tid / kLanesPerToken;
-    const bool valid = t < p.M;
-    float vals[KMAX];
-    int ids[KMAX];
-    topk_row<KMAX>(logits + (int64_t)(valid ? t : 0) * p.E, p.E, q, valid, vals, ids);
-    if (!valid) continue;
-    // softmax over the chosen logits, shifted by the largest, summed in slot
-    // order; a place left over (fewer than k logits above -inf) has weight 0
-    // and belongs to no expert
-    const float l0 = vals[0];
-    float denom = 0.0f;
-#pragma unroll
-    for (int j = 0; j < KMAX; ++j)
-      if (j < p.k && ids[j] < p.E) denom += expf(vals[j] - l0);
-#pragma unroll
-    for (int j = 0; j < KMAX; ++j) {
-      if (j < p.k && j == q) {
-        const int f = t * p.k + j;
-        const bool chosen = ids[j] < p.E;
-        int e = chosen ? ids[j] - p.base : -1;
-        if (e >= p.EL) e = -1;
-        p.w[f] = chosen ? expf(vals[j] - l0) / denom : 0.0f;
-        p.f2s[f] = e >= 0 ? f : -1;
-        slot[f] = (short)e;
-        if (e >= 0) atomicAdd(&cnt[e], 1);
-      }
+  if constexpr (KMAX == 0) {
+    for (int f = tid; f < p.M * p.k; f += kPlanThreads) {
+      const int e = p.list[f];
+      slot[f] = (short)e;
+      if (e >= 0) atomicAdd(&cnt[e], 1);
+    }
+  } else {
+    const int q = tid % kLanesPerToken;
+    for (int t0 = 0; t0 < p.M; t0 += kPlanThreads / kLanesPerToken) {
+      const int t = t0 + tid / kLanesPerToken;
+      const int e = route_token<KMAX>(logits, p, t, q, t < p.M, true);
+      if (t < p.M && q < p.k) slot[t * p.k + q] = (short)e;
+      if (e >= 0) atomicAdd(&cnt[e], 1);
     }
   }
   __syncthreads();
@@ -108,10 +136,10 @@ __global__ __launch_bounds__(kPlanThreads) void decode_plan_kernel(const float* 
 }
 
 // --------------------------------------------------------------- products ---
-// Byte offset of the entry's token row i (a row past its end: its last one):
-// pair list[i], at (pair / div) * pitch.
+// Byte offset of the entry's token row i: pair list[i], at (pair / div) *
+// pitch.  Past its end nothing is read.
 __device__ __forceinline__ uint32_t decode_row(const DecodePlan& p, int4 ent, int i, int div, uint32_t pitch) {
-  return (uint32_t)(p.list[ent.y + min(i, ent.z - 1)] / div) * pitch;
+  return i < ent.z ? (uint32_t)(p.list[ent.y + i] / div) * pitch : kNoRow;
 }
 
 // LDS of a product kernel: the waves' lines, then the sums of G groups.
@@ -178,15 +206,12 @@ __global__ __launch_bounds__(kStreamThreads) void decode_l0_kernel(DecodeArgs a)
     decode_l0_tile<Op, NF, MAXNT, NP>(a, ent, lds);
 }
 
-// Layer0 of an entry of more than 32 rows: the waves split the columns.
+// Layer0 where experts get many rows (entries of up to 64): the waves split
+// the columns and share the token rows.
 constexpr int kWideL0 = 4;  // waves; 16 columns each
 
-template <class Op, int NP>
-__global__ __launch_bounds__(64 * kWideL0) void decode_l0_wide_kernel(DecodeArgs a) {
-  __shared__ __attribute__((aligned(16))) char lds[stream_wide_bytes<Op, kWideL0, 2, 4>()];
-  if ((int)blockIdx.y >= a.plan.hdr[0]) return;
-  const int4 ent = a.plan.entries[blockIdx.y];
-  if (ent.z <= 32) return;
+template <class Op, int NT, int NP>
+__device__ __forceinline__ void decode_l0_wide_tile(const DecodeArgs& a, int4 ent, char* lds) {
   const int f0 = blockIdx.x * 16 * kWideL0;
   StreamArgs s{};
   s.row_bytes = a.x_pitch;
@@ -197,15 +222,26 @@ __global__ __launch_bounds__(64 * kWideL0) void decode_l0_wide_kernel(DecodeArgs
   s.x = a.x;
   s.x_bytes = (uint32_t)a.plan.M * a.x_pitch;
   s.lines = a.H / Op::kLine;
-  f32x4_t acc[2][4];
-  stream_wide<Op, kWideL0, 2, true, 4, 3, true>(
+  f32x4_t acc[2][NT];
+  stream_wide<Op, kWideL0, 2, true, NT, 4, true>(
       s, [&](int i) { return decode_row(a.plan, ent, i, a.plan.k, a.x_pitch); }, lds, acc);
   const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
 #pragma unroll
-  for (int j = 0; j < 4; ++j) {
+  for (int j = 0; j < NT; ++j) {
     const int i = 16 * j + (lane & 15);
     if (i < ent.z) store_h<NP>(a, a.plan.list[ent.y + i], f0 + 16 * wave + 4 * (lane >> 4), acc[0][j], acc[1][j]);
   }
+}
+
+template <class Op, int NP>
+__global__ __launch_bounds__(64 * kWideL0) void decode_l0_wide_kernel(DecodeArgs a) {
+  __shared__ __attribute__((aligned(16))) char lds[stream_wide_bytes<Op, kWideL0, 2, 4>()];
+  if ((int)blockIdx.y >= a.plan.hdr[0]) return;
+  const int4 ent = a.plan.entries[blockIdx.y];
+  if (ent.z <= 32)
+    decode_l0_wide_tile<Op, 2, NP>(a, ent, lds);
+  else
+    decode_l0_wide_tile<Op, 4, NP>(a, ent, lds);
 }
 
 // Layer1 of one entry: 16 NW WAVES columns of y for its rows (f32, at the
@@ -229,7 +265,7 @@ __device__ __forceinline__ void decode_l1_tile(const DecodeArgs& a, int4 ent, ch
     s.scale_pitch = a.F;
   }
   f32x4_t acc[NW][NT];
-  constexpr int kDepth = NT * Op::kP * Op::kXH > 8 ? 2 : 3;
+  constexpr int kDepth = Op::kXH * NT * Op::kP > 12 ? 2 : 4;
   stream_wide<Op, WAVES, NW, false, NT, kDepth, true>(
       s, [&](int i) { return decode_row(a.plan, ent, i, 1, a.h_pitch); }, lds, acc);
   const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
@@ -246,18 +282,15 @@ __device__ __forceinline__ void decode_l1_tile(const DecodeArgs& a, int4 ent, ch
   }
 }
 
-// Entries of LO < rows <= HI: one kernel for every range that a batch may
-// have, so that short entries do not pay for the registers of long ones.
-template <class Op, int WAVES, int NW, int LO, int HI, bool MX>
+template <class Op, int WAVES, int NW, int MAXNT, bool MX>
 __global__ __launch_bounds__(64 * WAVES) void decode_l1_kernel(DecodeArgs a) {
-  __shared__ __attribute__((aligned(16))) char lds[stream_wide_bytes<Op, WAVES, NW, HI / 16>()];
+  __shared__ __attribute__((aligned(16))) char lds[stream_wide_bytes<Op, WAVES, NW, MAXNT>()];
   if ((int)blockIdx.y >= a.plan.hdr[0]) return;
   const int4 ent = a.plan.entries[blockIdx.y];
-  if (ent.z <= LO || ent.z > HI) return;
-  if (HI > 16 && ent.z <= 16)
-    decode_l1_tile<Op, WAVES, NW, 1, MX>(a, ent, lds);
+  if (MAXNT > 1 && ent.z <= 8 * MAXNT)
+    decode_l1_tile<Op, WAVES, NW, (MAXNT > 1 ? MAXNT / 2 : 1), MX>(a, ent, lds);
   else
-    decode_l1_tile<Op, WAVES, NW, HI / 16, MX>(a, ent, lds);
+    decode_l1_tile<Op, WAVES, NW, MAXNT, MX>(a, ent, lds);
 }
 
 // ------------------------------------------------------------ few tokens ---
@@ -312,33 +345,9 @@ __global__ __launch_bounds__(kStreamThreads) void decode_few_l0_kernel(const flo
   const int t = tid / kLanesPerToken, q = tid % kLanesPerToken;
   if (blockIdx.x == 0 && blockIdx.y == 0)
     for (int i = tid; i < a.H / 16; i += kStreamThreads) a.arrived[i] = 0;
-  float vals[KMAX];
-  int ids[KMAX];
   if (wave * 64 < p.M * kLanesPerToken) {
-    const bool valid = t < p.M;
-    topk_row<KMAX>(logits + (int64_t)(valid ? t : 0) * p.E, p.E, q, valid, vals, ids);
-    int e = -1;
-#pragma unroll
-    for (int j = 0; j < KMAX; ++j)
-      if (j == q && ids[j] < p.E) e = ids[j] - p.base;
-    if (e >= p.EL) e = -1;
-    if (valid && q < p.k) slots[t * p.k + q] = e;
-    if (valid && blockIdx.x == 0 && blockIdx.y == 0) {
-      // softmax over the chosen logits (see the plan kernel)
-      const float l0 = vals[0];
-      float denom = 0.0f, mine = 0.0f;
-#pragma unroll
-      for (int j = 0; j < KMAX; ++j) {
-        if (j >= p.k || ids[j] >= p.E) continue;
-        const float v = expf(vals[j] - l0);
-        denom += v;
-        if (j == q) mine = v;
-      }
-      if (q < p.k) {
-        p.w[t * p.k + q] = mine > 0.0f ? mine / denom : 0.0f;
-        p.f2s[t * p.k + q] = e;
-      }
-    }
+    const int e = route_token<KMAX>(logits, p, t, q, t < p.M, blockIdx.x == 0 && blockIdx.y == 0);
+    if (t < p.M && q < p.k) slots[t * p.k + q] = e;
   }
   __syncthreads();
   if (wave == 0) {
@@ -371,7 +380,7 @@ __global__ __launch_bounds__(kStreamThreads) void decode_few_l0_kernel(const flo
   s.lines = a.H / Op::kLine;
   f32x4_t acc[2][1];
   stream_share<Op, 2, true, 1, 4, kFewRows, true>(
-      s, wave, kStreamWaves, [&](int i) { return (uint32_t)(ent.pair[i] / p.k) * a.x_pitch; }, lds + wave * kLine, acc);
+      s, wave, kStreamWaves, [&](int i) { return i < rows ? (uint32_t)(ent.pair[i] / p.k) * a.x_pitch : kNoRow; }, lds + wave * kLine, acc);
   stream_reduce<kStreamWaves, 2, 1, 2, 2>(acc, reinterpret_cast<f32x4_t*>(lds), [&](int, int, const f32x4_t (&gu)[2]) {
     const int i = lane & 15;
     if (i < rows) store_h<NP>(a, ent.pair[i], f0 + 4 * (lane >> 4), gu[0], gu[1]);
@@ -427,7 +436,7 @@ __global__ __launch_bounds__(kStreamThreads) void decode_few_l1_kernel(DecodeArg
     }
     f32x4_t acc[1][1];
     stream_share<Op, 1, false, 1, 4, kFewRows, true>(
-        s, wave, kStreamWaves, [&](int i) { return (uint32_t)(i == lane >> 3 ? row_pair : ent->pair[i]) * a.h_pitch; },
+        s, wave, kStreamWaves, [&](int i) { return i < rows ? (uint32_t)(i == lane >> 3 ? row_pair : ent->pair[i]) * a.h_pitch : kNoRow; },
         lds + wave * kLine, acc);
     stream_reduce<kStreamWaves, 1, 1, 1, 1>(acc, reinterpret_cast<f32x4_t*>(lds), [&](int, int, const f32x4_t (&y)[1]) {
       if ((lane & 15) < rows) put_y(a.y + (int64_t)out_pair * a.H + n0 + 4 * (lane >> 4), y[0]);
@@ -478,34 +487,53 @@ static void launch_few(const DecodeArgs& a, const float* logits, const OutEpilog
   decode_few_l1_kernel<Op1, MX><<<dim3((unsigned)(a.H / 16), grid.y), kStreamThreads, 0, s>>>(a, ep);
 }
 
-// Rows an entry may hold, by the token count (an expert gets at most one row
-// of every token): 16, 32, or blocks of 64.
-static int decode_max_nt(int M) { return M <= 16 ? 1 : M <= 32 ? 2 : 4; }
+// Rows an entry may hold, in 16s.  An expert gets at most one row of every
+// token: 16 tokens need no more than 16.  Beyond, entries of 32 rows stream
+// the weights by reduction-splitting waves, entries of 64 by column-splitting
+// ones that share the rows; the latter where experts get more than 16 rows on
+// average.  (Layer0 of 8 experts 4096 x 14336: 25 rows each 302 us with 32-row
+// entries, 380 with 64; 50 rows each, where every expert takes two entries of
+// 32 and the weights are read twice, 540 and 345.)
+static int decode_max_nt(int M, int k, int E) { return M <= 16 ? 1 : M <= 32 || M * k <= 16 * E ? 2 : 4; }
 
-int decode_entry_rows(int M) { return 16 * decode_max_nt(M); }
+int decode_entry_rows(int M, int k, int E) { return 16 * decode_max_nt(M, k, E); }
 
-static int decode_max_entries(int M, int k, int EL) {
+static int decode_max_entries(int M, int k, int E, int EL) {
   const int R = M * k;
-  return (EL < R ? EL : R) + R / decode_entry_rows(M);
+  return (EL < R ? EL : R) + R / decode_entry_rows(M, k, E);
 }
 
-size_t decode_entry_bytes(int M, int k, int EL) {
-  const size_t many = sizeof(int4) * (size_t)decode_max_entries(M, k, EL), few = sizeof(FewEntry) * kFewPairs;
+size_t decode_entry_bytes(int M, int k, int E, int EL) {
+  const size_t many = sizeof(int4) * (size_t)decode_max_entries(M, k, E, EL), few = sizeof(FewEntry) * kFewPairs;
   return many > few ? many : few;
 }
 
 template <class Op0, class Op1, int NP, bool MX>
 static void launch_products(const DecodeArgs& a, int entries, hipStream_t s) {
-  const int nt = decode_max_nt(a.plan.M);
+  const int nt = decode_max_nt(a.plan.M, a.plan.k, a.plan.E);
   auto grid = [&](int n, int cols) { return dim3((unsigned)((n + cols - 1) / cols), (unsigned)entries); };
   if (nt == 1) {
     decode_l0_kernel<Op0, 1, 1, NP><<<grid(a.F, 16), kStreamThreads, 0, s>>>(a);
-    decode_l1_kernel<Op1, 4, 1, 0, 16, MX><<<grid(a.H, 64), 256, 0, s>>>(a);
-  } else {
+    decode_l1_kernel<Op1, 4, 1, 1, MX><<<grid(a.H, 64), 256, 0, s>>>(a);
+  } else if (nt == 2) {
     decode_l0_kernel<Op0, 1, 2, NP><<<grid(a.F, 16), kStreamThreads, 0, s>>>(a);
-    if (nt == 4) decode_l0_wide_kernel<Op0, NP><<<grid(a.F, 16 * kWideL0), 64 * kWideL0, 0, s>>>(a);
-    decode_l1_kernel<Op1, 4, 1, 0, 32, MX><<<grid(a.H, 64), 256, 0, s>>>(a);
-    if (nt == 4) decode_l1_kernel<Op1, 8, 1, 32, 64, MX><<<grid(a.H, 128), 512, 0, s>>>(a);
+    decode_l1_kernel<Op1, 4, 1, 2, MX><<<grid(a.H, 64), 256, 0, s>>>(a);
+  } else {
+    decode_l0_wide_kernel<Op0, NP><<<grid(a.F, 16 * kWideL0), 64 * kWideL0, 0, s>>>(a);
+    decode_l1_kernel<Op1, 8, 1, 4, MX><<<grid(a.H, 128), 512, 0, s>>>(a);
+  }
+}
+
+template <int KMAX>
+static void launch_plan(const float* logits, const DecodePlan& p, hipStream_t s) {
+  // routed by the plan's one workgroup (64 tokens at a time) where that takes
+  // less than a launch: 4.5 us at 17 tokens, k = 2; at 64 tokens, k = 8, 15 us
+  // against 4 + 4
+  if ((p.M + 63) / 64 * KMAX <= 4) {
+    decode_plan_kernel<KMAX><<<1, kPlanThreads, 0, s>>>(logits, p);
+  } else {
+    decode_route_kernel<KMAX><<<(p.M + 15) / 16, 256, 0, s>>>(logits, p);
+    decode_plan_kernel<0><<<1, kPlanThreads, 0, s>>>(nullptr, p);
   }
 }
 
@@ -525,20 +553,17 @@ hipError_t launch_decode(const DecodeArgs& a, const float* logits, int dtype, in
       launch_few<StreamBf16<1>, StreamMx<2>, 2, true>(a, logits, ep, s);
     return hipGetLastError();
   }
-  const dim3 block(kPlanThreads);
-  if (p.k <= 1)
-    decode_plan_kernel<1><<<1, block, 0, s>>>(logits, p);
-  else if (p.k <= 2)
-    decode_plan_kernel<2><<<1, block, 0, s>>>(logits, p);
+  if (p.k <= 2)
+    launch_plan<2>(logits, p, s);
   else if (p.k <= 4)
-    decode_plan_kernel<4><<<1, block, 0, s>>>(logits, p);
+    launch_plan<4>(logits, p, s);
   else if (p.k <= 8)
-    decode_plan_kernel<8><<<1, block, 0, s>>>(logits, p);
+    launch_plan<8>(logits, p, s);
   else
-    decode_plan_kernel<16><<<1, block, 0, s>>>(logits, p);
+    launch_plan<16>(logits, p, s);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  const int entries = decode_max_entries(p.M, p.k, p.EL);
+  const int entries = decode_max_entries(p.M, p.k, p.E, p.EL);
   if (dtype == MOE_DTYPE_F32)
     launch_products<StreamF32, StreamF32, 0, false>(a, entries, s);
   else if (dtype == MOE_DTYPE_BF16 && planes == 3)

@@ -105,8 +105,8 @@ struct DecodeArgs {
   int H, F;
   uint32_t x_pitch, h_pitch, wd_pitch;  // bytes of a row of x (and of the gate and up weights), h, W_down
 };
-int decode_entry_rows(int M);
-size_t decode_entry_bytes(int M, int k, int EL);  // of DecodePlan::entries
+int decode_entry_rows(int M, int k, int E);
+size_t decode_entry_bytes(int M, int k, int E, int EL);  // of DecodePlan::entries
 hipError_t launch_decode(const DecodeArgs& a, const float* logits, int dtype, int planes, const OutEpilogue& ep,
                          hipStream_t s);
 

@@ -16,7 +16,7 @@
 // are different rows, needs no LDS but gives 38 bytes per ns and CU from the
 // L2; 8 lanes to a row give 124 (measured; HBM gives 27).  With weights and
 // token rows on that path, 200 rows x 4096 x 4096 took 33 us.
-// Rows that do not exist read the last one that does (their sums are not
+// Weight rows that do not exist read the last one that does (their sums are not
 // used).
 #pragma once
 
