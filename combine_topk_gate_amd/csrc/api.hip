@@ -245,13 +245,13 @@ DecodeWs decode_ws(const moe_problem_t* p) {
   DecodeWs w;
   size_t o = 0;
   w.hdr = o; o += align_up(16);
-  w.entries = o; o += align_up(decode_entry_bytes(M, p->topk, p->num_experts, held(p)));
+  w.entries = o; o += align_up(decode_entry_bytes(M, p->topk, p->num_experts, held(p), is_mx(p)));
   w.list = o; o += align_up((size_t)R * 4);
   w.f2s = o; o += align_up((size_t)R * 4);
   w.w = o; o += align_up((size_t)R * 4);
   w.arrived = o; o += align_up((size_t)p->hidden / 16 * 4);
   w.hact = o; o += align_up((size_t)R * p->ffn * (p->dtype == MOE_DTYPE_F32 ? 4 : 6));
-  w.y = o; o += align_up((size_t)R * p->hidden * 4);
+  w.y = o; o += align_up((size_t)R * p->hidden * 4 * decode_parts(M, p->topk, p->num_experts, is_mx(p)));
   w.total = o;
   return w;
 }
@@ -625,7 +625,7 @@ moe_status_t moe_layer_decode(const moe_problem_t* p, const void* x, const float
   a.plan.E = p->num_experts;
   a.plan.EL = held(p);
   a.plan.base = held_base(p);
-  a.plan.rows = decode_entry_rows(a.plan.M, a.plan.k, a.plan.E);
+  a.plan.rows = decode_entry_rows(a.plan.M, a.plan.k, a.plan.E, mx);
   a.plan.hdr = at<int32_t>(ws, L.hdr);
   a.plan.entries = at<int4>(ws, L.entries);
   a.plan.list = at<int32_t>(ws, L.list);

@@ -206,7 +206,7 @@ __global__ __launch_bounds__(kStreamThreads) void decode_l0_kernel(DecodeArgs a)
     decode_l0_tile<Op, NF, MAXNT, NP>(a, ent, lds);
 }
 
-// Layer0 where experts get many rows (entries of up to 64): the waves split
+// Layer0 where experts get many rows (entries of 64 or 128): the waves split
 // the columns and share the token rows.
 constexpr int kWideL0 = 4;  // waves; 16 columns each
 
@@ -233,20 +233,22 @@ __device__ __forceinline__ void decode_l0_wide_tile(const DecodeArgs& a, int4 en
   }
 }
 
-template <class Op, int NP>
+template <class Op, int MAXNT, int NP>
 __global__ __launch_bounds__(64 * kWideL0) void decode_l0_wide_kernel(DecodeArgs a) {
-  __shared__ __attribute__((aligned(16))) char lds[stream_wide_bytes<Op, kWideL0, 2, 4>()];
+  __shared__ __attribute__((aligned(16))) char lds[stream_wide_bytes<Op, kWideL0, 2, MAXNT>()];
   if ((int)blockIdx.y >= a.plan.hdr[0]) return;
   const int4 ent = a.plan.entries[blockIdx.y];
-  if (ent.z <= 32)
-    decode_l0_wide_tile<Op, 2, NP>(a, ent, lds);
+  if (ent.z <= 8 * MAXNT)
+    decode_l0_wide_tile<Op, MAXNT / 2, NP>(a, ent, lds);
   else
-    decode_l0_wide_tile<Op, 4, NP>(a, ent, lds);
+    decode_l0_wide_tile<Op, MAXNT, NP>(a, ent, lds);
 }
 
 // Layer1 of one entry: 16 NW WAVES columns of y for its rows (f32, at the
 // pair's own row).  Waves split the columns: h is wider than a weight row (two
-// or three planes), so its lines are shared.
+// or three planes), so its lines are shared.  Block z of gridDim.z takes its
+// share of the lines and has a y of its own, which the combine adds: so that
+// there is a block for every CU where the tiles are large.
 template <class Op, int WAVES, int NW, int NT, bool MX>
 __device__ __forceinline__ void decode_l1_tile(const DecodeArgs& a, int4 ent, char* lds) {
   const int n0 = blockIdx.x * 16 * NW * WAVES;
@@ -258,14 +260,17 @@ __device__ __forceinline__ void decode_l1_tile(const DecodeArgs& a, int4 ent, ch
   s.x = a.hact;
   s.x_bytes = (uint32_t)(a.plan.M * a.plan.k) * a.h_pitch;
   s.plane = 2u * a.F;
-  s.lines = a.F / Op::kLine;
+  const int lines = a.F / Op::kLine, parts = gridDim.z;
+  s.line0 = (int)blockIdx.z * lines / parts;
+  s.lines = (int)(blockIdx.z + 1) * lines / parts - s.line0;
   if constexpr (MX) {
     s.scale = a.wd_scale + (row0 >> 5) * (int64_t)a.F;
     s.scale_row = (int)(row0 & 31);
     s.scale_pitch = a.F;
   }
   f32x4_t acc[NW][NT];
-  constexpr int kDepth = Op::kXH * NT * Op::kP > 12 ? 2 : 4;
+  constexpr int kDepth = Op::kXH * NT * Op::kP > 12 ? 2 : NW > 1 ? 3 : 4;
+  float* y = a.y + (int64_t)blockIdx.z * a.plan.M * a.plan.k * a.H;
   stream_wide<Op, WAVES, NW, false, NT, kDepth, true>(
       s, [&](int i) { return decode_row(a.plan, ent, i, 1, a.h_pitch); }, lds, acc);
   const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
@@ -277,7 +282,7 @@ __device__ __forceinline__ void decode_l1_tile(const DecodeArgs& a, int4 ent, ch
 #pragma unroll
     for (int g = 0; g < NW; ++g) {
       const int n = n0 + 16 * (wave * NW + g) + 4 * (lane >> 4);
-      if (n < a.H) *reinterpret_cast<f32x4_t*>(a.y + pair * a.H + n) = acc[g][j];
+      if (n < a.H) *reinterpret_cast<f32x4_t*>(y + pair * a.H + n) = acc[g][j];
     }
   }
 }
@@ -291,6 +296,43 @@ __global__ __launch_bounds__(64 * WAVES) void decode_l1_kernel(DecodeArgs a) {
     decode_l1_tile<Op, WAVES, NW, (MAXNT > 1 ? MAXNT / 2 : 1), MX>(a, ent, lds);
   else
     decode_l1_tile<Op, WAVES, NW, MAXNT, MX>(a, ent, lds);
+}
+
+// out[t, n .. n + 3] a thread: the pairs in slot order, each the sum of its
+// parts in order.
+__global__ __launch_bounds__(256) void decode_combine_kernel(DecodeArgs a, int parts, OutEpilogue ep) {
+  const DecodePlan& p = a.plan;
+  const int64_t i = 4 * ((int64_t)blockIdx.x * 256 + threadIdx.x);
+  if (i >= (int64_t)p.M * a.H) return;
+  const int t = (int)(i / a.H), n = (int)(i - (int64_t)t * a.H);
+  const int64_t part = (int64_t)p.M * p.k * a.H;
+  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+  // 4 slots' loads in flight
+  for (int f0 = t * p.k; f0 < (t + 1) * p.k; f0 += 4) {
+    f32x4_t y[4];
+    float w[4];
+    bool has[4];
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const int f = min(f0 + u, (t + 1) * p.k - 1);
+      has[u] = f0 + u < (t + 1) * p.k && p.f2s[f] >= 0;
+      w[u] = p.w[f];
+      const float* at = a.y + (int64_t)f * a.H + n;
+      y[u] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+      if (!has[u]) continue;
+      y[u] = *reinterpret_cast<const f32x4_t*>(at);
+      for (int s = 1; s < parts; ++s) y[u] += *reinterpret_cast<const f32x4_t*>(at + s * part);
+    }
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      if (!has[u]) continue;
+      o.x = fmaf(w[u], y[u][0], o.x);
+      o.y = fmaf(w[u], y[u][1], o.y);
+      o.z = fmaf(w[u], y[u][2], o.z);
+      o.w = fmaf(w[u], y[u][3], o.w);
+    }
+  }
+  store_out(ep, i, o);
 }
 
 // ------------------------------------------------------------ few tokens ---
@@ -489,39 +531,60 @@ static void launch_few(const DecodeArgs& a, const float* logits, const OutEpilog
 
 // Rows an entry may hold, in 16s.  An expert gets at most one row of every
 // token: 16 tokens need no more than 16.  Beyond, entries of 32 rows stream
-// the weights by reduction-splitting waves, entries of 64 by column-splitting
-// ones that share the rows; the latter where experts get more than 16 rows on
-// average.  (Layer0 of 8 experts 4096 x 14336: 25 rows each 302 us with 32-row
-// entries, 380 with 64; 50 rows each, where every expert takes two entries of
-// 32 and the weights are read twice, 540 and 345.)
-static int decode_max_nt(int M, int k, int E) { return M <= 16 ? 1 : M <= 32 || M * k <= 16 * E ? 2 : 4; }
-
-int decode_entry_rows(int M, int k, int E) { return 16 * decode_max_nt(M, k, E); }
-
-static int decode_max_entries(int M, int k, int E, int EL) {
-  const int R = M * k;
-  return (EL < R ? EL : R) + R / decode_entry_rows(M, k, E);
+// the weights by reduction-splitting waves, entries of 64 and 128 by
+// column-splitting ones that share the rows; the latter where experts get more
+// than 16 (40) rows on average, so that few experts' weights are read twice.
+// (Layer0 of 8 experts 4096 x 14336: 25 rows each 302 us with 32-row entries,
+// 380 with 64; 50 rows each, where every expert takes two entries of 32, 540
+// and 345.)
+// MXFP8's token lines are twice as long: 128 rows do not fit the LDS.
+static int decode_max_nt(int M, int k, int E, bool mx) {
+  return M <= 16 ? 1 : M <= 32 || M * k <= 16 * E ? 2 : mx || M <= 64 || M * k <= 40 * E ? 4 : 8;
 }
 
-size_t decode_entry_bytes(int M, int k, int E, int EL) {
-  const size_t many = sizeof(int4) * (size_t)decode_max_entries(M, k, E, EL), few = sizeof(FewEntry) * kFewPairs;
+int decode_entry_rows(int M, int k, int E, bool mx) { return 16 * decode_max_nt(M, k, E, mx); }
+
+int decode_parts(int M, int k, int E, bool mx) { return decode_max_nt(M, k, E, mx) >= 4 ? 2 : 1; }
+
+static int decode_max_entries(int M, int k, int E, int EL, bool mx) {
+  const int R = M * k;
+  return (EL < R ? EL : R) + R / decode_entry_rows(M, k, E, mx);
+}
+
+size_t decode_entry_bytes(int M, int k, int E, int EL, bool mx) {
+  const size_t many = sizeof(int4) * (size_t)decode_max_entries(M, k, E, EL, mx), few = sizeof(FewEntry) * kFewPairs;
   return many > few ? many : few;
 }
 
+// Returns the parts of Layer1's reduction (1 or 2).
 template <class Op0, class Op1, int NP, bool MX>
-static void launch_products(const DecodeArgs& a, int entries, hipStream_t s) {
-  const int nt = decode_max_nt(a.plan.M, a.plan.k, a.plan.E);
-  auto grid = [&](int n, int cols) { return dim3((unsigned)((n + cols - 1) / cols), (unsigned)entries); };
+static int launch_products(const DecodeArgs& a, int entries, hipStream_t s) {
+  const int nt = decode_max_nt(a.plan.M, a.plan.k, a.plan.E, MX);
+  auto grid = [&](int n, int cols, int parts = 1) {
+    return dim3((unsigned)((n + cols - 1) / cols), (unsigned)entries, (unsigned)parts);
+  };
   if (nt == 1) {
     decode_l0_kernel<Op0, 1, 1, NP><<<grid(a.F, 16), kStreamThreads, 0, s>>>(a);
     decode_l1_kernel<Op1, 4, 1, 1, MX><<<grid(a.H, 64), 256, 0, s>>>(a);
-  } else if (nt == 2) {
+    return 1;
+  }
+  if (nt == 2) {
     decode_l0_kernel<Op0, 1, 2, NP><<<grid(a.F, 16), kStreamThreads, 0, s>>>(a);
     decode_l1_kernel<Op1, 4, 1, 2, MX><<<grid(a.H, 64), 256, 0, s>>>(a);
-  } else {
-    decode_l0_wide_kernel<Op0, NP><<<grid(a.F, 16 * kWideL0), 64 * kWideL0, 0, s>>>(a);
-    decode_l1_kernel<Op1, 8, 1, 4, MX><<<grid(a.H, 128), 512, 0, s>>>(a);
+    return 1;
   }
+  constexpr int NW1 = MX ? 1 : 2;  // (MXFP8's lines take the registers of the second group)
+  const dim3 g0 = grid(a.F, 16 * kWideL0), g1 = grid(a.H, 128 * NW1, 2);
+  if (nt == 4) {
+    decode_l0_wide_kernel<Op0, 4, NP><<<g0, 64 * kWideL0, 0, s>>>(a);
+    decode_l1_kernel<Op1, 8, NW1, 4, MX><<<g1, 512, 0, s>>>(a);
+  } else {
+    if constexpr (!MX) {
+      decode_l0_wide_kernel<Op0, 8, NP><<<g0, 64 * kWideL0, 0, s>>>(a);
+      decode_l1_kernel<Op1, 8, NW1, 8, MX><<<g1, 512, 0, s>>>(a);
+    }
+  }
+  return 2;  // = decode_parts()
 }
 
 template <int KMAX>
@@ -563,20 +626,22 @@ hipError_t launch_decode(const DecodeArgs& a, const float* logits, int dtype, in
     launch_plan<16>(logits, p, s);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  const int entries = decode_max_entries(p.M, p.k, p.E, p.EL);
+  const int entries = decode_max_entries(p.M, p.k, p.E, p.EL, dtype == MOE_DTYPE_BF16_MXFP8);
+  int parts;
   if (dtype == MOE_DTYPE_F32)
-    launch_products<StreamF32, StreamF32, 0, false>(a, entries, s);
+    parts = launch_products<StreamF32, StreamF32, 0, false>(a, entries, s);
   else if (dtype == MOE_DTYPE_BF16 && planes == 3)
-    launch_products<StreamBf16<1>, StreamBf16<3>, 3, false>(a, entries, s);
+    parts = launch_products<StreamBf16<1>, StreamBf16<3>, 3, false>(a, entries, s);
   else if (dtype == MOE_DTYPE_BF16)
-    launch_products<StreamBf16<1>, StreamBf16<2>, 2, false>(a, entries, s);
+    parts = launch_products<StreamBf16<1>, StreamBf16<2>, 2, false>(a, entries, s);
   else if (planes == 3)
-    launch_products<StreamBf16<1>, StreamMx<3>, 3, true>(a, entries, s);
+    parts = launch_products<StreamBf16<1>, StreamMx<3>, 3, true>(a, entries, s);
   else
-    launch_products<StreamBf16<1>, StreamMx<2>, 2, true>(a, entries, s);
+    parts = launch_products<StreamBf16<1>, StreamMx<2>, 2, true>(a, entries, s);
   e = hipGetLastError();
   if (e != hipSuccess) return e;
-  return launch_combine(a.y, p.w, p.f2s, p.M, a.H, p.k, ep, s);
+  decode_combine_kernel<<<(unsigned)(((int64_t)p.M * a.H / 4 + 255) / 256), 256, 0, s>>>(a, parts, ep);
+  return hipGetLastError();
 }
 
 }  // namespace moe

@@ -100,13 +100,14 @@ struct DecodeArgs {
   const void* w_down;
   const uint8_t* wd_scale;  // MXFP8: the scale bytes of W_down
   void* hact;               // [M k][planes][F] bf16, or [M k][F] f32
-  float* y;                 // [M k][H]
+  float* y;                 // [decode_parts][M k][H]
   int32_t* arrived;         // [H / 16] Layer1 blocks done per 16 columns (few tokens)
   int H, F;
   uint32_t x_pitch, h_pitch, wd_pitch;  // bytes of a row of x (and of the gate and up weights), h, W_down
 };
-int decode_entry_rows(int M, int k, int E);
-size_t decode_entry_bytes(int M, int k, int E, int EL);  // of DecodePlan::entries
+int decode_entry_rows(int M, int k, int E, bool mx);
+int decode_parts(int M, int k, int E, bool mx);  // y's in the workspace
+size_t decode_entry_bytes(int M, int k, int E, int EL, bool mx);  // of DecodePlan::entries
 hipError_t launch_decode(const DecodeArgs& a, const float* logits, int dtype, int planes, const OutEpilogue& ep,
                          hipStream_t s);
 

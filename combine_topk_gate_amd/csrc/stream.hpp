@@ -135,6 +135,7 @@ struct StreamArgs {
   uint32_t x_bytes;      // bytes that exist there (below 2^31)
   uint32_t plane;        // bytes between the planes of a token row
   int lines;             // K / Op::kLine
+  int line0;             // first line of the tile (stream_wide), usually 0
   const uint8_t* scale;  // MXFP8: scale bytes of the 32-row group that holds weight row 0
   int scale_row;         // row of that group which is weight row 0 (0 or 16)
   uint32_t scale_pitch;  // bytes of a 32-row group (= K)
@@ -339,7 +340,7 @@ __device__ __forceinline__ void stream_wide(const StreamArgs& a, RowOff row_off,
   static_assert(!PAIRED || NW % 2 == 0, "a wave's pairs are its own");
   auto load = [&](Line& c, int line) {
     const bool live = line < a.lines;  // else nothing is read (see stream_share)
-    const uint32_t at = live ? (uint32_t)line : 0u;
+    const uint32_t at = live ? (uint32_t)(a.line0 + line) : 0u;
     const __amdgpu_buffer_rsrc_t r0 = make_rsrc(a.w0, live ? w_bytes : 0u);
     const __amdgpu_buffer_rsrc_t r1 = make_rsrc(PAIRED ? a.w1 : a.w0, live ? w_bytes : 0u);
     const __amdgpu_buffer_rsrc_t rx = make_rsrc(a.x, live ? a.x_bytes : 0u);
@@ -387,20 +388,25 @@ __device__ __forceinline__ void stream_wide(const StreamArgs& a, RowOff row_off,
 #pragma unroll
         for (int g = 0; g < NW; ++g)
           w[g] = *reinterpret_cast<const i32x4_t*>(ldw + (16 * g + r) * 128 + (((4 * h + q) ^ swz_w(r)) << 4));
-        i32x4_t x[NT][Op::kXH * Op::kP];
+        // up to 4 groups of 16 token rows at a time, so that their fragments fit
+        constexpr int NS = NT > 4 ? 4 : NT;
 #pragma unroll
-        for (int p = 0; p < Op::kP; ++p)
+        for (int j0 = 0; j0 < NT; j0 += NS) {
+          i32x4_t x[NS][Op::kXH * Op::kP];
 #pragma unroll
-          for (int j = 0; j < NT; ++j)
+          for (int p = 0; p < Op::kP; ++p)
 #pragma unroll
-            for (int t = 0; t < Op::kXH; ++t)
-              x[j][p * Op::kXH + t] = *reinterpret_cast<const i32x4_t*>(
-                  xb + ((p * NT + j) * 16 + r) * XPITCH + ((Op::x_chunk(h, q, t) ^ swz_x(r)) << 4));
+            for (int j = 0; j < NS; ++j)
 #pragma unroll
-        for (int g = 0; g < NW; ++g) {
-          const float sc =
-              MX ? __builtin_bit_cast(float, ((scales[MX ? g : 0] >> (8 * (2 * h + (q >> 1)))) & 0xFFu) << 23) : 0.f;
-          Op::template mma<NT>(acc[g], w[g], sc, x);
+              for (int t = 0; t < Op::kXH; ++t)
+                x[j][p * Op::kXH + t] = *reinterpret_cast<const i32x4_t*>(
+                    xb + ((p * NT + j0 + j) * 16 + r) * XPITCH + ((Op::x_chunk(h, q, t) ^ swz_x(r)) << 4));
+#pragma unroll
+          for (int g = 0; g < NW; ++g) {
+            const float sc =
+                MX ? __builtin_bit_cast(float, ((scales[MX ? g : 0] >> (8 * (2 * h + (q >> 1)))) & 0xFFu) << 23) : 0.f;
+            Op::template mma<NS>(*reinterpret_cast<f32x4_t(*)[NS]>(&acc[g][j0]), w[g], sc, x);
+          }
         }
       }
       __builtin_amdgcn_sched_barrier(0);
