@@ -276,47 +276,45 @@ def moe_layer_ex(p, x, logits, src_block, w_gate, w_up, w_down, epi, out, ws, au
                                        _nbytes(ws), _stream(stream)), "moe_layer_ex")
 
 
-def _refuse(what, name, t, dtype, shape, device):
+def _refuse(what, name, t, dtype, shape):
     raise MoeError(MOE_ERR_INVALID_ARGUMENT,
-                   f"{what}: {name} must be a contiguous {dtype} tensor of shape {shape} on {device}, a GPU; "
+                   f"{what}: {name} must be a contiguous {dtype} tensor of shape {shape} on the GPU that holds x; "
                    f"got {t.dtype} {tuple(t.shape)} strides {t.stride()} on {t.device}")
 
 
-def _operand(what, name, t, dtype, shape, device):
+def _addr(what, name, t, dtype, shape, gpu):
     """The data pointer of t (None: NULL), which must be what the call reads:
-    contiguous, of this type and shape (None: any), on this GPU; otherwise
-    MoeError with MOE_ERR_INVALID_ARGUMENT, before the library sees it."""
+    contiguous, of this type and shape, on GPU number `gpu` (-1, no GPU, never
+    is); otherwise MoeError with MOE_ERR_INVALID_ARGUMENT, before the library
+    sees it."""
     if t is None:
         return None
-    if t.dtype != dtype or (shape is not None and t.shape != shape) or not t.is_contiguous() or t.device != device:
-        _refuse(what, name, t, dtype, shape, device)
-    return t.data_ptr()
+    if t.dtype is dtype and t.shape == shape and t.get_device() == gpu >= 0 and t.is_contiguous():
+        return t.data_ptr()
+    _refuse(what, name, t, dtype, shape)
 
 
-def _call_on(device, stream, call):
-    """call(stream) with `device` current: a stream given is used as it is,
-    otherwise torch's current stream of that device."""
+def _workspace(what, ws, gpu):
+    """(pointer, bytes) of a workspace: any contiguous tensor on the GPU."""
+    if ws is None:
+        return None, 0
+    if ws.get_device() != gpu or not ws.is_contiguous():
+        _refuse(what, "ws", ws, "uint8", "any")
+    return ws.data_ptr(), ws.numel() * ws.element_size()
+
+
+def _call_on(gpu, stream, f, *args):
+    """f(*args, stream) with GPU number `gpu` current, on the stream given or
+    torch's current one of that GPU."""
     import torch
     if stream is None:
-        raw = torch.cuda.current_stream(device).cuda_stream
+        raw = torch._C._cuda_getCurrentRawStream(gpu)
     else:
         raw = stream if isinstance(stream, int) else stream.cuda_stream
-    if device.index == torch.cuda.current_device():
-        return call(raw)
-    with torch.cuda.device(device):
-        return call(raw)
-
-
-def _epilogue_type(epi):
-    import torch
-    return torch.bfloat16 if epi is not None and epi.out_dtype == MOE_DTYPE_BF16 else torch.float32
-
-
-def _activation_type(what, x, dtype):
-    import torch
-    if not x.is_cuda:
-        _refuse(what, "x", x, "floating", None, "cuda")
-    return torch.float32 if dtype == MOE_DTYPE_F32 else torch.bfloat16
+    if torch._C._cuda_getDevice() == gpu:
+        return f(*args, raw)
+    with torch.cuda.device(gpu):
+        return f(*args, raw)
 
 
 def moe_layer_decode(p, x, logits, w_gate, w_up, w_down, epi, out, ws, stream=None):
@@ -326,17 +324,21 @@ def moe_layer_decode(p, x, logits, w_gate, w_up, w_down, epi, out, ws, stream=No
     moe_workspace_bytes(p, MOE_OP_LAYER_DECODE) bytes."""
     import torch
     what = "moe_layer_decode"
-    M, H, F, EL, dev = p.num_tokens, p.hidden, p.ffn, p.local_experts or p.num_experts, x.device
-    act = _activation_type(what, x, p.dtype)
-    down = (torch.uint8, (mx_bytes(EL * H, F),)) if p.dtype == MOE_DTYPE_BF16_MXFP8 else (act, (EL, H, F))
-    a = (_operand(what, "x", x, act, (M, H), dev),
-         _operand(what, "logits", logits, torch.float32, (M, p.num_experts), dev),
-         _operand(what, "w_gate", w_gate, act, (EL, F, H), dev), _operand(what, "w_up", w_up, act, (EL, F, H), dev),
-         _operand(what, "w_down", w_down, *down, dev), ctypes.byref(epi) if epi is not None else None,
-         _operand(what, "out", out, _epilogue_type(epi), (M, H), dev),
-         _operand(what, "ws", ws, torch.uint8, None, dev), 0 if ws is None else ws.numel())
-    f = load_library().moe_layer_decode
-    _check(_call_on(dev, stream, lambda s: f(ctypes.byref(p), *a, s)), what)
+    f32 = torch.float32
+    M, H, F, E, dtype = p.num_tokens, p.hidden, p.ffn, p.num_experts, p.dtype
+    EL, gpu = p.local_experts or E, x.get_device()
+    act = f32 if dtype == MOE_DTYPE_F32 else torch.bfloat16
+    odt = torch.bfloat16 if epi is not None and epi.out_dtype == MOE_DTYPE_BF16 else f32
+    if dtype == MOE_DTYPE_BF16_MXFP8:
+        down = _addr(what, "w_down", w_down, torch.uint8, (mx_bytes(EL * H, F),), gpu)
+    else:
+        down = _addr(what, "w_down", w_down, act, (EL, H, F), gpu)
+    _check(_call_on(gpu, stream, load_library().moe_layer_decode, ctypes.byref(p),
+                    _addr(what, "x", x, act, (M, H), gpu), _addr(what, "logits", logits, f32, (M, E), gpu),
+                    _addr(what, "w_gate", w_gate, act, (EL, F, H), gpu),
+                    _addr(what, "w_up", w_up, act, (EL, F, H), gpu), down,
+                    None if epi is None else ctypes.byref(epi), _addr(what, "out", out, odt, (M, H), gpu),
+                    *_workspace(what, ws, gpu)), what)
 
 
 def moe_adapter_workspace_bytes(q: AdapterProblem) -> int:
@@ -351,17 +353,18 @@ def moe_adapter_linear(q, x, w, a, b, scale, adapter_idx, epi, out, ws, stream=N
     num_adapters 0: a, b, scale, adapter_idx and ws may be None."""
     import torch
     what = "moe_adapter_linear"
-    M, H, N, r, P, dev = q.num_tokens, q.in_features, q.out_features, q.rank, q.num_adapters, x.device
-    act = _activation_type(what, x, q.dtype)
-    args = (_operand(what, "x", x, act, (M, H), dev), _operand(what, "w", w, act, (N, H), dev),
-            _operand(what, "a", a, act, (P, r, H), dev), _operand(what, "b", b, act, (P, N, r), dev),
-            _operand(what, "scale", scale, torch.float32, (P,), dev),
-            _operand(what, "adapter_idx", adapter_idx, torch.int32, (M,), dev),
-            ctypes.byref(epi) if epi is not None else None,
-            _operand(what, "out", out, _epilogue_type(epi), (M, N), dev),
-            _operand(what, "ws", ws, torch.uint8, None, dev), 0 if ws is None else ws.numel())
-    f = load_library().moe_adapter_linear
-    _check(_call_on(dev, stream, lambda s: f(ctypes.byref(q), *args, s)), what)
+    f32 = torch.float32
+    M, H, N, r, P = q.num_tokens, q.in_features, q.out_features, q.rank, q.num_adapters
+    gpu = x.get_device()
+    act = f32 if q.dtype == MOE_DTYPE_F32 else torch.bfloat16
+    odt = torch.bfloat16 if epi is not None and epi.out_dtype == MOE_DTYPE_BF16 else f32
+    _check(_call_on(gpu, stream, load_library().moe_adapter_linear, ctypes.byref(q),
+                    _addr(what, "x", x, act, (M, H), gpu), _addr(what, "w", w, act, (N, H), gpu),
+                    _addr(what, "a", a, act, (P, r, H), gpu), _addr(what, "b", b, act, (P, N, r), gpu),
+                    _addr(what, "scale", scale, f32, (P,), gpu),
+                    _addr(what, "adapter_idx", adapter_idx, torch.int32, (M,), gpu),
+                    None if epi is None else ctypes.byref(epi), _addr(what, "out", out, odt, (M, N), gpu),
+                    *_workspace(what, ws, gpu)), what)
 
 
 def moe_debug_device_status(p, ws, stream=None) -> int:
