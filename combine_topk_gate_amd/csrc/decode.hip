@@ -344,6 +344,9 @@ __global__ __launch_bounds__(256) void decode_combine_kernel(DecodeArgs a, int p
 // is).  Layer1 blocks of 16 waves that own 16 columns of every pair need no
 // such hand-over, but then each expert's stream starts when the one before
 // has ended: 73 us at 8 tokens, 64 experts of 2048 x 1408, instead of 43.
+// (Not kept: 8 waves a block, 15.2 + 11.2 us instead of 14.3 + 9.6 at one token
+// and 4 such experts; every wave routing for itself without the exchange
+// through LDS, 88 us instead of 78 for Layer0 of 2 experts 4096 x 14336.)
 constexpr int kFewTokens = 8;
 constexpr int kFewPairs = 64;
 constexpr int kFewRows = 8;  // rows of one expert: one a token
@@ -533,13 +536,13 @@ static void launch_few(const DecodeArgs& a, const float* logits, const OutEpilog
 // token: 16 tokens need no more than 16.  Beyond, entries of 32 rows stream
 // the weights by reduction-splitting waves, entries of 64 and 128 by
 // column-splitting ones that share the rows; the latter where experts get more
-// than 16 (40) rows on average, so that few experts' weights are read twice.
-// (Layer0 of 8 experts 4096 x 14336: 25 rows each 302 us with 32-row entries,
-// 380 with 64; 50 rows each, where every expert takes two entries of 32, 540
+// than 24 (40) rows on average, so that few experts' weights are read twice.
+// (Layer0 of 8 experts 4096 x 14336: 25 rows each 305 us with 32-row entries,
+// 345 with 64; 50 rows each, where every expert takes two entries of 32, 540
 // and 345.)
 // MXFP8's token lines are twice as long: 128 rows do not fit the LDS.
 static int decode_max_nt(int M, int k, int E, bool mx) {
-  return M <= 16 ? 1 : M <= 32 || M * k <= 16 * E ? 2 : mx || M <= 64 || M * k <= 40 * E ? 4 : 8;
+  return M <= 16 ? 1 : M <= 32 || M * k <= 24 * E ? 2 : mx || M <= 64 || M * k <= 40 * E ? 4 : 8;
 }
 
 int decode_entry_rows(int M, int k, int E, bool mx) { return 16 * decode_max_nt(M, k, E, mx); }
@@ -565,12 +568,12 @@ static int launch_products(const DecodeArgs& a, int entries, hipStream_t s) {
   };
   if (nt == 1) {
     decode_l0_kernel<Op0, 1, 1, NP><<<grid(a.F, 16), kStreamThreads, 0, s>>>(a);
-    decode_l1_kernel<Op1, 4, 1, 1, MX><<<grid(a.H, 64), 256, 0, s>>>(a);
+    decode_l1_kernel<Op1, 4, 2, 1, MX><<<grid(a.H, 128), 256, 0, s>>>(a);
     return 1;
   }
   if (nt == 2) {
     decode_l0_kernel<Op0, 1, 2, NP><<<grid(a.F, 16), kStreamThreads, 0, s>>>(a);
-    decode_l1_kernel<Op1, 4, 1, 2, MX><<<grid(a.H, 64), 256, 0, s>>>(a);
+    decode_l1_kernel<Op1, 4, 2, 2, MX><<<grid(a.H, 128), 256, 0, s>>>(a);
     return 1;
   }
   constexpr int NW1 = MX ? 1 : 2;  // (MXFP8's lines take the registers of the second group)
