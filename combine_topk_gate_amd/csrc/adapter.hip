@@ -116,8 +116,8 @@ __global__ __launch_bounds__(64 * WAVES) void adapter_stream_kernel(AdapterArgs 
   __shared__ __attribute__((aligned(16))) char lds[kLds];
   // the row blocks of one weight block run next to each other on one XCD (whose
   // workgroups come 8 apart), so its L2 reads the weights once
-  const int64_t per = ((int64_t)mb * nb + 7) / 8, v0 = (int64_t)(blockIdx.x & 7) * per + (blockIdx.x >> 3);
-  if (v0 >= (int64_t)mb * nb) return;
+  const int64_t v0 = xcd_tile((int64_t)mb * nb);
+  if (v0 < 0) return;
   const int64_t m0 = v0 % mb * 16 * NT;
   const int n0 = (int)(v0 / mb) * 16 * NW;
   const int lane = threadIdx.x & 63;
@@ -179,8 +179,7 @@ static void launch_shrink(const AdapterArgs& a, hipStream_t s) {
 template <class Op, class T, int WAVES, int NW, int NT>
 static void launch_stream_as(const AdapterArgs& a, hipStream_t s) {
   const int mb = (int)((a.M + 16 * NT - 1) / (16 * NT)), nb = (a.N + 16 * NW - 1) / (16 * NW);
-  const unsigned grid = (unsigned)(((int64_t)mb * nb + 7) / 8 * 8);
-  adapter_stream_kernel<Op, T, WAVES, NW, NT><<<grid, 64 * WAVES, 0, s>>>(a, mb, nb);
+  adapter_stream_kernel<Op, T, WAVES, NW, NT><<<tile_grid((int64_t)mb * nb), 64 * WAVES, 0, s>>>(a, mb, nb);
 }
 
 // Which kernel: the tiles of each differ in how long a round of them (one
@@ -237,7 +236,7 @@ hipError_t launch_adapter_linear(AdapterArgs a, bool f32, hipStream_t s) {
   } else {
     if ((e = shrink(a.out.out_bf16 ? 2 : 3)) != hipSuccess) return e;
     const int64_t rows = g256 < g128 ? 256 : 128, mt = (a.M + rows - 1) / rows, nt = (a.N + 255) / 256;
-    const dim3 grid((unsigned)((mt * nt + 7) / 8 * 8));
+    const dim3 grid = tile_grid(mt * nt);
     if (g256 < g128)
       adapter_gemm_kernel<256><<<grid, kGemmThreads, 0, s>>>(a, (int)mt, (int)nt);
     else

@@ -44,6 +44,23 @@ __device__ __forceinline__ void adapter_store(const AdapterArgs& a, int64_t m, i
   }
 }
 
+// Grid of a kernel whose blocks take `tiles` tiles by xcd_tile: a multiple of 8
+// wide, and high where the work items of one dimension would pass 32 bits.
+inline dim3 tile_grid(int64_t tiles) {
+  constexpr int64_t kWide = 1 << 20;
+  const int64_t n = (tiles + 7) / 8 * 8;
+  return n <= kWide ? dim3((unsigned)n) : dim3((unsigned)kWide, (unsigned)((n + kWide - 1) / kWide));
+}
+
+// This block's tile, -1 for none: the workgroups go to the 8 XCDs in turn, and
+// each XCD's take a contiguous run of tiles, so that neighbouring tiles share
+// operands in its L2.
+__device__ __forceinline__ int64_t xcd_tile(int64_t tiles) {
+  const int64_t b = (int64_t)blockIdx.y * gridDim.x + blockIdx.x, per = (tiles + 7) / 8;
+  const int64_t v = (b & 7) * per + (b >> 3);
+  return (b >> 3) < per && v < tiles ? v : -1;
+}
+
 struct AdapterTileLds {
   int id[256];    // adapter of each row, -1: none
   int list[256];  // the tile's distinct adapters
@@ -419,15 +436,13 @@ __device__ __forceinline__ void adapter_gemm_tile(const AdapterArgs& p, int64_t 
 
 // Tiles of the grid, in an order that lets the workgroups of one XCD share
 // operand panels in its L2: 8 row tiles x all column tiles at a time, the row
-// tiles fastest, a contiguous run of that order per XCD (workgroups go to the
-// 8 XCDs in turn).
+// tiles fastest, a contiguous run of that order per XCD.
 template <int TM>
 __global__ __launch_bounds__(kGemmThreads) void adapter_gemm_kernel(AdapterArgs p, int mt, int nt) {
   __shared__ __attribute__((aligned(16))) char lds[kGemmLdsBytes];
   __shared__ AdapterTileLds tl;
-  const int64_t tiles = (int64_t)mt * nt, per = (tiles + 7) / 8;
-  const int64_t v = (int64_t)(blockIdx.x & 7) * per + (blockIdx.x >> 3);
-  if (v >= tiles) return;
+  const int64_t v = xcd_tile((int64_t)mt * nt);
+  if (v < 0) return;
   const int64_t band = v / (8ll * nt);
   const int rb = min(8, mt - (int)band * 8);
   const int64_t in = v - band * 8ll * nt;

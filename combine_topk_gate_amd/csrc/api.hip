@@ -230,7 +230,7 @@ LayerWs layer_ws(const moe_problem_t* p) {
 
 // ------------------------------------------------------- decode layer ----
 // bf16 planes of h (0: f32): three hold the f32 value exactly, two hold it
-// to 2^-17, for a bf16 output.
+// to 2^-16, for a bf16 output.
 int decode_planes(const moe_problem_t* p, const OutEpilogue& ep) {
   return p->dtype == MOE_DTYPE_F32 ? 0 : ep.out_bf16 ? 2 : 3;
 }
@@ -286,7 +286,8 @@ moe_status_t check_adapter(const moe_adapter_problem_t* q) {
   if (q->num_adapters > 0 && (q->rank < 8 || q->rank > 256 || q->rank % 8)) return MOE_ERR_INVALID_ARGUMENT;
   if (q->dtype != MOE_DTYPE_F32 && q->dtype != MOE_DTYPE_BF16)
     return q->dtype == MOE_DTYPE_BF16_MXFP8 ? MOE_ERR_UNSUPPORTED : MOE_ERR_INVALID_ARGUMENT;
-  if (q->num_tokens >= (1ll << 31)) return MOE_ERR_UNSUPPORTED;
+  // grids: 512 work items per 16 rows, below 2^32; a block per 16 x 16 outputs
+  if (q->num_tokens >= (1ll << 27) || q->num_tokens * q->out_features >= (1ll << 40)) return MOE_ERR_UNSUPPORTED;
   return MOE_OK;
 }
 

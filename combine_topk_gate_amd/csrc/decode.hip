@@ -15,8 +15,8 @@
 // h is not rounded to the layer's type between the products as in the chain
 // (there it halves the traffic of R x F values; here R is small): it is kept
 // in f32, for bf16 weights as bf16 planes whose sum is the f32 value (three,
-// exact, for an f32 output; two, 2^-17 of the value, for a bf16 output, whose
-// own rounding is 2^-9).
+// exact, for an f32 output; two, 2^-16 of the value, for a bf16 output, whose
+// own rounding is 2^-8).
 #include "common.hpp"
 #include "launch.hpp"
 #include "stream.hpp"

@@ -36,13 +36,22 @@ __device__ __forceinline__ i32x4_t load_weight(__amdgpu_buffer_rsrc_t r, uint32_
 }
 
 // f32 value as NP bf16 values whose sum is the value (NP = 3: exactly, but
-// for magnitudes below 2^-110; NP = 2: to 2^-17 of it).
+// for magnitudes below 2^-110; NP = 2: to 2^-16 of it).  An infinity or NaN is
+// its first plane alone; a finite value that would round to infinity is cut
+// off instead of rounded there.
 template <int NP>
 __device__ __forceinline__ void split_bf16(float v, __bf16 (&p)[NP]) {
+  p[0] = (__bf16)v;
+  float f = (float)p[0];
+  if (__builtin_isinf(f)) {
+    f = __builtin_bit_cast(float, __builtin_bit_cast(uint32_t, v) & 0xFFFF0000u);
+    p[0] = (__bf16)f;
+  }
+  float rest = __builtin_isfinite(f) ? v - f : 0.0f;
 #pragma unroll
-  for (int i = 0; i < NP; ++i) {
-    p[i] = (__bf16)v;
-    v -= (float)p[i];
+  for (int i = 1; i < NP; ++i) {
+    p[i] = (__bf16)rest;
+    rest -= (float)p[i];
   }
 }
 

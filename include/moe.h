@@ -390,7 +390,7 @@ moe_status_t moe_layer_ex(const moe_problem_t* p, const void* x, const float* lo
  *   - a logit of -inf is an expert the token may not choose: it is never
  *     chosen, a token with fewer than k others uses those, and a row with
  *     none (an idle row of a fixed batch) gives 0 (plus the residual);
- *   - the activation between the products is kept in f32 (to 2^-17 when the
+ *   - the activation between the products is kept in f32 (to 2^-16 when the
  *     output is bf16), not rounded to the dtype.  MOE_DTYPE_BF16_MXFP8 takes
  *     W_down in MXFP8 as moe_layer does, and its activation is not quantised
  *     (the products are bound by reading the weights);
@@ -425,9 +425,9 @@ moe_status_t moe_layer_decode(const moe_problem_t* p, const void* x, const float
  *   [M,N] (NULL: f32 out, no residual).  out may be the residual itself
  *   (same type), and otherwise overlaps neither x, w, residual nor ws.
  *   P = 0: the projection alone (a, b, scale, adapter_idx and ws unused).
- * Limits: 0 <= M < 2^31; H a multiple of 64 in [64, 65536]; 1 <= N <= 65536;
- * rank a multiple of 8 in [8, 256] (smaller ranks: pad with zeros); 0 <= P
- * <= 65536.
+ * Limits: 0 <= M < 2^27 and M N < 2^40 (else MOE_ERR_UNSUPPORTED); H a
+ * multiple of 64 in [64, 65536]; 1 <= N <= 65536; rank a multiple of 8 in [8,
+ * 256] (smaller ranks: pad with zeros); 0 <= P <= 65536.
  *   ws: moe_adapter_workspace_bytes(q) bytes, 256-byte aligned, for this call
  *   alone while it runs (its contents need no clearing).
  * MOE_DEBUG_VALIDATE=1 refuses an adapter_idx outside [-1, P).

@@ -212,6 +212,30 @@ def test_infinities_and_nan_stay_in_their_rows(what):
     assert not bool(torch.isfinite(out[touched]).all())
 
 
+@pytest.mark.parametrize("out", ["f32", "bf16"])
+@pytest.mark.parametrize("M", [1, 12, 60])
+def test_an_activation_past_the_range_is_infinite(M, out):
+    # h = silu(1e25) * 1e25 overflows f32; 3.4e38 does not, and rounds past bf16's largest value
+    H, F = 64, 64
+    p, d, epi, o, ws, _ = make(M, H, F, 1, 1, out=out, seed=14)
+    for k in ("x", "w_gate", "w_up", "w_down"):
+        d[k].zero_()
+    d["x"][:, 0] = 1.0
+    d["w_gate"][0, 0, 0] = d["w_up"][0, 0, 0] = 1e25
+    d["w_down"][0, 3, 0] = 1.0
+    call(p, d, epi, o, ws)
+    assert bool((o[:, 3] == float("inf")).all())
+    # (in a call of its own: every other column is 0 times that infinity)
+    a, b = 127 / 64 * 2.0 ** 63, 129 / 128 * 2.0 ** 64  # both bf16 values
+    assert torch.finfo(torch.bfloat16).max * (1 + 2.0 ** -9) < a * b < torch.finfo(torch.float32).max
+    d["w_gate"][0, 0, 0], d["w_up"][0, 0, 0] = a, b
+    d["w_down"][0, 3, 0] = 2.0 ** -100
+    call(p, d, epi, o, ws)
+    err = (o[:, 3].double() / (a * b * 2.0 ** -100) - 1).abs().max()
+    # f32 roundings; with a bf16 output two planes, the first cut off (2^-7) instead of rounded, and the cast
+    assert float(err) <= 8 * ref.U + (2.0 ** -7 * ref.BF16 + ref.BF16 if out == "bf16" else 0), float(err)
+
+
 @pytest.mark.parametrize("M", [1, 6, 40])
 def test_same_bits_on_every_call(M):
     p, d, epi, out, ws, _ = make(M=M, H=512, F=704, E=16, k=4, out="bf16", residual=True, seed=11)

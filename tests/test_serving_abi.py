@@ -102,7 +102,8 @@ def test_decode_workspace_covers_the_intermediates(lib):
 @pytest.mark.parametrize("kw,err", [(dict(M=-1), INV), (dict(H=32), INV), (dict(H=100), INV), (dict(H=1 << 17), INV),
                                     (dict(N=0), INV), (dict(N=65537), INV), (dict(rank=0), INV), (dict(rank=12), INV),
                                     (dict(rank=264), INV), (dict(num_adapters=-1), INV),
-                                    (dict(num_adapters=65537), INV), (dict(M=1 << 31), UNS),
+                                    (dict(num_adapters=65537), INV), (dict(M=1 << 27), UNS),
+                                    (dict(M=1 << 62), UNS), (dict(M=1 << 25, N=1 << 15), UNS),
                                     (dict(dtype="bf16_mxfp8"), UNS)])
 def test_adapter_refuses_bad_problems(lib, kw, err):
     q = moe.adapter_problem(**dict(dict(M=4, H=64, N=8, rank=8, num_adapters=2), **kw))
