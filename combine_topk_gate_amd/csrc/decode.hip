@@ -294,6 +294,8 @@ __global__ __launch_bounds__(64 * WAVES) void decode_l1_kernel(DecodeArgs a) {
   const int4 ent = a.plan.entries[blockIdx.y];
   if (MAXNT > 1 && ent.z <= 8 * MAXNT)
     decode_l1_tile<Op, WAVES, NW, (MAXNT > 1 ? MAXNT / 2 : 1), MX>(a, ent, lds);
+  else if (MAXNT == 8 && ent.z <= 96)
+    decode_l1_tile<Op, WAVES, NW, (MAXNT == 8 ? 6 : MAXNT), MX>(a, ent, lds);
   else
     decode_l1_tile<Op, WAVES, NW, MAXNT, MX>(a, ent, lds);
 }

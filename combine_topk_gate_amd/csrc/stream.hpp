@@ -398,7 +398,7 @@ __device__ __forceinline__ void stream_wide(const StreamArgs& a, RowOff row_off,
         for (int g = 0; g < NW; ++g)
           w[g] = *reinterpret_cast<const i32x4_t*>(ldw + (16 * g + r) * 128 + (((4 * h + q) ^ swz_w(r)) << 4));
         // up to 4 groups of 16 token rows at a time, so that their fragments fit
-        constexpr int NS = NT > 4 ? 4 : NT;
+        constexpr int NS = NT == 6 ? 3 : NT > 4 ? 4 : NT;
 #pragma unroll
         for (int j0 = 0; j0 < NT; j0 += NS) {
           i32x4_t x[NS][Op::kXH * Op::kP];
