@@ -60,7 +60,7 @@ __global__ __launch_bounds__(64 * WAVES) void adapter_shrink_kernel(AdapterArgs 
       if (__shfl(id, i) != mine || j >= a.r) return;  // r is a multiple of 8
 #pragma unroll
       for (int c = 0; c < 4; ++c) v[c] *= sc;
-      if (a.planes == 0) {
+      if (a.planes == 1) {  // f32
         *reinterpret_cast<f32x4_t*>(reinterpret_cast<float*>(a.t) + (m0 + i) * a.r + j) = v;
         return;
       }
@@ -80,43 +80,81 @@ __global__ __launch_bounds__(64 * WAVES) void adapter_shrink_kernel(AdapterArgs 
 }
 
 // ------------------------------------------------------------- projection ---
-template <class T>
-__device__ __forceinline__ float to_f32(T v) {
-  return (float)v;
-}
-
-// acc[c] += t . B[id, n + c] for the columns that exist, in increasing rank.
-// The loads of 32 (f32: 16) ranks are issued together: one at a time, each
-// waits for the L2.
-template <class T>
-__device__ __forceinline__ void add_adapter(const AdapterArgs& a, int64_t m, int id, int n, f32x4_t& acc) {
-  constexpr int V = 16 / sizeof(T), U = 4;  // elements per vector (r is a multiple of 8); vectors in flight
-  typedef T vec_t __attribute__((ext_vector_type(V)));
-  typedef float tvec_t __attribute__((ext_vector_type(V)));
-  const float* t = reinterpret_cast<const float*>(a.t) + m * a.r;
-  const T* b = reinterpret_cast<const T*>(a.b) + ((int64_t)id * a.N + n) * a.r;
-  int64_t col[4];  // (past the last column it is read again, not used)
-#pragma unroll
-  for (int c = 0; c < 4; ++c) col[c] = (int64_t)min(c, a.N - n - 1) * a.r;
-  for (int j0 = 0; j0 < a.r; j0 += U * V) {
-    tvec_t tv[U];
-    vec_t bv[U][4];
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int j = min(j0 + u * V, a.r - V);
-      tv[u] = *reinterpret_cast<const tvec_t*>(t + j);
-#pragma unroll
-      for (int c = 0; c < 4; ++c) bv[u][c] = *reinterpret_cast<const vec_t*>(b + col[c] + j);
+// acc += t . B for the adapters among the tile's rows, on the matrix cores: a
+// unit is 16 bytes of a lane's B row (32 ranks, f32: 16) of one adapter; unit
+// i of adapter a is wave a + i's, whatever else the tile holds, so a row's sum
+// does not depend on the other rows (the waves' accumulators are added later).
+// A row of another adapter holds zeros, which only cancel finite values: a
+// non-finite element of B is left out, and the result says so (add_nonfinite).
+// row_id: adapter of row m0 + lane.  (Each thread taking the ranks of its own
+// outputs in the epilogue: 78 instead of 41 us at 1000 x 4096 x 2048, rank
+// 128; 13.5 instead of 12.2 at 333 x 2048 x 1408, rank 32; but 12 instead of 13.2
+// where 48 rows have 48 adapters of rank 16.)
+template <class Op, class T, int WAVES, int NW, int NT>
+__device__ __forceinline__ bool add_adapters(const AdapterArgs& a, int64_t m0, int rows, int n0, int row_id,
+                                             f32x4_t (&acc)[NW][NT]) {
+  constexpr int V = 16 / sizeof(T), K = 4 * V;  // elements of a lane, of a unit
+  const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6), r = lane & 15;
+  const int cols = min(16 * NW, a.N - n0), planes = a.planes, pitch = planes * a.r;
+  const __amdgpu_buffer_rsrc_t rt = make_rsrc(reinterpret_cast<const T*>(a.t) + m0 * pitch, (uint32_t)(rows * pitch) * sizeof(T));
+  bool left_out = false;
+  uint64_t left = __ballot(lane < rows && (uint32_t)row_id < (uint32_t)a.P &&
+                           ((wave - row_id) & (WAVES - 1)) * K < a.r);  // rows of adapters with a unit of this wave
+  int id = 0, k0 = a.r;
+  auto next = [&]() {  // this wave's next unit: adapter id, ranks k0 ..
+    k0 += WAVES * K;
+    while (k0 >= a.r) {
+      if (!left) return false;
+      id = __builtin_amdgcn_readlane(row_id, __ffsll((unsigned long long)left) - 1);
+      left &= ~__ballot(row_id == id);
+      k0 = ((wave - id) & (WAVES - 1)) * K;
     }
+    return true;
+  };
+  struct Unit {
+    i32x4_t w[NW], x[NT][3];
+  };
+  auto load = [&](Unit& u) {
+    const __amdgpu_buffer_rsrc_t rb = make_rsrc(reinterpret_cast<const T*>(a.b) + ((int64_t)id * a.N + n0) * a.r,
+                                                (uint32_t)(cols * a.r) * sizeof(T));
+    const int k = k0 + V * (lane >> 4);
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      if (j0 + u * V >= a.r) break;
+    for (int g = 0; g < NW; ++g)
+      u.w[g] = buf_load16(rb, k < a.r ? (uint32_t)((16 * g + r) * a.r + k) * sizeof(T) : kNoRow, 0);
 #pragma unroll
-      for (int c = 0; c < 4; ++c)
+    for (int j = 0; j < NT; ++j) {
+      const bool mine = __shfl(row_id, 16 * j + r) == id && k < a.r;
 #pragma unroll
-        for (int v = 0; v < V; ++v) acc[c] = fmaf(tv[u][v], to_f32(bv[u][c][v]), acc[c]);
+      for (int p = 0; p < 3; ++p)
+        u.x[j][p] = buf_load16(rt, mine && p < planes ? (uint32_t)((16 * j + r) * pitch + p * a.r + k) * sizeof(T) : kNoRow, 0);
     }
+  };
+  auto multiply = [&](Unit& u) {
+#pragma unroll
+    for (int g = 0; g < NW; ++g) left_out |= drop_nonfinite<T>(u.w[g]);
+#pragma unroll
+    for (int p = 0; p < 3; ++p) {
+      if (p >= planes) break;
+      i32x4_t x[NT][1];
+#pragma unroll
+      for (int j = 0; j < NT; ++j) x[j][0] = u.x[j][p];
+#pragma unroll
+      for (int g = 0; g < NW; ++g) Op::template mma<NT>(acc[g], u.w[g], 0.0f, x);
+    }
+  };
+  Unit u0, u1;  // the next unit's loads are under way during a unit's products
+  bool more = next();
+  if (more) load(u0);
+  while (more) {
+    more = next();
+    if (more) load(u1);
+    multiply(u0);
+    if (!more) break;
+    more = next();
+    if (more) load(u0);
+    multiply(u1);
   }
+  return __any(left_out);
 }
 
 // 16 NW columns of 16 NT rows: the weight rows stream past the token rows
@@ -126,6 +164,7 @@ __global__ __launch_bounds__(64 * WAVES) void adapter_stream_kernel(AdapterArgs 
   constexpr int G = NW * NT * WAVES <= 64 ? NW : NW * NT * WAVES <= 128 && NW % 2 == 0 ? NW / 2 : 1;
   constexpr int kLds = WAVES * imax(stream_line_bytes<Op, NW, NT>(), G * NT * 1024);
   __shared__ __attribute__((aligned(16))) char lds[kLds];
+  __shared__ int left_out[WAVES];
   // the row blocks of one weight block run next to each other on one XCD (whose
   // workgroups come 8 apart), so its L2 reads the weights once
   const int64_t v0 = xcd_tile((int64_t)mb * nb);
@@ -146,13 +185,22 @@ __global__ __launch_bounds__(64 * WAVES) void adapter_stream_kernel(AdapterArgs 
   f32x4_t acc[NW][NT];
   stream_tile<Op, WAVES, NW, false, NT, 2, false>(s, [&](int m) { return (uint32_t)min(m, rows - 1) * a.row_bytes; },
                                         lds + uniform(threadIdx.x >> 6) * stream_line_bytes<Op, NW, NT>(), acc);
+  if (a.P > 0) {
+    const bool bad = add_adapters<Op, T, WAVES, NW, NT>(a, m0, rows, n0, row_id, acc);
+    if (lane == 0) left_out[threadIdx.x >> 6] = bad;
+  }
   stream_reduce<WAVES, NW, NT, G, 1>(acc, reinterpret_cast<f32x4_t*>(lds), [&](int g, int j, const f32x4_t (&sum)[1]) {
     f32x4_t v = sum[0];
     const int i = 16 * j + (lane & 15);
     const int n = n0 + 16 * g + 4 * (lane >> 4);
     const int id = __shfl(row_id, i);
     if (i >= rows || n >= a.N) return;
-    if ((uint32_t)id < (uint32_t)a.P) add_adapter<T>(a, m0 + i, id, n, v);
+    if (a.P > 0) {
+      bool bad = false;
+#pragma unroll
+      for (int w = 0; w < WAVES; ++w) bad |= left_out[w] != 0;
+      if (bad && (uint32_t)id < (uint32_t)a.P) add_nonfinite<T>(a, m0 + i, id, n, v);
+    }
     adapter_store(a, m0 + i, n, v);
   });
 }
@@ -228,28 +276,24 @@ static void launch_stream(const AdapterArgs& a, const StreamCost& c, hipStream_t
     launch_stream_as<Op, T, 8, 1, 1>(a, s);
 }
 
-hipError_t launch_adapter_linear(AdapterArgs a, bool f32, hipStream_t s) {
+hipError_t launch_adapter_linear(const AdapterArgs& a, bool f32, hipStream_t s) {
   if (a.M == 0) return hipSuccess;
   const float g128 = tile_cost(a, 128, 256, 57.0f), g256 = tile_cost(a, 256, 256, 105.0f);
   const StreamCost sc = f32 ? stream_cost(a, 77.0f, 21.0f, 7.0f) : stream_cost(a, 17.5f, 7.0f, 4.0f);
-  auto shrink = [&](int planes) {
-    a.planes = planes;
-    if (a.P == 0) return hipSuccess;
+  if (a.P > 0) {
     if (f32)
       launch_shrink<StreamF32>(a, s);
     else
       launch_shrink<StreamBf16<1>>(a, s);
-    return hipGetLastError();
-  };
-  hipError_t e;
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
   if (f32 || a.H < 128 || sc.least() <= fminf(g128, g256)) {
-    if ((e = shrink(0)) != hipSuccess) return e;
     if (f32)
       launch_stream<StreamF32, float>(a, sc, s);
     else
       launch_stream<StreamBf16<1>, __bf16>(a, sc, s);
   } else {
-    if ((e = shrink(a.out.out_bf16 ? 2 : 3)) != hipSuccess) return e;
     const int64_t rows = g256 < g128 ? 256 : 128, mt = (a.M + rows - 1) / rows, nt = (a.N + 255) / 256;
     const dim3 grid = tile_grid(mt * nt);
     if (g256 < g128)

@@ -107,19 +107,40 @@ __device__ __forceinline__ void list_adapters(const AdapterArgs& p, int64_t m0, 
   __syncthreads();
 }
 
-__device__ __forceinline__ bool bf16_nonfinite(uint32_t bits) { return (bits & 0x7F80u) == 0x7F80u; }
+// Non-finite elements among 32 bits of B (f32, or two bf16), as a mask of
+// their bits.
+template <class T>
+__device__ __forceinline__ uint32_t nonfinite_bits(uint32_t d) {
+  if (sizeof(T) == 4) return (d & 0x7F800000u) == 0x7F800000u ? ~0u : 0u;
+  return ((d & 0x7F80u) == 0x7F80u ? 0xFFFFu : 0u) | ((d & 0x7F800000u) == 0x7F800000u ? 0xFFFF0000u : 0u);
+}
 
-// The elements of B that the tile left out, for 4 columns of a row.
-__device__ __forceinline__ void add_nonfinite(const AdapterArgs& p, int planes, int64_t m, int id, int n, f32x4_t& acc) {
-  const uint16_t* b = reinterpret_cast<const uint16_t*>(p.b) + ((int64_t)id * p.N + n) * p.r;
-  const __bf16* t = reinterpret_cast<const __bf16*>(p.t) + m * planes * p.r;
+// Sets the non-finite elements of 16 bytes of B to zero; whether there were any.
+template <class T>
+__device__ __forceinline__ bool drop_nonfinite(i32x4_t& v) {
+  uint32_t bad[4], any = 0;
+#pragma unroll
+  for (int e = 0; e < 4; ++e) any |= bad[e] = nonfinite_bits<T>((uint32_t)v[e]);
+  if (any) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) v[e] = (int)((uint32_t)v[e] & ~bad[e]);
+  }
+  return any != 0;
+}
+
+// The elements of B that a tile left out, for 4 columns of row m (its t, in
+// p.planes parts).
+template <class T>
+__device__ __forceinline__ void add_nonfinite(const AdapterArgs& p, int64_t m, int id, int n, f32x4_t& acc) {
+  const T* b = reinterpret_cast<const T*>(p.b) + ((int64_t)id * p.N + n) * p.r;
+  const T* t = reinterpret_cast<const T*>(p.t) + m * p.planes * p.r;
   for (int c = 0; c < 4 && n + c < p.N; ++c)
     for (int j = 0; j < p.r; ++j) {
-      const uint32_t v = b[(int64_t)c * p.r + j];
-      if (!bf16_nonfinite(v)) continue;
+      const float v = (float)b[(int64_t)c * p.r + j];
+      if (__builtin_isfinite(v)) continue;
       float tv = 0.0f;
-      for (int q = planes - 1; q >= 0; --q) tv += (float)t[q * p.r + j];
-      acc[c] += tv * __builtin_bit_cast(float, v << 16);
+      for (int q = p.planes - 1; q >= 0; --q) tv += (float)t[q * p.r + j];
+      acc[c] += tv * v;
     }
 }
 
@@ -166,7 +187,7 @@ __device__ __forceinline__ void adapter_gemm_tile(const AdapterArgs& p, int64_t 
       *reinterpret_cast<i32x4_t*>(dst + kOperandBytes + (q * XQ + j - 2) * 4096) = xreg[q * XQ + j - 2];
   };
   // the extension's step s: slice s % slices of adapter list[s / slices]
-  const int planes = p.out.out_bf16 ? 2 : 3, kx = planes * p.r, slices = (kx + kBK - 1) / kBK;
+  const int kx = p.planes * p.r, slices = (kx + kBK - 1) / kBK;
   int ext = 0;  // its steps
   auto ext_step = [&](int s) {
     const int ai = s / slices, kk = (s - ai * slices) * kBK + 8 * lc;
@@ -183,23 +204,10 @@ __device__ __forceinline__ void adapter_gemm_tile(const AdapterArgs& p, int64_t 
 #pragma unroll
     for (int i = 0; i < XI; ++i) xdead |= (tl.id[lr + 32 * i] != id ? 1u : 0u) << i;
   };
-  auto drop_nonfinite = [&]() {
+  auto drop_step = [&]() {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      i32x4_t v = wreg[i];
-      bool bad = false;
-#pragma unroll
-      for (int e = 0; e < 4; ++e) bad |= bf16_nonfinite((uint32_t)v[e]) || bf16_nonfinite((uint32_t)v[e] >> 16);
-      if (bad) {
-        tl.nonfinite = 1;
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const uint32_t d = (uint32_t)v[e];
-          v[e] = (int)((bf16_nonfinite(d) ? 0u : d & 0xFFFFu) | (bf16_nonfinite(d >> 16) ? 0u : d & 0xFFFF0000u));
-        }
-        wreg[i] = v;
-      }
-    }
+    for (int i = 0; i < 8; ++i)
+      if (drop_nonfinite<__bf16>(wreg[i])) tl.nonfinite = 1;
   };
 
   // fragments
@@ -276,7 +284,7 @@ __device__ __forceinline__ void adapter_gemm_tile(const AdapterArgs& p, int64_t 
     if (kt + 2 >= nk && ext > 0) {
       soff = 0;
       if (kt + 2 < steps) ext_step(kt + 2 - nk);
-      if (kt + 1 >= nk) drop_nonfinite();
+      if (kt + 1 >= nk) drop_step();
     }
     auto load_one = [&](int q, int j) { gload_one(soff, q, j); };
 #pragma unroll
@@ -426,7 +434,7 @@ __device__ __forceinline__ void adapter_gemm_tile(const AdapterArgs& p, int64_t 
         f32x4_t v = staged(i);
         const int row = tile_row(i);
         if (row >= rows || n >= p.N) continue;
-        if (fixup && tl.id[row] >= 0) add_nonfinite(p, planes, m0 + row, tl.id[row], n, v);
+        if (fixup && tl.id[row] >= 0) add_nonfinite<__bf16>(p, m0 + row, tl.id[row], n, v);
         adapter_store(p, m0 + row, n, v);
       }
     }

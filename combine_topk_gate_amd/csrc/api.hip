@@ -696,7 +696,7 @@ moe_status_t moe_adapter_linear(const moe_adapter_problem_t* q, const void* x, c
   g.scale = scale;
   g.idx = adapter_idx;
   g.t = need > 0 ? ws : nullptr;
-  g.planes = 0;  // set by the launcher
+  g.planes = f32 ? 1 : g.out.out_bf16 ? 2 : 3;
   g.row_bytes = (uint32_t)(g.H * eb);
   return hip_status(launch_adapter_linear(g, f32, (hipStream_t)stream));
 }
