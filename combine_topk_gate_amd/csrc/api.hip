@@ -236,22 +236,25 @@ int decode_planes(const moe_problem_t* p, const OutEpilogue& ep) {
 }
 
 struct DecodeWs {
-  size_t hdr, entries, list, f2s, w, arrived, hact, y, total;
+  size_t entries, list, f2s, w, arrived, hact, y, total;
 };
 
+DecodeSplit split_of(const moe_problem_t* p) {
+  return decode_split((int)p->num_tokens, p->topk, p->num_experts, held(p), p->hidden, p->ffn, p->dtype);
+}
+
 // The workspace does not depend on the output's type (three planes).
-DecodeWs decode_ws(const moe_problem_t* p) {
+DecodeWs decode_ws(const moe_problem_t* p, const DecodeSplit& split) {
   const int M = (int)p->num_tokens, R = M * p->topk;
   DecodeWs w;
   size_t o = 0;
-  w.hdr = o; o += align_up(16);
-  w.entries = o; o += align_up(decode_entry_bytes(M, p->topk, p->num_experts, held(p), is_mx(p)));
+  w.entries = o; o += align_up(decode_entry_bytes(decode_max_entries(M, p->topk, held(p), split.nt)));
   w.list = o; o += align_up((size_t)R * 4);
   w.f2s = o; o += align_up((size_t)R * 4);
   w.w = o; o += align_up((size_t)R * 4);
   w.arrived = o; o += align_up((size_t)p->hidden / 16 * 4);
   w.hact = o; o += align_up((size_t)R * p->ffn * (p->dtype == MOE_DTYPE_F32 ? 4 : 6));
-  w.y = o; o += align_up((size_t)R * p->hidden * 4 * decode_parts(M, p->topk, p->num_experts, is_mx(p)));
+  w.y = o; o += align_up((size_t)R * p->hidden * 4 * split.parts);
   w.total = o;
   return w;
 }
@@ -324,7 +327,7 @@ size_t moe_workspace_bytes(const moe_problem_t* p, int32_t op) {
     case MOE_OP_DISPATCH: return permute_ws_bytes(plan_of(p));
     case MOE_OP_GROUPED_GEMM: return p->dtype == MOE_DTYPE_BF16 ? gemm_split_ws_bytes() : 0;
     case MOE_OP_LAYER: return layer_ws(p).total;
-    case MOE_OP_LAYER_DECODE: return check_decode(p) == MOE_OK ? decode_ws(p).total : 0;
+    case MOE_OP_LAYER_DECODE: return check_decode(p) == MOE_OK ? decode_ws(p, split_of(p)).total : 0;
   }
   return 0;
 }
@@ -603,7 +606,8 @@ moe_status_t moe_layer_decode(const moe_problem_t* p, const void* x, const float
   if (!x || !logits || !out) return MOE_ERR_INVALID_ARGUMENT;
   if (!aligned(x, 16) || !aligned(logits, 4)) return MOE_ERR_INVALID_ARGUMENT;
   const int64_t n = p->num_tokens * p->hidden;
-  const DecodeWs L = decode_ws(p);
+  const DecodeSplit split = split_of(p);
+  const DecodeWs L = decode_ws(p, split);
   if (!ws || ws_bytes < L.total) return MOE_ERR_WORKSPACE_TOO_SMALL;
   if (!aligned(ws, kAlign)) return MOE_ERR_INVALID_ARGUMENT;
   const size_t nout = (size_t)n * (ep.out_bf16 ? 2 : 4);
@@ -626,8 +630,9 @@ moe_status_t moe_layer_decode(const moe_problem_t* p, const void* x, const float
   a.plan.E = p->num_experts;
   a.plan.EL = held(p);
   a.plan.base = held_base(p);
-  a.plan.rows = decode_entry_rows(a.plan.M, a.plan.k, a.plan.E, mx);
-  a.plan.hdr = at<int32_t>(ws, L.hdr);
+  a.plan.rows = 16 * split.nt;
+  a.split = split;
+  a.plan.max_entries = decode_max_entries(a.plan.M, a.plan.k, a.plan.EL, split.nt);
   a.plan.entries = at<int4>(ws, L.entries);
   a.plan.list = at<int32_t>(ws, L.list);
   a.plan.f2s = at<int32_t>(ws, L.f2s);

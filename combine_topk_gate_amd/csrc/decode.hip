@@ -74,7 +74,7 @@ __global__ __launch_bounds__(256) void decode_route_kernel(const float* __restri
 }
 
 // One workgroup: per held expert the list of its pairs f = t k + j, cut into
-// entries of at most `rows` rows.  (Which place of an expert's list a pair
+// entries of at most `rows` rows; entries past the last have none.  (Which place of an expert's list a pair
 // gets is decided by an LDS atomic; a row's result does not depend on its
 // place.)  KMAX 0: the route kernel has left the pairs' experts in list;
 // otherwise the tokens are routed here.
@@ -129,7 +129,7 @@ __global__ __launch_bounds__(kPlanThreads) void decode_plan_kernel(const float* 
       p.entries[entry + b] = v;
     }
   }
-  if (tid == 0) p.hdr[0] = scan[p.EL - 1] >> 16;
+  for (int i = (scan[p.EL - 1] >> 16) + tid; i < p.max_entries; i += kPlanThreads) p.entries[i] = int4{0, 0, 0, 0};
   __syncthreads();
   for (int f = tid; f < p.M * p.k; f += kPlanThreads)
     if (slot[f] >= 0) p.list[atomicAdd(&cur[slot[f]], 1)] = f;
@@ -168,42 +168,42 @@ __device__ __forceinline__ void store_h(const DecodeArgs& a, int64_t pair, int c
   }
 }
 
-// Layer0 of one entry: 16 NF columns of h for its rows.  NP: bf16 planes of
-// h (0: f32).
-template <class Op, int NF, int NT, int NP>
+// Layer0 of one entry: 16 columns of h for its rows.  NP: bf16 planes of h
+// (0: f32).
+template <class Op, int NT, int NP>
 __device__ __forceinline__ void decode_l0_tile(const DecodeArgs& a, int4 ent, char* lds) {
-  const int f0 = blockIdx.x * 16 * NF;
+  const int f0 = blockIdx.x * 16;
   StreamArgs s{};
   s.row_bytes = a.x_pitch;  // a gate or up row is as long as a row of x, in the same type
   const int64_t at = ((int64_t)ent.x * a.F + f0) * (int64_t)s.row_bytes;
   s.w0 = reinterpret_cast<const char*>(a.w_gate) + at;
   s.w1 = reinterpret_cast<const char*>(a.w_up) + at;
-  s.w_rows = 16 * NF;
+  s.w_rows = 16;
   s.x = a.x;
   s.x_bytes = (uint32_t)a.plan.M * a.x_pitch;
   s.lines = a.H / Op::kLine;
-  f32x4_t acc[2 * NF][NT];
+  f32x4_t acc[2][NT];
   const int wave = uniform(threadIdx.x >> 6);
-  stream_tile<Op, kStreamWaves, 2 * NF, true, NT, 4, true>(
+  stream_tile<Op, kStreamWaves, 2, true, NT, 4, true>(
       s, [&](int i) { return decode_row(a.plan, ent, i, a.plan.k, a.x_pitch); },
-      lds + wave * stream_line_bytes<Op, 2 * NF, NT>(), acc);
+      lds + wave * stream_line_bytes<Op, 2, NT>(), acc);
   const int lane = threadIdx.x & 63;
-  stream_reduce<kStreamWaves, 2 * NF, NT, 2, 2>(acc, reinterpret_cast<f32x4_t*>(lds), [&](int grp, int j, const f32x4_t (&gu)[2]) {
+  stream_reduce<kStreamWaves, 2, NT, 2, 2>(acc, reinterpret_cast<f32x4_t*>(lds), [&](int, int j, const f32x4_t (&gu)[2]) {
     const int i = 16 * j + (lane & 15);
     if (i >= ent.z) return;
-    store_h<NP>(a, a.plan.list[ent.y + i], f0 + 8 * grp + 4 * (lane >> 4), gu[0], gu[1]);
+    store_h<NP>(a, a.plan.list[ent.y + i], f0 + 4 * (lane >> 4), gu[0], gu[1]);
   });
 }
 
-template <class Op, int NF, int MAXNT, int NP>
+template <class Op, int MAXNT, int NP>
 __global__ __launch_bounds__(kStreamThreads) void decode_l0_kernel(DecodeArgs a) {
-  __shared__ __attribute__((aligned(16))) char lds[product_lds<Op, 2 * NF, MAXNT, 2>()];
-  if ((int)blockIdx.y >= a.plan.hdr[0]) return;
+  __shared__ __attribute__((aligned(16))) char lds[product_lds<Op, 2, MAXNT, 2>()];
   const int4 ent = a.plan.entries[blockIdx.y];
+  if (ent.z == 0) return;
   if (MAXNT == 1 || ent.z <= 16)
-    decode_l0_tile<Op, NF, 1, NP>(a, ent, lds);
-  else if (ent.z <= 32)
-    decode_l0_tile<Op, NF, MAXNT, NP>(a, ent, lds);
+    decode_l0_tile<Op, 1, NP>(a, ent, lds);
+  else
+    decode_l0_tile<Op, MAXNT, NP>(a, ent, lds);
 }
 
 // Layer0 where experts get many rows (entries of 64 or 128): the waves split
@@ -236,8 +236,8 @@ __device__ __forceinline__ void decode_l0_wide_tile(const DecodeArgs& a, int4 en
 template <class Op, int MAXNT, int NP>
 __global__ __launch_bounds__(64 * kWideL0) void decode_l0_wide_kernel(DecodeArgs a) {
   __shared__ __attribute__((aligned(16))) char lds[stream_wide_bytes<Op, kWideL0, 2, MAXNT>()];
-  if ((int)blockIdx.y >= a.plan.hdr[0]) return;
   const int4 ent = a.plan.entries[blockIdx.y];
+  if (ent.z == 0) return;
   if (ent.z <= 8 * MAXNT)
     decode_l0_wide_tile<Op, MAXNT / 2, NP>(a, ent, lds);
   else
@@ -290,8 +290,8 @@ __device__ __forceinline__ void decode_l1_tile(const DecodeArgs& a, int4 ent, ch
 template <class Op, int WAVES, int NW, int MAXNT, bool MX>
 __global__ __launch_bounds__(64 * WAVES) void decode_l1_kernel(DecodeArgs a) {
   __shared__ __attribute__((aligned(16))) char lds[stream_wide_bytes<Op, WAVES, NW, MAXNT>()];
-  if ((int)blockIdx.y >= a.plan.hdr[0]) return;
   const int4 ent = a.plan.entries[blockIdx.y];
+  if (ent.z == 0) return;
   if (MAXNT > 1 && ent.z <= 8 * MAXNT)
     decode_l1_tile<Op, WAVES, NW, (MAXNT > 1 ? MAXNT / 2 : 1), MX>(a, ent, lds);
   else if (MAXNT == 8 && ent.z <= 96)
@@ -301,37 +301,39 @@ __global__ __launch_bounds__(64 * WAVES) void decode_l1_kernel(DecodeArgs a) {
 }
 
 // out[t, n .. n + 3] a thread: the pairs in slot order, each the sum of its
-// parts in order.
-__global__ __launch_bounds__(256) void decode_combine_kernel(DecodeArgs a, int parts, OutEpilogue ep) {
+// PARTS parts in order; the loads of up to 16 of them are under way together.
+template <int PARTS>
+__global__ __launch_bounds__(256) void decode_combine_kernel(DecodeArgs a, OutEpilogue ep) {
+  constexpr int U = PARTS > 4 ? 16 / PARTS : 4;
   const DecodePlan& p = a.plan;
   const int64_t i = 4 * ((int64_t)blockIdx.x * 256 + threadIdx.x);
   if (i >= (int64_t)p.M * a.H) return;
   const int t = (int)(i / a.H), n = (int)(i - (int64_t)t * a.H);
   const int64_t part = (int64_t)p.M * p.k * a.H;
   float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-  // 4 slots' loads in flight
-  for (int f0 = t * p.k; f0 < (t + 1) * p.k; f0 += 4) {
-    f32x4_t y[4];
-    float w[4];
-    bool has[4];
+  for (int f0 = t * p.k; f0 < (t + 1) * p.k; f0 += U) {
+    f32x4_t y[U][PARTS];
+    float w[U];
+    bool has[U];
 #pragma unroll
-    for (int u = 0; u < 4; ++u) {
+    for (int u = 0; u < U; ++u) {
       const int f = min(f0 + u, (t + 1) * p.k - 1);
       has[u] = f0 + u < (t + 1) * p.k && p.f2s[f] >= 0;
       w[u] = p.w[f];
       const float* at = a.y + (int64_t)f * a.H + n;
-      y[u] = f32x4_t{0.f, 0.f, 0.f, 0.f};
       if (!has[u]) continue;
-      y[u] = *reinterpret_cast<const f32x4_t*>(at);
-      for (int s = 1; s < parts; ++s) y[u] += *reinterpret_cast<const f32x4_t*>(at + s * part);
+#pragma unroll
+      for (int s = 0; s < PARTS; ++s) y[u][s] = *reinterpret_cast<const f32x4_t*>(at + s * part);
     }
 #pragma unroll
-    for (int u = 0; u < 4; ++u) {
+    for (int u = 0; u < U; ++u) {
       if (!has[u]) continue;
-      o.x = fmaf(w[u], y[u][0], o.x);
-      o.y = fmaf(w[u], y[u][1], o.y);
-      o.z = fmaf(w[u], y[u][2], o.z);
-      o.w = fmaf(w[u], y[u][3], o.w);
+#pragma unroll
+      for (int s = 1; s < PARTS; ++s) y[u][0] += y[u][s];
+      o.x = fmaf(w[u], y[u][0][0], o.x);
+      o.y = fmaf(w[u], y[u][0][1], o.y);
+      o.z = fmaf(w[u], y[u][0][2], o.z);
+      o.w = fmaf(w[u], y[u][0][3], o.w);
     }
   }
   store_out(ep, i, o);
@@ -415,23 +417,25 @@ __global__ __launch_bounds__(kStreamThreads) void decode_few_l0_kernel(const flo
   __syncthreads();
   const int rows = uniform(ent.rows);
   if (rows == 0) return;
-  const int f0 = blockIdx.x * 16;
-  StreamArgs s{};
-  s.row_bytes = a.x_pitch;
-  const int64_t at = ((int64_t)uniform(ent.expert) * a.F + f0) * (int64_t)s.row_bytes;
-  s.w0 = reinterpret_cast<const char*>(a.w_gate) + at;
-  s.w1 = reinterpret_cast<const char*>(a.w_up) + at;
-  s.w_rows = 16;
-  s.x = a.x;
-  s.x_bytes = (uint32_t)p.M * a.x_pitch;
-  s.lines = a.H / Op::kLine;
-  f32x4_t acc[2][1];
-  stream_share<Op, 2, true, 1, 4, kFewRows, true>(
-      s, wave, kStreamWaves, [&](int i) { return i < rows ? (uint32_t)(ent.pair[i] / p.k) * a.x_pitch : kNoRow; }, lds + wave * kLine, acc);
-  stream_reduce<kStreamWaves, 2, 1, 2, 2>(acc, reinterpret_cast<f32x4_t*>(lds), [&](int, int, const f32x4_t (&gu)[2]) {
-    const int i = lane & 15;
-    if (i < rows) store_h<NP>(a, ent.pair[i], f0 + 4 * (lane >> 4), gu[0], gu[1]);
-  });
+  for (int f0 = blockIdx.x * 16; f0 < a.F; f0 += gridDim.x * 16) {
+    StreamArgs s{};
+    s.row_bytes = a.x_pitch;
+    const int64_t at = ((int64_t)uniform(ent.expert) * a.F + f0) * (int64_t)s.row_bytes;
+    s.w0 = reinterpret_cast<const char*>(a.w_gate) + at;
+    s.w1 = reinterpret_cast<const char*>(a.w_up) + at;
+    s.w_rows = 16;
+    s.x = a.x;
+    s.x_bytes = (uint32_t)p.M * a.x_pitch;
+    s.lines = a.H / Op::kLine;
+    f32x4_t acc[2][1];
+    stream_share<Op, 2, true, 1, 4, kFewRows, true>(
+        s, wave, kStreamWaves, [&](int i) { return i < rows ? (uint32_t)(ent.pair[i] / p.k) * a.x_pitch : kNoRow; }, lds + wave * kLine, acc);
+    stream_reduce<kStreamWaves, 2, 1, 2, 2>(acc, reinterpret_cast<f32x4_t*>(lds), [&](int, int, const f32x4_t (&gu)[2]) {
+      const int i = lane & 15;
+      if (i < rows) store_h<NP>(a, ent.pair[i], f0 + 4 * (lane >> 4), gu[0], gu[1]);
+    });
+    __syncthreads();  // the sums are read before the next columns' lines come
+  }
 }
 
 // 16 bytes of y between blocks: stored past the XCD's L2 and loaded past it
@@ -516,13 +520,19 @@ __global__ __launch_bounds__(kStreamThreads) void decode_few_l1_kernel(DecodeArg
 }
 
 // ---------------------------------------------------------------- launch ---
+constexpr int kCus = 256;
+
 template <class Op0, class Op1, int NP, bool MX>
 static void launch_few(const DecodeArgs& a, const float* logits, const OutEpilogue& ep, hipStream_t s) {
   const DecodePlan& p = a.plan;
   const int pairs = p.M * p.k;
   // one token's entries are its slots, held or not
   const int entries = p.M == 1 ? p.k : p.EL < pairs ? p.EL : pairs;
-  const dim3 grid((unsigned)(a.F / 16), (unsigned)entries);
+  // Layer0: as many blocks as are resident at once (7 on a CU), each taking
+  // the same number of column groups: more of them would only route again (8
+  // tokens, 22 experts of 448 x 4992: 51 us instead of 73)
+  const int groups = a.F / 16, at_once = 7 * kCus, turns = (groups * entries + at_once - 1) / at_once;
+  const dim3 grid((unsigned)((groups + turns - 1) / turns), (unsigned)entries);
   if (p.k <= 2)
     decode_few_l0_kernel<Op0, 2, NP><<<grid, kStreamThreads, 0, s>>>(logits, a);
   else if (p.k <= 4)
@@ -543,53 +553,68 @@ static void launch_few(const DecodeArgs& a, const float* logits, const OutEpilog
 // 345 with 64; 50 rows each, where every expert takes two entries of 32, 540
 // and 345.)
 // MXFP8's token lines are twice as long: 128 rows do not fit the LDS.
-static int decode_max_nt(int M, int k, int E, bool mx) {
-  return M <= 16 ? 1 : M <= 32 || M * k <= 24 * E ? 2 : mx || M <= 64 || M * k <= 40 * E ? 4 : 8;
-}
-
-int decode_entry_rows(int M, int k, int E, bool mx) { return 16 * decode_max_nt(M, k, E, mx); }
-
-int decode_parts(int M, int k, int E, bool mx) { return decode_max_nt(M, k, E, mx) >= 4 ? 2 : 1; }
-
-static int decode_max_entries(int M, int k, int E, int EL, bool mx) {
+// Where the wide Layer0 would leave most CUs idle (f32, which the matrix cores
+// bound: some), its entries stay at 32 rows (73 tokens, 4 experts of 2368 x
+// 448, f32: 20 us instead of 91; 144 tokens, 6 experts of 1856 x 640: 25
+// instead of 29; but 60 tokens, 6 experts of 512 x 2432: 20 instead of 11).
+// Layer1's reduction is cut into parts until every CU has a block (29 tokens, 4
+// experts of 960 x 10368, f32: 32 us instead of 217; 51 tokens, 3 experts of
+// that size, bf16: 16 instead of 67; until it has four: 200 tokens, 8 experts
+// of 4096 x 14336, 229 instead of 200).
+DecodeSplit decode_split(int M, int k, int E, int EL, int H, int F, int dtype) {
+  const bool mx = dtype == MOE_DTYPE_BF16_MXFP8, f32 = dtype == MOE_DTYPE_F32;
   const int R = M * k;
-  return (EL < R ? EL : R) + R / decode_entry_rows(M, k, E, mx);
+  const int64_t held = ((int64_t)R * EL + E - 1) / E;  // of the pairs, about
+  const int experts = held < 1 ? 1 : (int)(held < EL ? held : EL);
+  DecodeSplit d;
+  d.nt = M <= 16 ? 1 : M <= 32 || R <= 24 * E ? 2 : mx || M <= 64 || R <= 40 * E ? 4 : 8;
+  if (d.nt > 2 && F / 64 * experts < (f32 ? kCus : kCus / 4)) d.nt = 2;
+  const int64_t rows = (held + experts - 1) / experts;
+  const int64_t entries = experts * ((rows + 16 * d.nt - 1) / (16 * d.nt));
+  const int64_t blocks = (H + 127) / 128 * entries / (d.nt > 2 && !mx ? 2 : 1);
+  const int lines = F / (mx ? 128 : f32 ? 32 : 64);
+  d.parts = d.nt > 2 ? 2 : 1;
+  while (d.parts < 8 && blocks * d.parts < kCus && lines >= 8 * d.parts) d.parts *= 2;
+  return d;
 }
 
-size_t decode_entry_bytes(int M, int k, int E, int EL, bool mx) {
-  const size_t many = sizeof(int4) * (size_t)decode_max_entries(M, k, E, EL, mx), few = sizeof(FewEntry) * kFewPairs;
+int decode_max_entries(int M, int k, int EL, int nt) {
+  const int R = M * k;
+  return (EL < R ? EL : R) + R / (16 * nt);
+}
+
+size_t decode_entry_bytes(int max_entries) {
+  const size_t many = sizeof(int4) * (size_t)max_entries, few = sizeof(FewEntry) * kFewPairs;
   return many > few ? many : few;
 }
 
-// Returns the parts of Layer1's reduction (1 or 2).
 template <class Op0, class Op1, int NP, bool MX>
-static int launch_products(const DecodeArgs& a, int entries, hipStream_t s) {
-  const int nt = decode_max_nt(a.plan.M, a.plan.k, a.plan.E, MX);
+static void launch_products(const DecodeArgs& a, hipStream_t s) {
+  const int entries = a.plan.max_entries;
   auto grid = [&](int n, int cols, int parts = 1) {
     return dim3((unsigned)((n + cols - 1) / cols), (unsigned)entries, (unsigned)parts);
   };
-  if (nt == 1) {
-    decode_l0_kernel<Op0, 1, 1, NP><<<grid(a.F, 16), kStreamThreads, 0, s>>>(a);
-    decode_l1_kernel<Op1, 4, 2, 1, MX><<<grid(a.H, 128), 256, 0, s>>>(a);
-    return 1;
-  }
-  if (nt == 2) {
-    decode_l0_kernel<Op0, 1, 2, NP><<<grid(a.F, 16), kStreamThreads, 0, s>>>(a);
-    decode_l1_kernel<Op1, 4, 2, 2, MX><<<grid(a.H, 128), 256, 0, s>>>(a);
-    return 1;
-  }
+  const int parts = a.split.parts;
   constexpr int NW1 = MX ? 1 : 2;  // (MXFP8's lines take the registers of the second group)
-  const dim3 g0 = grid(a.F, 16 * kWideL0), g1 = grid(a.H, 128 * NW1, 2);
-  if (nt == 4) {
-    decode_l0_wide_kernel<Op0, 4, NP><<<g0, 64 * kWideL0, 0, s>>>(a);
-    decode_l1_kernel<Op1, 8, NW1, 4, MX><<<g1, 512, 0, s>>>(a);
-  } else {
-    if constexpr (!MX) {
-      decode_l0_wide_kernel<Op0, 8, NP><<<g0, 64 * kWideL0, 0, s>>>(a);
-      decode_l1_kernel<Op1, 8, NW1, 8, MX><<<g1, 512, 0, s>>>(a);
-    }
+  switch (a.split.nt) {
+    case 1:
+      decode_l0_kernel<Op0, 1, NP><<<grid(a.F, 16), kStreamThreads, 0, s>>>(a);
+      decode_l1_kernel<Op1, 4, 2, 1, MX><<<grid(a.H, 128, parts), 256, 0, s>>>(a);
+      break;
+    case 2:
+      decode_l0_kernel<Op0, 2, NP><<<grid(a.F, 16), kStreamThreads, 0, s>>>(a);
+      decode_l1_kernel<Op1, 4, 2, 2, MX><<<grid(a.H, 128, parts), 256, 0, s>>>(a);
+      break;
+    case 4:
+      decode_l0_wide_kernel<Op0, 4, NP><<<grid(a.F, 16 * kWideL0), 64 * kWideL0, 0, s>>>(a);
+      decode_l1_kernel<Op1, 8, NW1, 4, MX><<<grid(a.H, 128 * NW1, parts), 512, 0, s>>>(a);
+      break;
+    default:
+      if constexpr (!MX) {
+        decode_l0_wide_kernel<Op0, 8, NP><<<grid(a.F, 16 * kWideL0), 64 * kWideL0, 0, s>>>(a);
+        decode_l1_kernel<Op1, 8, NW1, 8, MX><<<grid(a.H, 128 * NW1, parts), 512, 0, s>>>(a);
+      }
   }
-  return 2;  // = decode_parts()
 }
 
 template <int KMAX>
@@ -597,12 +622,14 @@ static void launch_plan(const float* logits, const DecodePlan& p, hipStream_t s)
   // routed by the plan's one workgroup (64 tokens at a time) where that takes
   // less than a launch: 4.5 us at 17 tokens, k = 2; at 64 tokens, k = 8, 15 us
   // against 4 + 4
-  if ((p.M + 63) / 64 * KMAX <= 4) {
-    decode_plan_kernel<KMAX><<<1, kPlanThreads, 0, s>>>(logits, p);
-  } else {
-    decode_route_kernel<KMAX><<<(p.M + 15) / 16, 256, 0, s>>>(logits, p);
-    decode_plan_kernel<0><<<1, kPlanThreads, 0, s>>>(nullptr, p);
+  if constexpr (KMAX <= 4) {
+    if ((p.M + 63) / 64 * KMAX <= 4) {
+      decode_plan_kernel<KMAX><<<1, kPlanThreads, 0, s>>>(logits, p);
+      return;
+    }
   }
+  decode_route_kernel<KMAX><<<(p.M + 15) / 16, 256, 0, s>>>(logits, p);
+  decode_plan_kernel<0><<<1, kPlanThreads, 0, s>>>(nullptr, p);
 }
 
 hipError_t launch_decode(const DecodeArgs& a, const float* logits, int dtype, int planes, const OutEpilogue& ep,
@@ -631,21 +658,25 @@ hipError_t launch_decode(const DecodeArgs& a, const float* logits, int dtype, in
     launch_plan<16>(logits, p, s);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  const int entries = decode_max_entries(p.M, p.k, p.E, p.EL, dtype == MOE_DTYPE_BF16_MXFP8);
-  int parts;
   if (dtype == MOE_DTYPE_F32)
-    parts = launch_products<StreamF32, StreamF32, 0, false>(a, entries, s);
+    launch_products<StreamF32, StreamF32, 0, false>(a, s);
   else if (dtype == MOE_DTYPE_BF16 && planes == 3)
-    parts = launch_products<StreamBf16<1>, StreamBf16<3>, 3, false>(a, entries, s);
+    launch_products<StreamBf16<1>, StreamBf16<3>, 3, false>(a, s);
   else if (dtype == MOE_DTYPE_BF16)
-    parts = launch_products<StreamBf16<1>, StreamBf16<2>, 2, false>(a, entries, s);
+    launch_products<StreamBf16<1>, StreamBf16<2>, 2, false>(a, s);
   else if (planes == 3)
-    parts = launch_products<StreamBf16<1>, StreamMx<3>, 3, true>(a, entries, s);
+    launch_products<StreamBf16<1>, StreamMx<3>, 3, true>(a, s);
   else
-    parts = launch_products<StreamBf16<1>, StreamMx<2>, 2, true>(a, entries, s);
+    launch_products<StreamBf16<1>, StreamMx<2>, 2, true>(a, s);
   e = hipGetLastError();
   if (e != hipSuccess) return e;
-  decode_combine_kernel<<<(unsigned)(((int64_t)p.M * a.H / 4 + 255) / 256), 256, 0, s>>>(a, parts, ep);
+  const unsigned blocks = (unsigned)(((int64_t)p.M * a.H / 4 + 255) / 256);
+  switch (a.split.parts) {
+    case 1: decode_combine_kernel<1><<<blocks, 256, 0, s>>>(a, ep); break;
+    case 2: decode_combine_kernel<2><<<blocks, 256, 0, s>>>(a, ep); break;
+    case 4: decode_combine_kernel<4><<<blocks, 256, 0, s>>>(a, ep); break;
+    default: decode_combine_kernel<8><<<blocks, 256, 0, s>>>(a, ep);
+  }
   return hipGetLastError();
 }
 

@@ -83,10 +83,15 @@ hipError_t launch_combine(const float* y, const float* topk_w, const int32_t* fl
                           int k, const OutEpilogue& ep, hipStream_t s);
 
 // Decode layer (at most MOE_DECODE_MAX_TOKENS tokens).
+struct DecodeSplit {
+  int nt;       // 16s of rows that an entry may hold: 1, 2, 4 or 8
+  int parts;    // of Layer1's reduction (y's in the workspace)
+};
+DecodeSplit decode_split(int M, int k, int E, int EL, int H, int F, int dtype);
 struct DecodePlan {
   int M, k, E, EL, base;
-  int rows;       // rows an entry may hold (decode_entry_rows)
-  int32_t* hdr;   // [0]: number of entries
+  int rows;       // rows an entry may hold (16 DecodeSplit::nt)
+  int max_entries;  // (the last ones may have no rows)
   int4* entries;  // {held expert, first place in list, rows, 0}
   int32_t* list;  // pairs f = t k + j, expert by expert
   int32_t* f2s;   // [M k] f, or -1 for a pair of no held expert
@@ -100,14 +105,14 @@ struct DecodeArgs {
   const void* w_down;
   const uint8_t* wd_scale;  // MXFP8: the scale bytes of W_down
   void* hact;               // [M k][planes][F] bf16, or [M k][F] f32
-  float* y;                 // [decode_parts][M k][H]
+  DecodeSplit split;
+  float* y;                 // [split.parts][M k][H]
   int32_t* arrived;         // [H / 16] Layer1 blocks done per 16 columns (few tokens)
   int H, F;
   uint32_t x_pitch, h_pitch, wd_pitch;  // bytes of a row of x (and of the gate and up weights), h, W_down
 };
-int decode_entry_rows(int M, int k, int E, bool mx);
-int decode_parts(int M, int k, int E, bool mx);  // y's in the workspace
-size_t decode_entry_bytes(int M, int k, int E, int EL, bool mx);  // of DecodePlan::entries
+int decode_max_entries(int M, int k, int EL, int nt);
+size_t decode_entry_bytes(int max_entries);  // of DecodePlan::entries
 hipError_t launch_decode(const DecodeArgs& a, const float* logits, int dtype, int planes, const OutEpilogue& ep,
                          hipStream_t s);
 
