@@ -85,7 +85,7 @@ __global__ __launch_bounds__(64 * WAVES) void adapter_shrink_kernel(AdapterArgs 
 // i of adapter a is wave a + i's, whatever else the tile holds, so a row's sum
 // does not depend on the other rows (the waves' accumulators are added later).
 // A row of another adapter holds zeros, which only cancel finite values: a
-// non-finite element of B is left out, and the result says so (add_nonfinite).
+// non-finite element of B is left out, and the result says so (nonfinite_part).
 // row_id: adapter of row m0 + lane.  (Each thread taking the ranks of its own
 // outputs in the epilogue: 78 instead of 41 us at 1000 x 4096 x 2048, rank
 // 128; 13.5 instead of 12.2 at 333 x 2048 x 1408, rank 32; but 12 instead of 13.2
@@ -199,7 +199,9 @@ __global__ __launch_bounds__(64 * WAVES) void adapter_stream_kernel(AdapterArgs 
       bool bad = false;
 #pragma unroll
       for (int w = 0; w < WAVES; ++w) bad |= left_out[w] != 0;
-      if (bad && (uint32_t)id < (uint32_t)a.P) add_nonfinite<T>(a, m0 + i, id, n, v);
+      if (bad && (uint32_t)id < (uint32_t)a.P) {
+        for (int c = 0; c < 4 && n + c < a.N; ++c) v[c] += nonfinite_part<T>(a, m0 + i, id, n + c);
+      }
     }
     adapter_store(a, m0 + i, n, v);
   });
@@ -245,32 +247,40 @@ static void launch_stream_as(const AdapterArgs& a, hipStream_t s) {
   adapter_stream_kernel<Op, T, WAVES, NW, NT><<<tile_grid((int64_t)mb * nb), 64 * WAVES, 0, s>>>(a, mb, nb);
 }
 
-// Which kernel: the tiles of each differ in how long a round of them (one
-// per CU) takes, and the rule takes the fewest rounds times that.  Measured
-// at H = 4096, in us a round: bf16 stream tiles of 64 x 64, 32 x 32 and 16 x
-// 16 outputs 17.5, 7 and 4; the matrix-core tiles of 128 x 256 and 256 x 256
-// 57 and 105 (they keep more of the operands in LDS, but one of them alone on
-// a CU waits longer for its loads).  E.g. 1024 x 4096 x 2048: 64 x 64 tiles 34
-// us, 128 x 256 tiles 55; 2048 x 4096 x 4096: 168 and 72.  f32 (the matrix
-// cores bound it): 77, 21 and 7.
-static float tile_cost(const AdapterArgs& a, int rows, int cols, float us) {
-  const float tiles = (float)((a.M + rows - 1) / rows) * (float)((a.N + cols - 1) / cols);
-  return ceilf(tiles / (float)device_cu_count()) * us;
-}
-
-struct StreamCost {
-  float c4, c2, c1;
-  float least() const { return fminf(c4, fminf(c2, c1)); }
+// Which kernel: each takes about start + rounds x (round + step H / 1024) us, a
+// round being one tile per CU; the rule takes the least.  Fitted to 256 tiles
+// at H = 256, 1024 and 4096 (two and four rounds at 1024 for the small ones),
+// in us: bf16 stream tiles of 64 x 64, 32 x 32, 16 x 16 outputs 6.6 9.4 19,
+// 4.8 5.7 10, 3.7 4.0 6.5; matrix-core tiles of 128 x 256 and 256 x 256 (they
+// keep more of the operands in LDS, but one of them alone on a CU waits longer
+// for its loads) 16 28 73, 28 46 123; f32 10 24 80, 6.4 9.8 23, 4.2 5.6 10.
+// Adapters lengthen the reduction by their planes: one adapter a stream tile, two
+// a matrix-core tile (in steps of 64, and it lists them: 3 us), are assumed;
+// the latter's stores of rows that are not whole 8-byte units take 8 us more.
+struct TileKind {
+  int rows, cols;
+  float start, round, step;
 };
-static StreamCost stream_cost(const AdapterArgs& a, float us4, float us2, float us1) {
-  return {tile_cost(a, 64, 64, us4), tile_cost(a, 32, 32, us2), tile_cost(a, 16, 16, us1)};
+constexpr TileKind kStream64{64, 64, 1.3f, 4.8f, 3.25f}, kStream32{32, 32, 3.2f, 1.1f, 1.4f},
+    kStream16{16, 16, 3.0f, 0.25f, 0.8f}, kGemm128{128, 256, 1.5f, 10.5f, 15.3f}, kGemm256{256, 256, 1.5f, 20.0f, 25.2f};
+constexpr TileKind kStreamF64{64, 64, 1.3f, 3.9f, 18.5f}, kStreamF32{32, 32, 3.2f, 2.1f, 4.45f},
+    kStreamF16{16, 16, 3.0f, 0.75f, 1.6f};
+
+static float tile_cost(const AdapterArgs& a, const TileKind& t) {
+  const float tiles = (float)((a.M + t.rows - 1) / t.rows) * (float)((a.N + t.cols - 1) / t.cols);
+  const int part = a.planes * a.r;
+  const bool gemm = t.cols == 256;
+  const float round = t.round + (gemm ? (a.P > 0 ? 3.0f : 0.0f) + (a.N & 3 ? 8.0f : 0.0f) : 0.0f);
+  const int k = a.H + (gemm ? 2 * ((part + kBK - 1) / kBK * kBK) : part);
+  return t.start + ceilf(tiles / (float)device_cu_count()) * (round + t.step * (float)k / 1024.0f);
 }
 
+// c16, c32, c64: the costs of the tiles.
 template <class Op, class T>
-static void launch_stream(const AdapterArgs& a, const StreamCost& c, hipStream_t s) {
-  if (c.c4 <= c.c2 && c.c4 <= c.c1)
+static void launch_stream(const AdapterArgs& a, float c16, float c32, float c64, hipStream_t s) {
+  if (c64 <= c32 && c64 <= c16)
     launch_stream_as<Op, T, 8, 4, 4>(a, s);
-  else if (c.c2 <= c.c1)
+  else if (c32 <= c16)
     launch_stream_as<Op, T, 8, 2, 2>(a, s);
   else
     launch_stream_as<Op, T, 8, 1, 1>(a, s);
@@ -278,8 +288,6 @@ static void launch_stream(const AdapterArgs& a, const StreamCost& c, hipStream_t
 
 hipError_t launch_adapter_linear(const AdapterArgs& a, bool f32, hipStream_t s) {
   if (a.M == 0) return hipSuccess;
-  const float g128 = tile_cost(a, 128, 256, 57.0f), g256 = tile_cost(a, 256, 256, 105.0f);
-  const StreamCost sc = f32 ? stream_cost(a, 77.0f, 21.0f, 7.0f) : stream_cost(a, 17.5f, 7.0f, 4.0f);
   if (a.P > 0) {
     if (f32)
       launch_shrink<StreamF32>(a, s);
@@ -288,11 +296,14 @@ hipError_t launch_adapter_linear(const AdapterArgs& a, bool f32, hipStream_t s) 
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
-  if (f32 || a.H < 128 || sc.least() <= fminf(g128, g256)) {
-    if (f32)
-      launch_stream<StreamF32, float>(a, sc, s);
-    else
-      launch_stream<StreamBf16<1>, __bf16>(a, sc, s);
+  if (f32) {
+    launch_stream<StreamF32, float>(a, tile_cost(a, kStreamF16), tile_cost(a, kStreamF32), tile_cost(a, kStreamF64), s);
+    return hipGetLastError();
+  }
+  const float c16 = tile_cost(a, kStream16), c32 = tile_cost(a, kStream32), c64 = tile_cost(a, kStream64);
+  const float g128 = tile_cost(a, kGemm128), g256 = tile_cost(a, kGemm256);
+  if (a.H < 128 || fminf(c16, fminf(c32, c64)) <= fminf(g128, g256)) {
+    launch_stream<StreamBf16<1>, __bf16>(a, c16, c32, c64, s);
   } else {
     const int64_t rows = g256 < g128 ? 256 : 128, mt = (a.M + rows - 1) / rows, nt = (a.N + 255) / 256;
     const dim3 grid = tile_grid(mt * nt);

@@ -128,20 +128,21 @@ __device__ __forceinline__ bool drop_nonfinite(i32x4_t& v) {
   return any != 0;
 }
 
-// The elements of B that a tile left out, for 4 columns of row m (its t, in
-// p.planes parts).
+// What the elements of B that a tile left out add to out[m, n] (t in p.planes
+// parts).
 template <class T>
-__device__ __forceinline__ void add_nonfinite(const AdapterArgs& p, int64_t m, int id, int n, f32x4_t& acc) {
+__device__ __forceinline__ float nonfinite_part(const AdapterArgs& p, int64_t m, int id, int n) {
   const T* b = reinterpret_cast<const T*>(p.b) + ((int64_t)id * p.N + n) * p.r;
   const T* t = reinterpret_cast<const T*>(p.t) + m * p.planes * p.r;
-  for (int c = 0; c < 4 && n + c < p.N; ++c)
-    for (int j = 0; j < p.r; ++j) {
-      const float v = (float)b[(int64_t)c * p.r + j];
-      if (__builtin_isfinite(v)) continue;
-      float tv = 0.0f;
-      for (int q = p.planes - 1; q >= 0; --q) tv += (float)t[q * p.r + j];
-      acc[c] += tv * v;
-    }
+  float s = 0.0f;
+  for (int j = 0; j < p.r; ++j) {
+    const float v = (float)b[j];
+    if (__builtin_isfinite(v)) continue;
+    float tv = 0.0f;
+    for (int q = p.planes - 1; q >= 0; --q) tv += (float)t[q * p.r + j];
+    s += tv * v;
+  }
+  return s;
 }
 
 template <int TM>
@@ -376,13 +377,13 @@ __device__ __forceinline__ void adapter_gemm_tile(const AdapterArgs& p, int64_t 
   // 8192 x 4096 x 4096).  (8 columns per thread, i.e. wider stores but two
   // lanes per LDS bank, took 7 us more per tile.)
   const bool fixup = ext > 0 && uniform(tl.nonfinite) != 0;
-  const int c = tid & 63, n = n0 + 4 * c;
+  const int c = tid & 63, n = n0 + 4 * c, wv = uniform(wave);
   const bool wide = (p.N & 3) == 0;
-  const bool pre = wide && p.out.residual && p.out.res_bf16 && n < p.N;
+  const bool pre = wide && p.out.residual && n < p.N;
 #pragma unroll
   for (int P = 0; P < NJ / 2; ++P) {
     auto tile_row = [&](int i) {  // of the thread's i-th staged row of the pass
-      const int ts = (tid >> 6) + 4 * i;
+      const int ts = wv + 4 * i;
       return (ts >> 6) * (TM / 2) + 64 * P + (ts & 63);
     };
     bf16x4_t res[32];
@@ -408,13 +409,21 @@ __device__ __forceinline__ void adapter_gemm_tile(const AdapterArgs& p, int64_t 
     }
     __syncthreads();
     auto staged = [&](int i) {
-      const int ts = (tid >> 6) + 4 * i;
-      return *reinterpret_cast<const f32x4_t*>(lds + ts * 1024 + ((c ^ (ts & 15)) << 4));
+      const int ts = wv + 4 * i;
+      return reinterpret_cast<f32x4_t*>(lds + ts * 1024 + ((c ^ (ts & 15)) << 4));
     };
-    if (wide && !fixup && !(p.out.residual && !p.out.res_bf16)) {
+    if (fixup) {
+      for (int i = 0; i < 32; ++i) {
+        const int row = tile_row(i);
+        if (row >= rows || tl.id[row] < 0) continue;
+        for (int e = 0; e < 4 && n + e < p.N; ++e)
+          (*staged(i))[e] += nonfinite_part<__bf16>(p, m0 + row, tl.id[row], n + e);
+      }
+    }
+    if (wide) {
 #pragma unroll
       for (int i = 0; i < 32; ++i) {
-        f32x4_t v = staged(i);
+        f32x4_t v = *staged(i);
         const int row = tile_row(i);
         if (pre) {
 #pragma unroll
@@ -429,13 +438,32 @@ __device__ __forceinline__ void adapter_gemm_tile(const AdapterArgs& p, int64_t 
           *reinterpret_cast<f32x4_t*>(reinterpret_cast<float*>(p.out.out) + at) = v;
         }
       }
-    } else {
-      for (int i = 0; i < 32; ++i) {
-        f32x4_t v = staged(i);
-        const int row = tile_row(i);
-        if (row >= rows || n >= p.N) continue;
-        if (fixup && tl.id[row] >= 0) add_nonfinite<__bf16>(p, m0 + row, tl.id[row], n, v);
-        adapter_store(p, m0 + row, n, v);
+    } else if (n < p.N) {
+      // element by element; the residuals of 8 rows are loaded together
+      const __bf16* r0 = reinterpret_cast<const __bf16*>(p.out.residual) + n;
+#pragma unroll 1
+      for (int i0 = 0; i0 < 32; i0 += 8) {
+        __bf16 r[8][4];
+#pragma unroll
+        for (int u = 0; u < 8; ++u)
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            r[u][e] = p.out.residual ? r0[(m0 + min(tile_row(i0 + u), rows - 1)) * p.N + min(e, p.N - 1 - n)] : (__bf16)0.0f;
+#pragma unroll
+        for (int u = 0; u < 8; ++u) {
+          const f32x4_t v = *staged(i0 + u);
+          const int row = tile_row(i0 + u);
+          if (row >= rows) break;
+          const int64_t at = (m0 + row) * p.N + n;
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            if (n + e >= p.N) break;
+            if (p.out.out_bf16)
+              reinterpret_cast<__bf16*>(p.out.out)[at + e] = (__bf16)(v[e] + (float)r[u][e]);
+            else
+              reinterpret_cast<float*>(p.out.out)[at + e] = v[e] + (float)r[u][e];
+          }
+        }
       }
     }
     __syncthreads();
