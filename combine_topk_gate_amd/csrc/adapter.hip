@@ -80,16 +80,49 @@ __global__ __launch_bounds__(64 * WAVES) void adapter_shrink_kernel(AdapterArgs 
 }
 
 // ------------------------------------------------------------- projection ---
+// The adapters' part of a stream tile's outputs, in one of two ways.  Up to
+// kDirectRank ranks each thread adds those of its own outputs in the epilogue
+// (48 rows of 48 adapters of rank 16, 4096 x 4096: 12 us instead of 14); beyond,
+// they go through the matrix cores (333 x 2048 x 1408, rank 32: 11.6 us instead
+// of 13.5; 1000 x 4096 x 2048, rank 128: 41 instead of 78).
+constexpr int kDirectRank = 16;
+
+// acc[c] += t . B[id, n + c] for the columns that exist, in increasing rank (t
+// in f32; all loads are under way together).
+template <class T>
+__device__ __forceinline__ void add_adapter(const AdapterArgs& a, int64_t m, int id, int n, f32x4_t& acc) {
+  constexpr int V = 16 / sizeof(T), U = kDirectRank / V;  // elements per vector (r is a multiple of 8); vectors
+  typedef T vec_t __attribute__((ext_vector_type(V)));
+  typedef float tvec_t __attribute__((ext_vector_type(V)));
+  const float* t = reinterpret_cast<const float*>(a.t) + m * a.r;
+  const T* b = reinterpret_cast<const T*>(a.b) + ((int64_t)id * a.N + n) * a.r;
+  tvec_t tv[U];
+  vec_t bv[U][4];
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    const int j = min(u * V, a.r - V);
+    tv[u] = *reinterpret_cast<const tvec_t*>(t + j);
+#pragma unroll
+    for (int c = 0; c < 4; ++c)  // (past the last column it is read again, not used)
+      bv[u][c] = *reinterpret_cast<const vec_t*>(b + (int64_t)min(c, a.N - n - 1) * a.r + j);
+  }
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    if (u * V >= a.r) break;
+#pragma unroll
+    for (int c = 0; c < 4; ++c)
+#pragma unroll
+      for (int v = 0; v < V; ++v) acc[c] = fmaf(tv[u][v], (float)bv[u][c][v], acc[c]);
+  }
+}
+
 // acc += t . B for the adapters among the tile's rows, on the matrix cores: a
 // unit is 16 bytes of a lane's B row (32 ranks, f32: 16) of one adapter; unit
 // i of adapter a is wave a + i's, whatever else the tile holds, so a row's sum
 // does not depend on the other rows (the waves' accumulators are added later).
 // A row of another adapter holds zeros, which only cancel finite values: a
 // non-finite element of B is left out, and the result says so (nonfinite_part).
-// row_id: adapter of row m0 + lane.  (Each thread taking the ranks of its own
-// outputs in the epilogue: 78 instead of 41 us at 1000 x 4096 x 2048, rank
-// 128; 13.5 instead of 12.2 at 333 x 2048 x 1408, rank 32; but 12 instead of 13.2
-// where 48 rows have 48 adapters of rank 16.)
+// row_id: adapter of row m0 + lane.
 template <class Op, class T, int WAVES, int NW, int NT>
 __device__ __forceinline__ bool add_adapters(const AdapterArgs& a, int64_t m0, int rows, int n0, int row_id,
                                              f32x4_t (&acc)[NW][NT]) {
@@ -185,7 +218,8 @@ __global__ __launch_bounds__(64 * WAVES) void adapter_stream_kernel(AdapterArgs 
   f32x4_t acc[NW][NT];
   stream_tile<Op, WAVES, NW, false, NT, 2, false>(s, [&](int m) { return (uint32_t)min(m, rows - 1) * a.row_bytes; },
                                         lds + uniform(threadIdx.x >> 6) * stream_line_bytes<Op, NW, NT>(), acc);
-  if (a.P > 0) {
+  const bool direct = a.r <= kDirectRank;
+  if (a.P > 0 && !direct) {
     const bool bad = add_adapters<Op, T, WAVES, NW, NT>(a, m0, rows, n0, row_id, acc);
     if (lane == 0) left_out[threadIdx.x >> 6] = bad;
   }
@@ -195,7 +229,9 @@ __global__ __launch_bounds__(64 * WAVES) void adapter_stream_kernel(AdapterArgs 
     const int n = n0 + 16 * g + 4 * (lane >> 4);
     const int id = __shfl(row_id, i);
     if (i >= rows || n >= a.N) return;
-    if (a.P > 0) {
+    if (direct) {
+      if ((uint32_t)id < (uint32_t)a.P) add_adapter<T>(a, m0 + i, id, n, v);
+    } else {
       bool bad = false;
 #pragma unroll
       for (int w = 0; w < WAVES; ++w) bad |= left_out[w] != 0;
@@ -286,8 +322,19 @@ static void launch_stream(const AdapterArgs& a, float c16, float c32, float c64,
     launch_stream_as<Op, T, 8, 1, 1>(a, s);
 }
 
-hipError_t launch_adapter_linear(const AdapterArgs& a, bool f32, hipStream_t s) {
+hipError_t launch_adapter_linear(AdapterArgs a, bool f32, hipStream_t s) {
   if (a.M == 0) return hipSuccess;
+  float c16, c32, c64, g128 = 0.0f, g256 = 0.0f;
+  a.planes = f32 ? 1 : a.out.out_bf16 ? 2 : 3;
+  bool stream = true;
+  if (f32) {
+    c16 = tile_cost(a, kStreamF16), c32 = tile_cost(a, kStreamF32), c64 = tile_cost(a, kStreamF64);
+  } else {
+    c16 = tile_cost(a, kStream16), c32 = tile_cost(a, kStream32), c64 = tile_cost(a, kStream64);
+    g128 = tile_cost(a, kGemm128), g256 = tile_cost(a, kGemm256);
+    stream = a.H < 128 || fminf(c16, fminf(c32, c64)) <= fminf(g128, g256);
+  }
+  if (stream && a.r <= kDirectRank) a.planes = 1;  // t as f32 values
   if (a.P > 0) {
     if (f32)
       launch_shrink<StreamF32>(a, s);
@@ -297,12 +344,8 @@ hipError_t launch_adapter_linear(const AdapterArgs& a, bool f32, hipStream_t s) 
     if (e != hipSuccess) return e;
   }
   if (f32) {
-    launch_stream<StreamF32, float>(a, tile_cost(a, kStreamF16), tile_cost(a, kStreamF32), tile_cost(a, kStreamF64), s);
-    return hipGetLastError();
-  }
-  const float c16 = tile_cost(a, kStream16), c32 = tile_cost(a, kStream32), c64 = tile_cost(a, kStream64);
-  const float g128 = tile_cost(a, kGemm128), g256 = tile_cost(a, kGemm256);
-  if (a.H < 128 || fminf(c16, fminf(c32, c64)) <= fminf(g128, g256)) {
+    launch_stream<StreamF32, float>(a, c16, c32, c64, s);
+  } else if (stream) {
     launch_stream<StreamBf16<1>, __bf16>(a, c16, c32, c64, s);
   } else {
     const int64_t rows = g256 < g128 ? 256 : 128, mt = (a.M + rows - 1) / rows, nt = (a.N + 255) / 256;

@@ -614,6 +614,10 @@ moe_status_t moe_layer_decode(const moe_problem_t* p, const void* x, const float
   if (overlap(out, nout, x, (size_t)n * elem_bytes(p)) || overlap(out, nout, ws, L.total) || residual_clash(ep, n) ||
       overlap(out, nout, logits, (size_t)p->num_tokens * p->num_experts * 4))
     return MOE_ERR_INVALID_ARGUMENT;
+  const size_t nw = (size_t)held(p) * p->hidden * p->ffn;
+  if (overlap(out, nout, w_gate, nw * elem_bytes(p)) || overlap(out, nout, w_up, nw * elem_bytes(p)) ||
+      overlap(out, nout, w_down, is_mx(p) ? nw + nw / 32 : nw * elem_bytes(p)))
+    return MOE_ERR_INVALID_ARGUMENT;
   hipStream_t s = (hipStream_t)stream;
   if (debug_validate()) {
     // -inf is an expert the token may not choose; NaN and +inf are errors
@@ -690,6 +694,9 @@ moe_status_t moe_adapter_linear(const moe_adapter_problem_t* q, const void* x, c
   if (overlap(out, nout, x, (size_t)g.M * g.H * eb) || overlap(out, nout, w, (size_t)g.N * g.H * eb) ||
       (need > 0 && overlap(out, nout, ws, need)) || residual_clash(g.out, g.M * g.N))
     return MOE_ERR_INVALID_ARGUMENT;
+  if (g.P > 0 && (overlap(out, nout, a, (size_t)g.P * g.r * g.H * eb) || overlap(out, nout, b, (size_t)g.P * g.N * g.r * eb) ||
+                  overlap(out, nout, scale, (size_t)g.P * 4) || overlap(out, nout, adapter_idx, (size_t)g.M * 4)))
+    return MOE_ERR_INVALID_ARGUMENT;
   if (debug_validate() && g.P > 0) {
     const moe_status_t sv = check_range(adapter_idx, g.M, -1, g.P, (hipStream_t)stream);
     if (sv != MOE_OK) return sv;
@@ -701,7 +708,7 @@ moe_status_t moe_adapter_linear(const moe_adapter_problem_t* q, const void* x, c
   g.scale = scale;
   g.idx = adapter_idx;
   g.t = need > 0 ? ws : nullptr;
-  g.planes = f32 ? 1 : g.out.out_bf16 ? 2 : 3;
+  g.planes = 1;  // set by the launcher
   g.row_bytes = (uint32_t)(g.H * eb);
   return hip_status(launch_adapter_linear(g, f32, (hipStream_t)stream));
 }

@@ -127,11 +127,11 @@ struct AdapterArgs {
   const float* scale;
   const int32_t* idx;
   void* t;             // workspace: [M, r] f32, or [M, planes, r] bf16
-  int planes;          // parts of a value of t (1: f32)
+  int planes;          // parts of a value of t (1: f32), set by the launcher
   OutEpilogue out;
   uint32_t row_bytes;  // bytes of a row of x, W and A
 };
-hipError_t launch_adapter_linear(const AdapterArgs& a, bool f32, hipStream_t s);
+hipError_t launch_adapter_linear(AdapterArgs a, bool f32, hipStream_t s);
 
 int device_cu_count();
 

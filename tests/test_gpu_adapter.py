@@ -112,15 +112,26 @@ def test_no_adapters_is_the_projection(M, dtype):
     ref.check(out, y, bound, (M, dtype))
 
 
-def test_rows_do_not_depend_on_the_batch():
-    # a row's bits are the same alone among 16 rows, whatever the others are
-    q, d, epi, out, ws, _ = make(M=16, H=512, N=256, r=16, P=8, seed=4)
+@pytest.mark.parametrize("r", [16, 48])
+def test_rows_do_not_depend_on_the_batch(r):
+    # a row's bits are the same alone as among 16 rows, whatever the others are
+    q, d, epi, out, ws, _ = make(M=16, H=512, N=256, r=r, P=8, seed=4)
     call(q, d, epi, out, ws)
     for m in (0, 7, 15):
         one = {k: (v[m:m + 1].contiguous() if k in ("x", "idx") else v) for k, v in d.items()}
         o = torch.empty((1, 256), device=DEV)
-        call(moe.adapter_problem(1, 512, 256, 16, 8), one, None, o, ws)
+        call(moe.adapter_problem(1, 512, 256, r, 8), one, None, o, ws)
         assert torch.equal(o[0], out[m])
+
+
+# the matrix-core tiles, with rows at any address, residuals, many adapters a tile
+@pytest.mark.parametrize("out,residual", [("f32", False), ("bf16", True), ("f32", True)])
+@pytest.mark.parametrize("shape", [dict(M=3000, H=320, N=2049, r=72, P=7, mix="runs"),
+                                   dict(M=3001, H=320, N=2052, r=16, P=40, mix="rows"),
+                                   dict(M=5004, H=192, N=1753, r=16, P=5, mix="runs"),
+                                   dict(M=4100, H=128, N=1999, r=8, P=3, mix="one")])
+def test_long_batches(shape, out, residual):
+    run_and_check(**shape, out=out, residual=residual, seed=13)
 
 
 def test_output_in_place_of_the_residual():
@@ -131,23 +142,30 @@ def test_output_in_place_of_the_residual():
     assert torch.equal(r, first)
 
 
-@pytest.mark.parametrize("M", [20, 300])
-def test_nan_in_an_unused_adapter_and_in_a_row_stays_there(M):
-    q, d, epi, out, ws, _ = make(M=M, H=128, N=72, P=6, mix="rows", seed=6)
+@pytest.mark.parametrize("M,N,r,dtype", [(20, 72, 16, "bf16"), (300, 72, 16, "bf16"), (20, 72, 40, "bf16"),
+                                         (300, 72, 40, "bf16"), (20, 72, 40, "f32"), (300, 72, 72, "f32"),
+                                         (3000, 2052, 40, "bf16"), (4000, 2049, 24, "bf16")])
+def test_nan_in_an_unused_adapter_and_in_a_row_stays_there(M, N, r, dtype):
+    q, d, epi, out, ws, _ = make(M=M, H=128, N=N, r=r, P=6, mix="rows", dtype=dtype, seed=6)
     d["idx"][d["idx"] == 2] = 1
     d["a"][2], d["b"][2], d["scale"][2] = float("nan"), float("inf"), float("nan")
-    y, bound = want(d, "bf16", "f32")
+    y, bound = want(d, dtype, "f32")
     call(q, d, epi, out, ws)
     ref.check(out, y, bound, "unused adapter")
     clean = out.clone()
     d["x"][3] = float("nan")
     d["b"][4, 5] = float("inf")
+    d["b"][4, N - 1, r - 1] = float("-inf")
     call(q, d, epi, out, ws)
-    same = torch.ones((M, 72), dtype=torch.bool, device=DEV)
+    same = torch.ones((M, N), dtype=torch.bool, device=DEV)
     same[3] = False
-    same[d["idx"] == 4, 5] = False
+    rows = d["idx"] == 4
+    same[rows, 5] = same[rows, N - 1] = False
     assert torch.equal(out[same], clean[same])
     assert bool(torch.isnan(out[3]).all())
+    # one infinite element, the others finite: t's sign decides
+    rows[3] = False
+    assert bool(torch.isinf(out[rows, N - 1]).all()) and not bool(torch.isfinite(out[rows, 5]).any())
 
 
 def test_same_bits_on_every_call():

@@ -96,10 +96,38 @@ SHAPES = [
 ]
 
 
+# entries of 64 and 128 rows (Layer0 wide enough for every CU), with 1 to 128
+# rows in them; Layer1's reduction in 4 and 8 parts; Layer0 blocks of few
+# tokens that take several column groups
+SPLITS = [
+    dict(M=60, H=192, F=1408, E=3, k=2),
+    dict(M=100, H=128, F=1408, E=3, k=2),
+    dict(M=255, H=64, F=1408, E=3, k=2),
+    dict(M=256, H=320, F=1024, E=4, k=4),
+    dict(M=97, H=64, F=4096, E=1, k=1),
+    dict(M=20, H=64, F=8192, E=2, k=2),
+    dict(M=9, H=192, F=2560, E=8, k=1),
+    dict(M=8, H=64, F=8576, E=22, k=5),
+]
+
+
 @pytest.mark.parametrize("out,residual", [("f32", False), ("bf16", True)])
-@pytest.mark.parametrize("shape", SHAPES)
+@pytest.mark.parametrize("shape", SHAPES + SPLITS)
 def test_shapes_bf16(shape, out, residual):
     run_and_check(**shape, out=out, residual=residual)
+
+
+@pytest.mark.parametrize("out", ["f32", "bf16"])
+@pytest.mark.parametrize("shape", SPLITS)
+def test_splits_mxfp8(shape, out):
+    run_and_check(**shape, dtype="bf16_mxfp8", out=out, seed=5)
+
+
+@pytest.mark.parametrize("shape", [dict(M=60, H=64, F=5504, E=3, k=2), dict(M=120, H=64, F=5504, E=3, k=2),
+                                   dict(M=255, H=64, F=5504, E=3, k=2), dict(M=73, H=192, F=448, E=4, k=2),
+                                   dict(M=29, H=64, F=4096, E=4, k=4), dict(M=8, H=64, F=8576, E=22, k=5)])
+def test_splits_f32(shape):
+    run_and_check(**shape, dtype="f32", residual=True, seed=6)
 
 
 @pytest.mark.parametrize("shape", [s for s in SHAPES if s["E"] <= 64])

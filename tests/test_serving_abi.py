@@ -83,6 +83,8 @@ def test_decode_refuses_overlaps(lib):
     assert decode(lib, p, out=at(0)) == INV  # x
     assert decode(lib, p, out=P(at(1).value + 64)) == INV  # logits
     assert decode(lib, p, out=P(at(6).value + 256)) == INV  # ws
+    for i in (2, 3, 4):  # the last bytes of the weights
+        assert decode(lib, p, out=P(at(i).value + 8 * 64 * 64 * 2 - 16)) == INV
     # the residual one row further, or in place with another type
     assert decode(lib, p, epi=moe.Epilogue(at(5).value + 128, moe.MOE_DTYPE_BF16)) == INV
     assert decode(lib, p, epi=moe.Epilogue(at(5).value, moe.MOE_DTYPE_F32)) == INV
@@ -91,6 +93,13 @@ def test_decode_refuses_overlaps(lib):
 def test_decode_without_tokens_launches_nothing(lib):
     p = moe.problem(0, 64, 64, 8, 2)
     assert decode(lib, p, x=None, logits=None, out=None, ws=None, ws_bytes=0) == moe.MOE_OK
+
+
+def test_workspace_sizes_without_tokens(lib):
+    for dtype in ("bf16", "f32", "bf16_mxfp8"):
+        for E, k, held in ((1, 1, 0), (512, 16, 3)):
+            p = moe.problem(0, 64, 128, E, k, dtype=dtype, local_experts=held)
+            assert 0 <= moe.moe_workspace_bytes(p, moe.MOE_OP_LAYER_DECODE) < 1 << 16
 
 
 def test_decode_workspace_covers_the_intermediates(lib):
@@ -136,6 +145,10 @@ def test_adapter_refuses_overlaps(lib):
     q = moe.adapter_problem(64, 64, 64, 8, 2)
     assert adapter(lib, q, out=P(at(0).value + 64)) == INV  # x
     assert adapter(lib, q, out=at(1)) == INV  # w
+    assert adapter(lib, q, out=P(at(2).value + 2 * 8 * 64 * 2 - 16)) == INV  # a
+    assert adapter(lib, q, out=P(at(3).value + 2 * 64 * 8 * 2 - 16)) == INV  # b
+    assert adapter(lib, q, out=at(4)) == INV  # scale
+    assert adapter(lib, q, out=P(at(5).value + 240)) == INV  # adapter_idx
     assert adapter(lib, q, out=at(7)) == INV  # ws
     assert adapter(lib, q, epi=moe.Epilogue(at(6).value + 128, moe.MOE_DTYPE_BF16)) == INV
     assert adapter(lib, q, epi=moe.Epilogue(at(6).value, moe.MOE_DTYPE_F32)) == INV
