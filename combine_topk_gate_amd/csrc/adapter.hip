@@ -51,7 +51,7 @@ __global__ __launch_bounds__(64 * WAVES) void adapter_shrink_kernel(AdapterArgs 
     // (of the rows of other adapters nothing is read, computed or stored)
     s.w0 = reinterpret_cast<const char*>(a.a) + ((int64_t)mine * a.r + j0) * a.row_bytes;
     f32x4_t acc[NW][NT];
-    stream_tile<Op, WAVES, NW, false, NT, 2, false>(s, [&](int m) { return __shfl(id, m) == mine ? (uint32_t)m * a.row_bytes : kNoRow; },
+    stream_tile<Op, WAVES, NW, kOne, NT, 2, false>(s, [&](int m) { return __shfl(id, m) == mine ? (uint32_t)m * a.row_bytes : kNoRow; },
                                           lds + wave * stream_line_bytes<Op, NW, NT>(), acc);
     const float sc = a.scale[mine];
     stream_reduce<WAVES, NW, NT, NW, 1>(acc, reinterpret_cast<f32x4_t*>(lds), [&](int g, int jt, const f32x4_t (&t)[1]) {
@@ -88,31 +88,32 @@ __global__ __launch_bounds__(64 * WAVES) void adapter_shrink_kernel(AdapterArgs 
 constexpr int kDirectRank = 16;
 
 // acc[c] += t . B[id, n + c] for the columns that exist, in increasing rank (t
-// in f32; all loads are under way together).
+// in f32; the loads of 16 ranks are under way together).
 template <class T>
-__device__ __forceinline__ void add_adapter(const AdapterArgs& a, int64_t m, int id, int n, f32x4_t& acc) {
+__device__ __forceinline__ void add_adapter(const AdapterArgs& a, const float* t, int id, int n, f32x4_t& acc) {
   constexpr int V = 16 / sizeof(T), U = kDirectRank / V;  // elements per vector (r is a multiple of 8); vectors
   typedef T vec_t __attribute__((ext_vector_type(V)));
   typedef float tvec_t __attribute__((ext_vector_type(V)));
-  const float* t = reinterpret_cast<const float*>(a.t) + m * a.r;
   const T* b = reinterpret_cast<const T*>(a.b) + ((int64_t)id * a.N + n) * a.r;
-  tvec_t tv[U];
-  vec_t bv[U][4];
+  for (int j0 = 0; j0 < a.r; j0 += kDirectRank) {
+    tvec_t tv[U];
+    vec_t bv[U][4];
 #pragma unroll
-  for (int u = 0; u < U; ++u) {
-    const int j = min(u * V, a.r - V);
-    tv[u] = *reinterpret_cast<const tvec_t*>(t + j);
+    for (int u = 0; u < U; ++u) {
+      const int j = min(j0 + u * V, a.r - V);
+      tv[u] = *reinterpret_cast<const tvec_t*>(t + j);
 #pragma unroll
-    for (int c = 0; c < 4; ++c)  // (past the last column it is read again, not used)
-      bv[u][c] = *reinterpret_cast<const vec_t*>(b + (int64_t)min(c, a.N - n - 1) * a.r + j);
-  }
+      for (int c = 0; c < 4; ++c)  // (past the last column it is read again, not used)
+        bv[u][c] = *reinterpret_cast<const vec_t*>(b + (int64_t)min(c, a.N - n - 1) * a.r + j);
+    }
 #pragma unroll
-  for (int u = 0; u < U; ++u) {
-    if (u * V >= a.r) break;
+    for (int u = 0; u < U; ++u) {
+      if (j0 + u * V >= a.r) break;
 #pragma unroll
-    for (int c = 0; c < 4; ++c)
+      for (int c = 0; c < 4; ++c)
 #pragma unroll
-      for (int v = 0; v < V; ++v) acc[c] = fmaf(tv[u][v], (float)bv[u][c][v], acc[c]);
+        for (int v = 0; v < V; ++v) acc[c] = fmaf(tv[u][v], (float)bv[u][c][v], acc[c]);
+    }
   }
 }
 
@@ -216,7 +217,7 @@ __global__ __launch_bounds__(64 * WAVES) void adapter_stream_kernel(AdapterArgs 
   // lane's row: m0 + lane (loaded early: t and B wait for it)
   const int row_id = a.P > 0 ? a.idx[m0 + min(lane, rows - 1)] : -1;
   f32x4_t acc[NW][NT];
-  stream_tile<Op, WAVES, NW, false, NT, 2, false>(s, [&](int m) { return (uint32_t)min(m, rows - 1) * a.row_bytes; },
+  stream_tile<Op, WAVES, NW, kOne, NT, 2, false>(s, [&](int m) { return (uint32_t)min(m, rows - 1) * a.row_bytes; },
                                         lds + uniform(threadIdx.x >> 6) * stream_line_bytes<Op, NW, NT>(), acc);
   const bool direct = a.r <= kDirectRank;
   if (a.P > 0 && !direct) {
@@ -230,7 +231,7 @@ __global__ __launch_bounds__(64 * WAVES) void adapter_stream_kernel(AdapterArgs 
     const int id = __shfl(row_id, i);
     if (i >= rows || n >= a.N) return;
     if (direct) {
-      if ((uint32_t)id < (uint32_t)a.P) add_adapter<T>(a, m0 + i, id, n, v);
+      if ((uint32_t)id < (uint32_t)a.P) add_adapter<T>(a, reinterpret_cast<const float*>(a.t) + (m0 + i) * a.r, id, n, v);
     } else {
       bool bad = false;
 #pragma unroll
@@ -241,6 +242,56 @@ __global__ __launch_bounds__(64 * WAVES) void adapter_stream_kernel(AdapterArgs 
     }
     adapter_store(a, m0 + i, n, v);
   });
+}
+
+// At most 8 rows that use one adapter between them (one row, or one adapter),
+// 16 columns a block: the adapter's A streams past the rows as NA further
+// groups of 16 weight rows, so every block has t for itself and there is one
+// launch (one row, 2048 x 64, rank 8: 4.6 us instead of 3.8 + 4.0 in two; 4096 x
+// 4096, rank 16: 9.6 instead of 5.1 + 8.7, rank 64: 15 instead of 6.8 + 8.4).
+constexpr int kOneRows = 8;
+
+template <class Op, class T, int NA>
+__global__ __launch_bounds__(512) void adapter_one_kernel(AdapterArgs a) {
+  constexpr int WAVES = 8, NW = 1 + NA, kLine = stream_line_bytes<Op, NW, 1, kOneRows>();
+  __shared__ __attribute__((aligned(16))) char lds[WAVES * imax(kLine, NW * 1024)];
+  __shared__ __attribute__((aligned(32))) float t[kOneRows][16 * NA];
+  const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6), rows = (int)a.M;
+  const int n0 = blockIdx.x * 16;
+  int row_id = lane < rows ? a.idx[lane] : -1;
+  if ((uint32_t)row_id >= (uint32_t)a.P) row_id = -1;
+  const uint64_t used = __ballot(row_id >= 0);
+  const int id = used ? __builtin_amdgcn_readlane(row_id, __ffsll((unsigned long long)used) - 1) : 0;
+  StreamArgs s{};
+  s.row_bytes = a.row_bytes;
+  s.w0 = reinterpret_cast<const char*>(a.w) + (int64_t)n0 * a.row_bytes;
+  s.w_rows = min(16, a.N - n0);
+  s.w1 = reinterpret_cast<const char*>(a.a) + (int64_t)id * a.r * a.row_bytes;
+  s.w1_rows = a.r;
+  s.x = a.x;
+  s.x_bytes = (uint32_t)rows * a.row_bytes;
+  s.lines = a.H / Op::kLine;
+  f32x4_t acc[NW][1], out = {0.f, 0.f, 0.f, 0.f};
+  stream_share<Op, NW, kFirst, 1, 2, kOneRows, false>(
+      s, wave, WAVES, [&](int m) { return m < rows ? (uint32_t)m * a.row_bytes : kNoRow; }, lds + wave * kLine, acc);
+  const float sc = a.scale[id];
+  // wave 0 gets the projection's sums, the next ones t's
+  stream_reduce<WAVES, NW, 1, NW, 1>(acc, reinterpret_cast<f32x4_t*>(lds), [&](int g, int, const f32x4_t (&sum)[1]) {
+    if (g == 0) {
+      out = sum[0];
+    } else if ((lane & 15) < kOneRows) {
+      f32x4_t v = sum[0];
+#pragma unroll
+      for (int c = 0; c < 4; ++c) v[c] *= sc;
+      *reinterpret_cast<f32x4_t*>(&t[lane & 15][16 * (g - 1) + 4 * (lane >> 4)]) = v;
+    }
+  });
+  __syncthreads();
+  const int i = lane & 15, n = n0 + 4 * (lane >> 4);
+  const int mine = __shfl(row_id, i);
+  if (wave > 0 || i >= rows || n >= a.N) return;
+  if (mine >= 0) add_adapter<T>(a, t[i], id, n, out);
+  adapter_store(a, i, n, out);
 }
 
 // ----------------------------------------------------------------- launch ---
@@ -322,8 +373,34 @@ static void launch_stream(const AdapterArgs& a, float c16, float c32, float c64,
     launch_stream_as<Op, T, 8, 1, 1>(a, s);
 }
 
+template <class Op, class T>
+static void launch_one(const AdapterArgs& a, hipStream_t s) {
+  const unsigned blocks = (unsigned)((a.N + 15) / 16);
+  if (a.r <= 16)
+    adapter_one_kernel<Op, T, 1><<<blocks, 512, 0, s>>>(a);
+  else if (a.r <= 32)
+    adapter_one_kernel<Op, T, 2><<<blocks, 512, 0, s>>>(a);
+  else
+    adapter_one_kernel<Op, T, 4><<<blocks, 512, 0, s>>>(a);
+}
+
+// One launch (adapter_one_kernel) where the blocks' reading A from the L2, at
+// about 124 bytes a ns and CU, takes less than the other launch.
+static bool one_launch(const AdapterArgs& a) {
+  if (a.P == 0 || a.M > kOneRows || (a.M > 1 && a.P > 1) || a.r > 64) return false;
+  const int64_t rounds = (a.N + 16 * device_cu_count() - 1) / (16 * device_cu_count());
+  return rounds * a.r * a.row_bytes <= 768 << 10;
+}
+
 hipError_t launch_adapter_linear(AdapterArgs a, bool f32, hipStream_t s) {
   if (a.M == 0) return hipSuccess;
+  if (one_launch(a)) {
+    if (f32)
+      launch_one<StreamF32, float>(a, s);
+    else
+      launch_one<StreamBf16<1>, __bf16>(a, s);
+    return hipGetLastError();
+  }
   float c16, c32, c64, g128 = 0.0f, g256 = 0.0f;
   a.planes = f32 ? 1 : a.out.out_bf16 ? 2 : 3;
   bool stream = true;

@@ -184,7 +184,7 @@ __device__ __forceinline__ void decode_l0_tile(const DecodeArgs& a, int4 ent, ch
   s.lines = a.H / Op::kLine;
   f32x4_t acc[2][NT];
   const int wave = uniform(threadIdx.x >> 6);
-  stream_tile<Op, kStreamWaves, 2, true, NT, 4, true>(
+  stream_tile<Op, kStreamWaves, 2, kPaired, NT, 4, true>(
       s, [&](int i) { return decode_row(a.plan, ent, i, a.plan.k, a.x_pitch); },
       lds + wave * stream_line_bytes<Op, 2, NT>(), acc);
   const int lane = threadIdx.x & 63;
@@ -223,7 +223,7 @@ __device__ __forceinline__ void decode_l0_wide_tile(const DecodeArgs& a, int4 en
   s.x_bytes = (uint32_t)a.plan.M * a.x_pitch;
   s.lines = a.H / Op::kLine;
   f32x4_t acc[2][NT];
-  stream_wide<Op, kWideL0, 2, true, NT, 4, true>(
+  stream_wide<Op, kWideL0, 2, kPaired, NT, 4, true>(
       s, [&](int i) { return decode_row(a.plan, ent, i, a.plan.k, a.x_pitch); }, lds, acc);
   const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
 #pragma unroll
@@ -271,7 +271,7 @@ __device__ __forceinline__ void decode_l1_tile(const DecodeArgs& a, int4 ent, ch
   f32x4_t acc[NW][NT];
   constexpr int kDepth = Op::kXH * NT * Op::kP > 12 ? 2 : NW > 1 ? 3 : 4;
   float* y = a.y + (int64_t)blockIdx.z * a.plan.M * a.plan.k * a.H;
-  stream_wide<Op, WAVES, NW, false, NT, kDepth, true>(
+  stream_wide<Op, WAVES, NW, kOne, NT, kDepth, true>(
       s, [&](int i) { return decode_row(a.plan, ent, i, 1, a.h_pitch); }, lds, acc);
   const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
 #pragma unroll
@@ -428,7 +428,7 @@ __global__ __launch_bounds__(kStreamThreads) void decode_few_l0_kernel(const flo
     s.x_bytes = (uint32_t)p.M * a.x_pitch;
     s.lines = a.H / Op::kLine;
     f32x4_t acc[2][1];
-    stream_share<Op, 2, true, 1, 4, kFewRows, true>(
+    stream_share<Op, 2, kPaired, 1, 4, kFewRows, true>(
         s, wave, kStreamWaves, [&](int i) { return i < rows ? (uint32_t)(ent.pair[i] / p.k) * a.x_pitch : kNoRow; }, lds + wave * kLine, acc);
     stream_reduce<kStreamWaves, 2, 1, 2, 2>(acc, reinterpret_cast<f32x4_t*>(lds), [&](int, int, const f32x4_t (&gu)[2]) {
       const int i = lane & 15;
@@ -486,7 +486,7 @@ __global__ __launch_bounds__(kStreamThreads) void decode_few_l1_kernel(DecodeArg
       s.scale_pitch = a.F;
     }
     f32x4_t acc[1][1];
-    stream_share<Op, 1, false, 1, 4, kFewRows, true>(
+    stream_share<Op, 1, kOne, 1, 4, kFewRows, true>(
         s, wave, kStreamWaves, [&](int i) { return i < rows ? (uint32_t)(i == lane >> 3 ? row_pair : ent->pair[i]) * a.h_pitch : kNoRow; },
         lds + wave * kLine, acc);
     stream_reduce<kStreamWaves, 1, 1, 1, 1>(acc, reinterpret_cast<f32x4_t*>(lds), [&](int, int, const f32x4_t (&y)[1]) {

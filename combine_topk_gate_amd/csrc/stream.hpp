@@ -136,9 +136,10 @@ struct StreamMx {
 
 // The rows a tile reads.
 struct StreamArgs {
-  const void* w0;        // first weight row; PAIRED: of the even groups of 16 rows
-  const void* w1;        // PAIRED: first weight row of the odd groups
+  const void* w0;        // first weight row (of kPaired: of the even groups of 16)
+  const void* w1;        // first weight row of the other groups (kPaired, kFirst)
   int w_rows;            // weight rows that exist there (>= 1)
+  int w1_rows;           // kFirst: ... at w1
   uint32_t row_bytes;    // bytes of a weight row
   const void* x;         // base of the token rows
   uint32_t x_bytes;      // bytes that exist there (below 2^31)
@@ -157,9 +158,12 @@ constexpr int stream_line_bytes() {
   return 16 * NW * 128 + XG * NT * Op::kP * Op::kXC * 16;
 }
 
-// One wave's share of the tile: lines first, first + stride, ....  Weight
-// group g is rows 16 g .. of w0, or, PAIRED, rows 16 (g / 2) .. of w0 (g even)
-// or w1 (g odd).  row_off(i): byte offset from a.x of token row i (0 <= i <
+// The rows of weight group g: kOne, rows 16 g .. of w0; kPaired, rows 16 (g / 2)
+// .. of w0 (g even) or w1 (g odd); kFirst, rows 0 .. of w0 (g = 0) or 16 (g - 1)
+// .. of w1.
+constexpr int kOne = 0, kPaired = 1, kFirst = 2;
+
+// One wave's share of the tile: lines first, first + stride, ....  row_off(i): byte offset from a.x of token row i (0 <= i <
 // 16 NT), any row for one that does not exist.  lds: stream_line_bytes() of
 // the wave's own.  DEPTH: lines in flight (as many as about 96 registers hold,
 // at most): 4 where the weights come from HBM for long (decode, 2 experts of
@@ -172,7 +176,7 @@ constexpr int stream_depth() {
   return d > DEPTH ? DEPTH : d < 1 ? 1 : d;
 }
 
-template <class Op, int NW, bool PAIRED, int NT, int DEPTH, int XG, bool ONCE, class RowOff>
+template <class Op, int NW, int GROUPS, int NT, int DEPTH, int XG, bool ONCE, class RowOff>
 __device__ __forceinline__ void stream_share(const StreamArgs& a, int first, int stride, RowOff row_off,
                                              char* __restrict__ lds, f32x4_t (&acc)[NW][NT]) {
   constexpr bool MX = Op::kMx;
@@ -188,8 +192,10 @@ __device__ __forceinline__ void stream_share(const StreamArgs& a, int first, int
   uint32_t woff[2 * NW], xo[XL * NT];
 #pragma unroll
   for (int l = 0; l < 2 * NW; ++l) {
-    const int i = 8 * (l & 1) + (lane >> 3), grp = PAIRED ? l >> 2 : l >> 1;
-    woff[l] = (uint32_t)min(16 * grp + i, a.w_rows - 1) * a.row_bytes + 16u * ((lane & 7) ^ swz_w(i));
+    const int i = 8 * (l & 1) + (lane >> 3), g = l >> 1;
+    const int grp = GROUPS == kPaired ? g >> 1 : GROUPS == kFirst && g > 0 ? g - 1 : g;
+    const int last = (GROUPS == kFirst && g > 0 ? a.w1_rows : a.w_rows) - 1;
+    woff[l] = (uint32_t)min(16 * grp + i, last) * a.row_bytes + 16u * ((lane & 7) ^ swz_w(i));
   }
 #pragma unroll
   for (int l = 0; l < XL * NT; ++l) {
@@ -218,10 +224,12 @@ __device__ __forceinline__ void stream_share(const StreamArgs& a, int first, int
     const bool live = line < a.lines;
     const uint32_t at = live ? (uint32_t)line : 0u;
     const __amdgpu_buffer_rsrc_t r0 = make_rsrc(a.w0, live ? w_bytes : 0u);
-    const __amdgpu_buffer_rsrc_t r1 = make_rsrc(PAIRED ? a.w1 : a.w0, live ? w_bytes : 0u);
+    const __amdgpu_buffer_rsrc_t r1 =
+        make_rsrc(GROUPS == kOne ? a.w0 : a.w1, live ? GROUPS == kFirst ? (uint32_t)a.w1_rows * a.row_bytes : w_bytes : 0u);
+    auto second = [](int l) { return GROUPS == kPaired ? (l & 2) != 0 : GROUPS == kFirst && l >= 2; };
     const __amdgpu_buffer_rsrc_t rx = make_rsrc(a.x, live ? a.x_bytes : 0u);
 #pragma unroll
-    for (int l = 0; l < 2 * NW; ++l) c.w[l] = load_weight<ONCE>(PAIRED && (l & 2) ? r1 : r0, woff[l], at * 128u);
+    for (int l = 0; l < 2 * NW; ++l) c.w[l] = load_weight<ONCE>(second(l) ? r1 : r0, woff[l], at * 128u);
     if constexpr (MX) {
 #pragma unroll
       for (int g = 0; g < NW; ++g)
@@ -287,10 +295,10 @@ __device__ __forceinline__ void stream_share(const StreamArgs& a, int first, int
 }
 
 // The whole tile by the WAVES waves of a block.
-template <class Op, int WAVES, int NW, bool PAIRED, int NT, int DEPTH, bool ONCE, class RowOff>
+template <class Op, int WAVES, int NW, int GROUPS, int NT, int DEPTH, bool ONCE, class RowOff>
 __device__ __forceinline__ void stream_tile(const StreamArgs& a, RowOff row_off, char* __restrict__ lds,
                                             f32x4_t (&acc)[NW][NT]) {
-  stream_share<Op, NW, PAIRED, NT, DEPTH, 16, ONCE>(a, uniform(threadIdx.x >> 6), WAVES, row_off, lds, acc);
+  stream_share<Op, NW, GROUPS, NT, DEPTH, 16, ONCE>(a, uniform(threadIdx.x >> 6), WAVES, row_off, lds, acc);
 }
 
 constexpr int imax(int a, int b) { return a > b ? a : b; }
@@ -307,7 +315,7 @@ constexpr int stream_wide_bytes() {
   return WAVES * NW * 2048 + 2 * 16 * NT * Op::kP * Op::kXC * 16;
 }
 
-template <class Op, int WAVES, int NW, bool PAIRED, int NT, int DEPTH, bool ONCE, class RowOff>
+template <class Op, int WAVES, int NW, int GROUPS, int NT, int DEPTH, bool ONCE, class RowOff>
 __device__ __forceinline__ void stream_wide(const StreamArgs& a, RowOff row_off, char* __restrict__ lds,
                                             f32x4_t (&acc)[NW][NT]) {
   constexpr bool MX = Op::kMx;
@@ -322,7 +330,7 @@ __device__ __forceinline__ void stream_wide(const StreamArgs& a, RowOff row_off,
 #pragma unroll
   for (int l = 0; l < 2 * NW; ++l) {
     const int i = 8 * (l & 1) + (lane >> 3), grp = wave * NW + (l >> 1);
-    woff[l] = (uint32_t)min(16 * (PAIRED ? grp >> 1 : grp) + i, a.w_rows - 1) * a.row_bytes +
+    woff[l] = (uint32_t)min(16 * (GROUPS == kPaired ? grp >> 1 : grp) + i, a.w_rows - 1) * a.row_bytes +
               16u * ((lane & 7) ^ swz_w(i));
   }
   // token load l of a line: plane l / (XL NT), rows XR (l % (XL NT)) ..
@@ -346,15 +354,15 @@ __device__ __forceinline__ void stream_wide(const StreamArgs& a, RowOff row_off,
     i32x4_t x[XW];
     uint32_t s[MX ? NW : 1];
   };
-  static_assert(!PAIRED || NW % 2 == 0, "a wave's pairs are its own");
+  static_assert(GROUPS == kOne || (GROUPS == kPaired && NW % 2 == 0), "a wave's pairs are its own");
   auto load = [&](Line& c, int line) {
     const bool live = line < a.lines;  // else nothing is read (see stream_share)
     const uint32_t at = live ? (uint32_t)(a.line0 + line) : 0u;
     const __amdgpu_buffer_rsrc_t r0 = make_rsrc(a.w0, live ? w_bytes : 0u);
-    const __amdgpu_buffer_rsrc_t r1 = make_rsrc(PAIRED ? a.w1 : a.w0, live ? w_bytes : 0u);
+    const __amdgpu_buffer_rsrc_t r1 = make_rsrc(GROUPS == kPaired ? a.w1 : a.w0, live ? w_bytes : 0u);
     const __amdgpu_buffer_rsrc_t rx = make_rsrc(a.x, live ? a.x_bytes : 0u);
 #pragma unroll
-    for (int l = 0; l < 2 * NW; ++l) c.w[l] = load_weight<ONCE>(PAIRED && (l & 2) ? r1 : r0, woff[l], at * 128u);
+    for (int l = 0; l < 2 * NW; ++l) c.w[l] = load_weight<ONCE>(GROUPS == kPaired && (l & 2) ? r1 : r0, woff[l], at * 128u);
     if constexpr (MX) {
 #pragma unroll
       for (int g = 0; g < NW; ++g) c.s[g] = *reinterpret_cast<const uint32_t*>(a.scale + so[g] + at * 128u);

@@ -423,7 +423,7 @@ moe_status_t moe_layer_decode(const moe_problem_t* p, const void* x, const float
  *   (MOE_DTYPE_BF16_MXFP8: MOE_ERR_UNSUPPORTED); scale [P] f32;
  *   adapter_idx [M] int32; epi as in moe_combine_ex, with residual and out
  *   [M,N] (NULL: f32 out, no residual).  out may be the residual itself
- *   (same type), and otherwise overlaps neither x, w, residual nor ws.
+ *   (same type), and otherwise overlaps no input and not ws.
  *   P = 0: the projection alone (a, b, scale, adapter_idx and ws unused).
  * Limits: 0 <= M < 2^27 and M N < 2^40 (else MOE_ERR_UNSUPPORTED); H a
  * multiple of 64 in [64, 65536]; 1 <= N <= 65536; rank a multiple of 8 in [8,

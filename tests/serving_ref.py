@@ -136,11 +136,15 @@ def check_norm(got, want, roundings, out_bf16, what):
     """Relative 2-norm of the error: `roundings` f32 roundings of independent
     signs, each at most u of a partial sum, whose rms is at most the sum's:
     sqrt(roundings) u, times 4 for the stages; plus the cast's rms, half a
-    step / sqrt(3) at most, for a bf16 output."""
+    step / sqrt(3) at most, for a bf16 output.  That is a mean over many
+    elements: a single one may be off by the whole half step (0.6078 lies
+    between the bf16 values 0.60547 and 0.60938, 0.0016 from the nearer: 2.6e-3
+    of it, above 2^-8 / sqrt(3) = 2.3e-3 and below 2^-8 = 3.9e-3), so outputs of
+    fewer than 64 elements get the half step itself."""
     ref = want.norm()
     if float(ref) == 0.0:
         assert not bool(got.double().any()), what
         return
     rel = float((got.double() - want).norm() / ref)
-    bound = 4 * roundings ** 0.5 * U + (BF16 / 3 ** 0.5 if out_bf16 else 0.0)
+    bound = 4 * roundings ** 0.5 * U + ((BF16 / 3 ** 0.5 if got.numel() >= 64 else BF16) if out_bf16 else 0.0)
     assert rel <= bound, (what, rel, bound)

@@ -112,16 +112,28 @@ def test_no_adapters_is_the_projection(M, dtype):
     ref.check(out, y, bound, (M, dtype))
 
 
-@pytest.mark.parametrize("r", [16, 48])
-def test_rows_do_not_depend_on_the_batch(r):
-    # a row's bits are the same alone as among 16 rows, whatever the others are
-    q, d, epi, out, ws, _ = make(M=16, H=512, N=256, r=r, P=8, seed=4)
+@pytest.mark.parametrize("M,r", [(16, 16), (16, 48), (100, 40)])
+def test_rows_do_not_depend_on_the_other_rows(M, r):
+    # a row's bits are the same whatever the other rows and their adapters are
+    q, d, epi, out, ws, _ = make(M=M, H=512, N=256, r=r, P=8, seed=4)
     call(q, d, epi, out, ws)
-    for m in (0, 7, 15):
-        one = {k: (v[m:m + 1].contiguous() if k in ("x", "idx") else v) for k, v in d.items()}
-        o = torch.empty((1, 256), device=DEV)
-        call(moe.adapter_problem(1, 512, 256, r, 8), one, None, o, ws)
-        assert torch.equal(o[0], out[m])
+    first = out.clone()
+    for m in (0, 7, M - 1):
+        other = dict(d, x=-2 * d["x"], idx=d["idx"].flip(0).contiguous())
+        other["x"][m], other["idx"][m] = d["x"][m], d["idx"][m]
+        call(q, other, epi, out, ws)
+        assert torch.equal(out[m], first[m])
+
+
+# at most 8 rows and one adapter between them: one launch, up to rank 64
+@pytest.mark.parametrize("dtype,out,residual", [("bf16", "f32", False), ("bf16", "bf16", True), ("f32", "f32", True)])
+@pytest.mark.parametrize("shape", [dict(M=1, H=64, N=1, r=8, P=3), dict(M=1, H=320, N=1001, r=24, P=3),
+                                   dict(M=1, H=4096, N=257, r=64, P=9), dict(M=1, H=192, N=40, r=72, P=2),
+                                   dict(M=8, H=256, N=60, r=40, P=1), dict(M=5, H=1024, N=130, r=16, P=1),
+                                   dict(M=9, H=256, N=60, r=16, P=1), dict(M=2, H=256, N=60, r=16, P=2)])
+def test_few_rows_of_one_adapter(shape, dtype, out, residual):
+    for mix in ("one", "none", "rows", "outside"):
+        run_and_check(**shape, dtype=dtype, out=out, residual=residual, mix=mix, seed=14)
 
 
 # the matrix-core tiles, with rows at any address, residuals, many adapters a tile
