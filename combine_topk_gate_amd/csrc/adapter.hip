@@ -119,29 +119,30 @@ __device__ __forceinline__ void add_adapter(const AdapterArgs& a, const float* t
 
 // acc += t . B for the adapters among the tile's rows, on the matrix cores: a
 // unit is 16 bytes of a lane's B row (32 ranks, f32: 16) of one adapter; unit
-// i of adapter a is wave a + i's, whatever else the tile holds, so a row's sum
-// does not depend on the other rows (the waves' accumulators are added later).
+// i of adapter a is share a + i's, whatever else the tile holds, so a row's sum
+// does not depend on the other rows (SHARES > 1: the waves that split the
+// reduction, whose accumulators are added later).
 // A row of another adapter holds zeros, which only cancel finite values: a
 // non-finite element of B is left out, and the result says so (nonfinite_part).
 // row_id: adapter of row m0 + lane.
-template <class Op, class T, int WAVES, int NW, int NT>
-__device__ __forceinline__ bool add_adapters(const AdapterArgs& a, int64_t m0, int rows, int n0, int row_id,
+template <class Op, class T, int SHARES, int NW, int NT>
+__device__ __forceinline__ bool add_adapters(const AdapterArgs& a, int64_t m0, int rows, int n0, int row_id, int share,
                                              f32x4_t (&acc)[NW][NT]) {
   constexpr int V = 16 / sizeof(T), K = 4 * V;  // elements of a lane, of a unit
-  const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6), r = lane & 15;
+  const int lane = threadIdx.x & 63, r = lane & 15;
   const int cols = min(16 * NW, a.N - n0), planes = a.planes, pitch = planes * a.r;
   const __amdgpu_buffer_rsrc_t rt = make_rsrc(reinterpret_cast<const T*>(a.t) + m0 * pitch, (uint32_t)(rows * pitch) * sizeof(T));
   bool left_out = false;
   uint64_t left = __ballot(lane < rows && (uint32_t)row_id < (uint32_t)a.P &&
-                           ((wave - row_id) & (WAVES - 1)) * K < a.r);  // rows of adapters with a unit of this wave
+                           ((share - row_id) & (SHARES - 1)) * K < a.r);  // rows of adapters with a unit of this share
   int id = 0, k0 = a.r;
-  auto next = [&]() {  // this wave's next unit: adapter id, ranks k0 ..
-    k0 += WAVES * K;
+  auto next = [&]() {  // the share's next unit: adapter id, ranks k0 ..
+    k0 += SHARES * K;
     while (k0 >= a.r) {
       if (!left) return false;
       id = __builtin_amdgcn_readlane(row_id, __ffsll((unsigned long long)left) - 1);
       left &= ~__ballot(row_id == id);
-      k0 = ((wave - id) & (WAVES - 1)) * K;
+      k0 = ((share - id) & (SHARES - 1)) * K;
     }
     return true;
   };
@@ -221,7 +222,7 @@ __global__ __launch_bounds__(64 * WAVES) void adapter_stream_kernel(AdapterArgs 
                                         lds + uniform(threadIdx.x >> 6) * stream_line_bytes<Op, NW, NT>(), acc);
   const bool direct = a.r <= kDirectRank;
   if (a.P > 0 && !direct) {
-    const bool bad = add_adapters<Op, T, WAVES, NW, NT>(a, m0, rows, n0, row_id, acc);
+    const bool bad = add_adapters<Op, T, WAVES, NW, NT>(a, m0, rows, n0, row_id, uniform(threadIdx.x >> 6), acc);
     if (lane == 0) left_out[threadIdx.x >> 6] = bad;
   }
   stream_reduce<WAVES, NW, NT, G, 1>(acc, reinterpret_cast<f32x4_t*>(lds), [&](int g, int j, const f32x4_t (&sum)[1]) {
@@ -242,6 +243,50 @@ __global__ __launch_bounds__(64 * WAVES) void adapter_stream_kernel(AdapterArgs 
     }
     adapter_store(a, m0 + i, n, v);
   });
+}
+
+// 16 NW WAVES columns of 64 rows: the waves split the columns and share the
+// token rows' lines, which halves what a 64 x 64 tile reads of them for an output
+// (1102 x 768 x 3020, rank 64: 25 us, 37 by the matrix-core tile; 3588 x 1216 x
+// 728, rank 16: 20 us, 32 by 64 x 64 tiles).  Bound by the L2 and the LDS.
+template <class Op, class T, int WAVES, int NW>
+__global__ __launch_bounds__(64 * WAVES) void adapter_wide_kernel(AdapterArgs a, int mb, int nb) {
+  constexpr int NT = 4;
+  __shared__ __attribute__((aligned(16))) char lds[stream_wide_bytes<Op, WAVES, NW, NT>()];
+  const int64_t v0 = xcd_tile((int64_t)mb * nb);
+  if (v0 < 0) return;
+  const int64_t m0 = v0 % mb * 16 * NT;
+  const int n0 = (int)(v0 / mb) * 16 * NW * WAVES;
+  const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
+  const int rows = (int)min((int64_t)16 * NT, a.M - m0);
+  StreamArgs s{};
+  s.row_bytes = a.row_bytes;
+  s.w0 = reinterpret_cast<const char*>(a.w) + (int64_t)n0 * a.row_bytes;
+  s.w_rows = min(16 * NW * WAVES, a.N - n0);
+  s.x = reinterpret_cast<const char*>(a.x) + m0 * a.row_bytes;
+  s.x_bytes = (uint32_t)rows * a.row_bytes;
+  s.lines = a.H / Op::kLine;
+  const int row_id = a.P > 0 ? a.idx[m0 + min(lane, rows - 1)] : -1;  // of row m0 + lane
+  f32x4_t acc[NW][NT];
+  stream_wide<Op, WAVES, NW, kOne, NT, 2, false>(
+      s, [&](int m) { return (uint32_t)min(m, rows - 1) * a.row_bytes; }, lds, acc);
+  const int nw = n0 + 16 * NW * wave;
+  if (nw >= a.N) return;
+  const bool bad = a.P > 0 && add_adapters<Op, T, 1, NW, NT>(a, m0, rows, nw, row_id, 0, acc);
+#pragma unroll
+  for (int j = 0; j < NT; ++j) {
+    const int i = 16 * j + (lane & 15), id = __shfl(row_id, i);
+#pragma unroll
+    for (int g = 0; g < NW; ++g) {
+      const int n = nw + 16 * g + 4 * (lane >> 4);
+      if (i >= rows || n >= a.N) continue;
+      f32x4_t v = acc[g][j];
+      if (bad && (uint32_t)id < (uint32_t)a.P) {
+        for (int c = 0; c < 4 && n + c < a.N; ++c) v[c] += nonfinite_part<T>(a, m0 + i, id, n + c);
+      }
+      adapter_store(a, m0 + i, n, v);
+    }
+  }
 }
 
 // At most 8 rows that use one adapter between them (one row, or one adapter),
@@ -338,28 +383,33 @@ static void launch_stream_as(const AdapterArgs& a, hipStream_t s) {
 // round being one tile per CU; the rule takes the least.  Fitted to 256 tiles
 // at H = 256, 1024 and 4096 (two and four rounds at 1024 for the small ones),
 // in us: bf16 stream tiles of 64 x 64, 32 x 32, 16 x 16 outputs 6.6 9.4 19,
-// 4.8 5.7 10, 3.7 4.0 6.5; matrix-core tiles of 128 x 256 and 256 x 256 (they
+// 4.8 5.7 10, 3.7 4.0 6.5, column-splitting ones of 64 x 256 9 17 47;
+// matrix-core tiles of 128 x 256 and 256 x 256 (they
 // keep more of the operands in LDS, but one of them alone on a CU waits longer
 // for its loads) 16 28 73, 28 46 123; f32 10 24 80, 6.4 9.8 23, 4.2 5.6 10.
-// Adapters lengthen the reduction by their planes: one adapter a stream tile, two
-// a matrix-core tile (in steps of 64, and it lists them: 3 us), are assumed;
-// the latter's stores of rows that are not whole 8-byte units take 8 us more.
+// With adapters: the stream tiles' reduction is longer by the planes (one
+// adapter a tile is assumed), the matrix-core tiles' by those of two adapters in
+// steps of 64, and a round takes `adapters` us and `part` us for 32 ranks of a
+// plane more; rows that are not whole 8-byte units take `odd` us more.
 struct TileKind {
   int rows, cols;
   float start, round, step;
+  float adapters = 0.0f, part = 0.0f, odd = 0.0f;
+  int assumed = 1, unit = 1;  // adapters; ranks that they take a multiple of
 };
+constexpr TileKind kWide{64, 256, 4.3f, 2.1f, 10.1f, 2.0f, 1.0f, 4.0f};
 constexpr TileKind kStream64{64, 64, 1.3f, 4.8f, 3.25f}, kStream32{32, 32, 3.2f, 1.1f, 1.4f},
-    kStream16{16, 16, 3.0f, 0.25f, 0.8f}, kGemm128{128, 256, 1.5f, 10.5f, 15.3f}, kGemm256{256, 256, 1.5f, 20.0f, 25.2f};
+    kStream16{16, 16, 3.0f, 0.25f, 0.8f}, kGemm128{128, 256, 1.5f, 10.5f, 15.3f, 3.0f, 0.0f, 8.0f, 2, kBK},
+    kGemm256{256, 256, 1.5f, 20.0f, 25.2f, 3.0f, 0.0f, 8.0f, 2, kBK};
 constexpr TileKind kStreamF64{64, 64, 1.3f, 3.9f, 18.5f}, kStreamF32{32, 32, 3.2f, 2.1f, 4.45f},
     kStreamF16{16, 16, 3.0f, 0.75f, 1.6f};
 
-static float tile_cost(const AdapterArgs& a, const TileKind& t) {
+static float tile_cost(const AdapterArgs& a, const TileKind& t, int planes) {
   const float tiles = (float)((a.M + t.rows - 1) / t.rows) * (float)((a.N + t.cols - 1) / t.cols);
-  const int part = a.planes * a.r;
-  const bool gemm = t.cols == 256;
-  const float round = t.round + (gemm ? (a.P > 0 ? 3.0f : 0.0f) + (a.N & 3 ? 8.0f : 0.0f) : 0.0f);
-  const int k = a.H + (gemm ? 2 * ((part + kBK - 1) / kBK * kBK) : part);
-  return t.start + ceilf(tiles / (float)device_cu_count()) * (round + t.step * (float)k / 1024.0f);
+  const int ranks = planes * a.r;  // (none without adapters)
+  const float more = (a.P > 0 ? t.adapters + t.part * (float)ranks / 32.0f : 0.0f) + (a.N & 3 ? t.odd : 0.0f);
+  const int k = a.H + t.assumed * ((ranks + t.unit - 1) / t.unit * t.unit);
+  return t.start + ceilf(tiles / (float)device_cu_count()) * (t.round + more + t.step * (float)k / 1024.0f);
 }
 
 // c16, c32, c64: the costs of the tiles.
@@ -401,17 +451,13 @@ hipError_t launch_adapter_linear(AdapterArgs a, bool f32, hipStream_t s) {
       launch_one<StreamBf16<1>, __bf16>(a, s);
     return hipGetLastError();
   }
-  float c16, c32, c64, g128 = 0.0f, g256 = 0.0f;
-  a.planes = f32 ? 1 : a.out.out_bf16 ? 2 : 3;
-  bool stream = true;
-  if (f32) {
-    c16 = tile_cost(a, kStreamF16), c32 = tile_cost(a, kStreamF32), c64 = tile_cost(a, kStreamF64);
-  } else {
-    c16 = tile_cost(a, kStream16), c32 = tile_cost(a, kStream32), c64 = tile_cost(a, kStream64);
-    g128 = tile_cost(a, kGemm128), g256 = tile_cost(a, kGemm256);
-    stream = a.H < 128 || fminf(c16, fminf(c32, c64)) <= fminf(g128, g256);
-  }
-  if (stream && a.r <= kDirectRank) a.planes = 1;  // t as f32 values
+  const int planes = f32 ? 1 : a.out.out_bf16 ? 2 : 3;
+  auto cost = [&](const TileKind& t) { return tile_cost(a, t, planes); };
+  const float c16 = cost(f32 ? kStreamF16 : kStream16), c32 = cost(f32 ? kStreamF32 : kStream32),
+              c64 = cost(f32 ? kStreamF64 : kStream64), stream = fminf(c16, fminf(c32, c64));
+  const float wide = cost(kWide), g128 = cost(kGemm128), g256 = cost(kGemm256);
+  const bool by_stream = f32 || stream <= fminf(wide, fminf(g128, g256));
+  a.planes = by_stream && a.r <= kDirectRank ? 1 : planes;
   if (a.P > 0) {
     if (f32)
       launch_shrink<StreamF32>(a, s);
@@ -422,8 +468,11 @@ hipError_t launch_adapter_linear(AdapterArgs a, bool f32, hipStream_t s) {
   }
   if (f32) {
     launch_stream<StreamF32, float>(a, c16, c32, c64, s);
-  } else if (stream) {
+  } else if (by_stream) {
     launch_stream<StreamBf16<1>, __bf16>(a, c16, c32, c64, s);
+  } else if (a.H < 128 || wide <= fminf(g128, g256)) {
+    const int mb = (int)((a.M + 63) / 64), nb = (a.N + 255) / 256;
+    adapter_wide_kernel<StreamBf16<1>, __bf16, 8, 2><<<tile_grid((int64_t)mb * nb), 512, 0, s>>>(a, mb, nb);
   } else {
     const int64_t rows = g256 < g128 ? 256 : 128, mt = (a.M + rows - 1) / rows, nt = (a.N + 255) / 256;
     const dim3 grid = tile_grid(mt * nt);

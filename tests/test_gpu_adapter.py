@@ -136,9 +136,13 @@ def test_few_rows_of_one_adapter(shape, dtype, out, residual):
         run_and_check(**shape, dtype=dtype, out=out, residual=residual, mix=mix, seed=14)
 
 
-# the matrix-core tiles, with rows at any address, residuals, many adapters a tile
+# the column-splitting and the matrix-core tiles, with rows at any address,
+# residuals, many adapters a tile
 @pytest.mark.parametrize("out,residual", [("f32", False), ("bf16", True), ("f32", True)])
-@pytest.mark.parametrize("shape", [dict(M=3000, H=320, N=2049, r=72, P=7, mix="runs"),
+@pytest.mark.parametrize("shape", [dict(M=700, H=256, N=3020, r=40, P=5, mix="runs"),
+                                   dict(M=900, H=64, N=3333, r=16, P=30, mix="rows"),
+                                   dict(M=641, H=192, N=4099, r=8, P=2, mix="distinct"),
+                                   dict(M=3000, H=320, N=2049, r=72, P=7, mix="runs"),
                                    dict(M=3001, H=320, N=2052, r=16, P=40, mix="rows"),
                                    dict(M=5004, H=192, N=1753, r=16, P=5, mix="runs"),
                                    dict(M=4100, H=128, N=1999, r=8, P=3, mix="one")])
@@ -156,6 +160,7 @@ def test_output_in_place_of_the_residual():
 
 @pytest.mark.parametrize("M,N,r,dtype", [(20, 72, 16, "bf16"), (300, 72, 16, "bf16"), (20, 72, 40, "bf16"),
                                          (300, 72, 40, "bf16"), (20, 72, 40, "f32"), (300, 72, 72, "f32"),
+                                         (700, 3001, 40, "bf16"), (900, 3020, 16, "bf16"),
                                          (3000, 2052, 40, "bf16"), (4000, 2049, 24, "bf16")])
 def test_nan_in_an_unused_adapter_and_in_a_row_stays_there(M, N, r, dtype):
     q, d, epi, out, ws, _ = make(M=M, H=128, N=N, r=r, P=6, mix="rows", dtype=dtype, seed=6)
