@@ -292,7 +292,7 @@ __global__ __launch_bounds__(64 * WAVES) void adapter_wide_kernel(AdapterArgs a,
 // At most 8 rows that use one adapter between them (one row, or one adapter),
 // 16 columns a block: the adapter's A streams past the rows as NA further
 // groups of 16 weight rows, so every block has t for itself and there is one
-// launch (one row, 2048 x 64, rank 8: 4.6 us instead of 3.8 + 4.0 in two; 4096 x
+// launch (one row, 2048 x 64, rank 8: 4.3 us instead of 3.8 + 4.0 in two; 4096 x
 // 4096, rank 16: 9.6 instead of 5.1 + 8.7, rank 64: 15 instead of 6.8 + 8.4).
 constexpr int kOneRows = 8;
 
@@ -346,8 +346,13 @@ static void launch_shrink_as(const AdapterArgs& a, unsigned slots, hipStream_t s
   adapter_shrink_kernel<Op, WAVES, NW, NT><<<grid, 64 * WAVES, 0, s>>>(a);
 }
 
-// Short batches: 16 waves for every adapter that 16 rows can have.  Long
-// ones: the largest tile that still gives a block for every CU (x is read
+// Short batches: a block of 8 waves for every adapter that 16 rows can have, or
+// 8 of them beyond 64 rows, where most would find none (with 4: 200 mixed rows
+// of 8 adapters 8.9 us instead of 5.5, 500 rows in runs, rank 64, 7.4 instead of
+// 11), and for every 16 ranks, or 32 beyond 64 rows (16 rows, H = 6528, rank
+// 32, f32: 13.5 us instead of 19; 500 rows: 13.5 instead of 10).  (16 waves a
+// block: 7.5 instead of 6.3 us at 48 rows, H = 4096, rank 16.)
+// Long ones: the largest tile that still gives a block for every CU (x is read
 // once per 16 NW of the rank, A once per 16 NT rows), whose adapters 4 blocks
 // share (1000 rows of 20 adapters, H = 4096, rank 16: 5.7 us instead of 8.7 by
 // one).
@@ -357,11 +362,13 @@ static void launch_shrink(const AdapterArgs& a, hipStream_t s) {
   auto blocks = [&](int nw, int nt) {
     return ((a.M + 16 * nt - 1) / (16 * nt)) * ((a.r + 16 * nw - 1) / (16 * nw));
   };
-  if (a.M <= 512) {
+  if (a.M <= 64) {
+    launch_shrink_as<Op, 8, 1, 1>(a, a.P < 16 ? a.P : 16, s);
+  } else if (a.M <= 512) {
     if (a.r <= 16)
-      launch_shrink_as<Op, 16, 1, 1>(a, 16, s);
+      launch_shrink_as<Op, 8, 1, 1>(a, a.P < 8 ? a.P : 8, s);
     else
-      launch_shrink_as<Op, 16, 2, 1>(a, 16, s);
+      launch_shrink_as<Op, 8, 2, 1>(a, a.P < 8 ? a.P : 8, s);
   } else if (a.r > 32 && blocks(4, 2) >= cus) {
     launch_shrink_as<Op, 8, 4, 2>(a, 4, s);
   } else if (a.r > 16 && blocks(2, 2) >= cus) {
