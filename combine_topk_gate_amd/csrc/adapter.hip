@@ -404,9 +404,9 @@ struct TileKind {
   float adapters = 0.0f, part = 0.0f, odd = 0.0f;
   int assumed = 1, unit = 1;  // adapters; ranks that they take a multiple of
 };
-constexpr TileKind kWide{64, 256, 4.3f, 2.1f, 10.1f, 2.0f, 1.0f, 4.0f};
+constexpr TileKind kWide{64, 256, 4.3f, 2.1f, 10.1f, 2.0f, 1.0f, 1.0f};
 constexpr TileKind kStream64{64, 64, 1.3f, 4.8f, 3.25f}, kStream32{32, 32, 3.2f, 1.1f, 1.4f},
-    kStream16{16, 16, 3.0f, 0.25f, 0.8f}, kGemm128{128, 256, 1.5f, 10.5f, 15.3f, 3.0f, 0.0f, 8.0f, 2, kBK},
+    kStream16{16, 16, 3.0f, 0.25f, 0.8f}, kGemm128{128, 256, 1.5f, 10.5f, 15.3f, 3.0f, 0.0f, 2.0f, 2, kBK},
     kGemm256{256, 256, 1.5f, 20.0f, 25.2f, 3.0f, 0.0f, 8.0f, 2, kBK};
 constexpr TileKind kStreamF64{64, 64, 1.3f, 3.9f, 18.5f}, kStreamF32{32, 32, 3.2f, 2.1f, 4.45f},
     kStreamF16{16, 16, 3.0f, 0.75f, 1.6f};
