@@ -6,10 +6,12 @@
 //
 // ("Grouped GEMM 为什么适合 MoE": many small products of different row
 // counts beside one large product; the row groups here are the requests of
-// one adapter.)  A first kernel computes t for every row, a second one the
-// projection with the adapters' part, the residual and the cast in its
-// epilogue, so out is written once and nothing of the size of out is read
-// back.
+// one adapter.)  At most 8 rows of one adapter are one launch.  Otherwise a
+// first kernel computes t for every row, a second one the projection, with the
+// adapters' part (t . B) added on the matrix cores or in the epilogue, the
+// residual and the cast, so out is written once and nothing of the size of out
+// is read back.  What bounds them: latency for a few rows, the L2 and the LDS for
+// hundreds, the matrix cores beyond (adapter_gemm.hpp).
 #include <math.h>
 
 #include "adapter_gemm.hpp"
