@@ -506,14 +506,26 @@ __global__ __launch_bounds__(kStreamThreads) void decode_few_l1_kernel(DecodeArg
   if (tid < p.M * 4) {
     const int t = tid >> 2, n = n0 + 4 * (tid & 3);
     float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int f = t * p.k; f < (t + 1) * p.k; ++f) {
-      const float w = p.w[f];
-      if (p.f2s[f] < 0) continue;
-      const f32x4_t y = get_y(a.y + (int64_t)f * a.H + n);
-      o.x = fmaf(w, y[0], o.x);
-      o.y = fmaf(w, y[1], o.y);
-      o.z = fmaf(w, y[2], o.z);
-      o.w = fmaf(w, y[3], o.w);
+    // 4 slots' loads in flight: each comes from beyond the L2
+    for (int f0 = t * p.k; f0 < (t + 1) * p.k; f0 += 4) {
+      f32x4_t y[4];
+      float w[4];
+      bool has[4];
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        const int f = min(f0 + u, (t + 1) * p.k - 1);
+        y[u] = get_y(a.y + (int64_t)f * a.H + n);  // (of a pair of no held expert: not used)
+        w[u] = p.w[f];
+        has[u] = f0 + u < (t + 1) * p.k && p.f2s[f] >= 0;
+      }
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        if (!has[u]) continue;
+        o.x = fmaf(w[u], y[u][0], o.x);
+        o.y = fmaf(w[u], y[u][1], o.y);
+        o.z = fmaf(w[u], y[u][2], o.z);
+        o.w = fmaf(w[u], y[u][3], o.w);
+      }
     }
     store_out(ep, (int64_t)t * a.H + n, o);
   }
@@ -528,10 +540,13 @@ static void launch_few(const DecodeArgs& a, const float* logits, const OutEpilog
   const int pairs = p.M * p.k;
   // one token's entries are its slots, held or not
   const int entries = p.M == 1 ? p.k : p.EL < pairs ? p.EL : pairs;
-  // Layer0: as many blocks as are resident at once (7 on a CU), each taking
-  // the same number of column groups: more of them would only route again (8
-  // tokens, 22 experts of 448 x 4992: 51 us instead of 73)
-  const int groups = a.F / 16, at_once = 7 * kCus, turns = (groups * entries + at_once - 1) / at_once;
+  // Layer0 of short rows: as many blocks as are resident at once (7 on a CU),
+  // each taking the same number of column groups; more of them would only route
+  // again (8 tokens, k = 8, 64 experts of 2048 x 1408: 84 us instead of 109; 22
+  // experts of 448 x 4992: 51 instead of 73).  Rows of more than 4 KiB hide the
+  // routing (8 tokens, 8 experts of 4096 x 14336: 276 us in turn, 263 not).
+  const int groups = a.F / 16, at_once = 7 * kCus;
+  const int turns = a.x_pitch > 4096 ? 1 : (groups * entries + at_once - 1) / at_once;
   const dim3 grid((unsigned)((groups + turns - 1) / turns), (unsigned)entries);
   if (p.k <= 2)
     decode_few_l0_kernel<Op0, 2, NP><<<grid, kStreamThreads, 0, s>>>(logits, a);
