@@ -38,9 +38,12 @@ __device__ __forceinline__ i32x4_t load_weight(__amdgpu_buffer_rsrc_t r, uint32_
 // f32 value as NP bf16 values whose sum is the value (NP = 3: exactly, but
 // for magnitudes below 2^-110; NP = 2: to 2^-16 of it).  An infinity or NaN is
 // its first plane alone; a finite value that would round to infinity is cut
-// off instead of rounded there.
+// off instead of rounded there.  (No contraction: where v is a product, the
+// compiler made v - f an fma of the unrounded one in some copies of the code and
+// not in others, so that a row's bits depended on its place in a tile.)
 template <int NP>
 __device__ __forceinline__ void split_bf16(float v, __bf16 (&p)[NP]) {
+#pragma clang fp contract(off)
   p[0] = (__bf16)v;
   float f = (float)p[0];
   if (__builtin_isinf(f)) {

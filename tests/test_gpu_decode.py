@@ -342,3 +342,17 @@ def test_weights_past_32_bit_offsets():
     moe.moe_layer_decode(p, x, lg, *w, None, out, ws)
     y, bound = ref.layer(x, lg, w[0], w[1], w[2], 2, 0, None, False, False)
     ref.check(out, y, bound, "large weights")
+
+
+@pytest.mark.parametrize("dtype,out", [("bf16", "f32"), ("bf16", "bf16"), ("bf16_mxfp8", "f32"), ("f32", "f32")])
+@pytest.mark.parametrize("shape", [dict(M=100, H=128, F=1408, E=3, k=2), dict(M=255, H=64, F=1408, E=3, k=2),
+                                   dict(M=256, H=320, F=1024, E=4, k=4), dict(M=200, H=1024, F=2048, E=8, k=2)])
+def test_same_bits_whichever_place_a_row_gets(shape, dtype, out):
+    # entries of 64 and 128 rows, whose places, and an expert's two entries, are dealt by atomics
+    p, d, epi, o, ws, _ = make(**shape, dtype=dtype, out=out, residual=True, seed=15)
+    call(p, d, epi, o, ws)
+    first = o.clone()
+    for _ in range(12):
+        o.zero_()
+        call(p, d, epi, o, ws)
+        assert torch.equal(o, first)
