@@ -274,6 +274,7 @@ __device__ __forceinline__ void decode_l1_tile(const DecodeArgs& a, int4 ent, ch
   stream_wide<Op, WAVES, NW, kOne, NT, kDepth, true>(
       s, [&](int i) { return decode_row(a.plan, ent, i, 1, a.h_pitch); }, lds, acc);
   const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
+  bool nan = false;
 #pragma unroll
   for (int j = 0; j < NT; ++j) {
     const int i = 16 * j + (lane & 15);
@@ -283,6 +284,23 @@ __device__ __forceinline__ void decode_l1_tile(const DecodeArgs& a, int4 ent, ch
     for (int g = 0; g < NW; ++g) {
       const int n = n0 + 16 * (wave * NW + g) + 4 * (lane >> 4);
       if (n < a.H) *reinterpret_cast<f32x4_t*>(y + pair * a.H + n) = acc[g][j];
+#pragma unroll
+      for (int c = 0; c < 4; ++c) nan |= n < a.H && __builtin_isnan(acc[g][j][c]);
+    }
+  }
+  if constexpr (Op::kP > 1) {
+    if (__any(nan)) {  // (after the stores, so that the usual path keeps its registers)
+#pragma unroll 1
+      for (int j = 0; j < NT * NW; ++j) {
+        const int i = 16 * (j / NW) + (lane & 15), row = 16 * (wave * NW + j % NW) + 4 * (lane >> 4);
+        const bool live = i < ent.z && n0 + row < a.H;
+        const int64_t pair = live ? a.plan.list[ent.y + i] : 0;
+        f32x4_t* at = reinterpret_cast<f32x4_t*>(y + pair * a.H + n0 + row);
+        f32x4_t v = {0.f, 0.f, 0.f, 0.f};
+        if (live) v = *at;
+        stream_resum<Op>(s, row, (uint32_t)pair * a.h_pitch, live, v);
+        if (live) *at = v;
+      }
     }
   }
 }
@@ -490,7 +508,10 @@ __global__ __launch_bounds__(kStreamThreads) void decode_few_l1_kernel(DecodeArg
         s, wave, kStreamWaves, [&](int i) { return i < rows ? (uint32_t)(i == lane >> 3 ? row_pair : ent->pair[i]) * a.h_pitch : kNoRow; },
         lds + wave * kLine, acc);
     stream_reduce<kStreamWaves, 1, 1, 1, 1>(acc, reinterpret_cast<f32x4_t*>(lds), [&](int, int, const f32x4_t (&y)[1]) {
-      if ((lane & 15) < rows) put_y(a.y + (int64_t)out_pair * a.H + n0 + 4 * (lane >> 4), y[0]);
+      f32x4_t v = y[0];
+      const bool live = (lane & 15) < rows;
+      stream_resum<Op>(s, 4 * (lane >> 4), (uint32_t)out_pair * a.h_pitch, live, v);
+      if (live) put_y(a.y + (int64_t)out_pair * a.H + n0 + 4 * (lane >> 4), v);
     });
   }
   // wave 0 has stored the block's rows: it waits until they are at the point

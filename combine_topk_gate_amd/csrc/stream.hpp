@@ -68,6 +68,10 @@ template <int NP>
 struct StreamBf16 {
   static constexpr int kLine = 64, kP = NP, kXC = 8;
   static constexpr bool kMx = false;
+  // element k of a weight row
+  static __device__ __forceinline__ float weight(const char* row, const uint8_t*, int k) {
+    return (float)reinterpret_cast<const __bf16*>(row)[k];
+  }
   // x chunks that go with half h: one per plane
   static constexpr int kXH = 1;
   static __device__ __forceinline__ int x_chunk(int h, int q, int) { return 4 * h + q; }
@@ -108,6 +112,12 @@ template <int NP>
 struct StreamMx {
   static constexpr int kLine = 128, kP = NP, kXC = 16;
   static constexpr bool kMx = true;
+  // scale: the row's bytes of the first line (those of the next: 128 bytes on)
+  static __device__ __forceinline__ float weight(const char* row, const uint8_t* scale, int k) {
+    const int s = scale[k / 128 * 128 + k / 32 % 4];
+    const float v = __builtin_amdgcn_cvt_f32_fp8((uint8_t)row[k], 0);
+    return s == 255 ? __builtin_nanf("") : ldexpf(v, s - 127);
+  }
   static constexpr int kXH = 2;
   static __device__ __forceinline__ int x_chunk(int h, int q, int s) { return 2 * (4 * h + q) + s; }
   template <int NT>
@@ -430,6 +440,53 @@ __device__ __forceinline__ void stream_wide(const StreamArgs& a, RowOff row_off,
         }
       }
       __builtin_amdgcn_sched_barrier(0);
+    }
+  }
+}
+
+// The planes of a token value are multiplied one by one, and where a weight is
+// infinite, or a product past the range, they give NaN (inf * 0, inf - inf)
+// for what is an infinity: a plane may be zero or of the other sign.  No sum
+// that is not NaN is wrong in this way (its infinities have one sign, that of
+// the first planes').  So a NaN is summed again from the whole values, in f32,
+// by the wave, until each is known to be one (a NaN among the values or
+// weights ends it at once).
+//   v: the lane's sums of weight rows row .. row + 3 of a.w0 (kOne) and the
+// token row at byte x_off; live: they are used.  The whole wave calls it, for
+// the tile's lines line0 .. line0 + lines - 1.
+template <class Op>
+__device__ __forceinline__ void stream_resum(const StreamArgs& a, int row, uint32_t x_off, bool live, f32x4_t& v) {
+  if constexpr (Op::kP > 1) {
+    int nan = 0;  // bit c: v[c]
+#pragma unroll
+    for (int c = 0; c < 4; ++c) nan |= __builtin_isnan(v[c]) ? 1 << c : 0;
+    const int lane = threadIdx.x & 63;
+    const int k0 = a.line0 * Op::kLine, k1 = k0 + a.lines * Op::kLine;
+#pragma unroll 1
+    for (uint64_t left = __ballot(live && nan); left; left &= left - 1) {
+      const int src = __ffsll((unsigned long long)left) - 1, r0 = __builtin_amdgcn_readlane(row, src);
+      const char* x = reinterpret_cast<const char*>(a.x) + (uint32_t)__builtin_amdgcn_readlane((int)x_off, src);
+      const char* w = reinterpret_cast<const char*>(a.w0) + (int64_t)r0 * a.row_bytes;
+      const int sr = a.scale_row + r0;
+      const uint8_t* scale = Op::kMx ? a.scale + (int64_t)(sr >> 5) * a.scale_pitch + 4 * (sr & 31) : nullptr;
+      f32x4_t s = {0.f, 0.f, 0.f, 0.f};
+      int open = __builtin_amdgcn_readlane(nan, src);  // the sums that may yet be infinite
+#pragma unroll 1
+      for (int k = k0 + lane; k < k1 && open; k += 64) {  // (lines are whole 64s: the waves' lanes stay together)
+        float h = 0.0f;
+#pragma unroll
+        for (int p = Op::kP - 1; p >= 0; --p) h += (float)reinterpret_cast<const __bf16*>(x + p * (int64_t)a.plane)[k];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          s[c] = fmaf(Op::weight(w + c * (int64_t)a.row_bytes, scale + 4 * c, k), h, s[c]);
+          if (__any(__builtin_isnan(s[c]))) open &= ~(1 << c);
+        }
+      }
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        for (int off = 1; off < 64; off <<= 1) s[c] += __shfl_xor(s[c], off);
+        if (lane == src && (open >> c & 1)) v[c] = s[c];
+      }
     }
   }
 }

@@ -393,7 +393,8 @@ moe_status_t moe_layer_ex(const moe_problem_t* p, const void* x, const float* lo
  *   - the activation between the products is kept in f32 (to 2^-16 when the
  *     output is bf16), not rounded to the dtype.  MOE_DTYPE_BF16_MXFP8 takes
  *     W_down in MXFP8 as moe_layer does, and its activation is not quantised
- *     (the products are bound by reading the weights);
+ *     (the products are bound by reading the weights).  Infinities and NaN
+ *     of the weights and of the activation act as in f32 products;
  *   - num_src_blocks has no effect on the result: there are no segments, and
  *     no src_block argument.
  *   x [M,H] dtype; logits [M,E] f32 (finite or -inf); w_gate, w_up [EL,F,H];

@@ -356,3 +356,71 @@ def test_same_bits_whichever_place_a_row_gets(shape, dtype, out):
         o.zero_()
         call(p, d, epi, o, ws)
         assert torch.equal(o, first)
+
+
+# both few-token kernels, entries of 16 to 128 rows, the reduction in parts
+NONFINITE = [dict(M=1, H=128, F=192, E=4, k=2), dict(M=6, H=128, F=192, E=6, k=2), dict(M=12, H=128, F=2560, E=4, k=2),
+             dict(M=30, H=192, F=320, E=5, k=3), dict(M=60, H=192, F=1408, E=3, k=2), dict(M=100, H=128, F=1408, E=3, k=2),
+             dict(M=255, H=64, F=1408, E=3, k=2)]
+
+
+@pytest.mark.parametrize("dtype,out", [("bf16", "f32"), ("bf16", "bf16"), ("f32", "f32")])
+@pytest.mark.parametrize("shape", NONFINITE)
+def test_infinite_down_weights(shape, dtype, out):
+    # an infinity of W_down makes its column infinite, with the sign of the activation; the rest keeps its bits
+    p, d, epi, o, ws, _ = make(**shape, dtype=dtype, out=out, residual=True, seed=15)
+    call(p, d, epi, o, ws)
+    clean = o.clone()
+    e = int(d["logits"][0].argmax())
+    d["w_down"][e, 9, 5] = float("inf")
+    d["w_down"][e, 40, p.ffn - 1] = float("-inf")
+    y, _ = want(p, d, dtype, out)
+    y = y.float()
+    assert not bool(torch.isnan(y).any()) and bool(torch.isinf(y[0, [9, 40]]).all())
+    o.fill_(0.0)
+    call(p, d, epi, o, ws)
+    there = torch.isinf(y)
+    assert torch.equal(o.float()[there], y[there])
+    assert torch.equal(o[~there], clean[~there])
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("M", [1, 12, 60])
+def test_an_infinite_weight_and_short_activations(M, dtype):
+    # h = silu(64) * 2 = 128, one plane; 0 * inf is NaN, an infinity of each sign too
+    p, d, epi, o, ws, _ = make(M, 64, 128, 1, 1, dtype=dtype, seed=16)
+    for k in ("x", "w_gate", "w_up", "w_down"):
+        d[k].zero_()
+    d["x"][:, 0] = 1.0
+    d["w_gate"][0, :2, 0], d["w_up"][0, 0, 0], d["w_up"][0, 1, 0] = 64.0, 2.0, -1.0
+    d["w_down"][0, 3, 0] = d["w_down"][0, 4, 1] = d["w_down"][0, 5, 7] = float("inf")
+    d["w_down"][0, 6, :2] = float("inf")
+    d["w_down"][0, 7, 0], d["w_down"][0, 7, 1] = float("inf"), float("-inf")
+    d["w_down"][0, 8, 2] = float("nan")
+    call(p, d, epi, o, ws)
+    assert bool((o[:, [3, 7]] == float("inf")).all()) and bool((o[:, 4] == float("-inf")).all())
+    assert bool(torch.isnan(o[:, [5, 6, 8]]).all())
+    assert not bool(o[:, :3].any()) and not bool(o[:, 9:].any())
+
+
+@pytest.mark.parametrize("dtype,out", [("bf16", "f32"), ("bf16", "bf16"), ("bf16_mxfp8", "f32"), ("f32", "f32")])
+@pytest.mark.parametrize("M", [1, 12, 60])
+def test_a_product_past_the_range_is_infinite(M, dtype, out):
+    # h = 16383 2^27 takes two planes of opposite sign (2^41, -2^27); times 2^110 each is past the range
+    H, F = 64, 128
+    p, d, epi, o, ws, _ = make(M, H, F, 1, 1, dtype=dtype, out=out, seed=17)
+    for k in ("x", "w_gate", "w_up"):
+        d[k].zero_()
+    d["x"][:, 0] = 1.0
+    d["w_gate"][0, 0, 0], d["w_up"][0, 0, 0] = 127 / 64 * 2.0 ** 20, 129 / 128 * 2.0 ** 20
+    w = torch.zeros((H, F), device=DEV)
+    w[3, 0], w[4, 0], w[5, 0] = 2.0 ** 110, -2.0 ** 110, 2.0 ** 80
+    if dtype == "bf16_mxfp8":
+        d["w_down"], _ = ref.quantize_mxfp8(w)
+    else:
+        d["w_down"][0] = w.to(d["w_down"].dtype)
+    call(p, d, epi, o, ws)
+    assert bool((o[:, 3] == float("inf")).all()) and bool((o[:, 4] == float("-inf")).all())
+    h = 127 / 64 * 129 / 128 * 2.0 ** 40
+    err = (o[:, 5].double() / (h * 2.0 ** 80) - 1).abs().max()
+    assert float(err) <= 8 * ref.U + (ref.BF16 * ref.BF16 + ref.BF16 if out == "bf16" else 0), float(err)
