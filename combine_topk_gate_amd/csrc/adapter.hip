@@ -125,7 +125,7 @@ __device__ __forceinline__ void add_adapter(const AdapterArgs& a, const float* t
 // does not depend on the other rows (SHARES > 1: the waves that split the
 // reduction, whose accumulators are added later).
 // A row of another adapter holds zeros, which only cancel finite values: a
-// non-finite element of B is left out, and the result says so (nonfinite_part).
+// non-finite element of B is left out, and the result says so (mend_sum).
 // row_id: adapter of row m0 + lane.
 template <class Op, class T, int SHARES, int NW, int NT>
 __device__ __forceinline__ bool add_adapters(const AdapterArgs& a, int64_t m0, int rows, int n0, int row_id, int share,
@@ -239,9 +239,7 @@ __global__ __launch_bounds__(64 * WAVES) void adapter_stream_kernel(AdapterArgs 
       bool bad = false;
 #pragma unroll
       for (int w = 0; w < WAVES; ++w) bad |= left_out[w] != 0;
-      if (bad && (uint32_t)id < (uint32_t)a.P) {
-        for (int c = 0; c < 4 && n + c < a.N; ++c) v[c] += nonfinite_part<T>(a, m0 + i, id, n + c);
-      }
+      mend_sums<T>(a, m0 + i, id, n, bad, v);
     }
     adapter_store(a, m0 + i, n, v);
   });
@@ -283,9 +281,7 @@ __global__ __launch_bounds__(64 * WAVES) void adapter_wide_kernel(AdapterArgs a,
       const int n = nw + 16 * g + 4 * (lane >> 4);
       if (i >= rows || n >= a.N) continue;
       f32x4_t v = acc[g][j];
-      if (bad && (uint32_t)id < (uint32_t)a.P) {
-        for (int c = 0; c < 4 && n + c < a.N; ++c) v[c] += nonfinite_part<T>(a, m0 + i, id, n + c);
-      }
+      mend_sums<T>(a, m0 + i, id, n, bad, v);
       adapter_store(a, m0 + i, n, v);
     }
   }

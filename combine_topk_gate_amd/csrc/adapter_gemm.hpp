@@ -14,7 +14,8 @@
 // change, so the loop is one and the same.
 // Zeros only cancel finite values, so an element of B that is infinite or NaN
 // is left out of the product (staged as zero) and added in the epilogue, to
-// the rows of its adapter alone.
+// the rows of its adapter alone; rows where that, or t's planes, may have made a
+// NaN of an infinity are formed again there (mend_sum).
 #pragma once
 
 #include "gemm_bf16.hpp"
@@ -157,21 +158,58 @@ __device__ __forceinline__ bool drop_nonfinite(i32x4_t& v) {
   return any != 0;
 }
 
-// What the elements of B that a tile left out add to out[m, n] (t in p.planes
-// parts).
+// Value j of t[m] (p.planes parts).
+template <class T>
+__device__ __forceinline__ float t_value(const AdapterArgs& p, int64_t m, int j) {
+  const T* t = reinterpret_cast<const T*>(p.t) + m * p.planes * p.r + j;
+  float v = 0.0f;
+  for (int q = p.planes - 1; q >= 0; --q) v += (float)t[q * p.r];
+  return v;
+}
+
+// What the elements of B that a tile left out add to out[m, n].
 template <class T>
 __device__ __forceinline__ float nonfinite_part(const AdapterArgs& p, int64_t m, int id, int n) {
   const T* b = reinterpret_cast<const T*>(p.b) + ((int64_t)id * p.N + n) * p.r;
-  const T* t = reinterpret_cast<const T*>(p.t) + m * p.planes * p.r;
   float s = 0.0f;
   for (int j = 0; j < p.r; ++j) {
     const float v = (float)b[j];
     if (__builtin_isfinite(v)) continue;
-    float tv = 0.0f;
-    for (int q = p.planes - 1; q >= 0; --q) tv += (float)t[q * p.r + j];
-    s += tv * v;
+    s += t_value<T>(p, m, j) * v;
   }
   return s;
+}
+
+// A tile's sum v for out[m, n] (before the residual) of a row with adapter id,
+// with what the tile left out of it.  A NaN may stand for an infinity: an
+// infinite t times the zero of an element left out, or products of t's planes
+// past the range with opposite signs.  Then t . B is formed again from whole
+// values, and, if that is infinite, x . W as well.
+template <class T>
+__device__ __forceinline__ float mend_sum(const AdapterArgs& p, int64_t m, int id, int n, bool left_out, float v) {
+  if (left_out) v += nonfinite_part<T>(p, m, id, n);
+  if (!__builtin_isnan(v)) return v;
+  const T* b = reinterpret_cast<const T*>(p.b) + ((int64_t)id * p.N + n) * p.r;
+  float tb = 0.0f;
+#pragma unroll 1
+  for (int j = 0; j < p.r; ++j) tb = fmaf(t_value<T>(p, m, j), (float)b[j], tb);
+  if (!__builtin_isinf(tb)) return v;
+  const T* x = reinterpret_cast<const T*>(p.x) + m * p.H;
+  const T* w = reinterpret_cast<const T*>(p.w) + (int64_t)n * p.H;
+  float xw = 0.0f;
+#pragma unroll 1
+  for (int h = 0; h < p.H; ++h) xw = fmaf((float)x[h], (float)w[h], xw);
+  return xw + tb;
+}
+
+// The same for 4 columns n .. n + 3 (those below N).
+template <class T>
+__device__ __forceinline__ void mend_sums(const AdapterArgs& p, int64_t m, int id, int n, bool left_out, f32x4_t& v) {
+  const bool nan = __builtin_isnan(v[0]) | __builtin_isnan(v[1]) | __builtin_isnan(v[2]) | __builtin_isnan(v[3]);
+  if ((!left_out && !nan) || (uint32_t)id >= (uint32_t)p.P) return;
+#pragma unroll
+  for (int c = 0; c < 4; ++c)
+    if (n + c < p.N) v[c] = mend_sum<T>(p, m, id, n + c, left_out, v[c]);
 }
 
 template <int TM>
@@ -405,7 +443,7 @@ __device__ __forceinline__ void adapter_gemm_tile(const AdapterArgs& p, int64_t 
   // of them before the staging (loaded row by row it cost 67 us of 279 at
   // 8192 x 4096 x 4096).  (8 columns per thread, i.e. wider stores but two
   // lanes per LDS bank, took 7 us more per tile.)
-  const bool fixup = ext > 0 && uniform(tl.nonfinite) != 0;
+  const bool left_out = ext > 0 && uniform(tl.nonfinite) != 0;
   const int c = tid & 63, n = n0 + 4 * c, wv = uniform(wave);
   const bool whole = n + 4 <= p.N;  // all of the thread's columns exist
   const bool pre = p.out.residual && whole;
@@ -441,12 +479,28 @@ __device__ __forceinline__ void adapter_gemm_tile(const AdapterArgs& p, int64_t 
       const int ts = wv + 4 * i;
       return reinterpret_cast<f32x4_t*>(lds + ts * 1024 + ((c ^ (ts & 15)) << 4));
     };
-    if (fixup) {
+    // Whether a sum of the thread's is not finite: a pass of its own over the
+    // staged sums (1.7 us of 267 at 8192 x 4096 x 4096; looked at before the
+    // staging, or kept in registers for the stores, the sums spill).
+    if (ext > 0) {
+      float bad = 0.0f;  // NaN once one is not
+#pragma unroll 8
       for (int i = 0; i < 32; ++i) {
-        const int row = tile_row(i);
-        if (row >= rows || tl.id[row] < 0) continue;
-        for (int e = 0; e < 4 && n + e < p.N; ++e)
-          (*staged(i))[e] += nonfinite_part<__bf16>(p, m0 + row, tl.id[row], n + e);
+        const f32x4_t v = *staged(i);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) bad = fmaf(v[e], 0.0f, bad);
+      }
+      if (left_out || __builtin_isnan(bad)) {
+#pragma unroll 1
+        for (int i = 0; i < 32; ++i) {
+          const int row = tile_row(i);
+          if (row >= rows || tl.id[row] < 0) continue;
+#pragma unroll 1
+          for (int e = 0; e < 4 && n + e < p.N; ++e) {
+            float* at = reinterpret_cast<float*>(staged(i)) + e;
+            *at = mend_sum<__bf16>(p, m0 + row, tl.id[row], n + e, left_out, *at);
+          }
+        }
       }
     }
 #pragma unroll

@@ -314,3 +314,56 @@ def test_a_decode_step_of_both_operators(M):
     ref.check(y, y64, by, "layer")
     o64, bo = want(do, "bf16", "f32")
     ref.check(out, o64, bo, "projection")
+
+
+# the tiles of 16, 32 and 64 rows, the column-splitting one, both matrix-core ones
+OVER = [(20, 128, 72, 24, "bf16"), (20, 128, 72, 40, "f32"), (333, 2048, 1408, 32, "bf16"), (1000, 128, 516, 40, "f32"),
+        (2048, 64, 516, 64, "bf16"), (700, 128, 3001, 40, "bf16"), (2100, 320, 2049, 72, "bf16"),
+        (8191, 1024, 2048, 24, "bf16")]
+
+
+@pytest.mark.parametrize("out", ["f32", "bf16"])
+@pytest.mark.parametrize("M,H,N,r,dtype", OVER)
+def test_values_past_the_range_of_a_row_and_its_adapter(M, H, N, r, dtype, out):
+    # one value of t is infinite (1e30 * 1e30) in two rows; B has infinities of both signs in its column, and
+    # products past the range without any; the rows beside them keep their bits
+    q, d, epi, o, ws, _ = make(M=M, H=H, N=N, r=r, P=3, mix="rows", dtype=dtype, out=out, residual=True, seed=15)
+    rows = torch.tensor([3, M - 2], device=DEV)
+    d["idx"][rows] = 1
+    d["w"][:, 7] = 0
+    d["a"][:, :, 7] = 0
+    d["a"][1, 4, 7] = 1e30
+    d["x"][:, 7] = 0
+    d["scale"][1] = 1.0
+    d["b"][1, :, 4] = d["b"][1, :, 4].abs() + 0.5
+    call(q, d, epi, o, ws)
+    clean = o.clone()
+    d["x"][rows, 7] = 1e30
+    d["b"][1, 5, 4], d["b"][1, N - 1, 4], d["b"][1, 6, 4] = float("inf"), float("-inf"), -1.0
+    d["b"][1, 8, 4], d["b"][1, 8, 0] = float("inf"), float("nan")
+    call(q, d, epi, o, ws)
+    got = o[rows].float()
+    sign = torch.ones(N, device=DEV)
+    sign[6] = sign[N - 1] = -1
+    keep = torch.ones(N, dtype=torch.bool, device=DEV)
+    keep[8] = False
+    assert torch.equal(got[:, keep], (sign * float("inf"))[keep].expand(2, -1)), got
+    assert bool(torch.isnan(got[:, 8]).all())
+    same = torch.ones((M, N), dtype=torch.bool, device=DEV)
+    same[rows] = False
+    one = d["idx"] == 1
+    one[rows] = False
+    for n in (5, 6, 8, N - 1):
+        same[one, n] = False
+    assert torch.equal(o[same], clean[same])
+    # the other rows of that adapter: t is finite there
+    t4 = d["x"].double()[one] @ d["a"][1, 4].double()
+    assert torch.equal(o[one, 5].float(), (torch.sign(t4) * float("inf")).float())
+    assert torch.equal(o[one, N - 1].float(), (torch.sign(t4) * float("-inf")).float())
+    # t = 16383 2^27, in planes 2^41 and -2^27: each times 2^110 is past the range
+    d["x"][rows, 7], d["a"][1, 4, 7] = 127 / 64 * 2.0 ** 20, 129 / 128 * 2.0 ** 20
+    d["b"][1, 5, 4], d["b"][1, N - 1, 4] = 2.0 ** 110, -2.0 ** 110
+    call(q, d, epi, o, ws)
+    got = o[rows].float()
+    assert bool((got[:, 5] == float("inf")).all()) and bool((got[:, N - 1] == float("-inf")).all()), got[:, [5, N - 1]]
+    assert bool(torch.isfinite(got[:, :5]).all())
