@@ -67,6 +67,7 @@ class AdapterProblem(ctypes.Structure):
 
 class Epilogue(ctypes.Structure):
     _fields_ = [("residual", ctypes.c_void_p), ("out_dtype", ctypes.c_int32)]
+    tensor = None  # the residual's tensor, where epilogue() was given one
 
 
 class LayerAux(ctypes.Structure):
@@ -151,8 +152,11 @@ def adapter_problem(M, H, N, rank, num_adapters, dtype="bf16") -> AdapterProblem
 
 
 def epilogue(residual=None, out_dtype="f32") -> Epilogue:
-    """The combine's output epilogue: out = cast(acc + residual)."""
-    return Epilogue(None if residual is None else residual.data_ptr(), _DTYPES[out_dtype])
+    """The combine's output epilogue: out = cast(acc + residual).  It holds the
+    residual's tensor."""
+    epi = Epilogue(None if residual is None else residual.data_ptr(), _DTYPES[out_dtype])
+    epi.tensor = residual
+    return epi
 
 
 def _ptr(t):
@@ -294,6 +298,17 @@ def _addr(what, name, t, dtype, shape, gpu):
     _refuse(what, name, t, dtype, shape)
 
 
+def _epilogue(what, epi, dtype, shape, gpu):
+    """The epilogue for the library; its residual is checked as the other
+    tensors are (one given as a bare address is the caller's word)."""
+    if epi is None:
+        return None
+    if epi.tensor is not None and epi.residual:
+        if _addr(what, "residual", epi.tensor, dtype, shape, gpu) != epi.residual:
+            raise MoeError(MOE_ERR_INVALID_ARGUMENT, f"{what}: the residual has moved since its epilogue was made")
+    return ctypes.byref(epi)
+
+
 def _workspace(what, ws, gpu):
     """(pointer, bytes) of a workspace: any contiguous tensor on the GPU."""
     if ws is None:
@@ -337,7 +352,7 @@ def moe_layer_decode(p, x, logits, w_gate, w_up, w_down, epi, out, ws, stream=No
                     _addr(what, "x", x, act, (M, H), gpu), _addr(what, "logits", logits, f32, (M, E), gpu),
                     _addr(what, "w_gate", w_gate, act, (EL, F, H), gpu),
                     _addr(what, "w_up", w_up, act, (EL, F, H), gpu), down,
-                    None if epi is None else ctypes.byref(epi), _addr(what, "out", out, odt, (M, H), gpu),
+                    _epilogue(what, epi, act, (M, H), gpu), _addr(what, "out", out, odt, (M, H), gpu),
                     *_workspace(what, ws, gpu)), what)
 
 
@@ -363,7 +378,7 @@ def moe_adapter_linear(q, x, w, a, b, scale, adapter_idx, epi, out, ws, stream=N
                     _addr(what, "a", a, act, (P, r, H), gpu), _addr(what, "b", b, act, (P, N, r), gpu),
                     _addr(what, "scale", scale, f32, (P,), gpu),
                     _addr(what, "adapter_idx", adapter_idx, torch.int32, (M,), gpu),
-                    None if epi is None else ctypes.byref(epi), _addr(what, "out", out, odt, (M, N), gpu),
+                    _epilogue(what, epi, act, (M, N), gpu), _addr(what, "out", out, odt, (M, N), gpu),
                     *_workspace(what, ws, gpu)), what)
 
 

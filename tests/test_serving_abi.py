@@ -204,3 +204,93 @@ def test_reference_quantiser_matches_its_values():
     err = (v.view(64, 8, 32) - w.double().view(64, 8, 32)).abs()
     bound = torch.maximum(torch.maximum(2.0 ** -4 * a, 2.0 ** -10 * S), a - 448 * S)
     assert bool((err <= bound).all())
+
+
+class OnGpu(torch.Tensor):
+    """A host tensor that says it is on GPU 0: what the binding looks at."""
+
+    def get_device(self):
+        return 0
+
+
+def on_gpu(*shape, dtype=torch.bfloat16):
+    return torch.zeros(shape, dtype=dtype).as_subclass(OnGpu)
+
+
+def binding_calls():
+    """name -> (call, its tensors by name): calls that the binding passes on."""
+    f32 = torch.float32
+    p = moe.problem(4, 64, 128, 8, 2)
+    q = moe.adapter_problem(4, 64, 16, 8, 3)
+
+    def decode(x, logits, w_gate, w_up, w_down, residual, out, ws):
+        moe.moe_layer_decode(p, x, logits, w_gate, w_up, w_down, moe.epilogue(residual, "bf16"), out, ws, stream=0)
+
+    def linear(x, w, a, b, scale, adapter_idx, residual, out, ws):
+        moe.moe_adapter_linear(q, x, w, a, b, scale, adapter_idx, moe.epilogue(residual, "bf16"), out, ws, stream=0)
+
+    return {
+        "decode": (decode, dict(x=on_gpu(4, 64), logits=on_gpu(4, 8, dtype=f32), w_gate=on_gpu(8, 128, 64),
+                                w_up=on_gpu(8, 128, 64), w_down=on_gpu(8, 64, 128), residual=on_gpu(4, 64),
+                                out=on_gpu(4, 64), ws=on_gpu(1 << 20, dtype=torch.uint8))),
+        "linear": (linear, dict(x=on_gpu(4, 64), w=on_gpu(16, 64), a=on_gpu(3, 8, 64), b=on_gpu(3, 16, 8),
+                                scale=on_gpu(3, dtype=f32), adapter_idx=on_gpu(4, dtype=torch.int32),
+                                residual=on_gpu(4, 16), out=on_gpu(4, 16), ws=on_gpu(1 << 20, dtype=torch.uint8))),
+    }
+
+
+BINDING_TENSORS = [("decode", n) for n in ("x", "logits", "w_gate", "w_up", "w_down", "residual", "out", "ws")] + \
+                  [("linear", n) for n in ("x", "w", "a", "b", "scale", "adapter_idx", "residual", "out", "ws")]
+
+
+@pytest.fixture
+def passed_on(lib, monkeypatch):
+    """The calls that the binding has passed on to the library (which is not called)."""
+    calls = []
+    monkeypatch.setattr(moe, "_call_on", lambda gpu, stream, f, *args: calls.append(args) or moe.MOE_OK)
+    return calls
+
+
+@pytest.mark.parametrize("which,name", BINDING_TENSORS)
+def test_binding_checks_each_tensor(which, name, passed_on):
+    """Right but for one tensor's type, shape, strides or device."""
+    call, t = binding_calls()[which]
+    call(**t)
+    assert len(passed_on) == 1
+    good = t[name]
+    wide = torch.zeros(good.shape[:-1] + (2 * good.shape[-1],), dtype=good.dtype).as_subclass(OnGpu)
+    bad = {"strides": wide[..., ::2], "device": good.as_subclass(torch.Tensor)}
+    if name != "ws":
+        bad["type"] = good.to(torch.float16)
+        bad["shape"] = torch.cat([good, good]).as_subclass(OnGpu)
+        if good.dim() > 1:
+            bad["transposed"] = good.transpose(0, 1)
+    assert bad["strides"].shape == good.shape and bad["device"].get_device() == -1
+    for what, b in bad.items():
+        with pytest.raises(moe.MoeError) as ex:
+            call(**dict(t, **{name: b}))
+        assert ex.value.status == INV, what
+    assert len(passed_on) == 1
+
+
+def test_epilogue_keeps_its_residual():
+    r = torch.zeros(4, 64)
+    at = r.data_ptr()
+    epi = moe.epilogue(r)
+    del r
+    assert epi.tensor.data_ptr() == at == epi.residual
+    assert moe.epilogue().tensor is None and moe.epilogue().residual is None
+
+
+def test_a_residual_that_moved_is_refused(passed_on):
+    call, t = binding_calls()["decode"]
+    p = moe.problem(4, 64, 128, 8, 2)
+    epi = moe.epilogue(t["residual"], "bf16")
+    args = [t[n] for n in ("x", "logits", "w_gate", "w_up", "w_down")]
+    moe.moe_layer_decode(p, *args, epi, t["out"], t["ws"], stream=0)
+    epi.tensor.set_(torch.zeros(4, 64, dtype=torch.bfloat16))
+    with pytest.raises(moe.MoeError):
+        moe.moe_layer_decode(p, *args, epi, t["out"], t["ws"], stream=0)
+    # an address without a tensor is passed on as it is
+    moe.moe_layer_decode(p, *args, moe.Epilogue(1 << 40, moe.MOE_DTYPE_BF16), t["out"], t["ws"], stream=0)
+    assert len(passed_on) == 2
