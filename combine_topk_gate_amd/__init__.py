@@ -286,6 +286,12 @@ def _refuse(what, name, t, dtype, shape):
                    f"got {t.dtype} {tuple(t.shape)} strides {t.stride()} on {t.device}")
 
 
+def _gpu_of(what, x):
+    if x is None:
+        raise MoeError(MOE_ERR_INVALID_ARGUMENT, f"{what}: x is missing")
+    return x.get_device()
+
+
 def _addr(what, name, t, dtype, shape, gpu):
     """The data pointer of t (None: NULL), which must be what the call reads:
     contiguous, of this type and shape, on GPU number `gpu` (-1, no GPU, never
@@ -341,7 +347,7 @@ def moe_layer_decode(p, x, logits, w_gate, w_up, w_down, epi, out, ws, stream=No
     what = "moe_layer_decode"
     f32 = torch.float32
     M, H, F, E, dtype = p.num_tokens, p.hidden, p.ffn, p.num_experts, p.dtype
-    EL, gpu = p.local_experts or E, x.get_device()
+    EL, gpu = p.local_experts or E, _gpu_of(what, x)
     act = f32 if dtype == MOE_DTYPE_F32 else torch.bfloat16
     odt = torch.bfloat16 if epi is not None and epi.out_dtype == MOE_DTYPE_BF16 else f32
     if dtype == MOE_DTYPE_BF16_MXFP8:
@@ -370,7 +376,7 @@ def moe_adapter_linear(q, x, w, a, b, scale, adapter_idx, epi, out, ws, stream=N
     what = "moe_adapter_linear"
     f32 = torch.float32
     M, H, N, r, P = q.num_tokens, q.in_features, q.out_features, q.rank, q.num_adapters
-    gpu = x.get_device()
+    gpu = _gpu_of(what, x)
     act = f32 if q.dtype == MOE_DTYPE_F32 else torch.bfloat16
     odt = torch.bfloat16 if epi is not None and epi.out_dtype == MOE_DTYPE_BF16 else f32
     _check(_call_on(gpu, stream, load_library().moe_adapter_linear, ctypes.byref(q),

@@ -294,3 +294,12 @@ def test_a_residual_that_moved_is_refused(passed_on):
     # an address without a tensor is passed on as it is
     moe.moe_layer_decode(p, *args, moe.Epilogue(1 << 40, moe.MOE_DTYPE_BF16), t["out"], t["ws"], stream=0)
     assert len(passed_on) == 2
+
+
+def test_binding_refuses_calls_without_x(passed_on):
+    for which in ("decode", "linear"):
+        call, t = binding_calls()[which]
+        with pytest.raises(moe.MoeError) as ex:
+            call(**dict(t, x=None))
+        assert ex.value.status == INV
+    assert not passed_on
