@@ -10,7 +10,7 @@ missing, loading it raises.
 The entry points keep the C names: ``moe_route``, ``moe_dispatch``,
 ``moe_dispatch_noalloc``, ``moe_grouped_gemm``, ``moe_combine``, ``moe_combine_ex``, ``moe_layer``,
 ``moe_layer_ex``, ``moe_layer_decode``, ``moe_adapter_linear`` (plus
-``moe_workspace_bytes``, ``moe_adapter_workspace_bytes``, ``moe_layer_default_movers``,
+``moe_workspace_bytes``, ``moe_adapter_workspace_bytes``, ``moe_adapter_tiles``, ``moe_layer_default_movers``,
 ``moe_debug_device_status``, ``moe_status_string``, ``moe_abi_version``).
 """
 from __future__ import annotations
@@ -42,7 +42,7 @@ MOE_DECODE_MAX_TOKENS = 256
 MOE_NOALLOC_SCRATCH_BYTES = 1 << 20
 
 EXPORTED = ("moe_workspace_bytes", "moe_route", "moe_dispatch", "moe_dispatch_noalloc", "moe_grouped_gemm", "moe_combine", "moe_combine_ex",
-            "moe_layer", "moe_layer_ex", "moe_layer_decode", "moe_adapter_linear", "moe_adapter_workspace_bytes",
+            "moe_layer", "moe_layer_ex", "moe_layer_decode", "moe_adapter_linear", "moe_adapter_workspace_bytes", "moe_adapter_tiles",
             "moe_quantize_mxfp8", "moe_transpose_weights", "moe_layer_default_movers",
             "moe_debug_device_status",
             "moe_status_string", "moe_abi_version")
@@ -108,6 +108,7 @@ def load_library(path: str = LIB_PATH):
                           ctypes.POINTER(LayerOpts), P, SZ, P], I32),
         "moe_layer_decode": ([PP, P, P, P, P, P, ctypes.POINTER(Epilogue), P, P, SZ, P], I32),
         "moe_adapter_workspace_bytes": ([PA], SZ),
+        "moe_adapter_tiles": ([PA, I32, ctypes.POINTER(I32)], I32),
         "moe_adapter_linear": ([PA, P, P, P, P, P, P, ctypes.POINTER(Epilogue), P, P, SZ, P], I32),
         "moe_quantize_mxfp8": ([ctypes.c_int64, I32, I32, P, P, P], I32),
         "moe_transpose_weights": ([ctypes.c_int64, I32, I32, I32, P, P, P], I32),
@@ -364,6 +365,14 @@ def moe_layer_decode(p, x, logits, w_gate, w_up, w_down, epi, out, ws, stream=No
 
 def moe_adapter_workspace_bytes(q: AdapterProblem) -> int:
     return load_library().moe_adapter_workspace_bytes(ctypes.byref(q))
+
+
+def moe_adapter_tiles(q: AdapterProblem, out_dtype="f32"):
+    """(rows, columns) of the projection's tile and (rows, ranks) of t's that
+    moe_adapter_linear takes, as one tuple (moe.h)."""
+    tiles = (ctypes.c_int32 * 4)()
+    _check(load_library().moe_adapter_tiles(ctypes.byref(q), _DTYPES[out_dtype], tiles), "moe_adapter_tiles")
+    return tuple(tiles)
 
 
 def moe_adapter_linear(q, x, w, a, b, scale, adapter_idx, epi, out, ws, stream=None):

@@ -354,28 +354,34 @@ static void launch_shrink_as(const AdapterArgs& a, unsigned slots, hipStream_t s
 // once per 16 NW of the rank, A once per 16 NT rows), whose adapters 4 blocks
 // share (1000 rows of 20 adapters, H = 4096, rank 16: 5.7 us instead of 8.7 by
 // one).
+struct ShrinkTile {
+  int rows, ranks;
+};
+static ShrinkTile shrink_tile(const AdapterArgs& a) {
+  const int64_t cus = device_cu_count();
+  auto blocks = [&](int ranks, int rows) { return ((a.M + rows - 1) / rows) * ((a.r + ranks - 1) / ranks); };
+  if (a.M <= 64) return {16, 16};
+  if (a.M <= 512) return {16, a.r <= 16 ? 16 : 32};
+  if (a.r > 32 && blocks(64, 32) >= cus) return {32, 64};
+  if (a.r > 16 && blocks(32, 32) >= cus) return {32, 32};
+  return {blocks(16, 32) >= cus ? 32 : 16, 16};
+}
+
 template <class Op>
 static void launch_shrink(const AdapterArgs& a, hipStream_t s) {
-  const int64_t cus = device_cu_count();
-  auto blocks = [&](int nw, int nt) {
-    return ((a.M + 16 * nt - 1) / (16 * nt)) * ((a.r + 16 * nw - 1) / (16 * nw));
-  };
-  if (a.M <= 64) {
-    launch_shrink_as<Op, 8, 1, 1>(a, a.P < 16 ? a.P : 16, s);
-  } else if (a.M <= 512) {
-    if (a.r <= 16)
-      launch_shrink_as<Op, 8, 1, 1>(a, a.P < 8 ? a.P : 8, s);
-    else
-      launch_shrink_as<Op, 8, 2, 1>(a, a.P < 8 ? a.P : 8, s);
-  } else if (a.r > 32 && blocks(4, 2) >= cus) {
-    launch_shrink_as<Op, 8, 4, 2>(a, 4, s);
-  } else if (a.r > 16 && blocks(2, 2) >= cus) {
-    launch_shrink_as<Op, 8, 2, 2>(a, 4, s);
-  } else if (blocks(1, 2) >= cus) {
-    launch_shrink_as<Op, 8, 1, 2>(a, 4, s);
-  } else {
-    launch_shrink_as<Op, 8, 1, 1>(a, 4, s);
-  }
+  const ShrinkTile t = shrink_tile(a);
+  const int most = a.M <= 64 ? 16 : 8;
+  const unsigned slots = a.M > 512 ? 4 : a.P < most ? a.P : most;
+  if (t.rows == 32 && t.ranks == 64)
+    launch_shrink_as<Op, 8, 4, 2>(a, slots, s);
+  else if (t.rows == 32 && t.ranks == 32)
+    launch_shrink_as<Op, 8, 2, 2>(a, slots, s);
+  else if (t.rows == 32)
+    launch_shrink_as<Op, 8, 1, 2>(a, slots, s);
+  else if (t.ranks == 32)
+    launch_shrink_as<Op, 8, 2, 1>(a, slots, s);
+  else
+    launch_shrink_as<Op, 8, 1, 1>(a, slots, s);
 }
 
 template <class Op, class T, int WAVES, int NW, int NT>
@@ -417,17 +423,6 @@ static float tile_cost(const AdapterArgs& a, const TileKind& t, int planes) {
   return t.start + ceilf(tiles / (float)device_cu_count()) * (t.round + more + t.step * (float)k / 1024.0f);
 }
 
-// c16, c32, c64: the costs of the tiles.
-template <class Op, class T>
-static void launch_stream(const AdapterArgs& a, float c16, float c32, float c64, hipStream_t s) {
-  if (c64 <= c32 && c64 <= c16)
-    launch_stream_as<Op, T, 8, 4, 4>(a, s);
-  else if (c32 <= c16)
-    launch_stream_as<Op, T, 8, 2, 2>(a, s);
-  else
-    launch_stream_as<Op, T, 8, 1, 1>(a, s);
-}
-
 template <class Op, class T>
 static void launch_one(const AdapterArgs& a, hipStream_t s) {
   const unsigned blocks = (unsigned)((a.N + 15) / 16);
@@ -447,22 +442,53 @@ static bool one_launch(const AdapterArgs& a) {
   return rounds * a.r * a.row_bytes <= 768 << 10;
 }
 
+static int planes_of(const AdapterArgs& a, bool f32) { return f32 ? 1 : a.out.out_bf16 ? 2 : 3; }
+
+AdapterTiles adapter_tiles(const AdapterArgs& a, bool f32) {
+  if (one_launch(a)) return {kOneRows, 16, 0, 0};
+  const int planes = planes_of(a, f32);
+  const TileKind* best = f32 ? &kStreamF64 : &kStream64;
+  float least = tile_cost(a, *best, planes);
+  auto consider = [&](const TileKind& t) {
+    const float c = tile_cost(a, t, planes);
+    if (c >= least) return;
+    least = c;
+    best = &t;
+  };
+  consider(f32 ? kStreamF32 : kStream32);
+  consider(f32 ? kStreamF16 : kStream16);
+  if (!f32) {
+    consider(kWide);
+    consider(kGemm128);
+    consider(kGemm256);
+    if (a.H < 128 && best->cols == 256) best = &kWide;  // the matrix-core tiles take two steps of 64 at least
+  }
+  const ShrinkTile t = a.P > 0 ? shrink_tile(a) : ShrinkTile{0, 0};
+  return {best->rows, best->cols, t.rows, t.ranks};
+}
+
+template <class Op, class T>
+static void launch_tiles(const AdapterArgs& a, const AdapterTiles& t, hipStream_t s) {
+  if (t.rows == kStream64.rows)
+    launch_stream_as<Op, T, 8, 4, 4>(a, s);
+  else if (t.rows == kStream32.rows)
+    launch_stream_as<Op, T, 8, 2, 2>(a, s);
+  else
+    launch_stream_as<Op, T, 8, 1, 1>(a, s);
+}
+
 hipError_t launch_adapter_linear(AdapterArgs a, bool f32, hipStream_t s) {
   if (a.M == 0) return hipSuccess;
-  if (one_launch(a)) {
+  const AdapterTiles t = adapter_tiles(a, f32);
+  if (t.rows == kOneRows) {
     if (f32)
       launch_one<StreamF32, float>(a, s);
     else
       launch_one<StreamBf16<1>, __bf16>(a, s);
     return hipGetLastError();
   }
-  const int planes = f32 ? 1 : a.out.out_bf16 ? 2 : 3;
-  auto cost = [&](const TileKind& t) { return tile_cost(a, t, planes); };
-  const float c16 = cost(f32 ? kStreamF16 : kStream16), c32 = cost(f32 ? kStreamF32 : kStream32),
-              c64 = cost(f32 ? kStreamF64 : kStream64), stream = fminf(c16, fminf(c32, c64));
-  const float wide = cost(kWide), g128 = cost(kGemm128), g256 = cost(kGemm256);
-  const bool by_stream = f32 || stream <= fminf(wide, fminf(g128, g256));
-  a.planes = by_stream && a.r <= kDirectRank ? 1 : planes;
+  const bool by_stream = t.cols <= kStream64.cols;
+  a.planes = by_stream && a.r <= kDirectRank ? 1 : planes_of(a, f32);
   if (a.P > 0) {
     if (f32)
       launch_shrink<StreamF32>(a, s);
@@ -472,16 +498,16 @@ hipError_t launch_adapter_linear(AdapterArgs a, bool f32, hipStream_t s) {
     if (e != hipSuccess) return e;
   }
   if (f32) {
-    launch_stream<StreamF32, float>(a, c16, c32, c64, s);
+    launch_tiles<StreamF32, float>(a, t, s);
   } else if (by_stream) {
-    launch_stream<StreamBf16<1>, __bf16>(a, c16, c32, c64, s);
-  } else if (a.H < 128 || wide <= fminf(g128, g256)) {
+    launch_tiles<StreamBf16<1>, __bf16>(a, t, s);
+  } else if (t.rows == kWide.rows) {
     const int mb = (int)((a.M + 63) / 64), nb = (a.N + 255) / 256;
     adapter_wide_kernel<StreamBf16<1>, __bf16, 8, 2><<<tile_grid((int64_t)mb * nb), 512, 0, s>>>(a, mb, nb);
   } else {
-    const int64_t rows = g256 < g128 ? 256 : 128, mt = (a.M + rows - 1) / rows, nt = (a.N + 255) / 256;
+    const int64_t mt = (a.M + t.rows - 1) / t.rows, nt = (a.N + 255) / 256;
     const dim3 grid = tile_grid(mt * nt);
-    if (g256 < g128)
+    if (t.rows == kGemm256.rows)
       adapter_gemm_kernel<256><<<grid, kGemmThreads, 0, s>>>(a, (int)mt, (int)nt);
     else
       adapter_gemm_kernel<128><<<grid, kGemmThreads, 0, s>>>(a, (int)mt, (int)nt);

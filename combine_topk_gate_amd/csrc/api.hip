@@ -298,6 +298,22 @@ size_t adapter_ws(const moe_adapter_problem_t* q) {
   return q->num_adapters > 0 ? align_up((size_t)q->num_tokens * q->rank * 6) : 0;  // f32, or three bf16 planes
 }
 
+// Sizes and types of a valid problem; the pointers are left to the call.
+AdapterArgs adapter_args(const moe_adapter_problem_t* q, int32_t out_dtype) {
+  const bool f32 = q->dtype == MOE_DTYPE_F32;
+  AdapterArgs g{};
+  g.M = q->num_tokens;
+  g.H = q->in_features;
+  g.N = q->out_features;
+  g.P = q->num_adapters;
+  g.r = g.P > 0 ? q->rank : 0;
+  g.out.res_bf16 = !f32;
+  g.out.out_bf16 = out_dtype == MOE_DTYPE_BF16;
+  g.planes = 1;  // set by the launcher
+  g.row_bytes = (uint32_t)(g.H * (f32 ? 4 : 2));
+  return g;
+}
+
 template <typename T>
 T* at(void* ws, size_t off) {
   return reinterpret_cast<T*>(reinterpret_cast<char*>(ws) + off);
@@ -307,7 +323,7 @@ T* at(void* ws, size_t off) {
 
 extern "C" {
 
-int32_t moe_abi_version(void) { return (2 << 16) | 1; }
+int32_t moe_abi_version(void) { return (2 << 16) | 2; }
 
 const char* moe_status_string(moe_status_t s) {
   switch (s) {
@@ -661,6 +677,19 @@ size_t moe_adapter_workspace_bytes(const moe_adapter_problem_t* q) {
   return check_adapter(q) == MOE_OK ? adapter_ws(q) : 0;
 }
 
+moe_status_t moe_adapter_tiles(const moe_adapter_problem_t* q, int32_t out_dtype, int32_t tiles[4]) {
+  const moe_status_t st = check_adapter(q);
+  if (st != MOE_OK) return st;
+  if (!tiles || (out_dtype != MOE_DTYPE_F32 && out_dtype != MOE_DTYPE_BF16)) return MOE_ERR_INVALID_ARGUMENT;
+  const AdapterTiles t =
+      q->num_tokens > 0 ? adapter_tiles(adapter_args(q, out_dtype), q->dtype == MOE_DTYPE_F32) : AdapterTiles{};
+  tiles[0] = t.rows;
+  tiles[1] = t.cols;
+  tiles[2] = t.t_rows;
+  tiles[3] = t.t_ranks;
+  return MOE_OK;
+}
+
 moe_status_t moe_adapter_linear(const moe_adapter_problem_t* q, const void* x, const void* w, const void* a,
                                 const void* b, const float* scale, const int32_t* adapter_idx,
                                 const moe_epilogue_t* epi, void* out, void* ws, size_t ws_bytes, void* stream) {
@@ -668,16 +697,9 @@ moe_status_t moe_adapter_linear(const moe_adapter_problem_t* q, const void* x, c
   if (st != MOE_OK) return st;
   const bool f32 = q->dtype == MOE_DTYPE_F32;
   const size_t eb = f32 ? 4 : 2;
-  AdapterArgs g;
-  g.M = q->num_tokens;
-  g.H = q->in_features;
-  g.N = q->out_features;
-  g.P = q->num_adapters;
-  g.r = g.P > 0 ? q->rank : 0;
+  AdapterArgs g = adapter_args(q, epi ? epi->out_dtype : MOE_DTYPE_F32);
   g.out.out = out;
   g.out.residual = epi ? epi->residual : nullptr;
-  g.out.res_bf16 = !f32;
-  g.out.out_bf16 = epi && epi->out_dtype == MOE_DTYPE_BF16;
   if (epi && epi->out_dtype != MOE_DTYPE_F32 && epi->out_dtype != MOE_DTYPE_BF16) return MOE_ERR_INVALID_ARGUMENT;
   if (!w || (g.P > 0 && (!a || !b || !scale))) return MOE_ERR_INVALID_ARGUMENT;
   if (!aligned(x, 16) || !aligned(w, 16) || !aligned(a, 16) || !aligned(b, 16) || !aligned(out, 16) ||
@@ -708,8 +730,6 @@ moe_status_t moe_adapter_linear(const moe_adapter_problem_t* q, const void* x, c
   g.scale = scale;
   g.idx = adapter_idx;
   g.t = need > 0 ? ws : nullptr;
-  g.planes = 1;  // set by the launcher
-  g.row_bytes = (uint32_t)(g.H * eb);
   return hip_status(launch_adapter_linear(g, f32, (hipStream_t)stream));
 }
 

@@ -131,6 +131,11 @@ struct AdapterArgs {
   OutEpilogue out;
   uint32_t row_bytes;  // bytes of a row of x, W and A
 };
+// The tiles of a call: of the projection, and of t (0: not a launch of its own).
+struct AdapterTiles {
+  int rows, cols, t_rows, t_ranks;
+};
+AdapterTiles adapter_tiles(const AdapterArgs& a, bool f32);
 hipError_t launch_adapter_linear(AdapterArgs a, bool f32, hipStream_t s);
 
 int device_cu_count();

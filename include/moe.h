@@ -449,6 +449,14 @@ moe_status_t moe_adapter_linear(const moe_adapter_problem_t* q, const void* x, c
                                 const void* b, const float* scale, const int32_t* adapter_idx,
                                 const moe_epilogue_t* epi, void* out, void* ws, size_t ws_bytes, void* stream);
 
+/* The tiles that moe_adapter_linear takes for this problem and output type (a
+ * rule on sizes and types; for tests and profiles): rows and columns of the
+ * projection's, {8, 16}: one launch for few rows of one adapter, {16, 16}, {32,
+ * 32} and {64, 64}: streamed, {64, 256}: column-splitting, {128, 256} and {256,
+ * 256}: matrix-core; then rows and ranks of t's (0: no launch of its own).  All
+ * 0 for no rows. */
+moe_status_t moe_adapter_tiles(const moe_adapter_problem_t* q, int32_t out_dtype, int32_t tiles[4]);
+
 /* The plan the profiled split table picks for this problem (what moe_layer
  * does when opts->n_mover < 0): the number of dedicated combine workgroups
  * of the fused kernel (0: the combine shares the work queue), or -1 when the

@@ -148,3 +148,46 @@ def check_norm(got, want, roundings, out_bf16, what):
     rel = float((got.double() - want).norm() / ref)
     bound = 4 * roundings ** 0.5 * U + ((BF16 / 3 ** 0.5 if got.numel() >= 64 else BF16) if out_bf16 else 0.0)
     assert rel <= bound, (what, rel, bound)
+
+
+# Projections (bf16 unless dtype says) with the tiles that 256 CUs take for
+# them, rows and columns of the projection's, rows and ranks of t's: every
+# kernel, with ragged rows and columns, rows at any address, one to many
+# adapters a tile, none at all.
+TILES = [
+    (dict(M=1, H=320, N=1001, r=24, P=3), (8, 16, 0, 0)),
+    (dict(M=20, H=128, N=72, r=24, P=3), (16, 16, 16, 16)),
+    (dict(M=20, H=128, N=70, r=16, P=3), (16, 16, 16, 16)),
+    (dict(M=48, H=4096, N=4096, r=16, P=64), (32, 32, 16, 16)),
+    (dict(M=333, H=2048, N=1408, r=32, P=6, mix="runs"), (32, 32, 16, 32)),
+    (dict(M=335, H=1024, N=1021, r=8, P=9), (32, 32, 16, 16)),
+    (dict(M=130, H=2048, N=1001, P=0), (32, 32, 0, 0)),
+    (dict(M=1001, H=1024, N=1022, r=40, P=5, mix="runs"), (64, 64, 16, 16)),
+    (dict(M=1001, H=1024, N=1021, r=8, P=5), (64, 64, 16, 16)),
+    (dict(M=1000, H=1024, N=1021, P=0), (64, 64, 0, 0)),
+    (dict(M=700, H=128, N=3001, r=40, P=6), (64, 256, 16, 16)),
+    (dict(M=900, H=64, N=3333, r=16, P=30), (64, 256, 16, 16)),
+    (dict(M=3000, H=320, N=2049, P=0), (64, 256, 0, 0)),
+    (dict(M=1900, H=2048, N=4090, r=16, P=40), (128, 256, 16, 16)),
+    (dict(M=2001, H=512, N=4093, r=24, P=6, mix="runs"), (128, 256, 16, 16)),
+    (dict(M=3500, H=1024, N=2302, r=72, P=9, mix="runs"), (128, 256, 32, 32)),
+    (dict(M=2001, H=1024, N=4093, P=0), (128, 256, 0, 0)),
+    (dict(M=2000, H=192, N=7168, r=24, P=5), (256, 256, 16, 16)),
+    (dict(M=2001, H=1024, N=7167, r=24, P=6, mix="runs"), (256, 256, 16, 16)),
+    (dict(M=8191, H=1024, N=2045, r=16, P=33), (256, 256, 32, 16)),
+    (dict(M=8191, H=1024, N=2048, r=24, P=3, mix="runs"), (256, 256, 32, 32)),
+    (dict(M=8192, H=1024, N=2046, r=40, P=7), (256, 256, 32, 64)),
+    (dict(M=4001, H=1024, N=4093, P=0), (256, 256, 0, 0)),
+    # t's tiles for long batches beside short projections
+    (dict(M=8200, H=128, N=64, r=64, P=3), (64, 64, 32, 64)),
+    (dict(M=8200, H=128, N=66, r=24, P=300), (16, 16, 32, 32)),
+    (dict(M=8200, H=128, N=64, r=16, P=3, mix="runs"), (16, 16, 32, 16)),
+    (dict(M=20, H=128, N=72, r=40, P=3, dtype="f32"), (16, 16, 16, 16)),
+    (dict(M=333, H=256, N=1001, r=40, P=5, dtype="f32"), (32, 32, 16, 32)),
+    (dict(M=500, H=256, N=257, r=16, P=5, dtype="f32"), (32, 32, 16, 16)),
+    (dict(M=1000, H=128, N=515, r=40, P=3, dtype="f32"), (64, 64, 16, 16)),
+    (dict(M=700, H=128, N=700, r=16, P=3, dtype="f32", mix="runs"), (64, 64, 16, 16)),
+    (dict(M=8200, H=64, N=40, r=64, P=3, dtype="f32"), (64, 64, 32, 64)),
+    (dict(M=8200, H=64, N=40, r=24, P=30, dtype="f32"), (64, 64, 32, 32)),
+    (dict(M=8200, H=64, N=39, r=8, P=3, dtype="f32", mix="runs"), (64, 64, 32, 16)),
+]

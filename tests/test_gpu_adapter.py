@@ -367,3 +367,64 @@ def test_values_past_the_range_of_a_row_and_its_adapter(M, H, N, r, dtype, out):
     got = o[rows].float()
     assert bool((got[:, 5] == float("inf")).all()) and bool((got[:, N - 1] == float("-inf")).all()), got[:, [5, N - 1]]
     assert bool(torch.isfinite(got[:, :5]).all())
+
+
+def on_tiles(shape, tiles, out="f32"):
+    s = dict(dict(r=0, dtype="bf16"), **shape)
+    got = moe.moe_adapter_tiles(moe.adapter_problem(s["M"], s["H"], s["N"], s["r"], s["P"], s["dtype"]), out)
+    assert got == tiles, (shape, got)
+
+
+@pytest.mark.parametrize("shape,tiles", ref.TILES)
+def test_every_tile(shape, tiles):
+    on_tiles(shape, tiles)
+    run_and_check(**shape, residual=shape["N"] % 2 == 1, seed=16)
+
+
+# tiles that a bf16 output and a residual in place take too
+WIDE = [(dict(M=1001, H=1024, N=1022, r=40, P=5), (64, 64, 16, 16)), (dict(M=700, H=128, N=3001, r=40, P=6), (64, 256, 16, 16)),
+        (dict(M=2001, H=512, N=4093, r=24, P=6), (128, 256, 16, 16)), (dict(M=2001, H=1024, N=7167, r=24, P=6), (256, 256, 16, 16)),
+        (dict(M=2000, H=192, N=7168, r=24, P=5), (256, 256, 16, 16))]
+
+
+@pytest.mark.parametrize("shape,tiles", WIDE)
+def test_long_batches_in_place_of_the_residual(shape, tiles):
+    on_tiles(shape, tiles, "bf16")
+    q, d, epi, out, ws = run_and_check(**shape, out="bf16", residual=True, seed=17)
+    r = d["residual"]
+    call(q, d, moe.epilogue(r, "bf16"), r, ws)
+    assert torch.equal(r, out)
+
+
+@pytest.mark.parametrize("shape,tiles", WIDE)
+def test_rows_of_long_batches_do_not_depend_on_the_others(shape, tiles):
+    on_tiles(shape, tiles)
+    M = shape["M"]
+    q, d, epi, out, ws, _ = make(**shape, seed=18)
+    call(q, d, epi, out, ws)
+    first = out.clone()
+    other = dict(d, x=-2 * d["x"], idx=d["idx"].flip(0).contiguous())
+    rows = [0, 70, 255, 256, M // 2, M - 1]
+    for m in rows:
+        other["x"][m], other["idx"][m] = d["x"][m], d["idx"][m]
+    call(q, other, epi, out, ws)
+    assert torch.equal(out[rows], first[rows])
+
+
+@pytest.mark.parametrize("M,N,r,tiles", [(2001, 7168, 24, (256, 256, 16, 16)), (700, 3001, 40, (64, 256, 16, 16)),
+                                         (3000, 2052, 40, (128, 256, 32, 16))])
+def test_nan_and_infinities_on_the_long_tiles(M, N, r, tiles):
+    on_tiles(dict(M=M, H=128, N=N, r=r, P=6), tiles)
+    test_nan_in_an_unused_adapter_and_in_a_row_stays_there(M, N, r, "bf16")
+
+
+def test_same_bits_on_the_long_tiles():
+    for shape, tiles in WIDE:
+        on_tiles(shape, tiles, "bf16")
+        q, d, epi, out, ws, _ = make(**shape, out="bf16", residual=True, seed=19)
+        call(q, d, epi, out, ws)
+        first = out.clone()
+        for _ in range(4):
+            out.zero_()
+            call(q, d, epi, out, ws)
+            assert torch.equal(out, first), shape

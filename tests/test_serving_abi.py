@@ -303,3 +303,36 @@ def test_binding_refuses_calls_without_x(passed_on):
             call(**dict(t, x=None))
         assert ex.value.status == INV
     assert not passed_on
+
+
+def tiles_of(shape, out="f32"):
+    s = dict(dict(r=0, dtype="bf16"), **shape)
+    return moe.moe_adapter_tiles(moe.adapter_problem(s["M"], s["H"], s["N"], s["r"], s["P"], s["dtype"]), out)
+
+
+@pytest.mark.parametrize("shape,tiles", ref.TILES)
+def test_adapter_tiles(lib, shape, tiles):
+    """The rule on sizes: the shapes that the GPU tests run take the kernels
+    that they are there for."""
+    assert tiles_of(shape) == tiles
+
+
+def test_adapter_tiles_covers_every_kernel(lib):
+    bf16 = [t for s, t in ref.TILES if s.get("dtype") != "f32"]
+    f32 = [t for s, t in ref.TILES if s.get("dtype") == "f32"]
+    streamed = {(16, 16), (32, 32), (64, 64)}
+    assert {t[:2] for t in bf16} == streamed | {(8, 16), (64, 256), (128, 256), (256, 256)}
+    assert {t[:2] for t in f32} == streamed
+    t_tiles = {(16, 16), (16, 32), (32, 16), (32, 32), (32, 64)}
+    assert {t[2:] for t in bf16} == {t[2:] for t in f32} | {(0, 0)} == t_tiles | {(0, 0)}
+
+
+def test_adapter_tiles_refuses_bad_arguments(lib):
+    q = moe.adapter_problem(4, 64, 8, 8, 2)
+    tiles = (ctypes.c_int32 * 4)()
+    assert lib.moe_adapter_tiles(None, moe.MOE_DTYPE_F32, tiles) == INV
+    assert lib.moe_adapter_tiles(B(q), moe.MOE_DTYPE_BF16_MXFP8, tiles) == INV
+    assert lib.moe_adapter_tiles(B(q), moe.MOE_DTYPE_F32, None) == INV
+    assert lib.moe_adapter_tiles(B(moe.adapter_problem(4, 64, 8, 12, 2)), moe.MOE_DTYPE_F32, tiles) == INV
+    assert lib.moe_adapter_tiles(B(moe.adapter_problem(4, 64, 8, 8, 2, "bf16_mxfp8")), moe.MOE_DTYPE_F32, tiles) == UNS
+    assert tiles_of(dict(M=0, H=64, N=8, r=8, P=2)) == (0, 0, 0, 0)
