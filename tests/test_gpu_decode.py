@@ -424,3 +424,12 @@ def test_a_product_past_the_range_is_infinite(M, dtype, out):
     h = 127 / 64 * 129 / 128 * 2.0 ** 40
     err = (o[:, 5].double() / (h * 2.0 ** 80) - 1).abs().max()
     assert float(err) <= 8 * ref.U + (ref.BF16 * ref.BF16 + ref.BF16 if out == "bf16" else 0), float(err)
+
+
+# few tokens with k of 9 to 16 (up to 64 pairs: two kernels; 72: the plan)
+@pytest.mark.parametrize("dtype", ["bf16", "f32", "bf16_mxfp8"])
+@pytest.mark.parametrize("logits,held,base", [("random", 0, 0), ("masked", 7, 5), ("idle", 0, 0), ("few", 0, 0),
+                                              ("ties", 20, 0)])
+@pytest.mark.parametrize("M,k", [(1, 16), (4, 16), (7, 9), (8, 8), (8, 9)])
+def test_many_experts_of_few_tokens(M, k, logits, held, base, dtype):
+    run_and_check(M=M, H=128, F=256, E=24, k=k, held=held, base=base, dtype=dtype, logits=logits, residual=M == 7, seed=18)

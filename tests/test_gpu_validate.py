@@ -126,3 +126,62 @@ def test_out_of_range_expert_ids_stay_inside_the_buffers_without_validation():
     assert int(offs[-1]) == R - 1 and int(counts.sum()) == R - 1
     kept = np.sort(s2f[: R - 1].cpu().numpy())
     assert np.array_equal(kept, np.setdiff1d(np.arange(R), [7 * cfg.k + 1]))
+
+
+def _decode_case(M):
+    H, F, E, k = 128, 128, 8, 2
+    g = torch.Generator(device="cuda")
+    g.manual_seed(5)
+    w = [(torch.randn(s, generator=g, device="cuda") * 0.05).bfloat16() for s in ((E, F, H), (E, F, H), (E, H, F))]
+    x = torch.randn((M, H), generator=g, device="cuda").bfloat16()
+    logits = torch.randn((M, E), generator=g, device="cuda")
+    p = moe.problem(M, H, F, E, k)
+    ws = torch.empty(moe.moe_workspace_bytes(p, moe.MOE_OP_LAYER_DECODE), dtype=torch.uint8, device="cuda")
+    return p, x, logits, w, torch.zeros((M, H), device="cuda"), ws
+
+
+@pytest.mark.parametrize("M", [3, 40])
+def test_decode_logits(validating, M):
+    p, x, logits, w, out, ws = _decode_case(M)
+    logits[1] = float("-inf")  # an idle row, and a closed expert: allowed
+    logits[0, 2] = float("-inf")
+    moe.moe_layer_decode(p, x, logits, *w, None, out, ws)
+    first = out.clone()
+    assert bool(first[0].any()) and not bool(first[1].any())
+    for bad in (float("nan"), float("inf")):
+        wrong = logits.clone()
+        wrong[M - 1, 5] = bad
+        with pytest.raises(moe.MoeError) as ex:
+            moe.moe_layer_decode(p, x, wrong, *w, None, out, ws)
+        assert ex.value.status == moe.MOE_ERR_INVALID_ARGUMENT
+        torch.cuda.synchronize()
+        assert torch.equal(out, first)  # nothing launched
+    os.environ.pop("MOE_DEBUG_VALIDATE")
+    moe.moe_layer_decode(p, x, logits, *w, None, out, ws)
+    assert torch.equal(out, first)
+
+
+def test_adapter_indices(validating):
+    M, H, N, r, P = 20, 128, 72, 16, 3
+    q = moe.adapter_problem(M, H, N, r, P)
+    g = torch.Generator(device="cuda")
+    g.manual_seed(6)
+    x, w, a, b = ((torch.randn(s, generator=g, device="cuda")).bfloat16() for s in ((M, H), (N, H), (P, r, H), (P, N, r)))
+    scale = torch.ones(P, device="cuda")
+    idx = torch.randint(-1, P, (M,), generator=g, device="cuda", dtype=torch.int32)
+    idx[:2] = torch.tensor([-1, P - 1])
+    out = torch.zeros((M, N), device="cuda")
+    ws = torch.empty(moe.moe_adapter_workspace_bytes(q), dtype=torch.uint8, device="cuda")
+    moe.moe_adapter_linear(q, x, w, a, b, scale, idx, None, out, ws)
+    first = out.clone()
+    for bad in (P, -2):
+        wrong = idx.clone()
+        wrong[M - 1] = bad
+        with pytest.raises(moe.MoeError) as ex:
+            moe.moe_adapter_linear(q, x, w, a, b, scale, wrong, None, out, ws)
+        assert ex.value.status == moe.MOE_ERR_INVALID_ARGUMENT
+        torch.cuda.synchronize()
+        assert torch.equal(out, first)
+    os.environ.pop("MOE_DEBUG_VALIDATE")
+    moe.moe_adapter_linear(q, x, w, a, b, scale, idx, None, out, ws)
+    assert torch.equal(out, first)
