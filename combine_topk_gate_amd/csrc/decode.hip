@@ -553,8 +553,6 @@ __global__ __launch_bounds__(kStreamThreads) void decode_few_l1_kernel(DecodeArg
 }
 
 // ---------------------------------------------------------------- launch ---
-constexpr int kCus = 256;
-
 template <class Op0, class Op1, int NP, bool MX>
 static void launch_few(const DecodeArgs& a, const float* logits, const OutEpilogue& ep, hipStream_t s) {
   const DecodePlan& p = a.plan;
@@ -566,7 +564,7 @@ static void launch_few(const DecodeArgs& a, const float* logits, const OutEpilog
   // again (8 tokens, k = 8, 64 experts of 2048 x 1408: 84 us instead of 109; 22
   // experts of 448 x 4992: 51 instead of 73).  Rows of more than 4 KiB hide the
   // routing (8 tokens, 8 experts of 4096 x 14336: 276 us in turn, 263 not).
-  const int groups = a.F / 16, at_once = 7 * kCus;
+  const int groups = a.F / 16, at_once = 7 * device_cu_count();
   const int turns = a.x_pitch > 4096 ? 1 : (groups * entries + at_once - 1) / at_once;
   const dim3 grid((unsigned)((groups + turns - 1) / turns), (unsigned)entries);
   if (p.k <= 2)
@@ -599,18 +597,18 @@ static void launch_few(const DecodeArgs& a, const float* logits, const OutEpilog
 // of 4096 x 14336, 229 instead of 200).
 DecodeSplit decode_split(int M, int k, int E, int EL, int H, int F, int dtype) {
   const bool mx = dtype == MOE_DTYPE_BF16_MXFP8, f32 = dtype == MOE_DTYPE_F32;
-  const int R = M * k;
+  const int R = M * k, cus = device_cu_count();
   const int64_t held = ((int64_t)R * EL + E - 1) / E;  // of the pairs, about
   const int experts = held < 1 ? 1 : (int)(held < EL ? held : EL);
   DecodeSplit d;
   d.nt = M <= 16 ? 1 : M <= 32 || R <= 24 * E ? 2 : mx || M <= 64 || R <= 40 * E ? 4 : 8;
-  if (d.nt > 2 && F / 64 * experts < (f32 ? kCus : kCus / 4)) d.nt = 2;
+  if (d.nt > 2 && F / 64 * experts < (f32 ? cus : cus / 4)) d.nt = 2;
   const int64_t rows = (held + experts - 1) / experts;
   const int64_t entries = experts * ((rows + 16 * d.nt - 1) / (16 * d.nt));
   const int64_t blocks = (H + 127) / 128 * entries / (d.nt > 2 && !mx ? 2 : 1);
   const int lines = F / (mx ? 128 : f32 ? 32 : 64);
   d.parts = d.nt > 2 ? 2 : 1;
-  while (d.parts < 8 && blocks * d.parts < kCus && lines >= 8 * d.parts) d.parts *= 2;
+  while (d.parts < 8 && blocks * d.parts < cus && lines >= 8 * d.parts) d.parts *= 2;
   return d;
 }
 
