@@ -17,6 +17,8 @@
 // in f32, for bf16 weights as bf16 planes whose sum is the f32 value (three,
 // exact, for an f32 output; two, 2^-16 of the value, for a bf16 output, whose
 // own rounding is 2^-8).
+// A weight that is infinite, and a product past the range, act as in f32
+// (stream_resum).
 #include "common.hpp"
 #include "launch.hpp"
 #include "stream.hpp"

@@ -8,8 +8,8 @@
 // is 128 bytes of every row, wave w takes lines w, w + waves, ...; the partial
 // accumulators are added in LDS in wave order at the end (a fixed order: the
 // bits do not depend on timing).  A wave loads a line of 8 rows with one
-// instruction, 8 lanes of 16 bytes beside each other in a row, keeps DEPTH
-// lines in flight in registers, and turns each to the matrix cores' layout
+// instruction, 8 lanes of 16 bytes beside each other in a row, keeps one to
+// four lines in flight in registers, and turns each to the matrix cores' layout
 // (lane = row, then 16-byte chunk) through a place in LDS of its own, without
 // a barrier.
 //   Loading straight in the matrix cores' layout, where neighbouring lanes
@@ -178,8 +178,9 @@ constexpr int kOne = 0, kPaired = 1, kFirst = 2;
 
 // One wave's share of the tile: lines first, first + stride, ....  row_off(i): byte offset from a.x of token row i (0 <= i <
 // 16 NT), any row for one that does not exist.  lds: stream_line_bytes() of
-// the wave's own.  DEPTH: lines in flight (as many as about 96 registers hold,
-// at most): 4 where the weights come from HBM for long (decode, 2 experts of
+// the wave's own.  DEPTH: lines in flight, fewer where about 96 registers hold
+// fewer (stream_depth; a line of 64 weight and 64 token rows takes 64: one is in
+// flight): 4 where the weights come from HBM for long (decode, 2 experts of
 // 4096 x 14336: 81 us for Layer0 instead of 84), 2 for short streams, where
 // filling and draining the pipe costs more (333 x 2048 x 1408: 13 us, 17).
 // ONCE: the weights are not used again soon (load_weight).
