@@ -433,3 +433,36 @@ def test_a_product_past_the_range_is_infinite(M, dtype, out):
 @pytest.mark.parametrize("M,k", [(1, 16), (4, 16), (7, 9), (8, 8), (8, 9)])
 def test_many_experts_of_few_tokens(M, k, logits, held, base, dtype):
     run_and_check(M=M, H=128, F=256, E=24, k=k, held=held, base=base, dtype=dtype, logits=logits, residual=M == 7, seed=18)
+
+
+@pytest.mark.parametrize("out", ["f32", "bf16"])
+@pytest.mark.parametrize("M,F", [(1, 384), (6, 1280), (12, 2560), (24, 640), (130, 1408)])
+def test_mxfp8_products_past_the_range(M, F, out):
+    # in any row of a group of 32, line and part of the reduction, beside ordinary weights, which keep their bits
+    H, E = 192, 2
+    p, d, epi, o, ws, _ = make(M, H, F, E, 1, dtype="bf16_mxfp8", out=out, seed=19)
+    d["x"][:, 0] = 1.0
+    at = [(0, 3), (37, F - 1), (63, F // 2 + 1), (64, 130), (191, F - 70)]
+    for _, f in at:  # h = 16383 2^27, as planes 2^41 and -2^27
+        for k in ("w_gate", "w_up"):
+            d[k][:, f] = 0
+        d["w_gate"][:, f, 0], d["w_up"][:, f, 0] = 127 / 64 * 2.0 ** 20, 129 / 128 * 2.0 ** 20
+    w = d["values_down"].float().clone()
+    for _, f in at:
+        w[:, :, f] = 0
+    buf, values = ref.quantize_mxfp8(w.view(E * H, F))
+    d["w_down"], d["values_down"] = buf, values.view(E, H, F)
+    call(p, d, epi, o, ws)
+    clean = o.clone()
+    assert bool(torch.isfinite(clean).all())
+    for i, (n, f) in enumerate(at):  # (the other weights of the element's block round to zero beside it)
+        w[:, n, f] = 2.0 ** 110 * (-1) ** i
+    d["w_down"], v = ref.quantize_mxfp8(w.view(E * H, F))
+    o.fill_(0.0)
+    call(p, d, epi, o, ws)
+    rows = [n for n, _ in at]
+    keep = torch.ones(H, dtype=torch.bool, device=DEV)
+    keep[rows] = False
+    sign = torch.tensor([(-1.0) ** i for i in range(len(at))], device=DEV)
+    assert torch.equal(o[:, rows].float(), (sign * float("inf")).expand(M, -1))
+    assert torch.equal(o[:, keep], clean[:, keep])
