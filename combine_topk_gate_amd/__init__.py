@@ -9,7 +9,9 @@ missing, loading it raises.
 
 The entry points keep the C names: ``moe_route``, ``moe_dispatch``,
 ``moe_dispatch_noalloc``, ``moe_grouped_gemm``, ``moe_combine``, ``moe_combine_ex``, ``moe_layer``,
-``moe_layer_ex``, ``moe_layer_decode``, ``moe_adapter_linear`` (plus
+``moe_layer_ex``, ``moe_layer_decode``, ``moe_adapter_linear``, and for training
+``moe_combine_dropout``, ``moe_combine_backward``, ``moe_dispatch_backward``, ``moe_route_backward``,
+``moe_grouped_gemm_aux``, ``moe_grouped_gemm_backward``, ``moe_grouped_gemm_backward_weights`` (plus
 ``moe_workspace_bytes``, ``moe_adapter_workspace_bytes``, ``moe_adapter_tiles``, ``moe_layer_default_movers``,
 ``moe_debug_device_status``, ``moe_status_string``, ``moe_abi_version``).
 """
@@ -36,6 +38,7 @@ MOE_OP_DISPATCH = 0
 MOE_OP_GROUPED_GEMM = 1
 MOE_OP_LAYER = 2
 MOE_OP_LAYER_DECODE = 3
+MOE_OP_GROUPED_GEMM_BACKWARD = 4
 
 MOE_DECODE_MAX_TOKENS = 256
 
@@ -43,6 +46,8 @@ MOE_NOALLOC_SCRATCH_BYTES = 1 << 20
 
 EXPORTED = ("moe_workspace_bytes", "moe_route", "moe_dispatch", "moe_dispatch_noalloc", "moe_grouped_gemm", "moe_combine", "moe_combine_ex",
             "moe_layer", "moe_layer_ex", "moe_layer_decode", "moe_adapter_linear", "moe_adapter_workspace_bytes", "moe_adapter_tiles",
+            "moe_combine_dropout", "moe_combine_backward", "moe_dispatch_backward", "moe_route_backward",
+            "moe_grouped_gemm_aux", "moe_grouped_gemm_backward", "moe_grouped_gemm_backward_weights",
             "moe_quantize_mxfp8", "moe_transpose_weights", "moe_layer_default_movers",
             "moe_debug_device_status",
             "moe_status_string", "moe_abi_version")
@@ -68,6 +73,11 @@ class AdapterProblem(ctypes.Structure):
 class Epilogue(ctypes.Structure):
     _fields_ = [("residual", ctypes.c_void_p), ("out_dtype", ctypes.c_int32)]
     tensor = None  # the residual's tensor, where epilogue() was given one
+
+
+class Dropout(ctypes.Structure):
+    _fields_ = [("p", ctypes.c_double), ("rng", ctypes.c_void_p)]
+    tensor = None  # the {seed, offset} tensor, where dropout() was given one
 
 
 class LayerAux(ctypes.Structure):
@@ -110,6 +120,13 @@ def load_library(path: str = LIB_PATH):
         "moe_adapter_workspace_bytes": ([PA], SZ),
         "moe_adapter_tiles": ([PA, I32, ctypes.POINTER(I32)], I32),
         "moe_adapter_linear": ([PA, P, P, P, P, P, P, ctypes.POINTER(Epilogue), P, P, SZ, P], I32),
+        "moe_combine_dropout": ([PP, P, P, P, ctypes.POINTER(Epilogue), ctypes.POINTER(Dropout), P, P], I32),
+        "moe_combine_backward": ([PP, P, I32, P, P, P, ctypes.POINTER(Dropout), P, P, P], I32),
+        "moe_dispatch_backward": ([PP, P, P, ctypes.POINTER(Epilogue), P, P], I32),
+        "moe_route_backward": ([PP, P, P, P, P, P], I32),
+        "moe_grouped_gemm_aux": ([PP, P, P, P, P, P, P, P, P], I32),
+        "moe_grouped_gemm_backward": ([PP, I32, P, P, P, P, P, P, P, P, P, P, SZ, P], I32),
+        "moe_grouped_gemm_backward_weights": ([PP, I32, P, P, P, P, I32, I32, P, P, P, SZ, P], I32),
         "moe_quantize_mxfp8": ([ctypes.c_int64, I32, I32, P, P, P], I32),
         "moe_transpose_weights": ([ctypes.c_int64, I32, I32, I32, P, P, P], I32),
         "moe_layer_default_movers": ([PP], I32),
@@ -158,6 +175,14 @@ def epilogue(residual=None, out_dtype="f32") -> Epilogue:
     epi = Epilogue(None if residual is None else residual.data_ptr(), _DTYPES[out_dtype])
     epi.tensor = residual
     return epi
+
+
+def dropout(p, rng) -> Dropout:
+    """Dropout with probability p (0 <= p < 1) whose mask comes from rng, a device
+    int64 tensor {seed, offset} that the kernels read.  It holds the tensor."""
+    drop = Dropout(float(p), rng.data_ptr())
+    drop.tensor = rng
+    return drop
 
 
 def _ptr(t):
@@ -394,6 +419,143 @@ def moe_adapter_linear(q, x, w, a, b, scale, adapter_idx, epi, out, ws, stream=N
                     _addr(what, "scale", scale, f32, (P,), gpu),
                     _addr(what, "adapter_idx", adapter_idx, torch.int32, (M,), gpu),
                     _epilogue(what, epi, act, (M, N), gpu), _addr(what, "out", out, odt, (M, N), gpu),
+                    *_workspace(what, ws, gpu)), what)
+
+
+def _dropout(what, drop, gpu):
+    """The dropout for the library; its rng is checked as the other tensors are."""
+    if drop is None:
+        return None
+    if drop.tensor is not None:
+        import torch
+        if _addr(what, "rng", drop.tensor, torch.int64, (2,), gpu) != drop.rng:
+            raise MoeError(MOE_ERR_INVALID_ARGUMENT, f"{what}: the rng tensor has moved since its dropout was made")
+    return ctypes.byref(drop)
+
+
+def _dtypes(p, epi=None):
+    """(dtype of the problem's activations, dtype of an output under epi)."""
+    import torch
+    act = torch.float32 if p.dtype == MOE_DTYPE_F32 else torch.bfloat16
+    return act, torch.bfloat16 if epi is not None and epi.out_dtype == MOE_DTYPE_BF16 else torch.float32
+
+
+def moe_combine_dropout(p, y, topk_w, flat_to_sorted, epi, drop, out, stream=None):
+    """moe_combine_ex with a dropout (dropout(p, rng), or None) on the sum before
+    the epilogue: y [R, H] f32, topk_w [M, k] f32, flat_to_sorted [R] int32, out
+    [M, H] in epi's type."""
+    import torch
+    what = "moe_combine_dropout"
+    M, H, k, gpu = p.num_tokens, p.hidden, p.topk, _gpu_of(what, y)
+    act, odt = _dtypes(p, epi)
+    _check(_call_on(gpu, stream, load_library().moe_combine_dropout, ctypes.byref(p),
+                    _addr(what, "y", y, torch.float32, (M * k, H), gpu),
+                    _addr(what, "topk_w", topk_w, torch.float32, (M, k), gpu),
+                    _addr(what, "flat_to_sorted", flat_to_sorted, torch.int32, (M * k,), gpu),
+                    _epilogue(what, epi, act, (M, H), gpu), _dropout(what, drop, gpu),
+                    _addr(what, "out", out, odt, (M, H), gpu)), what)
+
+
+def moe_combine_backward(p, dout, y, topk_w, flat_to_sorted, drop, dy, dtopk_w, stream=None):
+    """Gradient of the combine: dout [M, H] f32 or bf16, y [R, H] f32, topk_w [M,
+    k], flat_to_sorted [R], drop as in the forward call (or None) -> dy [R, H] in
+    the problem's dtype, dtopk_w [M, k] f32."""
+    import torch
+    what = "moe_combine_backward"
+    M, H, k, gpu = p.num_tokens, p.hidden, p.topk, _gpu_of(what, dout)
+    bf16 = dout.dtype is torch.bfloat16
+    _check(_call_on(gpu, stream, load_library().moe_combine_backward, ctypes.byref(p),
+                    _addr(what, "dout", dout, torch.bfloat16 if bf16 else torch.float32, (M, H), gpu),
+                    MOE_DTYPE_BF16 if bf16 else MOE_DTYPE_F32, _addr(what, "y", y, torch.float32, (M * k, H), gpu),
+                    _addr(what, "topk_w", topk_w, torch.float32, (M, k), gpu),
+                    _addr(what, "flat_to_sorted", flat_to_sorted, torch.int32, (M * k,), gpu),
+                    _dropout(what, drop, gpu), _addr(what, "dy", dy, _dtypes(p)[0], (M * k, H), gpu),
+                    _addr(what, "dtopk_w", dtopk_w, torch.float32, (M, k), gpu)), what)
+
+
+def moe_dispatch_backward(p, dx_perm, flat_to_sorted, epi, dx, stream=None):
+    """Gradient of the dispatch's copy: dx_perm [R, H] in the problem's dtype,
+    flat_to_sorted [R] -> dx [M, H] in epi's type (its residual added)."""
+    import torch
+    what = "moe_dispatch_backward"
+    M, H, k, gpu = p.num_tokens, p.hidden, p.topk, _gpu_of(what, dx_perm)
+    act, odt = _dtypes(p, epi)
+    _check(_call_on(gpu, stream, load_library().moe_dispatch_backward, ctypes.byref(p),
+                    _addr(what, "dx_perm", dx_perm, act, (M * k, H), gpu),
+                    _addr(what, "flat_to_sorted", flat_to_sorted, torch.int32, (M * k,), gpu),
+                    _epilogue(what, epi, act, (M, H), gpu), _addr(what, "dx", dx, odt, (M, H), gpu)), what)
+
+
+def moe_route_backward(p, topk_idx, topk_w, dtopk_w, dlogits, stream=None):
+    """Gradient of the router: topk_idx [M, k] int32, topk_w and dtopk_w [M, k] f32
+    -> dlogits [M, E] f32."""
+    import torch
+    what = "moe_route_backward"
+    M, E, k, gpu = p.num_tokens, p.num_experts, p.topk, _gpu_of(what, topk_idx)
+    f32 = torch.float32
+    _check(_call_on(gpu, stream, load_library().moe_route_backward, ctypes.byref(p),
+                    _addr(what, "topk_idx", topk_idx, torch.int32, (M, k), gpu),
+                    _addr(what, "topk_w", topk_w, f32, (M, k), gpu), _addr(what, "dtopk_w", dtopk_w, f32, (M, k), gpu),
+                    _addr(what, "dlogits", dlogits, f32, (M, E), gpu)), what)
+
+
+def _segments(p):
+    return p.num_src_blocks * (p.local_experts or p.num_experts)
+
+
+def moe_grouped_gemm_aux(p, a, w0, w1, offsets, gate, up, c, stream=None):
+    """Layer 0 of the grouped GEMM that keeps its products for the gradient: a
+    [R, H], w0, w1 [EL, F, H], offsets [G + 1] -> gate, up, c (Hact) [R, F]."""
+    import torch
+    what = "moe_grouped_gemm_aux"
+    R, H, F, gpu = p.num_tokens * p.topk, p.hidden, p.ffn, _gpu_of(what, a)
+    EL, act = p.local_experts or p.num_experts, _dtypes(p)[0]
+    _check(_call_on(gpu, stream, load_library().moe_grouped_gemm_aux, ctypes.byref(p),
+                    _addr(what, "a", a, act, (R, H), gpu), _addr(what, "w0", w0, act, (EL, F, H), gpu),
+                    _addr(what, "w1", w1, act, (EL, F, H), gpu),
+                    _addr(what, "offsets", offsets, torch.int32, (_segments(p) + 1,), gpu),
+                    _addr(what, "gate", gate, act, (R, F), gpu), _addr(what, "up", up, act, (R, F), gpu),
+                    _addr(what, "c", c, act, (R, F), gpu)), what)
+
+
+def moe_grouped_gemm_backward(p, layer, d0, d1, w0, w1, gate, up, offsets, o0, o1, ws=None, stream=None):
+    """Gradient of the grouped GEMM for its rows.  Layer 1: d0 = dY [R, H], w0 =
+    W_down, gate, up [R, F] -> o0 = dgate, o1 = dup [R, F] (d1, w1 None).  Layer 0:
+    d0 = dgate, d1 = dup, w0 = W_gate, w1 = W_up -> o0 = dX_perm [R, H] (gate, up,
+    o1 None).  ws moe_workspace_bytes(p, MOE_OP_GROUPED_GEMM_BACKWARD) bytes."""
+    import torch
+    what = "moe_grouped_gemm_backward"
+    R, H, F, gpu = p.num_tokens * p.topk, p.hidden, p.ffn, _gpu_of(what, d0)
+    EL, act = p.local_experts or p.num_experts, _dtypes(p)[0]
+    din, dout = (F, H) if layer == 0 else (H, F)
+    wshape = (EL, F, H) if layer == 0 else (EL, H, F)
+    _check(_call_on(gpu, stream, load_library().moe_grouped_gemm_backward, ctypes.byref(p), int(layer),
+                    _addr(what, "d0", d0, act, (R, din), gpu), _addr(what, "d1", d1, act, (R, din), gpu),
+                    _addr(what, "w0", w0, act, wshape, gpu), _addr(what, "w1", w1, act, wshape, gpu),
+                    _addr(what, "gate", gate, act, (R, F), gpu), _addr(what, "up", up, act, (R, F), gpu),
+                    _addr(what, "offsets", offsets, torch.int32, (_segments(p) + 1,), gpu),
+                    _addr(what, "o0", o0, act, (R, dout), gpu), _addr(what, "o1", o1, act, (R, dout), gpu),
+                    *_workspace(what, ws, gpu)), what)
+
+
+def moe_grouped_gemm_backward_weights(p, layer, d0, d1, a, offsets, dw0, dw1, accumulate=False, ws=None, stream=None):
+    """Gradient of the grouped GEMM for its weights.  Layer 1: d0 = dY [R, H], a =
+    Hact [R, F] -> dw0 = dW_down [EL, H, F] (d1, dw1 None).  Layer 0: d0 = dgate, d1
+    = dup [R, F], a = X_perm [R, H] -> dw0 = dW_gate, dw1 = dW_up [EL, F, H].  dw0
+    and dw1 f32 or bf16; accumulate (f32): added to what they hold."""
+    import torch
+    what = "moe_grouped_gemm_backward_weights"
+    R, H, F, gpu = p.num_tokens * p.topk, p.hidden, p.ffn, _gpu_of(what, a)
+    EL, act = p.local_experts or p.num_experts, _dtypes(p)[0]
+    n, m = (F, H) if layer == 0 else (H, F)
+    bf16 = dw0 is not None and dw0.dtype is torch.bfloat16
+    odt = torch.bfloat16 if bf16 else torch.float32
+    _check(_call_on(gpu, stream, load_library().moe_grouped_gemm_backward_weights, ctypes.byref(p), int(layer),
+                    _addr(what, "d0", d0, act, (R, n), gpu), _addr(what, "d1", d1, act, (R, n), gpu),
+                    _addr(what, "a", a, act, (R, m), gpu),
+                    _addr(what, "offsets", offsets, torch.int32, (_segments(p) + 1,), gpu),
+                    MOE_DTYPE_BF16 if bf16 else MOE_DTYPE_F32, int(bool(accumulate)),
+                    _addr(what, "dw0", dw0, odt, (EL, n, m), gpu), _addr(what, "dw1", dw1, odt, (EL, n, m), gpu),
                     *_workspace(what, ws, gpu)), what)
 
 

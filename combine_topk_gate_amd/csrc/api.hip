@@ -314,6 +314,68 @@ AdapterArgs adapter_args(const moe_adapter_problem_t* q, int32_t out_dtype) {
   return g;
 }
 
+// ------------------------------------------------------------- training ---
+// A buffer of a call, for the checks: bytes, and whether the call writes it.
+struct Span {
+  const void* p;
+  size_t n;
+  bool out;
+};
+
+// Every tensor given and 16-byte aligned, and no output overlaps another span.
+moe_status_t check_spans(const Span* s, int n) {
+  for (int i = 0; i < n; ++i) {
+    if (!s[i].p && s[i].n) return MOE_ERR_INVALID_ARGUMENT;
+    if (!aligned(s[i].p, 16)) return MOE_ERR_INVALID_ARGUMENT;
+  }
+  for (int i = 0; i < n; ++i)
+    for (int j = i + 1; j < n; ++j)
+      if ((s[i].out || s[j].out) && overlap(s[i].p, s[i].n, s[j].p, s[j].n)) return MOE_ERR_INVALID_ARGUMENT;
+  return MOE_OK;
+}
+
+// An index or per-pair array: given and 4-byte aligned, and apart from the outputs.
+moe_status_t check_words(const void* p, size_t n, const Span* s, int ns) {
+  if ((!p && n) || !aligned(p, 4)) return MOE_ERR_INVALID_ARGUMENT;
+  for (int i = 0; i < ns; ++i)
+    if (s[i].out && overlap(p, n, s[i].p, s[i].n)) return MOE_ERR_INVALID_ARGUMENT;
+  return MOE_OK;
+}
+
+// The kernels' dropout from the caller's description (null: none, rng null).
+moe_status_t dropout_of(const moe_dropout_t* drop, Dropout* d) {
+  d->rng = nullptr;
+  d->threshold = 0;
+  d->scale = 1.0f;
+  if (!drop) return MOE_OK;
+  if (!(drop->p >= 0.0 && drop->p < 1.0)) return MOE_ERR_INVALID_ARGUMENT;  // NaN too
+  if (!drop->rng || !aligned(drop->rng, 8)) return MOE_ERR_INVALID_ARGUMENT;
+  d->rng = drop->rng;
+  d->threshold = (uint32_t)(drop->p * 4294967296.0);
+  d->scale = (float)(1.0 / (1.0 - drop->p));
+  return MOE_OK;
+}
+
+// Problem and layer of a gradient of the grouped GEMM.
+moe_status_t check_grad_gemm(const moe_problem_t* p, int32_t layer) {
+  const moe_status_t st = check_problem(p);
+  if (st != MOE_OK) return st;
+  if (layer != 0 && layer != 1) return MOE_ERR_INVALID_ARGUMENT;
+  return is_mx(p) ? MOE_ERR_UNSUPPORTED : MOE_OK;
+}
+
+GradGemmArgs grad_args(const moe_problem_t* p, const int32_t* offsets) {
+  GradGemmArgs g{};
+  g.offsets = offsets;
+  g.R = p->num_tokens * p->topk;
+  g.H = p->hidden;
+  g.F = p->ffn;
+  g.E = held(p);
+  g.G = segments(p);
+  g.shuffle = debug_shuffle();
+  return g;
+}
+
 template <typename T>
 T* at(void* ws, size_t off) {
   return reinterpret_cast<T*>(reinterpret_cast<char*>(ws) + off);
@@ -323,7 +385,7 @@ T* at(void* ws, size_t off) {
 
 extern "C" {
 
-int32_t moe_abi_version(void) { return (2 << 16) | 2; }
+int32_t moe_abi_version(void) { return (2 << 16) | 3; }
 
 const char* moe_status_string(moe_status_t s) {
   switch (s) {
@@ -343,6 +405,7 @@ size_t moe_workspace_bytes(const moe_problem_t* p, int32_t op) {
     case MOE_OP_DISPATCH: return permute_ws_bytes(plan_of(p));
     case MOE_OP_GROUPED_GEMM: return p->dtype == MOE_DTYPE_BF16 ? gemm_split_ws_bytes() : 0;
     case MOE_OP_LAYER: return layer_ws(p).total;
+    case MOE_OP_GROUPED_GEMM_BACKWARD: return 0;
     case MOE_OP_LAYER_DECODE: return check_decode(p) == MOE_OK ? decode_ws(p, split_of(p)).total : 0;
   }
   return 0;
@@ -731,6 +794,214 @@ moe_status_t moe_adapter_linear(const moe_adapter_problem_t* q, const void* x, c
   g.idx = adapter_idx;
   g.t = need > 0 ? ws : nullptr;
   return hip_status(launch_adapter_linear(g, f32, (hipStream_t)stream));
+}
+
+moe_status_t moe_combine_dropout(const moe_problem_t* p, const float* y, const float* topk_w,
+                                 const int32_t* flat_to_sorted, const moe_epilogue_t* epi, const moe_dropout_t* drop,
+                                 void* out, void* stream) {
+  moe_status_t st = check_problem(p);
+  if (st != MOE_OK) return st;
+  Dropout d;
+  OutEpilogue ep;
+  if ((st = dropout_of(drop, &d)) != MOE_OK || (st = epilogue_of(p, epi, out, &ep)) != MOE_OK) return st;
+  if (p->num_tokens == 0) return MOE_OK;
+  const int64_t R = p->num_tokens * p->topk, n = p->num_tokens * p->hidden;
+  const Span s[] = {{y, (size_t)R * p->hidden * 4, false}, {out, (size_t)n * (ep.out_bf16 ? 2 : 4), true}};
+  if ((st = check_spans(s, 2)) != MOE_OK || (st = check_words(topk_w, (size_t)R * 4, s, 2)) != MOE_OK ||
+      (st = check_words(flat_to_sorted, (size_t)R * 4, s, 2)) != MOE_OK ||
+      (st = check_words(d.rng, d.rng ? 16 : 0, s, 2)) != MOE_OK)
+    return st;
+  if (residual_clash(ep, n)) return MOE_ERR_INVALID_ARGUMENT;
+  if (debug_validate()) {
+    st = check_range(flat_to_sorted, R, -1, (int32_t)R, (hipStream_t)stream);
+    if (st != MOE_OK) return st;
+  }
+  return hip_status(launch_combine(y, topk_w, flat_to_sorted, p->num_tokens, p->hidden, p->topk, ep,
+                                   (hipStream_t)stream, d.rng ? &d : nullptr));
+}
+
+moe_status_t moe_combine_backward(const moe_problem_t* p, const void* dout, int32_t dout_dtype, const float* y,
+                                  const float* topk_w, const int32_t* flat_to_sorted, const moe_dropout_t* drop,
+                                  void* dy, float* dtopk_w, void* stream) {
+  moe_status_t st = check_problem(p);
+  if (st != MOE_OK) return st;
+  CombineBackwardArgs a;
+  if ((st = dropout_of(drop, &a.drop)) != MOE_OK) return st;
+  if (dout_dtype != MOE_DTYPE_F32 && dout_dtype != MOE_DTYPE_BF16) return MOE_ERR_INVALID_ARGUMENT;
+  if (p->num_tokens == 0) return MOE_OK;
+  const int64_t R = p->num_tokens * p->topk, n = p->num_tokens * p->hidden;
+  // dtopk_w is an output, but as the other per-pair arrays 4-byte aligned
+  const Span s[] = {{dout, (size_t)n * (dout_dtype == MOE_DTYPE_BF16 ? 2 : 4), false},
+                    {y, (size_t)R * p->hidden * 4, false},
+                    {dy, (size_t)R * p->hidden * elem_bytes(p), true}};
+  const Span w[] = {{dtopk_w, (size_t)R * 4, true}};
+  if ((st = check_spans(s, 3)) != MOE_OK || (st = check_words(dtopk_w, (size_t)R * 4, s, 3)) != MOE_OK) return st;
+  for (const Span& b : s)
+    if (overlap(dtopk_w, (size_t)R * 4, b.p, b.n)) return MOE_ERR_INVALID_ARGUMENT;
+  const void* words[] = {topk_w, flat_to_sorted};
+  for (const void* b : words)
+    if ((st = check_words(b, (size_t)R * 4, s, 3)) != MOE_OK || (st = check_words(b, (size_t)R * 4, w, 1)) != MOE_OK)
+      return st;
+  if (a.drop.rng && ((st = check_words(a.drop.rng, 16, s, 3)) != MOE_OK || (st = check_words(a.drop.rng, 16, w, 1)) != MOE_OK))
+    return st;
+  if (debug_validate()) {
+    st = check_range(flat_to_sorted, R, -1, (int32_t)R, (hipStream_t)stream);
+    if (st != MOE_OK) return st;
+  }
+  a.dout = dout;
+  a.dout_bf16 = dout_dtype == MOE_DTYPE_BF16;
+  a.y = y;
+  a.topk_w = topk_w;
+  a.f2s = flat_to_sorted;
+  a.dy = dy;
+  a.dy_bf16 = p->dtype != MOE_DTYPE_F32;
+  a.dtopk_w = dtopk_w;
+  a.M = p->num_tokens;
+  a.H = p->hidden;
+  a.k = p->topk;
+  return hip_status(launch_combine_backward(a, (hipStream_t)stream));
+}
+
+moe_status_t moe_dispatch_backward(const moe_problem_t* p, const void* dx_perm, const int32_t* flat_to_sorted,
+                                   const moe_epilogue_t* epi, void* dx, void* stream) {
+  moe_status_t st = check_problem(p);
+  if (st != MOE_OK) return st;
+  OutEpilogue ep;
+  if ((st = epilogue_of(p, epi, dx, &ep)) != MOE_OK) return st;
+  if (p->num_tokens == 0) return MOE_OK;
+  const int64_t R = p->num_tokens * p->topk, n = p->num_tokens * p->hidden;
+  const Span s[] = {{dx_perm, (size_t)R * p->hidden * elem_bytes(p), false},
+                    {dx, (size_t)n * (ep.out_bf16 ? 2 : 4), true}};
+  if ((st = check_spans(s, 2)) != MOE_OK || (st = check_words(flat_to_sorted, (size_t)R * 4, s, 2)) != MOE_OK) return st;
+  if (residual_clash(ep, n)) return MOE_ERR_INVALID_ARGUMENT;
+  if (debug_validate()) {
+    st = check_range(flat_to_sorted, R, -1, (int32_t)R, (hipStream_t)stream);
+    if (st != MOE_OK) return st;
+  }
+  return hip_status(launch_dispatch_backward(dx_perm, p->dtype != MOE_DTYPE_F32, flat_to_sorted, p->num_tokens,
+                                             p->hidden, p->topk, ep, (hipStream_t)stream));
+}
+
+moe_status_t moe_route_backward(const moe_problem_t* p, const int32_t* topk_idx, const float* topk_w,
+                                const float* dtopk_w, float* dlogits, void* stream) {
+  moe_status_t st = check_problem(p);
+  if (st != MOE_OK) return st;
+  if (p->num_tokens == 0) return MOE_OK;
+  const int64_t R = p->num_tokens * p->topk;
+  const Span s[] = {{dlogits, (size_t)p->num_tokens * p->num_experts * 4, true}};
+  if ((st = check_spans(s, 1)) != MOE_OK || (st = check_words(topk_idx, (size_t)R * 4, s, 1)) != MOE_OK ||
+      (st = check_words(topk_w, (size_t)R * 4, s, 1)) != MOE_OK ||
+      (st = check_words(dtopk_w, (size_t)R * 4, s, 1)) != MOE_OK)
+    return st;
+  if (debug_validate()) {
+    st = check_range(topk_idx, R, 0, p->num_experts, (hipStream_t)stream);
+    if (st != MOE_OK) return st;
+  }
+  return hip_status(launch_route_backward(topk_idx, topk_w, dtopk_w, p->num_tokens, p->num_experts, p->topk, dlogits,
+                                          (hipStream_t)stream));
+}
+
+moe_status_t moe_grouped_gemm_aux(const moe_problem_t* p, const void* a, const void* w0, const void* w1,
+                                  const int32_t* offsets, void* gate, void* up, void* c, void* stream) {
+  moe_status_t st = check_grad_gemm(p, 0);
+  if (st != MOE_OK) return st;
+  const int64_t R = p->num_tokens * p->topk;
+  const size_t nh = (size_t)R * p->hidden * elem_bytes(p), nf = (size_t)R * p->ffn * elem_bytes(p);
+  const size_t nw = (size_t)held(p) * p->hidden * p->ffn * elem_bytes(p);
+  const Span s[] = {{a, nh, false}, {w0, nw, false}, {w1, nw, false}, {gate, nf, true}, {up, nf, true}, {c, nf, true}};
+  if ((st = check_spans(s, 6)) != MOE_OK || (st = check_words(offsets, (size_t)(segments(p) + 1) * 4, s, 6)) != MOE_OK)
+    return st;
+  if (R == 0) return MOE_OK;
+  hipStream_t hs = (hipStream_t)stream;
+  if (debug_validate()) {
+    st = validate_offsets(p, offsets, hs);
+    if (st != MOE_OK) return st;
+  }
+  GemmProblem gp;
+  gp.layer = 0;
+  gp.a = a;
+  gp.w0 = w0;
+  gp.w1 = w1;
+  gp.offsets = offsets;
+  gp.c = c;
+  gp.R = R;
+  gp.K = p->hidden;
+  gp.N = p->ffn;
+  gp.E = held(p);
+  gp.G = segments(p);
+  gp.rowmap = combine_blocks(p);
+  gp.shuffle = debug_shuffle();
+  gp.gate = gate;
+  gp.up = up;
+  return hip_status(p->dtype == MOE_DTYPE_BF16 ? launch_grouped_gemm_bf16(gp, hs) : launch_grouped_gemm_f32(gp, hs));
+}
+
+moe_status_t moe_grouped_gemm_backward(const moe_problem_t* p, int32_t layer, const void* d0, const void* d1,
+                                       const void* w0, const void* w1, const void* gate, const void* up,
+                                       const int32_t* offsets, void* o0, void* o1, void* ws, size_t ws_bytes,
+                                       void* stream) {
+  moe_status_t st = check_grad_gemm(p, layer);
+  if (st != MOE_OK) return st;
+  const int64_t R = p->num_tokens * p->topk;
+  const size_t eb = elem_bytes(p), nh = (size_t)R * p->hidden * eb, nf = (size_t)R * p->ffn * eb;
+  const size_t nw = (size_t)held(p) * p->hidden * p->ffn * eb;
+  if (layer == 0 ? (gate || up || o1) : (d1 || w1)) return MOE_ERR_INVALID_ARGUMENT;
+  const Span rows1[] = {{d0, nh, false}, {w0, nw, false}, {gate, nf, false}, {up, nf, false}, {o0, nf, true}, {o1, nf, true}};
+  const Span rows0[] = {{d0, nf, false}, {d1, nf, false}, {w0, nw, false}, {w1, nw, false}, {o0, nh, true}};
+  const Span* s = layer == 0 ? rows0 : rows1;
+  const int n = layer == 0 ? 5 : 6;
+  if ((st = check_spans(s, n)) != MOE_OK || (st = check_words(offsets, (size_t)(segments(p) + 1) * 4, s, n)) != MOE_OK)
+    return st;
+  if (R == 0) return MOE_OK;
+  hipStream_t hs = (hipStream_t)stream;
+  if (debug_validate()) {
+    st = validate_offsets(p, offsets, hs);
+    if (st != MOE_OK) return st;
+  }
+  GradGemmArgs g = grad_args(p, offsets);
+  g.d0 = d0;
+  g.d1 = d1;
+  g.w0 = w0;
+  g.w1 = w1;
+  g.gate = gate;
+  g.up = up;
+  g.o0 = o0;
+  g.o1 = o1;
+  return hip_status(launch_grad_rows(g, layer, p->dtype == MOE_DTYPE_BF16, hs));
+}
+
+moe_status_t moe_grouped_gemm_backward_weights(const moe_problem_t* p, int32_t layer, const void* d0, const void* d1,
+                                               const void* a, const int32_t* offsets, int32_t dw_dtype,
+                                               int32_t accumulate, void* dw0, void* dw1, void* ws, size_t ws_bytes,
+                                               void* stream) {
+  moe_status_t st = check_grad_gemm(p, layer);
+  if (st != MOE_OK) return st;
+  if (dw_dtype != MOE_DTYPE_F32 && dw_dtype != MOE_DTYPE_BF16) return MOE_ERR_INVALID_ARGUMENT;
+  if (accumulate && dw_dtype != MOE_DTYPE_F32) return MOE_ERR_UNSUPPORTED;
+  const int64_t R = p->num_tokens * p->topk;
+  const size_t eb = elem_bytes(p), nh = (size_t)R * p->hidden * eb, nf = (size_t)R * p->ffn * eb;
+  const size_t nw = (size_t)held(p) * p->hidden * p->ffn * (dw_dtype == MOE_DTYPE_BF16 ? 2 : 4);
+  if (layer == 1 && (d1 || dw1)) return MOE_ERR_INVALID_ARGUMENT;
+  const Span w1[] = {{d0, nh, false}, {a, nf, false}, {dw0, nw, true}};
+  const Span w0[] = {{d0, nf, false}, {d1, nf, false}, {a, nh, false}, {dw0, nw, true}, {dw1, nw, true}};
+  const Span* s = layer == 0 ? w0 : w1;
+  const int n = layer == 0 ? 5 : 3;
+  if ((st = check_spans(s, n)) != MOE_OK || (st = check_words(offsets, (size_t)(segments(p) + 1) * 4, s, n)) != MOE_OK)
+    return st;
+  hipStream_t hs = (hipStream_t)stream;
+  if (debug_validate()) {
+    st = validate_offsets(p, offsets, hs);
+    if (st != MOE_OK) return st;
+  }
+  GradGemmArgs g = grad_args(p, offsets);
+  g.d0 = d0;
+  g.d1 = d1;
+  g.x = a;
+  g.o0 = dw0;
+  g.o1 = dw1;
+  g.out_bf16 = dw_dtype == MOE_DTYPE_BF16;
+  g.accumulate = accumulate != 0;
+  return hip_status(launch_grad_weights(g, layer, p->dtype == MOE_DTYPE_BF16, hs));
 }
 
 moe_status_t moe_quantize_mxfp8(int64_t rows, int32_t cols, int32_t src_dtype, const void* src, void* dst,

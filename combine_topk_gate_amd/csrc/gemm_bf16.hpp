@@ -54,6 +54,8 @@ struct Bf16GemmArgs {
   const __bf16* w0;  // layer 0: W_gate [E, F, H]; layer 1: W_down [E, H, F]
   const __bf16* w1;  // layer 0: W_up [E, F, H]
   void* c;           // layer 0: Hact [R, F] bf16 (or MXFP8 codes); layer 1: Y [R, H] f32
+  __bf16* gate = nullptr;  // KEEP: X W_gate^T and X W_up^T [R, F]
+  __bf16* up = nullptr;
   // MXFP8 (one e8m0 scale byte per 32 values along the reduction index,
   // stored in groups of 32 rows: the byte of row r, block b of a tensor of
   // `cols` columns sits at (r / 32) * cols + (b / 4) * 128 + (r % 32) * 4 +
@@ -94,8 +96,11 @@ __device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirs
 // segment made of the rows of several source blocks for one expert, whose
 // rows lie apart in the sorted order.  seg_rows and m0 then count the rows
 // of that combined segment, and seg_start is unused.
+//
+// KEEP (layer 0): the two products are stored as well, rounded to bf16, for
+// the gradient (Hact is formed from the f32 values as without it).
 template <int LAYER, bool GATHER = false, int TM = kTileRows, bool PARTIAL = false, bool OUT8 = false,
-          bool ROWMAP = false>
+          bool ROWMAP = false, bool KEEP = false>
 __device__ __forceinline__ void bf16_gemm_tile(const Bf16GemmArgs& p, int g, int seg_start, int seg_rows, int m0,
                                                int nt, char* __restrict__ lds, int k0 = 0, int k1 = -1,
                                                float* __restrict__ part = nullptr,
@@ -104,6 +109,7 @@ __device__ __forceinline__ void bf16_gemm_tile(const Bf16GemmArgs& p, int g, int
   static_assert(TM == 256 || TM == 128, "token tile height");
   static_assert(!PARTIAL || (TM == 256 && LAYER == 1), "partial tiles: layer 1, full height");
   static_assert(!OUT8 || (LAYER == 0 && !PARTIAL), "MXFP8 output: layer 0");
+  static_assert(!KEEP || (LAYER == 0 && !OUT8), "kept products: bf16 layer 0");
   constexpr int NJ = TM / 64;      // token fragments per wave
   constexpr int XI = TM / 32;      // token-row loads per thread per K step
   constexpr int XQ = XI / 4;       // ... per sub-step
@@ -490,38 +496,47 @@ __device__ __forceinline__ void bf16_gemm_tile(const Bf16GemmArgs& p, int g, int
   } else if (LAYER == 0) {
     // 256 B per staged row (128 bf16 columns); 8-byte unit u of row t at
     // unit u ^ (t & 31): conflict-free for 32 rows writing the same unit.
-    char* stg = lds;
+    auto stage = [&](char* stg, auto value) {
 #pragma unroll
-    for (int nj = 0; nj < NJ; ++nj) {
-      const int t = wm * (TM / 2) + nj * 32 + lrow;
+      for (int nj = 0; nj < NJ; ++nj) {
+        const int t = wm * (TM / 2) + nj * 32 + lrow;
 #pragma unroll
-      for (int mi = 0; mi < 2; ++mi) {
+        for (int mi = 0; mi < 2; ++mi) {
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          bf16x4_t h;
+          for (int q = 0; q < 4; ++q) {
+            bf16x4_t h;
 #pragma unroll
-          for (int v = 0; v < 4; ++v) {
-            const float gt = acc[mi][nj][4 * q + v], up = acc[mi + 2][nj][4 * q + v];
-            h[v] = (__bf16)silu_mul_fast(gt, up);
+            for (int v = 0; v < 4; ++v) h[v] = (__bf16)value(acc[mi][nj][4 * q + v], acc[mi + 2][nj][4 * q + v]);
+            const int u = wn * 16 + mi * 8 + 2 * q + lk;
+            *reinterpret_cast<bf16x4_t*>(stg + t * 256 + ((u ^ (t & 31)) << 3)) = h;
           }
-          const int u = wn * 16 + mi * 8 + 2 * q + lk;
-          *reinterpret_cast<bf16x4_t*>(stg + t * 256 + ((u ^ (t & 31)) << 3)) = h;
         }
       }
-    }
-    __syncthreads();
+    };
     // 16 threads per row, 16 B (8 columns) each: chunk c of row t sits at
     // chunk c ^ ((t & 31) >> 1), its two halves swapped when t is odd.
-    __bf16* hact = reinterpret_cast<__bf16*>(p.c);
     const int c = tid & 15;
     const int f = col0 + 8 * c;
+    auto store = [&](const char* stg, __bf16* dst) {
 #pragma unroll 4
-    for (int t = tid >> 4; t < TM; t += kGemmThreads / 16) {
-      i32x4_t v = *reinterpret_cast<const i32x4_t*>(stg + t * 256 + ((c ^ ((t & 31) >> 1)) << 4));
-      if (t & 1) v = i32x4_t{v[2], v[3], v[0], v[1]};
-      const int trow = m0 + t;
-      if (trow < seg_rows && f < N)
-        *reinterpret_cast<i32x4_t*>(hact + (int64_t)(ROWMAP ? rowpos[t] : seg_start + trow) * N + f) = v;
+      for (int t = tid >> 4; t < TM; t += kGemmThreads / 16) {
+        i32x4_t v = *reinterpret_cast<const i32x4_t*>(stg + t * 256 + ((c ^ ((t & 31) >> 1)) << 4));
+        if (t & 1) v = i32x4_t{v[2], v[3], v[0], v[1]};
+        const int trow = m0 + t;
+        if (trow < seg_rows && f < N)
+          *reinterpret_cast<i32x4_t*>(dst + (int64_t)(ROWMAP ? rowpos[t] : seg_start + trow) * N + f) = v;
+      }
+    };
+    stage(lds, [](float gt, float up) { return silu_mul_fast(gt, up); });
+    if constexpr (KEEP) stage(lds + kStageBytes, [](float gt, float) { return gt; });  // the other half of the LDS
+    __syncthreads();
+    store(lds, reinterpret_cast<__bf16*>(p.c));
+    if constexpr (KEEP) {
+      store(lds + kStageBytes, p.gate);
+      __syncthreads();
+      stage(lds, [](float, float up) { return up; });
+      __syncthreads();
+      store(lds, p.up);
     }
     __syncthreads();
   } else {
@@ -574,16 +589,16 @@ __device__ __forceinline__ void bf16_gemm_tile(const Bf16GemmArgs& p, int g, int
 // running at once on an XCD stay in step and share the segment's weight
 // panels in its L2 (measured: halving those last tiles cost more in
 // re-read weights than it saved).
-template <int LAYER, bool GATHER = false, bool OUT8 = false, bool ROWMAP = false>
+template <int LAYER, bool GATHER = false, bool OUT8 = false, bool ROWMAP = false, bool KEEP = false>
 __device__ __forceinline__ void bf16_gemm_row_tile(const Bf16GemmArgs& p, int g, int seg_start, int seg_rows, int m0,
                                                    int nt, char* __restrict__ lds,
                                                    const int* __restrict__ rowpos = nullptr) {
   if (seg_rows <= kTileRows / 2)
-    bf16_gemm_tile<LAYER, GATHER, kTileRows / 2, false, OUT8, ROWMAP>(p, g, seg_start, seg_rows, m0, nt, lds, 0, -1,
-                                                                      nullptr, rowpos);
+    bf16_gemm_tile<LAYER, GATHER, kTileRows / 2, false, OUT8, ROWMAP, KEEP>(p, g, seg_start, seg_rows, m0, nt, lds, 0,
+                                                                            -1, nullptr, rowpos);
   else
-    bf16_gemm_tile<LAYER, GATHER, kTileRows, false, OUT8, ROWMAP>(p, g, seg_start, seg_rows, m0, nt, lds, 0, -1,
-                                                                  nullptr, rowpos);
+    bf16_gemm_tile<LAYER, GATHER, kTileRows, false, OUT8, ROWMAP, KEEP>(p, g, seg_start, seg_rows, m0, nt, lds, 0, -1,
+                                                                        nullptr, rowpos);
 }
 
 }  // namespace moe

@@ -54,7 +54,8 @@ __device__ __forceinline__ bool split_pays(int nk, int s, bool halfable) {
 // always splits the same tiles the same way.
 // OUT8 (layer 0): Hact is written in MXFP8 (codes to args.c, scales to
 // args.c_scale) for the MXFP8 Layer1 below.
-template <int LAYER, bool OUT8 = false>
+// KEEP (layer 0): the gate and up products are stored too.
+template <int LAYER, bool OUT8 = false, bool KEEP = false>
 __global__ __launch_bounds__(kGemmThreads) void grouped_gemm_bf16_kernel(Bf16GemmArgs args,
                                                                          const int32_t* __restrict__ offsets, int G,
                                                                          int xcd_slots, SplitWs split,
@@ -107,14 +108,14 @@ __global__ __launch_bounds__(kGemmThreads) void grouped_gemm_bf16_kernel(Bf16Gem
   for (int v = xcd_slot(blockIdx.x, grid); v < entries; v += grid) {
     if (v < T - half) {
       const TileCoord c = tile_coord(shuffled(sm, v), G, NT, kTileRows, xcd_slots, rtb, tl);
-      bf16_gemm_row_tile<LAYER, false, OUT8>(args, c.g, tl.seg_start[c.g], tl.seg_rows[c.g], c.m0, c.nt, lds);
+      bf16_gemm_row_tile<LAYER, false, OUT8, false, KEEP>(args, c.g, tl.seg_start[c.g], tl.seg_rows[c.g], c.m0, c.nt, lds);
     } else {
       const int j = v - (T - half);
       const TileCoord c = tile_coord(T - half + shuffled(sh, j / 2), G, NT, kTileRows, xcd_slots, rtb, tl);
       const int m0 = c.m0 + (j & 1) * (kTileRows / 2);
       if (m0 < tl.seg_rows[c.g])
-        bf16_gemm_tile<LAYER, false, kTileRows / 2, false, OUT8>(args, c.g, tl.seg_start[c.g], tl.seg_rows[c.g], m0,
-                                                                 c.nt, lds);
+        bf16_gemm_tile<LAYER, false, kTileRows / 2, false, OUT8, false, KEEP>(args, c.g, tl.seg_start[c.g],
+                                                                              tl.seg_rows[c.g], m0, c.nt, lds);
     }
   }
 }
@@ -130,7 +131,7 @@ __global__ __launch_bounds__(kGemmThreads) void grouped_gemm_bf16_kernel(Bf16Gem
 // same static schedule and last-round halves as the kernel above; no split
 // along k.  Every element is computed as in any other tile, so the bits do
 // not change.
-template <int LAYER>
+template <int LAYER, bool KEEP = false>
 __global__ __launch_bounds__(kGemmThreads) void grouped_gemm_bf16_expert_kernel(Bf16GemmArgs args,
                                                                                 const int32_t* __restrict__ offsets,
                                                                                 int G, int xcd_slots,
@@ -158,10 +159,10 @@ __global__ __launch_bounds__(kGemmThreads) void grouped_gemm_bf16_expert_kernel(
     rowpos[threadIdx.x] = expert_row(tl, c.g, EL, S, m0, threadIdx.x);
     __syncthreads();
     if (is_half)
-      bf16_gemm_tile<LAYER, false, kTileRows / 2, false, false, true>(args, c.g, 0, n, m0, c.nt, lds, 0, -1, nullptr,
-                                                                      rowpos);
+      bf16_gemm_tile<LAYER, false, kTileRows / 2, false, false, true, KEEP>(args, c.g, 0, n, m0, c.nt, lds, 0, -1,
+                                                                            nullptr, rowpos);
     else
-      bf16_gemm_row_tile<LAYER, false, false, true>(args, c.g, 0, n, m0, c.nt, lds, rowpos);
+      bf16_gemm_row_tile<LAYER, false, false, true, KEEP>(args, c.g, 0, n, m0, c.nt, lds, rowpos);
   }
 }
 
@@ -304,7 +305,8 @@ __global__ __launch_bounds__(256) void grouped_gemm_f32_kernel(const float* __re
                                                                const float* __restrict__ W0,
                                                                const float* __restrict__ W1, float* __restrict__ C,
                                                                int K, int N, int E, const int32_t* __restrict__ offsets,
-                                                               int G, uint32_t shuffle) {
+                                                               int G, uint32_t shuffle, float* __restrict__ gate,
+                                                               float* __restrict__ up) {
   __shared__ float xs[kF32Rows][kF32BK + 1];
   __shared__ float ws[kF32Rows][kF32BK + 1];
   __shared__ TileLds tl;
@@ -359,7 +361,12 @@ __global__ __launch_bounds__(256) void grouped_gemm_f32_kernel(const float* __re
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
           const int f = col0 + tx + 16 * i;
-          if (f < N) dst[f] = silu_f32(acc[i][j]) * acc[i + 2][j];
+          if (f >= N) continue;
+          dst[f] = silu_f32(acc[i][j]) * acc[i + 2][j];
+          if (gate) {
+            gate[(int64_t)(s0 + tr) * N + f] = acc[i][j];
+            up[(int64_t)(s0 + tr) * N + f] = acc[i + 2][j];
+          }
         }
       } else {
 #pragma unroll
@@ -398,6 +405,8 @@ hipError_t launch_grouped_gemm_bf16(const GemmProblem& gp, hipStream_t s) {
   a.w0 = (const __bf16*)gp.w0;
   a.w1 = (const __bf16*)gp.w1;
   a.c = gp.c;
+  a.gate = (__bf16*)gp.gate;
+  a.up = (__bf16*)gp.up;
   a.K = gp.K;
   a.N = gp.N;
   a.E = gp.E;
@@ -412,7 +421,10 @@ hipError_t launch_grouped_gemm_bf16(const GemmProblem& gp, hipStream_t s) {
   const int xcd_slots = grid / kXcds > 0 ? grid / kXcds : 1;
   if (gp.rowmap) {
     a.M = gp.R;  // rows of the token-row buffer, read at their own positions
-    if (gp.layer == 0)
+    if (gp.gate)
+      grouped_gemm_bf16_expert_kernel<0, true><<<grid, kGemmThreads, 0, s>>>(a, gp.offsets, gp.G, xcd_slots,
+                                                                             gp.shuffle);
+    else if (gp.layer == 0)
       grouped_gemm_bf16_expert_kernel<0><<<grid, kGemmThreads, 0, s>>>(a, gp.offsets, gp.G, xcd_slots, gp.shuffle);
     else
       grouped_gemm_bf16_expert_kernel<1><<<grid, kGemmThreads, 0, s>>>(a, gp.offsets, gp.G, xcd_slots, gp.shuffle);
@@ -426,7 +438,10 @@ hipError_t launch_grouped_gemm_bf16(const GemmProblem& gp, hipStream_t s) {
     sp.desc = sp.hdr + 4;
     sp.part = reinterpret_cast<float*>(w + kSplitHdrBytes);
   }
-  if (gp.layer == 0)
+  if (gp.gate)
+    grouped_gemm_bf16_kernel<0, false, true><<<grid, kGemmThreads, 0, s>>>(a, gp.offsets, gp.G, xcd_slots, sp,
+                                                                           gp.shuffle);
+  else if (gp.layer == 0)
     grouped_gemm_bf16_kernel<0><<<grid, kGemmThreads, 0, s>>>(a, gp.offsets, gp.G, xcd_slots, sp, gp.shuffle);
   else
     grouped_gemm_bf16_kernel<1><<<grid, kGemmThreads, 0, s>>>(a, gp.offsets, gp.G, xcd_slots, sp, gp.shuffle);
@@ -492,10 +507,11 @@ hipError_t launch_grouped_gemm_f32(const GemmProblem& gp, hipStream_t s) {
   const int grid = device_cu_count() * 2;
   if (gp.layer == 0)
     grouped_gemm_f32_kernel<0><<<grid, 256, 0, s>>>((const float*)gp.a, (const float*)gp.w0, (const float*)gp.w1,
-                                                     (float*)gp.c, gp.K, gp.N, gp.E, gp.offsets, gp.G, gp.shuffle);
+                                                     (float*)gp.c, gp.K, gp.N, gp.E, gp.offsets, gp.G, gp.shuffle,
+                                                     (float*)gp.gate, (float*)gp.up);
   else
     grouped_gemm_f32_kernel<1><<<grid, 256, 0, s>>>((const float*)gp.a, (const float*)gp.w0, nullptr,
-                                                    (float*)gp.c, gp.K, gp.N, gp.E, gp.offsets, gp.G, gp.shuffle);
+                                                    (float*)gp.c, gp.K, gp.N, gp.E, gp.offsets, gp.G, gp.shuffle, nullptr, nullptr);
   return hipGetLastError();
 }
 

@@ -1,0 +1,191 @@
+// Gradients of the experts' products (grouped GEMM), rows and weights.
+//
+// "Grouped GEMM 为什么适合 MoE" (C_i = A_i B_i per expert) transposed: with the
+// forward g = X Wg^T, u = X Wu^T, h = silu(g) u, Y = h Wd^T per expert,
+//   rows, layer 1     dh = dY Wd;  s = 1 / (1 + e^-g);
+//                     dg = dh u s (1 + g (1 - s)),  du = dh g s
+//   rows, layer 0     dX = dg Wg + du Wu
+//   weights, layer 1  dWd = dY^T h
+//   weights, layer 0  dWg = dg^T X,  dWu = du^T X   (the sums run over rows)
+// A static tile queue as in the forward grouped GEMM; each output element is
+// formed by one workgroup in a fixed order, so nothing depends on scheduling.
+#include "common.hpp"
+#include "gemm_grad_f32.hpp"
+#include "launch.hpp"
+#include "tiles.hpp"
+
+namespace moe {
+
+// d silu(g) u / dg and / du times dh, in f32
+struct SwigluGrad {
+  float dg, du;
+};
+__device__ __forceinline__ SwigluGrad swiglu_grad(float dh, float g, float u) {
+  const float s = 1.0f / (1.0f + expf(-g));
+  return {dh * u * (s * fmaf(g, 1.0f - s, 1.0f)), dh * (g * s)};
+}
+
+// ------------------------------------------------------------------- rows ---
+template <int LAYER, typename T, int TS>
+__global__ __launch_bounds__(kGfThreads) void grad_rows_f32_kernel(GradGemmArgs a) {
+  __shared__ __attribute__((aligned(16))) float lds[gf_lds_floats<TS>];
+  __shared__ TileLds tl;
+  __shared__ int rowpos[TS];
+  const int K = LAYER == 0 ? a.F : a.H, N = LAYER == 0 ? a.H : a.F;  // reduction and columns of a product
+  const int NT = (N + TS - 1) / TS, S = a.G / a.E;
+  const int total = build_expert_tile_table(a.offsets, a.G, a.E, TS, tl) * NT;
+  const Shuffle sm = make_shuffle(a.shuffle, total);
+  constexpr int kBuf = kGfK * gf_pitch<TS>;
+  for (int v = blockIdx.x; v < total; v += gridDim.x) {
+    const TileCoord c = tile_coord(shuffled(sm, v), a.E, NT, TS, 1, 0, tl);
+    const int e = c.g, col0 = c.nt * TS;
+    for (int i = threadIdx.x; i < TS; i += kGfThreads) rowpos[i] = expert_row(tl, e, a.E, S, c.m0, i);
+    __syncthreads();
+    const T* rows0[TS / 32];
+    const T* rows1[TS / 32];
+#pragma unroll
+    for (int i = 0; i < TS / 32; ++i) {
+      const int r = rowpos[(threadIdx.x >> 3) + 32 * i];
+      rows0[i] = r >= 0 ? (const T*)a.d0 + (int64_t)r * K : nullptr;
+      rows1[i] = LAYER == 0 && r >= 0 ? (const T*)a.d1 + (int64_t)r * K : nullptr;
+    }
+    const T* w0 = (const T*)a.w0 + (int64_t)e * K * N;
+    const T* w1 = LAYER == 0 ? (const T*)a.w1 + (int64_t)e * K * N : nullptr;
+    const int per = K / kGfK, steps = LAYER == 0 ? 2 * per : per;
+    GfPart<TS> pw, px;
+    auto load = [&](int s) {
+      const bool second = LAYER == 0 && s >= per;
+      const int k = (second ? s - per : s) * kGfK;
+      gf_load_k<TS, T>(px, second ? rows1 : rows0, k);
+      gf_load_c<TS, T>(pw, (second ? w1 : w0) + (int64_t)k * N, N, kGfK, col0, N);
+    };
+    auto store = [&](int b) {
+      gf_store_c<TS>(lds + b * 2 * kBuf, pw);
+      gf_store_k<TS>(lds + b * 2 * kBuf + kBuf, px);
+    };
+    GfAcc<TS> acc;
+    gf_zero(acc);
+    load(0);
+    store(0);
+    __syncthreads();
+    for (int s = 0; s < steps; ++s) {
+      if (s + 1 < steps) load(s + 1);
+      gf_mul<TS>(acc, lds + (s & 1) * 2 * kBuf, lds + (s & 1) * 2 * kBuf + kBuf);
+      if (s + 1 < steps) store((s + 1) & 1);
+      __syncthreads();
+    }
+    gf_each<TS>(acc, [&](int t, int n, f32x4_t o) {
+      const int r = rowpos[t];
+      if (r < 0 || col0 + n >= N) return;
+      const int64_t at = (int64_t)r * N + col0 + n;
+      if constexpr (LAYER == 0) {
+        gf_store4((T*)a.o0 + at, o);
+      } else {
+        const f32x4_t g = gf_load4((const T*)a.gate + at), u = gf_load4((const T*)a.up + at);
+        f32x4_t dg, du;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const SwigluGrad d = swiglu_grad(o[i], g[i], u[i]);
+          dg[i] = d.dg;
+          du[i] = d.du;
+        }
+        gf_store4((T*)a.o0 + at, dg);
+        gf_store4((T*)a.o1 + at, du);
+      }
+    });
+    __syncthreads();  // rowpos and the LDS buffers are free for the next tile
+  }
+}
+
+// ---------------------------------------------------------------- weights ---
+// Tile of dW[e]: TS of the first operand's columns (its rows) x TS of x's.
+// The K steps run over the expert's segments one after the other, the last
+// step of each filled up with zero rows.
+template <int LAYER, typename T, int TS>
+__global__ __launch_bounds__(kGfThreads) void grad_weights_f32_kernel(GradGemmArgs a) {
+  __shared__ __attribute__((aligned(16))) float lds[gf_lds_floats<TS>];
+  const int N = LAYER == 0 ? a.F : a.H, C = LAYER == 0 ? a.H : a.F;  // rows and columns of dW
+  const int NR = (N + TS - 1) / TS, NC = (C + TS - 1) / TS, S = a.G / a.E;
+  const int mats = LAYER == 0 ? 2 : 1;
+  const int64_t total = (int64_t)a.E * mats * NR * NC;
+  constexpr int kBuf = kGfK * gf_pitch<TS>;
+  for (int64_t v = blockIdx.x; v < total; v += gridDim.x) {
+    const int e = (int)(v / ((int64_t)mats * NR * NC));
+    int l = (int)(v - (int64_t)e * mats * NR * NC);
+    const int m = l / (NR * NC);
+    l -= m * NR * NC;
+    const int row0 = l % NR * TS, col0 = l / NR * TS;
+    const T* d = (const T*)(m ? a.d1 : a.d0);
+    int s = 0, r = 0, end = 0;  // the segment being read, its next row and its end
+    auto next_segment = [&] {  // to the first unread row; false: none left
+      while (r >= end && s < S) {
+        r = a.offsets[s * a.E + e];
+        end = a.offsets[s * a.E + e + 1];
+        ++s;
+      }
+      return r < end;
+    };
+    GfPart<TS> pw, px;
+    auto load = [&] {
+      const int n = end - r;
+      gf_load_c<TS, T>(pw, (const T*)a.x + (int64_t)r * C, C, n, col0, C);
+      gf_load_c<TS, T>(px, d + (int64_t)r * N, N, n, row0, N);
+      r += kGfK;
+    };
+    auto store = [&](int b) {
+      gf_store_c<TS>(lds + b * 2 * kBuf, pw);
+      gf_store_c<TS>(lds + b * 2 * kBuf + kBuf, px);
+    };
+    GfAcc<TS> acc;
+    gf_zero(acc);
+    bool more = next_segment();
+    if (more) {
+      load();
+      store(0);
+    }
+    __syncthreads();
+    for (int b = 0; more; b ^= 1) {
+      more = next_segment();
+      if (more) load();
+      gf_mul<TS>(acc, lds + b * 2 * kBuf, lds + b * 2 * kBuf + kBuf);
+      if (more) store(b ^ 1);
+      __syncthreads();
+    }
+    void* out = m ? a.o1 : a.o0;
+    gf_each<TS>(acc, [&](int t, int n, f32x4_t o) {
+      if (row0 + t >= N || col0 + n >= C) return;
+      const int64_t at = ((int64_t)e * N + row0 + t) * C + col0 + n;
+      if (a.out_bf16) {
+        gf_store4((__bf16*)out + at, o);
+      } else {
+        float* p = (float*)out + at;
+        gf_store4(p, a.accumulate ? *(const f32x4_t*)p + o : o);
+      }
+    });
+  }
+}
+
+template <int LAYER, typename T>
+hipError_t grad_rows_launch(const GradGemmArgs& a, hipStream_t s) {
+  grad_rows_f32_kernel<LAYER, T, 64><<<2 * device_cu_count(), kGfThreads, 0, s>>>(a);
+  return hipGetLastError();
+}
+
+hipError_t launch_grad_rows(const GradGemmArgs& a, int layer, bool bf16, hipStream_t s) {
+  if (a.R == 0) return hipSuccess;
+  if (bf16) return layer == 0 ? grad_rows_launch<0, __bf16>(a, s) : grad_rows_launch<1, __bf16>(a, s);
+  return layer == 0 ? grad_rows_launch<0, float>(a, s) : grad_rows_launch<1, float>(a, s);
+}
+
+template <int LAYER, typename T>
+hipError_t grad_weights_launch(const GradGemmArgs& a, hipStream_t s) {
+  grad_weights_f32_kernel<LAYER, T, 64><<<2 * device_cu_count(), kGfThreads, 0, s>>>(a);
+  return hipGetLastError();
+}
+
+hipError_t launch_grad_weights(const GradGemmArgs& a, int layer, bool bf16, hipStream_t s) {
+  if (bf16) return layer == 0 ? grad_weights_launch<0, __bf16>(a, s) : grad_weights_launch<1, __bf16>(a, s);
+  return layer == 0 ? grad_weights_launch<0, float>(a, s) : grad_weights_launch<1, float>(a, s);
+}
+
+}  // namespace moe

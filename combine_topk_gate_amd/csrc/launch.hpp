@@ -7,6 +7,7 @@
 #include <stdint.h>
 
 #include "common.hpp"
+#include "philox.hpp"
 
 namespace moe {
 
@@ -63,6 +64,8 @@ struct GemmProblem {
   size_t ws_bytes = 0;
   int rowmap = 0;           // bf16: each expert's segments of all source blocks as one (G / E of them)
   uint32_t shuffle = 0;     // nonzero: tiles in a seeded permutation of their order (debug check)
+  void* gate = nullptr;     // layer 0: X W_gate^T and X W_up^T are stored here too, both or neither
+  void* up = nullptr;
 };
 // Workspace that lets the bf16 grouped GEMM split its last round along K.
 size_t gemm_split_ws_bytes();
@@ -79,8 +82,52 @@ hipError_t launch_mx_quantize(const void* src, int src_bf16, int64_t rows, int c
 // and cols multiples of 64; bf16 (else f32) elements.
 hipError_t launch_transpose(const void* src, void* dst, int64_t batch, int rows, int cols, bool bf16, hipStream_t s);
 
+// drop (null: none): the dropout between the sum and the epilogue
 hipError_t launch_combine(const float* y, const float* topk_w, const int32_t* flat_to_sorted, int64_t M, int H,
-                          int k, const OutEpilogue& ep, hipStream_t s);
+                          int k, const OutEpilogue& ep, hipStream_t s, const Dropout* drop = nullptr);
+
+// Gradients of the combine, the dispatch and the router.
+struct CombineBackwardArgs {
+  const void* dout;  // [M,H] f32 or bf16
+  int dout_bf16;
+  const float* y;
+  const float* topk_w;
+  const int32_t* f2s;
+  Dropout drop;      // rng null: none
+  void* dy;          // [R,H] f32 or bf16
+  int dy_bf16;
+  float* dtopk_w;
+  int64_t M;
+  int H, k;
+};
+hipError_t launch_combine_backward(const CombineBackwardArgs& a, hipStream_t s);
+hipError_t launch_dispatch_backward(const void* dxp, bool bf16, const int32_t* f2s, int64_t M, int H, int k,
+                                    const OutEpilogue& ep, hipStream_t s);
+hipError_t launch_route_backward(const int32_t* idx, const float* w, const float* dw, int64_t M, int E, int k,
+                                 float* dlogits, hipStream_t s);
+
+// Gradients of the grouped GEMM.  Rows: layer 1 takes dY through W_down and
+// SwiGLU to the gradients of gate and up; layer 0 those through W_gate and
+// W_up to that of X_perm.  Weights: the products over each expert's rows.
+struct GradGemmArgs {
+  const void* d0;  // rows: dY [R,H] (layer 1) or dgate [R,F] (layer 0); weights: the same
+  const void* d1;  // layer 0: dup [R,F]
+  const void* w0;  // rows: W_down [E,H,F] or W_gate [E,F,H]
+  const void* w1;  // rows, layer 0: W_up [E,F,H]
+  const void* gate;  // rows, layer 1: [R,F]
+  const void* up;
+  const void* x;   // weights: Hact [R,F] (layer 1) or X_perm [R,H] (layer 0)
+  void* o0;        // rows: dgate [R,F] or dX_perm [R,H]; weights: dW_down [E,H,F] or dW_gate [E,F,H]
+  void* o1;        // rows, layer 1: dup [R,F]; weights, layer 0: dW_up [E,F,H]
+  const int32_t* offsets;
+  int64_t R;
+  int H, F, E, G;  // E: experts held
+  int out_bf16;    // weights: type of o0, o1
+  int accumulate;  // weights: add to what o0, o1 hold (f32)
+  uint32_t shuffle;
+};
+hipError_t launch_grad_rows(const GradGemmArgs& a, int layer, bool bf16, hipStream_t s);
+hipError_t launch_grad_weights(const GradGemmArgs& a, int layer, bool bf16, hipStream_t s);
 
 // Decode layer (at most MOE_DECODE_MAX_TOKENS tokens).
 struct DecodeSplit {

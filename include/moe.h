@@ -120,7 +120,13 @@ typedef enum {
 typedef enum { MOE_DTYPE_F32 = 0, MOE_DTYPE_BF16 = 1, MOE_DTYPE_BF16_MXFP8 = 2 } moe_dtype_t;
 
 /* Operation whose workspace moe_workspace_bytes sizes. */
-typedef enum { MOE_OP_DISPATCH = 0, MOE_OP_GROUPED_GEMM = 1, MOE_OP_LAYER = 2, MOE_OP_LAYER_DECODE = 3 } moe_op_t;
+typedef enum {
+  MOE_OP_DISPATCH = 0,
+  MOE_OP_GROUPED_GEMM = 1,
+  MOE_OP_LAYER = 2,
+  MOE_OP_LAYER_DECODE = 3,
+  MOE_OP_GROUPED_GEMM_BACKWARD = 4 /* moe_grouped_gemm_backward and ..._backward_weights */
+} moe_op_t;
 
 /*
  * Problem shape.  Limits: 0 <= M, M*k < 2^31; H and F multiples of 64 in
@@ -456,6 +462,125 @@ moe_status_t moe_adapter_linear(const moe_adapter_problem_t* q, const void* x, c
  * 256}: matrix-core; then rows and ranks of t's (0: no launch of its own).  All
  * 0 for no rows. */
 moe_status_t moe_adapter_tiles(const moe_adapter_problem_t* q, int32_t out_dtype, int32_t tiles[4]);
+
+/*
+ * Training: the gradients of the steps above ([COMET] §3.2, §4.1.1; [PTO] the
+ * seven serial stages, each transposed).  A training step is
+ *   forward   moe_route, moe_dispatch, moe_grouped_gemm_aux (layer 0, which
+ *             keeps gate and up), moe_grouped_gemm (layer 1),
+ *             moe_combine_dropout (or moe_combine_ex)
+ *   backward  moe_combine_backward (dY, dtopk_w), moe_grouped_gemm_backward and
+ *             ..._backward_weights with layer 1 (dgate, dup; dW_down), then with
+ *             layer 0 (dX_perm; dW_gate, dW_up), moe_dispatch_backward (dx),
+ *             moe_route_backward (dlogits)
+ * in MOE_DTYPE_BF16 or MOE_DTYPE_F32; the calls of the grouped GEMM return
+ * MOE_ERR_UNSUPPORTED for MOE_DTYPE_BF16_MXFP8, in the others its x is bf16.
+ * Sums are held in f32; a gradient in the problem's dtype is rounded once.
+ * With experts held elsewhere (local_experts), dropped pairs add nothing, and
+ * dx and dlogits are this call's shares of the sum over the holders.  Rows of
+ * per-pair buffers from offsets[G] on are neither read nor written.  No
+ * output overlaps an input or another output (MOE_ERR_INVALID_ARGUMENT), but
+ * for a residual as said.  Results do not depend on scheduling: no atomics.
+ * MOE_DEBUG_VALIDATE=1 checks flat_to_sorted, topk_idx and offsets as above.
+ */
+
+/* Dropout on the layer's output: out[t, n] stays where the 32-bit word of its
+ * place is at least floor(p 2^32) and is then multiplied by 1 / (1 - p) (f32),
+ * else it becomes 0.  The word is number n % 4 of the Philox 4x32-10 block
+ * (Salmon et al. 2011) with key {seed low, high} and counter {i low, i high,
+ * offset low, high}, i = (t H + n) / 4; the mask is never stored.  rng points
+ * to {seed, offset} in DEVICE memory (8-byte aligned), which the kernels read,
+ * so a captured graph can be given new ones before each replay.  0 <= p < 1. */
+typedef struct {
+  double p;
+  const uint64_t* rng;
+} moe_dropout_t;
+
+/* moe_combine_ex with the dropout between the sum and the epilogue: out[t, n] =
+ * cast(dropout(acc[t, n]) + residual[t, n]).  NULL drop: moe_combine_ex.  With
+ * EL < E every holder applies the same mask to its share.  out may be the
+ * residual itself (same type). */
+moe_status_t moe_combine_dropout(const moe_problem_t* p, const float* y, const float* topk_w,
+                                 const int32_t* flat_to_sorted, const moe_epilogue_t* epi, const moe_dropout_t* drop,
+                                 void* out, void* stream);
+
+/*
+ * Gradient of the combine (of the residual: dout itself).  With g[t, n] =
+ * dout[t, n], or under `drop` (NULL: none) the same mask's dout[t, n] / (1 - p)
+ * or 0, and r = flat_to_sorted[t*k + j]:
+ *   dy[r, n] = topk_w[t, j] g[t, n]               [R,H] dtype (f32, else bf16)
+ *   dtopk_w[t, j] = sum_n g[t, n] y[r, n], over the n that the mask keeps;
+ *                   0 for a dropped pair          [M,k] f32
+ *   dout [M,H] in dout_dtype (MOE_DTYPE_F32 or MOE_DTYPE_BF16); y [R,H] f32.
+ */
+moe_status_t moe_combine_backward(const moe_problem_t* p, const void* dout, int32_t dout_dtype, const float* y,
+                                  const float* topk_w, const int32_t* flat_to_sorted, const moe_dropout_t* drop,
+                                  void* dy, float* dtopk_w, void* stream);
+
+/*
+ * Gradient of the dispatch's copy: dx[t] = cast(sum_j dx_perm[flat_to_sorted[t*k
+ * + j]] + residual[t]), f32 from zero in slot order over the kept pairs; epi as
+ * in moe_combine_ex (the residual: another gradient of x, in the dtype of x; dx
+ * may be the residual itself, same type).
+ *   dx_perm [R,H] dtype (f32, else bf16); dx [M,H] in epi->out_dtype (NULL: f32).
+ */
+moe_status_t moe_dispatch_backward(const moe_problem_t* p, const void* dx_perm, const int32_t* flat_to_sorted,
+                                   const moe_epilogue_t* epi, void* dx, void* stream);
+
+/*
+ * Gradient of the router: dlogits[t, topk_idx[t,j]] = topk_w[t,j] (dtopk_w[t,j]
+ * - sum_i topk_w[t,i] dtopk_w[t,i]), 0 for the experts not chosen; slots of one
+ * token that name the same expert add up.  It is linear in dtopk_w, so the
+ * shares of calls that hold different experts may be added before or after.
+ *   topk_idx [M,k] int32, topk_w, dtopk_w [M,k] f32; dlogits [M,E] f32.
+ */
+moe_status_t moe_route_backward(const moe_problem_t* p, const int32_t* topk_idx, const float* topk_w,
+                                const float* dtopk_w, float* dlogits, void* stream);
+
+/*
+ * moe_grouped_gemm's layer 0 that also keeps its two products for the gradient:
+ * gate = X_perm W_gate^T and up = X_perm W_up^T [R,F] rounded to dtype; c =
+ * Hact as moe_grouped_gemm writes it, bit for bit (from the f32 products).
+ */
+moe_status_t moe_grouped_gemm_aux(const moe_problem_t* p, const void* a, const void* w0, const void* w1,
+                                  const int32_t* offsets, void* gate, void* up, void* c, void* stream);
+
+/*
+ * Gradient of the grouped GEMM for its rows, over the G segments:
+ *   layer 1 (with SwiGLU): d0 = dY [R,H]; w0 = W_down; gate, up [R,F] as kept:
+ *     dh[r, f] = sum_n dY[r,n] W_down[e,n,f], s = 1 / (1 + exp(-gate));
+ *     o0 = dgate = dh up s (1 + gate (1 - s)); o1 = dup = dh gate s [R,F].
+ *     d1, w1 NULL.
+ *   layer 0: d0 = dgate, d1 = dup [R,F]; w0 = W_gate, w1 = W_up:
+ *     o0 = dX_perm[r, h] = sum_f dgate[r,f] W_gate[e,f,h] + dup[r,f] W_up[e,f,h]
+ *     [R,H].  gate, up, o1 NULL.
+ *   All in dtype.  ws: moe_workspace_bytes(p, MOE_OP_GROUPED_GEMM_BACKWARD)
+ *   bytes, 256-byte aligned, for this call alone while it runs (no clearing
+ *   needed; NULL where that is 0).
+ */
+moe_status_t moe_grouped_gemm_backward(const moe_problem_t* p, int32_t layer, const void* d0, const void* d1,
+                                       const void* w0, const void* w1, const void* gate, const void* up,
+                                       const int32_t* offsets, void* o0, void* o1, void* ws, size_t ws_bytes,
+                                       void* stream);
+
+/*
+ * Gradient of the grouped GEMM for its weights, summed over the rows of each
+ * expert held (all its segments):
+ *   layer 1: d0 = dY [R,H], a = Hact [R,F]:
+ *     dw0 = dW_down[e,n,f] = sum_r dY[r,n] Hact[r,f]          [EL,H,F]
+ *     (d1, dw1 NULL)
+ *   layer 0: d0 = dgate, d1 = dup [R,F], a = X_perm [R,H]:
+ *     dw0 = dW_gate[e,f,h] = sum_r dgate[r,f] X_perm[r,h], dw1 = dW_up likewise
+ *     with dup                                                [EL,F,H]
+ *   dw_dtype MOE_DTYPE_F32 or MOE_DTYPE_BF16; accumulate != 0 (f32 only, else
+ *   MOE_ERR_UNSUPPORTED): added to what dw0, dw1 hold, as over micro-batches.
+ *   An expert without rows gets 0 (unchanged with accumulate), also for M = 0.
+ *   ws as for moe_grouped_gemm_backward.
+ */
+moe_status_t moe_grouped_gemm_backward_weights(const moe_problem_t* p, int32_t layer, const void* d0, const void* d1,
+                                               const void* a, const int32_t* offsets, int32_t dw_dtype,
+                                               int32_t accumulate, void* dw0, void* dw1, void* ws, size_t ws_bytes,
+                                               void* stream);
 
 /* The plan the profiled split table picks for this problem (what moe_layer
  * does when opts->n_mover < 0): the number of dedicated combine workgroups
