@@ -364,8 +364,9 @@ moe_status_t check_grad_gemm(const moe_problem_t* p, int32_t layer) {
   return is_mx(p) ? MOE_ERR_UNSUPPORTED : MOE_OK;
 }
 
-GradGemmArgs grad_args(const moe_problem_t* p, const int32_t* offsets) {
+GradGemmArgs grad_args(const moe_problem_t* p, int layer, const int32_t* offsets) {
   GradGemmArgs g{};
+  g.layer = layer;
   g.offsets = offsets;
   g.R = p->num_tokens * p->topk;
   g.H = p->hidden;
@@ -958,7 +959,7 @@ moe_status_t moe_grouped_gemm_backward(const moe_problem_t* p, int32_t layer, co
     st = validate_offsets(p, offsets, hs);
     if (st != MOE_OK) return st;
   }
-  GradGemmArgs g = grad_args(p, offsets);
+  GradGemmArgs g = grad_args(p, layer, offsets);
   g.d0 = d0;
   g.d1 = d1;
   g.w0 = w0;
@@ -967,7 +968,7 @@ moe_status_t moe_grouped_gemm_backward(const moe_problem_t* p, int32_t layer, co
   g.up = up;
   g.o0 = o0;
   g.o1 = o1;
-  return hip_status(launch_grad_rows(g, layer, p->dtype == MOE_DTYPE_BF16, hs));
+  return hip_status(launch_grad_rows(g, p->dtype == MOE_DTYPE_BF16, hs));
 }
 
 moe_status_t moe_grouped_gemm_backward_weights(const moe_problem_t* p, int32_t layer, const void* d0, const void* d1,
@@ -993,7 +994,7 @@ moe_status_t moe_grouped_gemm_backward_weights(const moe_problem_t* p, int32_t l
     st = validate_offsets(p, offsets, hs);
     if (st != MOE_OK) return st;
   }
-  GradGemmArgs g = grad_args(p, offsets);
+  GradGemmArgs g = grad_args(p, layer, offsets);
   g.d0 = d0;
   g.d1 = d1;
   g.x = a;
@@ -1001,7 +1002,7 @@ moe_status_t moe_grouped_gemm_backward_weights(const moe_problem_t* p, int32_t l
   g.o1 = dw1;
   g.out_bf16 = dw_dtype == MOE_DTYPE_BF16;
   g.accumulate = accumulate != 0;
-  return hip_status(launch_grad_weights(g, layer, p->dtype == MOE_DTYPE_BF16, hs));
+  return hip_status(launch_grad_weights(g, p->dtype == MOE_DTYPE_BF16, hs));
 }
 
 moe_status_t moe_quantize_mxfp8(int64_t rows, int32_t cols, int32_t src_dtype, const void* src, void* dst,

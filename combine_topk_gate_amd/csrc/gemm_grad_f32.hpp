@@ -9,8 +9,6 @@
 // An operand whose memory is contiguous along k (the token rows of a rows'
 // gradient) is turned while it is stored to LDS; all others (weights there,
 // both operands of a weights' gradient) lie as LDS has them.
-//
-// T is the type in memory: f32, or bf16 converted (exactly) on the way in.
 #pragma once
 
 #include "common.hpp"
@@ -22,15 +20,7 @@ namespace moe {
 constexpr int kGfThreads = 256;
 constexpr int kGfK = 32;
 
-template <typename T>
-__device__ __forceinline__ f32x4_t gf_load4(const T* p) {
-  if constexpr (sizeof(T) == 4) {
-    return *reinterpret_cast<const f32x4_t*>(p);
-  } else {
-    const bf16x4_t b = *reinterpret_cast<const bf16x4_t*>(p);
-    return f32x4_t{(float)b[0], (float)b[1], (float)b[2], (float)b[3]};
-  }
-}
+__device__ __forceinline__ f32x4_t gf_load4(const float* p) { return *reinterpret_cast<const f32x4_t*>(p); }
 
 template <typename T>
 __device__ __forceinline__ void gf_store4(T* p, f32x4_t v) {
@@ -56,8 +46,8 @@ template <int TS>
 constexpr int gf_lds_floats = 4 * kGfK * gf_pitch<TS>;
 
 // k contiguous: row i of the tile at rows[i] (null: zeros), values k .. k + 31
-template <int TS, typename T>
-__device__ __forceinline__ void gf_load_k(GfPart<TS>& o, const T* const (&rows)[TS / 32], int k) {
+template <int TS>
+__device__ __forceinline__ void gf_load_k(GfPart<TS>& o, const float* const (&rows)[TS / 32], int k) {
 #pragma unroll
   for (int i = 0; i < TS / 32; ++i)
     o.v[i] = rows[i] ? gf_load4(rows[i] + k + 4 * (threadIdx.x & 7)) : f32x4_t{0.f, 0.f, 0.f, 0.f};
@@ -71,8 +61,8 @@ __device__ __forceinline__ void gf_store_k(float* lds, const GfPart<TS>& o) {
 }
 
 // columns contiguous: k rows base + kk * pitch, kk < valid, columns col0 .. col0 + TS (those from cols on: zeros)
-template <int TS, typename T>
-__device__ __forceinline__ void gf_load_c(GfPart<TS>& o, const T* base, int64_t pitch, int valid, int col0, int cols) {
+template <int TS>
+__device__ __forceinline__ void gf_load_c(GfPart<TS>& o, const float* base, int64_t pitch, int valid, int col0, int cols) {
   constexpr int per = TS / 4, step = kGfThreads / per;
   const int c = col0 + 4 * (threadIdx.x % per);
 #pragma unroll

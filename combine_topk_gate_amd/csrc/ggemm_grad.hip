@@ -10,23 +10,77 @@
 // A static tile queue as in the forward grouped GEMM; each output element is
 // formed by one workgroup in a fixed order, so nothing depends on scheduling.
 #include "common.hpp"
+#include "gemm_grad_bf16.hpp"
 #include "gemm_grad_f32.hpp"
 #include "launch.hpp"
 #include "tiles.hpp"
 
 namespace moe {
 
-// d silu(g) u / dg and / du times dh, in f32
-struct SwigluGrad {
-  float dg, du;
-};
+// as swiglu_grad_fast, for f32 outputs
 __device__ __forceinline__ SwigluGrad swiglu_grad(float dh, float g, float u) {
   const float s = 1.0f / (1.0f + expf(-g));
   return {dh * u * (s * fmaf(g, 1.0f - s, 1.0f)), dh * (g * s)};
 }
 
-// ------------------------------------------------------------------- rows ---
-template <int LAYER, typename T, int TS>
+// ------------------------------------------------------------------- bf16 ---
+// Rows: the experts' rows (over all source blocks) in tiles of 256, or of 128
+// where an expert has no more, in the forward queue's order.
+template <GradKind KIND>
+__global__ __launch_bounds__(kGemmThreads) void grad_rows_bf16_kernel(GradGemmArgs a, int xcd_slots) {
+  __shared__ __attribute__((aligned(16))) char lds[kGemmLdsBytes];
+  __shared__ TileLds tl;
+  __shared__ int rowpos[kTileRows];
+  const int K = KIND == kGradRows0 ? a.F : a.H, N = KIND == kGradRows0 ? a.H : a.F, S = a.G / a.E;
+  const int NT = (N + 255) / 256;
+  const int T = build_expert_tile_table(a.offsets, a.G, a.E, kTileRows, tl) * NT;
+  const int64_t panel = (int64_t)kTileRows * K * (KIND == kGradRows0 ? 4 : 2);
+  const int grid = gridDim.x;
+  const int r = T % grid;
+  const int half = (r > 0 && 2 * r <= grid && T > grid) ? r : 0;  // tiles of the last round to halve
+  const int entries = T + half;
+  const Shuffle sm = make_shuffle(a.shuffle, T - half), sh = make_shuffle(a.shuffle, half);
+  for (int v = xcd_slot(blockIdx.x, grid); v < entries; v += grid) {
+    const bool is_half = v >= T - half;
+    const int j = v - (T - half);
+    const TileCoord c = tile_coord(is_half ? T - half + shuffled(sh, j / 2) : shuffled(sm, v), a.E, NT, kTileRows, xcd_slots,
+                                   panel, tl);
+    const int m0 = is_half ? c.m0 + (j & 1) * (kTileRows / 2) : c.m0;
+    const int n = tl.expert_rows[c.g];
+    if (m0 >= n) continue;
+    rowpos[threadIdx.x] = expert_row(tl, c.g, a.E, S, m0, threadIdx.x);
+    __syncthreads();
+    const GradTile t{c.g, 0, c.nt * 256, 0};
+    if (is_half || n <= kTileRows / 2)
+      grad_tile<KIND, kTileRows / 2>(a, t, lds, rowpos);
+    else
+      grad_tile<KIND, kTileRows>(a, t, lds, rowpos);
+  }
+}
+
+// Weights: 256 x 256 tiles of dW, expert by expert; the row tiles (layer 0:
+// of both matrices, which share x's panels) in blocks of 8, so that the 32
+// tiles an XCD runs at once share 8 + 4 panels in its L2.
+__global__ __launch_bounds__(kGemmThreads) void grad_weights_bf16_kernel(GradGemmArgs a) {
+  __shared__ __attribute__((aligned(16))) char lds[kGemmLdsBytes];
+  const bool l0 = a.layer == 0;
+  const int N = l0 ? a.F : a.H, C = l0 ? a.H : a.F;
+  const int NR = (N + 255) / 256, NC = (C + 255) / 256, rows = (l0 ? 2 : 1) * NR;
+  const int T = a.E * rows * NC, grid = gridDim.x;
+  const Shuffle sm = make_shuffle(a.shuffle, T);
+  for (int v = xcd_slot(blockIdx.x, grid); v < T; v += grid) {
+    const int s = shuffled(sm, v), e = s / (rows * NC), l = s - e * rows * NC;
+    const int nb = (rows + 7) / 8, b = min((int)((int64_t)(l / NC) * nb / rows), nb - 1);
+    auto first = [&](int i) { return (int)((int64_t)i * rows / nb); };
+    const int bb = first(b + 1) <= l / NC ? b + 1 : b;
+    const int r0 = first(bb), rb = first(bb + 1) - r0, lb = l - r0 * NC;
+    const int row = r0 + lb % rb, second = row >= NR;
+    grad_tile<kGradWeights, kTileRows>(a, GradTile{e, (row - second * NR) * 256, lb / rb * 256, second}, lds, nullptr);
+  }
+}
+
+// -------------------------------------------------------------------- f32 ---
+template <int LAYER, int TS>
 __global__ __launch_bounds__(kGfThreads) void grad_rows_f32_kernel(GradGemmArgs a) {
   __shared__ __attribute__((aligned(16))) float lds[gf_lds_floats<TS>];
   __shared__ TileLds tl;
@@ -41,23 +95,23 @@ __global__ __launch_bounds__(kGfThreads) void grad_rows_f32_kernel(GradGemmArgs 
     const int e = c.g, col0 = c.nt * TS;
     for (int i = threadIdx.x; i < TS; i += kGfThreads) rowpos[i] = expert_row(tl, e, a.E, S, c.m0, i);
     __syncthreads();
-    const T* rows0[TS / 32];
-    const T* rows1[TS / 32];
+    const float* rows0[TS / 32];
+    const float* rows1[TS / 32];
 #pragma unroll
     for (int i = 0; i < TS / 32; ++i) {
       const int r = rowpos[(threadIdx.x >> 3) + 32 * i];
-      rows0[i] = r >= 0 ? (const T*)a.d0 + (int64_t)r * K : nullptr;
-      rows1[i] = LAYER == 0 && r >= 0 ? (const T*)a.d1 + (int64_t)r * K : nullptr;
+      rows0[i] = r >= 0 ? (const float*)a.d0 + (int64_t)r * K : nullptr;
+      rows1[i] = LAYER == 0 && r >= 0 ? (const float*)a.d1 + (int64_t)r * K : nullptr;
     }
-    const T* w0 = (const T*)a.w0 + (int64_t)e * K * N;
-    const T* w1 = LAYER == 0 ? (const T*)a.w1 + (int64_t)e * K * N : nullptr;
+    const float* w0 = (const float*)a.w0 + (int64_t)e * K * N;
+    const float* w1 = LAYER == 0 ? (const float*)a.w1 + (int64_t)e * K * N : nullptr;
     const int per = K / kGfK, steps = LAYER == 0 ? 2 * per : per;
     GfPart<TS> pw, px;
     auto load = [&](int s) {
       const bool second = LAYER == 0 && s >= per;
       const int k = (second ? s - per : s) * kGfK;
-      gf_load_k<TS, T>(px, second ? rows1 : rows0, k);
-      gf_load_c<TS, T>(pw, (second ? w1 : w0) + (int64_t)k * N, N, kGfK, col0, N);
+      gf_load_k<TS>(px, second ? rows1 : rows0, k);
+      gf_load_c<TS>(pw, (second ? w1 : w0) + (int64_t)k * N, N, kGfK, col0, N);
     };
     auto store = [&](int b) {
       gf_store_c<TS>(lds + b * 2 * kBuf, pw);
@@ -79,9 +133,9 @@ __global__ __launch_bounds__(kGfThreads) void grad_rows_f32_kernel(GradGemmArgs 
       if (r < 0 || col0 + n >= N) return;
       const int64_t at = (int64_t)r * N + col0 + n;
       if constexpr (LAYER == 0) {
-        gf_store4((T*)a.o0 + at, o);
+        gf_store4((float*)a.o0 + at, o);
       } else {
-        const f32x4_t g = gf_load4((const T*)a.gate + at), u = gf_load4((const T*)a.up + at);
+        const f32x4_t g = gf_load4((const float*)a.gate + at), u = gf_load4((const float*)a.up + at);
         f32x4_t dg, du;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -89,19 +143,18 @@ __global__ __launch_bounds__(kGfThreads) void grad_rows_f32_kernel(GradGemmArgs 
           dg[i] = d.dg;
           du[i] = d.du;
         }
-        gf_store4((T*)a.o0 + at, dg);
-        gf_store4((T*)a.o1 + at, du);
+        gf_store4((float*)a.o0 + at, dg);
+        gf_store4((float*)a.o1 + at, du);
       }
     });
     __syncthreads();  // rowpos and the LDS buffers are free for the next tile
   }
 }
 
-// ---------------------------------------------------------------- weights ---
 // Tile of dW[e]: TS of the first operand's columns (its rows) x TS of x's.
 // The K steps run over the expert's segments one after the other, the last
 // step of each filled up with zero rows.
-template <int LAYER, typename T, int TS>
+template <int LAYER, int TS>
 __global__ __launch_bounds__(kGfThreads) void grad_weights_f32_kernel(GradGemmArgs a) {
   __shared__ __attribute__((aligned(16))) float lds[gf_lds_floats<TS>];
   const int N = LAYER == 0 ? a.F : a.H, C = LAYER == 0 ? a.H : a.F;  // rows and columns of dW
@@ -115,7 +168,7 @@ __global__ __launch_bounds__(kGfThreads) void grad_weights_f32_kernel(GradGemmAr
     const int m = l / (NR * NC);
     l -= m * NR * NC;
     const int row0 = l % NR * TS, col0 = l / NR * TS;
-    const T* d = (const T*)(m ? a.d1 : a.d0);
+    const float* d = (const float*)(m ? a.d1 : a.d0);
     int s = 0, r = 0, end = 0;  // the segment being read, its next row and its end
     auto next_segment = [&] {  // to the first unread row; false: none left
       while (r >= end && s < S) {
@@ -128,8 +181,8 @@ __global__ __launch_bounds__(kGfThreads) void grad_weights_f32_kernel(GradGemmAr
     GfPart<TS> pw, px;
     auto load = [&] {
       const int n = end - r;
-      gf_load_c<TS, T>(pw, (const T*)a.x + (int64_t)r * C, C, n, col0, C);
-      gf_load_c<TS, T>(px, d + (int64_t)r * N, N, n, row0, N);
+      gf_load_c<TS>(pw, (const float*)a.x + (int64_t)r * C, C, n, col0, C);
+      gf_load_c<TS>(px, d + (int64_t)r * N, N, n, row0, N);
       r += kGfK;
     };
     auto store = [&](int b) {
@@ -165,27 +218,37 @@ __global__ __launch_bounds__(kGfThreads) void grad_weights_f32_kernel(GradGemmAr
   }
 }
 
-template <int LAYER, typename T>
+template <int LAYER>
 hipError_t grad_rows_launch(const GradGemmArgs& a, hipStream_t s) {
-  grad_rows_f32_kernel<LAYER, T, 64><<<2 * device_cu_count(), kGfThreads, 0, s>>>(a);
+  grad_rows_f32_kernel<LAYER, 64><<<2 * device_cu_count(), kGfThreads, 0, s>>>(a);
   return hipGetLastError();
 }
 
-hipError_t launch_grad_rows(const GradGemmArgs& a, int layer, bool bf16, hipStream_t s) {
+hipError_t launch_grad_rows(const GradGemmArgs& a, bool bf16, hipStream_t s) {
   if (a.R == 0) return hipSuccess;
-  if (bf16) return layer == 0 ? grad_rows_launch<0, __bf16>(a, s) : grad_rows_launch<1, __bf16>(a, s);
-  return layer == 0 ? grad_rows_launch<0, float>(a, s) : grad_rows_launch<1, float>(a, s);
+  const int grid = device_cu_count(), xcd_slots = grid / kXcds > 0 ? grid / kXcds : 1;
+  if (bf16) {
+    if (a.layer == 0)
+      grad_rows_bf16_kernel<kGradRows0><<<grid, kGemmThreads, 0, s>>>(a, xcd_slots);
+    else
+      grad_rows_bf16_kernel<kGradRows1><<<grid, kGemmThreads, 0, s>>>(a, xcd_slots);
+    return hipGetLastError();
+  }
+  return a.layer == 0 ? grad_rows_launch<0>(a, s) : grad_rows_launch<1>(a, s);
 }
 
-template <int LAYER, typename T>
+template <int LAYER>
 hipError_t grad_weights_launch(const GradGemmArgs& a, hipStream_t s) {
-  grad_weights_f32_kernel<LAYER, T, 64><<<2 * device_cu_count(), kGfThreads, 0, s>>>(a);
+  grad_weights_f32_kernel<LAYER, 64><<<2 * device_cu_count(), kGfThreads, 0, s>>>(a);
   return hipGetLastError();
 }
 
-hipError_t launch_grad_weights(const GradGemmArgs& a, int layer, bool bf16, hipStream_t s) {
-  if (bf16) return layer == 0 ? grad_weights_launch<0, __bf16>(a, s) : grad_weights_launch<1, __bf16>(a, s);
-  return layer == 0 ? grad_weights_launch<0, float>(a, s) : grad_weights_launch<1, float>(a, s);
+hipError_t launch_grad_weights(const GradGemmArgs& a, bool bf16, hipStream_t s) {
+  if (bf16) {
+    grad_weights_bf16_kernel<<<device_cu_count(), kGemmThreads, 0, s>>>(a);
+    return hipGetLastError();
+  }
+  return a.layer == 0 ? grad_weights_launch<0>(a, s) : grad_weights_launch<1>(a, s);
 }
 
 }  // namespace moe

@@ -110,6 +110,7 @@ hipError_t launch_route_backward(const int32_t* idx, const float* w, const float
 // SwiGLU to the gradients of gate and up; layer 0 those through W_gate and
 // W_up to that of X_perm.  Weights: the products over each expert's rows.
 struct GradGemmArgs {
+  int layer;
   const void* d0;  // rows: dY [R,H] (layer 1) or dgate [R,F] (layer 0); weights: the same
   const void* d1;  // layer 0: dup [R,F]
   const void* w0;  // rows: W_down [E,H,F] or W_gate [E,F,H]
@@ -126,8 +127,8 @@ struct GradGemmArgs {
   int accumulate;  // weights: add to what o0, o1 hold (f32)
   uint32_t shuffle;
 };
-hipError_t launch_grad_rows(const GradGemmArgs& a, int layer, bool bf16, hipStream_t s);
-hipError_t launch_grad_weights(const GradGemmArgs& a, int layer, bool bf16, hipStream_t s);
+hipError_t launch_grad_rows(const GradGemmArgs& a, bool bf16, hipStream_t s);
+hipError_t launch_grad_weights(const GradGemmArgs& a, bool bf16, hipStream_t s);
 
 // Decode layer (at most MOE_DECODE_MAX_TOKENS tokens).
 struct DecodeSplit {
