@@ -493,50 +493,93 @@ __device__ __forceinline__ void bf16_gemm_tile(const Bf16GemmArgs& p, int g, int
       }
     }
     __syncthreads();
+  } else if (KEEP) {
+    // Hact, gate and up, one row fragment of the wave (32 rows x 64 columns) at
+    // a time, through 32 KiB of LDS of the wave's own, in two halves by turns:
+    // no barrier, and a fragment's 12 stores go out together.  128 B per staged
+    // row; 8-byte unit u of row i at u ^ (i / 2), so 32 rows write one unit, and
+    // 8 lanes a row read 16-byte chunks, without a conflict.  The stores are
+    // buffer ones: rows and columns that the tile lacks lie past the range.
+    // (the lane's number is hidden from the optimiser, which would keep every
+    // swizzled address in a register through the K loop)
+    int ln = lane;
+    asm volatile("" : "+v"(ln));
+    const int er = ln & 31, ek = ln >> 5;
+    char* const mine = lds + wave * 32768;
+    void* const outs[3] = {p.c, p.gate, p.up};
+#pragma unroll
+    for (int nj = 0; nj < NJ; ++nj) {
+      char* const stg = mine + (nj & 1) * 16384;
+#pragma unroll
+      for (int mi = 0; mi < 2; ++mi) {
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          bf16x4_t o[3];
+#pragma unroll
+          for (int v = 0; v < 4; ++v) {
+            const float gt = acc[mi][nj][4 * q + v], up = acc[mi + 2][nj][4 * q + v];
+            o[0][v] = (__bf16)silu_mul_fast(gt, up);
+            o[1][v] = (__bf16)gt;
+            o[2][v] = (__bf16)up;
+          }
+          const int u = mi * 8 + 2 * q + ek;
+#pragma unroll
+          for (int m = 0; m < 3; ++m)
+            *reinterpret_cast<bf16x4_t*>(stg + m * 4096 + er * 128 + ((u ^ (er >> 1)) << 3)) = o[m];
+        }
+      }
+      const int c = ln & 7, f = col0 + wn * 64 + 8 * c;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int row = 8 * i + (ln >> 3), t = wm * (TM / 2) + nj * 32 + row;
+        const int pos = m0 + t < seg_rows ? (ROWMAP ? rowpos[t] : seg_start + m0 + t) : -1;
+        // at most R F < 2^31 elements: past every range
+        const uint32_t at = pos >= 0 && f < N ? ((uint32_t)pos * (uint32_t)N + (uint32_t)f) * 2u : 0xFFFFFFF0u;
+#pragma unroll
+        for (int m = 0; m < 3; ++m) {
+          i32x4_t v = *reinterpret_cast<const i32x4_t*>(stg + m * 4096 + row * 128 + ((c ^ (row >> 2)) << 4));
+          if ((row >> 1) & 1) v = i32x4_t{v[2], v[3], v[0], v[1]};
+          // as used once (nt): the rows go by, the weight panels stay in the L2
+          __builtin_amdgcn_raw_buffer_store_b128(v, make_rsrc(outs[m], (uint32_t)(p.M * N * 2)), (int)at, 0, 2);
+        }
+      }
+    }
+    __syncthreads();
   } else if (LAYER == 0) {
     // 256 B per staged row (128 bf16 columns); 8-byte unit u of row t at
     // unit u ^ (t & 31): conflict-free for 32 rows writing the same unit.
-    auto stage = [&](char* stg, auto value) {
+    char* stg = lds;
 #pragma unroll
-      for (int nj = 0; nj < NJ; ++nj) {
-        const int t = wm * (TM / 2) + nj * 32 + lrow;
+    for (int nj = 0; nj < NJ; ++nj) {
+      const int t = wm * (TM / 2) + nj * 32 + lrow;
 #pragma unroll
-        for (int mi = 0; mi < 2; ++mi) {
+      for (int mi = 0; mi < 2; ++mi) {
 #pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            bf16x4_t h;
+        for (int q = 0; q < 4; ++q) {
+          bf16x4_t h;
 #pragma unroll
-            for (int v = 0; v < 4; ++v) h[v] = (__bf16)value(acc[mi][nj][4 * q + v], acc[mi + 2][nj][4 * q + v]);
-            const int u = wn * 16 + mi * 8 + 2 * q + lk;
-            *reinterpret_cast<bf16x4_t*>(stg + t * 256 + ((u ^ (t & 31)) << 3)) = h;
+          for (int v = 0; v < 4; ++v) {
+            const float gt = acc[mi][nj][4 * q + v], up = acc[mi + 2][nj][4 * q + v];
+            h[v] = (__bf16)silu_mul_fast(gt, up);
           }
+          const int u = wn * 16 + mi * 8 + 2 * q + lk;
+          *reinterpret_cast<bf16x4_t*>(stg + t * 256 + ((u ^ (t & 31)) << 3)) = h;
         }
       }
-    };
+    }
+    __syncthreads();
     // 16 threads per row, 16 B (8 columns) each: chunk c of row t sits at
     // chunk c ^ ((t & 31) >> 1), its two halves swapped when t is odd.
+    __bf16* hact = reinterpret_cast<__bf16*>(p.c);
     const int c = tid & 15;
     const int f = col0 + 8 * c;
-    auto store = [&](const char* stg, __bf16* dst) {
 #pragma unroll 4
-      for (int t = tid >> 4; t < TM; t += kGemmThreads / 16) {
-        i32x4_t v = *reinterpret_cast<const i32x4_t*>(stg + t * 256 + ((c ^ ((t & 31) >> 1)) << 4));
-        if (t & 1) v = i32x4_t{v[2], v[3], v[0], v[1]};
-        const int trow = m0 + t;
-        if (trow < seg_rows && f < N)
-          *reinterpret_cast<i32x4_t*>(dst + (int64_t)(ROWMAP ? rowpos[t] : seg_start + trow) * N + f) = v;
-      }
-    };
-    stage(lds, [](float gt, float up) { return silu_mul_fast(gt, up); });
-    if constexpr (KEEP) stage(lds + kStageBytes, [](float gt, float) { return gt; });  // the other half of the LDS
-    __syncthreads();
-    store(lds, reinterpret_cast<__bf16*>(p.c));
-    if constexpr (KEEP) {
-      store(lds + kStageBytes, p.gate);
-      __syncthreads();
-      stage(lds, [](float, float up) { return up; });
-      __syncthreads();
-      store(lds, p.up);
+    for (int t = tid >> 4; t < TM; t += kGemmThreads / 16) {
+      i32x4_t v = *reinterpret_cast<const i32x4_t*>(stg + t * 256 + ((c ^ ((t & 31) >> 1)) << 4));
+      if (t & 1) v = i32x4_t{v[2], v[3], v[0], v[1]};
+      const int trow = m0 + t;
+      if (trow < seg_rows && f < N)
+        *reinterpret_cast<i32x4_t*>(hact + (int64_t)(ROWMAP ? rowpos[t] : seg_start + trow) * N + f) = v;
     }
     __syncthreads();
   } else {

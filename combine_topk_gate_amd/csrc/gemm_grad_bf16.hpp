@@ -55,6 +55,28 @@ __device__ __forceinline__ SwigluGrad swiglu_grad_fast(float dh, float g, float 
   return {dh * u * fmaf(a, 1.0f - s, s), dh * a};
 }
 
+typedef int i32x2_t __attribute__((ext_vector_type(2)));
+
+// Results are stored, and gate and up loaded, as used once ("nt"): kept like
+// other lines they push the operands' panels, which the tiles of an XCD share,
+// out of its L2 (weights of 64 experts 2048 x 1408, 256 rows each: 466 us, as
+// used once 366; 16 experts 4096 x 6400: 3065, 3047).
+constexpr int kOnce = 2;
+
+__device__ __forceinline__ void buf_store16(__amdgpu_buffer_rsrc_t r, uint32_t voff, i32x4_t v) {
+  __builtin_amdgcn_raw_buffer_store_b128(v, r, (int)voff, 0, kOnce);
+}
+__device__ __forceinline__ i32x4_t buf_load16_once(__amdgpu_buffer_rsrc_t r, uint32_t voff) {
+  return __builtin_bit_cast(i32x4_t, __builtin_amdgcn_raw_buffer_load_b128(r, (int)voff, 0, kOnce));
+}
+
+// Byte offset of column n of row pos in a bf16 buffer of N columns; past any
+// range (of at most 2^32 - 128 bytes) for a row that the tile lacks (-1) or a
+// column that the buffer lacks.
+__device__ __forceinline__ uint32_t grad_offset(int pos, int n, int N) {
+  return pos >= 0 && n < N ? ((uint32_t)pos * (uint32_t)N + (uint32_t)n) * 2u : 0xFFFFFFF0u;
+}
+
 struct GradTile {
   int e;        // weight slot
   int row0;     // weights: first row of dW (column of D)
@@ -62,56 +84,60 @@ struct GradTile {
   int second;   // weights: the second pair of matrices (d1, o1)
 };
 
+// What a wave does for one tile after the other:
+//   begin(t)     addresses, and the loads of the first K step into registers
+//   multiply()   the K loop
+//   epilogue(t)  from the accumulators to memory
+// The kernels call begin of the next tile before the epilogue of this one, so
+// the first loads' latency is not waited for.
 template <GradKind KIND, int TM>
-__device__ __forceinline__ void grad_tile(const GradGemmArgs& p, const GradTile& t, char* __restrict__ lds,
-                                          const int* __restrict__ rowpos) {
-  constexpr bool XKC = KIND != kGradWeights;  // x operand contiguous along k
+struct GradWave {
+  static constexpr bool XKC = KIND != kGradWeights;  // x operand contiguous along k
   static_assert(TM == 256 || (TM == 128 && XKC), "tile height");
-  constexpr int NJ = TM / 64;                  // row fragments per wave
-  constexpr int XI = XKC ? TM / 32 : 8;        // x loads per thread per K step
-  constexpr int XQ = XI / 4;                   // ... per sub-step
-  constexpr int NRX = XKC ? NJ : 2 * NJ;       // LDS reads of x per sub-step
-  constexpr int NR = 8 + NRX;                  // LDS reads per sub-step
-  constexpr int NW = 2 + XQ;                   // LDS stores (and loads) per sub-step
-  constexpr int NM = 4 * NJ;                   // matrix instructions per sub-step
-  const int tid = threadIdx.x;
-  const int lane = tid & 63, wave = tid >> 6;
-  const int wn = wave & 1, wm = wave >> 1;
-  const int e = uniform(t.e), col0 = uniform(t.col0), row0 = uniform(t.row0);
-  // reduction length of one product and columns of the output
-  const int K = KIND == kGradRows0 ? p.F : p.H;
-  const int layer_cols = KIND == kGradRows0 ? p.H : p.F;
-  // weights: dW is [F, H] in layer 0, [H, F] in layer 1
-  const bool l0 = KIND == kGradWeights && p.layer == 0;
-  const int N = KIND == kGradWeights ? (l0 ? p.H : p.F) : layer_cols;   // columns
-  const int DN = KIND == kGradWeights ? (l0 ? p.F : p.H) : K;           // columns of D
-  const uint32_t wpitch = (uint32_t)N * 2u, xpitch = (uint32_t)DN * 2u;
+  static constexpr int NJ = TM / 64;             // row fragments per wave
+  static constexpr int XI = XKC ? TM / 32 : 8;   // x loads per thread per K step
+  static constexpr int XQ = XI / 4;              // ... per sub-step
+  static constexpr int NRX = XKC ? NJ : 2 * NJ;  // LDS reads of x per sub-step
+  static constexpr int NR = 8 + NRX;             // LDS reads per sub-step
+  static constexpr int NW = 2 + XQ;              // LDS stores (and loads) per sub-step
+  static constexpr int NM = 4 * NJ;              // matrix instructions per sub-step
 
-  // ---- sources of the K steps
-  // current step to load: buffers, and (rows) the byte offset along k
+  const GradGemmArgs& p;
+  char* __restrict__ const lds;
+  const int* const offsets;  // weights: the offsets, in LDS
+  const int tid = threadIdx.x, lane = tid & 63, wn = (tid >> 6) & 1, wm = tid >> 7;
+  const int lrow = lane & 31, lk = lane >> 5;
+  // a product's reduction length (rows), the columns of D and of the output
+  const bool l0 = KIND == kGradRows0 || (KIND == kGradWeights && p.layer == 0);
+  const int K = KIND == kGradRows0 ? p.F : p.H;
+  const int N = KIND == kGradRows1 ? p.F : KIND == kGradRows0 ? p.H : (l0 ? p.H : p.F);
+  const int DN = KIND == kGradWeights ? (l0 ? p.F : p.H) : K;
+  const uint32_t wpitch = (uint32_t)N * 2u, xpitch = (uint32_t)DN * 2u;
+  const int cr = tid >> 5, cc = tid & 31;
+  const uint32_t wvoff = (uint32_t)cr * wpitch + (uint32_t)cc * 16u;
+
+  // the K step to load next
   __amdgpu_buffer_rsrc_t rw, rx;
   uint32_t xs = 0;
-  const __bf16* d = (const __bf16*)(KIND == kGradWeights && t.second ? p.d1 : p.d0);
-  int nk;
-  // weights: the segment's next row and end, the next source block
-  int r = 0, rend = 0, sb = 0;
-  const int S = p.G / p.E;
-  if constexpr (KIND == kGradWeights) {
-    nk = 0;
-    for (int s = 0; s < S; ++s) nk += (p.offsets[s * p.E + e + 1] - p.offsets[s * p.E + e] + kBK - 1) / kBK;
-    nk = uniform(nk);
-  } else {
-    nk = (KIND == kGradRows0 ? 2 : 1) * (K / kBK);
-  }
-  const int per = K / kBK;
-  // steps are asked for in order, once each; past the last one it stays
-  auto source = [&](int kt) {
+  int e = 0, col0 = 0, row0 = 0, nk = 0;
+  const __bf16* d = nullptr;
+  int r = 0, rend = 0, sb = 0;  // weights: the segment's row and end, the next source block
+  uint32_t xvoff[XKC ? XI : 1];
+
+  i32x4_t wreg[8], xreg[XI];
+  f32x16_t acc[4][NJ];
+
+  __device__ __forceinline__ GradWave(const GradGemmArgs& p, char* lds, const int* offsets)
+      : p(p), lds(lds), offsets(offsets) {}
+
+  // Steps are asked for in order, once each; past the last one the buffers stay.
+  __device__ __forceinline__ void source(int kt) {
     if constexpr (KIND == kGradWeights) {
       if (kt < nk) {
         r += kBK;
         while (r >= rend) {
-          r = uniform(p.offsets[sb * p.E + e]);
-          rend = uniform(p.offsets[sb * p.E + e + 1]);
+          r = uniform(offsets[sb * p.E + e]);
+          rend = uniform(offsets[sb * p.E + e + 1]);
           ++sb;
         }
         const uint32_t n = (uint32_t)min(rend - r, kBK);
@@ -119,6 +145,7 @@ __device__ __forceinline__ void grad_tile(const GradGemmArgs& p, const GradTile&
         rx = make_rsrc(d + (int64_t)r * DN + row0, n * xpitch - (uint32_t)row0 * 2u);
       }
     } else {
+      const int per = K / kBK;
       kt = min(kt, nk - 1);
       const bool second = KIND == kGradRows0 && kt >= per;
       const int kk = second ? kt - per : kt;
@@ -127,42 +154,26 @@ __device__ __forceinline__ void grad_tile(const GradGemmArgs& p, const GradTile&
       rx = make_rsrc(second ? p.d1 : p.d0, (uint32_t)(p.R * (int64_t)xpitch));
       xs = (uint32_t)kk * (kBK * 2);
     }
-  };
-
-  // ---- global -> register loads.  [k][columns]: thread owns 16-byte chunk
-  // tid & 31 of k rows (tid >> 5) + 8 i; [rows][k]: chunk tid & 7 of rows
-  // (tid >> 3) + 32 i
-  const int cr = tid >> 5, cc = tid & 31;
-  const uint32_t wvoff = (uint32_t)cr * wpitch + (uint32_t)cc * 16u, wstep = 8u * wpitch;
-  uint32_t xvoff[XKC ? XI : 1], xstep = 8u * xpitch;
-  if constexpr (XKC) {
-#pragma unroll
-    for (int i = 0; i < XI; ++i) {
-      const int pos = rowpos[(tid >> 3) + 32 * i];
-      // a row that the tile lacks: past the range, or (buffers over 2 GiB) another row, whose sums are not stored
-      xvoff[i] = pos >= 0 ? (uint32_t)pos * xpitch + (uint32_t)(tid & 7) * 16u : 0x80000000u;
-    }
-  } else {
-    xvoff[0] = (uint32_t)cr * xpitch + (uint32_t)cc * 16u;
   }
-  const uint32_t st_kr = (uint32_t)cr * 512u + ((uint32_t)(cc ^ ((cr & 3) << 2)) << 4);
-  const int lr = tid >> 3;
-  const uint32_t st_kc = (uint32_t)lr * 128u + ((uint32_t)((tid & 7) ^ (lr & 7) ^ ((lr >> 3) & 1)) << 4);
 
-  i32x4_t wreg[8], xreg[XI];
-  auto gload_one = [&](int q, int j) {
+  // Global -> register loads.  [k][columns]: thread owns 16-byte chunk tid & 31
+  // of k rows (tid >> 5) + 8 i; [rows][k]: chunk tid & 7 of rows (tid >> 3) + 32 i.
+  __device__ __forceinline__ void gload_one(int q, int j) {
     if (j < 2) {
       const int i = 2 * q + j;
-      wreg[i] = buf_load16(rw, wvoff + (uint32_t)i * wstep, 0);
+      wreg[i] = buf_load16(rw, wvoff + (uint32_t)i * (8u * wpitch), 0);
     } else {
       const int i = q * XQ + j - 2;
       if constexpr (XKC)
         xreg[i] = buf_load16(rx, xvoff[i], xs);
       else
-        xreg[i] = buf_load16(rx, xvoff[0] + (uint32_t)i * xstep, 0);
+        xreg[i] = buf_load16(rx, xvoff[0] + (uint32_t)i * (8u * xpitch), 0);
     }
-  };
-  auto lstore_one = [&](int stage, int q, int j) {
+  }
+  __device__ __forceinline__ void lstore_one(int stage, int q, int j) {
+    const uint32_t st_kr = (uint32_t)cr * 512u + ((uint32_t)(cc ^ ((cr & 3) << 2)) << 4);
+    const int lr = tid >> 3;
+    const uint32_t st_kc = (uint32_t)lr * 128u + ((uint32_t)((tid & 7) ^ (lr & 7) ^ ((lr >> 3) & 1)) << 4);
     char* wdst = lds + stage * kStageBytes;
     if (j < 2) {
       const int i = 2 * q + j;
@@ -171,78 +182,105 @@ __device__ __forceinline__ void grad_tile(const GradGemmArgs& p, const GradTile&
       const int i = q * XQ + j - 2;
       *reinterpret_cast<i32x4_t*>(wdst + kOperandBytes + (XKC ? st_kc : st_kr) + i * 4096) = xreg[i];
     }
-  };
+  }
 
-  // ---- fragment addressing
-  const int lrow = lane & 31, lk = lane >> 5;
-  uint32_t wrd[4], xrd[4];
-  {
-    // lane's 16-lane group: columns 16 (g & 1), k rows 8 (g >> 1); in it, row l >> 2, 8-byte piece l & 3
-    const int g = lane >> 4, l = lane & 15, lq = l >> 2;
-    const uint32_t base = (uint32_t)(8 * (g >> 1) + lq) * 512u + (uint32_t)(g & 1) * 32u + (uint32_t)(l & 3) * 8u;
+  // rowpos (rows): the rows of the tile in the buffers, -1 for those it lacks.
+  __device__ __forceinline__ void begin(const GradTile& t, const int* __restrict__ rowpos) {
+    e = uniform(t.e);
+    col0 = uniform(t.col0);
+    if constexpr (KIND == kGradWeights) {
+      row0 = uniform(t.row0);
+      d = (const __bf16*)(uniform(t.second) ? p.d1 : p.d0);
+      nk = 0;
+      const int S = p.G / p.E;
+      for (int s = 0; s < S; ++s) nk += (offsets[s * p.E + e + 1] - offsets[s * p.E + e] + kBK - 1) / kBK;
+      nk = uniform(nk);
+      r = -kBK;
+      rend = sb = 0;
+      xvoff[0] = (uint32_t)cr * xpitch + (uint32_t)cc * 16u;
+    } else {
+      nk = (KIND == kGradRows0 ? 2 : 1) * (K / kBK);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      wrd[i] = base + (uint32_t)(wn * 8 + ((i ^ lq) << 1)) * 32u;
-      if constexpr (XKC)  // sub-step i of the wave's rows
-        xrd[i] = (uint32_t)(kOperandBytes + (wm * (TM / 2) + lrow) * 128) +
-                 (uint32_t)(((2 * i + lk) ^ (lrow & 7) ^ ((lrow >> 3) & 1)) << 4);
-      else
-        xrd[i] = (uint32_t)kOperandBytes + base + (uint32_t)(wm * 8 + ((i ^ lq) << 1)) * 32u;
+      for (int i = 0; i < XI; ++i) {
+        const int pos = rowpos[(tid >> 3) + 32 * i];
+        // a row that the tile lacks: past the range, or (buffers over 2 GiB) another row, whose sums are not stored
+        xvoff[i] = pos >= 0 ? (uint32_t)pos * xpitch + (uint32_t)(tid & 7) * 16u : 0x80000000u;
+      }
+    }
+    if (nk > 0) {
+      source(0);
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+#pragma unroll
+        for (int j = 0; j < NW; ++j) gload_one(q, j);
     }
   }
-  lds_byte* l3 = (lds_byte*)lds;
-  bf16x4_t fa[2][4][2];
-  bf16x4_t fx4[2][XKC ? 1 : NJ][2];
-  bf16x8_t fx8[2][XKC ? NJ : 1];
-  auto read_tr = [&](uint32_t at, int stage, int ks, int h) {
-    return __builtin_amdgcn_ds_read_tr16_b64_v4bf16(
-        (lds_bf16x4*)(l3 + stage * kStageBytes + at + (uint32_t)(ks * 16 + 4 * h) * 512u));
-  };
-  // read j of sub-step ks, in the order the matrix instructions use them: column fragment 0, the row fragments, columns 1..3
-  auto read_one = [&](int set, int stage, int ks, int j) {
-    if (j < 2) {
-      fa[set][0][j] = read_tr(wrd[0], stage, ks, j);
-    } else if (j < 2 + NRX) {
-      if constexpr (XKC)
-        fx8[set][j - 2] = *reinterpret_cast<const bf16x8_t*>(lds + stage * kStageBytes + xrd[ks] + (j - 2) * 4096);
-      else
-        fx4[set][(j - 2) / 2][j & 1] = read_tr(xrd[(j - 2) / 2], stage, ks, j & 1);
-    } else {
-      const int i = j - NRX;
-      fa[set][i / 2][i & 1] = read_tr(wrd[i / 2], stage, ks, i & 1);
-    }
-  };
 
-  f32x16_t acc[4][NJ];
+  // All waves of the block call it together; every LDS use of the tile before is behind its first barrier.
+  __device__ __forceinline__ void multiply() {
+    // fragment addresses
+    uint32_t wrd[4], xrd[4];
+    {
+      // lane's 16-lane group: columns 16 (g & 1), k rows 8 (g >> 1); in it, row l >> 2, 8-byte piece l & 3
+      const int g = lane >> 4, l = lane & 15, lq = l >> 2;
+      const uint32_t base = (uint32_t)(8 * (g >> 1) + lq) * 512u + (uint32_t)(g & 1) * 32u + (uint32_t)(l & 3) * 8u;
 #pragma unroll
-  for (int mi = 0; mi < 4; ++mi)
-#pragma unroll
-    for (int nj = 0; nj < NJ; ++nj)
-#pragma unroll
-      for (int v = 0; v < 16; ++v) acc[mi][nj][v] = 0.0f;
-  auto mfma_rows = [&](int set, int mi0, int mi1) {
-#pragma unroll
-    for (int mi = mi0; mi < mi1; ++mi)
-#pragma unroll
-      for (int nj = 0; nj < NJ; ++nj) {
-        const bf16x8_t a = __builtin_shufflevector(fa[set][mi][0], fa[set][mi][1], 0, 1, 2, 3, 4, 5, 6, 7);
-        bf16x8_t b;
-        if constexpr (XKC)
-          b = fx8[set][nj];
+      for (int i = 0; i < 4; ++i) {
+        wrd[i] = base + (uint32_t)(wn * 8 + ((i ^ lq) << 1)) * 32u;
+        if constexpr (XKC)  // sub-step i of the wave's rows
+          xrd[i] = (uint32_t)(kOperandBytes + (wm * (TM / 2) + lrow) * 128) +
+                   (uint32_t)(((2 * i + lk) ^ (lrow & 7) ^ ((lrow >> 3) & 1)) << 4);
         else
-          b = __builtin_shufflevector(fx4[set][nj][0], fx4[set][nj][1], 0, 1, 2, 3, 4, 5, 6, 7);
-        acc[mi][nj] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, acc[mi][nj], 0, 0, 0);
+          xrd[i] = (uint32_t)kOperandBytes + base + (uint32_t)(wm * 8 + ((i ^ lq) << 1)) * 32u;
       }
-  };
+    }
+    lds_byte* l3 = (lds_byte*)lds;
+    bf16x4_t fa[2][4][2];
+    bf16x4_t fx4[2][XKC ? 1 : NJ][2];
+    bf16x8_t fx8[2][XKC ? NJ : 1];
+    auto read_tr = [&](uint32_t at, int stage, int ks, int h) {
+      return __builtin_amdgcn_ds_read_tr16_b64_v4bf16(
+          (lds_bf16x4*)(l3 + stage * kStageBytes + at + (uint32_t)(ks * 16 + 4 * h) * 512u));
+    };
+    // read j of sub-step ks, in the order the matrix instructions use them: column fragment 0, the row fragments,
+    // columns 1..3
+    auto read_one = [&](int set, int stage, int ks, int j) {
+      if (j < 2) {
+        fa[set][0][j] = read_tr(wrd[0], stage, ks, j);
+      } else if (j < 2 + NRX) {
+        if constexpr (XKC)
+          fx8[set][j - 2] = *reinterpret_cast<const bf16x8_t*>(lds + stage * kStageBytes + xrd[ks] + (j - 2) * 4096);
+        else
+          fx4[set][(j - 2) / 2][j & 1] = read_tr(xrd[(j - 2) / 2], stage, ks, j & 1);
+      } else {
+        const int i = j - NRX;
+        fa[set][i / 2][i & 1] = read_tr(wrd[i / 2], stage, ks, i & 1);
+      }
+    };
+    auto mfma_rows = [&](int set, int mi0, int mi1) {
+#pragma unroll
+      for (int mi = mi0; mi < mi1; ++mi)
+#pragma unroll
+        for (int nj = 0; nj < NJ; ++nj) {
+          const bf16x8_t a = __builtin_shufflevector(fa[set][mi][0], fa[set][mi][1], 0, 1, 2, 3, 4, 5, 6, 7);
+          bf16x8_t b;
+          if constexpr (XKC)
+            b = fx8[set][nj];
+          else
+            b = __builtin_shufflevector(fx4[set][nj][0], fx4[set][nj][1], 0, 1, 2, 3, 4, 5, 6, 7);
+          acc[mi][nj] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, acc[mi][nj], 0, 0, 0);
+        }
+    };
 
-  if (nk > 0) {
+#pragma unroll
+    for (int mi = 0; mi < 4; ++mi)
+#pragma unroll
+      for (int nj = 0; nj < NJ; ++nj)
+#pragma unroll
+        for (int v = 0; v < 16; ++v) acc[mi][nj][v] = 0.0f;
+    __syncthreads();
+    if (nk == 0) return;
     // prologue: step 0 into LDS, step 1 into registers, fragments of (0, 0)
-    if constexpr (KIND == kGradWeights) r = -kBK;
-    source(0);
-#pragma unroll
-    for (int q = 0; q < 4; ++q)
-#pragma unroll
-      for (int j = 0; j < NW; ++j) gload_one(q, j);
 #pragma unroll
     for (int q = 0; q < 4; ++q)
 #pragma unroll
@@ -318,104 +356,162 @@ __device__ __forceinline__ void grad_tile(const GradGemmArgs& p, const GradTile&
     }
   }
 
-  // ---- epilogue, staged through LDS (free after the loop's last barrier, as
-  // in bf16_gemm_tile) so that each wave stores whole row segments.  Lane
-  // (lrow, lk) holds, per row fragment nj and column fragment mi, the 4-column
-  // groups 8 q + 4 lk of row wm TM/2 + 32 nj + lrow.
-  char* stg = lds;
-  if constexpr (KIND == kGradRows0) {
-    // 512 B per staged row (256 bf16); 8-byte unit u of row t at u ^ (t & 31)
+  // Lane (lrow, lk) holds, per row fragment nj and column fragment mi, the
+  // 4-column groups 8 q + 4 lk of row wm TM/2 + 32 nj + lrow.  A wave turns one
+  // row fragment at a time (32 rows x 128 columns) in 32 KiB of LDS of its own,
+  // in two halves by turns, so that it stores whole row segments (256 or 512 B)
+  // and waits for no other wave.  After the loop's last barrier no wave uses a
+  // value of the stages again.  The loads and stores are buffer ones: what lies
+  // outside the tile's rows or columns has an offset past the range, so there is
+  // no branch, and a fragment's accesses are in flight together.
+  __device__ __forceinline__ void epilogue(const GradTile& t, const int* __restrict__ rowpos) {
+    // The lane's number hidden from the optimiser: the swizzled addresses below would otherwise be computed once before
+    // the tiles, some fifty registers kept (spilled) through the K loop for one instruction each.
+    int lane = this->lane;
+    asm volatile("" : "+v"(lane));
+    const int lrow = lane & 31, lk = lane >> 5;
+    char* const mine = lds + (tid >> 6) * 32768;
+    const int tcol = uniform(t.col0) + wn * 128;  // the wave's first column
+    if constexpr (KIND == kGradRows0) {
+      // 256 B a staged row; 8-byte unit u of row i at u ^ i; read as 16-byte chunks: c ^ (i >> 1), halves swapped for
+      // an odd row.  16 lanes a row, 8 columns each.
+      const __amdgpu_buffer_rsrc_t ro = make_rsrc(p.o0, (uint32_t)(p.R * N * 2));
+      const int c = lane & 15;
 #pragma unroll
-    for (int nj = 0; nj < NJ; ++nj) {
-      const int tr = wm * (TM / 2) + nj * 32 + lrow;
+      for (int nj = 0; nj < NJ; ++nj) {
+        char* const stg = mine + (nj & 1) * 8192;
 #pragma unroll
-      for (int mi = 0; mi < 4; ++mi)
+        for (int mi = 0; mi < 4; ++mi)
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          bf16x4_t h;
+          for (int q = 0; q < 4; ++q) {
+            bf16x4_t h;
 #pragma unroll
-          for (int v = 0; v < 4; ++v) h[v] = (__bf16)acc[mi][nj][4 * q + v];
-          const int u = wn * 32 + mi * 8 + 2 * q + lk;
-          *reinterpret_cast<bf16x4_t*>(stg + tr * 512 + ((u ^ (tr & 31)) << 3)) = h;
+            for (int v = 0; v < 4; ++v) h[v] = (__bf16)acc[mi][nj][4 * q + v];
+            *reinterpret_cast<bf16x4_t*>(stg + lrow * 256 + (((mi * 8 + 2 * q + lk) ^ lrow) << 3)) = h;
+          }
+        i32x4_t v[8];
+        uint32_t at[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const int row = 4 * i + (lane >> 4);
+          at[i] = grad_offset(rowpos[wm * (TM / 2) + nj * 32 + row], tcol + 8 * c, N);
+          v[i] = *reinterpret_cast<const i32x4_t*>(stg + row * 256 + ((c ^ (row >> 1)) << 4));
         }
-    }
-    __syncthreads();
-    const int c = tid & 31, n = col0 + 8 * c;
-#pragma unroll 4
-    for (int tr = tid >> 5; tr < TM; tr += kGemmThreads / 32) {
-      i32x4_t v = *reinterpret_cast<const i32x4_t*>(stg + tr * 512 + ((c ^ ((tr & 31) >> 1)) << 4));
-      if (tr & 1) v = i32x4_t{v[2], v[3], v[0], v[1]};
-      const int pos = rowpos[tr];
-      if (pos >= 0 && n < N) *reinterpret_cast<i32x4_t*>((__bf16*)p.o0 + (int64_t)pos * N + n) = v;
-    }
-    __syncthreads();
-  } else {
-    // passes of 128 rows, 1 KiB per staged row (256 f32); 16-byte unit u of staged row t' at u ^ (t' & 15)
-    constexpr int passes = NJ / 2;
 #pragma unroll
-    for (int P = 0; P < passes; ++P) {
-#pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        const int ts = wm * 64 + j * 32 + lrow;
+        for (int i = 0; i < 8; ++i)
+          buf_store16(ro, at[i], (lane >> 4) & 1 ? i32x4_t{v[i][2], v[i][3], v[i][0], v[i][1]} : v[i]);
+      }
+    } else {
+      // 512 B a staged row (f32): 16-byte unit u of row i at (u / 2 + 16 (u % 2)) ^ (i & 15), so that both the lanes
+      // that read every unit and those that read every other one (8 columns each) read 256 bytes in a row
+      auto stage = [&](int nj) {
+        char* const stg = mine + (nj & 1) * 16384;
 #pragma unroll
         for (int mi = 0; mi < 4; ++mi)
 #pragma unroll
           for (int q = 0; q < 4; ++q) {
             f32x4_t o;
 #pragma unroll
-            for (int v = 0; v < 4; ++v) o[v] = acc[mi][2 * P + j][4 * q + v];
-            const int u = wn * 32 + mi * 8 + 2 * q + lk;
-            *reinterpret_cast<f32x4_t*>(stg + ts * 1024 + ((u ^ (ts & 15)) << 4)) = o;
+            for (int v = 0; v < 4; ++v) o[v] = acc[mi][nj][4 * q + v];
+            *reinterpret_cast<f32x4_t*>(stg + lrow * 512 + (((mi * 4 + q + 16 * lk) ^ (lrow & 15)) << 4)) = o;
           }
-      }
-      __syncthreads();
+      };
       if constexpr (KIND == kGradRows1) {
-        // 32 threads per row, 8 columns each
-        const int c = tid & 31, n = col0 + 8 * c;
-#pragma unroll 4
-        for (int ts = tid >> 5; ts < 128; ts += kGemmThreads / 32) {
-          const int pos = rowpos[(ts >> 6) * (TM / 2) + 64 * P + (ts & 63)];
-          if (pos < 0 || n >= N) continue;
-          const int64_t at = (int64_t)pos * N + n;
-          const bf16x8_t g = *reinterpret_cast<const bf16x8_t*>((const __bf16*)p.gate + at);
-          const bf16x8_t u = *reinterpret_cast<const bf16x8_t*>((const __bf16*)p.up + at);
-          bf16x8_t og, ou;
+        // 16 lanes a row, 8 columns each: batches of 4 x 4 rows, 2 a fragment; gate and up are loaded two batches ahead
+        const uint32_t bytes = (uint32_t)(p.R * N * 2);
+        const __amdgpu_buffer_rsrc_t rg = make_rsrc(p.gate, bytes), ru = make_rsrc(p.up, bytes);
+        const __amdgpu_buffer_rsrc_t r0 = make_rsrc(p.o0, bytes), r1 = make_rsrc(p.o1, bytes);
+        const int c = lane & 15;
+        i32x4_t g[3][4], u[3][4];
+        uint32_t at[3][4];
+        auto load = [&](int b) {
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const f32x4_t dh = *reinterpret_cast<const f32x4_t*>(stg + ts * 1024 + (((2 * c + h) ^ (ts & 15)) << 4));
-#pragma unroll
-            for (int v = 0; v < 4; ++v) {
-              const SwigluGrad s = swiglu_grad_fast(dh[v], (float)g[4 * h + v], (float)u[4 * h + v]);
-              og[4 * h + v] = (__bf16)s.dg;
-              ou[4 * h + v] = (__bf16)s.du;
-            }
+          for (int i = 0; i < 4; ++i) {
+            const int row = wm * (TM / 2) + b * 16 + 4 * i + (lane >> 4);
+            at[b % 3][i] = grad_offset(rowpos[row], tcol + 8 * c, N);
+            g[b % 3][i] = buf_load16_once(rg, at[b % 3][i]);
+            u[b % 3][i] = buf_load16_once(ru, at[b % 3][i]);
           }
-          *reinterpret_cast<bf16x8_t*>((__bf16*)p.o0 + at) = og;
-          *reinterpret_cast<bf16x8_t*>((__bf16*)p.o1 + at) = ou;
+        };
+        load(0);
+        load(1);
+#pragma unroll
+        for (int b = 0; b < 2 * NJ; ++b) {
+          if (b % 2 == 0) stage(b / 2);
+          if (b + 2 < 2 * NJ) load(b + 2);
+          const char* const stg = mine + (b / 2 & 1) * 16384;
+          f32x4_t dh[4][2];
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              const int row = (b & 1) * 16 + 4 * i + (lane >> 4);
+              dh[i][h] = *reinterpret_cast<const f32x4_t*>(stg + row * 512 + (((c + 16 * h) ^ (row & 15)) << 4));
+            }
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const bf16x8_t gv = __builtin_bit_cast(bf16x8_t, g[b % 3][i]), uv = __builtin_bit_cast(bf16x8_t, u[b % 3][i]);
+            bf16x8_t og, ou;
+#pragma unroll
+            for (int v = 0; v < 8; ++v) {
+              const SwigluGrad s = swiglu_grad_fast(dh[i][v / 4][v % 4], (float)gv[v], (float)uv[v]);
+              og[v] = (__bf16)s.dg;
+              ou[v] = (__bf16)s.du;
+            }
+            buf_store16(r0, at[b % 3][i], __builtin_bit_cast(i32x4_t, og));
+            buf_store16(r1, at[b % 3][i], __builtin_bit_cast(i32x4_t, ou));
+          }
         }
       } else {
-        void* out = t.second ? p.o1 : p.o0;
-        const int c = tid & 63, n = col0 + 4 * c;
-#pragma unroll 4
-        for (int ts = tid >> 6; ts < 128; ts += kGemmThreads / 64) {
-          const f32x4_t v = *reinterpret_cast<const f32x4_t*>(stg + ts * 1024 + ((c ^ (ts & 15)) << 4));
-          const int row = row0 + (ts >> 6) * (TM / 2) + 64 * P + (ts & 63);
-          if (row >= DN || n >= N) continue;
-          const int64_t at = ((int64_t)e * DN + row) * N + n;
-          if (p.out_bf16) {
-            bf16x4_t b;
+        // 32 lanes a row, 4 columns each
+        const int trow = uniform(t.row0), rows = min(DN - trow, TM), te = uniform(t.e);
+        const int es = p.out_bf16 ? 2 : 4;
+        const char* const out = (const char*)(uniform(t.second) ? p.o1 : p.o0) + (((int64_t)te * DN + trow) * N) * es;
+        const __amdgpu_buffer_rsrc_t ro = make_rsrc(out, (uint32_t)rows * (uint32_t)(N * es));
+        const int n = tcol + 4 * (lane & 31);
+        const uint32_t pitch = (uint32_t)(N * es);
+        const uint32_t at0 = n < N ? (uint32_t)(wm * (TM / 2) + lk) * pitch + (uint32_t)(n * es) : 0x80000000u;
+        auto each = [&](auto&& store) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) b[i] = (__bf16)v[i];
-            *reinterpret_cast<bf16x4_t*>((__bf16*)out + at) = b;
-          } else {
-            f32x4_t* dst = reinterpret_cast<f32x4_t*>((float*)out + at);
-            *dst = p.accumulate ? *dst + v : v;
+          for (int nj = 0; nj < NJ; ++nj) {
+            stage(nj);
+            const char* const stg = mine + (nj & 1) * 16384;
+            f32x4_t v[16];
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+              const int row = 2 * i + lk, u = lane & 31;
+              v[i] = *reinterpret_cast<const f32x4_t*>(stg + row * 512 + (((u / 2 + 16 * (u % 2)) ^ (row & 15)) << 4));
+            }
+            store(v, at0 + (uint32_t)(nj * 32) * pitch);
           }
+        };
+        if (p.out_bf16) {
+          each([&](f32x4_t (&v)[16], uint32_t at) {
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+              bf16x4_t b;
+#pragma unroll
+              for (int j = 0; j < 4; ++j) b[j] = (__bf16)v[i][j];
+              __builtin_amdgcn_raw_buffer_store_b64(__builtin_bit_cast(i32x2_t, b), ro, (int)(at + 2u * i * pitch), 0, kOnce);
+            }
+          });
+        } else if (p.accumulate) {
+          each([&](f32x4_t (&v)[16], uint32_t at) {
+            f32x4_t w[16];
+#pragma unroll
+            for (int i = 0; i < 16; ++i) w[i] = __builtin_bit_cast(f32x4_t, buf_load16_once(ro, at + 2u * i * pitch));
+#pragma unroll
+            for (int i = 0; i < 16; ++i) buf_store16(ro, at + 2u * i * pitch, __builtin_bit_cast(i32x4_t, w[i] + v[i]));
+          });
+        } else {
+          each([&](f32x4_t (&v)[16], uint32_t at) {
+#pragma unroll
+            for (int i = 0; i < 16; ++i) buf_store16(ro, at + 2u * i * pitch, __builtin_bit_cast(i32x4_t, v[i]));
+          });
         }
       }
-      __syncthreads();
     }
   }
-}
+};
 
 }  // namespace moe

@@ -419,8 +419,8 @@ hipError_t launch_grouped_gemm_bf16(const GemmProblem& gp, hipStream_t s) {
   a.a_scale_bytes = a.w_scale_bytes = 0;
   const int grid = device_cu_count();
   const int xcd_slots = grid / kXcds > 0 ? grid / kXcds : 1;
+  if (gp.rowmap || gp.gate) a.M = gp.R;  // rows of the token-row buffers, read (rowmap) and stored (KEEP) at their own positions
   if (gp.rowmap) {
-    a.M = gp.R;  // rows of the token-row buffer, read at their own positions
     if (gp.gate)
       grouped_gemm_bf16_expert_kernel<0, true><<<grid, kGemmThreads, 0, s>>>(a, gp.offsets, gp.G, xcd_slots,
                                                                              gp.shuffle);

@@ -25,12 +25,13 @@ __device__ __forceinline__ SwigluGrad swiglu_grad(float dh, float g, float u) {
 
 // ------------------------------------------------------------------- bf16 ---
 // Rows: the experts' rows (over all source blocks) in tiles of 256, or of 128
-// where an expert has no more, in the forward queue's order.
+// where an expert has no more and in a last round that would leave half the
+// workgroups idle, in the forward queue's order.
 template <GradKind KIND>
 __global__ __launch_bounds__(kGemmThreads) void grad_rows_bf16_kernel(GradGemmArgs a, int xcd_slots) {
   __shared__ __attribute__((aligned(16))) char lds[kGemmLdsBytes];
   __shared__ TileLds tl;
-  __shared__ int rowpos[kTileRows];
+  __shared__ int rowpos[2][kTileRows];  // of this tile and of the next
   const int K = KIND == kGradRows0 ? a.F : a.H, N = KIND == kGradRows0 ? a.H : a.F, S = a.G / a.E;
   const int NT = (N + 255) / 256;
   const int T = build_expert_tile_table(a.offsets, a.G, a.E, kTileRows, tl) * NT;
@@ -40,21 +41,52 @@ __global__ __launch_bounds__(kGemmThreads) void grad_rows_bf16_kernel(GradGemmAr
   const int half = (r > 0 && 2 * r <= grid && T > grid) ? r : 0;  // tiles of the last round to halve
   const int entries = T + half;
   const Shuffle sm = make_shuffle(a.shuffle, T - half), sh = make_shuffle(a.shuffle, half);
-  for (int v = xcd_slot(blockIdx.x, grid); v < entries; v += grid) {
-    const bool is_half = v >= T - half;
-    const int j = v - (T - half);
-    const TileCoord c = tile_coord(is_half ? T - half + shuffled(sh, j / 2) : shuffled(sm, v), a.E, NT, kTileRows, xcd_slots,
-                                   panel, tl);
-    const int m0 = is_half ? c.m0 + (j & 1) * (kTileRows / 2) : c.m0;
-    const int n = tl.expert_rows[c.g];
-    if (m0 >= n) continue;
-    rowpos[threadIdx.x] = expert_row(tl, c.g, a.E, S, m0, threadIdx.x);
-    __syncthreads();
-    const GradTile t{c.g, 0, c.nt * 256, 0};
-    if (is_half || n <= kTileRows / 2)
-      grad_tile<KIND, kTileRows / 2>(a, t, lds, rowpos);
+  GradTile t{0, 0, 0, 0};
+  bool low = false;  // 128 rows
+  // Entry v or the next one of this workgroup that has rows; its rows' positions into rowpos[b].
+  auto find = [&](int v, int b) {
+    for (; v < entries; v += grid) {
+      const bool is_half = v >= T - half;
+      const int j = v - (T - half);
+      const TileCoord c = tile_coord(is_half ? T - half + shuffled(sh, j / 2) : shuffled(sm, v), a.E, NT, kTileRows,
+                                     xcd_slots, panel, tl);
+      const int m0 = is_half ? c.m0 + (j & 1) * (kTileRows / 2) : c.m0;
+      const int n = tl.expert_rows[c.g];
+      if (m0 >= n) continue;
+      rowpos[b][threadIdx.x] = expert_row(tl, c.g, a.E, S, m0, threadIdx.x);
+      t = {c.g, 0, c.nt * 256, 0};
+      low = is_half || n <= kTileRows / 2;
+      break;
+    }
+    return v;
+  };
+  int b = 0;
+  int v = find(xcd_slot(blockIdx.x, grid), b);
+  // Tiles as long as they are of one height; the first loads of each but the first are issued before the epilogue of
+  // the one before.
+  auto run = [&]<int TM>() {
+    GradWave<KIND, TM> wave(a, lds, nullptr);
+    __syncthreads();  // rowpos[b]
+    wave.begin(t, rowpos[b]);
+    bool more;
+    do {
+      const GradTile now = t;
+      wave.multiply();
+      v = find(v + grid, b ^ 1);
+      more = v < entries && low == (TM < kTileRows);
+      if (more) {
+        __syncthreads();
+        wave.begin(t, rowpos[b ^ 1]);
+      }
+      wave.epilogue(now, rowpos[b]);
+      b ^= 1;
+    } while (more);
+  };
+  while (v < entries) {
+    if (low)
+      run.template operator()<kTileRows / 2>();
     else
-      grad_tile<KIND, kTileRows>(a, t, lds, rowpos);
+      run.template operator()<kTileRows>();
   }
 }
 
@@ -63,19 +95,38 @@ __global__ __launch_bounds__(kGemmThreads) void grad_rows_bf16_kernel(GradGemmAr
 // tiles an XCD runs at once share 8 + 4 panels in its L2.
 __global__ __launch_bounds__(kGemmThreads) void grad_weights_bf16_kernel(GradGemmArgs a) {
   __shared__ __attribute__((aligned(16))) char lds[kGemmLdsBytes];
+  __shared__ int offsets[kMaxTileSegs + 1];
+  for (int i = threadIdx.x; i <= a.G; i += kGemmThreads) offsets[i] = a.offsets[i];
   const bool l0 = a.layer == 0;
   const int N = l0 ? a.F : a.H, C = l0 ? a.H : a.F;
   const int NR = (N + 255) / 256, NC = (C + 255) / 256, rows = (l0 ? 2 : 1) * NR;
   const int T = a.E * rows * NC, grid = gridDim.x;
   const Shuffle sm = make_shuffle(a.shuffle, T);
-  for (int v = xcd_slot(blockIdx.x, grid); v < T; v += grid) {
+  auto tile = [&](int v) {
     const int s = shuffled(sm, v), e = s / (rows * NC), l = s - e * rows * NC;
     const int nb = (rows + 7) / 8, b = min((int)((int64_t)(l / NC) * nb / rows), nb - 1);
     auto first = [&](int i) { return (int)((int64_t)i * rows / nb); };
     const int bb = first(b + 1) <= l / NC ? b + 1 : b;
     const int r0 = first(bb), rb = first(bb + 1) - r0, lb = l - r0 * NC;
     const int row = r0 + lb % rb, second = row >= NR;
-    grad_tile<kGradWeights, kTileRows>(a, GradTile{e, (row - second * NR) * 256, lb / rb * 256, second}, lds, nullptr);
+    return GradTile{e, (row - second * NR) * 256, lb / rb * 256, second};
+  };
+  GradWave<kGradWeights, kTileRows> wave(a, lds, offsets);
+  int v = xcd_slot(blockIdx.x, grid);
+  if (v >= T) return;
+  __syncthreads();
+  GradTile t = tile(v);
+  wave.begin(t, nullptr);
+  while (true) {
+    wave.multiply();
+    v += grid;
+    const GradTile now = t;
+    if (v < T) {
+      t = tile(v);
+      wave.begin(t, nullptr);
+    }
+    wave.epilogue(now, nullptr);
+    if (v >= T) break;
   }
 }
 
