@@ -364,6 +364,18 @@ moe_status_t check_grad_gemm(const moe_problem_t* p, int32_t layer) {
   return is_mx(p) ? MOE_ERR_UNSUPPORTED : MOE_OK;
 }
 
+// The workspace of a gradient of the grouped GEMM, and that it overlaps nothing.
+moe_status_t check_grad_ws(const moe_problem_t* p, const void* ws, size_t ws_bytes, const Span* s, int n,
+                           const int32_t* offsets) {
+  const size_t need = moe_workspace_bytes(p, MOE_OP_GROUPED_GEMM_BACKWARD);
+  if (need == 0) return MOE_OK;
+  if (!ws || ws_bytes < need) return MOE_ERR_WORKSPACE_TOO_SMALL;
+  if (!aligned(ws, kAlign) || overlap(ws, need, offsets, (size_t)(segments(p) + 1) * 4)) return MOE_ERR_INVALID_ARGUMENT;
+  for (int i = 0; i < n; ++i)
+    if (overlap(ws, need, s[i].p, s[i].n)) return MOE_ERR_INVALID_ARGUMENT;
+  return MOE_OK;
+}
+
 GradGemmArgs grad_args(const moe_problem_t* p, int layer, const int32_t* offsets) {
   GradGemmArgs g{};
   g.layer = layer;
@@ -373,6 +385,7 @@ GradGemmArgs grad_args(const moe_problem_t* p, int layer, const int32_t* offsets
   g.F = p->ffn;
   g.E = held(p);
   g.G = segments(p);
+  g.all_held = held(p) == p->num_experts;
   g.shuffle = debug_shuffle();
   return g;
 }
@@ -406,7 +419,7 @@ size_t moe_workspace_bytes(const moe_problem_t* p, int32_t op) {
     case MOE_OP_DISPATCH: return permute_ws_bytes(plan_of(p));
     case MOE_OP_GROUPED_GEMM: return p->dtype == MOE_DTYPE_BF16 ? gemm_split_ws_bytes() : 0;
     case MOE_OP_LAYER: return layer_ws(p).total;
-    case MOE_OP_GROUPED_GEMM_BACKWARD: return 0;
+    case MOE_OP_GROUPED_GEMM_BACKWARD: return is_mx(p) || p->num_tokens == 0 ? 0 : grad_ws_bytes();
     case MOE_OP_LAYER_DECODE: return check_decode(p) == MOE_OK ? decode_ws(p, split_of(p)).total : 0;
   }
   return 0;
@@ -918,6 +931,16 @@ moe_status_t moe_grouped_gemm_aux(const moe_problem_t* p, const void* a, const v
     st = validate_offsets(p, offsets, hs);
     if (st != MOE_OK) return st;
   }
+  if (p->dtype == MOE_DTYPE_F32) {
+    GradGemmArgs g = grad_args(p, 0, offsets);
+    g.x = a;
+    g.w0 = w0;
+    g.w1 = w1;
+    g.o0 = gate;
+    g.o1 = up;
+    g.o2 = c;
+    return hip_status(launch_keep_f32(g, hs));
+  }
   GemmProblem gp;
   gp.layer = 0;
   gp.a = a;
@@ -934,7 +957,7 @@ moe_status_t moe_grouped_gemm_aux(const moe_problem_t* p, const void* a, const v
   gp.shuffle = debug_shuffle();
   gp.gate = gate;
   gp.up = up;
-  return hip_status(p->dtype == MOE_DTYPE_BF16 ? launch_grouped_gemm_bf16(gp, hs) : launch_grouped_gemm_f32(gp, hs));
+  return hip_status(launch_grouped_gemm_bf16(gp, hs));
 }
 
 moe_status_t moe_grouped_gemm_backward(const moe_problem_t* p, int32_t layer, const void* d0, const void* d1,
@@ -954,6 +977,7 @@ moe_status_t moe_grouped_gemm_backward(const moe_problem_t* p, int32_t layer, co
   if ((st = check_spans(s, n)) != MOE_OK || (st = check_words(offsets, (size_t)(segments(p) + 1) * 4, s, n)) != MOE_OK)
     return st;
   if (R == 0) return MOE_OK;
+  if ((st = check_grad_ws(p, ws, ws_bytes, s, n, offsets)) != MOE_OK) return st;
   hipStream_t hs = (hipStream_t)stream;
   if (debug_validate()) {
     st = validate_offsets(p, offsets, hs);
@@ -968,7 +992,7 @@ moe_status_t moe_grouped_gemm_backward(const moe_problem_t* p, int32_t layer, co
   g.up = up;
   g.o0 = o0;
   g.o1 = o1;
-  return hip_status(launch_grad_rows(g, p->dtype == MOE_DTYPE_BF16, hs));
+  return hip_status(launch_grad_rows(g, p->dtype == MOE_DTYPE_BF16, ws, hs));
 }
 
 moe_status_t moe_grouped_gemm_backward_weights(const moe_problem_t* p, int32_t layer, const void* d0, const void* d1,
@@ -989,6 +1013,7 @@ moe_status_t moe_grouped_gemm_backward_weights(const moe_problem_t* p, int32_t l
   const int n = layer == 0 ? 5 : 3;
   if ((st = check_spans(s, n)) != MOE_OK || (st = check_words(offsets, (size_t)(segments(p) + 1) * 4, s, n)) != MOE_OK)
     return st;
+  if ((st = check_grad_ws(p, ws, ws_bytes, s, n, offsets)) != MOE_OK) return st;
   hipStream_t hs = (hipStream_t)stream;
   if (debug_validate()) {
     st = validate_offsets(p, offsets, hs);
@@ -1002,7 +1027,7 @@ moe_status_t moe_grouped_gemm_backward_weights(const moe_problem_t* p, int32_t l
   g.o1 = dw1;
   g.out_bf16 = dw_dtype == MOE_DTYPE_BF16;
   g.accumulate = accumulate != 0;
-  return hip_status(launch_grad_weights(g, p->dtype == MOE_DTYPE_BF16, hs));
+  return hip_status(launch_grad_weights(g, p->dtype == MOE_DTYPE_BF16, ws, hs));
 }
 
 moe_status_t moe_quantize_mxfp8(int64_t rows, int32_t cols, int32_t src_dtype, const void* src, void* dst,

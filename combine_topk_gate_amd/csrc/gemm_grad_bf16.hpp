@@ -82,12 +82,25 @@ struct GradTile {
   int row0;     // weights: first row of dW (column of D)
   int col0;     // first column
   int second;   // weights: the second pair of matrices (d1, o1)
+  int part, parts;  // which of the parts of the K steps (0 of 1: all)
 };
+
+// First step of part i of n of nk K steps.
+__device__ __forceinline__ int part_begin(int nk, int i, int n) { return (int)((int64_t)nk * i / n); }
+
+// K steps of expert e's weights' gradient: each segment's last one is filled up with zero rows.
+__device__ __forceinline__ int weight_steps(const GradGemmArgs& p, const int* offsets, int e) {
+  int nk = 0;
+  const int S = p.G / p.E;
+  for (int s = 0; s < S; ++s) nk += (offsets[s * p.E + e + 1] - offsets[s * p.E + e] + kBK - 1) / kBK;
+  return uniform(nk);
+}
 
 // What a wave does for one tile after the other:
 //   begin(t)     addresses, and the loads of the first K step into registers
 //   multiply()   the K loop
-//   epilogue(t)  from the accumulators to memory
+//   epilogue(t)  from the accumulators to memory, or store_part(u): a split
+//                tile's sums over its part of the K steps, as they are
 // The kernels call begin of the next tile before the epilogue of this one, so
 // the first loads' latency is not waited for.
 template <GradKind KIND, int TM>
@@ -119,7 +132,7 @@ struct GradWave {
   // the K step to load next
   __amdgpu_buffer_rsrc_t rw, rx;
   uint32_t xs = 0;
-  int e = 0, col0 = 0, row0 = 0, nk = 0;
+  int e = 0, col0 = 0, row0 = 0, k0 = 0, nk = 0;  // K steps k0 .. k0 + nk
   const __bf16* d = nullptr;
   int r = 0, rend = 0, sb = 0;  // weights: the segment's row and end, the next source block
   uint32_t xvoff[XKC ? XI : 1];
@@ -146,7 +159,7 @@ struct GradWave {
       }
     } else {
       const int per = K / kBK;
-      kt = min(kt, nk - 1);
+      kt = k0 + min(kt, nk - 1);
       const bool second = KIND == kGradRows0 && kt >= per;
       const int kk = second ? kt - per : kt;
       const __bf16* w = (const __bf16*)(second ? p.w1 : p.w0) + (int64_t)e * K * N;
@@ -184,6 +197,12 @@ struct GradWave {
     }
   }
 
+  // The tile's part of all nk steps.
+  __device__ __forceinline__ void range(const GradTile& t) {
+    k0 = uniform(part_begin(nk, t.part, t.parts));
+    nk = uniform(part_begin(nk, t.part + 1, t.parts)) - k0;
+  }
+
   // rowpos (rows): the rows of the tile in the buffers, -1 for those it lacks.
   __device__ __forceinline__ void begin(const GradTile& t, const int* __restrict__ rowpos) {
     e = uniform(t.e);
@@ -191,15 +210,25 @@ struct GradWave {
     if constexpr (KIND == kGradWeights) {
       row0 = uniform(t.row0);
       d = (const __bf16*)(uniform(t.second) ? p.d1 : p.d0);
-      nk = 0;
-      const int S = p.G / p.E;
-      for (int s = 0; s < S; ++s) nk += (offsets[s * p.E + e + 1] - offsets[s * p.E + e] + kBK - 1) / kBK;
-      nk = uniform(nk);
-      r = -kBK;
-      rend = sb = 0;
+      nk = weight_steps(p, offsets, e);
+      range(t);
+      // to the step before k0
+      r = rend = sb = 0;
+      for (int left = k0;;) {
+        const int n = (rend - r + kBK - 1) / kBK;
+        if (left <= n) {
+          r += (left - 1) * kBK;
+          break;
+        }
+        left -= n;
+        r = uniform(offsets[sb * p.E + e]);
+        rend = uniform(offsets[sb * p.E + e + 1]);
+        ++sb;
+      }
       xvoff[0] = (uint32_t)cr * xpitch + (uint32_t)cc * 16u;
     } else {
       nk = (KIND == kGradRows0 ? 2 : 1) * (K / kBK);
+      range(t);
 #pragma unroll
       for (int i = 0; i < XI; ++i) {
         const int pos = rowpos[(tid >> 3) + 32 * i];
@@ -511,6 +540,22 @@ struct GradWave {
         }
       }
     }
+  }
+
+  // The accumulators as they lie: 16 bytes a lane, fragment by fragment (mi NJ + nj) of each wave.
+  __device__ __forceinline__ void store_part(int u) {
+    f32x4_t* dst = reinterpret_cast<f32x4_t*>(p.split.part) + ((int64_t)u * 4 + (tid >> 6)) * 16 * 4 * 64 + lane;
+#pragma unroll
+    for (int mi = 0; mi < 4; ++mi)
+#pragma unroll
+      for (int nj = 0; nj < NJ; ++nj)
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          f32x4_t o;
+#pragma unroll
+          for (int v = 0; v < 4; ++v) o[v] = acc[mi][nj][4 * q + v];
+          dst[((mi * NJ + nj) * 4 + q) * 64] = o;
+        }
   }
 };
 

@@ -305,8 +305,7 @@ __global__ __launch_bounds__(256) void grouped_gemm_f32_kernel(const float* __re
                                                                const float* __restrict__ W0,
                                                                const float* __restrict__ W1, float* __restrict__ C,
                                                                int K, int N, int E, const int32_t* __restrict__ offsets,
-                                                               int G, uint32_t shuffle, float* __restrict__ gate,
-                                                               float* __restrict__ up) {
+                                                               int G, uint32_t shuffle) {
   __shared__ float xs[kF32Rows][kF32BK + 1];
   __shared__ float ws[kF32Rows][kF32BK + 1];
   __shared__ TileLds tl;
@@ -361,12 +360,7 @@ __global__ __launch_bounds__(256) void grouped_gemm_f32_kernel(const float* __re
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
           const int f = col0 + tx + 16 * i;
-          if (f >= N) continue;
-          dst[f] = silu_f32(acc[i][j]) * acc[i + 2][j];
-          if (gate) {
-            gate[(int64_t)(s0 + tr) * N + f] = acc[i][j];
-            up[(int64_t)(s0 + tr) * N + f] = acc[i + 2][j];
-          }
+          if (f < N) dst[f] = silu_f32(acc[i][j]) * acc[i + 2][j];
         }
       } else {
 #pragma unroll
@@ -507,11 +501,10 @@ hipError_t launch_grouped_gemm_f32(const GemmProblem& gp, hipStream_t s) {
   const int grid = device_cu_count() * 2;
   if (gp.layer == 0)
     grouped_gemm_f32_kernel<0><<<grid, 256, 0, s>>>((const float*)gp.a, (const float*)gp.w0, (const float*)gp.w1,
-                                                     (float*)gp.c, gp.K, gp.N, gp.E, gp.offsets, gp.G, gp.shuffle,
-                                                     (float*)gp.gate, (float*)gp.up);
+                                                     (float*)gp.c, gp.K, gp.N, gp.E, gp.offsets, gp.G, gp.shuffle);
   else
     grouped_gemm_f32_kernel<1><<<grid, 256, 0, s>>>((const float*)gp.a, (const float*)gp.w0, nullptr,
-                                                    (float*)gp.c, gp.K, gp.N, gp.E, gp.offsets, gp.G, gp.shuffle, nullptr, nullptr);
+                                                    (float*)gp.c, gp.K, gp.N, gp.E, gp.offsets, gp.G, gp.shuffle);
   return hipGetLastError();
 }
 

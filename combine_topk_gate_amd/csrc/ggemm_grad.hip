@@ -23,6 +23,58 @@ __device__ __forceinline__ SwigluGrad swiglu_grad(float dh, float g, float u) {
   return {dh * u * (s * fmaf(g, 1.0f - s, 1.0f)), dh * (g * s)};
 }
 
+// ------------------------------------------------------------------- split ---
+// The grid's last round (or only one) of r tiles is cut along K into s units
+// each, at most one a workgroup, where that is shorter: in microseconds, a K
+// step (bf16 64, f32 128 terms) takes `step` with few workgroups at work and
+// step + more with all, storing a unit's sums and reading them once more `store`
+// of the whole card's bandwidth, the second kernel 6.  Measured (whole, split):
+// 60 rows, 448 x 8576, one expert, 2 tiles of 268 steps: 178, 34 us; 1000 rows,
+// 1024 x 4096, 4 experts: 149, 78; weights of 8 experts 256 x 512, 32768 rows:
+// 132, 58.
+struct SplitCost {
+  float step, more, store;
+};
+constexpr SplitCost kSplitBf16{0.65f, 0.75f, 0.1f};
+constexpr SplitCost kSplitF32{2.0f, 0.0f, 0.01f};
+__host__ __device__ inline int split_parts(const SplitCost& c, int r, int nk, int grid) {
+  if (r <= 0) return 1;
+  int best = 1;
+  float least = 0.f;
+  const int most = nk / 2 < grid / r ? nk / 2 : grid / r;
+  for (int s = 1; s <= most; s += (s + 1) / 2) {  // 1, 2, 3, 5, 8, 12, ...
+    const float units = (float)(r * s);
+    const float t = (float)((nk + s - 1) / s) * (c.step + c.more * units / (float)grid) + (s > 1 ? c.store * units + 6.0f : 0.0f);
+    if (s == 1 || t < least) {
+      least = t;
+      best = s;
+    }
+  }
+  return best;
+}
+// Whether an f32 product takes tiles of 128 x 128 (tiles: how many there are)
+// with two groups of waves: from eight rounds of the CUs on, where their padding
+// and the last round's idle CUs weigh little; below, tiles of 64 x 64 with four
+// groups.  Measured (128, 64): weights of 4 experts 2048 x 8192, 512 rows each,
+// 64 rounds: 1.40, 1.77 ms; rows of 8 experts 2048 x 4096, 256 each, 1 round:
+// 1.24, 0.80.
+static bool wide_f32(int64_t tiles, int cus) { return tiles >= 8 * cus; }
+
+// A split tile's description for the second kernel.
+struct GradDesc {
+  int e, row0, col0, second, tm, rows, steps;
+};
+__device__ __forceinline__ void put_desc(const GradGemmArgs& a, int j, const GradDesc& d) {
+  int32_t* o = a.split.desc + (int64_t)j * kGradDescInts;
+  o[0] = d.e;
+  o[1] = d.row0;
+  o[2] = d.col0;
+  o[3] = d.second;
+  o[4] = d.tm;
+  o[5] = d.rows;
+  o[6] = d.steps;
+}
+
 // ------------------------------------------------------------------- bf16 ---
 // Rows: the experts' rows (over all source blocks) in tiles of 256, or of 128
 // where an expert has no more and in a last round that would leave half the
@@ -37,25 +89,30 @@ __global__ __launch_bounds__(kGemmThreads) void grad_rows_bf16_kernel(GradGemmAr
   const int T = build_expert_tile_table(a.offsets, a.G, a.E, kTileRows, tl) * NT;
   const int64_t panel = (int64_t)kTileRows * K * (KIND == kGradRows0 ? 4 : 2);
   const int grid = gridDim.x;
-  const int r = T % grid;
-  const int half = (r > 0 && 2 * r <= grid && T > grid) ? r : 0;  // tiles of the last round to halve
-  const int entries = T + half;
-  const Shuffle sm = make_shuffle(a.shuffle, T - half), sh = make_shuffle(a.shuffle, half);
-  GradTile t{0, 0, 0, 0};
+  // the last round's r tiles: split along K, or cut into two halves of 128 rows, or neither
+  const int r = T % grid, steps = (KIND == kGradRows0 ? 2 : 1) * (K / kBK);
+  const int s = a.split.hdr ? split_parts(kSplitBf16, r, steps, grid) : 1;
+  const int cut = s > 1 ? s : (r > 0 && 2 * r <= grid && T > grid) ? 2 : 1;
+  const int whole = cut > 1 ? T - r : T, entries = whole + (cut > 1 && s == 1 ? 2 * r : 0);
+  const Shuffle sm = make_shuffle(a.shuffle, whole), sh = make_shuffle(a.shuffle, T - whole);
+  if (a.split.hdr && blockIdx.x == 0 && threadIdx.x == 0) {
+    a.split.hdr[0] = s > 1 ? r : 0;
+    a.split.hdr[1] = s;
+  }
+  GradTile t{};
   bool low = false;  // 128 rows
   // Entry v or the next one of this workgroup that has rows; its rows' positions into rowpos[b].
   auto find = [&](int v, int b) {
     for (; v < entries; v += grid) {
-      const bool is_half = v >= T - half;
-      const int j = v - (T - half);
-      const TileCoord c = tile_coord(is_half ? T - half + shuffled(sh, j / 2) : shuffled(sm, v), a.E, NT, kTileRows,
-                                     xcd_slots, panel, tl);
-      const int m0 = is_half ? c.m0 + (j & 1) * (kTileRows / 2) : c.m0;
+      const int u = v - whole;  // from 0 on: halves
+      const TileCoord c = tile_coord(u >= 0 ? whole + shuffled(sh, u / 2) : shuffled(sm, v), a.E, NT, kTileRows, xcd_slots,
+                                     panel, tl);
+      const int m0 = u >= 0 ? c.m0 + (u & 1) * (kTileRows / 2) : c.m0;
       const int n = tl.expert_rows[c.g];
       if (m0 >= n) continue;
       rowpos[b][threadIdx.x] = expert_row(tl, c.g, a.E, S, m0, threadIdx.x);
-      t = {c.g, 0, c.nt * 256, 0};
-      low = is_half || n <= kTileRows / 2;
+      t = {uniform(c.g), 0, uniform(c.nt) * 256, 0, 0, 1};
+      low = uniform(u >= 0 || n <= kTileRows / 2);
       break;
     }
     return v;
@@ -88,6 +145,32 @@ __global__ __launch_bounds__(kGemmThreads) void grad_rows_bf16_kernel(GradGemmAr
     else
       run.template operator()<kTileRows>();
   }
+  // a unit of a split tile (a copy of the K loop of its own: with store_part beside the epilogue in one, the compiler
+  // spills up to 130 registers a tile)
+  const int slot = xcd_slot(blockIdx.x, grid), mine = slot - whole % grid + (slot < whole % grid ? grid : 0);
+  if (s == 1 || mine >= r * s) return;
+  const int j = mine / s, part = mine - j * s;
+  const TileCoord c = tile_coord(whole + shuffled(sh, j), a.E, NT, kTileRows, xcd_slots, panel, tl);
+  const int n = tl.expert_rows[c.g], pos = expert_row(tl, c.g, a.E, S, c.m0, threadIdx.x);
+  low = uniform(n <= kTileRows / 2);
+  t = {uniform(c.g), 0, uniform(c.nt) * 256, 0, part, s};
+  __syncthreads();
+  rowpos[0][threadIdx.x] = pos;
+  if (part == 0) {
+    if (threadIdx.x == 0) put_desc(a, j, {t.e, 0, t.col0, 0, low ? 128 : 256, min(n - c.m0, kTileRows), steps});
+    a.split.desc[(int64_t)j * kGradDescInts + 8 + threadIdx.x] = pos;
+  }
+  __syncthreads();
+  auto unit = [&]<int TM>() {
+    GradWave<KIND, TM> wave(a, lds, nullptr);
+    wave.begin(t, rowpos[0]);
+    wave.multiply();
+    wave.store_part(mine);
+  };
+  if (low)
+    unit.template operator()<kTileRows / 2>();
+  else
+    unit.template operator()<kTileRows>();
 }
 
 // Weights: 256 x 256 tiles of dW, expert by expert; the row tiles (layer 0:
@@ -101,205 +184,471 @@ __global__ __launch_bounds__(kGemmThreads) void grad_weights_bf16_kernel(GradGem
   const int N = l0 ? a.F : a.H, C = l0 ? a.H : a.F;
   const int NR = (N + 255) / 256, NC = (C + 255) / 256, rows = (l0 ? 2 : 1) * NR;
   const int T = a.E * rows * NC, grid = gridDim.x;
-  const Shuffle sm = make_shuffle(a.shuffle, T);
-  auto tile = [&](int v) {
-    const int s = shuffled(sm, v), e = s / (rows * NC), l = s - e * rows * NC;
+  const int r = T % grid;
+  int s = 1;
+  __syncthreads();
+  if (a.split.hdr) {
+    s = split_parts(kSplitBf16, r, (offsets[a.G] + a.E * kBK - 1) / (a.E * kBK), grid);  // steps: the experts' mean
+    if (blockIdx.x == 0 && threadIdx.x == 0) {
+      a.split.hdr[0] = s > 1 ? r : 0;
+      a.split.hdr[1] = s;
+    }
+  }
+  const int whole = s > 1 ? T - r : T;
+  const Shuffle sm = make_shuffle(a.shuffle, whole), sh = make_shuffle(a.shuffle, T - whole);
+  // tile n of the order
+  auto tile = [&](int n) {
+    const int e = n / (rows * NC), l = n - e * rows * NC;
     const int nb = (rows + 7) / 8, b = min((int)((int64_t)(l / NC) * nb / rows), nb - 1);
     auto first = [&](int i) { return (int)((int64_t)i * rows / nb); };
     const int bb = first(b + 1) <= l / NC ? b + 1 : b;
     const int r0 = first(bb), rb = first(bb + 1) - r0, lb = l - r0 * NC;
     const int row = r0 + lb % rb, second = row >= NR;
-    return GradTile{e, (row - second * NR) * 256, lb / rb * 256, second};
+    return GradTile{e, (row - second * NR) * 256, lb / rb * 256, second, 0, 1};
   };
-  GradWave<kGradWeights, kTileRows> wave(a, lds, offsets);
-  int v = xcd_slot(blockIdx.x, grid);
-  if (v >= T) return;
-  __syncthreads();
-  GradTile t = tile(v);
-  wave.begin(t, nullptr);
-  while (true) {
-    wave.multiply();
-    v += grid;
-    const GradTile now = t;
-    if (v < T) {
-      t = tile(v);
-      wave.begin(t, nullptr);
+  const int slot = xcd_slot(blockIdx.x, grid);
+  int v = slot;
+  if (v < whole) {
+    GradWave<kGradWeights, kTileRows> wave(a, lds, offsets);
+    GradTile t = tile(shuffled(sm, v));
+    wave.begin(t, nullptr);
+    while (true) {
+      wave.multiply();
+      v += grid;
+      const GradTile now = t;
+      if (v < whole) {
+        t = tile(shuffled(sm, v));
+        wave.begin(t, nullptr);
+      }
+      wave.epilogue(now, nullptr);
+      if (v >= whole) break;
     }
-    wave.epilogue(now, nullptr);
-    if (v >= T) break;
   }
+  // a unit of a split tile
+  const int mine = slot - whole % grid + (slot < whole % grid ? grid : 0);
+  if (s == 1 || mine >= r * s) return;
+  const int j = mine / s;
+  GradTile t = tile(whole + shuffled(sh, j));
+  t.part = mine - j * s;
+  t.parts = s;
+  if (t.part == 0 && threadIdx.x == 0)
+    put_desc(a, j, {t.e, t.row0, t.col0, t.second, 256, min(N - t.row0, 256), weight_steps(a, offsets, t.e)});
+  GradWave<kGradWeights, kTileRows> wave(a, lds, offsets);
+  wave.begin(t, nullptr);
+  wave.multiply();
+  wave.store_part(mine);
+}
+
+// Second kernel of a split: a wave per fragment of 32 x 32 outputs adds the
+// parts' sums (in order, from the first) and stores what the tile's epilogue
+// would.  The lanes hold what they held in the tile: row lane % 32, columns 8 q
+// + 4 (lane / 32).  T is the products' type: it fixes the tiles' width (256, 64)
+// and the fragments of a wave (16 places in bf16, 1).
+template <GradKind KIND, typename T>
+__global__ __launch_bounds__(256) void grad_reduce_kernel(GradGemmArgs a) {
+  constexpr bool F32 = sizeof(T) == 4;
+  constexpr int TC = F32 ? 64 : 256, FW = F32 ? 1 : 16, MI = TC / 64;
+  const int tiles = a.split.hdr[0], parts = a.split.hdr[1];
+  const int lane = threadIdx.x & 63, lrow = lane & 31, lk = lane >> 5;
+  const bool l0 = KIND == kGradRows0 || (KIND == kGradWeights && a.layer == 0);
+  const int N = KIND == kGradRows1 ? a.F : KIND == kGradRows0 ? a.H : (l0 ? a.H : a.F);
+  const int DN = l0 ? a.F : a.H;
+  for (int item = blockIdx.x * 4 + (threadIdx.x >> 6); item < tiles * 4 * FW; item += gridDim.x * 4) {
+    const int j = item / (4 * FW), wave = item / FW % 4, f = item % FW;
+    const int32_t* desc = a.split.desc + (int64_t)j * kGradDescInts;
+    const int e = desc[0], row0 = desc[1], col0 = desc[2], second = desc[3], tm = desc[4], rows = desc[5], nk = desc[6];
+    const int NJ = tm / 64, mi = f / NJ, nj = f - mi * NJ;
+    if (mi >= MI) continue;
+    const int row = (wave >> 1) * (tm / 2) + nj * 32, n0 = col0 + (wave & 1) * (TC / 2) + mi * 32 + 4 * lk;
+    if (row >= rows || n0 - 4 * lk >= N) continue;
+    const f32x4_t* src = reinterpret_cast<const f32x4_t*>(a.split.part) + (((int64_t)j * parts * 4 + wave) * FW + f) * 4 * 64 + lane;
+    constexpr int64_t kUnit = 4 * FW * 4 * 64;
+    f32x4_t sum[4] = {};
+    for (int i = 0; i < parts; i += 4) {
+      f32x4_t v[4][4];
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        const bool has = i + u < parts && part_begin(nk, i + u + 1, parts) > part_begin(nk, i + u, parts);
+#pragma unroll
+        for (int q = 0; q < 4; ++q) v[u][q] = has ? src[(i + u) * kUnit + q * 64] : f32x4_t{0.f, 0.f, 0.f, 0.f};
+      }
+#pragma unroll
+      for (int u = 0; u < 4; ++u)
+#pragma unroll
+        for (int q = 0; q < 4; ++q) sum[q] += v[u][q];
+    }
+    if constexpr (KIND == kGradWeights) {
+      if (row + lrow >= rows) continue;
+      void* const out = second ? a.o1 : a.o0;
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const int n = n0 + 8 * q;
+        if (n >= N) continue;
+        const int64_t at = ((int64_t)e * DN + row0 + row + lrow) * N + n;
+        if (a.out_bf16) {
+          gf_store4((__bf16*)out + at, sum[q]);
+        } else {
+          float* p = (float*)out + at;
+          gf_store4(p, a.accumulate ? *(const f32x4_t*)p + sum[q] : sum[q]);
+        }
+      }
+    } else {
+      const int pos = desc[8 + row + lrow];
+      if (pos < 0) continue;
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const int n = n0 + 8 * q;
+        if (n >= N) continue;
+        const int64_t at = (int64_t)pos * N + n;
+        if constexpr (KIND == kGradRows0) {
+          gf_store4((T*)a.o0 + at, sum[q]);
+        } else {
+          typedef T T4 __attribute__((ext_vector_type(4)));
+          const T4 g = *(const T4*)((const T*)a.gate + at), u = *(const T4*)((const T*)a.up + at);
+          f32x4_t og, ou;
+#pragma unroll
+          for (int v = 0; v < 4; ++v) {
+            const SwigluGrad d = F32 ? swiglu_grad(sum[q][v], (float)g[v], (float)u[v])
+                                     : swiglu_grad_fast(sum[q][v], (float)g[v], (float)u[v]);
+            og[v] = d.dg;
+            ou[v] = d.du;
+          }
+          gf_store4((T*)a.o0 + at, og);
+          gf_store4((T*)a.o1 + at, ou);
+        }
+      }
+    }
+  }
+}
+
+template <GradKind KIND, typename T>
+hipError_t grad_reduce_launch(const GradGemmArgs& a, hipStream_t s) {
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess || !a.split.hdr) return e;
+  grad_reduce_kernel<KIND, T><<<4 * device_cu_count(), 256, 0, s>>>(a);
+  return hipGetLastError();
 }
 
 // -------------------------------------------------------------------- f32 ---
-template <int LAYER, int TS>
-__global__ __launch_bounds__(kGfThreads) void grad_rows_f32_kernel(GradGemmArgs a) {
-  __shared__ __attribute__((aligned(16))) float lds[gf_lds_floats<TS>];
+// Rows (KIND) as the bf16 kernel above, tiles of TX x TX.
+template <GradKind KIND, int TX, int KG>
+__global__ __launch_bounds__(256 * KG) void grad_rows_f32_kernel(GradGemmArgs a) {
+  typedef GfTile<TX, TX, KG> Tile;
+  __shared__ __attribute__((aligned(16))) float lds[Tile::kLds];
   __shared__ TileLds tl;
-  __shared__ int rowpos[TS];
-  const int K = LAYER == 0 ? a.F : a.H, N = LAYER == 0 ? a.H : a.F;  // reduction and columns of a product
-  const int NT = (N + TS - 1) / TS, S = a.G / a.E;
-  const int total = build_expert_tile_table(a.offsets, a.G, a.E, TS, tl) * NT;
-  const Shuffle sm = make_shuffle(a.shuffle, total);
-  constexpr int kBuf = kGfK * gf_pitch<TS>;
-  for (int v = blockIdx.x; v < total; v += gridDim.x) {
-    const TileCoord c = tile_coord(shuffled(sm, v), a.E, NT, TS, 1, 0, tl);
-    const int e = c.g, col0 = c.nt * TS;
-    for (int i = threadIdx.x; i < TS; i += kGfThreads) rowpos[i] = expert_row(tl, e, a.E, S, c.m0, i);
+  __shared__ int rowpos[TX];
+  const int K = KIND == kGradRows0 ? a.F : a.H, N = KIND == kGradRows0 ? a.H : a.F;  // reduction and columns of a product
+  const int NT = (N + TX - 1) / TX, S = a.G / a.E, grid = gridDim.x;
+  const int T = build_expert_tile_table(a.offsets, a.G, a.E, TX, tl) * NT;
+  const int per = K / kGfK, steps = KIND == kGradRows0 ? 2 * per : per;
+  const int r = T % grid, s = a.split.hdr ? split_parts(kSplitF32, r, steps / KG, grid) : 1;
+  const int whole = s > 1 ? T - r : T, entries = whole + (s > 1 ? r * s : 0);
+  const Shuffle sm = make_shuffle(a.shuffle, whole), sh = make_shuffle(a.shuffle, T - whole);
+  if (a.split.hdr && blockIdx.x == 0 && threadIdx.x == 0) {
+    a.split.hdr[0] = s > 1 ? r : 0;
+    a.split.hdr[1] = s;
+  }
+  const int i = threadIdx.x & 255, g = threadIdx.x >> 8;
+  for (int v = blockIdx.x; v < entries; v += grid) {
+    const int u = v - whole, j = u / s, part = u >= 0 ? u - j * s : 0, parts = u >= 0 ? s : 1;
+    const TileCoord c = tile_coord(u >= 0 ? whole + shuffled(sh, j) : shuffled(sm, v), a.E, NT, TX, 1, 0, tl);
+    const int e = c.g, col0 = c.nt * TX;
+    if (threadIdx.x < TX) {
+      const int pos = expert_row(tl, e, a.E, S, c.m0, threadIdx.x);
+      rowpos[threadIdx.x] = pos;
+      if (u >= 0 && part == 0) a.split.desc[(int64_t)j * kGradDescInts + 8 + threadIdx.x] = pos;
+    }
+    if (u >= 0 && part == 0 && threadIdx.x == 0)
+      put_desc(a, j, {e, 0, col0, 0, TX, min(tl.expert_rows[e] - c.m0, TX), steps});
     __syncthreads();
-    const float* rows0[TS / 32];
-    const float* rows1[TS / 32];
+    const float* rows0[TX / 32];
+    const float* rows1[TX / 32];
 #pragma unroll
-    for (int i = 0; i < TS / 32; ++i) {
-      const int r = rowpos[(threadIdx.x >> 3) + 32 * i];
-      rows0[i] = r >= 0 ? (const float*)a.d0 + (int64_t)r * K : nullptr;
-      rows1[i] = LAYER == 0 && r >= 0 ? (const float*)a.d1 + (int64_t)r * K : nullptr;
+    for (int h = 0; h < TX / 32; ++h) {
+      const int pos = rowpos[(i >> 3) + 32 * h];
+      rows0[h] = pos >= 0 ? (const float*)a.d0 + (int64_t)pos * K : nullptr;
+      rows1[h] = KIND == kGradRows0 && pos >= 0 ? (const float*)a.d1 + (int64_t)pos * K : nullptr;
     }
     const float* w0 = (const float*)a.w0 + (int64_t)e * K * N;
-    const float* w1 = LAYER == 0 ? (const float*)a.w1 + (int64_t)e * K * N : nullptr;
-    const int per = K / kGfK, steps = LAYER == 0 ? 2 * per : per;
-    GfPart<TS> pw, px;
-    auto load = [&](int s) {
-      const bool second = LAYER == 0 && s >= per;
-      const int k = (second ? s - per : s) * kGfK;
-      gf_load_k<TS>(px, second ? rows1 : rows0, k);
-      gf_load_c<TS>(pw, (second ? w1 : w0) + (int64_t)k * N, N, kGfK, col0, N);
+    const float* w1 = KIND == kGradRows0 ? (const float*)a.w1 + (int64_t)e * K * N : nullptr;
+    // the unit's steps, and of them this group's
+    const int k0 = part_begin(steps, part, parts), n = part_begin(steps, part + 1, parts) - k0;
+    const int b = k0 + part_begin(n, g, KG), end = k0 + part_begin(n, g + 1, KG);
+    GfPart<TX> pw, px;
+    auto load = [&](int at) {
+      const int st = b + at;
+      const bool second = KIND == kGradRows0 && st >= per;
+      const int k = (second ? st - per : st) * kGfK;
+      px.load_k(second ? rows1 : rows0, k, i);
+      pw.load_c((second ? w1 : w0) + (int64_t)k * N, N, kGfK, col0, N, i);
     };
-    auto store = [&](int b) {
-      gf_store_c<TS>(lds + b * 2 * kBuf, pw);
-      gf_store_k<TS>(lds + b * 2 * kBuf + kBuf, px);
-    };
-    GfAcc<TS> acc;
-    gf_zero(acc);
-    load(0);
-    store(0);
-    __syncthreads();
-    for (int s = 0; s < steps; ++s) {
-      if (s + 1 < steps) load(s + 1);
-      gf_mul<TS>(acc, lds + (s & 1) * 2 * kBuf, lds + (s & 1) * 2 * kBuf + kBuf);
-      if (s + 1 < steps) store((s + 1) & 1);
-      __syncthreads();
-    }
-    gf_each<TS>(acc, [&](int t, int n, f32x4_t o) {
-      const int r = rowpos[t];
-      if (r < 0 || col0 + n >= N) return;
-      const int64_t at = (int64_t)r * N + col0 + n;
-      if constexpr (LAYER == 0) {
-        gf_store4((float*)a.o0 + at, o);
-      } else {
-        const f32x4_t g = gf_load4((const float*)a.gate + at), u = gf_load4((const float*)a.up + at);
-        f32x4_t dg, du;
+    Tile tile;
+    tile.run(lds, end - b, (n + KG - 1) / KG, load, [&](float* l) { px.store_k(l, i); }, [&](float* l) { pw.store_c(l, i); });
+    tile.each(lds, [&](int fj, int q, f32x4_t (&o)[Tile::MI]) {
+      if (u >= 0) {
+        if constexpr (Tile::MI == 1)
+          reinterpret_cast<f32x4_t*>(a.split.part)[(((int64_t)u * 4 + (i >> 6)) * 4 + q) * 64 + (i & 63)] = o[0];
+        return;
+      }
+      const int pos = rowpos[Tile::row(fj)];
+      if (pos < 0) return;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const SwigluGrad d = swiglu_grad(o[i], g[i], u[i]);
-          dg[i] = d.dg;
-          du[i] = d.du;
+      for (int m = 0; m < Tile::MI; ++m) {
+        const int col = col0 + Tile::col(m, q);
+        if (col >= N) continue;
+        const int64_t at = (int64_t)pos * N + col;
+        if constexpr (KIND == kGradRows0) {
+          gf_store4((float*)a.o0 + at, o[m]);
+        } else {
+          const f32x4_t gv = *(const f32x4_t*)((const float*)a.gate + at), uv = *(const f32x4_t*)((const float*)a.up + at);
+          f32x4_t dg, du;
+#pragma unroll
+          for (int h = 0; h < 4; ++h) {
+            const SwigluGrad d = swiglu_grad(o[m][h], gv[h], uv[h]);
+            dg[h] = d.dg;
+            du[h] = d.du;
+          }
+          gf_store4((float*)a.o0 + at, dg);
+          gf_store4((float*)a.o1 + at, du);
         }
-        gf_store4((float*)a.o0 + at, dg);
-        gf_store4((float*)a.o1 + at, du);
       }
     });
-    __syncthreads();  // rowpos and the LDS buffers are free for the next tile
+    __syncthreads();  // rowpos and the buffers are free for the next tile
   }
 }
 
-// Tile of dW[e]: TS of the first operand's columns (its rows) x TS of x's.
-// The K steps run over the expert's segments one after the other, the last
-// step of each filled up with zero rows.
-template <int LAYER, int TS>
-__global__ __launch_bounds__(kGfThreads) void grad_weights_f32_kernel(GradGemmArgs a) {
-  __shared__ __attribute__((aligned(16))) float lds[gf_lds_floats<TS>];
-  const int N = LAYER == 0 ? a.F : a.H, C = LAYER == 0 ? a.H : a.F;  // rows and columns of dW
-  const int NR = (N + TS - 1) / TS, NC = (C + TS - 1) / TS, S = a.G / a.E;
-  const int mats = LAYER == 0 ? 2 : 1;
-  const int64_t total = (int64_t)a.E * mats * NR * NC;
-  constexpr int kBuf = kGfK * gf_pitch<TS>;
-  for (int64_t v = blockIdx.x; v < total; v += gridDim.x) {
-    const int e = (int)(v / ((int64_t)mats * NR * NC));
-    int l = (int)(v - (int64_t)e * mats * NR * NC);
+// Weights: tiles of dW[e], TX of the first operand's columns (its rows) x TX of
+// x's.  The K steps run over the expert's segments one after the other, the
+// last step of each filled up with zero rows.
+template <int TX, int KG>
+__global__ __launch_bounds__(256 * KG) void grad_weights_f32_kernel(GradGemmArgs a) {
+  typedef GfTile<TX, TX, KG> Tile;
+  __shared__ __attribute__((aligned(16))) float lds[Tile::kLds];
+  __shared__ int offsets[kMaxTileSegs + 1];
+  for (int h = threadIdx.x; h <= a.G; h += 256 * KG) offsets[h] = a.offsets[h];
+  __syncthreads();
+  const bool l0 = a.layer == 0;
+  const int N = l0 ? a.F : a.H, C = l0 ? a.H : a.F;  // rows and columns of dW
+  const int NR = (N + TX - 1) / TX, NC = (C + TX - 1) / TX, S = a.G / a.E, mats = l0 ? 2 : 1, grid = gridDim.x;
+  const int T = a.E * mats * NR * NC;
+  const int r = T % grid, mean = (offsets[a.G] + a.E * kGfK - 1) / (a.E * kGfK);
+  const int s = a.split.hdr ? split_parts(kSplitF32, r, mean / KG, grid) : 1;
+  const int whole = s > 1 ? T - r : T, entries = whole + (s > 1 ? r * s : 0);
+  const Shuffle sm = make_shuffle(a.shuffle, whole), sh = make_shuffle(a.shuffle, T - whole);
+  if (a.split.hdr && blockIdx.x == 0 && threadIdx.x == 0) {
+    a.split.hdr[0] = s > 1 ? r : 0;
+    a.split.hdr[1] = s;
+  }
+  const int i = threadIdx.x & 255, g = threadIdx.x >> 8;
+  for (int v = blockIdx.x; v < entries; v += grid) {
+    const int u = v - whole, j = u / s, part = u >= 0 ? u - j * s : 0, parts = u >= 0 ? s : 1;
+    int l = u >= 0 ? whole + shuffled(sh, j) : shuffled(sm, v);
+    const int e = l / (mats * NR * NC);
+    l -= e * mats * NR * NC;
     const int m = l / (NR * NC);
     l -= m * NR * NC;
-    const int row0 = l % NR * TS, col0 = l / NR * TS;
+    const int row0 = l % NR * TX, col0 = l / NR * TX;
+    int steps = 0;
+    for (int h = 0; h < S; ++h) steps += (offsets[h * a.E + e + 1] - offsets[h * a.E + e] + kGfK - 1) / kGfK;
+    if (u >= 0 && part == 0 && threadIdx.x == 0) put_desc(a, j, {e, row0, col0, m, TX, min(N - row0, TX), steps});
+    const int k0 = part_begin(steps, part, parts), n = part_begin(steps, part + 1, parts) - k0;
+    const int b = k0 + part_begin(n, g, KG), end = k0 + part_begin(n, g + 1, KG);
     const float* d = (const float*)(m ? a.d1 : a.d0);
-    int s = 0, r = 0, end = 0;  // the segment being read, its next row and its end
-    auto next_segment = [&] {  // to the first unread row; false: none left
-      while (r >= end && s < S) {
-        r = a.offsets[s * a.E + e];
-        end = a.offsets[s * a.E + e + 1];
-        ++s;
+    int row = 0, rend = 0, sb = 0;  // the step before b: its row, the segment's end, the next source block
+    for (int left = b;;) {
+      const int have = (rend - row + kGfK - 1) / kGfK;
+      if (left <= have) {
+        row += (left - 1) * kGfK;
+        break;
       }
-      return r < end;
-    };
-    GfPart<TS> pw, px;
-    auto load = [&] {
-      const int n = end - r;
-      gf_load_c<TS>(pw, (const float*)a.x + (int64_t)r * C, C, n, col0, C);
-      gf_load_c<TS>(px, d + (int64_t)r * N, N, n, row0, N);
-      r += kGfK;
-    };
-    auto store = [&](int b) {
-      gf_store_c<TS>(lds + b * 2 * kBuf, pw);
-      gf_store_c<TS>(lds + b * 2 * kBuf + kBuf, px);
-    };
-    GfAcc<TS> acc;
-    gf_zero(acc);
-    bool more = next_segment();
-    if (more) {
-      load();
-      store(0);
+      left -= have;
+      row = offsets[sb * a.E + e];
+      rend = offsets[sb * a.E + e + 1];
+      ++sb;
     }
-    __syncthreads();
-    for (int b = 0; more; b ^= 1) {
-      more = next_segment();
-      if (more) load();
-      gf_mul<TS>(acc, lds + b * 2 * kBuf, lds + b * 2 * kBuf + kBuf);
-      if (more) store(b ^ 1);
-      __syncthreads();
-    }
-    void* out = m ? a.o1 : a.o0;
-    gf_each<TS>(acc, [&](int t, int n, f32x4_t o) {
-      if (row0 + t >= N || col0 + n >= C) return;
-      const int64_t at = ((int64_t)e * N + row0 + t) * C + col0 + n;
-      if (a.out_bf16) {
-        gf_store4((__bf16*)out + at, o);
-      } else {
-        float* p = (float*)out + at;
-        gf_store4(p, a.accumulate ? *(const f32x4_t*)p + o : o);
+    GfPart<TX> pw, px;
+    auto load = [&](int) {
+      row += kGfK;
+      while (row >= rend) {
+        row = offsets[sb * a.E + e];
+        rend = offsets[sb * a.E + e + 1];
+        ++sb;
+      }
+      pw.load_c((const float*)a.x + (int64_t)row * C, C, rend - row, col0, C, i);
+      px.load_c(d + (int64_t)row * N, N, rend - row, row0, N, i);
+    };
+    Tile tile;
+    tile.run(lds, end - b, (n + KG - 1) / KG, load, [&](float* q) { px.store_c(q, i); }, [&](float* q) { pw.store_c(q, i); });
+    void* const out = m ? a.o1 : a.o0;
+    tile.each(lds, [&](int fj, int q, f32x4_t (&o)[Tile::MI]) {
+      if (u >= 0) {
+        if constexpr (Tile::MI == 1)
+          reinterpret_cast<f32x4_t*>(a.split.part)[(((int64_t)u * 4 + (i >> 6)) * 4 + q) * 64 + (i & 63)] = o[0];
+        return;
+      }
+      const int dr = row0 + Tile::row(fj);
+      if (dr >= N) return;
+#pragma unroll
+      for (int h = 0; h < Tile::MI; ++h) {
+        const int col = col0 + Tile::col(h, q);
+        if (col >= C) continue;
+        const int64_t at = ((int64_t)e * N + dr) * C + col;
+        if (a.out_bf16) {
+          gf_store4((__bf16*)out + at, o[h]);
+        } else {
+          float* p = (float*)out + at;
+          gf_store4(p, a.accumulate ? *(const f32x4_t*)p + o[h] : o[h]);
+        }
       }
     });
+    __syncthreads();
   }
 }
 
-template <int LAYER>
-hipError_t grad_rows_launch(const GradGemmArgs& a, hipStream_t s) {
-  grad_rows_f32_kernel<LAYER, 64><<<2 * device_cu_count(), kGfThreads, 0, s>>>(a);
-  return hipGetLastError();
+// The forward gate and up products, kept: tiles of 64 rows x 64 columns of both
+// (128 weight rows, those of a wave 32 of gate and the same 32 of up, so a lane
+// has both of an element).
+__global__ __launch_bounds__(512) void keep_f32_kernel(GradGemmArgs a) {
+  constexpr int KG = 2;
+  typedef GfTile<64, 128, KG> Tile;
+  __shared__ __attribute__((aligned(16))) float lds[Tile::kLds];
+  __shared__ TileLds tl;
+  __shared__ int rowpos[64];
+  const int K = a.H, N = a.F, NT = (N + 63) / 64, S = a.G / a.E;
+  const int T = build_expert_tile_table(a.offsets, a.G, a.E, 64, tl) * NT;
+  const Shuffle sm = make_shuffle(a.shuffle, T);
+  const int i = threadIdx.x & 255, g = threadIdx.x >> 8;
+  for (int v = blockIdx.x; v < T; v += gridDim.x) {
+    const TileCoord c = tile_coord(shuffled(sm, v), a.E, NT, 64, 1, 0, tl);
+    const int e = c.g, col0 = c.nt * 64;
+    if (threadIdx.x < 64) rowpos[threadIdx.x] = expert_row(tl, e, a.E, S, c.m0, threadIdx.x);
+    __syncthreads();
+    const float* xr[2];
+    const float* wr[4];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int pos = rowpos[(i >> 3) + 32 * h];
+      xr[h] = pos >= 0 ? (const float*)a.x + (int64_t)pos * K : nullptr;
+    }
+#pragma unroll
+    for (int h = 0; h < 4; ++h) {  // weight rows 32 h ..: gate, up of the first 32 columns, of the second
+      const int f = col0 + (h >> 1) * 32 + (i >> 3);
+      wr[h] = f < N ? (const float*)(h & 1 ? a.w1 : a.w0) + ((int64_t)e * N + f) * K : nullptr;
+    }
+    const int steps = K / kGfK, b = part_begin(steps, g, KG), end = part_begin(steps, g + 1, KG);
+    GfPart<128> pw;
+    GfPart<64> px;
+    auto load = [&](int at) {
+      px.load_k(xr, (b + at) * kGfK, i);
+      pw.load_k(wr, (b + at) * kGfK, i);
+    };
+    Tile tile;
+    tile.run(lds, end - b, (steps + KG - 1) / KG, load, [&](float* l) { px.store_k(l, i); }, [&](float* l) { pw.store_k(l, i); });
+    tile.each(lds, [&](int fj, int q, f32x4_t (&o)[2]) {
+      const int pos = rowpos[Tile::row(fj)], f = col0 + ((i >> 6) & 1) * 32 + 8 * q + 4 * ((i & 63) >> 5);
+      if (pos < 0 || f >= N) return;
+      const int64_t at = (int64_t)pos * N + f;
+      f32x4_t h;
+#pragma unroll
+      for (int u = 0; u < 4; ++u) h[u] = silu_f32(o[0][u]) * o[1][u];
+      gf_store4((float*)a.o0 + at, o[0]);
+      gf_store4((float*)a.o1 + at, o[1]);
+      gf_store4((float*)a.o2 + at, h);
+    });
+    __syncthreads();
+  }
 }
 
-hipError_t launch_grad_rows(const GradGemmArgs& a, bool bf16, hipStream_t s) {
+// ------------------------------------------------------------------ launch ---
+constexpr size_t kGradUnitBytes = 4 * 16 * 4 * 64 * 16;  // of a bf16 unit, the largest
+
+size_t grad_ws_bytes() { return 256 + (size_t)device_cu_count() * (kGradDescInts * 4 + kGradUnitBytes); }
+
+// The arguments with the workspace's parts, or (ws null) without: no tile is split.
+static GradGemmArgs with_split(const GradGemmArgs& a, void* ws) {
+  GradGemmArgs g = a;
+  g.split = {nullptr, nullptr, nullptr};
+  if (ws) {
+    const size_t cus = device_cu_count();
+    g.split.part = (float*)ws;
+    g.split.desc = (int32_t*)((char*)ws + cus * kGradUnitBytes);
+    g.split.hdr = g.split.desc + cus * kGradDescInts;
+  }
+  return g;
+}
+
+// Whether a rows' gradient may split tiles: the number of row tiles depends on
+// the routing, between `lo` and `hi`; the second kernel's launch (about 3 us)
+// is saved where none of a few candidates would split.
+static bool rows_may_split(const SplitCost& c, const GradGemmArgs& a, int rows, int NT, int steps, int grid) {
+  const int64_t hi = a.R / rows + (a.R < a.E ? a.R : a.E), lo = a.all_held ? (a.R + rows - 1) / rows : 0;
+  if (hi - lo > 16) return split_parts(c, 1, steps, grid) > 1;
+  for (int64_t mt = lo; mt <= hi; ++mt)
+    if (split_parts(c, (int)(mt * NT % grid), steps, grid) > 1) return true;
+  return false;
+}
+
+hipError_t launch_grad_rows(const GradGemmArgs& a, bool bf16, void* ws, hipStream_t s) {
   if (a.R == 0) return hipSuccess;
-  const int grid = device_cu_count(), xcd_slots = grid / kXcds > 0 ? grid / kXcds : 1;
+  const int cus = device_cu_count(), xcd_slots = cus / kXcds > 0 ? cus / kXcds : 1;
+  const int N = a.layer == 0 ? a.H : a.F, K = a.layer == 0 ? 2 * a.F : a.H;
   if (bf16) {
+    const bool split = rows_may_split(kSplitBf16, a, kTileRows, (N + 255) / 256, K / kBK, cus);
+    const GradGemmArgs g = with_split(a, split ? ws : nullptr);
+    if (a.layer == 0) {
+      grad_rows_bf16_kernel<kGradRows0><<<cus, kGemmThreads, 0, s>>>(g, xcd_slots);
+      return grad_reduce_launch<kGradRows0, __bf16>(g, s);
+    }
+    grad_rows_bf16_kernel<kGradRows1><<<cus, kGemmThreads, 0, s>>>(g, xcd_slots);
+    return grad_reduce_launch<kGradRows1, __bf16>(g, s);
+  }
+  if (wide_f32(a.R / 128 * ((N + 127) / 128), cus)) {
     if (a.layer == 0)
-      grad_rows_bf16_kernel<kGradRows0><<<grid, kGemmThreads, 0, s>>>(a, xcd_slots);
+      grad_rows_f32_kernel<kGradRows0, 128, 2><<<cus, 512, 0, s>>>(with_split(a, nullptr));
     else
-      grad_rows_bf16_kernel<kGradRows1><<<grid, kGemmThreads, 0, s>>>(a, xcd_slots);
+      grad_rows_f32_kernel<kGradRows1, 128, 2><<<cus, 512, 0, s>>>(with_split(a, nullptr));
     return hipGetLastError();
   }
-  return a.layer == 0 ? grad_rows_launch<0>(a, s) : grad_rows_launch<1>(a, s);
+  const bool split = rows_may_split(kSplitF32, a, 64, (N + 63) / 64, K / kGfK / 4, cus);
+  const GradGemmArgs g = with_split(a, split ? ws : nullptr);
+  if (a.layer == 0) {
+    grad_rows_f32_kernel<kGradRows0, 64, 4><<<cus, 1024, 0, s>>>(g);
+    return grad_reduce_launch<kGradRows0, float>(g, s);
+  }
+  grad_rows_f32_kernel<kGradRows1, 64, 4><<<cus, 1024, 0, s>>>(g);
+  return grad_reduce_launch<kGradRows1, float>(g, s);
 }
 
-template <int LAYER>
-hipError_t grad_weights_launch(const GradGemmArgs& a, hipStream_t s) {
-  grad_weights_f32_kernel<LAYER, 64><<<2 * device_cu_count(), kGfThreads, 0, s>>>(a);
-  return hipGetLastError();
-}
-
-hipError_t launch_grad_weights(const GradGemmArgs& a, bool bf16, hipStream_t s) {
+hipError_t launch_grad_weights(const GradGemmArgs& a, bool bf16, void* ws, hipStream_t s) {
+  const int cus = device_cu_count(), T = bf16 ? 256 : 64;
+  const int64_t N = a.layer == 0 ? a.F : a.H, C = a.layer == 0 ? a.H : a.F, mats = a.layer == 0 ? 2 : 1;
+  const auto tiles = [&](int t) { return a.E * mats * ((N + t - 1) / t) * ((C + t - 1) / t); };
+  // the experts' mean of steps, if all rows are kept: with fewer a split pays less
+  const int64_t step = a.E * (bf16 ? kBK : 4 * kGfK), mean = (a.R + step - 1) / step;
+  const bool split = split_parts(bf16 ? kSplitBf16 : kSplitF32, (int)(tiles(T) % cus), (int)mean, cus) > 1;
+  const GradGemmArgs g = with_split(a, split ? ws : nullptr);
   if (bf16) {
-    grad_weights_bf16_kernel<<<device_cu_count(), kGemmThreads, 0, s>>>(a);
+    grad_weights_bf16_kernel<<<cus, kGemmThreads, 0, s>>>(g);
+    return grad_reduce_launch<kGradWeights, __bf16>(g, s);
+  }
+  if (wide_f32(tiles(128), cus)) {
+    grad_weights_f32_kernel<128, 2><<<cus, 512, 0, s>>>(with_split(a, nullptr));
     return hipGetLastError();
   }
-  return a.layer == 0 ? grad_weights_launch<0>(a, s) : grad_weights_launch<1>(a, s);
+  // fewer steps than the groups can share: one group a tile, four workgroups a CU (8 experts 256 x 7680, a row each:
+  // 34 us with four groups, 23 with one; 8 experts 256 x 512, 64 rows each: 13.5, 9.4)
+  if (mean < 4 && !split) {
+    grad_weights_f32_kernel<64, 1><<<4 * cus, 256, 0, s>>>(g);
+    return hipGetLastError();
+  }
+  grad_weights_f32_kernel<64, 4><<<cus, 1024, 0, s>>>(g);
+  return grad_reduce_launch<kGradWeights, float>(g, s);
+}
+
+hipError_t launch_keep_f32(const GradGemmArgs& a, hipStream_t s) {
+  if (a.R == 0) return hipSuccess;
+  keep_f32_kernel<<<device_cu_count(), 512, 0, s>>>(with_split(a, nullptr));
+  return hipGetLastError();
 }
 
 }  // namespace moe

@@ -109,6 +109,14 @@ hipError_t launch_route_backward(const int32_t* idx, const float* w, const float
 // Gradients of the grouped GEMM.  Rows: layer 1 takes dY through W_down and
 // SwiGLU to the gradients of gate and up; layer 0 those through W_gate and
 // W_up to that of X_perm.  Weights: the products over each expert's rows.
+// Split tiles: few tiles with a long reduction are cut along K into units
+// whose sums a second kernel adds in order (hdr null: no workspace).
+struct GradSplit {
+  int32_t* hdr;   // {tiles, parts}, for the second kernel
+  int32_t* desc;  // per split tile kGradDescInts
+  float* part;    // 256 KiB a unit, at most one unit per CU
+};
+constexpr int kGradDescInts = 8 + 256;
 struct GradGemmArgs {
   int layer;
   const void* d0;  // rows: dY [R,H] (layer 1) or dgate [R,F] (layer 0); weights: the same
@@ -120,15 +128,22 @@ struct GradGemmArgs {
   const void* x;   // weights: Hact [R,F] (layer 1) or X_perm [R,H] (layer 0)
   void* o0;        // rows: dgate [R,F] or dX_perm [R,H]; weights: dW_down [E,H,F] or dW_gate [E,F,H]
   void* o1;        // rows, layer 1: dup [R,F]; weights, layer 0: dW_up [E,F,H]
+  void* o2;        // kept products (launch_keep_f32): Hact; o0, o1: gate, up
   const int32_t* offsets;
   int64_t R;
   int H, F, E, G;  // E: experts held
+  int all_held;    // no pair is dropped
   int out_bf16;    // weights: type of o0, o1
   int accumulate;  // weights: add to what o0, o1 hold (f32)
   uint32_t shuffle;
+  GradSplit split;
 };
-hipError_t launch_grad_rows(const GradGemmArgs& a, bool bf16, hipStream_t s);
-hipError_t launch_grad_weights(const GradGemmArgs& a, bool bf16, hipStream_t s);
+// Workspace of the split tiles' sums.
+size_t grad_ws_bytes();
+hipError_t launch_grad_rows(const GradGemmArgs& a, bool bf16, void* ws, hipStream_t s);
+hipError_t launch_grad_weights(const GradGemmArgs& a, bool bf16, void* ws, hipStream_t s);
+// f32: gate, up and Hact (o0, o1, o2) of x, w0, w1
+hipError_t launch_keep_f32(const GradGemmArgs& a, hipStream_t s);
 
 // Decode layer (at most MOE_DECODE_MAX_TOKENS tokens).
 struct DecodeSplit {

@@ -71,11 +71,11 @@ __device__ inline int build_tile_table(const int32_t* __restrict__ offsets, int 
 // rows of several small segments of the same expert and every weight panel
 // serves full tiles.  Fills seg_start and seg_rows of the G segments,
 // expert_rows[e] and mt_start[e] (prefix of the experts' M-tile counts);
-// returns the number of M-tiles.  All threads of the block (<= 256) call it.
+// returns the number of M-tiles.  All threads of the block call it.
 __device__ inline int build_expert_tile_table(const int32_t* __restrict__ offsets, int G, int EL, int rows,
                                               TileLds& t) {
-  const int nthr = blockDim.x;
-  for (int g = threadIdx.x; g < G; g += nthr) {
+  const int nthr = min((int)blockDim.x, 256);  // those that scan
+  for (int g = threadIdx.x; g < G; g += blockDim.x) {
     t.seg_start[g] = offsets[g];
     t.seg_rows[g] = offsets[g + 1] - offsets[g];
   }
@@ -90,15 +90,16 @@ __device__ inline int build_expert_tile_table(const int32_t* __restrict__ offset
     t.expert_rows[e] = n;
     run += (n + rows - 1) / rows;
   }
-  t.scratch[threadIdx.x] = run;
+  const bool scans = (int)threadIdx.x < nthr;
+  if (scans) t.scratch[threadIdx.x] = run;
   __syncthreads();
   for (int off = 1; off < nthr; off <<= 1) {
-    const int v = (threadIdx.x >= (unsigned)off) ? t.scratch[threadIdx.x - off] : 0;
+    const int v = scans && threadIdx.x >= (unsigned)off ? t.scratch[threadIdx.x - off] : 0;
     __syncthreads();
-    t.scratch[threadIdx.x] += v;
+    if (scans) t.scratch[threadIdx.x] += v;
     __syncthreads();
   }
-  int acc = t.scratch[threadIdx.x] - run;
+  int acc = scans ? t.scratch[threadIdx.x] - run : 0;
   for (int e = e0; e < e0 + per && e < EL; ++e) {
     t.mt_start[e] = acc;
     acc += (t.expert_rows[e] + rows - 1) / rows;

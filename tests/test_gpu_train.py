@@ -236,7 +236,11 @@ EXPERTS = [dict(M=1, H=64, F=64, E=1, k=1), dict(M=1, H=256, F=320, E=8, k=2), d
            dict(M=64, H=192, F=128, E=4, k=2, skip=(0, 3)), dict(M=200, H=320, F=448, E=3, k=1, crowd=1.5),
            dict(M=129, H=64, F=576, E=16, k=4, S=3), dict(M=300, H=448, F=192, E=12, k=3, held=3, base=4, S=2),
            dict(M=700, H=512, F=256, E=2, k=1), dict(M=520, H=256, F=704, E=4, k=2, held=2, base=1, crowd=3.0),
-           dict(M=90, H=128, F=128, E=40, k=2), dict(M=257, H=576, F=320, E=1, k=1)]
+           dict(M=90, H=128, F=128, E=40, k=2), dict(M=257, H=576, F=320, E=1, k=1),
+           # few tiles with long reductions: split along K
+           dict(M=70, H=1088, F=2112, E=2, k=1), dict(M=1500, H=64, F=128, E=1, k=1),
+           dict(M=1400, H=128, F=64, E=3, k=2, S=3, held=2, base=1), dict(M=300, H=1024, F=1024, E=2, k=1, skip=(1,)),
+           dict(M=3000, H=320, F=64, E=2, k=1, crowd=2.5)]
 
 
 def experts(M, H, F, E, k, dtype, S=1, held=0, base=0, crowd=0.0, skip=(), seed=0):
@@ -311,7 +315,10 @@ def test_experts(shape, dtype):
     check_rows(o["up"], u, bu, 2 * H, bf16, (shape, "up"))
     c = torch.full_like(o["c"], 5.0)
     moe.moe_grouped_gemm(prob, 0, d["xp"], d["wg"], d["wu"], d["offsets"], c)
-    assert torch.equal(o["c"], c)
+    if bf16:
+        assert torch.equal(o["c"], c)
+    else:
+        check_rows(o["c"], *ref.hact(d["xp"], d["wg"], d["wu"], d["offsets"]), 2 * H + 8, False, (shape, "hact"))
     g, bg, u, bu = ref.rows1(d["dy"], d["wd"], d["gate"], d["up"], d["offsets"], bf16)
     check_rows(o["dgate"], g, bg, 2 * H + 64, bf16, (shape, "dgate"))
     check_rows(o["dup"], u, bu, 2 * H + 64, bf16, (shape, "dup"))
@@ -541,6 +548,7 @@ def test_debug_validate_refuses_bad_indices():
     dw, dl = torch.zeros(M, k, device=DEV), torch.zeros(M, E, device=DEV)
     z = lambda *s: torch.zeros(s, device=DEV)
     wt, rows, rowsf = z(E, F, H), z(M * k, H), z(M * k, F)
+    ws = torch.empty(moe.moe_workspace_bytes(prob, moe.MOE_OP_GROUPED_GEMM_BACKWARD), dtype=torch.uint8, device=DEV)
     bad_f2s, bad_idx, bad_off = f2s.clone(), idx.clone(), offsets.clone()
     bad_f2s[3], bad_idx[5, 1], bad_off[2] = M * k, E, -1
     calls = [(lambda i: moe.moe_route_backward(prob, i, w, dw, dl), idx, bad_idx),
@@ -548,8 +556,8 @@ def test_debug_validate_refuses_bad_indices():
              (lambda i: moe.moe_combine_backward(prob, z(M, H), y, w, i, None, rows, dw), f2s, bad_f2s),
              (lambda i: moe.moe_dispatch_backward(prob, y, i, None, z(M, H)), f2s, bad_f2s),
              (lambda i: moe.moe_grouped_gemm_aux(prob, y, wt, wt, i, rowsf, z(M * k, F), z(M * k, F)), offsets, bad_off),
-             (lambda i: moe.moe_grouped_gemm_backward(prob, 0, rowsf, rowsf, wt, wt, None, None, i, rows, None), offsets, bad_off),
-             (lambda i: moe.moe_grouped_gemm_backward_weights(prob, 0, rowsf, rowsf, y, i, z(E, F, H), z(E, F, H)), offsets, bad_off)]
+             (lambda i: moe.moe_grouped_gemm_backward(prob, 0, rowsf, rowsf, wt, wt, None, None, i, rows, None, ws), offsets, bad_off),
+             (lambda i: moe.moe_grouped_gemm_backward_weights(prob, 0, rowsf, rowsf, y, i, z(E, F, H), z(E, F, H), False, ws), offsets, bad_off)]
     os.environ["MOE_DEBUG_VALIDATE"] = "1"
     try:
         for n, (call, good, bad) in enumerate(calls):

@@ -104,6 +104,22 @@ def test_layers_and_their_operands(lib, name):
         assert call(lib, name, **{a: at(17)}) == INV, a
 
 
+@pytest.mark.parametrize("name", ["rows1", "rows0", "weights1", "weights0"])
+def test_workspaces(lib, name):
+    op = moe.MOE_OP_GROUPED_GEMM_BACKWARD
+    for dtype in ("f32", "bf16"):
+        p = moe.problem(M, H, F, E, k, dtype=dtype)
+        need = moe.moe_workspace_bytes(p, op)
+        assert need > 0
+        assert call(lib, name, problem=p, ws=None) == moe.MOE_ERR_WORKSPACE_TOO_SMALL
+        assert call(lib, name, problem=p, ws_bytes=need - 1) == moe.MOE_ERR_WORKSPACE_TOO_SMALL
+        assert call(lib, name, problem=p, ws=P(at(15).value + 128)) == INV
+        for a in tensors(name):  # no buffer of the call lies in it
+            assert call(lib, name, problem=p, ws=at(CALLS[name].index(a))) == INV, a
+    assert moe.moe_workspace_bytes(moe.problem(0, H, F, E, k), op) == 0
+    assert moe.moe_workspace_bytes(moe.problem(M, H, F, E, k, dtype="bf16_mxfp8"), op) == 0
+
+
 def test_weights_types(lib):
     for name in ("weights1", "weights0"):
         for bad in (-1, 2, 7):

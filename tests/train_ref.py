@@ -152,6 +152,15 @@ def products(xp, wg, wu, offsets, bf16):
     return o
 
 
+def hact(xp, wg, wu, offsets):
+    """silu(gate) up of the f32 products, and its bound: |silu'| <= 1.1; the exponential, the division and the products
+    8 u."""
+    g, bg, u, bu = products(xp, wg, wu, offsets, False)
+    silu = g * torch.sigmoid(g)
+    h = silu * u
+    return h, 1.1 * bg * (u.abs() + bu) + silu.abs() * bu + 8 * U * h.abs()
+
+
 def rows1(dy, wd, gate, up, offsets, bf16):
     """dgate, its bound, dup, its bound."""
     o = _empty(gate.shape[0], gate.shape[1], dy.device, 2)
