@@ -315,6 +315,9 @@ AdapterArgs adapter_args(const moe_adapter_problem_t* q, int32_t out_dtype) {
 }
 
 // ------------------------------------------------------------- training ---
+// Pairs that an even routing keeps.
+int64_t kept_rows(const moe_problem_t* p) { return p->num_tokens * p->topk * held(p) / p->num_experts; }
+
 // A buffer of a call, for the checks: bytes, and whether the call writes it.
 struct Span {
   const void* p;
@@ -830,8 +833,10 @@ moe_status_t moe_combine_dropout(const moe_problem_t* p, const float* y, const f
     st = check_range(flat_to_sorted, R, -1, (int32_t)R, (hipStream_t)stream);
     if (st != MOE_OK) return st;
   }
-  return hip_status(launch_combine(y, topk_w, flat_to_sorted, p->num_tokens, p->hidden, p->topk, ep,
-                                   (hipStream_t)stream, d.rng ? &d : nullptr));
+  if (!d.rng)
+    return hip_status(launch_combine(y, topk_w, flat_to_sorted, p->num_tokens, p->hidden, p->topk, ep, (hipStream_t)stream));
+  return hip_status(launch_combine_dropout(y, topk_w, flat_to_sorted, p->num_tokens, kept_rows(p), p->hidden, p->topk, ep,
+                                           d, (hipStream_t)stream));
 }
 
 moe_status_t moe_combine_backward(const moe_problem_t* p, const void* dout, int32_t dout_dtype, const float* y,
@@ -871,6 +876,7 @@ moe_status_t moe_combine_backward(const moe_problem_t* p, const void* dout, int3
   a.dy_bf16 = p->dtype != MOE_DTYPE_F32;
   a.dtopk_w = dtopk_w;
   a.M = p->num_tokens;
+  a.rows = kept_rows(p);
   a.H = p->hidden;
   a.k = p->topk;
   return hip_status(launch_combine_backward(a, (hipStream_t)stream));
@@ -893,7 +899,7 @@ moe_status_t moe_dispatch_backward(const moe_problem_t* p, const void* dx_perm, 
     if (st != MOE_OK) return st;
   }
   return hip_status(launch_dispatch_backward(dx_perm, p->dtype != MOE_DTYPE_F32, flat_to_sorted, p->num_tokens,
-                                             p->hidden, p->topk, ep, (hipStream_t)stream));
+                                             kept_rows(p), p->hidden, p->topk, ep, (hipStream_t)stream));
 }
 
 moe_status_t moe_route_backward(const moe_problem_t* p, const int32_t* topk_idx, const float* topk_w,

@@ -8,23 +8,20 @@
 // in f32, from zero, j increasing, one fused multiply-add per term, over
 // the slots whose pair is held here (a row index outside [0, M k) counts as
 // not held); then the epilogue (optional residual add, f32 or bf16 output).
-// With DROP, acc goes through the dropout before the residual (moe_combine_dropout).
 // A block walks whole token rows, 4 columns per lane per step, so every
 // Y row read and every out row write is contiguous.
 #include "common.hpp"
 #include "launch.hpp"
-#include "philox.hpp"
 
 namespace moe {
 
 constexpr int kCombineThreads = 256;
 constexpr int kCombineUnroll = 4;
 
-template <bool DROP>
 __global__ __launch_bounds__(kCombineThreads) void combine_kernel(const float* __restrict__ y,
                                                                   const float* __restrict__ topk_w,
                                                                   const int32_t* __restrict__ f2s, int64_t M, int H,
-                                                                  int k, OutEpilogue ep, Dropout drop) {
+                                                                  int k, OutEpilogue ep) {
   __shared__ int rows[16];
   __shared__ float w[16];
   const int groups = H / 4;
@@ -75,9 +72,7 @@ __global__ __launch_bounds__(kCombineThreads) void combine_kernel(const float* _
 #pragma unroll
       for (int u = 0; u < kCombineUnroll; ++u) {
         const int q = q0 + u * kCombineThreads;
-        if (q >= groups) continue;
-        if constexpr (DROP) acc[u] = dropped(kept(Philox(drop.rng), drop, (uint64_t)t * groups + q), drop.scale, acc[u]);
-        store_out(ep, t * H + (int64_t)q * 4, acc[u]);
+        if (q < groups) store_out(ep, t * H + (int64_t)q * 4, acc[u]);
       }
     }
     __syncthreads();
@@ -85,14 +80,10 @@ __global__ __launch_bounds__(kCombineThreads) void combine_kernel(const float* _
 }
 
 hipError_t launch_combine(const float* y, const float* topk_w, const int32_t* flat_to_sorted, int64_t M, int H,
-                          int k, const OutEpilogue& ep, hipStream_t s, const Dropout* drop) {
+                          int k, const OutEpilogue& ep, hipStream_t s) {
   if (M == 0) return hipSuccess;
   const int64_t grid = M < 16384 ? M : 16384;
-  if (drop)
-    combine_kernel<true><<<(unsigned)grid, kCombineThreads, 0, s>>>(y, topk_w, flat_to_sorted, M, H, k, ep, *drop);
-  else
-    combine_kernel<false><<<(unsigned)grid, kCombineThreads, 0, s>>>(y, topk_w, flat_to_sorted, M, H, k, ep,
-                                                                      Dropout{});
+  combine_kernel<<<(unsigned)grid, kCombineThreads, 0, s>>>(y, topk_w, flat_to_sorted, M, H, k, ep);
   return hipGetLastError();
 }
 

@@ -11,6 +11,8 @@
 //             dlogits[t, idx_j] = w_j (dw_j - sum_i w_i dw_i), the rest 0
 // All are bound by HBM traffic.  Nothing is added by atomics: a token's rows
 // are read (or written) by the lanes that own the token.
+#include <type_traits>
+
 #include "common.hpp"
 #include "launch.hpp"
 #include "philox.hpp"
@@ -21,14 +23,33 @@ constexpr int kGradThreads = 256;
 
 __device__ __forceinline__ bool pair_held(int32_t row, int64_t R) { return (uint64_t)(int64_t)row < (uint64_t)R; }
 
-__device__ __forceinline__ float4 load4(const void* p, int bf16, int64_t i) {
-  if (bf16) {
-    const bf16x4_t b = *reinterpret_cast<const bf16x4_t*>(reinterpret_cast<const __bf16*>(p) + i);
-    return make_float4((float)b[0], (float)b[1], (float)b[2], (float)b[3]);
-  }
-  return *reinterpret_cast<const float4*>(reinterpret_cast<const float*>(p) + i);
+// Outputs are stored as used once ("nt"), so that they do not wait for the L2 to
+// make room.  f32 rows of a large call are loaded so too (ONCE): from about 96
+// MiB on they have left the last-level cache (256 MB) since they were written,
+// and loading them there again only pushes out the rest.  Measured with inputs
+// that change from call to call, plain loads and once, tokens of 4096, top 2:
+// combine with dropout of 2048 tokens (64 MiB) 17.5, 19.5 us; 4096: 41, 35;
+// 8192: 77, 65; its gradient 22, 27; 51, 43; 94, 78.  bf16 rows are loaded
+// plainly (4096 tokens of 2048, top 4: 16.4 us, once 29).
+template <bool ONCE>
+__device__ __forceinline__ float4 load4(const float* p) {
+  f32x4_t v;
+  if constexpr (ONCE)
+    v = __builtin_nontemporal_load(reinterpret_cast<const f32x4_t*>(p));
+  else
+    v = *reinterpret_cast<const f32x4_t*>(p);
+  return make_float4(v[0], v[1], v[2], v[3]);
 }
-
+template <bool>
+__device__ __forceinline__ float4 load4(const __bf16* p) {
+  const bf16x4_t b = *reinterpret_cast<const bf16x4_t*>(p);
+  return make_float4((float)b[0], (float)b[1], (float)b[2], (float)b[3]);
+}
+template <bool ONCE>
+__device__ __forceinline__ float4 load4(const void* p, int bf16, int64_t i) {
+  return bf16 ? load4<ONCE>(reinterpret_cast<const __bf16*>(p) + i) : load4<ONCE>(reinterpret_cast<const float*>(p) + i);
+}
+constexpr int64_t kOnceBytes = 96ll << 20;
 __device__ __forceinline__ void store4(void* p, int bf16, int64_t i, float4 v) {
   if (bf16) {
     bf16x4_t o;
@@ -36,23 +57,129 @@ __device__ __forceinline__ void store4(void* p, int bf16, int64_t i, float4 v) {
     o[1] = (__bf16)v.y;
     o[2] = (__bf16)v.z;
     o[3] = (__bf16)v.w;
-    *reinterpret_cast<bf16x4_t*>(reinterpret_cast<__bf16*>(p) + i) = o;
+    __builtin_nontemporal_store(o, reinterpret_cast<bf16x4_t*>(reinterpret_cast<__bf16*>(p) + i));
   } else {
-    *reinterpret_cast<float4*>(reinterpret_cast<float*>(p) + i) = v;
+    const f32x4_t o{v.x, v.y, v.z, v.w};
+    __builtin_nontemporal_store(o, reinterpret_cast<f32x4_t*>(reinterpret_cast<float*>(p) + i));
+  }
+}
+// The values of out from element i on: acc and the residual's, one f32 addition, then the cast (as store_out).
+__device__ __forceinline__ void finish4(const OutEpilogue& ep, int64_t i, float4 acc) {
+  if (ep.residual) {
+    const float4 r = load4<false>(ep.residual, ep.res_bf16, i);
+    acc.x += r.x;
+    acc.y += r.y;
+    acc.z += r.z;
+    acc.w += r.w;
+  }
+  store4(ep.out, ep.out_bf16, i, acc);
+}
+
+// All kernels here: TPT threads own a token (256 / TPT tokens a block) and walk
+// its columns, 4 a thread and U such groups at a time, all of whose loads are
+// issued before any is used.  Threads per token by the row's length, so that
+// each has one to four groups where it can.
+// f(TPT, ONCE); f32_bytes: the f32 rows read.
+template <typename F>
+hipError_t by_size(int H, int64_t f32_bytes, F&& f) {
+  if (H <= 128) return f(std::integral_constant<int, 16>{}, std::false_type{});
+  if (H <= 512) return f(std::integral_constant<int, 64>{}, std::false_type{});
+  if (f32_bytes < kOnceBytes) return f(std::integral_constant<int, 256>{}, std::false_type{});
+  return f(std::integral_constant<int, 256>{}, std::true_type{});
+}
+inline unsigned token_blocks(int64_t M, int tpt) {
+  const int64_t n = (M + kGradThreads / tpt - 1) / (kGradThreads / tpt);
+  return (unsigned)(n < 16384 ? n : 16384);
+}
+
+// ---------------------------------------------------------- rows to tokens ---
+// Forward combine with dropout (SRC f32, weights w, DROP) and the dispatch's
+// gradient (SRC the problem's type): the sum over the token's held pairs of
+// their rows (times w), f32 from zero in slot order, two slots' loads together.
+template <int TPT, bool ONCE, typename SRC, bool DROP>
+__global__ __launch_bounds__(kGradThreads) void rows_to_tokens_kernel(const SRC* __restrict__ src,
+                                                                      const float* __restrict__ w,
+                                                                      const int32_t* __restrict__ f2s, int64_t M, int H,
+                                                                      int k, OutEpilogue ep, Dropout drop) {
+  constexpr int TOK = kGradThreads / TPT, U = 2;
+  const int q0 = threadIdx.x % TPT, groups = H / 4;
+  for (int64_t t = (int64_t)blockIdx.x * TOK + threadIdx.x / TPT; t < M; t += (int64_t)gridDim.x * TOK) {
+    for (int q = q0; q < groups; q += U * TPT) {
+      float4 acc[U];
+#pragma unroll
+      for (int u = 0; u < U; ++u) acc[u] = make_float4(0.f, 0.f, 0.f, 0.f);
+      for (int j0 = 0; j0 < k; j0 += 2) {
+        float4 v[2][U];
+        bool held[2];
+        float wj[2];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const int64_t f = t * k + j0 + h;
+          const int32_t row = j0 + h < k ? f2s[f] : -1;
+          held[h] = pair_held(row, M * k);
+          wj[h] = DROP && held[h] ? w[f] : 1.f;
+          const SRC* p = src + (int64_t)(held[h] ? row : 0) * H;
+#pragma unroll
+          for (int u = 0; u < U; ++u)
+            v[h][u] = held[h] && q + u * TPT < groups ? load4<ONCE>(p + (int64_t)(q + u * TPT) * 4) : make_float4(0.f, 0.f, 0.f, 0.f);
+        }
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          if (!held[h]) continue;
+#pragma unroll
+          for (int u = 0; u < U; ++u) {
+            acc[u].x = fmaf(wj[h], v[h][u].x, acc[u].x);
+            acc[u].y = fmaf(wj[h], v[h][u].y, acc[u].y);
+            acc[u].z = fmaf(wj[h], v[h][u].z, acc[u].z);
+            acc[u].w = fmaf(wj[h], v[h][u].w, acc[u].w);
+          }
+        }
+      }
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int qu = q + u * TPT;
+        if (qu >= groups) continue;
+        if constexpr (DROP) acc[u] = dropped(kept(Philox(drop.rng), drop, (uint64_t)t * groups + qu), drop.scale, acc[u]);
+        finish4(ep, t * H + (int64_t)qu * 4, acc[u]);
+      }
+    }
   }
 }
 
-// ---------------------------------------------------------------- combine ---
-// TPT threads own a token (256 / TPT tokens a block) and walk its columns, 4
-// a thread and step; g is formed once for all k pairs, the k sums of dw stay
-// in registers (KMAX >= k of them) and are added across the token's threads
-// in a fixed order.
-template <int TPT, int KMAX, bool DROP>
+hipError_t launch_combine_dropout(const float* y, const float* topk_w, const int32_t* f2s, int64_t M, int64_t rows, int H,
+                                  int k, const OutEpilogue& ep, const Dropout& drop, hipStream_t s) {
+  if (M == 0) return hipSuccess;
+  return by_size(H, rows * H * 4, [&](auto tpt, auto once) {
+    rows_to_tokens_kernel<tpt.value, once.value, float, true>
+        <<<token_blocks(M, tpt.value), kGradThreads, 0, s>>>(y, topk_w, f2s, M, H, k, ep, drop);
+    return hipGetLastError();
+  });
+}
+
+hipError_t launch_dispatch_backward(const void* dxp, bool bf16, const int32_t* f2s, int64_t M, int64_t rows, int H,
+                                    int k, const OutEpilogue& ep, hipStream_t s) {
+  if (M == 0) return hipSuccess;
+  return by_size(H, bf16 ? 0 : rows * H * 4, [&](auto tpt, auto once) {
+    const unsigned grid = token_blocks(M, tpt.value);
+    if (bf16)
+      rows_to_tokens_kernel<tpt.value, false, __bf16, false>
+          <<<grid, kGradThreads, 0, s>>>((const __bf16*)dxp, nullptr, f2s, M, H, k, ep, Dropout{});
+    else
+      rows_to_tokens_kernel<tpt.value, once.value, float, false>
+          <<<grid, kGradThreads, 0, s>>>((const float*)dxp, nullptr, f2s, M, H, k, ep, Dropout{});
+    return hipGetLastError();
+  });
+}
+
+// ------------------------------------------------------- combine's gradient ---
+// g is formed once for all k pairs; the k sums of dw stay in registers (KMAX >=
+// k of them) and are added across the token's threads in a fixed order.
+template <int TPT, bool ONCE, int KMAX, bool DROP>
 __global__ __launch_bounds__(kGradThreads) void combine_backward_kernel(CombineBackwardArgs a) {
-  constexpr int TOK = kGradThreads / TPT;  // tokens per block
+  constexpr int TOK = kGradThreads / TPT;
+  constexpr int U = 2, JG = KMAX < 4 ? KMAX : 4;  // pairs whose loads are issued together
   __shared__ float part[kGradThreads / kWave][KMAX];
-  const int q0 = threadIdx.x % TPT;
-  const int groups = a.H / 4;
+  const int q0 = threadIdx.x % TPT, groups = a.H / 4;
   const int64_t R = a.M * a.k;
   for (int64_t t0 = (int64_t)blockIdx.x * TOK; t0 < a.M; t0 += (int64_t)gridDim.x * TOK) {
     const int64_t t = t0 + threadIdx.x / TPT;
@@ -65,28 +192,51 @@ __global__ __launch_bounds__(kGradThreads) void combine_backward_kernel(CombineB
       row[j] = in ? a.f2s[t * a.k + j] : -1;
       w[j] = in ? a.topk_w[t * a.k + j] : 0.f;
       if (!pair_held(row[j], R)) row[j] = -1;
+      if constexpr (TPT >= kWave) row[j] = __builtin_amdgcn_readfirstlane(row[j]);  // one token a wave
       s[j] = 0.f;
     }
-    for (int q = q0; valid && q < groups; q += TPT) {
-      float4 g = load4(a.dout, a.dout_bf16, t * a.H + (int64_t)q * 4);
-      float4 y[KMAX];
+    for (int q = q0; valid && q < groups; q += U * TPT) {
+      float4 g[U];
 #pragma unroll
-      for (int j = 0; j < KMAX; ++j)
-        y[j] = row[j] >= 0 ? *reinterpret_cast<const float4*>(a.y + (int64_t)row[j] * a.H + (int64_t)q * 4)
-                           : make_float4(0.f, 0.f, 0.f, 0.f);
-      if constexpr (DROP) {
-        // what is dropped adds nothing to dw, whatever y holds there
-        const Kept keep = kept(Philox(a.drop.rng), a.drop, (uint64_t)t * groups + q);
-        g = dropped(keep, a.drop.scale, g);
+      for (int u = 0; u < U; ++u)
+        g[u] = q + u * TPT < groups ? load4<false>(a.dout, a.dout_bf16, t * a.H + (int64_t)(q + u * TPT) * 4)
+                                    : make_float4(0.f, 0.f, 0.f, 0.f);
+      Kept keep[U];
 #pragma unroll
-        for (int j = 0; j < KMAX; ++j) y[j] = dropped(keep, 1.f, y[j]);
-      }
+      for (int j0 = 0; j0 < KMAX; j0 += JG) {
+        float4 y[JG][U];
 #pragma unroll
-      for (int j = 0; j < KMAX; ++j) {
-        if (row[j] < 0) continue;
-        s[j] = fmaf(g.x, y[j].x, fmaf(g.y, y[j].y, fmaf(g.z, y[j].z, fmaf(g.w, y[j].w, s[j]))));
-        store4(a.dy, a.dy_bf16, (int64_t)row[j] * a.H + (int64_t)q * 4,
-               make_float4(w[j] * g.x, w[j] * g.y, w[j] * g.z, w[j] * g.w));
+        for (int h = 0; h < JG; ++h) {
+          if (row[j0 + h] < 0) continue;
+#pragma unroll
+          for (int u = 0; u < U; ++u)
+            y[h][u] = q + u * TPT < groups ? load4<ONCE>(a.y + (int64_t)row[j0 + h] * a.H + (int64_t)(q + u * TPT) * 4)
+                                           : make_float4(0.f, 0.f, 0.f, 0.f);
+        }
+        if constexpr (DROP) {
+          if (j0 == 0) {  // behind the first loads
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+              keep[u] = kept(Philox(a.drop.rng), a.drop, (uint64_t)t * groups + q + u * TPT);
+              g[u] = dropped(keep[u], a.drop.scale, g[u]);
+            }
+          }
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          const int qu = q + u * TPT;
+          if (qu >= groups) continue;
+#pragma unroll
+          for (int h = 0; h < JG; ++h) {
+            const int j = j0 + h;
+            if (row[j] < 0) continue;
+            // what is dropped adds nothing to dw, whatever y holds there
+            const float4 v = DROP ? dropped(keep[u], 1.f, y[h][u]) : y[h][u];
+            s[j] = fmaf(g[u].x, v.x, fmaf(g[u].y, v.y, fmaf(g[u].z, v.z, fmaf(g[u].w, v.w, s[j]))));
+            store4(a.dy, a.dy_bf16, (int64_t)row[j] * a.H + (int64_t)qu * 4,
+                   make_float4(w[j] * g[u].x, w[j] * g[u].y, w[j] * g[u].z, w[j] * g[u].w));
+          }
+        }
       }
     }
     // across the token's lanes, then (TPT > a wave) across its waves
@@ -116,23 +266,16 @@ __global__ __launch_bounds__(kGradThreads) void combine_backward_kernel(CombineB
   }
 }
 
-template <int TPT, int KMAX>
-hipError_t combine_backward_launch(const CombineBackwardArgs& a, hipStream_t s) {
-  const int64_t blocks = (a.M + kGradThreads / TPT - 1) / (kGradThreads / TPT);
-  const unsigned grid = (unsigned)(blocks < 16384 ? blocks : 16384);
-  if (a.drop.rng)
-    combine_backward_kernel<TPT, KMAX, true><<<grid, kGradThreads, 0, s>>>(a);
-  else
-    combine_backward_kernel<TPT, KMAX, false><<<grid, kGradThreads, 0, s>>>(a);
-  return hipGetLastError();
-}
-
 template <int KMAX>
 hipError_t combine_backward_k(const CombineBackwardArgs& a, hipStream_t s) {
-  // threads per token: no more than the 4-column groups of a row
-  if (a.H <= 128) return combine_backward_launch<16, KMAX>(a, s);
-  if (a.H <= 512) return combine_backward_launch<64, KMAX>(a, s);
-  return combine_backward_launch<256, KMAX>(a, s);
+  return by_size(a.H, a.rows * a.H * 4, [&](auto tpt, auto once) {
+    const unsigned grid = token_blocks(a.M, tpt.value);
+    if (a.drop.rng)
+      combine_backward_kernel<tpt.value, once.value, KMAX, true><<<grid, kGradThreads, 0, s>>>(a);
+    else
+      combine_backward_kernel<tpt.value, once.value, KMAX, false><<<grid, kGradThreads, 0, s>>>(a);
+    return hipGetLastError();
+  });
 }
 
 hipError_t launch_combine_backward(const CombineBackwardArgs& a, hipStream_t s) {
@@ -144,56 +287,12 @@ hipError_t launch_combine_backward(const CombineBackwardArgs& a, hipStream_t s) 
   return combine_backward_k<16>(a, s);
 }
 
-// --------------------------------------------------------------- dispatch ---
-// dx[t] = sum over the token's held pairs of their rows, f32 from zero in slot
-// order, then the output epilogue.
-template <int TPT>
-__global__ __launch_bounds__(kGradThreads) void dispatch_backward_kernel(const void* __restrict__ dxp, int bf16,
-                                                                         const int32_t* __restrict__ f2s, int64_t M,
-                                                                         int H, int k, OutEpilogue ep) {
-  constexpr int TOK = kGradThreads / TPT;
-  const int q0 = threadIdx.x % TPT;
-  const int groups = H / 4;
-  for (int64_t t = (int64_t)blockIdx.x * TOK + threadIdx.x / TPT; t < M; t += (int64_t)gridDim.x * TOK) {
-    for (int q = q0; q < groups; q += TPT) {
-      float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-      for (int j = 0; j < k; ++j) {
-        const int32_t row = f2s[t * k + j];
-        if (!pair_held(row, M * k)) continue;
-        const float4 v = load4(dxp, bf16, (int64_t)row * H + (int64_t)q * 4);
-        acc.x += v.x;
-        acc.y += v.y;
-        acc.z += v.z;
-        acc.w += v.w;
-      }
-      store_out(ep, t * H + (int64_t)q * 4, acc);
-    }
-  }
-}
-
-template <int TPT>
-hipError_t dispatch_backward_launch(const void* dxp, int bf16, const int32_t* f2s, int64_t M, int H, int k,
-                                    const OutEpilogue& ep, hipStream_t s) {
-  const int64_t blocks = (M + kGradThreads / TPT - 1) / (kGradThreads / TPT);
-  dispatch_backward_kernel<TPT><<<(unsigned)(blocks < 16384 ? blocks : 16384), kGradThreads, 0, s>>>(dxp, bf16, f2s, M,
-                                                                                                      H, k, ep);
-  return hipGetLastError();
-}
-
-hipError_t launch_dispatch_backward(const void* dxp, bool bf16, const int32_t* f2s, int64_t M, int H, int k,
-                                    const OutEpilogue& ep, hipStream_t s) {
-  if (M == 0) return hipSuccess;
-  if (H <= 128) return dispatch_backward_launch<16>(dxp, bf16, f2s, M, H, k, ep, s);
-  if (H <= 512) return dispatch_backward_launch<64>(dxp, bf16, f2s, M, H, k, ep, s);
-  return dispatch_backward_launch<256>(dxp, bf16, f2s, M, H, k, ep, s);
-}
-
 // ----------------------------------------------------------------- router ---
 // A block builds the rows of `tokens` tokens in LDS (zeros, then the k values
 // of each) and stores them as one contiguous range, 16 bytes a lane.  A thread
 // per pair adds the pairs of its token that name the same expert in slot order
 // (moe_route never repeats one), so equal ones all write the same sum.
-constexpr int kRouteGradFloats = 8192;  // row values a block holds: 32 KiB
+constexpr int kRouteGradFloats = 2048;  // row values a block holds
 constexpr int kRouteGradPairs = 1024;
 
 __global__ __launch_bounds__(kGradThreads) void route_backward_kernel(const int32_t* __restrict__ idx,
@@ -235,7 +334,7 @@ hipError_t launch_route_backward(const int32_t* idx, const float* w, const float
   if (M == 0) return hipSuccess;
   // a multiple of 4 tokens, so that every block's range starts 16-byte aligned
   int tokens = kRouteGradFloats / E < kRouteGradPairs / k ? kRouteGradFloats / E : kRouteGradPairs / k;
-  tokens = tokens < 64 ? tokens / 4 * 4 : 64;  // E <= 512: at least 16
+  tokens = tokens < 64 ? tokens / 4 * 4 : 64;  // E <= 512: at least 4
   const int64_t blocks = (M + tokens - 1) / tokens;
   route_backward_kernel<<<(unsigned)blocks, kGradThreads, 0, s>>>(idx, w, dw, M, E, k, tokens, dlogits);
   return hipGetLastError();

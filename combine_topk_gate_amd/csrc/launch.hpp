@@ -82,9 +82,12 @@ hipError_t launch_mx_quantize(const void* src, int src_bf16, int64_t rows, int c
 // and cols multiples of 64; bf16 (else f32) elements.
 hipError_t launch_transpose(const void* src, void* dst, int64_t batch, int rows, int cols, bool bf16, hipStream_t s);
 
-// drop (null: none): the dropout between the sum and the epilogue
 hipError_t launch_combine(const float* y, const float* topk_w, const int32_t* flat_to_sorted, int64_t M, int H,
-                          int k, const OutEpilogue& ep, hipStream_t s, const Dropout* drop = nullptr);
+                          int k, const OutEpilogue& ep, hipStream_t s);
+// ... with a dropout between the sum and the epilogue
+// (rows here and below: the pairs that are probably kept, for the choice of a variant)
+hipError_t launch_combine_dropout(const float* y, const float* topk_w, const int32_t* f2s, int64_t M, int64_t rows, int H,
+                                  int k, const OutEpilogue& ep, const Dropout& drop, hipStream_t s);
 
 // Gradients of the combine, the dispatch and the router.
 struct CombineBackwardArgs {
@@ -97,12 +100,12 @@ struct CombineBackwardArgs {
   void* dy;          // [R,H] f32 or bf16
   int dy_bf16;
   float* dtopk_w;
-  int64_t M;
+  int64_t M, rows;
   int H, k;
 };
 hipError_t launch_combine_backward(const CombineBackwardArgs& a, hipStream_t s);
-hipError_t launch_dispatch_backward(const void* dxp, bool bf16, const int32_t* f2s, int64_t M, int H, int k,
-                                    const OutEpilogue& ep, hipStream_t s);
+hipError_t launch_dispatch_backward(const void* dxp, bool bf16, const int32_t* f2s, int64_t M, int64_t rows, int H,
+                                    int k, const OutEpilogue& ep, hipStream_t s);
 hipError_t launch_route_backward(const int32_t* idx, const float* w, const float* dw, int64_t M, int E, int k,
                                  float* dlogits, hipStream_t s);
 
