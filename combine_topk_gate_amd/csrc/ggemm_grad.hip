@@ -559,6 +559,88 @@ __global__ __launch_bounds__(512) void keep_f32_kernel(GradGemmArgs a) {
   }
 }
 
+// ... of few tiles: 32 rows x 32 columns of both, and the block's 8 waves take
+// an eighth of the K steps each, every operand loaded straight into the matrix
+// instruction's layout (lane: row lane % 32, 4 consecutive k of 8), a step ahead,
+// so that there is no barrier before the waves' sums are added (in order) in LDS.
+// Measured (the tiles above, these): 21 rows, one expert of 2112 x 448: 98, 34
+// us; 482 rows, 2304 x 320: 112, 40; 500 rows, 8 experts 2048 x 640: 101, 72.
+constexpr int kFewWaves = 8;
+__global__ __launch_bounds__(64 * kFewWaves) void keep_f32_few_kernel(GradGemmArgs a) {
+  __shared__ __attribute__((aligned(16))) f32x4_t sums[kFewWaves][2][4][64];
+  __shared__ TileLds tl;
+  const int K = a.H, N = a.F, NT = (N + 31) / 32, S = a.G / a.E;
+  const int T = build_expert_tile_table(a.offsets, a.G, a.E, 32, tl) * NT;
+  const Shuffle sm = make_shuffle(a.shuffle, T);
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, lrow = lane & 31, lk = lane >> 5;
+  for (int v = blockIdx.x; v < T; v += gridDim.x) {
+    const TileCoord c = tile_coord(shuffled(sm, v), a.E, NT, 32, 1, 0, tl);
+    const int e = c.g, f = c.nt * 32 + lrow, pos = expert_row(tl, e, a.E, S, c.m0, lrow);
+    // a row or column that the tile lacks: the first one's values, whose products are not stored
+    const int64_t wrow = ((int64_t)e * N + (f < N ? f : c.nt * 32)) * K + 4 * lk;
+    const float* src[3] = {(const float*)a.x + (int64_t)(pos >= 0 ? pos : expert_row(tl, e, a.E, S, c.m0, 0)) * K + 4 * lk,
+                           (const float*)a.w0 + wrow, (const float*)a.w1 + wrow};
+    const int steps = K / kGfK, b = part_begin(steps, wave, kFewWaves), end = part_begin(steps, wave + 1, kFewWaves);
+    f32x4_t now[3][4], next[3][4];
+    auto load = [&](f32x4_t (&o)[3][4], int s) {
+#pragma unroll
+      for (int u = 0; u < 4; ++u)
+#pragma unroll
+        for (int m = 0; m < 3; ++m) o[m][u] = *reinterpret_cast<const f32x4_t*>(src[m] + s * kGfK + 8 * u);
+    };
+    f32x16_t acc[2], sum[2];
+#pragma unroll
+    for (int m = 0; m < 2; ++m)
+#pragma unroll
+      for (int h = 0; h < 16; ++h) acc[m][h] = sum[m][h] = 0.f;
+    if (b < end) load(now, b);
+    for (int s = b; s < end; ++s) {
+      load(next, s + 1 < end ? s + 1 : s);
+#pragma unroll
+      for (int u = 0; u < 4; ++u)
+#pragma unroll
+        for (int h = 0; h < 4; ++h)
+#pragma unroll
+          for (int m = 0; m < 2; ++m)
+            acc[m] = __builtin_amdgcn_mfma_f32_32x32x2f32(now[1 + m][u][h], now[0][u][h], acc[m], 0, 0, 0);
+      if ((s - b) % kGfFlush == kGfFlush - 1 || s + 1 == end) {
+#pragma unroll
+        for (int m = 0; m < 2; ++m) {
+          sum[m] += acc[m];
+#pragma unroll
+          for (int h = 0; h < 16; ++h) acc[m][h] = 0.f;
+        }
+      }
+#pragma unroll
+      for (int m = 0; m < 3; ++m)
+#pragma unroll
+        for (int u = 0; u < 4; ++u) now[m][u] = next[m][u];
+    }
+    __syncthreads();  // the sums of the tile before are read
+#pragma unroll
+    for (int m = 0; m < 2; ++m)
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+        sums[wave][m][q][lane] = f32x4_t{sum[m][4 * q], sum[m][4 * q + 1], sum[m][4 * q + 2], sum[m][4 * q + 3]};
+    __syncthreads();
+    const int q = wave, n = c.nt * 32 + 8 * q + 4 * lk;
+    if (q < 4 && pos >= 0 && n < N) {
+      f32x4_t o[2] = {};
+#pragma unroll
+      for (int m = 0; m < 2; ++m)
+#pragma unroll
+        for (int w = 0; w < kFewWaves; ++w) o[m] += sums[w][m][q][lane];
+      const int64_t at = (int64_t)pos * N + n;
+      f32x4_t h;
+#pragma unroll
+      for (int u = 0; u < 4; ++u) h[u] = silu_f32(o[0][u]) * o[1][u];
+      gf_store4((float*)a.o0 + at, o[0]);
+      gf_store4((float*)a.o1 + at, o[1]);
+      gf_store4((float*)a.o2 + at, h);
+    }
+  }
+}
+
 // ------------------------------------------------------------------ launch ---
 constexpr size_t kGradUnitBytes = 4 * 16 * 4 * 64 * 16;  // of a bf16 unit, the largest
 
@@ -647,7 +729,13 @@ hipError_t launch_grad_weights(const GradGemmArgs& a, bool bf16, void* ws, hipSt
 
 hipError_t launch_keep_f32(const GradGemmArgs& a, hipStream_t s) {
   if (a.R == 0) return hipSuccess;
-  keep_f32_kernel<<<device_cu_count(), 512, 0, s>>>(with_split(a, nullptr));
+  const int cus = device_cu_count();
+  // tiles of 64 x 64 that an even routing gives: below one a CU, the smaller ones
+  const int64_t rows = a.all_held ? a.R : a.R / 2, tiles = (rows / 64 + (rows < a.E ? rows : a.E)) * ((a.F + 63) / 64);
+  if (tiles < cus)
+    keep_f32_few_kernel<<<cus, 64 * kFewWaves, 0, s>>>(with_split(a, nullptr));
+  else
+    keep_f32_kernel<<<cus, 512, 0, s>>>(with_split(a, nullptr));
   return hipGetLastError();
 }
 

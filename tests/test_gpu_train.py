@@ -240,7 +240,10 @@ EXPERTS = [dict(M=1, H=64, F=64, E=1, k=1), dict(M=1, H=256, F=320, E=8, k=2), d
            # few tiles with long reductions: split along K
            dict(M=70, H=1088, F=2112, E=2, k=1), dict(M=1500, H=64, F=128, E=1, k=1),
            dict(M=1400, H=128, F=64, E=3, k=2, S=3, held=2, base=1), dict(M=300, H=1024, F=1024, E=2, k=1, skip=(1,)),
-           dict(M=3000, H=320, F=64, E=2, k=1, crowd=2.5)]
+           dict(M=3000, H=320, F=64, E=2, k=1, crowd=2.5),
+           # many tiles: the larger f32 ones
+           dict(M=8200, H=64, F=4096, E=2, k=1), dict(M=4100, H=4160, F=64, E=3, k=2), dict(M=100, H=1088, F=1152, E=32, k=2),
+           dict(M=90, H=128, F=448, E=40, k=2)]
 
 
 def experts(M, H, F, E, k, dtype, S=1, held=0, base=0, crowd=0.0, skip=(), seed=0):
@@ -335,6 +338,101 @@ def test_experts(shape, dtype):
     for name, a, b in (("dwd", "dy", "h"), ("dwg", "dgate", "xp"), ("dwu", "dup", "xp")):
         want, bound = ref.weights(d[a], d[b], d["offsets"], EL, False, start=torch.full((), 3.0, device=DEV))
         serving_ref.check(more[name], want, bound, (shape, name, "accumulated"))
+
+
+@pytest.mark.parametrize("p", [0.0, 0.1])
+def test_rows_larger_than_the_cache(p):
+    # f32 rows of over 96 MiB take other loads
+    M, H, E, k = 3333, 4160, 8, 2
+    prob, w, f2s, y = combine_inputs(M, H, E, k, "bf16")
+    rng = rng_of(7, 8)
+    keep = ref.mask(M, H, p, rng, DEV) if p else None
+    drop = moe.dropout(p, rng) if p else None
+    x = normal(gen(31), M, H, dtype=torch.bfloat16)
+    out, i1 = guarded((M, H), torch.bfloat16)
+    moe.moe_combine_dropout(prob, y, w, f2s, moe.epilogue(x, "bf16"), drop, out)
+    serving_ref.check(out, *ref.combine(y, w, f2s, keep, p, x, True), "out")
+    dy, i2 = guarded((M * k, H), torch.bfloat16, fill=5.0)
+    dw, i3 = guarded((M, k), torch.float32)
+    moe.moe_combine_backward(prob, x, y, w, f2s, drop, dy, dw)
+    wy, by, ww, bw = ref.combine_backward(x, y, w, f2s, keep, p, True)
+    serving_ref.check(dy, wy, by, "dy")
+    serving_ref.check(dw, ww, bw, "dw")
+    dx, i4 = guarded((M, H), torch.float32)
+    moe.moe_dispatch_backward(moe.problem(M, H, 64, E, k, dtype="f32"), y, f2s, None, dx)
+    serving_ref.check(dx, *ref.dispatch_backward(y, f2s, M, k, None, False), "dx")
+    for c in (i1, i2, i3, i4):
+        c()
+
+
+def test_offsets_past_32_bits():
+    # y of 5.2 GB, and buffers of the experts' products of 2.6 GB: the first and the last tokens and rows
+    M, H, E, k = 40000, 16384, 3, 2
+    idx, w, f2s, offsets = routing(M, E, k, seed=77)
+    prob = moe.problem(M, H, 64, E, k)
+    y = torch.empty((M * k, H), device=DEV)
+    dout = normal(gen(5), M, H, dtype=torch.bfloat16)
+    ends = torch.cat([torch.arange(5), torch.arange(M - 5, M)]).to(DEV)
+    f = f2s.long().view(M, k)
+    y.normal_()
+    y[f[ends].flatten()] = normal(gen(6), 10 * k, H)
+    dy = torch.zeros((M * k, H), dtype=torch.bfloat16, device=DEV)
+    dw = torch.zeros((M, k), device=DEV)
+    rng = rng_of(1, 2)
+    moe.moe_combine_backward(prob, dout, y, w, f2s, None, dy, dw)
+    for t in ends.tolist():
+        r = f[t]
+        small = torch.arange(k, dtype=torch.int32, device=DEV)
+        wy, by, ww, bw = ref.combine_backward(dout[t:t + 1], y[r], w[t:t + 1], small, None, 0.0, True)
+        serving_ref.check(dy[r], wy, by, ("dy", t))
+        serving_ref.check(dw[t:t + 1], ww, bw, ("dw", t))
+    out = torch.zeros((M, H), device=DEV)
+    moe.moe_combine_dropout(prob, y, w, f2s, None, moe.dropout(0.5, rng), out)
+    words = ref.philox_words(M * H, 1, 2).reshape(M, H)
+    for t in ends.tolist():
+        keep = torch.from_numpy(words[t:t + 1] >= 2 ** 31).to(DEV)
+        small = torch.arange(k, dtype=torch.int32, device=DEV)
+        serving_ref.check(out[t:t + 1], *ref.combine(y[f[t]], w[t:t + 1], small, keep, 0.5, None, False), ("out", t))
+    dx = torch.zeros((M, H), device=DEV)
+    moe.moe_dispatch_backward(prob, dy, f2s, None, dx)
+    for t in ends.tolist():
+        small = torch.arange(k, dtype=torch.int32, device=DEV)
+        serving_ref.check(dx[t:t + 1], *ref.dispatch_backward(dy[f[t]], small, 1, k, None, False), ("dx", t))
+
+
+def test_product_buffers_past_two_gib():
+    M, H, F, E = 20011, 64, 65536, 2  # R F = 1.3e9: 2.6 GB a buffer
+    _, _, _, offsets = routing(M, E, 1, seed=78)
+    prob = moe.problem(M, H, F, E, 1)
+    ws = torch.empty(moe.moe_workspace_bytes(prob, moe.MOE_OP_GROUPED_GEMM_BACKWARD), dtype=torch.uint8, device=DEV)
+    g = gen(40)
+    n = lambda *s, std=1.0: torch.empty(s, dtype=torch.bfloat16, device=DEV).normal_(0.0, std, generator=g)
+    xp, dy, wg, wu, wd = n(M, H), n(M, H), n(E, F, H, std=0.1), n(E, F, H, std=0.1), n(E, H, F, std=0.1)
+    gate, up, h = (torch.zeros((M, F), dtype=torch.bfloat16, device=DEV) for _ in range(3))
+    moe.moe_grouped_gemm_aux(prob, xp, wg, wu, offsets, gate, up, h)
+    cut = int(offsets[1])
+    rows = [0, 1, cut - 1, cut, cut + 1, M - 2, M - 1]
+    part = lambda lo, hi: torch.tensor([0, 1, 1] if hi <= cut else [0, 0, 1], dtype=torch.int32)
+    for r in rows:
+        gw, bg, uw, bu = ref.products(xp[r:r + 1], wg, wu, part(r, r + 1), True)
+        serving_ref.check(gate[r:r + 1], gw, bg, ("gate", r))
+        serving_ref.check(up[r:r + 1], uw, bu, ("up", r))
+    dgate, dup = torch.zeros_like(gate), torch.zeros_like(up)
+    moe.moe_grouped_gemm_backward(prob, 1, dy, None, wd, None, gate, up, offsets, dgate, dup, ws)
+    for r in rows:
+        gw, bg, uw, bu = ref.rows1(dy[r:r + 1], wd, gate[r:r + 1], up[r:r + 1], part(r, r + 1), True)
+        serving_ref.check(dgate[r:r + 1], gw, bg, ("dgate", r))
+        serving_ref.check(dup[r:r + 1], uw, bu, ("dup", r))
+    dxp = torch.zeros_like(xp)
+    moe.moe_grouped_gemm_backward(prob, 0, dgate, dup, wg, wu, None, None, offsets, dxp, None, ws)
+    for r in rows:
+        serving_ref.check(dxp[r:r + 1], *ref.rows0(dgate[r:r + 1], dup[r:r + 1], wg, wu, part(r, r + 1), True), ("dxp", r))
+    dwg, dwu = (torch.zeros((E, F, H), device=DEV) for _ in range(2))
+    moe.moe_grouped_gemm_backward_weights(prob, 0, dgate, dup, xp, offsets, dwg, dwu, False, ws)
+    cols = torch.tensor([0, 5, 255, 256, F - 2, F - 1], device=DEV)
+    for d, o in ((dgate, dwg), (dup, dwu)):
+        want, bound = ref.weights(d[:, cols].contiguous(), xp, offsets, E, False)
+        serving_ref.check(o[:, cols], want, bound, "weights")
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
