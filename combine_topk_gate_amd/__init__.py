@@ -180,7 +180,7 @@ def epilogue(residual=None, out_dtype="f32") -> Epilogue:
 def dropout(p, rng) -> Dropout:
     """Dropout with probability p (0 <= p < 1) whose mask comes from rng, a device
     int64 tensor {seed, offset} that the kernels read.  It holds the tensor."""
-    drop = Dropout(float(p), rng.data_ptr())
+    drop = Dropout(float(p), None if rng is None else rng.data_ptr())
     drop.tensor = rng
     return drop
 

@@ -85,6 +85,11 @@ struct GradTile {
   int part, parts;  // which of the parts of the K steps (0 of 1: all)
 };
 
+__device__ __forceinline__ const __bf16* uniform_ptr(const __bf16* p) {
+  const uint64_t v = (uint64_t)p;
+  return (const __bf16*)((uint64_t)(uint32_t)uniform((int)(v >> 32)) << 32 | (uint32_t)uniform((int)v));
+}
+
 // First step of part i of n of nk K steps.
 __device__ __forceinline__ int part_begin(int nk, int i, int n) { return (int)((int64_t)nk * i / n); }
 
@@ -129,8 +134,10 @@ struct GradWave {
   const int cr = tid >> 5, cc = tid & 31;
   const uint32_t wvoff = (uint32_t)cr * wpitch + (uint32_t)cc * 16u;
 
-  // the K step to load next
+  // the K step to load next: its buffers, and (weights) where they begin and how long they are
   __amdgpu_buffer_rsrc_t rw, rx;
+  const __bf16 *wbase = nullptr, *xbase = nullptr;
+  uint32_t wbytes = 0, xbytes = 0;
   uint32_t xs = 0;
   int e = 0, col0 = 0, row0 = 0, k0 = 0, nk = 0;  // K steps k0 .. k0 + nk
   const __bf16* d = nullptr;
@@ -148,15 +155,20 @@ struct GradWave {
     if constexpr (KIND == kGradWeights) {
       if (kt < nk) {
         r += kBK;
-        while (r >= rend) {
+        while (r >= rend && sb < p.G / p.E) {
           r = uniform(offsets[sb * p.E + e]);
           rend = uniform(offsets[sb * p.E + e + 1]);
           ++sb;
         }
         const uint32_t n = (uint32_t)min(rend - r, kBK);
-        rw = make_rsrc((const __bf16*)p.x + (int64_t)r * N + col0, n * wpitch - (uint32_t)col0 * 2u);
-        rx = make_rsrc(d + (int64_t)r * DN + row0, n * xpitch - (uint32_t)row0 * 2u);
+        wbase = (const __bf16*)p.x + (int64_t)r * N + col0;
+        xbase = d + (int64_t)r * DN + row0;
+        wbytes = n * wpitch - (uint32_t)col0 * 2u;
+        xbytes = n * xpitch - (uint32_t)row0 * 2u;
       }
+      // (made uniform here, in every step: a descriptor that the compiler cannot tell to be is loaded through lane by lane)
+      rw = make_rsrc(uniform_ptr(wbase), (uint32_t)uniform((int)wbytes));
+      rx = make_rsrc(uniform_ptr(xbase), (uint32_t)uniform((int)xbytes));
     } else {
       const int per = K / kBK;
       kt = k0 + min(kt, nk - 1);
@@ -216,7 +228,7 @@ struct GradWave {
       r = rend = sb = 0;
       for (int left = k0;;) {
         const int n = (rend - r + kBK - 1) / kBK;
-        if (left <= n) {
+        if (left <= n || sb == p.G / p.E) {
           r += (left - 1) * kBK;
           break;
         }

@@ -179,7 +179,8 @@ __global__ __launch_bounds__(kGemmThreads) void grad_rows_bf16_kernel(GradGemmAr
 __global__ __launch_bounds__(kGemmThreads) void grad_weights_bf16_kernel(GradGemmArgs a) {
   __shared__ __attribute__((aligned(16))) char lds[kGemmLdsBytes];
   __shared__ int offsets[kMaxTileSegs + 1];
-  for (int i = threadIdx.x; i <= a.G; i += kGemmThreads) offsets[i] = a.offsets[i];
+  // (kept inside the rows, so that even bad ones read nothing else)
+  for (int i = threadIdx.x; i <= a.G; i += kGemmThreads) offsets[i] = min(max(a.offsets[i], 0), (int)a.R);
   const bool l0 = a.layer == 0;
   const int N = l0 ? a.F : a.H, C = l0 ? a.H : a.F;
   const int NR = (N + 255) / 256, NC = (C + 255) / 256, rows = (l0 ? 2 : 1) * NR;
@@ -354,7 +355,8 @@ __global__ __launch_bounds__(256 * KG) void grad_rows_f32_kernel(GradGemmArgs a)
     const TileCoord c = tile_coord(u >= 0 ? whole + shuffled(sh, j) : shuffled(sm, v), a.E, NT, TX, 1, 0, tl);
     const int e = c.g, col0 = c.nt * TX;
     if (threadIdx.x < TX) {
-      const int pos = expert_row(tl, e, a.E, S, c.m0, threadIdx.x);
+      int pos = expert_row(tl, e, a.E, S, c.m0, threadIdx.x);
+      if ((unsigned)pos >= (unsigned)a.R) pos = -1;
       rowpos[threadIdx.x] = pos;
       if (u >= 0 && part == 0) a.split.desc[(int64_t)j * kGradDescInts + 8 + threadIdx.x] = pos;
     }
@@ -425,7 +427,7 @@ __global__ __launch_bounds__(256 * KG) void grad_weights_f32_kernel(GradGemmArgs
   typedef GfTile<TX, TX, KG> Tile;
   __shared__ __attribute__((aligned(16))) float lds[Tile::kLds];
   __shared__ int offsets[kMaxTileSegs + 1];
-  for (int h = threadIdx.x; h <= a.G; h += 256 * KG) offsets[h] = a.offsets[h];
+  for (int h = threadIdx.x; h <= a.G; h += 256 * KG) offsets[h] = min(max(a.offsets[h], 0), (int)a.R);
   __syncthreads();
   const bool l0 = a.layer == 0;
   const int N = l0 ? a.F : a.H, C = l0 ? a.H : a.F;  // rows and columns of dW
@@ -457,7 +459,7 @@ __global__ __launch_bounds__(256 * KG) void grad_weights_f32_kernel(GradGemmArgs
     int row = 0, rend = 0, sb = 0;  // the step before b: its row, the segment's end, the next source block
     for (int left = b;;) {
       const int have = (rend - row + kGfK - 1) / kGfK;
-      if (left <= have) {
+      if (left <= have || sb == S) {
         row += (left - 1) * kGfK;
         break;
       }
@@ -469,7 +471,7 @@ __global__ __launch_bounds__(256 * KG) void grad_weights_f32_kernel(GradGemmArgs
     GfPart<TX> pw, px;
     auto load = [&](int) {
       row += kGfK;
-      while (row >= rend) {
+      while (row >= rend && sb < S) {
         row = offsets[sb * a.E + e];
         rend = offsets[sb * a.E + e + 1];
         ++sb;
@@ -521,7 +523,10 @@ __global__ __launch_bounds__(512) void keep_f32_kernel(GradGemmArgs a) {
   for (int v = blockIdx.x; v < T; v += gridDim.x) {
     const TileCoord c = tile_coord(shuffled(sm, v), a.E, NT, 64, 1, 0, tl);
     const int e = c.g, col0 = c.nt * 64;
-    if (threadIdx.x < 64) rowpos[threadIdx.x] = expert_row(tl, e, a.E, S, c.m0, threadIdx.x);
+    if (threadIdx.x < 64) {
+      const int pos = expert_row(tl, e, a.E, S, c.m0, threadIdx.x);
+      rowpos[threadIdx.x] = (unsigned)pos < (unsigned)a.R ? pos : -1;
+    }
     __syncthreads();
     const float* xr[2];
     const float* wr[4];
@@ -575,10 +580,11 @@ __global__ __launch_bounds__(64 * kFewWaves) void keep_f32_few_kernel(GradGemmAr
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, lrow = lane & 31, lk = lane >> 5;
   for (int v = blockIdx.x; v < T; v += gridDim.x) {
     const TileCoord c = tile_coord(shuffled(sm, v), a.E, NT, 32, 1, 0, tl);
-    const int e = c.g, f = c.nt * 32 + lrow, pos = expert_row(tl, e, a.E, S, c.m0, lrow);
-    // a row or column that the tile lacks: the first one's values, whose products are not stored
+    const int e = c.g, f = c.nt * 32 + lrow, found = expert_row(tl, e, a.E, S, c.m0, lrow);
+    const int pos = (unsigned)found < (unsigned)a.R ? found : -1;
+    // a row or column that the tile lacks: the first row's, whose products are not stored
     const int64_t wrow = ((int64_t)e * N + (f < N ? f : c.nt * 32)) * K + 4 * lk;
-    const float* src[3] = {(const float*)a.x + (int64_t)(pos >= 0 ? pos : expert_row(tl, e, a.E, S, c.m0, 0)) * K + 4 * lk,
+    const float* src[3] = {(const float*)a.x + (int64_t)(pos >= 0 ? pos : 0) * K + 4 * lk,
                            (const float*)a.w0 + wrow, (const float*)a.w1 + wrow};
     const int steps = K / kGfK, b = part_begin(steps, wave, kFewWaves), end = part_begin(steps, wave + 1, kFewWaves);
     f32x4_t now[3][4], next[3][4];
