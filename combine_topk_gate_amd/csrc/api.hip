@@ -937,33 +937,14 @@ moe_status_t moe_grouped_gemm_aux(const moe_problem_t* p, const void* a, const v
     st = validate_offsets(p, offsets, hs);
     if (st != MOE_OK) return st;
   }
-  if (p->dtype == MOE_DTYPE_F32) {
-    GradGemmArgs g = grad_args(p, 0, offsets);
-    g.x = a;
-    g.w0 = w0;
-    g.w1 = w1;
-    g.o0 = gate;
-    g.o1 = up;
-    g.o2 = c;
-    return hip_status(launch_keep_f32(g, hs));
-  }
-  GemmProblem gp;
-  gp.layer = 0;
-  gp.a = a;
-  gp.w0 = w0;
-  gp.w1 = w1;
-  gp.offsets = offsets;
-  gp.c = c;
-  gp.R = R;
-  gp.K = p->hidden;
-  gp.N = p->ffn;
-  gp.E = held(p);
-  gp.G = segments(p);
-  gp.rowmap = combine_blocks(p);
-  gp.shuffle = debug_shuffle();
-  gp.gate = gate;
-  gp.up = up;
-  return hip_status(launch_grouped_gemm_bf16(gp, hs));
+  GradGemmArgs g = grad_args(p, 0, offsets);
+  g.x = a;
+  g.w0 = w0;
+  g.w1 = w1;
+  g.o0 = gate;
+  g.o1 = up;
+  g.o2 = c;
+  return hip_status(launch_keep(g, p->dtype == MOE_DTYPE_BF16, hs));
 }
 
 moe_status_t moe_grouped_gemm_backward(const moe_problem_t* p, int32_t layer, const void* d0, const void* d1,

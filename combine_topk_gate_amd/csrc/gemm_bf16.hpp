@@ -54,8 +54,6 @@ struct Bf16GemmArgs {
   const __bf16* w0;  // layer 0: W_gate [E, F, H]; layer 1: W_down [E, H, F]
   const __bf16* w1;  // layer 0: W_up [E, F, H]
   void* c;           // layer 0: Hact [R, F] bf16 (or MXFP8 codes); layer 1: Y [R, H] f32
-  __bf16* gate = nullptr;  // KEEP: X W_gate^T and X W_up^T [R, F]
-  __bf16* up = nullptr;
   // MXFP8 (one e8m0 scale byte per 32 values along the reduction index,
   // stored in groups of 32 rows: the byte of row r, block b of a tensor of
   // `cols` columns sits at (r / 32) * cols + (b / 4) * 128 + (r % 32) * 4 +
@@ -96,11 +94,8 @@ __device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirs
 // segment made of the rows of several source blocks for one expert, whose
 // rows lie apart in the sorted order.  seg_rows and m0 then count the rows
 // of that combined segment, and seg_start is unused.
-//
-// KEEP (layer 0): the two products are stored as well, rounded to bf16, for
-// the gradient (Hact is formed from the f32 values as without it).
 template <int LAYER, bool GATHER = false, int TM = kTileRows, bool PARTIAL = false, bool OUT8 = false,
-          bool ROWMAP = false, bool KEEP = false>
+          bool ROWMAP = false>
 __device__ __forceinline__ void bf16_gemm_tile(const Bf16GemmArgs& p, int g, int seg_start, int seg_rows, int m0,
                                                int nt, char* __restrict__ lds, int k0 = 0, int k1 = -1,
                                                float* __restrict__ part = nullptr,
@@ -109,7 +104,6 @@ __device__ __forceinline__ void bf16_gemm_tile(const Bf16GemmArgs& p, int g, int
   static_assert(TM == 256 || TM == 128, "token tile height");
   static_assert(!PARTIAL || (TM == 256 && LAYER == 1), "partial tiles: layer 1, full height");
   static_assert(!OUT8 || (LAYER == 0 && !PARTIAL), "MXFP8 output: layer 0");
-  static_assert(!KEEP || (LAYER == 0 && !OUT8), "kept products: bf16 layer 0");
   constexpr int NJ = TM / 64;      // token fragments per wave
   constexpr int XI = TM / 32;      // token-row loads per thread per K step
   constexpr int XQ = XI / 4;       // ... per sub-step
@@ -493,58 +487,6 @@ __device__ __forceinline__ void bf16_gemm_tile(const Bf16GemmArgs& p, int g, int
       }
     }
     __syncthreads();
-  } else if (KEEP) {
-    // Hact, gate and up, one row fragment of the wave (32 rows x 64 columns) at
-    // a time, through 32 KiB of LDS of the wave's own, in two halves by turns:
-    // no barrier, and a fragment's 12 stores go out together.  128 B per staged
-    // row; 8-byte unit u of row i at u ^ (i / 2), so 32 rows write one unit, and
-    // 8 lanes a row read 16-byte chunks, without a conflict.  The stores are
-    // buffer ones: rows and columns that the tile lacks lie past the range.
-    // (the lane's number is hidden from the optimiser, which would keep every
-    // swizzled address in a register through the K loop)
-    int ln = lane;
-    asm volatile("" : "+v"(ln));
-    const int er = ln & 31, ek = ln >> 5;
-    char* const mine = lds + wave * 32768;
-    void* const outs[3] = {p.c, p.gate, p.up};
-#pragma unroll
-    for (int nj = 0; nj < NJ; ++nj) {
-      char* const stg = mine + (nj & 1) * 16384;
-#pragma unroll
-      for (int mi = 0; mi < 2; ++mi) {
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          bf16x4_t o[3];
-#pragma unroll
-          for (int v = 0; v < 4; ++v) {
-            const float gt = acc[mi][nj][4 * q + v], up = acc[mi + 2][nj][4 * q + v];
-            o[0][v] = (__bf16)silu_mul_fast(gt, up);
-            o[1][v] = (__bf16)gt;
-            o[2][v] = (__bf16)up;
-          }
-          const int u = mi * 8 + 2 * q + ek;
-#pragma unroll
-          for (int m = 0; m < 3; ++m)
-            *reinterpret_cast<bf16x4_t*>(stg + m * 4096 + er * 128 + ((u ^ (er >> 1)) << 3)) = o[m];
-        }
-      }
-      const int c = ln & 7, f = col0 + wn * 64 + 8 * c;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int row = 8 * i + (ln >> 3), t = wm * (TM / 2) + nj * 32 + row;
-        const int pos = m0 + t < seg_rows ? (ROWMAP ? rowpos[t] : seg_start + m0 + t) : -1;
-        // at most R F < 2^31 elements: past every range
-        const uint32_t at = pos >= 0 && f < N ? ((uint32_t)pos * (uint32_t)N + (uint32_t)f) * 2u : 0xFFFFFFF0u;
-#pragma unroll
-        for (int m = 0; m < 3; ++m) {
-          i32x4_t v = *reinterpret_cast<const i32x4_t*>(stg + m * 4096 + row * 128 + ((c ^ (row >> 2)) << 4));
-          if ((row >> 1) & 1) v = i32x4_t{v[2], v[3], v[0], v[1]};
-          // as used once (nt): the rows go by, the weight panels stay in the L2
-          __builtin_amdgcn_raw_buffer_store_b128(v, make_rsrc(outs[m], (uint32_t)(p.M * N * 2)), (int)at, 0, 2);
-        }
-      }
-    }
-    __syncthreads();
   } else if (LAYER == 0) {
     // 256 B per staged row (128 bf16 columns); 8-byte unit u of row t at
     // unit u ^ (t & 31): conflict-free for 32 rows writing the same unit.
@@ -632,16 +574,16 @@ __device__ __forceinline__ void bf16_gemm_tile(const Bf16GemmArgs& p, int g, int
 // running at once on an XCD stay in step and share the segment's weight
 // panels in its L2 (measured: halving those last tiles cost more in
 // re-read weights than it saved).
-template <int LAYER, bool GATHER = false, bool OUT8 = false, bool ROWMAP = false, bool KEEP = false>
+template <int LAYER, bool GATHER = false, bool OUT8 = false, bool ROWMAP = false>
 __device__ __forceinline__ void bf16_gemm_row_tile(const Bf16GemmArgs& p, int g, int seg_start, int seg_rows, int m0,
                                                    int nt, char* __restrict__ lds,
                                                    const int* __restrict__ rowpos = nullptr) {
   if (seg_rows <= kTileRows / 2)
-    bf16_gemm_tile<LAYER, GATHER, kTileRows / 2, false, OUT8, ROWMAP, KEEP>(p, g, seg_start, seg_rows, m0, nt, lds, 0,
-                                                                            -1, nullptr, rowpos);
+    bf16_gemm_tile<LAYER, GATHER, kTileRows / 2, false, OUT8, ROWMAP>(p, g, seg_start, seg_rows, m0, nt, lds, 0, -1,
+                                                                      nullptr, rowpos);
   else
-    bf16_gemm_tile<LAYER, GATHER, kTileRows, false, OUT8, ROWMAP, KEEP>(p, g, seg_start, seg_rows, m0, nt, lds, 0, -1,
-                                                                        nullptr, rowpos);
+    bf16_gemm_tile<LAYER, GATHER, kTileRows, false, OUT8, ROWMAP>(p, g, seg_start, seg_rows, m0, nt, lds, 0, -1,
+                                                                  nullptr, rowpos);
 }
 
 }  // namespace moe

@@ -1,7 +1,9 @@
-// bf16 MFMA tiles of the grouped GEMM's gradients (gfx950).
+// bf16 MFMA tiles of the grouped GEMM's training products (gfx950).
 //
 // The forward tile (gemm_bf16.hpp) has both operands contiguous along the
-// reduction.  Here that holds for the token rows of a rows' gradient alone:
+// reduction, and so have the forward products that are kept (keep: gate and up,
+// each tile 128 columns of both).  In the gradients that holds for the token
+// rows of a rows' gradient alone:
 //   rows     C[r, n] = sum_k D[r, k] W[k, n]: W's stored rows are the k index;
 //   weights  C[f, h] = sum_r D[r, f] X[r, h]: so are the rows of both operands.
 // An operand that lies [k][columns] in memory is staged the same way in LDS
@@ -40,7 +42,7 @@ namespace moe {
 typedef __attribute__((address_space(3))) char lds_byte;
 typedef __attribute__((address_space(3))) bf16x4_t lds_bf16x4;
 
-enum GradKind { kGradRows0, kGradRows1, kGradWeights };
+enum GradKind { kGradRows0, kGradRows1, kGradWeights, kKeep };
 
 // d silu(g) u / dg and / du times dh, with the hardware exponential and
 // reciprocal (about 1 ulp each), as the forward epilogue's silu_mul_fast: the
@@ -111,12 +113,14 @@ __device__ __forceinline__ int weight_steps(const GradGemmArgs& p, const int* of
 template <GradKind KIND, int TM>
 struct GradWave {
   static constexpr bool XKC = KIND != kGradWeights;  // x operand contiguous along k
+  static constexpr bool WKC = KIND == kKeep;         // w operand too
   static_assert(TM == 256 || (TM == 128 && XKC), "tile height");
   static constexpr int NJ = TM / 64;             // row fragments per wave
   static constexpr int XI = XKC ? TM / 32 : 8;   // x loads per thread per K step
   static constexpr int XQ = XI / 4;              // ... per sub-step
   static constexpr int NRX = XKC ? NJ : 2 * NJ;  // LDS reads of x per sub-step
-  static constexpr int NR = 8 + NRX;             // LDS reads per sub-step
+  static constexpr int WH = WKC ? 1 : 2;         // LDS reads of a w fragment
+  static constexpr int NR = 4 * WH + NRX;        // LDS reads per sub-step
   static constexpr int NW = 2 + XQ;              // LDS stores (and loads) per sub-step
   static constexpr int NM = 4 * NJ;              // matrix instructions per sub-step
 
@@ -128,11 +132,12 @@ struct GradWave {
   // a product's reduction length (rows), the columns of D and of the output
   const bool l0 = KIND == kGradRows0 || (KIND == kGradWeights && p.layer == 0);
   const int K = KIND == kGradRows0 ? p.F : p.H;
-  const int N = KIND == kGradRows1 ? p.F : KIND == kGradRows0 ? p.H : (l0 ? p.H : p.F);
+  const int N = KIND == kGradRows1 || KIND == kKeep ? p.F : KIND == kGradRows0 ? p.H : (l0 ? p.H : p.F);
   const int DN = KIND == kGradWeights ? (l0 ? p.F : p.H) : K;
   const uint32_t wpitch = (uint32_t)N * 2u, xpitch = (uint32_t)DN * 2u;
   const int cr = tid >> 5, cc = tid & 31;
   const uint32_t wvoff = (uint32_t)cr * wpitch + (uint32_t)cc * 16u;
+  __amdgpu_buffer_rsrc_t rw1;  // keep: W_up's rows (rw: W_gate's)
 
   // the K step to load next: its buffers, and (weights) where they begin and how long they are
   __amdgpu_buffer_rsrc_t rw, rx;
@@ -169,6 +174,8 @@ struct GradWave {
       // (made uniform here, in every step: a descriptor that the compiler cannot tell to be is loaded through lane by lane)
       rw = make_rsrc(uniform_ptr(wbase), (uint32_t)uniform((int)wbytes));
       rx = make_rsrc(uniform_ptr(xbase), (uint32_t)uniform((int)xbytes));
+    } else if constexpr (KIND == kKeep) {
+      xs = (uint32_t)min(kt, nk - 1) * (kBK * 2);
     } else {
       const int per = K / kBK;
       kt = k0 + min(kt, nk - 1);
@@ -182,11 +189,15 @@ struct GradWave {
   }
 
   // Global -> register loads.  [k][columns]: thread owns 16-byte chunk tid & 31
-  // of k rows (tid >> 5) + 8 i; [rows][k]: chunk tid & 7 of rows (tid >> 3) + 32 i.
+  // of k rows (tid >> 5) + 8 i; [rows][k]: chunk tid & 7 of rows (tid >> 3) + 32 i
+  // (keep's weights: 128 of gate, then 128 of up).
   __device__ __forceinline__ void gload_one(int q, int j) {
     if (j < 2) {
       const int i = 2 * q + j;
-      wreg[i] = buf_load16(rw, wvoff + (uint32_t)i * (8u * wpitch), 0);
+      if constexpr (WKC)
+        wreg[i] = buf_load16(i < 4 ? rw : rw1, (uint32_t)((tid >> 3) + 32 * (i & 3)) * xpitch + (uint32_t)(tid & 7) * 16u, xs);
+      else
+        wreg[i] = buf_load16(rw, wvoff + (uint32_t)i * (8u * wpitch), 0);
     } else {
       const int i = q * XQ + j - 2;
       if constexpr (XKC)
@@ -202,7 +213,7 @@ struct GradWave {
     char* wdst = lds + stage * kStageBytes;
     if (j < 2) {
       const int i = 2 * q + j;
-      *reinterpret_cast<i32x4_t*>(wdst + st_kr + i * 4096) = wreg[i];
+      *reinterpret_cast<i32x4_t*>(wdst + (WKC ? st_kc : st_kr) + i * 4096) = wreg[i];
     } else {
       const int i = q * XQ + j - 2;
       *reinterpret_cast<i32x4_t*>(wdst + kOperandBytes + (XKC ? st_kc : st_kr) + i * 4096) = xreg[i];
@@ -241,6 +252,13 @@ struct GradWave {
     } else {
       nk = (KIND == kGradRows0 ? 2 : 1) * (K / kBK);
       range(t);
+      if constexpr (KIND == kKeep) {
+        const uint32_t bytes = (uint32_t)min(N - col0, 128) * xpitch;
+        const int64_t at = ((int64_t)e * N + col0) * K;
+        rw = make_rsrc((const __bf16*)p.w0 + at, bytes);
+        rw1 = make_rsrc((const __bf16*)p.w1 + at, bytes);
+        rx = make_rsrc(p.x, (uint32_t)(p.R * (int64_t)xpitch));
+      }
 #pragma unroll
       for (int i = 0; i < XI; ++i) {
         const int pos = rowpos[(tid >> 3) + 32 * i];
@@ -267,16 +285,17 @@ struct GradWave {
       const uint32_t base = (uint32_t)(8 * (g >> 1) + lq) * 512u + (uint32_t)(g & 1) * 32u + (uint32_t)(l & 3) * 8u;
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        wrd[i] = base + (uint32_t)(wn * 8 + ((i ^ lq) << 1)) * 32u;
-        if constexpr (XKC)  // sub-step i of the wave's rows
-          xrd[i] = (uint32_t)(kOperandBytes + (wm * (TM / 2) + lrow) * 128) +
-                   (uint32_t)(((2 * i + lk) ^ (lrow & 7) ^ ((lrow >> 3) & 1)) << 4);
+        const uint32_t kc = (uint32_t)(((2 * i + lk) ^ (lrow & 7) ^ ((lrow >> 3) & 1)) << 4);  // sub-step i's chunk of a row
+        wrd[i] = WKC ? (uint32_t)(wn * 64 + lrow) * 128u + kc : base + (uint32_t)(wn * 8 + ((i ^ lq) << 1)) * 32u;
+        if constexpr (XKC)
+          xrd[i] = (uint32_t)(kOperandBytes + (wm * (TM / 2) + lrow) * 128) + kc;
         else
           xrd[i] = (uint32_t)kOperandBytes + base + (uint32_t)(wm * 8 + ((i ^ lq) << 1)) * 32u;
       }
     }
     lds_byte* l3 = (lds_byte*)lds;
-    bf16x4_t fa[2][4][2];
+    bf16x4_t fa[2][WKC ? 1 : 4][2];
+    bf16x8_t fa8[2][WKC ? 4 : 1];
     bf16x4_t fx4[2][XKC ? 1 : NJ][2];
     bf16x8_t fx8[2][XKC ? NJ : 1];
     auto read_tr = [&](uint32_t at, int stage, int ks, int h) {
@@ -286,16 +305,18 @@ struct GradWave {
     // read j of sub-step ks, in the order the matrix instructions use them: column fragment 0, the row fragments,
     // columns 1..3
     auto read_one = [&](int set, int stage, int ks, int j) {
-      if (j < 2) {
-        fa[set][0][j] = read_tr(wrd[0], stage, ks, j);
-      } else if (j < 2 + NRX) {
+      if (j >= WH && j < WH + NRX) {
+        const int i = j - WH;
         if constexpr (XKC)
-          fx8[set][j - 2] = *reinterpret_cast<const bf16x8_t*>(lds + stage * kStageBytes + xrd[ks] + (j - 2) * 4096);
+          fx8[set][i] = *reinterpret_cast<const bf16x8_t*>(lds + stage * kStageBytes + xrd[ks] + i * 4096);
         else
-          fx4[set][(j - 2) / 2][j & 1] = read_tr(xrd[(j - 2) / 2], stage, ks, j & 1);
+          fx4[set][i / 2][i & 1] = read_tr(xrd[i / 2], stage, ks, i & 1);
       } else {
-        const int i = j - NRX;
-        fa[set][i / 2][i & 1] = read_tr(wrd[i / 2], stage, ks, i & 1);
+        const int i = j < WH ? j : j - NRX;
+        if constexpr (WKC)  // gate rows 64 wn + 32 i (i < 2), up rows 128 + 64 wn + 32 (i - 2)
+          fa8[set][i] = *reinterpret_cast<const bf16x8_t*>(lds + stage * kStageBytes + wrd[ks] + (i & 1) * 4096 + (i >> 1) * 16384);
+        else
+          fa[set][i / 2][i & 1] = read_tr(wrd[i / 2], stage, ks, i & 1);
       }
     };
     auto mfma_rows = [&](int set, int mi0, int mi1) {
@@ -303,8 +324,11 @@ struct GradWave {
       for (int mi = mi0; mi < mi1; ++mi)
 #pragma unroll
         for (int nj = 0; nj < NJ; ++nj) {
-          const bf16x8_t a = __builtin_shufflevector(fa[set][mi][0], fa[set][mi][1], 0, 1, 2, 3, 4, 5, 6, 7);
-          bf16x8_t b;
+          bf16x8_t a, b;
+          if constexpr (WKC)
+            a = fa8[set][mi];
+          else
+            a = __builtin_shufflevector(fa[set][mi][0], fa[set][mi][1], 0, 1, 2, 3, 4, 5, 6, 7);
           if constexpr (XKC)
             b = fx8[set][nj];
           else
@@ -412,8 +436,51 @@ struct GradWave {
     asm volatile("" : "+v"(lane));
     const int lrow = lane & 31, lk = lane >> 5;
     char* const mine = lds + (tid >> 6) * 32768;
-    const int tcol = uniform(t.col0) + wn * 128;  // the wave's first column
-    if constexpr (KIND == kGradRows0) {
+    const int tcol = uniform(t.col0) + wn * (KIND == kKeep ? 64 : 128);  // the wave's first column
+    if constexpr (KIND == kKeep) {
+      // Hact (as the forward epilogue forms it, from the f32 products), gate and up, 64 columns each: 128 B a staged row;
+      // 8-byte unit u of row i at u ^ (i / 2), so that 32 rows write one unit, and 8 lanes a row read 16-byte chunks,
+      // without a conflict
+      const uint32_t bytes = (uint32_t)(p.R * N * 2);
+      const __amdgpu_buffer_rsrc_t ro[3] = {make_rsrc(p.o2, bytes), make_rsrc(p.o0, bytes), make_rsrc(p.o1, bytes)};
+      const int c = lane & 7;
+#pragma unroll
+      for (int nj = 0; nj < NJ; ++nj) {
+        char* const stg = mine + (nj & 1) * 16384;
+#pragma unroll
+        for (int mi = 0; mi < 2; ++mi)
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            bf16x4_t o[3];
+#pragma unroll
+            for (int v = 0; v < 4; ++v) {
+              const float g = acc[mi][nj][4 * q + v], u = acc[mi + 2][nj][4 * q + v];
+              o[0][v] = (__bf16)silu_mul_fast(g, u);
+              o[1][v] = (__bf16)g;
+              o[2][v] = (__bf16)u;
+            }
+            const int u = mi * 8 + 2 * q + lk;
+#pragma unroll
+            for (int m = 0; m < 3; ++m)
+              *reinterpret_cast<bf16x4_t*>(stg + m * 4096 + lrow * 128 + ((u ^ (lrow >> 1)) << 3)) = o[m];
+          }
+        i32x4_t v[4][3];
+        uint32_t at[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int row = 8 * i + (lane >> 3);
+          at[i] = grad_offset(rowpos[wm * (TM / 2) + nj * 32 + row], tcol + 8 * c, N);
+#pragma unroll
+          for (int m = 0; m < 3; ++m)
+            v[i][m] = *reinterpret_cast<const i32x4_t*>(stg + m * 4096 + row * 128 + ((c ^ (row >> 2)) << 4));
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+          for (int m = 0; m < 3; ++m)
+            buf_store16(ro[m], at[i], (lane >> 4) & 1 ? i32x4_t{v[i][m][2], v[i][m][3], v[i][m][0], v[i][m][1]} : v[i][m]);
+      }
+    } else if constexpr (KIND == kGradRows0) {
       // 256 B a staged row; 8-byte unit u of row i at u ^ i; read as 16-byte chunks: c ^ (i >> 1), halves swapped for
       // an odd row.  16 lanes a row, 8 columns each.
       const __amdgpu_buffer_rsrc_t ro = make_rsrc(p.o0, (uint32_t)(p.R * N * 2));

@@ -54,8 +54,7 @@ __device__ __forceinline__ bool split_pays(int nk, int s, bool halfable) {
 // always splits the same tiles the same way.
 // OUT8 (layer 0): Hact is written in MXFP8 (codes to args.c, scales to
 // args.c_scale) for the MXFP8 Layer1 below.
-// KEEP (layer 0): the gate and up products are stored too.
-template <int LAYER, bool OUT8 = false, bool KEEP = false>
+template <int LAYER, bool OUT8 = false>
 __global__ __launch_bounds__(kGemmThreads) void grouped_gemm_bf16_kernel(Bf16GemmArgs args,
                                                                          const int32_t* __restrict__ offsets, int G,
                                                                          int xcd_slots, SplitWs split,
@@ -108,14 +107,14 @@ __global__ __launch_bounds__(kGemmThreads) void grouped_gemm_bf16_kernel(Bf16Gem
   for (int v = xcd_slot(blockIdx.x, grid); v < entries; v += grid) {
     if (v < T - half) {
       const TileCoord c = tile_coord(shuffled(sm, v), G, NT, kTileRows, xcd_slots, rtb, tl);
-      bf16_gemm_row_tile<LAYER, false, OUT8, false, KEEP>(args, c.g, tl.seg_start[c.g], tl.seg_rows[c.g], c.m0, c.nt, lds);
+      bf16_gemm_row_tile<LAYER, false, OUT8>(args, c.g, tl.seg_start[c.g], tl.seg_rows[c.g], c.m0, c.nt, lds);
     } else {
       const int j = v - (T - half);
       const TileCoord c = tile_coord(T - half + shuffled(sh, j / 2), G, NT, kTileRows, xcd_slots, rtb, tl);
       const int m0 = c.m0 + (j & 1) * (kTileRows / 2);
       if (m0 < tl.seg_rows[c.g])
-        bf16_gemm_tile<LAYER, false, kTileRows / 2, false, OUT8, false, KEEP>(args, c.g, tl.seg_start[c.g],
-                                                                              tl.seg_rows[c.g], m0, c.nt, lds);
+        bf16_gemm_tile<LAYER, false, kTileRows / 2, false, OUT8>(args, c.g, tl.seg_start[c.g], tl.seg_rows[c.g], m0,
+                                                                 c.nt, lds);
     }
   }
 }
@@ -131,7 +130,7 @@ __global__ __launch_bounds__(kGemmThreads) void grouped_gemm_bf16_kernel(Bf16Gem
 // same static schedule and last-round halves as the kernel above; no split
 // along k.  Every element is computed as in any other tile, so the bits do
 // not change.
-template <int LAYER, bool KEEP = false>
+template <int LAYER>
 __global__ __launch_bounds__(kGemmThreads) void grouped_gemm_bf16_expert_kernel(Bf16GemmArgs args,
                                                                                 const int32_t* __restrict__ offsets,
                                                                                 int G, int xcd_slots,
@@ -159,10 +158,10 @@ __global__ __launch_bounds__(kGemmThreads) void grouped_gemm_bf16_expert_kernel(
     rowpos[threadIdx.x] = expert_row(tl, c.g, EL, S, m0, threadIdx.x);
     __syncthreads();
     if (is_half)
-      bf16_gemm_tile<LAYER, false, kTileRows / 2, false, false, true, KEEP>(args, c.g, 0, n, m0, c.nt, lds, 0, -1,
-                                                                            nullptr, rowpos);
+      bf16_gemm_tile<LAYER, false, kTileRows / 2, false, false, true>(args, c.g, 0, n, m0, c.nt, lds, 0, -1, nullptr,
+                                                                      rowpos);
     else
-      bf16_gemm_row_tile<LAYER, false, false, true, KEEP>(args, c.g, 0, n, m0, c.nt, lds, rowpos);
+      bf16_gemm_row_tile<LAYER, false, false, true>(args, c.g, 0, n, m0, c.nt, lds, rowpos);
   }
 }
 
@@ -399,8 +398,6 @@ hipError_t launch_grouped_gemm_bf16(const GemmProblem& gp, hipStream_t s) {
   a.w0 = (const __bf16*)gp.w0;
   a.w1 = (const __bf16*)gp.w1;
   a.c = gp.c;
-  a.gate = (__bf16*)gp.gate;
-  a.up = (__bf16*)gp.up;
   a.K = gp.K;
   a.N = gp.N;
   a.E = gp.E;
@@ -413,12 +410,9 @@ hipError_t launch_grouped_gemm_bf16(const GemmProblem& gp, hipStream_t s) {
   a.a_scale_bytes = a.w_scale_bytes = 0;
   const int grid = device_cu_count();
   const int xcd_slots = grid / kXcds > 0 ? grid / kXcds : 1;
-  if (gp.rowmap || gp.gate) a.M = gp.R;  // rows of the token-row buffers, read (rowmap) and stored (KEEP) at their own positions
   if (gp.rowmap) {
-    if (gp.gate)
-      grouped_gemm_bf16_expert_kernel<0, true><<<grid, kGemmThreads, 0, s>>>(a, gp.offsets, gp.G, xcd_slots,
-                                                                             gp.shuffle);
-    else if (gp.layer == 0)
+    a.M = gp.R;  // rows of the token-row buffer, read at their own positions
+    if (gp.layer == 0)
       grouped_gemm_bf16_expert_kernel<0><<<grid, kGemmThreads, 0, s>>>(a, gp.offsets, gp.G, xcd_slots, gp.shuffle);
     else
       grouped_gemm_bf16_expert_kernel<1><<<grid, kGemmThreads, 0, s>>>(a, gp.offsets, gp.G, xcd_slots, gp.shuffle);
@@ -432,10 +426,7 @@ hipError_t launch_grouped_gemm_bf16(const GemmProblem& gp, hipStream_t s) {
     sp.desc = sp.hdr + 4;
     sp.part = reinterpret_cast<float*>(w + kSplitHdrBytes);
   }
-  if (gp.gate)
-    grouped_gemm_bf16_kernel<0, false, true><<<grid, kGemmThreads, 0, s>>>(a, gp.offsets, gp.G, xcd_slots, sp,
-                                                                           gp.shuffle);
-  else if (gp.layer == 0)
+  if (gp.layer == 0)
     grouped_gemm_bf16_kernel<0><<<grid, kGemmThreads, 0, s>>>(a, gp.offsets, gp.G, xcd_slots, sp, gp.shuffle);
   else
     grouped_gemm_bf16_kernel<1><<<grid, kGemmThreads, 0, s>>>(a, gp.offsets, gp.G, xcd_slots, sp, gp.shuffle);

@@ -76,16 +76,18 @@ __device__ __forceinline__ void put_desc(const GradGemmArgs& a, int j, const Gra
 }
 
 // ------------------------------------------------------------------- bf16 ---
-// Rows: the experts' rows (over all source blocks) in tiles of 256, or of 128
-// where an expert has no more and in a last round that would leave half the
-// workgroups idle, in the forward queue's order.
+// Rows, and the forward products that are kept: the experts' rows (over all
+// source blocks) in tiles of 256, or of 128 where an expert has no more and in a
+// last round that would leave half the workgroups idle, in the forward queue's
+// order.
 template <GradKind KIND>
 __global__ __launch_bounds__(kGemmThreads) void grad_rows_bf16_kernel(GradGemmArgs a, int xcd_slots) {
   __shared__ __attribute__((aligned(16))) char lds[kGemmLdsBytes];
   __shared__ TileLds tl;
   __shared__ int rowpos[2][kTileRows];  // of this tile and of the next
+  constexpr int TC = KIND == kKeep ? 128 : 256;  // columns of a tile
   const int K = KIND == kGradRows0 ? a.F : a.H, N = KIND == kGradRows0 ? a.H : a.F, S = a.G / a.E;
-  const int NT = (N + 255) / 256;
+  const int NT = (N + TC - 1) / TC;
   const int T = build_expert_tile_table(a.offsets, a.G, a.E, kTileRows, tl) * NT;
   const int64_t panel = (int64_t)kTileRows * K * (KIND == kGradRows0 ? 4 : 2);
   const int grid = gridDim.x;
@@ -111,7 +113,7 @@ __global__ __launch_bounds__(kGemmThreads) void grad_rows_bf16_kernel(GradGemmAr
       const int n = tl.expert_rows[c.g];
       if (m0 >= n) continue;
       rowpos[b][threadIdx.x] = expert_row(tl, c.g, a.E, S, m0, threadIdx.x);
-      t = {uniform(c.g), 0, uniform(c.nt) * 256, 0, 0, 1};
+      t = {uniform(c.g), 0, uniform(c.nt) * TC, 0, 0, 1};
       low = uniform(u >= 0 || n <= kTileRows / 2);
       break;
     }
@@ -145,6 +147,7 @@ __global__ __launch_bounds__(kGemmThreads) void grad_rows_bf16_kernel(GradGemmAr
     else
       run.template operator()<kTileRows>();
   }
+  if constexpr (KIND == kKeep) return;  // (no workspace)
   // a unit of a split tile (a copy of the K loop of its own: with store_part beside the epilogue in one, the compiler
   // spills up to 130 registers a tile)
   const int slot = xcd_slot(blockIdx.x, grid), mine = slot - whole % grid + (slot < whole % grid ? grid : 0);
@@ -733,9 +736,13 @@ hipError_t launch_grad_weights(const GradGemmArgs& a, bool bf16, void* ws, hipSt
   return grad_reduce_launch<kGradWeights, float>(g, s);
 }
 
-hipError_t launch_keep_f32(const GradGemmArgs& a, hipStream_t s) {
+hipError_t launch_keep(const GradGemmArgs& a, bool bf16, hipStream_t s) {
   if (a.R == 0) return hipSuccess;
   const int cus = device_cu_count();
+  if (bf16) {
+    grad_rows_bf16_kernel<kKeep><<<cus, kGemmThreads, 0, s>>>(with_split(a, nullptr), cus / kXcds > 0 ? cus / kXcds : 1);
+    return hipGetLastError();
+  }
   // tiles of 64 x 64 that an even routing gives: below one a CU, the smaller ones
   const int64_t rows = a.all_held ? a.R : a.R / 2, tiles = (rows / 64 + (rows < a.E ? rows : a.E)) * ((a.F + 63) / 64);
   if (tiles < cus)

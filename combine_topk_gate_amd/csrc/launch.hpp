@@ -64,8 +64,6 @@ struct GemmProblem {
   size_t ws_bytes = 0;
   int rowmap = 0;           // bf16: each expert's segments of all source blocks as one (G / E of them)
   uint32_t shuffle = 0;     // nonzero: tiles in a seeded permutation of their order (debug check)
-  void* gate = nullptr;     // layer 0: X W_gate^T and X W_up^T are stored here too, both or neither
-  void* up = nullptr;
 };
 // Workspace that lets the bf16 grouped GEMM split its last round along K.
 size_t gemm_split_ws_bytes();
@@ -131,7 +129,7 @@ struct GradGemmArgs {
   const void* x;   // weights: Hact [R,F] (layer 1) or X_perm [R,H] (layer 0)
   void* o0;        // rows: dgate [R,F] or dX_perm [R,H]; weights: dW_down [E,H,F] or dW_gate [E,F,H]
   void* o1;        // rows, layer 1: dup [R,F]; weights, layer 0: dW_up [E,F,H]
-  void* o2;        // kept products (launch_keep_f32): Hact; o0, o1: gate, up
+  void* o2;        // kept products (launch_keep): Hact; o0, o1: gate, up
   const int32_t* offsets;
   int64_t R;
   int H, F, E, G;  // E: experts held
@@ -145,8 +143,8 @@ struct GradGemmArgs {
 size_t grad_ws_bytes();
 hipError_t launch_grad_rows(const GradGemmArgs& a, bool bf16, void* ws, hipStream_t s);
 hipError_t launch_grad_weights(const GradGemmArgs& a, bool bf16, void* ws, hipStream_t s);
-// f32: gate, up and Hact (o0, o1, o2) of x, w0, w1
-hipError_t launch_keep_f32(const GradGemmArgs& a, hipStream_t s);
+// gate, up and Hact (o0, o1, o2) of x, w0, w1
+hipError_t launch_keep(const GradGemmArgs& a, bool bf16, hipStream_t s);
 
 // Decode layer (at most MOE_DECODE_MAX_TOKENS tokens).
 struct DecodeSplit {
