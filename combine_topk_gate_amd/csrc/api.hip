@@ -422,7 +422,8 @@ size_t moe_workspace_bytes(const moe_problem_t* p, int32_t op) {
     case MOE_OP_DISPATCH: return permute_ws_bytes(plan_of(p));
     case MOE_OP_GROUPED_GEMM: return p->dtype == MOE_DTYPE_BF16 ? gemm_split_ws_bytes() : 0;
     case MOE_OP_LAYER: return layer_ws(p).total;
-    case MOE_OP_GROUPED_GEMM_BACKWARD: return is_mx(p) || p->num_tokens == 0 ? 0 : grad_ws_bytes();
+    case MOE_OP_GROUPED_GEMM_BACKWARD:
+      return is_mx(p) ? 0 : align_up(grad_ws_bytes(grad_args(p, 0, nullptr), p->dtype == MOE_DTYPE_BF16));
     case MOE_OP_LAYER_DECODE: return check_decode(p) == MOE_OK ? decode_ws(p, split_of(p)).total : 0;
   }
   return 0;

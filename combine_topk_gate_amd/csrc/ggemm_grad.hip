@@ -52,6 +52,9 @@ __host__ __device__ inline int split_parts(const SplitCost& c, int r, int nk, in
   }
   return best;
 }
+// ... as far as the workspace's units reach (they do for the rows that the offsets of this problem can have).
+__device__ __forceinline__ int split_within(const GradGemmArgs& a, int s, int r) { return r * s <= a.split.units ? s : 1; }
+
 // Whether an f32 product takes tiles of 128 x 128 (tiles: how many there are)
 // with two groups of waves: from eight rounds of the CUs on, where their padding
 // and the last round's idle CUs weigh little; below, tiles of 64 x 64 with four
@@ -93,7 +96,7 @@ __global__ __launch_bounds__(kGemmThreads) void grad_rows_bf16_kernel(GradGemmAr
   const int grid = gridDim.x;
   // the last round's r tiles: split along K, or cut into two halves of 128 rows, or neither
   const int r = T % grid, steps = (KIND == kGradRows0 ? 2 : 1) * (K / kBK);
-  const int s = a.split.hdr ? split_parts(kSplitBf16, r, steps, grid) : 1;
+  const int s = a.split.hdr ? split_within(a, split_parts(kSplitBf16, r, steps, grid), r) : 1;
   const int cut = s > 1 ? s : (r > 0 && 2 * r <= grid && T > grid) ? 2 : 1;
   const int whole = cut > 1 ? T - r : T, entries = whole + (cut > 1 && s == 1 ? 2 * r : 0);
   const Shuffle sm = make_shuffle(a.shuffle, whole), sh = make_shuffle(a.shuffle, T - whole);
@@ -192,7 +195,8 @@ __global__ __launch_bounds__(kGemmThreads) void grad_weights_bf16_kernel(GradGem
   int s = 1;
   __syncthreads();
   if (a.split.hdr) {
-    s = split_parts(kSplitBf16, r, (offsets[a.G] + a.E * kBK - 1) / (a.E * kBK), grid);  // steps: the experts' mean
+    // steps: the experts' mean
+    s = split_within(a, split_parts(kSplitBf16, r, (offsets[a.G] + a.E * kBK - 1) / (a.E * kBK), grid), r);
     if (blockIdx.x == 0 && threadIdx.x == 0) {
       a.split.hdr[0] = s > 1 ? r : 0;
       a.split.hdr[1] = s;
@@ -345,7 +349,7 @@ __global__ __launch_bounds__(256 * KG) void grad_rows_f32_kernel(GradGemmArgs a)
   const int NT = (N + TX - 1) / TX, S = a.G / a.E, grid = gridDim.x;
   const int T = build_expert_tile_table(a.offsets, a.G, a.E, TX, tl) * NT;
   const int per = K / kGfK, steps = KIND == kGradRows0 ? 2 * per : per;
-  const int r = T % grid, s = a.split.hdr ? split_parts(kSplitF32, r, steps / KG, grid) : 1;
+  const int r = T % grid, s = a.split.hdr ? split_within(a, split_parts(kSplitF32, r, steps / KG, grid), r) : 1;
   const int whole = s > 1 ? T - r : T, entries = whole + (s > 1 ? r * s : 0);
   const Shuffle sm = make_shuffle(a.shuffle, whole), sh = make_shuffle(a.shuffle, T - whole);
   if (a.split.hdr && blockIdx.x == 0 && threadIdx.x == 0) {
@@ -437,7 +441,7 @@ __global__ __launch_bounds__(256 * KG) void grad_weights_f32_kernel(GradGemmArgs
   const int NR = (N + TX - 1) / TX, NC = (C + TX - 1) / TX, S = a.G / a.E, mats = l0 ? 2 : 1, grid = gridDim.x;
   const int T = a.E * mats * NR * NC;
   const int r = T % grid, mean = (offsets[a.G] + a.E * kGfK - 1) / (a.E * kGfK);
-  const int s = a.split.hdr ? split_parts(kSplitF32, r, mean / KG, grid) : 1;
+  const int s = a.split.hdr ? split_within(a, split_parts(kSplitF32, r, mean / KG, grid), r) : 1;
   const int whole = s > 1 ? T - r : T, entries = whole + (s > 1 ? r * s : 0);
   const Shuffle sm = make_shuffle(a.shuffle, whole), sh = make_shuffle(a.shuffle, T - whole);
   if (a.split.hdr && blockIdx.x == 0 && threadIdx.x == 0) {
@@ -651,41 +655,81 @@ __global__ __launch_bounds__(64 * kFewWaves) void keep_f32_few_kernel(GradGemmAr
 }
 
 // ------------------------------------------------------------------ launch ---
-constexpr size_t kGradUnitBytes = 4 * 16 * 4 * 64 * 16;  // of a bf16 unit, the largest
+// How a call splits: the units that its workspace holds (0: no tile is split),
+// by sizes that the host knows.  The number of row tiles of a rows' gradient
+// depends on the routing, between `lo` and `hi`.
+struct GradPlan {
+  int units = 0;
+  bool wide = false;  // f32: tiles of 128
+  size_t unit_bytes = 0;
+  size_t bytes() const { return units ? 256 + (size_t)units * (unit_bytes + kGradDescInts * 4) : 0; }
+};
 
-size_t grad_ws_bytes() { return 256 + (size_t)device_cu_count() * (kGradDescInts * 4 + kGradUnitBytes); }
-
-// The arguments with the workspace's parts, or (ws null) without: no tile is split.
-static GradGemmArgs with_split(const GradGemmArgs& a, void* ws) {
-  GradGemmArgs g = a;
-  g.split = {nullptr, nullptr, nullptr};
-  if (ws) {
-    const size_t cus = device_cu_count();
-    g.split.part = (float*)ws;
-    g.split.desc = (int32_t*)((char*)ws + cus * kGradUnitBytes);
-    g.split.hdr = g.split.desc + cus * kGradDescInts;
-  }
-  return g;
+static GradPlan plan_rows(const GradGemmArgs& a, bool bf16) {
+  GradPlan p;
+  const int cus = device_cu_count(), rows = bf16 ? kTileRows : 64, cols = bf16 ? 256 : 64;
+  const int N = a.layer == 0 ? a.H : a.F, K = a.layer == 0 ? 2 * a.F : a.H, NT = (N + cols - 1) / cols;
+  p.wide = !bf16 && wide_f32(a.R / 128 * ((N + 127) / 128), cus);
+  if (p.wide) return p;
+  const SplitCost& c = bf16 ? kSplitBf16 : kSplitF32;
+  const int steps = bf16 ? K / kBK : K / kGfK / 4;
+  const int64_t hi = a.R / rows + (a.R < a.E ? a.R : a.E), lo = a.all_held ? (a.R + rows - 1) / rows : 0;
+  bool split = false;
+  if (hi - lo > 16)
+    split = split_parts(c, 1, steps, cus) > 1;
+  else
+    for (int64_t mt = lo; mt <= hi && !split; ++mt) split = split_parts(c, (int)(mt * NT % cus), steps, cus) > 1;
+  const int64_t most = hi * NT * (steps / 2);
+  p.units = !split ? 0 : most < cus ? (int)most : cus;
+  p.unit_bytes = bf16 ? 4 * 16 * 4 * 64 * 16 : 4 * 4 * 64 * 16;
+  return p;
 }
 
-// Whether a rows' gradient may split tiles: the number of row tiles depends on
-// the routing, between `lo` and `hi`; the second kernel's launch (about 3 us)
-// is saved where none of a few candidates would split.
-static bool rows_may_split(const SplitCost& c, const GradGemmArgs& a, int rows, int NT, int steps, int grid) {
-  const int64_t hi = a.R / rows + (a.R < a.E ? a.R : a.E), lo = a.all_held ? (a.R + rows - 1) / rows : 0;
-  if (hi - lo > 16) return split_parts(c, 1, steps, grid) > 1;
-  for (int64_t mt = lo; mt <= hi; ++mt)
-    if (split_parts(c, (int)(mt * NT % grid), steps, grid) > 1) return true;
-  return false;
+static GradPlan plan_weights(const GradGemmArgs& a, bool bf16) {
+  GradPlan p;
+  const int cus = device_cu_count(), T = bf16 ? 256 : 64;
+  const int64_t N = a.layer == 0 ? a.F : a.H, C = a.layer == 0 ? a.H : a.F, mats = a.layer == 0 ? 2 : 1;
+  const auto tiles = [&](int t) { return a.E * mats * ((N + t - 1) / t) * ((C + t - 1) / t); };
+  p.wide = !bf16 && wide_f32(tiles(128), cus);
+  if (p.wide) return p;
+  // the experts' mean of steps, if all rows are kept: with fewer a split pays less
+  const int64_t step = a.E * (bf16 ? kBK : 4 * kGfK), mean = (a.R + step - 1) / step, r = tiles(T) % cus;
+  const bool split = split_parts(bf16 ? kSplitBf16 : kSplitF32, (int)r, (int)mean, cus) > 1;
+  p.units = !split ? 0 : r * (mean / 2) < cus ? (int)(r * (mean / 2)) : cus;
+  p.unit_bytes = bf16 ? 4 * 16 * 4 * 64 * 16 : 4 * 4 * 64 * 16;
+  return p;
+}
+
+size_t grad_ws_bytes(const GradGemmArgs& a, bool bf16) {
+  size_t most = 0;
+  GradGemmArgs b = a;
+  for (b.layer = 0; b.layer < 2; ++b.layer) {
+    const size_t rows = plan_rows(b, bf16).bytes(), weights = plan_weights(b, bf16).bytes();
+    most = rows > most ? rows : most;
+    most = weights > most ? weights : most;
+  }
+  return most;
+}
+
+// The arguments with the workspace's parts, or without.
+static GradGemmArgs with_split(const GradGemmArgs& a, const GradPlan& p, void* ws) {
+  GradGemmArgs g = a;
+  g.split = {nullptr, nullptr, nullptr, 0};
+  if (ws && p.units) {
+    g.split.part = (float*)ws;
+    g.split.desc = (int32_t*)((char*)ws + p.units * p.unit_bytes);
+    g.split.hdr = g.split.desc + (size_t)p.units * kGradDescInts;
+    g.split.units = p.units;
+  }
+  return g;
 }
 
 hipError_t launch_grad_rows(const GradGemmArgs& a, bool bf16, void* ws, hipStream_t s) {
   if (a.R == 0) return hipSuccess;
   const int cus = device_cu_count(), xcd_slots = cus / kXcds > 0 ? cus / kXcds : 1;
-  const int N = a.layer == 0 ? a.H : a.F, K = a.layer == 0 ? 2 * a.F : a.H;
+  const GradPlan p = plan_rows(a, bf16);
+  const GradGemmArgs g = with_split(a, p, ws);
   if (bf16) {
-    const bool split = rows_may_split(kSplitBf16, a, kTileRows, (N + 255) / 256, K / kBK, cus);
-    const GradGemmArgs g = with_split(a, split ? ws : nullptr);
     if (a.layer == 0) {
       grad_rows_bf16_kernel<kGradRows0><<<cus, kGemmThreads, 0, s>>>(g, xcd_slots);
       return grad_reduce_launch<kGradRows0, __bf16>(g, s);
@@ -693,15 +737,13 @@ hipError_t launch_grad_rows(const GradGemmArgs& a, bool bf16, void* ws, hipStrea
     grad_rows_bf16_kernel<kGradRows1><<<cus, kGemmThreads, 0, s>>>(g, xcd_slots);
     return grad_reduce_launch<kGradRows1, __bf16>(g, s);
   }
-  if (wide_f32(a.R / 128 * ((N + 127) / 128), cus)) {
+  if (p.wide) {
     if (a.layer == 0)
-      grad_rows_f32_kernel<kGradRows0, 128, 2><<<cus, 512, 0, s>>>(with_split(a, nullptr));
+      grad_rows_f32_kernel<kGradRows0, 128, 2><<<cus, 512, 0, s>>>(g);
     else
-      grad_rows_f32_kernel<kGradRows1, 128, 2><<<cus, 512, 0, s>>>(with_split(a, nullptr));
+      grad_rows_f32_kernel<kGradRows1, 128, 2><<<cus, 512, 0, s>>>(g);
     return hipGetLastError();
   }
-  const bool split = rows_may_split(kSplitF32, a, 64, (N + 63) / 64, K / kGfK / 4, cus);
-  const GradGemmArgs g = with_split(a, split ? ws : nullptr);
   if (a.layer == 0) {
     grad_rows_f32_kernel<kGradRows0, 64, 4><<<cus, 1024, 0, s>>>(g);
     return grad_reduce_launch<kGradRows0, float>(g, s);
@@ -711,24 +753,20 @@ hipError_t launch_grad_rows(const GradGemmArgs& a, bool bf16, void* ws, hipStrea
 }
 
 hipError_t launch_grad_weights(const GradGemmArgs& a, bool bf16, void* ws, hipStream_t s) {
-  const int cus = device_cu_count(), T = bf16 ? 256 : 64;
-  const int64_t N = a.layer == 0 ? a.F : a.H, C = a.layer == 0 ? a.H : a.F, mats = a.layer == 0 ? 2 : 1;
-  const auto tiles = [&](int t) { return a.E * mats * ((N + t - 1) / t) * ((C + t - 1) / t); };
-  // the experts' mean of steps, if all rows are kept: with fewer a split pays less
-  const int64_t step = a.E * (bf16 ? kBK : 4 * kGfK), mean = (a.R + step - 1) / step;
-  const bool split = split_parts(bf16 ? kSplitBf16 : kSplitF32, (int)(tiles(T) % cus), (int)mean, cus) > 1;
-  const GradGemmArgs g = with_split(a, split ? ws : nullptr);
+  const int cus = device_cu_count();
+  const GradPlan p = plan_weights(a, bf16);
+  const GradGemmArgs g = with_split(a, p, ws);
   if (bf16) {
     grad_weights_bf16_kernel<<<cus, kGemmThreads, 0, s>>>(g);
     return grad_reduce_launch<kGradWeights, __bf16>(g, s);
   }
-  if (wide_f32(tiles(128), cus)) {
-    grad_weights_f32_kernel<128, 2><<<cus, 512, 0, s>>>(with_split(a, nullptr));
+  if (p.wide) {
+    grad_weights_f32_kernel<128, 2><<<cus, 512, 0, s>>>(g);
     return hipGetLastError();
   }
   // fewer steps than the groups can share: one group a tile, four workgroups a CU (8 experts 256 x 7680, a row each:
   // 34 us with four groups, 23 with one; 8 experts 256 x 512, 64 rows each: 13.5, 9.4)
-  if (mean < 4 && !split) {
+  if (a.R < 4ll * a.E * 4 * kGfK && !p.units) {
     grad_weights_f32_kernel<64, 1><<<4 * cus, 256, 0, s>>>(g);
     return hipGetLastError();
   }
@@ -740,15 +778,15 @@ hipError_t launch_keep(const GradGemmArgs& a, bool bf16, hipStream_t s) {
   if (a.R == 0) return hipSuccess;
   const int cus = device_cu_count();
   if (bf16) {
-    grad_rows_bf16_kernel<kKeep><<<cus, kGemmThreads, 0, s>>>(with_split(a, nullptr), cus / kXcds > 0 ? cus / kXcds : 1);
+    grad_rows_bf16_kernel<kKeep><<<cus, kGemmThreads, 0, s>>>(with_split(a, GradPlan{}, nullptr), cus / kXcds > 0 ? cus / kXcds : 1);
     return hipGetLastError();
   }
   // tiles of 64 x 64 that an even routing gives: below one a CU, the smaller ones
   const int64_t rows = a.all_held ? a.R : a.R / 2, tiles = (rows / 64 + (rows < a.E ? rows : a.E)) * ((a.F + 63) / 64);
   if (tiles < cus)
-    keep_f32_few_kernel<<<cus, 64 * kFewWaves, 0, s>>>(with_split(a, nullptr));
+    keep_f32_few_kernel<<<cus, 64 * kFewWaves, 0, s>>>(with_split(a, GradPlan{}, nullptr));
   else
-    keep_f32_kernel<<<cus, 512, 0, s>>>(with_split(a, nullptr));
+    keep_f32_kernel<<<cus, 512, 0, s>>>(with_split(a, GradPlan{}, nullptr));
   return hipGetLastError();
 }
 

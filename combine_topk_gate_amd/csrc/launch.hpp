@@ -115,7 +115,8 @@ hipError_t launch_route_backward(const int32_t* idx, const float* w, const float
 struct GradSplit {
   int32_t* hdr;   // {tiles, parts}, for the second kernel
   int32_t* desc;  // per split tile kGradDescInts
-  float* part;    // 256 KiB a unit, at most one unit per CU
+  float* part;    // 256 KiB a bf16 unit, 16 an f32 one; at most one unit per CU
+  int units;      // that it holds
 };
 constexpr int kGradDescInts = 8 + 256;
 struct GradGemmArgs {
@@ -139,8 +140,8 @@ struct GradGemmArgs {
   uint32_t shuffle;
   GradSplit split;
 };
-// Workspace of the split tiles' sums.
-size_t grad_ws_bytes();
+// Workspace of the split tiles' sums, for either layer, rows and weights (R, H, F, E and all_held of a).
+size_t grad_ws_bytes(const GradGemmArgs& a, bool bf16);
 hipError_t launch_grad_rows(const GradGemmArgs& a, bool bf16, void* ws, hipStream_t s);
 hipError_t launch_grad_weights(const GradGemmArgs& a, bool bf16, void* ws, hipStream_t s);
 // gate, up and Hact (o0, o1, o2) of x, w0, w1

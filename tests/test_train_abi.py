@@ -108,7 +108,7 @@ def test_layers_and_their_operands(lib, name):
 def test_workspaces(lib, name):
     op = moe.MOE_OP_GROUPED_GEMM_BACKWARD
     for dtype in ("f32", "bf16"):
-        p = moe.problem(M, H, F, E, k, dtype=dtype)
+        p = moe.problem(60, 448, 8576, 2, 1, dtype=dtype)  # few tiles with long reductions
         need = moe.moe_workspace_bytes(p, op)
         assert need > 0
         assert call(lib, name, problem=p, ws=None) == moe.MOE_ERR_WORKSPACE_TOO_SMALL
@@ -117,6 +117,8 @@ def test_workspaces(lib, name):
         for a in tensors(name):  # no buffer of the call lies in it
             assert call(lib, name, problem=p, ws=at(CALLS[name].index(a))) == INV, a
     assert moe.moe_workspace_bytes(moe.problem(0, H, F, E, k), op) == 0
+    # no tile would be split: none is needed, and one that is given is not looked at
+    assert moe.moe_workspace_bytes(moe.problem(M, H, F, E, k), op) == 0
     assert moe.moe_workspace_bytes(moe.problem(M, H, F, E, k, dtype="bf16_mxfp8"), op) == 0
 
 
