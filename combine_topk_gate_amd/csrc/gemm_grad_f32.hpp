@@ -4,8 +4,8 @@
 // A tile is TX rows x TW columns of the output, computed by KG groups of 4
 // waves (2 x 2, TX/2 x TW/2 each) that take a share of the K steps each: small
 // problems have few tiles with long reductions, and 4 waves a SIMD hide each
-// other's latency (tiny layer, 512 rows of 8 experts 256 x 512: 35 us with
-// one group of 4 waves a tile, see the table of cases).  The columns are the
+// other's latency (layer 0's rows, 512 of 8 experts 256 x 512: 35 us with one
+// group of 4 waves a tile, 21 with four).  The columns are the
 // instruction's first operand, so a lane holds 4 consecutive columns of one
 // row.  K is stepped by 32 through LDS, [k][T] per operand, double-buffered per
 // group, the next step's loads in registers while the current one is

@@ -91,7 +91,7 @@ __global__ __launch_bounds__(kGemmThreads) void grad_rows_bf16_kernel(GradGemmAr
   constexpr int TC = KIND == kKeep ? 128 : 256;  // columns of a tile
   const int K = KIND == kGradRows0 ? a.F : a.H, N = KIND == kGradRows0 ? a.H : a.F, S = a.G / a.E;
   const int NT = (N + TC - 1) / TC;
-  const int T = build_expert_tile_table(a.offsets, a.G, a.E, kTileRows, tl) * NT;
+  const int T = build_expert_tile_table(a.offsets, a.G, a.E, kTileRows, tl, (int)a.R) * NT;
   const int64_t panel = (int64_t)kTileRows * K * (KIND == kGradRows0 ? 4 : 2);
   const int grid = gridDim.x;
   // the last round's r tiles: split along K, or cut into two halves of 128 rows, or neither
@@ -347,7 +347,7 @@ __global__ __launch_bounds__(256 * KG) void grad_rows_f32_kernel(GradGemmArgs a)
   __shared__ int rowpos[TX];
   const int K = KIND == kGradRows0 ? a.F : a.H, N = KIND == kGradRows0 ? a.H : a.F;  // reduction and columns of a product
   const int NT = (N + TX - 1) / TX, S = a.G / a.E, grid = gridDim.x;
-  const int T = build_expert_tile_table(a.offsets, a.G, a.E, TX, tl) * NT;
+  const int T = build_expert_tile_table(a.offsets, a.G, a.E, TX, tl, (int)a.R) * NT;
   const int per = K / kGfK, steps = KIND == kGradRows0 ? 2 * per : per;
   const int r = T % grid, s = a.split.hdr ? split_within(a, split_parts(kSplitF32, r, steps / KG, grid), r) : 1;
   const int whole = s > 1 ? T - r : T, entries = whole + (s > 1 ? r * s : 0);
@@ -362,8 +362,7 @@ __global__ __launch_bounds__(256 * KG) void grad_rows_f32_kernel(GradGemmArgs a)
     const TileCoord c = tile_coord(u >= 0 ? whole + shuffled(sh, j) : shuffled(sm, v), a.E, NT, TX, 1, 0, tl);
     const int e = c.g, col0 = c.nt * TX;
     if (threadIdx.x < TX) {
-      int pos = expert_row(tl, e, a.E, S, c.m0, threadIdx.x);
-      if ((unsigned)pos >= (unsigned)a.R) pos = -1;
+      const int pos = expert_row(tl, e, a.E, S, c.m0, threadIdx.x);
       rowpos[threadIdx.x] = pos;
       if (u >= 0 && part == 0) a.split.desc[(int64_t)j * kGradDescInts + 8 + threadIdx.x] = pos;
     }
@@ -524,16 +523,13 @@ __global__ __launch_bounds__(512) void keep_f32_kernel(GradGemmArgs a) {
   __shared__ TileLds tl;
   __shared__ int rowpos[64];
   const int K = a.H, N = a.F, NT = (N + 63) / 64, S = a.G / a.E;
-  const int T = build_expert_tile_table(a.offsets, a.G, a.E, 64, tl) * NT;
+  const int T = build_expert_tile_table(a.offsets, a.G, a.E, 64, tl, (int)a.R) * NT;
   const Shuffle sm = make_shuffle(a.shuffle, T);
   const int i = threadIdx.x & 255, g = threadIdx.x >> 8;
   for (int v = blockIdx.x; v < T; v += gridDim.x) {
     const TileCoord c = tile_coord(shuffled(sm, v), a.E, NT, 64, 1, 0, tl);
     const int e = c.g, col0 = c.nt * 64;
-    if (threadIdx.x < 64) {
-      const int pos = expert_row(tl, e, a.E, S, c.m0, threadIdx.x);
-      rowpos[threadIdx.x] = (unsigned)pos < (unsigned)a.R ? pos : -1;
-    }
+    if (threadIdx.x < 64) rowpos[threadIdx.x] = expert_row(tl, e, a.E, S, c.m0, threadIdx.x);
     __syncthreads();
     const float* xr[2];
     const float* wr[4];
@@ -571,85 +567,126 @@ __global__ __launch_bounds__(512) void keep_f32_kernel(GradGemmArgs a) {
   }
 }
 
-// ... of few tiles: 32 rows x 32 columns of both, and the block's 8 waves take
-// an eighth of the K steps each, every operand loaded straight into the matrix
-// instruction's layout (lane: row lane % 32, 4 consecutive k of 8), a step ahead,
-// so that there is no barrier before the waves' sums are added (in order) in LDS.
-// Measured (the tiles above, these): 21 rows, one expert of 2112 x 448: 98, 34
+// Rows and kept products of few tiles: 32 rows x 32 columns (keep: of both
+// products), and the block's 8 waves take an eighth of the K steps each, every
+// operand loaded straight into the matrix instruction's layout (k 4 (lane / 32)
+// + 0..3 of 8; x: 16 bytes of row lane % 32; the weights of a rows' gradient: of
+// four rows the column lane % 32), a step ahead, so that there is no barrier
+// before the waves' sums are added (in order) in LDS.
+// Measured (the tiles above, these), keep: 21 rows, one expert of 2112 x 448: 98, 34
 // us; 482 rows, 2304 x 320: 112, 40; 500 rows, 8 experts 2048 x 640: 101, 72.
 constexpr int kFewWaves = 8;
-__global__ __launch_bounds__(64 * kFewWaves) void keep_f32_few_kernel(GradGemmArgs a) {
-  __shared__ __attribute__((aligned(16))) f32x4_t sums[kFewWaves][2][4][64];
+template <GradKind KIND>
+__global__ __launch_bounds__(64 * kFewWaves) void rows_f32_few_kernel(GradGemmArgs a) {
+  constexpr int NP = KIND == kKeep ? 2 : 1;  // products
+  __shared__ __attribute__((aligned(16))) f32x4_t sums[kFewWaves][NP][4][64];
   __shared__ TileLds tl;
-  const int K = a.H, N = a.F, NT = (N + 31) / 32, S = a.G / a.E;
-  const int T = build_expert_tile_table(a.offsets, a.G, a.E, 32, tl) * NT;
+  const int K = KIND == kGradRows0 ? a.F : a.H, N = KIND == kGradRows0 ? a.H : a.F, NT = N / 32, S = a.G / a.E;
+  const int T = build_expert_tile_table(a.offsets, a.G, a.E, 32, tl, (int)a.R) * NT;
   const Shuffle sm = make_shuffle(a.shuffle, T);
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, lrow = lane & 31, lk = lane >> 5;
+  const int per = K / kGfK, steps = KIND == kGradRows0 ? 2 * per : per;
+  const int b = part_begin(steps, wave, kFewWaves), end = part_begin(steps, wave + 1, kFewWaves);
   for (int v = blockIdx.x; v < T; v += gridDim.x) {
     const TileCoord c = tile_coord(shuffled(sm, v), a.E, NT, 32, 1, 0, tl);
-    const int e = c.g, f = c.nt * 32 + lrow, found = expert_row(tl, e, a.E, S, c.m0, lrow);
-    const int pos = (unsigned)found < (unsigned)a.R ? found : -1;
-    // a row or column that the tile lacks: the first row's, whose products are not stored
-    const int64_t wrow = ((int64_t)e * N + (f < N ? f : c.nt * 32)) * K + 4 * lk;
-    const float* src[3] = {(const float*)a.x + (int64_t)(pos >= 0 ? pos : 0) * K + 4 * lk,
-                           (const float*)a.w0 + wrow, (const float*)a.w1 + wrow};
-    const int steps = K / kGfK, b = part_begin(steps, wave, kFewWaves), end = part_begin(steps, wave + 1, kFewWaves);
-    f32x4_t now[3][4], next[3][4];
-    auto load = [&](f32x4_t (&o)[3][4], int s) {
+    const int e = c.g, pos = expert_row(tl, e, a.E, S, c.m0, lrow);
+    // (a row that the tile lacks: the first row, whose products are not stored)
+    const int64_t xat = (int64_t)(pos >= 0 ? pos : 0) * K + 4 * lk;
+    const float* const x0 = (const float*)(KIND == kKeep ? a.x : a.d0) + xat;
+    const float* const x1 = KIND == kGradRows0 ? (const float*)a.d1 + xat : nullptr;
+    const int64_t wat = KIND == kKeep ? ((int64_t)e * N + c.nt * 32 + lrow) * K + 4 * lk
+                                      : ((int64_t)e * K + 4 * lk) * N + c.nt * 32 + lrow;
+    const float* const w0 = (const float*)a.w0 + wat;
+    const float* const w1 = KIND == kGradRows1 ? nullptr : (const float*)a.w1 + wat;
+    f32x4_t nowx[4], noww[NP][4], nextx[4], nextw[NP][4];
+    auto load = [&](f32x4_t (&ox)[4], f32x4_t (&ow)[NP][4], int s) {
+      const bool second = KIND == kGradRows0 && s >= per;
+      const int k = (second ? s - per : s) * kGfK;
+      const float* const x = (second ? x1 : x0) + k;
+      const float* const w = second ? w1 : w0;
 #pragma unroll
-      for (int u = 0; u < 4; ++u)
+      for (int u = 0; u < 4; ++u) {
+        ox[u] = *reinterpret_cast<const f32x4_t*>(x + 8 * u);
+        if constexpr (KIND == kKeep) {
+          ow[0][u] = *reinterpret_cast<const f32x4_t*>(w0 + k + 8 * u);
+          ow[1][u] = *reinterpret_cast<const f32x4_t*>(w1 + k + 8 * u);
+        } else {
 #pragma unroll
-        for (int m = 0; m < 3; ++m) o[m][u] = *reinterpret_cast<const f32x4_t*>(src[m] + s * kGfK + 8 * u);
+          for (int h = 0; h < 4; ++h) ow[0][u][h] = w[(int64_t)(k + 8 * u + h) * N];
+        }
+      }
     };
-    f32x16_t acc[2], sum[2];
+    f32x16_t acc[NP], sum[NP];
 #pragma unroll
-    for (int m = 0; m < 2; ++m)
+    for (int m = 0; m < NP; ++m)
 #pragma unroll
       for (int h = 0; h < 16; ++h) acc[m][h] = sum[m][h] = 0.f;
-    if (b < end) load(now, b);
+    if (b < end) load(nowx, noww, b);
     for (int s = b; s < end; ++s) {
-      load(next, s + 1 < end ? s + 1 : s);
+      load(nextx, nextw, s + 1 < end ? s + 1 : s);
 #pragma unroll
       for (int u = 0; u < 4; ++u)
 #pragma unroll
         for (int h = 0; h < 4; ++h)
 #pragma unroll
-          for (int m = 0; m < 2; ++m)
-            acc[m] = __builtin_amdgcn_mfma_f32_32x32x2f32(now[1 + m][u][h], now[0][u][h], acc[m], 0, 0, 0);
+          for (int m = 0; m < NP; ++m)
+            acc[m] = __builtin_amdgcn_mfma_f32_32x32x2f32(noww[m][u][h], nowx[u][h], acc[m], 0, 0, 0);
       if ((s - b) % kGfFlush == kGfFlush - 1 || s + 1 == end) {
 #pragma unroll
-        for (int m = 0; m < 2; ++m) {
+        for (int m = 0; m < NP; ++m) {
           sum[m] += acc[m];
 #pragma unroll
           for (int h = 0; h < 16; ++h) acc[m][h] = 0.f;
         }
       }
 #pragma unroll
-      for (int m = 0; m < 3; ++m)
+      for (int u = 0; u < 4; ++u) {
+        nowx[u] = nextx[u];
 #pragma unroll
-        for (int u = 0; u < 4; ++u) now[m][u] = next[m][u];
+        for (int m = 0; m < NP; ++m) noww[m][u] = nextw[m][u];
+      }
+    }
+    const int q = wave, n = c.nt * 32 + 8 * q + 4 * lk;
+    const bool stores = q < 4 && pos >= 0;
+    const int64_t at = (int64_t)pos * N + n;
+    f32x4_t gv{}, uv{};
+    if (KIND == kGradRows1 && stores) {
+      gv = *(const f32x4_t*)((const float*)a.gate + at);
+      uv = *(const f32x4_t*)((const float*)a.up + at);
     }
     __syncthreads();  // the sums of the tile before are read
 #pragma unroll
-    for (int m = 0; m < 2; ++m)
+    for (int m = 0; m < NP; ++m)
 #pragma unroll
-      for (int q = 0; q < 4; ++q)
-        sums[wave][m][q][lane] = f32x4_t{sum[m][4 * q], sum[m][4 * q + 1], sum[m][4 * q + 2], sum[m][4 * q + 3]};
+      for (int h = 0; h < 4; ++h)
+        sums[wave][m][h][lane] = f32x4_t{sum[m][4 * h], sum[m][4 * h + 1], sum[m][4 * h + 2], sum[m][4 * h + 3]};
     __syncthreads();
-    const int q = wave, n = c.nt * 32 + 8 * q + 4 * lk;
-    if (q < 4 && pos >= 0 && n < N) {
-      f32x4_t o[2] = {};
+    if (stores) {
+      f32x4_t o[NP] = {};
 #pragma unroll
-      for (int m = 0; m < 2; ++m)
+      for (int m = 0; m < NP; ++m)
 #pragma unroll
         for (int w = 0; w < kFewWaves; ++w) o[m] += sums[w][m][q][lane];
-      const int64_t at = (int64_t)pos * N + n;
-      f32x4_t h;
+      if constexpr (KIND == kGradRows0) {
+        gf_store4((float*)a.o0 + at, o[0]);
+      } else if constexpr (KIND == kGradRows1) {
+        f32x4_t dg, du;
 #pragma unroll
-      for (int u = 0; u < 4; ++u) h[u] = silu_f32(o[0][u]) * o[1][u];
-      gf_store4((float*)a.o0 + at, o[0]);
-      gf_store4((float*)a.o1 + at, o[1]);
-      gf_store4((float*)a.o2 + at, h);
+        for (int u = 0; u < 4; ++u) {
+          const SwigluGrad d = swiglu_grad(o[0][u], gv[u], uv[u]);
+          dg[u] = d.dg;
+          du[u] = d.du;
+        }
+        gf_store4((float*)a.o0 + at, dg);
+        gf_store4((float*)a.o1 + at, du);
+      } else {
+        f32x4_t h;
+#pragma unroll
+        for (int u = 0; u < 4; ++u) h[u] = silu_f32(o[0][u]) * o[1][u];
+        gf_store4((float*)a.o0 + at, o[0]);
+        gf_store4((float*)a.o1 + at, o[1]);
+        gf_store4((float*)a.o2 + at, h);
+      }
     }
   }
 }
@@ -784,7 +821,7 @@ hipError_t launch_keep(const GradGemmArgs& a, bool bf16, hipStream_t s) {
   // tiles of 64 x 64 that an even routing gives: below one a CU, the smaller ones
   const int64_t rows = a.all_held ? a.R : a.R / 2, tiles = (rows / 64 + (rows < a.E ? rows : a.E)) * ((a.F + 63) / 64);
   if (tiles < cus)
-    keep_f32_few_kernel<<<cus, 64 * kFewWaves, 0, s>>>(with_split(a, GradPlan{}, nullptr));
+    rows_f32_few_kernel<kKeep><<<cus, 64 * kFewWaves, 0, s>>>(with_split(a, GradPlan{}, nullptr));
   else
     keep_f32_kernel<<<cus, 512, 0, s>>>(with_split(a, GradPlan{}, nullptr));
   return hipGetLastError();

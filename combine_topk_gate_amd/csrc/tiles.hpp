@@ -71,43 +71,42 @@ __device__ inline int build_tile_table(const int32_t* __restrict__ offsets, int 
 // rows of several small segments of the same expert and every weight panel
 // serves full tiles.  Fills seg_start and seg_rows of the G segments,
 // expert_rows[e] and mt_start[e] (prefix of the experts' M-tile counts);
-// returns the number of M-tiles.  All threads of the block call it.
+// returns the number of M-tiles.  The segments are kept inside rows 0 .. R - 1,
+// whatever the offsets say.  All threads of the block call it.
 __device__ inline int build_expert_tile_table(const int32_t* __restrict__ offsets, int G, int EL, int rows,
-                                              TileLds& t) {
-  const int nthr = min((int)blockDim.x, 256);  // those that scan
+                                              TileLds& t, int R = 0x7FFFFFFF) {
   for (int g = threadIdx.x; g < G; g += blockDim.x) {
-    t.seg_start[g] = offsets[g];
-    t.seg_rows[g] = offsets[g + 1] - offsets[g];
+    const int a = min(max(offsets[g], 0), R), b = min(max(offsets[g + 1], a), R);
+    t.seg_start[g] = a;
+    t.seg_rows[g] = b - a;
   }
   __syncthreads();
-  const int S = G / EL;
-  const int per = (EL + nthr - 1) / nthr;
-  const int e0 = threadIdx.x * per;
-  int run = 0;
-  for (int e = e0; e < e0 + per && e < EL; ++e) {
-    int n = 0;
-    for (int s = 0; s < S; ++s) n += t.seg_rows[s * EL + e];
-    t.expert_rows[e] = n;
-    run += (n + rows - 1) / rows;
+  // the first wave counts and scans: a lane's experts are `per` consecutive ones
+  if (threadIdx.x < kWave) {
+    const int S = G / EL, lane = threadIdx.x;
+    const int per = (EL + kWave - 1) / kWave, e0 = lane * per;
+    int run = 0;
+    for (int e = e0; e < e0 + per && e < EL; ++e) {
+      int n = 0;
+      for (int s = 0; s < S; ++s) n += t.seg_rows[s * EL + e];
+      t.expert_rows[e] = n;
+      run += (n + rows - 1) / rows;
+    }
+    int acc = run;
+#pragma unroll
+    for (int off = 1; off < kWave; off <<= 1) {
+      const int v = __shfl_up(acc, off);
+      if (lane >= off) acc += v;
+    }
+    if (lane == kWave - 1) t.mt_start[EL] = acc;
+    acc -= run;
+    for (int e = e0; e < e0 + per && e < EL; ++e) {
+      t.mt_start[e] = acc;
+      acc += (t.expert_rows[e] + rows - 1) / rows;
+    }
   }
-  const bool scans = (int)threadIdx.x < nthr;
-  if (scans) t.scratch[threadIdx.x] = run;
   __syncthreads();
-  for (int off = 1; off < nthr; off <<= 1) {
-    const int v = scans && threadIdx.x >= (unsigned)off ? t.scratch[threadIdx.x - off] : 0;
-    __syncthreads();
-    if (scans) t.scratch[threadIdx.x] += v;
-    __syncthreads();
-  }
-  int acc = scans ? t.scratch[threadIdx.x] - run : 0;
-  for (int e = e0; e < e0 + per && e < EL; ++e) {
-    t.mt_start[e] = acc;
-    acc += (t.expert_rows[e] + rows - 1) / rows;
-  }
-  const int total = t.scratch[nthr - 1];
-  if (threadIdx.x == 0) t.mt_start[EL] = total;
-  __syncthreads();
-  return total;
+  return t.mt_start[EL];
 }
 
 // Sorted row of row m0 + i (i < n) of expert e's combined segment, -1 past

@@ -12,6 +12,8 @@
  *   layer     all of the above in one persistent kernel: one ordered work
  *             queue of Layer0 tiles, Layer1 tiles and combine items, with
  *             ready counters between them
+ *   training  the gradient of each step, the forward steps as training needs
+ *             them (dropout on the output, gate and up kept)
  *
  * Sources (cited by page and section):
  *   [COMET]  "COMET: Fine-grained Computation-communication Overlapping for
