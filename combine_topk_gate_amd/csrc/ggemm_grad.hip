@@ -513,106 +513,65 @@ __global__ __launch_bounds__(256 * KG) void grad_weights_f32_kernel(GradGemmArgs
   }
 }
 
-// The forward gate and up products, kept: tiles of 64 rows x 64 columns of both
-// (128 weight rows, those of a wave 32 of gate and the same 32 of up, so a lane
-// has both of an element).
-__global__ __launch_bounds__(512) void keep_f32_kernel(GradGemmArgs a) {
-  constexpr int KG = 2;
-  typedef GfTile<64, 128, KG> Tile;
-  __shared__ __attribute__((aligned(16))) float lds[Tile::kLds];
-  __shared__ TileLds tl;
-  __shared__ int rowpos[64];
-  const int K = a.H, N = a.F, NT = (N + 63) / 64, S = a.G / a.E;
-  const int T = build_expert_tile_table(a.offsets, a.G, a.E, 64, tl, (int)a.R) * NT;
-  const Shuffle sm = make_shuffle(a.shuffle, T);
-  const int i = threadIdx.x & 255, g = threadIdx.x >> 8;
-  for (int v = blockIdx.x; v < T; v += gridDim.x) {
-    const TileCoord c = tile_coord(shuffled(sm, v), a.E, NT, 64, 1, 0, tl);
-    const int e = c.g, col0 = c.nt * 64;
-    if (threadIdx.x < 64) rowpos[threadIdx.x] = expert_row(tl, e, a.E, S, c.m0, threadIdx.x);
-    __syncthreads();
-    const float* xr[2];
-    const float* wr[4];
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const int pos = rowpos[(i >> 3) + 32 * h];
-      xr[h] = pos >= 0 ? (const float*)a.x + (int64_t)pos * K : nullptr;
-    }
-#pragma unroll
-    for (int h = 0; h < 4; ++h) {  // weight rows 32 h ..: gate, up of the first 32 columns, of the second
-      const int f = col0 + (h >> 1) * 32 + (i >> 3);
-      wr[h] = f < N ? (const float*)(h & 1 ? a.w1 : a.w0) + ((int64_t)e * N + f) * K : nullptr;
-    }
-    const int steps = K / kGfK, b = part_begin(steps, g, KG), end = part_begin(steps, g + 1, KG);
-    GfPart<128> pw;
-    GfPart<64> px;
-    auto load = [&](int at) {
-      px.load_k(xr, (b + at) * kGfK, i);
-      pw.load_k(wr, (b + at) * kGfK, i);
-    };
-    Tile tile;
-    tile.run(lds, end - b, (steps + KG - 1) / KG, load, [&](float* l) { px.store_k(l, i); }, [&](float* l) { pw.store_k(l, i); });
-    tile.each(lds, [&](int fj, int q, f32x4_t (&o)[2]) {
-      const int pos = rowpos[Tile::row(fj)], f = col0 + ((i >> 6) & 1) * 32 + 8 * q + 4 * ((i & 63) >> 5);
-      if (pos < 0 || f >= N) return;
-      const int64_t at = (int64_t)pos * N + f;
-      f32x4_t h;
-#pragma unroll
-      for (int u = 0; u < 4; ++u) h[u] = silu_f32(o[0][u]) * o[1][u];
-      gf_store4((float*)a.o0 + at, o[0]);
-      gf_store4((float*)a.o1 + at, o[1]);
-      gf_store4((float*)a.o2 + at, h);
-    });
-    __syncthreads();
-  }
-}
-
-// Rows and kept products of few tiles: 32 rows x 32 columns (keep: of both
-// products), and the block's 8 waves take an eighth of the K steps each, every
-// operand loaded straight into the matrix instruction's layout (k 4 (lane / 32)
-// + 0..3 of 8; x: 16 bytes of row lane % 32; the weights of a rows' gradient: of
-// four rows the column lane % 32), a step ahead, so that there is no barrier
-// before the waves' sums are added (in order) in LDS.
-// Measured (the tiles above, these), keep: 21 rows, one expert of 2112 x 448: 98, 34
-// us; 482 rows, 2304 x 320: 112, 40; 500 rows, 8 experts 2048 x 640: 101, 72.
-constexpr int kFewWaves = 8;
-template <GradKind KIND>
-__global__ __launch_bounds__(64 * kFewWaves) void rows_f32_few_kernel(GradGemmArgs a) {
-  constexpr int NP = KIND == kKeep ? 2 : 1;  // products
-  __shared__ __attribute__((aligned(16))) f32x4_t sums[kFewWaves][NP][4][64];
+// The kept products, and the rows' gradients of small problems: tiles of 32 rows
+// x 32 columns (keep: of both products), each wave a part of the K steps, loaded
+// one ahead, so that there is no barrier before the waves' sums are added (in order)
+// in LDS, and the waves of several blocks a CU hide each other's latency.  What
+// lies along k (x, and keep's weights) is loaded as whole lines (8 lanes a row)
+// and turned by the wave in LDS of its own; loaded as the matrix instruction takes
+// it, neighbouring lanes different rows, it comes at a third of the rate (keep, 250
+// tokens, 8 experts 2048 x 640, top 2: 53 us, loaded so 74).  The weights of a rows'
+// gradient lie as the instruction takes them.
+template <GradKind KIND, int WAVES>
+__global__ __launch_bounds__(64 * WAVES) void wave_f32_kernel(GradGemmArgs a) {
+  constexpr bool KEEP = KIND == kKeep;
+  constexpr int NP = KEEP ? 2 : 1;               // products
+  constexpr int kRegion = NP * 256;  // a wave's: 4 KiB for the operands in turn, then NP x 4 KiB of sums
+  __shared__ __attribute__((aligned(16))) f32x4_t lds[WAVES][kRegion];
   __shared__ TileLds tl;
   const int K = KIND == kGradRows0 ? a.F : a.H, N = KIND == kGradRows0 ? a.H : a.F, NT = N / 32, S = a.G / a.E;
   const int T = build_expert_tile_table(a.offsets, a.G, a.E, 32, tl, (int)a.R) * NT;
   const Shuffle sm = make_shuffle(a.shuffle, T);
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, lrow = lane & 31, lk = lane >> 5;
+  const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6), lrow = lane & 31, lk = lane >> 5;
+  const int lr = lane >> 3, lc = lane & 7;  // of the line loads: rows lr + 8 i, values 4 lc .. 4 lc + 3
   const int per = K / kGfK, steps = KIND == kGradRows0 ? 2 * per : per;
-  const int b = part_begin(steps, wave, kFewWaves), end = part_begin(steps, wave + 1, kFewWaves);
+  const int b = part_begin(steps, wave, WAVES), end = part_begin(steps, wave + 1, WAVES);
+  f32x4_t* const mine = lds[wave];
+  // 32 rows x 32 k (a wave's LDS accesses are done in order): 16-byte chunk c of row r at c ^ (r % 8)
+  auto turn = [&](const f32x4_t (&v)[4], f32x4_t (&o)[4]) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) mine[(lr + 8 * i) * 8 + (lc ^ lr)] = v[i];
+#pragma unroll
+    for (int u = 0; u < 4; ++u) o[u] = mine[lrow * 8 + ((2 * u + lk) ^ (lrow & 7))];
+  };
   for (int v = blockIdx.x; v < T; v += gridDim.x) {
     const TileCoord c = tile_coord(shuffled(sm, v), a.E, NT, 32, 1, 0, tl);
-    const int e = c.g, pos = expert_row(tl, e, a.E, S, c.m0, lrow);
-    // (a row that the tile lacks: the first row, whose products are not stored)
-    const int64_t xat = (int64_t)(pos >= 0 ? pos : 0) * K + 4 * lk;
-    const float* const x0 = (const float*)(KIND == kKeep ? a.x : a.d0) + xat;
-    const float* const x1 = KIND == kGradRows0 ? (const float*)a.d1 + xat : nullptr;
-    const int64_t wat = KIND == kKeep ? ((int64_t)e * N + c.nt * 32 + lrow) * K + 4 * lk
-                                      : ((int64_t)e * K + 4 * lk) * N + c.nt * 32 + lrow;
-    const float* const w0 = (const float*)a.w0 + wat;
-    const float* const w1 = KIND == kGradRows1 ? nullptr : (const float*)a.w1 + wat;
-    f32x4_t nowx[4], noww[NP][4], nextx[4], nextw[NP][4];
+    const int e = uniform(c.g), n0 = uniform(c.nt) * 32, pos = expert_row(tl, e, a.E, S, c.m0, lrow);
+    // lanes' places in the operands (R times a row is below 2^31); a row that the tile lacks: the first one, not stored
+    int xat[4], wat[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      xat[i] = max(__shfl(pos, lr + 8 * i), 0) * K + 4 * lc;
+      wat[i] = (lr + 8 * i) * K + 4 * lc;
+    }
+    const int64_t wbase = KEEP ? ((int64_t)e * N + n0) * K : ((int64_t)e * K + 4 * lk) * N + n0 + lrow;
+    const float* const w0 = (const float*)a.w0 + wbase;
+    const float* const w1 = KIND == kGradRows1 ? nullptr : (const float*)a.w1 + wbase;
+    f32x4_t xv[4], wv[NP][4], nextx[4], nextw[NP][4];
     auto load = [&](f32x4_t (&ox)[4], f32x4_t (&ow)[NP][4], int s) {
       const bool second = KIND == kGradRows0 && s >= per;
       const int k = (second ? s - per : s) * kGfK;
-      const float* const x = (second ? x1 : x0) + k;
-      const float* const w = second ? w1 : w0;
+      const float* const x = (const float*)(KEEP ? a.x : second ? a.d1 : a.d0) + k;
+      const float* const w = (second ? w1 : w0) + (KEEP ? k : (int64_t)k * N);
 #pragma unroll
-      for (int u = 0; u < 4; ++u) {
-        ox[u] = *reinterpret_cast<const f32x4_t*>(x + 8 * u);
-        if constexpr (KIND == kKeep) {
-          ow[0][u] = *reinterpret_cast<const f32x4_t*>(w0 + k + 8 * u);
-          ow[1][u] = *reinterpret_cast<const f32x4_t*>(w1 + k + 8 * u);
+      for (int i = 0; i < 4; ++i) {
+        ox[i] = *reinterpret_cast<const f32x4_t*>(x + xat[i]);
+        if constexpr (KEEP) {
+          ow[0][i] = *reinterpret_cast<const f32x4_t*>(w + wat[i]);
+          ow[1][i] = *reinterpret_cast<const f32x4_t*>(w1 + k + wat[i]);
         } else {
 #pragma unroll
-          for (int h = 0; h < 4; ++h) ow[0][u][h] = w[(int64_t)(k + 8 * u + h) * N];
+          for (int h = 0; h < 4; ++h) ow[0][i][h] = w[(int64_t)(8 * i + h) * N];
         }
       }
     };
@@ -621,16 +580,22 @@ __global__ __launch_bounds__(64 * kFewWaves) void rows_f32_few_kernel(GradGemmAr
     for (int m = 0; m < NP; ++m)
 #pragma unroll
       for (int h = 0; h < 16; ++h) acc[m][h] = sum[m][h] = 0.f;
-    if (b < end) load(nowx, noww, b);
+    if (b < end) load(xv, wv, b);
     for (int s = b; s < end; ++s) {
-      load(nextx, nextw, s + 1 < end ? s + 1 : s);
+      load(nextx, nextw, min(s + 1, end - 1));  // (with a branch here the loads are waited for at once)
+      f32x4_t fx[4], fw[NP][4];
+      turn(xv, fx);
+      if constexpr (KEEP) {
+        turn(wv[0], fw[0]);
+        turn(wv[1], fw[1]);
+      }
 #pragma unroll
       for (int u = 0; u < 4; ++u)
 #pragma unroll
         for (int h = 0; h < 4; ++h)
 #pragma unroll
           for (int m = 0; m < NP; ++m)
-            acc[m] = __builtin_amdgcn_mfma_f32_32x32x2f32(noww[m][u][h], nowx[u][h], acc[m], 0, 0, 0);
+            acc[m] = __builtin_amdgcn_mfma_f32_32x32x2f32(KEEP ? fw[m][u][h] : wv[m][u][h], fx[u][h], acc[m], 0, 0, 0);
       if ((s - b) % kGfFlush == kGfFlush - 1 || s + 1 == end) {
 #pragma unroll
         for (int m = 0; m < NP; ++m) {
@@ -641,12 +606,12 @@ __global__ __launch_bounds__(64 * kFewWaves) void rows_f32_few_kernel(GradGemmAr
       }
 #pragma unroll
       for (int u = 0; u < 4; ++u) {
-        nowx[u] = nextx[u];
+        xv[u] = nextx[u];
 #pragma unroll
-        for (int m = 0; m < NP; ++m) noww[m][u] = nextw[m][u];
+        for (int m = 0; m < NP; ++m) wv[m][u] = nextw[m][u];
       }
     }
-    const int q = wave, n = c.nt * 32 + 8 * q + 4 * lk;
+    const int q = wave, n = n0 + 8 * q + 4 * lk;
     const bool stores = q < 4 && pos >= 0;
     const int64_t at = (int64_t)pos * N + n;
     f32x4_t gv{}, uv{};
@@ -654,19 +619,18 @@ __global__ __launch_bounds__(64 * kFewWaves) void rows_f32_few_kernel(GradGemmAr
       gv = *(const f32x4_t*)((const float*)a.gate + at);
       uv = *(const f32x4_t*)((const float*)a.up + at);
     }
-    __syncthreads();  // the sums of the tile before are read
 #pragma unroll
     for (int m = 0; m < NP; ++m)
 #pragma unroll
       for (int h = 0; h < 4; ++h)
-        sums[wave][m][h][lane] = f32x4_t{sum[m][4 * h], sum[m][4 * h + 1], sum[m][4 * h + 2], sum[m][4 * h + 3]};
+        mine[(m * 4 + h) * 64 + lane] = f32x4_t{sum[m][4 * h], sum[m][4 * h + 1], sum[m][4 * h + 2], sum[m][4 * h + 3]};
     __syncthreads();
     if (stores) {
       f32x4_t o[NP] = {};
 #pragma unroll
       for (int m = 0; m < NP; ++m)
 #pragma unroll
-        for (int w = 0; w < kFewWaves; ++w) o[m] += sums[w][m][q][lane];
+        for (int w = 0; w < WAVES; ++w) o[m] += lds[w][(m * 4 + q) * 64 + lane];
       if constexpr (KIND == kGradRows0) {
         gf_store4((float*)a.o0 + at, o[0]);
       } else if constexpr (KIND == kGradRows1) {
@@ -688,6 +652,7 @@ __global__ __launch_bounds__(64 * kFewWaves) void rows_f32_few_kernel(GradGemmAr
         gf_store4((float*)a.o2 + at, h);
       }
     }
+    __syncthreads();  // the sums are read before the next tile's lines
   }
 }
 
@@ -698,16 +663,46 @@ __global__ __launch_bounds__(64 * kFewWaves) void rows_f32_few_kernel(GradGemmAr
 struct GradPlan {
   int units = 0;
   bool wide = false;  // f32: tiles of 128
+  bool wave = false;  // ... of 32
   size_t unit_bytes = 0;
   size_t bytes() const { return units ? 256 + (size_t)units * (unit_bytes + kGradDescInts * 4) : 0; }
 };
+
+// Tiles of 32 x 32 that an even routing gives, N columns wide.
+static int64_t wave_tiles(const GradGemmArgs& a, int N) {
+  const int64_t rows = a.all_held ? a.R : a.R / 2;
+  return (rows / 32 + (rows < a.E ? rows : a.E)) * (N / 32);
+}
+// The kept products take them always (tiles of 64 x 64 of both products through
+// common LDS buffers, these: 256 tokens, 8 experts 256 x 512, top 2: 18.8, 11.9
+// us; 1024, 4 of 2048 x 2048, top 1: 293, 204; 4096 tokens there: 874, 714), rows'
+// gradients for eight rounds of the CUs and sums of 2048 terms; longer ones are cut
+// into parts in the tiles of 64, which also read less.  Measured (tiles of 64,
+// these), layer 0: 256 tokens, 8 of 256 x 512, top 2 (192 tiles): 19.8, 11.8; 2000, 8
+// of 512 x 512 (2128): 69, 67; 4096, 8 of 2048 x 1024 (16896): 770, 938; 64, 2 of
+// 1024 x 4096, top 1 (8192 terms): 37, 57; layer 1: 512, 8 of 256 x 512, top 2 (640):
+// 14.4, 12.3; 100, 4 of 4096 x 576, top 1 (4096 terms): 32.9, 31.9.
+static bool wave_rows(const GradGemmArgs& a, int N, int K, int cus) { return wave_tiles(a, N) <= 8 * cus && K <= 2048; }
+// Up to a tile a CU 8 waves share one, above 4 (8, 4): layer 0's rows above 11.8,
+// 13.1 us; 512 tokens there (320 tiles): 20.5, 18.8; kept, 21 rows, one of 2112 x 448:
+// 28, 30; 500, 8 of 1024 x 1024: 73, 61.
+template <GradKind KIND>
+static hipError_t launch_wave(const GradGemmArgs& g, int N, hipStream_t s) {
+  const int cus = device_cu_count();
+  if (wave_tiles(g, N) <= cus)
+    wave_f32_kernel<KIND, 8><<<cus, 512, 0, s>>>(g);
+  else  // (keep, three blocks a CU: 4096 tokens of 4 experts 2048 x 2048 728 us, two 714)
+    wave_f32_kernel<KIND, 4><<<(KIND == kKeep ? 2 : 4) * cus, 256, 0, s>>>(g);
+  return hipGetLastError();
+}
 
 static GradPlan plan_rows(const GradGemmArgs& a, bool bf16) {
   GradPlan p;
   const int cus = device_cu_count(), rows = bf16 ? kTileRows : 64, cols = bf16 ? 256 : 64;
   const int N = a.layer == 0 ? a.H : a.F, K = a.layer == 0 ? 2 * a.F : a.H, NT = (N + cols - 1) / cols;
   p.wide = !bf16 && wide_f32(a.R / 128 * ((N + 127) / 128), cus);
-  if (p.wide) return p;
+  p.wave = !bf16 && wave_rows(a, N, K, cus);
+  if (p.wide || p.wave) return p;
   const SplitCost& c = bf16 ? kSplitBf16 : kSplitF32;
   const int steps = bf16 ? K / kBK : K / kGfK / 4;
   const int64_t hi = a.R / rows + (a.R < a.E ? a.R : a.E), lo = a.all_held ? (a.R + rows - 1) / rows : 0;
@@ -781,6 +776,7 @@ hipError_t launch_grad_rows(const GradGemmArgs& a, bool bf16, void* ws, hipStrea
       grad_rows_f32_kernel<kGradRows1, 128, 2><<<cus, 512, 0, s>>>(g);
     return hipGetLastError();
   }
+  if (p.wave) return a.layer == 0 ? launch_wave<kGradRows0>(g, a.H, s) : launch_wave<kGradRows1>(g, a.F, s);
   if (a.layer == 0) {
     grad_rows_f32_kernel<kGradRows0, 64, 4><<<cus, 1024, 0, s>>>(g);
     return grad_reduce_launch<kGradRows0, float>(g, s);
@@ -818,13 +814,7 @@ hipError_t launch_keep(const GradGemmArgs& a, bool bf16, hipStream_t s) {
     grad_rows_bf16_kernel<kKeep><<<cus, kGemmThreads, 0, s>>>(with_split(a, GradPlan{}, nullptr), cus / kXcds > 0 ? cus / kXcds : 1);
     return hipGetLastError();
   }
-  // tiles of 64 x 64 that an even routing gives: below one a CU, the smaller ones
-  const int64_t rows = a.all_held ? a.R : a.R / 2, tiles = (rows / 64 + (rows < a.E ? rows : a.E)) * ((a.F + 63) / 64);
-  if (tiles < cus)
-    rows_f32_few_kernel<kKeep><<<cus, 64 * kFewWaves, 0, s>>>(with_split(a, GradPlan{}, nullptr));
-  else
-    keep_f32_kernel<<<cus, 512, 0, s>>>(with_split(a, GradPlan{}, nullptr));
-  return hipGetLastError();
+  return launch_wave<kKeep>(with_split(a, GradPlan{}, nullptr), a.F, s);
 }
 
 }  // namespace moe

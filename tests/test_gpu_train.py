@@ -480,7 +480,8 @@ def test_infinities_and_nan_stay_in_their_row_or_column(dtype):
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
-@pytest.mark.parametrize("shape", [dict(M=600, H=320, F=448, E=6, k=2, S=2), dict(M=900, H=256, F=576, E=3, k=2)])
+@pytest.mark.parametrize("shape", [dict(M=600, H=320, F=448, E=6, k=2, S=2), dict(M=900, H=256, F=576, E=3, k=2),
+                                   dict(M=70, H=2176, F=2112, E=2, k=1)])
 def test_order_does_not_change_a_bit(shape, dtype):
     prob, d, ws = experts(**shape, dtype=dtype, seed=4)
     first = run_all(prob, d, ws)
