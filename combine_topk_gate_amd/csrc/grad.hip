@@ -92,6 +92,28 @@ inline unsigned token_blocks(int64_t M, int tpt) {
   return (unsigned)(n < 16384 ? n : 16384);
 }
 
+// A token's pairs, for waves that own one token each: lane j has pair j's row and
+// weight, and only those held are gone through, in slot order (a share of an
+// expert-parallel layer holds few: 16 of 128 experts, 4096 tokens of 7168, 8 pairs
+// each, all gone through and so: combine with dropout 76, 52 us, its gradient 78,
+// 50, the dispatch's 41, 32).
+struct TokenPairs {
+  int32_t row;  // of lane j
+  float w;
+  uint32_t held;  // bit j
+
+  __device__ __forceinline__ TokenPairs(const int32_t* f2s, const float* weights, int64_t t, int k, int64_t R) {
+    const int lane = threadIdx.x % kWave;
+    row = lane < k ? f2s[t * k + lane] : -1;
+    w = weights && lane < k ? weights[t * k + lane] : 1.f;
+    held = (uint32_t)__ballot(pair_held(row, R));
+  }
+  __device__ __forceinline__ int32_t row_of(int j) const { return __builtin_amdgcn_readlane(row, j); }
+  __device__ __forceinline__ float w_of(int j) const {
+    return __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, w), j));
+  }
+};
+
 // ---------------------------------------------------------- rows to tokens ---
 // Forward combine with dropout (SRC f32, weights w, DROP) and the dispatch's
 // gradient (SRC the problem's type): the sum over the token's held pairs of
@@ -104,20 +126,27 @@ __global__ __launch_bounds__(kGradThreads) void rows_to_tokens_kernel(const SRC*
   constexpr int TOK = kGradThreads / TPT, U = 2;
   const int q0 = threadIdx.x % TPT, groups = H / 4;
   for (int64_t t = (int64_t)blockIdx.x * TOK + threadIdx.x / TPT; t < M; t += (int64_t)gridDim.x * TOK) {
+    // short rows, several tokens a wave: all k pairs are gone through
+    constexpr bool ONE = TPT >= kWave;
+    const TokenPairs pairs(f2s, w, ONE ? t : 0, ONE ? k : 0, M * k);
     for (int q = q0; q < groups; q += U * TPT) {
       float4 acc[U];
 #pragma unroll
       for (int u = 0; u < U; ++u) acc[u] = make_float4(0.f, 0.f, 0.f, 0.f);
-      for (int j0 = 0; j0 < k; j0 += 2) {
+      uint32_t left = ONE ? pairs.held : (1u << k) - 1;
+      while (left) {
         float4 v[2][U];
         bool held[2];
         float wj[2];
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          const int64_t f = t * k + j0 + h;
-          const int32_t row = j0 + h < k ? f2s[f] : -1;
+          const int j = left ? __builtin_ctz(left) : -1;
+          left &= left - 1;
+          int32_t row = -1;
+          if (j >= 0) row = ONE ? pairs.row_of(j) : f2s[t * k + j];
           held[h] = pair_held(row, M * k);
-          wj[h] = DROP && held[h] ? w[f] : 1.f;
+          wj[h] = 1.f;
+          if (DROP && held[h]) wj[h] = ONE ? pairs.w_of(j) : w[t * k + j];
           const SRC* p = src + (int64_t)(held[h] ? row : 0) * H;
 #pragma unroll
           for (int u = 0; u < U; ++u)
@@ -184,18 +213,29 @@ __global__ __launch_bounds__(kGradThreads) void combine_backward_kernel(CombineB
   for (int64_t t0 = (int64_t)blockIdx.x * TOK; t0 < a.M; t0 += (int64_t)gridDim.x * TOK) {
     const int64_t t = t0 + threadIdx.x / TPT;
     const bool valid = t < a.M;
+    // the pairs gone through, and how many: of a wave that owns one token those held, else all k
+    constexpr bool ONE = TPT >= kWave;
+    const TokenPairs pairs(a.f2s, a.topk_w, ONE && valid ? t : 0, ONE && valid ? a.k : 0, R);
+    const int n = ONE ? __builtin_popcount(pairs.held) : KMAX;
     int32_t row[KMAX];
     float w[KMAX], s[KMAX];
+    uint32_t left = pairs.held;
 #pragma unroll
     for (int j = 0; j < KMAX; ++j) {
-      const bool in = valid && j < a.k;
-      row[j] = in ? a.f2s[t * a.k + j] : -1;
-      w[j] = in ? a.topk_w[t * a.k + j] : 0.f;
-      if (!pair_held(row[j], R)) row[j] = -1;
-      if constexpr (TPT >= kWave) row[j] = __builtin_amdgcn_readfirstlane(row[j]);  // one token a wave
-      s[j] = 0.f;
+      row[j] = -1;
+      w[j] = s[j] = 0.f;
+      if (ONE && j < n) {
+        const int from = __builtin_ctz(left);
+        left &= left - 1;
+        row[j] = pairs.row_of(from);
+        w[j] = pairs.w_of(from);
+      } else if (!ONE && valid && j < a.k) {
+        row[j] = a.f2s[t * a.k + j];
+        w[j] = a.topk_w[t * a.k + j];
+        if (!pair_held(row[j], R)) row[j] = -1;
+      }
     }
-    for (int q = q0; valid && q < groups; q += U * TPT) {
+    for (int q = q0; n > 0 && valid && q < groups; q += U * TPT) {  // (no pair held: dout is not read)
       float4 g[U];
 #pragma unroll
       for (int u = 0; u < U; ++u)
@@ -204,6 +244,7 @@ __global__ __launch_bounds__(kGradThreads) void combine_backward_kernel(CombineB
       Kept keep[U];
 #pragma unroll
       for (int j0 = 0; j0 < KMAX; j0 += JG) {
+        if (j0 >= n) continue;
         float4 y[JG][U];
 #pragma unroll
         for (int h = 0; h < JG; ++h) {
@@ -242,11 +283,15 @@ __global__ __launch_bounds__(kGradThreads) void combine_backward_kernel(CombineB
     // across the token's lanes, then (TPT > a wave) across its waves
 #pragma unroll
     for (int j = 0; j < KMAX; ++j) {
+      if (j >= n) continue;
 #pragma unroll
       for (int off = (TPT < kWave ? TPT : kWave) / 2; off > 0; off >>= 1) s[j] += __shfl_xor(s[j], off);
     }
+    // slot j's place among the pairs gone through
+    const uint32_t lane = threadIdx.x % kWave, at = __builtin_popcount(pairs.held & ((1u << (lane & 31)) - 1));
+    const bool held = lane < 32 && (pairs.held >> (lane & 31) & 1);
     if constexpr (TPT > kWave) {
-      if (threadIdx.x % kWave == 0) {
+      if (lane == 0) {
 #pragma unroll
         for (int j = 0; j < KMAX; ++j) part[threadIdx.x / kWave][j] = s[j];
       }
@@ -254,10 +299,15 @@ __global__ __launch_bounds__(kGradThreads) void combine_backward_kernel(CombineB
       if (threadIdx.x < a.k) {
         float sum = 0.f;
 #pragma unroll
-        for (int v = 0; v < kGradThreads / kWave; ++v) sum += part[v][threadIdx.x];
+        for (int v = 0; v < kGradThreads / kWave; ++v) sum += held ? part[v][at] : 0.f;
         a.dtopk_w[t * a.k + threadIdx.x] = sum;
       }
       __syncthreads();
+    } else if constexpr (ONE) {
+      float sum = 0.f;
+#pragma unroll
+      for (int j = 0; j < KMAX; ++j) sum = held && at == j ? s[j] : sum;
+      if (valid && lane < a.k) a.dtopk_w[t * a.k + lane] = sum;
     } else {
 #pragma unroll
       for (int j = 0; j < KMAX; ++j)
