@@ -513,65 +513,86 @@ __global__ __launch_bounds__(256 * KG) void grad_weights_f32_kernel(GradGemmArgs
   }
 }
 
-// The kept products, and the rows' gradients of small problems: tiles of 32 rows
-// x 32 columns (keep: of both products), each wave a part of the K steps, loaded
-// one ahead, so that there is no barrier before the waves' sums are added (in order)
-// in LDS, and the waves of several blocks a CU hide each other's latency.  What
-// lies along k (x, and keep's weights) is loaded as whole lines (8 lanes a row)
-// and turned by the wave in LDS of its own; loaded as the matrix instruction takes
-// it, neighbouring lanes different rows, it comes at a third of the rate (keep, 250
-// tokens, 8 experts 2048 x 640, top 2: 53 us, loaded so 74).  The weights of a rows'
-// gradient lie as the instruction takes them.
-template <GradKind KIND, int WAVES>
-__global__ __launch_bounds__(64 * WAVES) void wave_f32_kernel(GradGemmArgs a) {
-  constexpr bool KEEP = KIND == kKeep;
-  constexpr int NP = KEEP ? 2 : 1;               // products
-  constexpr int kRegion = NP * 256;  // a wave's: 4 KiB for the operands in turn, then NP x 4 KiB of sums
+// ------------------------------------------------------------ small tiles ---
+// The f32 kept products, and kept products and rows' gradients of small problems:
+// tiles of 32 rows x 32 columns (keep: of both products), each wave a part of the
+// K steps (128 bytes of a row), loaded one ahead, so that there is no barrier
+// before the waves' sums are added (in order) in LDS, and the waves of several
+// blocks a CU hide each other's latency.  What lies along k (x, and keep's weights)
+// is loaded as whole lines (8 lanes a row) and turned by the wave in LDS of its own;
+// loaded as the matrix instruction takes it, neighbouring lanes different rows, it
+// comes at a third of the rate (f32 keep, 250 tokens, 8 experts 2048 x 640, top 2:
+// 53 us, loaded so 74).  The weights of a rows' gradient, [k][columns], lie as the
+// f32 instruction takes them; in bf16 they pass through LDS too and are read turned
+// (ds_read_b64_tr_b16, as in the large tiles).
+template <GradKind KIND, typename T, int WAVES>
+__global__ __launch_bounds__(64 * WAVES) void wave_kernel(GradGemmArgs a) {
+  constexpr bool KEEP = KIND == kKeep, F32 = sizeof(T) == 4;
+  constexpr int NP = KEEP ? 2 : 1;      // products
+  constexpr int V = 16 / sizeof(T);     // values of 16 bytes
+  constexpr int KS = 8 * V;             // of a K step
+  constexpr int kRegion = NP * 256;     // a wave's: 4 KiB for the operands in turn, then NP x 4 KiB of sums
   __shared__ __attribute__((aligned(16))) f32x4_t lds[WAVES][kRegion];
   __shared__ TileLds tl;
   const int K = KIND == kGradRows0 ? a.F : a.H, N = KIND == kGradRows0 ? a.H : a.F, NT = N / 32, S = a.G / a.E;
-  const int T = build_expert_tile_table(a.offsets, a.G, a.E, 32, tl, (int)a.R) * NT;
-  const Shuffle sm = make_shuffle(a.shuffle, T);
+  const int tiles = build_expert_tile_table(a.offsets, a.G, a.E, 32, tl, (int)a.R) * NT;
+  const Shuffle sm = make_shuffle(a.shuffle, tiles);
   const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6), lrow = lane & 31, lk = lane >> 5;
-  const int lr = lane >> 3, lc = lane & 7;  // of the line loads: rows lr + 8 i, values 4 lc .. 4 lc + 3
-  const int per = K / kGfK, steps = KIND == kGradRows0 ? 2 * per : per;
+  const int lr = lane >> 3, lc = lane & 7;  // of the line loads: rows lr + 8 i, 16-byte chunk lc
+  const int per = K / KS, steps = KIND == kGradRows0 ? 2 * per : per;
   const int b = part_begin(steps, wave, WAVES), end = part_begin(steps, wave + 1, WAVES);
   f32x4_t* const mine = lds[wave];
-  // 32 rows x 32 k (a wave's LDS accesses are done in order): 16-byte chunk c of row r at c ^ (r % 8)
+  // 32 rows x 128 bytes: chunk c of row r at c ^ (r % 8).  (A wave's LDS accesses are done in order, and the compiler
+  // keeps it, as it cannot tell a lane's places of one from those of the other.)
   auto turn = [&](const f32x4_t (&v)[4], f32x4_t (&o)[4]) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) mine[(lr + 8 * i) * 8 + (lc ^ lr)] = v[i];
 #pragma unroll
     for (int u = 0; u < 4; ++u) o[u] = mine[lrow * 8 + ((2 * u + lk) ^ (lrow & 7))];
   };
-  for (int v = blockIdx.x; v < T; v += gridDim.x) {
+  // bf16, [64 k][32 columns]: rows of 64 bytes as loaded (chunk lane % 4 of rows lane / 4 + 16 i); a group of 16 lanes
+  // reads 4 k x 16 columns, each lane ends with a column's 4 k
+  auto turn_k = [&](const f32x4_t (&v)[4], f32x4_t (&o)[4]) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) mine[i * 64 + lane] = v[i];
+    const int g = lane >> 4, l = lane & 15;
+    lds_byte* const at = (lds_byte*)mine + (8 * (g >> 1) + (l >> 2)) * 64 + (g & 1) * 32 + (l & 3) * 8;
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const bf16x4_t lo = __builtin_amdgcn_ds_read_tr16_b64_v4bf16((lds_bf16x4*)(at + u * 1024));
+      const bf16x4_t hi = __builtin_amdgcn_ds_read_tr16_b64_v4bf16((lds_bf16x4*)(at + u * 1024 + 256));
+      o[u] = __builtin_bit_cast(f32x4_t, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
+    }
+  };
+  for (int v = blockIdx.x; v < tiles; v += gridDim.x) {
     const TileCoord c = tile_coord(shuffled(sm, v), a.E, NT, 32, 1, 0, tl);
     const int e = uniform(c.g), n0 = uniform(c.nt) * 32, pos = expert_row(tl, e, a.E, S, c.m0, lrow);
     // lanes' places in the operands (R times a row is below 2^31); a row that the tile lacks: the first one, not stored
     int xat[4], wat[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      xat[i] = max(__shfl(pos, lr + 8 * i), 0) * K + 4 * lc;
-      wat[i] = (lr + 8 * i) * K + 4 * lc;
+      xat[i] = max(__shfl(pos, lr + 8 * i), 0) * K + V * lc;
+      wat[i] = KEEP ? (lr + 8 * i) * K + V * lc : F32 ? 8 * i * N : 16 * i * N;
     }
-    const int64_t wbase = KEEP ? ((int64_t)e * N + n0) * K : ((int64_t)e * K + 4 * lk) * N + n0 + lrow;
-    const float* const w0 = (const float*)a.w0 + wbase;
-    const float* const w1 = KIND == kGradRows1 ? nullptr : (const float*)a.w1 + wbase;
+    const int64_t wbase = KEEP ? ((int64_t)e * N + n0) * K
+                               : ((int64_t)e * K + (F32 ? 4 * lk : lane >> 2)) * N + n0 + (F32 ? lrow : 8 * (lane & 3));
+    const T* const w0 = (const T*)a.w0 + wbase;
+    const T* const w1 = KIND == kGradRows1 ? nullptr : (const T*)a.w1 + wbase;
     f32x4_t xv[4], wv[NP][4], nextx[4], nextw[NP][4];
     auto load = [&](f32x4_t (&ox)[4], f32x4_t (&ow)[NP][4], int s) {
       const bool second = KIND == kGradRows0 && s >= per;
-      const int k = (second ? s - per : s) * kGfK;
-      const float* const x = (const float*)(KEEP ? a.x : second ? a.d1 : a.d0) + k;
-      const float* const w = (second ? w1 : w0) + (KEEP ? k : (int64_t)k * N);
+      const int k = (second ? s - per : s) * KS;
+      const T* const x = (const T*)(KEEP ? a.x : second ? a.d1 : a.d0) + k;
+      const T* const w = (second ? w1 : w0) + (KEEP ? k : (int64_t)k * N);
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         ox[i] = *reinterpret_cast<const f32x4_t*>(x + xat[i]);
-        if constexpr (KEEP) {
+        if constexpr (KEEP || !F32) {
           ow[0][i] = *reinterpret_cast<const f32x4_t*>(w + wat[i]);
-          ow[1][i] = *reinterpret_cast<const f32x4_t*>(w1 + k + wat[i]);
+          if constexpr (KEEP) ow[1][i] = *reinterpret_cast<const f32x4_t*>(w1 + k + wat[i]);
         } else {
 #pragma unroll
-          for (int h = 0; h < 4; ++h) ow[0][i][h] = w[(int64_t)(8 * i + h) * N];
+          for (int h = 0; h < 4; ++h) ow[0][i][h] = (w + wat[i])[(int64_t)h * N];
         }
       }
     };
@@ -585,18 +606,32 @@ __global__ __launch_bounds__(64 * WAVES) void wave_f32_kernel(GradGemmArgs a) {
       load(nextx, nextw, min(s + 1, end - 1));  // (with a branch here the loads are waited for at once)
       f32x4_t fx[4], fw[NP][4];
       turn(xv, fx);
-      if constexpr (KEEP) {
-        turn(wv[0], fw[0]);
-        turn(wv[1], fw[1]);
+#pragma unroll
+      for (int m = 0; m < NP; ++m) {
+        if constexpr (KEEP) {
+          turn(wv[m], fw[m]);
+        } else if constexpr (!F32) {
+          turn_k(wv[m], fw[m]);
+        } else {
+#pragma unroll
+          for (int u = 0; u < 4; ++u) fw[m][u] = wv[m][u];
+        }
       }
 #pragma unroll
-      for (int u = 0; u < 4; ++u)
+      for (int u = 0; u < 4; ++u) {
+        if constexpr (F32) {
 #pragma unroll
-        for (int h = 0; h < 4; ++h)
+          for (int h = 0; h < 4; ++h)
+#pragma unroll
+            for (int m = 0; m < NP; ++m) acc[m] = __builtin_amdgcn_mfma_f32_32x32x2f32(fw[m][u][h], fx[u][h], acc[m], 0, 0, 0);
+        } else {
 #pragma unroll
           for (int m = 0; m < NP; ++m)
-            acc[m] = __builtin_amdgcn_mfma_f32_32x32x2f32(KEEP ? fw[m][u][h] : wv[m][u][h], fx[u][h], acc[m], 0, 0, 0);
-      if ((s - b) % kGfFlush == kGfFlush - 1 || s + 1 == end) {
+            acc[m] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8_t, fw[m][u]),
+                                                             __builtin_bit_cast(bf16x8_t, fx[u]), acc[m], 0, 0, 0);
+        }
+      }
+      if (F32 ? (s - b) % kGfFlush == kGfFlush - 1 || s + 1 == end : s + 1 == end) {
 #pragma unroll
         for (int m = 0; m < NP; ++m) {
           sum[m] += acc[m];
@@ -614,10 +649,11 @@ __global__ __launch_bounds__(64 * WAVES) void wave_f32_kernel(GradGemmArgs a) {
     const int q = wave, n = n0 + 8 * q + 4 * lk;
     const bool stores = q < 4 && pos >= 0;
     const int64_t at = (int64_t)pos * N + n;
-    f32x4_t gv{}, uv{};
+    typedef T T4 __attribute__((ext_vector_type(4)));
+    T4 gv{}, uv{};
     if (KIND == kGradRows1 && stores) {
-      gv = *(const f32x4_t*)((const float*)a.gate + at);
-      uv = *(const f32x4_t*)((const float*)a.up + at);
+      gv = *(const T4*)((const T*)a.gate + at);
+      uv = *(const T4*)((const T*)a.up + at);
     }
 #pragma unroll
     for (int m = 0; m < NP; ++m)
@@ -632,24 +668,25 @@ __global__ __launch_bounds__(64 * WAVES) void wave_f32_kernel(GradGemmArgs a) {
 #pragma unroll
         for (int w = 0; w < WAVES; ++w) o[m] += lds[w][(m * 4 + q) * 64 + lane];
       if constexpr (KIND == kGradRows0) {
-        gf_store4((float*)a.o0 + at, o[0]);
+        gf_store4((T*)a.o0 + at, o[0]);
       } else if constexpr (KIND == kGradRows1) {
         f32x4_t dg, du;
 #pragma unroll
         for (int u = 0; u < 4; ++u) {
-          const SwigluGrad d = swiglu_grad(o[0][u], gv[u], uv[u]);
+          const SwigluGrad d = F32 ? swiglu_grad(o[0][u], (float)gv[u], (float)uv[u])
+                                   : swiglu_grad_fast(o[0][u], (float)gv[u], (float)uv[u]);
           dg[u] = d.dg;
           du[u] = d.du;
         }
-        gf_store4((float*)a.o0 + at, dg);
-        gf_store4((float*)a.o1 + at, du);
+        gf_store4((T*)a.o0 + at, dg);
+        gf_store4((T*)a.o1 + at, du);
       } else {
         f32x4_t h;
 #pragma unroll
-        for (int u = 0; u < 4; ++u) h[u] = silu_f32(o[0][u]) * o[1][u];
-        gf_store4((float*)a.o0 + at, o[0]);
-        gf_store4((float*)a.o1 + at, o[1]);
-        gf_store4((float*)a.o2 + at, h);
+        for (int u = 0; u < 4; ++u) h[u] = F32 ? silu_f32(o[0][u]) * o[NP - 1][u] : silu_mul_fast(o[0][u], o[NP - 1][u]);
+        gf_store4((T*)a.o0 + at, o[0]);
+        gf_store4((T*)a.o1 + at, o[NP - 1]);
+        gf_store4((T*)a.o2 + at, h);
       }
     }
     __syncthreads();  // the sums are read before the next tile's lines
@@ -663,7 +700,7 @@ __global__ __launch_bounds__(64 * WAVES) void wave_f32_kernel(GradGemmArgs a) {
 struct GradPlan {
   int units = 0;
   bool wide = false;  // f32: tiles of 128
-  bool wave = false;  // ... of 32
+  bool wave = false;  // tiles of 32
   size_t unit_bytes = 0;
   size_t bytes() const { return units ? 256 + (size_t)units * (unit_bytes + kGradDescInts * 4) : 0; }
 };
@@ -673,7 +710,7 @@ static int64_t wave_tiles(const GradGemmArgs& a, int N) {
   const int64_t rows = a.all_held ? a.R : a.R / 2;
   return (rows / 32 + (rows < a.E ? rows : a.E)) * (N / 32);
 }
-// The kept products take them always (tiles of 64 x 64 of both products through
+// f32: the kept products take them always (tiles of 64 x 64 of both products through
 // common LDS buffers, these: 256 tokens, 8 experts 256 x 512, top 2: 18.8, 11.9
 // us; 1024, 4 of 2048 x 2048, top 1: 293, 204; 4096 tokens there: 874, 714), rows'
 // gradients for eight rounds of the CUs and sums of 2048 terms; longer ones are cut
@@ -682,17 +719,33 @@ static int64_t wave_tiles(const GradGemmArgs& a, int N) {
 // of 512 x 512 (2128): 69, 67; 4096, 8 of 2048 x 1024 (16896): 770, 938; 64, 2 of
 // 1024 x 4096, top 1 (8192 terms): 37, 57; layer 1: 512, 8 of 256 x 512, top 2 (640):
 // 14.4, 12.3; 100, 4 of 4096 x 576, top 1 (4096 terms): 32.9, 31.9.
-static bool wave_rows(const GradGemmArgs& a, int N, int K, int cus) { return wave_tiles(a, N) <= 8 * cus && K <= 2048; }
+// bf16: a K step of 64 costs these about 0.2 us a CU (several waves at once) and a
+// wave alone 0.9, a tile four steps' time beside; the large tiles cost 15 us and
+// more but a fifth a step.  Measured (large tiles, these), top 2 of 8 experts, keep:
+// 256 tokens, 256 x 512 (1.5 tiles a CU of 4 steps): 13.1, 7.9; 2048 there (8.5):
+// 18.0, 19.6; 35, 3 of 3968 x 64 (8 tiles, 62 steps): 42, 12.7; 1000, 1024 x 1024 (8.8
+// a CU, 16): 34, 45.  Rows of layer 1: 256, 256 x 512: 14.5, 8.4; 2048 there: 25, 17;
+// 1000, 1024 x 1024: 38, 36; layer 0: 256, 256 x 512 (0.8, 16): 21, 9; 1000, 1024 x 1024
+// (8.8, 32): 47, 58; 60, one of 448 x 8576 (14 tiles, 268): 34, 36 (the large tiles cut
+// into parts).
+static bool wave_rows(const GradGemmArgs& a, bool bf16, int N, int K, int cus) {
+  const int64_t tiles = wave_tiles(a, N), steps = K / kBK;
+  return bf16 ? tiles * (steps + 4) <= 200 * cus && steps <= 192 : tiles <= 8 * cus && K <= 2048;
+}
+static bool wave_keep(const GradGemmArgs& a, bool bf16, int cus) {
+  const int64_t tiles = wave_tiles(a, a.F), steps = a.H / kBK;
+  return !bf16 || tiles <= cus || tiles * (steps + 4) <= 64 * cus;
+}
 // Up to a tile a CU 8 waves share one, above 4 (8, 4): layer 0's rows above 11.8,
 // 13.1 us; 512 tokens there (320 tiles): 20.5, 18.8; kept, 21 rows, one of 2112 x 448:
 // 28, 30; 500, 8 of 1024 x 1024: 73, 61.
-template <GradKind KIND>
+template <GradKind KIND, typename T>
 static hipError_t launch_wave(const GradGemmArgs& g, int N, hipStream_t s) {
   const int cus = device_cu_count();
   if (wave_tiles(g, N) <= cus)
-    wave_f32_kernel<KIND, 8><<<cus, 512, 0, s>>>(g);
-  else  // (keep, three blocks a CU: 4096 tokens of 4 experts 2048 x 2048 728 us, two 714)
-    wave_f32_kernel<KIND, 4><<<(KIND == kKeep ? 2 : 4) * cus, 256, 0, s>>>(g);
+    wave_kernel<KIND, T, 8><<<cus, 512, 0, s>>>(g);
+  else  // blocks a CU as registers hold (rows of 2048 tokens above 17 us, with a fourth that waits 19)
+    wave_kernel<KIND, T, 4><<<(KIND == kKeep ? 2 : 3) * cus, 256, 0, s>>>(g);
   return hipGetLastError();
 }
 
@@ -701,7 +754,7 @@ static GradPlan plan_rows(const GradGemmArgs& a, bool bf16) {
   const int cus = device_cu_count(), rows = bf16 ? kTileRows : 64, cols = bf16 ? 256 : 64;
   const int N = a.layer == 0 ? a.H : a.F, K = a.layer == 0 ? 2 * a.F : a.H, NT = (N + cols - 1) / cols;
   p.wide = !bf16 && wide_f32(a.R / 128 * ((N + 127) / 128), cus);
-  p.wave = !bf16 && wave_rows(a, N, K, cus);
+  p.wave = !p.wide && wave_rows(a, bf16, N, K, cus);
   if (p.wide || p.wave) return p;
   const SplitCost& c = bf16 ? kSplitBf16 : kSplitF32;
   const int steps = bf16 ? K / kBK : K / kGfK / 4;
@@ -761,6 +814,10 @@ hipError_t launch_grad_rows(const GradGemmArgs& a, bool bf16, void* ws, hipStrea
   const int cus = device_cu_count(), xcd_slots = cus / kXcds > 0 ? cus / kXcds : 1;
   const GradPlan p = plan_rows(a, bf16);
   const GradGemmArgs g = with_split(a, p, ws);
+  if (p.wave) {
+    if (bf16) return a.layer == 0 ? launch_wave<kGradRows0, __bf16>(g, a.H, s) : launch_wave<kGradRows1, __bf16>(g, a.F, s);
+    return a.layer == 0 ? launch_wave<kGradRows0, float>(g, a.H, s) : launch_wave<kGradRows1, float>(g, a.F, s);
+  }
   if (bf16) {
     if (a.layer == 0) {
       grad_rows_bf16_kernel<kGradRows0><<<cus, kGemmThreads, 0, s>>>(g, xcd_slots);
@@ -776,7 +833,6 @@ hipError_t launch_grad_rows(const GradGemmArgs& a, bool bf16, void* ws, hipStrea
       grad_rows_f32_kernel<kGradRows1, 128, 2><<<cus, 512, 0, s>>>(g);
     return hipGetLastError();
   }
-  if (p.wave) return a.layer == 0 ? launch_wave<kGradRows0>(g, a.H, s) : launch_wave<kGradRows1>(g, a.F, s);
   if (a.layer == 0) {
     grad_rows_f32_kernel<kGradRows0, 64, 4><<<cus, 1024, 0, s>>>(g);
     return grad_reduce_launch<kGradRows0, float>(g, s);
@@ -810,11 +866,10 @@ hipError_t launch_grad_weights(const GradGemmArgs& a, bool bf16, void* ws, hipSt
 hipError_t launch_keep(const GradGemmArgs& a, bool bf16, hipStream_t s) {
   if (a.R == 0) return hipSuccess;
   const int cus = device_cu_count();
-  if (bf16) {
-    grad_rows_bf16_kernel<kKeep><<<cus, kGemmThreads, 0, s>>>(with_split(a, GradPlan{}, nullptr), cus / kXcds > 0 ? cus / kXcds : 1);
-    return hipGetLastError();
-  }
-  return launch_wave<kKeep>(with_split(a, GradPlan{}, nullptr), a.F, s);
+  const GradGemmArgs g = with_split(a, GradPlan{}, nullptr);
+  if (wave_keep(a, bf16, cus)) return bf16 ? launch_wave<kKeep, __bf16>(g, a.F, s) : launch_wave<kKeep, float>(g, a.F, s);
+  grad_rows_bf16_kernel<kKeep><<<cus, kGemmThreads, 0, s>>>(g, cus / kXcds > 0 ? cus / kXcds : 1);
+  return hipGetLastError();
 }
 
 }  // namespace moe

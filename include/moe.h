@@ -542,8 +542,8 @@ moe_status_t moe_route_backward(const moe_problem_t* p, const int32_t* topk_idx,
 /*
  * moe_grouped_gemm's layer 0 that also keeps its two products for the gradient:
  * gate = X_perm W_gate^T and up = X_perm W_up^T [R,F] rounded to dtype; c =
- * Hact, formed from the f32 products: in bf16 what moe_grouped_gemm writes, bit
- * for bit; in f32 its sums over H are grouped differently (to the same bound).
+ * Hact, formed from the f32 products.  Sums over H may be grouped otherwise than
+ * moe_grouped_gemm's, to the same bound.
  */
 moe_status_t moe_grouped_gemm_aux(const moe_problem_t* p, const void* a, const void* w0, const void* w1,
                                   const int32_t* offsets, void* gate, void* up, void* c, void* stream);

@@ -152,13 +152,13 @@ def products(xp, wg, wu, offsets, bf16):
     return o
 
 
-def hact(xp, wg, wu, offsets):
+def hact(xp, wg, wu, offsets, bf16=False):
     """silu(gate) up of the f32 products, and its bound: |silu'| <= 1.1; the exponential, the division and the products
-    8 u."""
+    8 u; in bf16 |gate| u more, as the argument of the exponential is a rounded product (gate / ln 2)."""
     g, bg, u, bu = products(xp, wg, wu, offsets, False)
     silu = g * torch.sigmoid(g)
     h = silu * u
-    return h, 1.1 * bg * (u.abs() + bu) + silu.abs() * bu + 8 * U * h.abs()
+    return cast(h, 1.1 * bg * (u.abs() + bu) + silu.abs() * bu + (8 + (g.abs() if bf16 else 0)) * U * h.abs(), bf16)
 
 
 def rows1(dy, wd, gate, up, offsets, bf16):
