@@ -243,7 +243,12 @@ EXPERTS = [dict(M=1, H=64, F=64, E=1, k=1), dict(M=1, H=256, F=320, E=8, k=2), d
            dict(M=3000, H=320, F=64, E=2, k=1, crowd=2.5),
            # many tiles: the larger f32 ones
            dict(M=8200, H=64, F=4096, E=2, k=1), dict(M=4100, H=4160, F=64, E=3, k=2), dict(M=100, H=1088, F=1152, E=32, k=2),
-           dict(M=90, H=128, F=448, E=40, k=2)]
+           dict(M=90, H=128, F=448, E=40, k=2),
+           # the larger bf16 tiles: ragged segments over source blocks, a share, few rows an expert, split along K
+           dict(M=3000, H=832, F=1088, E=5, k=2, S=3, skip=(1,), crowd=1.0),
+           dict(M=5000, H=704, F=960, E=12, k=3, held=3, base=4, S=2), dict(M=300, H=1024, F=1408, E=64, k=4),
+           dict(M=60, H=448, F=6272, E=1, k=1), dict(M=60, H=12352, F=448, E=1, k=1),
+           dict(M=90, H=320, F=6272, E=12, k=3, S=3, held=3, base=4)]
 
 
 def experts(M, H, F, E, k, dtype, S=1, held=0, base=0, crowd=0.0, skip=(), seed=0):
@@ -457,9 +462,10 @@ def test_no_tokens(dtype):
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
-def test_infinities_and_nan_stay_in_their_row_or_column(dtype):
+@pytest.mark.parametrize("shape", [dict(M=150, H=192, F=320, E=3, k=2), dict(M=3000, H=832, F=1088, E=5, k=2)])
+def test_infinities_and_nan_stay_in_their_row_or_column(shape, dtype):
     # a value that is not finite reaches what the formula says and nothing else
-    prob, d, ws = experts(M=150, H=192, F=320, E=3, k=2, dtype=dtype, seed=3)
+    prob, d, ws = experts(**shape, dtype=dtype, seed=3)
     first = run_all(prob, d, ws)
     r = int(d["offsets"][1]) + 3  # a row of expert 1
     bad = {n: v.clone() for n, v in d.items()}
@@ -476,7 +482,8 @@ def test_infinities_and_nan_stay_in_their_row_or_column(dtype):
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 @pytest.mark.parametrize("shape", [dict(M=600, H=320, F=448, E=6, k=2, S=2), dict(M=900, H=256, F=576, E=3, k=2),
-                                   dict(M=70, H=2176, F=2112, E=2, k=1)])
+                                   dict(M=70, H=2176, F=2112, E=2, k=1), dict(M=3000, H=832, F=1088, E=5, k=2, S=3),
+                                   dict(M=60, H=448, F=6272, E=1, k=1)])
 def test_order_does_not_change_a_bit(shape, dtype):
     prob, d, ws = experts(**shape, dtype=dtype, seed=4)
     first = run_all(prob, d, ws)
