@@ -514,6 +514,21 @@ __global__ __launch_bounds__(256 * KG) void grad_weights_f32_kernel(GradGemmArgs
 }
 
 // ------------------------------------------------------------ small tiles ---
+// bf16, [64 k][32 columns] through a wave's 4 KiB of LDS: rows of 64 bytes as loaded (16-byte chunk lane % 4 of rows
+// lane / 4 + 16 i); a group of 16 lanes reads 4 k x 16 columns, each lane ends with a column's 4 k.
+__device__ __forceinline__ void turn_k(f32x4_t* mine, const f32x4_t (&v)[4], f32x4_t (&o)[4]) {
+  const int lane = threadIdx.x & 63, g = lane >> 4, l = lane & 15;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) mine[i * 64 + lane] = v[i];
+  lds_byte* const at = (lds_byte*)mine + (8 * (g >> 1) + (l >> 2)) * 64 + (g & 1) * 32 + (l & 3) * 8;
+#pragma unroll
+  for (int u = 0; u < 4; ++u) {
+    const bf16x4_t lo = __builtin_amdgcn_ds_read_tr16_b64_v4bf16((lds_bf16x4*)(at + u * 1024));
+    const bf16x4_t hi = __builtin_amdgcn_ds_read_tr16_b64_v4bf16((lds_bf16x4*)(at + u * 1024 + 256));
+    o[u] = __builtin_bit_cast(f32x4_t, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
+  }
+}
+
 // The f32 kept products, and kept products and rows' gradients of small problems:
 // tiles of 32 rows x 32 columns (keep: of both products), each wave a part of the
 // K steps (128 bytes of a row), loaded one ahead, so that there is no barrier
@@ -549,20 +564,6 @@ __global__ __launch_bounds__(64 * WAVES) void wave_kernel(GradGemmArgs a) {
     for (int i = 0; i < 4; ++i) mine[(lr + 8 * i) * 8 + (lc ^ lr)] = v[i];
 #pragma unroll
     for (int u = 0; u < 4; ++u) o[u] = mine[lrow * 8 + ((2 * u + lk) ^ (lrow & 7))];
-  };
-  // bf16, [64 k][32 columns]: rows of 64 bytes as loaded (chunk lane % 4 of rows lane / 4 + 16 i); a group of 16 lanes
-  // reads 4 k x 16 columns, each lane ends with a column's 4 k
-  auto turn_k = [&](const f32x4_t (&v)[4], f32x4_t (&o)[4]) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) mine[i * 64 + lane] = v[i];
-    const int g = lane >> 4, l = lane & 15;
-    lds_byte* const at = (lds_byte*)mine + (8 * (g >> 1) + (l >> 2)) * 64 + (g & 1) * 32 + (l & 3) * 8;
-#pragma unroll
-    for (int u = 0; u < 4; ++u) {
-      const bf16x4_t lo = __builtin_amdgcn_ds_read_tr16_b64_v4bf16((lds_bf16x4*)(at + u * 1024));
-      const bf16x4_t hi = __builtin_amdgcn_ds_read_tr16_b64_v4bf16((lds_bf16x4*)(at + u * 1024 + 256));
-      o[u] = __builtin_bit_cast(f32x4_t, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
-    }
   };
   for (int v = blockIdx.x; v < tiles; v += gridDim.x) {
     const TileCoord c = tile_coord(shuffled(sm, v), a.E, NT, 32, 1, 0, tl);
@@ -611,7 +612,7 @@ __global__ __launch_bounds__(64 * WAVES) void wave_kernel(GradGemmArgs a) {
         if constexpr (KEEP) {
           turn(wv[m], fw[m]);
         } else if constexpr (!F32) {
-          turn_k(wv[m], fw[m]);
+          turn_k(mine, wv[m], fw[m]);
         } else {
 #pragma unroll
           for (int u = 0; u < 4; ++u) fw[m][u] = wv[m][u];
@@ -687,6 +688,116 @@ __global__ __launch_bounds__(64 * WAVES) void wave_kernel(GradGemmArgs a) {
         gf_store4((T*)a.o0 + at, o[0]);
         gf_store4((T*)a.o1 + at, o[NP - 1]);
         gf_store4((T*)a.o2 + at, h);
+      }
+    }
+    __syncthreads();  // the sums are read before the next tile's lines
+  }
+}
+
+// bf16 weights' gradients of small problems: as above, tiles of 32 x 32 of dW, both
+// operands [rows][columns].  A K step is 64 rows of a segment of the expert, rows
+// past its end zeros.  (In f32 the tiles of 64 are as fast: 256 tokens, 8 experts 256
+// x 512: 9.7 us, these 16.)
+template <int WAVES>
+__global__ __launch_bounds__(64 * WAVES) void wave_weights_kernel(GradGemmArgs a) {
+  constexpr int KS = 64;
+  __shared__ __attribute__((aligned(16))) f32x4_t lds[WAVES][256];
+  __shared__ int offsets[kMaxTileSegs + 1];
+  for (int i = threadIdx.x; i <= a.G; i += 64 * WAVES) offsets[i] = min(max(a.offsets[i], 0), (int)a.R);
+  __syncthreads();
+  const bool l0 = a.layer == 0;
+  const int N = l0 ? a.F : a.H, C = l0 ? a.H : a.F, NR = N / 32, NC = C / 32;  // rows and columns of dW
+  const int S = a.G / a.E, mats = l0 ? 2 : 1, tiles = a.E * mats * NR * NC;
+  const Shuffle sm = make_shuffle(a.shuffle, tiles);
+  const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6), lrow = lane & 31, lk = lane >> 5;
+  f32x4_t* const mine = lds[wave];
+  for (int v = blockIdx.x; v < tiles; v += gridDim.x) {
+    int l = shuffled(sm, v);
+    const int e = l / (mats * NR * NC);
+    l -= e * mats * NR * NC;
+    const int m = l / (NR * NC);
+    l -= m * NR * NC;
+    const int row0 = l % NR * 32, col0 = l / NR * 32;
+    int steps = 0;
+    for (int h = 0; h < S; ++h) steps += (offsets[h * a.E + e + 1] - offsets[h * a.E + e] + KS - 1) / KS;
+    const int b = uniform(part_begin(steps, wave, WAVES)), end = uniform(part_begin(steps, wave + 1, WAVES));
+    // the step before b: its row, the segment's end, the next source block
+    int row = 0, rend = 0, sb = 0;
+    for (int left = b;;) {
+      const int have = (rend - row + KS - 1) / KS;
+      if (left <= have || sb == S) {
+        row += (left - 1) * KS;
+        break;
+      }
+      left -= have;
+      row = uniform(offsets[sb * a.E + e]);
+      rend = uniform(offsets[sb * a.E + e + 1]);
+      ++sb;
+    }
+    const __bf16* const d = (const __bf16*)(m ? a.d1 : a.d0) + row0;
+    const __bf16* const x = (const __bf16*)a.x + col0;
+    auto advance = [&] {
+      row += KS;
+      while (row >= rend && sb < S) {
+        row = uniform(offsets[sb * a.E + e]);
+        rend = uniform(offsets[sb * a.E + e + 1]);
+        ++sb;
+      }
+    };
+    // the step's rows at `row`; those that the segment lacks are its last one, and become zeros
+    auto load = [&](f32x4_t (&od)[4], f32x4_t (&ox)[4]) {
+      const int64_t r0 = min(row, (int)a.R - 1);
+      const int n = max(rend - row, 1);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int k = (lane >> 2) + 16 * i, r = min(k, n - 1), c = 8 * (lane & 3);
+        const f32x4_t dv = *reinterpret_cast<const f32x4_t*>(d + (r0 + r) * N + c);
+        const f32x4_t xv = *reinterpret_cast<const f32x4_t*>(x + (r0 + r) * C + c);
+#pragma unroll
+        for (int h = 0; h < 4; ++h) {
+          od[i][h] = k < n ? dv[h] : 0.f;
+          ox[i][h] = k < n ? xv[h] : 0.f;
+        }
+      }
+    };
+    f32x4_t dv[4], xv[4], nextd[4], nextx[4];
+    f32x16_t acc;
+#pragma unroll
+    for (int h = 0; h < 16; ++h) acc[h] = 0.f;
+    if (b < end) {
+      advance();
+      load(dv, xv);
+    }
+    for (int s = b; s < end; ++s) {
+      if (s + 1 < end) advance();
+      load(nextd, nextx);
+      f32x4_t fd[4], fx[4];
+      turn_k(mine, dv, fd);
+      turn_k(mine, xv, fx);
+#pragma unroll
+      for (int u = 0; u < 4; ++u)
+        acc = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8_t, fx[u]),
+                                                      __builtin_bit_cast(bf16x8_t, fd[u]), acc, 0, 0, 0);
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        dv[u] = nextd[u];
+        xv[u] = nextx[u];
+      }
+    }
+#pragma unroll
+    for (int h = 0; h < 4; ++h) mine[h * 64 + lane] = f32x4_t{acc[4 * h], acc[4 * h + 1], acc[4 * h + 2], acc[4 * h + 3]};
+    __syncthreads();
+    if (wave < 4) {
+      f32x4_t o{};
+#pragma unroll
+      for (int w = 0; w < WAVES; ++w) o += lds[w][wave * 64 + lane];
+      void* const out = m ? a.o1 : a.o0;
+      const int64_t at = ((int64_t)e * N + row0 + lrow) * C + col0 + 8 * wave + 4 * lk;
+      if (a.out_bf16) {
+        gf_store4((__bf16*)out + at, o);
+      } else {
+        float* p = (float*)out + at;
+        gf_store4(p, a.accumulate ? *(const f32x4_t*)p + o : o);
       }
     }
     __syncthreads();  // the sums are read before the next tile's lines
@@ -770,13 +881,23 @@ static GradPlan plan_rows(const GradGemmArgs& a, bool bf16) {
   return p;
 }
 
+// bf16 weights' gradients; steps: an expert's mean.  Measured (large tiles, these):
+// layer 0, 545 tokens, one expert 320 x 384 held (240 tiles, 17 steps): 18.4, 7.9;
+// 256, 8 of 256 x 512, top 2 (2048, 1): 13.7, 9.6; 2048 there (8 steps): 24.2, 20.4;
+// 1000, 8 of 512 x 512 (4096, 3): 18.9, 25.8; layer 1 of it (2048, 3): 17.3, 14.9.
+static bool wave_weights(const GradGemmArgs& a, int64_t tiles, int cus) {
+  const int64_t steps = (a.all_held ? a.R : a.R / 2) / (a.E * kBK);
+  return tiles * (steps + 4) <= (steps < 8 ? 64 : 96) * cus;
+}
+
 static GradPlan plan_weights(const GradGemmArgs& a, bool bf16) {
   GradPlan p;
   const int cus = device_cu_count(), T = bf16 ? 256 : 64;
   const int64_t N = a.layer == 0 ? a.F : a.H, C = a.layer == 0 ? a.H : a.F, mats = a.layer == 0 ? 2 : 1;
   const auto tiles = [&](int t) { return a.E * mats * ((N + t - 1) / t) * ((C + t - 1) / t); };
   p.wide = !bf16 && wide_f32(tiles(128), cus);
-  if (p.wide) return p;
+  p.wave = bf16 && wave_weights(a, tiles(32), cus);
+  if (p.wide || p.wave) return p;
   // the experts' mean of steps, if all rows are kept: with fewer a split pays less
   const int64_t step = a.E * (bf16 ? kBK : 4 * kGfK), mean = (a.R + step - 1) / step, r = tiles(T) % cus;
   const bool split = split_parts(bf16 ? kSplitBf16 : kSplitF32, (int)r, (int)mean, cus) > 1;
@@ -841,10 +962,21 @@ hipError_t launch_grad_rows(const GradGemmArgs& a, bool bf16, void* ws, hipStrea
   return grad_reduce_launch<kGradRows1, float>(g, s);
 }
 
+static hipError_t launch_wave_weights(const GradGemmArgs& g, hipStream_t s) {
+  const int cus = device_cu_count();
+  const int64_t tiles = (int64_t)g.E * (g.layer == 0 ? 2 : 1) * (g.F / 32) * (g.H / 32);
+  if (tiles <= cus)
+    wave_weights_kernel<8><<<cus, 512, 0, s>>>(g);
+  else
+    wave_weights_kernel<4><<<3 * cus, 256, 0, s>>>(g);
+  return hipGetLastError();
+}
+
 hipError_t launch_grad_weights(const GradGemmArgs& a, bool bf16, void* ws, hipStream_t s) {
   const int cus = device_cu_count();
   const GradPlan p = plan_weights(a, bf16);
   const GradGemmArgs g = with_split(a, p, ws);
+  if (p.wave) return launch_wave_weights(g, s);
   if (bf16) {
     grad_weights_bf16_kernel<<<cus, kGemmThreads, 0, s>>>(g);
     return grad_reduce_launch<kGradWeights, __bf16>(g, s);

@@ -248,7 +248,9 @@ EXPERTS = [dict(M=1, H=64, F=64, E=1, k=1), dict(M=1, H=256, F=320, E=8, k=2), d
            dict(M=3000, H=832, F=1088, E=5, k=2, S=3, skip=(1,), crowd=1.0),
            dict(M=5000, H=704, F=960, E=12, k=3, held=3, base=4, S=2), dict(M=300, H=1024, F=1408, E=64, k=4),
            dict(M=60, H=448, F=6272, E=1, k=1), dict(M=60, H=12352, F=448, E=1, k=1),
-           dict(M=90, H=320, F=6272, E=12, k=3, S=3, held=3, base=4)]
+           dict(M=90, H=320, F=6272, E=12, k=3, S=3, held=3, base=4),
+           # ... of few weights over many rows
+           dict(M=20000, H=256, F=320, E=4, k=2, S=3, held=2, base=1)]
 
 
 def experts(M, H, F, E, k, dtype, S=1, held=0, base=0, crowd=0.0, skip=(), seed=0):
@@ -483,7 +485,8 @@ def test_infinities_and_nan_stay_in_their_row_or_column(shape, dtype):
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 @pytest.mark.parametrize("shape", [dict(M=600, H=320, F=448, E=6, k=2, S=2), dict(M=900, H=256, F=576, E=3, k=2),
                                    dict(M=70, H=2176, F=2112, E=2, k=1), dict(M=3000, H=832, F=1088, E=5, k=2, S=3),
-                                   dict(M=60, H=448, F=6272, E=1, k=1)])
+                                   dict(M=60, H=448, F=6272, E=1, k=1),
+                                   dict(M=12000, H=256, F=320, E=2, k=1, S=2)])
 def test_order_does_not_change_a_bit(shape, dtype):
     prob, d, ws = experts(**shape, dtype=dtype, seed=4)
     first = run_all(prob, d, ws)
