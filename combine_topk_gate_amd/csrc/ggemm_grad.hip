@@ -7,8 +7,10 @@
 //   rows, layer 0     dX = dg Wg + du Wu
 //   weights, layer 1  dWd = dY^T h
 //   weights, layer 0  dWg = dg^T X,  dWu = du^T X   (the sums run over rows)
-// A static tile queue as in the forward grouped GEMM; each output element is
-// formed by one workgroup in a fixed order, so nothing depends on scheduling.
+// A static tile queue as in the forward grouped GEMM; each output element's sum is
+// formed in a fixed order, so nothing depends on scheduling.  Three sets of tiles,
+// by size: 256 x 256 (bf16), 64 or 128 square through common LDS buffers (f32), and
+// 32 x 32 with the waves sharing the reduction (small problems).
 #include "common.hpp"
 #include "gemm_grad_bf16.hpp"
 #include "gemm_grad_f32.hpp"
@@ -31,7 +33,7 @@ __device__ __forceinline__ SwigluGrad swiglu_grad(float dh, float g, float u) {
 // of the whole card's bandwidth, the second kernel 6.  Measured (whole, split):
 // 60 rows, 448 x 8576, one expert, 2 tiles of 268 steps: 178, 34 us; 1000 rows,
 // 1024 x 4096, 4 experts: 149, 78; weights of 8 experts 256 x 512, 32768 rows:
-// 132, 58.
+// 132, 65.
 struct SplitCost {
   float step, more, store;
 };
@@ -812,6 +814,7 @@ struct GradPlan {
   int units = 0;
   bool wide = false;  // f32: tiles of 128
   bool wave = false;  // tiles of 32
+  bool many = false;  // f32: tiles of 64, a group of waves each
   size_t unit_bytes = 0;
   size_t bytes() const { return units ? 256 + (size_t)units * (unit_bytes + kGradDescInts * 4) : 0; }
 };
@@ -860,6 +863,14 @@ static hipError_t launch_wave(const GradGemmArgs& g, int N, hipStream_t s) {
   return hipGetLastError();
 }
 
+// f32 tiles of 64 that are many for the CUs are not cut, and one group of waves
+// takes a tile, several workgroups a CU.  Measured (four groups, one): weights of 6
+// experts 1216 x 4224, about 300 rows each (7524 tiles): 287, 206 us; 4 of 2048 x 1024,
+// 1024 rows (2048): 190, 164; 4 of 1024 x 512 (512): 54, 56; rows of layer 1, 82 experts
+// 192 x 12288, 25 rows each: 572, 374; 4 of 2048 x 2048, 256 each (2.3 a CU): 123, 132;
+// of layer 0, 8 of 2048 x 1024, 1024 each (17 a CU): 772, 715.
+constexpr int kManyRows = 3, kManyWeights = 4;  // tiles a CU
+
 static GradPlan plan_rows(const GradGemmArgs& a, bool bf16) {
   GradPlan p;
   const int cus = device_cu_count(), rows = bf16 ? kTileRows : 64, cols = bf16 ? 256 : 64;
@@ -867,6 +878,9 @@ static GradPlan plan_rows(const GradGemmArgs& a, bool bf16) {
   p.wide = !bf16 && wide_f32(a.R / 128 * ((N + 127) / 128), cus);
   p.wave = !p.wide && wave_rows(a, bf16, N, K, cus);
   if (p.wide || p.wave) return p;
+  // (half the experts end in a tile of their own more than their rows fill)
+  p.many = !bf16 && ((a.all_held ? a.R : a.R / 2) / 64 + (a.R < a.E ? a.R : a.E) / 2) * NT >= kManyRows * cus;
+  if (p.many) return p;
   const SplitCost& c = bf16 ? kSplitBf16 : kSplitF32;
   const int steps = bf16 ? K / kBK : K / kGfK / 4;
   const int64_t hi = a.R / rows + (a.R < a.E ? a.R : a.E), lo = a.all_held ? (a.R + rows - 1) / rows : 0;
@@ -897,7 +911,8 @@ static GradPlan plan_weights(const GradGemmArgs& a, bool bf16) {
   const auto tiles = [&](int t) { return a.E * mats * ((N + t - 1) / t) * ((C + t - 1) / t); };
   p.wide = !bf16 && wide_f32(tiles(128), cus);
   p.wave = bf16 && wave_weights(a, tiles(32), cus);
-  if (p.wide || p.wave) return p;
+  p.many = !bf16 && tiles(64) >= kManyWeights * cus;
+  if (p.wide || p.wave || p.many) return p;
   // the experts' mean of steps, if all rows are kept: with fewer a split pays less
   const int64_t step = a.E * (bf16 ? kBK : 4 * kGfK), mean = (a.R + step - 1) / step, r = tiles(T) % cus;
   const bool split = split_parts(bf16 ? kSplitBf16 : kSplitF32, (int)r, (int)mean, cus) > 1;
@@ -954,6 +969,13 @@ hipError_t launch_grad_rows(const GradGemmArgs& a, bool bf16, void* ws, hipStrea
       grad_rows_f32_kernel<kGradRows1, 128, 2><<<cus, 512, 0, s>>>(g);
     return hipGetLastError();
   }
+  if (p.many) {
+    if (a.layer == 0)
+      grad_rows_f32_kernel<kGradRows0, 64, 1><<<3 * cus, 256, 0, s>>>(g);
+    else
+      grad_rows_f32_kernel<kGradRows1, 64, 1><<<3 * cus, 256, 0, s>>>(g);
+    return hipGetLastError();
+  }
   if (a.layer == 0) {
     grad_rows_f32_kernel<kGradRows0, 64, 4><<<cus, 1024, 0, s>>>(g);
     return grad_reduce_launch<kGradRows0, float>(g, s);
@@ -985,9 +1007,9 @@ hipError_t launch_grad_weights(const GradGemmArgs& a, bool bf16, void* ws, hipSt
     grad_weights_f32_kernel<128, 2><<<cus, 512, 0, s>>>(g);
     return hipGetLastError();
   }
-  // fewer steps than the groups can share: one group a tile, four workgroups a CU (8 experts 256 x 7680, a row each:
-  // 34 us with four groups, 23 with one; 8 experts 256 x 512, 64 rows each: 13.5, 9.4)
-  if (a.R < 4ll * a.E * 4 * kGfK && !p.units) {
+  // many tiles, or fewer steps than the groups can share: one group a tile, four workgroups a CU (8 experts 256 x 7680,
+  // a row each: 34 us with four groups, 23 with one; 8 experts 256 x 512, 64 rows each: 13.5, 9.4)
+  if (p.many || (a.R < 4ll * a.E * 4 * kGfK && !p.units)) {
     grad_weights_f32_kernel<64, 1><<<4 * cus, 256, 0, s>>>(g);
     return hipGetLastError();
   }

@@ -250,7 +250,9 @@ EXPERTS = [dict(M=1, H=64, F=64, E=1, k=1), dict(M=1, H=256, F=320, E=8, k=2), d
            dict(M=60, H=448, F=6272, E=1, k=1), dict(M=60, H=12352, F=448, E=1, k=1),
            dict(M=90, H=320, F=6272, E=12, k=3, S=3, held=3, base=4),
            # ... of few weights over many rows
-           dict(M=20000, H=256, F=320, E=4, k=2, S=3, held=2, base=1)]
+           dict(M=20000, H=256, F=320, E=4, k=2, S=3, held=2, base=1),
+           # the largest number of segments, the longest rows
+           dict(M=100, H=64, F=64, E=512, k=16, S=2), dict(M=3, H=65536, F=64, E=2, k=1), dict(M=3, H=64, F=65536, E=2, k=1)]
 
 
 def experts(M, H, F, E, k, dtype, S=1, held=0, base=0, crowd=0.0, skip=(), seed=0):
