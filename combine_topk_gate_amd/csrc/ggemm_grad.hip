@@ -59,10 +59,11 @@ __device__ __forceinline__ int split_within(const GradGemmArgs& a, int s, int r)
 
 // Whether an f32 product takes tiles of 128 x 128 (tiles: how many there are)
 // with two groups of waves: from eight rounds of the CUs on, where their padding
-// and the last round's idle CUs weigh little; below, tiles of 64 x 64 with four
-// groups.  Measured (128, 64): weights of 4 experts 2048 x 8192, 512 rows each,
-// 64 rounds: 1.40, 1.77 ms; rows of 8 experts 2048 x 4096, 256 each, 1 round:
-// 1.24, 0.80.
+// and the last round's idle CUs weigh little; below, tiles of 64 x 64.  Measured
+// (128; 64, one group): layer 0's weights of 4 experts 2048 x 4096, 2048 rows each:
+// 2.49, 2.57 ms; rows of layer 1, 8 of 2048 x 8192, 1024 each: 2.93, 3.01, 8 of 512
+// x 2048, 4096 each: 0.97, 0.93; 64 with four groups, rows of 8 experts 2048 x 4096,
+// 256 each, one round of 128: 1.24, 0.80.
 static bool wide_f32(int64_t tiles, int cus) { return tiles >= 8 * cus; }
 
 // A split tile's description for the second kernel.
