@@ -31,20 +31,22 @@ __device__ __forceinline__ SwigluGrad swiglu_grad(float dh, float g, float u) {
 // step (bf16 64, f32 128 terms) takes `step` with few workgroups at work and
 // step + more with all, storing a unit's sums and reading them once more `store`
 // of the whole card's bandwidth, the second kernel 6.  Measured (whole, split):
-// 60 rows, 448 x 8576, one expert, 2 tiles of 268 steps: 178, 34 us; 1000 rows,
-// 1024 x 4096, 4 experts: 149, 78; weights of 8 experts 256 x 512, 32768 rows:
-// 132, 65.
+// layer 0's rows, 60 of 448 x 8576, one expert, 2 tiles of 268 steps: 178, 36 us.
+// A weights' step, both operands read turned and none shared by many workgroups,
+// takes longer: 8 experts 256 x 512, 32768 rows: 121, 57 (with the rows' cost 65);
+// layer 1 of one 576 x 4224, 3311 rows, 51 tiles of 52 steps: 77, 48 (62).
 struct SplitCost {
   float step, more, store;
 };
 constexpr SplitCost kSplitBf16{0.65f, 0.75f, 0.1f};
+constexpr SplitCost kSplitWeights{1.5f, 0.4f, 0.06f};
 constexpr SplitCost kSplitF32{2.0f, 0.0f, 0.01f};
 __host__ __device__ inline int split_parts(const SplitCost& c, int r, int nk, int grid) {
   if (r <= 0) return 1;
   int best = 1;
   float least = 0.f;
   const int most = nk / 2 < grid / r ? nk / 2 : grid / r;
-  for (int s = 1; s <= most; s += (s + 1) / 2) {  // 1, 2, 3, 5, 8, 12, ...
+  for (int s = 1; s <= most; s += 1 + s / 8) {  // 1 .. 8, 10, 12, ...
     const float units = (float)(r * s);
     const float t = (float)((nk + s - 1) / s) * (c.step + c.more * units / (float)grid) + (s > 1 ? c.store * units + 6.0f : 0.0f);
     if (s == 1 || t < least) {
@@ -199,7 +201,7 @@ __global__ __launch_bounds__(kGemmThreads) void grad_weights_bf16_kernel(GradGem
   __syncthreads();
   if (a.split.hdr) {
     // steps: the experts' mean
-    s = split_within(a, split_parts(kSplitBf16, r, (offsets[a.G] + a.E * kBK - 1) / (a.E * kBK), grid), r);
+    s = split_within(a, split_parts(kSplitWeights, r, (offsets[a.G] + a.E * kBK - 1) / (a.E * kBK), grid), r);
     if (blockIdx.x == 0 && threadIdx.x == 0) {
       a.split.hdr[0] = s > 1 ? r : 0;
       a.split.hdr[1] = s;
@@ -916,7 +918,7 @@ static GradPlan plan_weights(const GradGemmArgs& a, bool bf16) {
   if (p.wide || p.wave || p.many) return p;
   // the experts' mean of steps, if all rows are kept: with fewer a split pays less
   const int64_t step = a.E * (bf16 ? kBK : 4 * kGfK), mean = (a.R + step - 1) / step, r = tiles(T) % cus;
-  const bool split = split_parts(bf16 ? kSplitBf16 : kSplitF32, (int)r, (int)mean, cus) > 1;
+  const bool split = split_parts(bf16 ? kSplitWeights : kSplitF32, (int)r, (int)mean, cus) > 1;
   p.units = !split ? 0 : r * (mean / 2) < cus ? (int)(r * (mean / 2)) : cus;
   p.unit_bytes = bf16 ? 4 * 16 * 4 * 64 * 16 : 4 * 4 * 64 * 16;
   return p;
