@@ -345,9 +345,10 @@ def test_experts(shape, dtype):
 
 
 @pytest.mark.parametrize("p", [0.0, 0.1])
-def test_rows_larger_than_the_cache(p):
+@pytest.mark.parametrize("M,H", [(3333, 4160), (16500, 832), (33333, 448)])
+def test_rows_larger_than_the_cache(M, H, p):
     # f32 rows of over 96 MiB take other loads
-    M, H, E, k = 3333, 4160, 8, 2
+    E, k = 8, 2
     prob, w, f2s, y = combine_inputs(M, H, E, k, "bf16")
     rng = rng_of(7, 8)
     keep = ref.mask(M, H, p, rng, DEV) if p else None
