@@ -593,10 +593,12 @@ def test_a_training_step_is_the_layers_gradient(dtype, p, kw):
             assert abs(diff - mine) <= 1e-4 * abs(mine), (n, diff, mine)
 
 
+# small tiles; large ones; reductions cut into parts (rows, weights)
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
-def test_graph_replays_equal_eager(dtype):
-    a = Step(300, 256, 320, 8, 2, dtype, 0.25, out=dtype, seed=12)
-    b = Step(300, 256, 320, 8, 2, dtype, 0.25, out=dtype, seed=12)
+@pytest.mark.parametrize("sizes", [(300, 256, 320, 8, 2), (2500, 832, 1088, 4, 2), (60, 448, 6272, 1, 1), (12000, 256, 320, 2, 1)])
+def test_graph_replays_equal_eager(sizes, dtype):
+    a = Step(*sizes, dtype, 0.25, out=dtype, seed=12)
+    b = Step(*sizes, dtype, 0.25, out=dtype, seed=12)
     side = torch.cuda.Stream()
     side.wait_stream(torch.cuda.current_stream())
     with torch.cuda.stream(side):
@@ -622,8 +624,10 @@ def test_graph_replays_equal_eager(dtype):
             assert torch.equal(got[n], want[n]), (rep, n)
 
 
-def test_two_steps_at_once_on_two_streams():
-    steps = [Step(800, 256, 448, 8, 2, "bf16", 0.1, seed=1), Step(500, 512, 256, 16, 4, "bf16", 0.5, seed=2)]
+@pytest.mark.parametrize("first,second", [((800, 256, 448, 8, 2), (500, 512, 256, 16, 4)),
+                                          ((2500, 832, 1088, 4, 2), (60, 448, 6272, 1, 1))])
+def test_two_steps_at_once_on_two_streams(first, second):
+    steps = [Step(*first, "bf16", 0.1, seed=1), Step(*second, "bf16", 0.5, seed=2)]
     serial = []
     for s in steps:
         serial.append({n: v.clone() for n, v in s.run().items()})
