@@ -842,12 +842,15 @@ static int64_t wave_tiles(const GradGemmArgs& a, int N) {
 // 256 tokens, 256 x 512 (1.5 tiles a CU of 4 steps): 13.1, 7.9; 2048 there (8.5):
 // 18.0, 19.6; 35, 3 of 3968 x 64 (8 tiles, 62 steps): 42, 12.7; 1000, 1024 x 1024 (8.8
 // a CU, 16): 34, 45.  Rows of layer 1: 256, 256 x 512: 14.5, 8.4; 2048 there: 25, 17;
-// 1000, 1024 x 1024: 38, 36; layer 0: 256, 256 x 512 (0.8, 16): 21, 9; 1000, 1024 x 1024
-// (8.8, 32): 47, 58; 60, one of 448 x 8576 (14 tiles, 268): 34, 36 (the large tiles cut
-// into parts).
+// 1000, 2048 x 512 (4.4, 32): 39, 34; 512, 16 of 1024 x 1024, top 4 (10, 16): 38, 48;
+// 6265, 44 of 3456 x 64 (3.4, 54): 90, 57; layer 0: 256, 256 x 512 (0.8, 16): 21, 9;
+// 1000, 1024 x 1024 (8.8, 32): 47, 58; 60, one of 448 x 8576 (14 tiles, 268): 34, 36
+// (the large tiles cut into parts).
 static bool wave_rows(const GradGemmArgs& a, bool bf16, int N, int K, int cus) {
   const int64_t tiles = wave_tiles(a, N), steps = K / kBK;
-  return bf16 ? tiles * (steps + 4) <= 200 * cus && steps <= 192 : tiles <= 8 * cus && K <= 2048;
+  if (!bf16) return tiles <= 8 * cus && K <= 2048;
+  // (of fewer than 256 columns a large tile is partly empty)
+  return tiles * (steps + 4) <= (N < 256 ? 256 : 170) * cus && steps <= 192;
 }
 static bool wave_keep(const GradGemmArgs& a, bool bf16, int cus) {
   const int64_t tiles = wave_tiles(a, a.F), steps = a.H / kBK;
