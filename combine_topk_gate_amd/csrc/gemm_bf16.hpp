@@ -68,7 +68,7 @@ struct Bf16GemmArgs {
   // row sorted_to_flat[r] / topk of x directly, so X_perm need not be written
   const int32_t* s2f;
   int topk;
-  int64_t M;
+  int64_t M;  // rows of a
 };
 
 __device__ __forceinline__ __amdgpu_buffer_rsrc_t make_rsrc(const void* base, uint32_t bytes) {

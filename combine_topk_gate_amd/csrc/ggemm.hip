@@ -62,7 +62,7 @@ __global__ __launch_bounds__(kGemmThreads) void grouped_gemm_bf16_kernel(Bf16Gem
   __shared__ __attribute__((aligned(16))) char lds[kGemmLdsBytes];
   __shared__ TileLds tl;
   const int NT = (args.N + (LAYER == 0 ? kL0Cols : kL1Cols) - 1) / (LAYER == 0 ? kL0Cols : kL1Cols);
-  const int T = build_tile_table(offsets, G, kTileRows, tl) * NT;
+  const int T = build_tile_table(offsets, G, kTileRows, tl, (int)args.M) * NT;
   const int64_t rtb = (int64_t)kTileRows * args.K * 2;  // bytes of a tile's operand panel (bf16)
   const int grid = gridDim.x;
   const int r = T % grid;
@@ -140,7 +140,7 @@ __global__ __launch_bounds__(kGemmThreads) void grouped_gemm_bf16_expert_kernel(
   __shared__ int rowpos[kTileRows];
   const int EL = args.E, S = G / EL;
   const int NT = (args.N + (LAYER == 0 ? kL0Cols : kL1Cols) - 1) / (LAYER == 0 ? kL0Cols : kL1Cols);
-  const int T = build_expert_tile_table(offsets, G, EL, kTileRows, tl) * NT;
+  const int T = build_expert_tile_table(offsets, G, EL, kTileRows, tl, (int)args.M) * NT;
   const int64_t rtb = (int64_t)kTileRows * args.K * 2;
   const int grid = gridDim.x;
   const int r = T % grid;
@@ -175,7 +175,7 @@ __global__ __launch_bounds__(kGemmThreads) void grouped_gemm_mx_kernel(Bf16GemmA
   __shared__ __attribute__((aligned(16))) char lds[kGemmLdsBytes];
   __shared__ TileLds tl;
   const int NT = (args.N + kL1Cols - 1) / kL1Cols;
-  const int T = build_tile_table(offsets, G, kTileRows, tl) * NT;
+  const int T = build_tile_table(offsets, G, kTileRows, tl, (int)args.M) * NT;
   const int64_t rtb = (int64_t)kTileRows * args.K;  // bytes of a tile's operand panel (fp8 codes)
   const int grid = gridDim.x;
   const int r = T % grid;
@@ -303,14 +303,15 @@ template <int LAYER>
 __global__ __launch_bounds__(256) void grouped_gemm_f32_kernel(const float* __restrict__ A,
                                                                const float* __restrict__ W0,
                                                                const float* __restrict__ W1, float* __restrict__ C,
-                                                               int K, int N, int E, const int32_t* __restrict__ offsets,
-                                                               int G, uint32_t shuffle) {
+                                                               int R, int K, int N, int E,
+                                                               const int32_t* __restrict__ offsets, int G,
+                                                               uint32_t shuffle) {
   __shared__ float xs[kF32Rows][kF32BK + 1];
   __shared__ float ws[kF32Rows][kF32BK + 1];
   __shared__ TileLds tl;
   constexpr int cols = (LAYER == 0) ? kF32Rows / 2 : kF32Rows;
   const int NT = (N + cols - 1) / cols;
-  const int total = build_tile_table(offsets, G, kF32Rows, tl) * NT;
+  const int total = build_tile_table(offsets, G, kF32Rows, tl, R) * NT;
   const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
   const Shuffle sm = make_shuffle(shuffle, total);
   for (int v = blockIdx.x; v < total; v += gridDim.x) {
@@ -403,7 +404,7 @@ hipError_t launch_grouped_gemm_bf16(const GemmProblem& gp, hipStream_t s) {
   a.E = gp.E;
   a.s2f = nullptr;
   a.topk = 1;
-  a.M = 0;
+  a.M = gp.R;
   a.c_scale = nullptr;
   a.a_scale = nullptr;
   a.w_scale = nullptr;
@@ -411,7 +412,6 @@ hipError_t launch_grouped_gemm_bf16(const GemmProblem& gp, hipStream_t s) {
   const int grid = device_cu_count();
   const int xcd_slots = grid / kXcds > 0 ? grid / kXcds : 1;
   if (gp.rowmap) {
-    a.M = gp.R;  // rows of the token-row buffer, read at their own positions
     if (gp.layer == 0)
       grouped_gemm_bf16_expert_kernel<0><<<grid, kGemmThreads, 0, s>>>(a, gp.offsets, gp.G, xcd_slots, gp.shuffle);
     else
@@ -446,7 +446,7 @@ hipError_t launch_grouped_gemm_mx(const GemmProblem& gp, hipStream_t s) {
   a.E = gp.E;
   a.s2f = nullptr;
   a.topk = 1;
-  a.M = 0;
+  a.M = gp.R;
   a.c_scale = nullptr;
   a.a_scale = nullptr;
   a.w_scale = nullptr;
@@ -492,10 +492,12 @@ hipError_t launch_grouped_gemm_f32(const GemmProblem& gp, hipStream_t s) {
   const int grid = device_cu_count() * 2;
   if (gp.layer == 0)
     grouped_gemm_f32_kernel<0><<<grid, 256, 0, s>>>((const float*)gp.a, (const float*)gp.w0, (const float*)gp.w1,
-                                                     (float*)gp.c, gp.K, gp.N, gp.E, gp.offsets, gp.G, gp.shuffle);
+                                                     (float*)gp.c, (int)gp.R, gp.K, gp.N, gp.E, gp.offsets, gp.G,
+                                                     gp.shuffle);
   else
     grouped_gemm_f32_kernel<1><<<grid, 256, 0, s>>>((const float*)gp.a, (const float*)gp.w0, nullptr,
-                                                    (float*)gp.c, gp.K, gp.N, gp.E, gp.offsets, gp.G, gp.shuffle);
+                                                    (float*)gp.c, (int)gp.R, gp.K, gp.N, gp.E, gp.offsets, gp.G,
+                                                    gp.shuffle);
   return hipGetLastError();
 }
 

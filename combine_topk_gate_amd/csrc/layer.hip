@@ -235,7 +235,7 @@ __global__ __launch_bounds__(kGemmThreads) void fused_layer_kernel(FusedArgs a) 
   __shared__ float comb_w[kCombineTokens * 16];
   __shared__ int comb_cnt[kCombineTokens];
 
-  const int MT = build_tile_table(a.offsets, a.G, kTileRows, tl);
+  const int MT = build_tile_table(a.offsets, a.G, kTileRows, tl, (int)(a.M * a.k));
   const int nt0 = (a.F + kL0Cols - 1) / kL0Cols;
   const int nt1 = (a.H + kL1Cols - 1) / kL1Cols;
   const int nc = (nt1 + kChunkTiles - 1) / kChunkTiles;

@@ -34,14 +34,16 @@ struct TileLds {
 };
 
 // Fills seg_start, seg_rows and mt_start from offsets; returns the number of
-// M-tiles.  All threads of the block (<= 256) must call it.
-__device__ inline int build_tile_table(const int32_t* __restrict__ offsets, int G, int rows, TileLds& t) {
+// M-tiles.  The segments are kept inside rows 0 .. R - 1, whatever the offsets
+// say, so bad ones reach no memory outside the row buffers.  All threads of the
+// block (<= 256) must call it.
+__device__ inline int build_tile_table(const int32_t* __restrict__ offsets, int G, int rows, TileLds& t, int R) {
   const int nthr = blockDim.x;
   const int per = (G + nthr - 1) / nthr;
   const int g0 = threadIdx.x * per;
   int run = 0;
   for (int g = g0; g < g0 + per && g < G; ++g) {
-    const int a = offsets[g], b = offsets[g + 1];
+    const int a = min(max(offsets[g], 0), R), b = min(max(offsets[g + 1], a), R);
     t.seg_start[g] = a;
     t.seg_rows[g] = b - a;
     run += (b - a + rows - 1) / rows;
@@ -71,10 +73,10 @@ __device__ inline int build_tile_table(const int32_t* __restrict__ offsets, int 
 // rows of several small segments of the same expert and every weight panel
 // serves full tiles.  Fills seg_start and seg_rows of the G segments,
 // expert_rows[e] and mt_start[e] (prefix of the experts' M-tile counts);
-// returns the number of M-tiles.  The segments are kept inside rows 0 .. R - 1,
-// whatever the offsets say.  All threads of the block call it.
+// returns the number of M-tiles.  The segments are kept inside rows 0 .. R - 1
+// as above.  All threads of the block call it.
 __device__ inline int build_expert_tile_table(const int32_t* __restrict__ offsets, int G, int EL, int rows,
-                                              TileLds& t, int R = 0x7FFFFFFF) {
+                                              TileLds& t, int R) {
   for (int g = threadIdx.x; g < G; g += blockDim.x) {
     const int a = min(max(offsets[g], 0), R), b = min(max(offsets[g + 1], a), R);
     t.seg_start[g] = a;
