@@ -83,17 +83,17 @@ __device__ inline int build_expert_tile_table(const int32_t* __restrict__ offset
     t.seg_rows[g] = b - a;
   }
   __syncthreads();
-  // the first wave counts and scans: a lane's experts are `per` consecutive ones
+  for (int e = threadIdx.x; e < EL; e += blockDim.x) {
+    int n = 0;
+    for (int s = 0; s < G / EL; ++s) n += t.seg_rows[s * EL + e];
+    t.expert_rows[e] = n;
+  }
+  __syncthreads();
+  // the first wave scans: a lane's experts are `per` consecutive ones
   if (threadIdx.x < kWave) {
-    const int S = G / EL, lane = threadIdx.x;
-    const int per = (EL + kWave - 1) / kWave, e0 = lane * per;
+    const int lane = threadIdx.x, per = (EL + kWave - 1) / kWave, e0 = lane * per;
     int run = 0;
-    for (int e = e0; e < e0 + per && e < EL; ++e) {
-      int n = 0;
-      for (int s = 0; s < S; ++s) n += t.seg_rows[s * EL + e];
-      t.expert_rows[e] = n;
-      run += (n + rows - 1) / rows;
-    }
+    for (int e = e0; e < e0 + per && e < EL; ++e) run += (t.expert_rows[e] + rows - 1) / rows;
     int acc = run;
 #pragma unroll
     for (int off = 1; off < kWave; off <<= 1) {
