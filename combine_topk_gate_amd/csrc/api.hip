@@ -384,11 +384,11 @@ GradGemmArgs grad_args(const moe_problem_t* p, int layer, const int32_t* offsets
   g.layer = layer;
   g.offsets = offsets;
   g.R = p->num_tokens * p->topk;
+  g.rows = kept_rows(p);
   g.H = p->hidden;
   g.F = p->ffn;
   g.E = held(p);
   g.G = segments(p);
-  g.all_held = held(p) == p->num_experts;
   g.shuffle = debug_shuffle();
   return g;
 }

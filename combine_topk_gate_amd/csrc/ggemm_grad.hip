@@ -811,8 +811,10 @@ __global__ __launch_bounds__(64 * WAVES) void wave_weights_kernel(GradGemmArgs a
 
 // ------------------------------------------------------------------ launch ---
 // How a call splits: the units that its workspace holds (0: no tile is split),
-// by sizes that the host knows.  The number of row tiles of a rows' gradient
-// depends on the routing, between `lo` and `hi`.
+// by sizes that the host knows.  Which tiles a call takes goes by the rows that
+// an even routing keeps (a.rows: of a share of the experts its part of all R).
+// The number of row tiles of a rows' gradient depends on the routing, between
+// `lo` and `hi`; the workspace holds what any routing can need.
 struct GradPlan {
   int units = 0;
   bool wide = false;  // f32: tiles of 128
@@ -823,9 +825,11 @@ struct GradPlan {
 };
 
 // Tiles of 32 x 32 that an even routing gives, N columns wide.
+// (A share of the experts taken for half of all pairs, as if it were large, and so:
+// kept, 512 tokens, 2 of 8 of 2048 x 1408, top 2: 39.6, 18.4 us; rows of layer 1, 4096, 8
+// of 128 of 256 x 512, top 8: 23.7, 12.3; f32, 512, 8 of 64 of 2048 x 1408: 97, 65.)
 static int64_t wave_tiles(const GradGemmArgs& a, int N) {
-  const int64_t rows = a.all_held ? a.R : a.R / 2;
-  return (rows / 32 + (rows < a.E ? rows : a.E)) * (N / 32);
+  return (a.rows / 32 + (a.rows < a.E ? a.rows : a.E)) * (N / 32);
 }
 // f32: the kept products take them always (tiles of 64 x 64 of both products through
 // common LDS buffers, these: 256 tokens, 8 experts 256 x 512, top 2: 18.8, 11.9
@@ -875,21 +879,26 @@ static hipError_t launch_wave(const GradGemmArgs& g, int N, hipStream_t s) {
 // 1024 rows (2048): 190, 164; 4 of 1024 x 512 (512): 54, 56; rows of layer 1, 82 experts
 // 192 x 12288, 25 rows each: 572, 374; 4 of 2048 x 2048, 256 each (2.3 a CU): 123, 132;
 // of layer 0, 8 of 2048 x 1024, 1024 each (17 a CU): 772, 715.
-constexpr int kManyRows = 3, kManyWeights = 4;  // tiles a CU
+// Rows of reductions up to 1024 terms so from more than two a CU on, a third round of
+// four groups being nearly empty: layer 1, 8 of 512 x K, 2.2 and 2.6 a CU, K = 256: 37,
+// 28 and 36, 28; 512: 52, 41 and 52, 42; 1024: 75, 71 and 83, 72; 2048: 124, 133 and
+// 151, 136; 4096: 216, 254 and 277, 257.
+static bool many_rows(int64_t tiles, int K, int cus) { return K <= 1024 ? tiles > 2 * cus : tiles >= 3 * cus; }
+constexpr int kManyWeights = 4;  // tiles a CU
 
 static GradPlan plan_rows(const GradGemmArgs& a, bool bf16) {
   GradPlan p;
   const int cus = device_cu_count(), rows = bf16 ? kTileRows : 64, cols = bf16 ? 256 : 64;
   const int N = a.layer == 0 ? a.H : a.F, K = a.layer == 0 ? 2 * a.F : a.H, NT = (N + cols - 1) / cols;
-  p.wide = !bf16 && wide_f32(a.R / 128 * ((N + 127) / 128), cus);
+  p.wide = !bf16 && wide_f32(a.rows / 128 * ((N + 127) / 128), cus);
   p.wave = !p.wide && wave_rows(a, bf16, N, K, cus);
   if (p.wide || p.wave) return p;
   // (half the experts end in a tile of their own more than their rows fill)
-  p.many = !bf16 && ((a.all_held ? a.R : a.R / 2) / 64 + (a.R < a.E ? a.R : a.E) / 2) * NT >= kManyRows * cus;
+  p.many = !bf16 && many_rows((a.rows / 64 + (a.rows < a.E ? a.rows : a.E) / 2) * NT, K, cus);
   if (p.many) return p;
   const SplitCost& c = bf16 ? kSplitBf16 : kSplitF32;
   const int steps = bf16 ? K / kBK : K / kGfK / 4;
-  const int64_t hi = a.R / rows + (a.R < a.E ? a.R : a.E), lo = a.all_held ? (a.R + rows - 1) / rows : 0;
+  const int64_t hi = a.R / rows + (a.R < a.E ? a.R : a.E), lo = a.rows == a.R ? (a.R + rows - 1) / rows : 0;
   bool split = false;
   if (hi - lo > 16)
     split = split_parts(c, 1, steps, cus) > 1;
@@ -902,11 +911,11 @@ static GradPlan plan_rows(const GradGemmArgs& a, bool bf16) {
 }
 
 // bf16 weights' gradients; steps: an expert's mean.  Measured (large tiles, these):
-// layer 0, 545 tokens, one expert 320 x 384 held (240 tiles, 17 steps): 18.4, 7.9;
-// 256, 8 of 256 x 512, top 2 (2048, 1): 13.7, 9.6; 2048 there (8 steps): 24.2, 20.4;
+// layer 0, 256 tokens, 8 of 256 x 512, top 2 (2048, 1): 13.7, 9.6; 2048 there (8 steps):
+// 24.2, 20.4; 4096, 2 of 16 of 1024 x 512 held, top 2 (2048, 8): 26.3, 21.4;
 // 1000, 8 of 512 x 512 (4096, 3): 18.9, 25.8; layer 1 of it (2048, 3): 17.3, 14.9.
 static bool wave_weights(const GradGemmArgs& a, int64_t tiles, int cus) {
-  const int64_t steps = (a.all_held ? a.R : a.R / 2) / (a.E * kBK);
+  const int64_t steps = a.rows / (a.E * kBK);
   return tiles * (steps + 4) <= (steps < 8 ? 64 : 96) * cus;
 }
 
@@ -919,10 +928,17 @@ static GradPlan plan_weights(const GradGemmArgs& a, bool bf16) {
   p.wave = bf16 && wave_weights(a, tiles(32), cus);
   p.many = !bf16 && tiles(64) >= kManyWeights * cus;
   if (p.wide || p.wave || p.many) return p;
-  // the experts' mean of steps, if all rows are kept: with fewer a split pays less
-  const int64_t step = a.E * (bf16 ? kBK : 4 * kGfK), mean = (a.R + step - 1) / step, r = tiles(T) % cus;
+  // f32, no split and few steps for the groups to share: one group too, below 160 rows an expert where a round holds all
+  // tiles and 512 where not.  Measured (four groups, one), weights of layer 1, 8 experts 256 x 512 (a round): 64 rows
+  // each 9.5, 8.6 us; 128: 12.1, 12.4; 192: 15.0, 15.9; 256: 17.4, 19.4; 384: 21.3, 25.2; 3 of 2048 x 512 (1.5): 64:
+  // 18.8, 11.9; 256: 29.9, 23.3; 384: 36.8, 30.2; 512: 44.2, 37.8; 5 of 576 x 704 (2.1): 384: 30.5, 27.4.
+  const bool few = !bf16 && a.rows < a.E * (tiles(64) <= cus ? 160ll : 512ll);
+  // the experts' mean of steps: of an even routing, for whether a split pays, and the most (all rows kept), for its units
+  const int64_t step = a.E * (bf16 ? kBK : 4 * kGfK), mean = (a.rows + step - 1) / step, most = (a.R + step - 1) / step;
+  const int64_t r = tiles(T) % cus;
   const bool split = split_parts(bf16 ? kSplitWeights : kSplitF32, (int)r, (int)mean, cus) > 1;
-  p.units = !split ? 0 : r * (mean / 2) < cus ? (int)(r * (mean / 2)) : cus;
+  p.units = !split ? 0 : r * (most / 2) < cus ? (int)(r * (most / 2)) : cus;
+  p.many = few && !split;
   p.unit_bytes = bf16 ? 4 * 16 * 4 * 64 * 16 : 4 * 4 * 64 * 16;
   return p;
 }
@@ -1013,9 +1029,7 @@ hipError_t launch_grad_weights(const GradGemmArgs& a, bool bf16, void* ws, hipSt
     grad_weights_f32_kernel<128, 2><<<cus, 512, 0, s>>>(g);
     return hipGetLastError();
   }
-  // many tiles, or fewer steps than the groups can share: one group a tile, four workgroups a CU (8 experts 256 x 7680,
-  // a row each: 34 us with four groups, 23 with one; 8 experts 256 x 512, 64 rows each: 13.5, 9.4)
-  if (p.many || (a.R < 4ll * a.E * 4 * kGfK && !p.units)) {
+  if (p.many) {  // one group a tile, four workgroups a CU
     grad_weights_f32_kernel<64, 1><<<4 * cus, 256, 0, s>>>(g);
     return hipGetLastError();
   }

@@ -133,14 +133,14 @@ struct GradGemmArgs {
   void* o2;        // kept products (launch_keep): Hact; o0, o1: gate, up
   const int32_t* offsets;
   int64_t R;
+  int64_t rows;    // of them, those that an even routing keeps: all, or the share of the experts held
   int H, F, E, G;  // E: experts held
-  int all_held;    // no pair is dropped
   int out_bf16;    // weights: type of o0, o1
   int accumulate;  // weights: add to what o0, o1 hold (f32)
   uint32_t shuffle;
   GradSplit split;
 };
-// Workspace of the split tiles' sums, for either layer, rows and weights (R, H, F, E and all_held of a).
+// Workspace of the split tiles' sums, for either layer, rows and weights (R, rows, H, F, E and G of a).
 size_t grad_ws_bytes(const GradGemmArgs& a, bool bf16);
 hipError_t launch_grad_rows(const GradGemmArgs& a, bool bf16, void* ws, hipStream_t s);
 hipError_t launch_grad_weights(const GradGemmArgs& a, bool bf16, void* ws, hipStream_t s);
