@@ -201,7 +201,7 @@ __global__ __launch_bounds__(kGemmThreads) void grad_weights_bf16_kernel(GradGem
   __syncthreads();
   if (a.split.hdr) {
     // steps: the experts' mean
-    s = split_within(a, split_parts(kSplitWeights, r, (offsets[a.G] + a.E * kBK - 1) / (a.E * kBK), grid), r);
+    s = split_within(a, split_parts(kSplitWeights, r, (offsets[a.G] + a.fill + a.E * kBK - 1) / (a.E * kBK), grid), r);
     if (blockIdx.x == 0 && threadIdx.x == 0) {
       a.split.hdr[0] = s > 1 ? r : 0;
       a.split.hdr[1] = s;
@@ -444,7 +444,7 @@ __global__ __launch_bounds__(256 * KG) void grad_weights_f32_kernel(GradGemmArgs
   const int N = l0 ? a.F : a.H, C = l0 ? a.H : a.F;  // rows and columns of dW
   const int NR = (N + TX - 1) / TX, NC = (C + TX - 1) / TX, S = a.G / a.E, mats = l0 ? 2 : 1, grid = gridDim.x;
   const int T = a.E * mats * NR * NC;
-  const int r = T % grid, mean = (offsets[a.G] + a.E * kGfK - 1) / (a.E * kGfK);
+  const int r = T % grid, mean = (offsets[a.G] + a.fill + a.E * kGfK - 1) / (a.E * kGfK);
   const int s = a.split.hdr ? split_within(a, split_parts(kSplitF32, r, mean / KG, grid), r) : 1;
   const int whole = s > 1 ? T - r : T, entries = whole + (s > 1 ? r * s : 0);
   const Shuffle sm = make_shuffle(a.shuffle, whole), sh = make_shuffle(a.shuffle, T - whole);
@@ -910,13 +910,30 @@ static GradPlan plan_rows(const GradGemmArgs& a, bool bf16) {
   return p;
 }
 
+// Zero rows that the K steps of the weights' gradients run over beside `rows` evenly
+// routed ones: they fill up every segment's last step (of `step` rows).  Of one source
+// block not counted; of several half a step for each further segment, and a step for
+// each at least, as far as there are rows (16 experts, 32 blocks, 8 rows a segment: 32
+// steps of 64 an expert, the rows alone 4).  Measured (rows alone, so; layer 1, bf16):
+// 16 experts 512 x 512, 8 blocks, 4 rows a segment: 28.6, 22.0 us; 256 x 512, 32 blocks,
+// 4 rows: 41.3, 37.1; 12800 rows in 8 blocks: 33.0, 31.5; 8 experts 256 x 512, 32768 rows
+// in 8: 42.6, 44.9.  (Counted from the offsets on the device, 1.2 us a call more.)
+static int fill_rows(const GradGemmArgs& a, int64_t rows, int step) {
+  if (a.G == a.E) return 0;
+  const int64_t even = (int64_t)(a.G - a.E) * step / 2, least = (a.G < rows ? a.G : rows) * step - rows;
+  return (int)(rows < a.G || least > even ? least : even);
+}
+
 // bf16 weights' gradients; steps: an expert's mean.  Measured (large tiles, these):
 // layer 0, 256 tokens, 8 of 256 x 512, top 2 (2048, 1): 13.7, 9.6; 2048 there (8 steps):
 // 24.2, 20.4; 4096, 2 of 16 of 1024 x 512 held, top 2 (2048, 8): 26.3, 21.4;
-// 1000, 8 of 512 x 512 (4096, 3): 18.9, 25.8; layer 1 of it (2048, 3): 17.3, 14.9.
+// 1000, 8 of 512 x 512 (4096, 3): 18.9, 25.8; layer 1 of it (2048, 3): 17.3, 14.9;
+// of 8 experts 256 x C, T tiles a CU, at s steps: T 2, s 40: 30, 26; 64: 33, 38; T 4, 16:
+// 27, 23; 24: 30, 31; T 6, 16: 30, 28; 24: 32, 38; T 8, 8: 25, 24; 12: 30, 30; 16: 31,
+// 37; T 10, 2: 15.8, 14.9; 4: 18.7, 19.8; T 12, 1: 14.2, 14.1; 2: 15.9, 17.3; T 16, 1: 14.8, 17.3.
 static bool wave_weights(const GradGemmArgs& a, int64_t tiles, int cus) {
-  const int64_t steps = a.rows / (a.E * kBK);
-  return tiles * (steps + 4) <= (steps < 8 ? 64 : 96) * cus;
+  const int64_t steps = (a.rows + fill_rows(a, a.rows, kBK)) / (a.E * kBK);
+  return tiles * (steps + 4) <= (tiles <= 4 * cus ? 104 : tiles <= 8 * cus ? 128 : 64) * cus;
 }
 
 static GradPlan plan_weights(const GradGemmArgs& a, bool bf16) {
@@ -934,7 +951,11 @@ static GradPlan plan_weights(const GradGemmArgs& a, bool bf16) {
   // 18.8, 11.9; 256: 29.9, 23.3; 384: 36.8, 30.2; 512: 44.2, 37.8; 5 of 576 x 704 (2.1): 384: 30.5, 27.4.
   const bool few = !bf16 && a.rows < a.E * (tiles(64) <= cus ? 160ll : 512ll);
   // the experts' mean of steps: of an even routing, for whether a split pays, and the most (all rows kept), for its units
-  const int64_t step = a.E * (bf16 ? kBK : 4 * kGfK), mean = (a.rows + step - 1) / step, most = (a.R + step - 1) / step;
+  const auto steps = [&](int64_t rows) {
+    const int64_t step = a.E * (bf16 ? kBK : 4 * kGfK);
+    return (rows + fill_rows(a, rows, bf16 ? kBK : kGfK) + step - 1) / step;
+  };
+  const int64_t mean = steps(a.rows), most = steps(a.R);
   const int64_t r = tiles(T) % cus;
   const bool split = split_parts(bf16 ? kSplitWeights : kSplitF32, (int)r, (int)mean, cus) > 1;
   p.units = !split ? 0 : r * (most / 2) < cus ? (int)(r * (most / 2)) : cus;
@@ -1019,7 +1040,8 @@ static hipError_t launch_wave_weights(const GradGemmArgs& g, hipStream_t s) {
 hipError_t launch_grad_weights(const GradGemmArgs& a, bool bf16, void* ws, hipStream_t s) {
   const int cus = device_cu_count();
   const GradPlan p = plan_weights(a, bf16);
-  const GradGemmArgs g = with_split(a, p, ws);
+  GradGemmArgs g = with_split(a, p, ws);
+  g.fill = fill_rows(a, a.rows, bf16 ? kBK : kGfK);
   if (p.wave) return launch_wave_weights(g, s);
   if (bf16) {
     grad_weights_bf16_kernel<<<cus, kGemmThreads, 0, s>>>(g);

@@ -135,6 +135,7 @@ struct GradGemmArgs {
   int64_t R;
   int64_t rows;    // of them, those that an even routing keeps: all, or the share of the experts held
   int H, F, E, G;  // E: experts held
+  int fill;        // weights: zero rows in the K steps of an even routing (set by the launcher)
   int out_bf16;    // weights: type of o0, o1
   int accumulate;  // weights: add to what o0, o1 hold (f32)
   uint32_t shuffle;

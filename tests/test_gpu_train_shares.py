@@ -1,6 +1,7 @@
 """The experts' gradients of a share of the experts (expert-parallel), whose tiles
 are chosen by the rows that an even routing keeps: shares of 1/4 to 1/16, evenly
-routed and crowded far past that, with source blocks."""
+routed and crowded far past that, with source blocks; and short segments of many
+blocks, each of which fills a step."""
 import pytest
 
 import test_gpu_train as train
@@ -18,7 +19,12 @@ SHARES = [dict(M=512, H=1024, F=512, E=16, k=8, held=2, base=7), dict(M=300, H=5
           dict(M=40, H=256, F=320, E=8, k=2, held=2, base=3, skip=(3, 4))]
 
 
+# short segments of many source blocks
+BLOCKS = [dict(M=2048, H=256, F=512, E=16, k=1, S=32), dict(M=512, H=512, F=512, E=16, k=1, S=8), dict(M=600, H=320, F=448, E=4, k=2, S=64),
+          dict(M=12000, H=256, F=320, E=8, k=1, S=8), dict(M=40, H=192, F=256, E=30, k=1, S=30), dict(M=700, H=1088, F=448, E=32, k=2, S=16, held=4, base=11)]
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
-@pytest.mark.parametrize("shape", SHARES)
+@pytest.mark.parametrize("shape", SHARES + BLOCKS)
 def test_experts_of_a_share(shape, dtype):
     train.test_experts(shape, dtype)

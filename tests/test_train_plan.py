@@ -35,3 +35,10 @@ def test_a_small_share_takes_small_tiles(M, H, F, E, held, k):
 def test_a_share_of_long_f32_products_is_cut_as_its_rows_are(M, H, F, E, held, k):
     assert need(M * k * held // E, H, F, held, 1, dtype="f32") > 0
     assert need(M, H, F, E, k, dtype="f32", expert_base=E // 2, local_experts=held) > 0
+
+
+@pytest.mark.parametrize("M,H,F,E,S", [(4096, 256, 512, 16, 32), (2048, 512, 512, 16, 32)])
+def test_short_segments_of_many_blocks_count_a_step_each(M, H, F, E, S):
+    # the rows alone are two to four steps of 64 an expert, its segments 32: a long reduction, which is cut
+    assert need(M, H, F, E, 1) == 0
+    assert need(M, H, F, E, 1, S) > 0
