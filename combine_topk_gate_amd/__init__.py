@@ -308,14 +308,14 @@ def moe_layer_ex(p, x, logits, src_block, w_gate, w_up, w_down, epi, out, ws, au
 
 def _refuse(what, name, t, dtype, shape):
     raise MoeError(MOE_ERR_INVALID_ARGUMENT,
-                   f"{what}: {name} must be a contiguous {dtype} tensor of shape {shape} on the GPU that holds x; "
+                   f"{what}: {name} must be a contiguous {dtype} tensor of shape {shape} on the call's GPU; "
                    f"got {t.dtype} {tuple(t.shape)} strides {t.stride()} on {t.device}")
 
 
-def _gpu_of(what, x):
-    if x is None:
-        raise MoeError(MOE_ERR_INVALID_ARGUMENT, f"{what}: x is missing")
-    return x.get_device()
+def _gpu_of(what, name, t):
+    if t is None:
+        raise MoeError(MOE_ERR_INVALID_ARGUMENT, f"{what}: {name} is missing")
+    return t.get_device()
 
 
 def _addr(what, name, t, dtype, shape, gpu):
@@ -373,7 +373,7 @@ def moe_layer_decode(p, x, logits, w_gate, w_up, w_down, epi, out, ws, stream=No
     what = "moe_layer_decode"
     f32 = torch.float32
     M, H, F, E, dtype = p.num_tokens, p.hidden, p.ffn, p.num_experts, p.dtype
-    EL, gpu = p.local_experts or E, _gpu_of(what, x)
+    EL, gpu = p.local_experts or E, _gpu_of(what, "x", x)
     act = f32 if dtype == MOE_DTYPE_F32 else torch.bfloat16
     odt = torch.bfloat16 if epi is not None and epi.out_dtype == MOE_DTYPE_BF16 else f32
     if dtype == MOE_DTYPE_BF16_MXFP8:
@@ -410,7 +410,7 @@ def moe_adapter_linear(q, x, w, a, b, scale, adapter_idx, epi, out, ws, stream=N
     what = "moe_adapter_linear"
     f32 = torch.float32
     M, H, N, r, P = q.num_tokens, q.in_features, q.out_features, q.rank, q.num_adapters
-    gpu = _gpu_of(what, x)
+    gpu = _gpu_of(what, "x", x)
     act = f32 if q.dtype == MOE_DTYPE_F32 else torch.bfloat16
     odt = torch.bfloat16 if epi is not None and epi.out_dtype == MOE_DTYPE_BF16 else f32
     _check(_call_on(gpu, stream, load_library().moe_adapter_linear, ctypes.byref(q),
@@ -446,7 +446,7 @@ def moe_combine_dropout(p, y, topk_w, flat_to_sorted, epi, drop, out, stream=Non
     [M, H] in epi's type."""
     import torch
     what = "moe_combine_dropout"
-    M, H, k, gpu = p.num_tokens, p.hidden, p.topk, _gpu_of(what, y)
+    M, H, k, gpu = p.num_tokens, p.hidden, p.topk, _gpu_of(what, "y", y)
     act, odt = _dtypes(p, epi)
     _check(_call_on(gpu, stream, load_library().moe_combine_dropout, ctypes.byref(p),
                     _addr(what, "y", y, torch.float32, (M * k, H), gpu),
@@ -462,7 +462,7 @@ def moe_combine_backward(p, dout, y, topk_w, flat_to_sorted, drop, dy, dtopk_w, 
     the problem's dtype, dtopk_w [M, k] f32."""
     import torch
     what = "moe_combine_backward"
-    M, H, k, gpu = p.num_tokens, p.hidden, p.topk, _gpu_of(what, dout)
+    M, H, k, gpu = p.num_tokens, p.hidden, p.topk, _gpu_of(what, "dout", dout)
     bf16 = dout.dtype is torch.bfloat16
     _check(_call_on(gpu, stream, load_library().moe_combine_backward, ctypes.byref(p),
                     _addr(what, "dout", dout, torch.bfloat16 if bf16 else torch.float32, (M, H), gpu),
@@ -478,7 +478,7 @@ def moe_dispatch_backward(p, dx_perm, flat_to_sorted, epi, dx, stream=None):
     flat_to_sorted [R] -> dx [M, H] in epi's type (its residual added)."""
     import torch
     what = "moe_dispatch_backward"
-    M, H, k, gpu = p.num_tokens, p.hidden, p.topk, _gpu_of(what, dx_perm)
+    M, H, k, gpu = p.num_tokens, p.hidden, p.topk, _gpu_of(what, "dx_perm", dx_perm)
     act, odt = _dtypes(p, epi)
     _check(_call_on(gpu, stream, load_library().moe_dispatch_backward, ctypes.byref(p),
                     _addr(what, "dx_perm", dx_perm, act, (M * k, H), gpu),
@@ -491,7 +491,7 @@ def moe_route_backward(p, topk_idx, topk_w, dtopk_w, dlogits, stream=None):
     -> dlogits [M, E] f32."""
     import torch
     what = "moe_route_backward"
-    M, E, k, gpu = p.num_tokens, p.num_experts, p.topk, _gpu_of(what, topk_idx)
+    M, E, k, gpu = p.num_tokens, p.num_experts, p.topk, _gpu_of(what, "topk_idx", topk_idx)
     f32 = torch.float32
     _check(_call_on(gpu, stream, load_library().moe_route_backward, ctypes.byref(p),
                     _addr(what, "topk_idx", topk_idx, torch.int32, (M, k), gpu),
@@ -508,7 +508,7 @@ def moe_grouped_gemm_aux(p, a, w0, w1, offsets, gate, up, c, stream=None):
     [R, H], w0, w1 [EL, F, H], offsets [G + 1] -> gate, up, c (Hact) [R, F]."""
     import torch
     what = "moe_grouped_gemm_aux"
-    R, H, F, gpu = p.num_tokens * p.topk, p.hidden, p.ffn, _gpu_of(what, a)
+    R, H, F, gpu = p.num_tokens * p.topk, p.hidden, p.ffn, _gpu_of(what, "a", a)
     EL, act = p.local_experts or p.num_experts, _dtypes(p)[0]
     _check(_call_on(gpu, stream, load_library().moe_grouped_gemm_aux, ctypes.byref(p),
                     _addr(what, "a", a, act, (R, H), gpu), _addr(what, "w0", w0, act, (EL, F, H), gpu),
@@ -525,7 +525,7 @@ def moe_grouped_gemm_backward(p, layer, d0, d1, w0, w1, gate, up, offsets, o0, o
     o1 None).  ws moe_workspace_bytes(p, MOE_OP_GROUPED_GEMM_BACKWARD) bytes."""
     import torch
     what = "moe_grouped_gemm_backward"
-    R, H, F, gpu = p.num_tokens * p.topk, p.hidden, p.ffn, _gpu_of(what, d0)
+    R, H, F, gpu = p.num_tokens * p.topk, p.hidden, p.ffn, _gpu_of(what, "d0", d0)
     EL, act = p.local_experts or p.num_experts, _dtypes(p)[0]
     din, dout = (F, H) if layer == 0 else (H, F)
     wshape = (EL, F, H) if layer == 0 else (EL, H, F)
@@ -545,7 +545,7 @@ def moe_grouped_gemm_backward_weights(p, layer, d0, d1, a, offsets, dw0, dw1, ac
     and dw1 f32 or bf16; accumulate (f32): added to what they hold."""
     import torch
     what = "moe_grouped_gemm_backward_weights"
-    R, H, F, gpu = p.num_tokens * p.topk, p.hidden, p.ffn, _gpu_of(what, a)
+    R, H, F, gpu = p.num_tokens * p.topk, p.hidden, p.ffn, _gpu_of(what, "a", a)
     EL, act = p.local_experts or p.num_experts, _dtypes(p)[0]
     n, m = (F, H) if layer == 0 else (H, F)
     bf16 = dw0 is not None and dw0.dtype is torch.bfloat16
