@@ -179,7 +179,9 @@ def epilogue(residual=None, out_dtype="f32") -> Epilogue:
 
 def dropout(p, rng) -> Dropout:
     """Dropout with probability p (0 <= p < 1) whose mask comes from rng, a device
-    int64 tensor {seed, offset} that the kernels read.  It holds the tensor."""
+    int64 tensor {seed, offset} that the kernels read: one of its own for every
+    layer, step and data-parallel rank, whose masks are else the same.  It holds
+    the tensor."""
     drop = Dropout(float(p), None if rng is None else rng.data_ptr())
     drop.tensor = rng
     return drop

@@ -492,7 +492,11 @@ moe_status_t moe_adapter_tiles(const moe_adapter_problem_t* q, int32_t out_dtype
  * (Salmon et al. 2011) with key {seed low, high} and counter {i low, i high,
  * offset low, high}, i = (t H + n) / 4; the mask is never stored.  rng points
  * to {seed, offset} in DEVICE memory (8-byte aligned), which the kernels read,
- * so a captured graph can be given new ones before each replay.  0 <= p < 1. */
+ * so a captured graph can be given new ones before each replay.  0 <= p < 1.
+ * The mask depends on seed, offset and place alone: every layer, every step and
+ * every data-parallel rank or micro-batch needs a {seed, offset} of its own (say
+ * a seed per layer and rank, an offset per step), or they drop the same places;
+ * the holders of one token's experts (local_experts) need the same one. */
 typedef struct {
   double p;
   const uint64_t* rng;
