@@ -62,7 +62,11 @@ typedef int i32x2_t __attribute__((ext_vector_type(2)));
 // Results are stored, and gate and up loaded, as used once ("nt"): kept like
 // other lines they push the operands' panels, which the tiles of an XCD share,
 // out of its L2 (weights of 64 experts 2048 x 1408, 256 rows each: 466 us, as
-// used once 366; 16 experts 4096 x 6400: 3065, 3047).
+// used once 366; 16 experts 4096 x 6400: 3065, 3047).  The next call of a training
+// step reads most of them, but whole steps gain too (bf16, dropout, kept, as used
+// once): 1024 tokens, 16 experts 2048 x 1408, top 4: 563, 526 us; 4096, 64 of them:
+// 1809, 1748; 2048, 8 of 1024 x 1024, top 2: 270, 270; 8192, 8 of 4096 x 14336:
+// 15.54, 15.48 ms.
 constexpr int kOnce = 2;
 
 __device__ __forceinline__ void buf_store16(__amdgpu_buffer_rsrc_t r, uint32_t voff, i32x4_t v) {

@@ -24,7 +24,9 @@ constexpr int kGradThreads = 256;
 __device__ __forceinline__ bool pair_held(int32_t row, int64_t R) { return (uint64_t)(int64_t)row < (uint64_t)R; }
 
 // Outputs are stored as used once ("nt"), so that they do not wait for the L2 to
-// make room.  f32 rows of a large call are loaded so too (ONCE): from about 96
+// make room, though the next call of a training step reads dY and dX_perm (whole
+// steps, kept and so: 1024 tokens, 16 experts 2048 x 1408, top 4: 533, 526 us; 8192,
+// 16 of them, top 2: 1212, 1201; 1024, 8 of 1024 x 512: 186, 186).  f32 rows of a large call are loaded so too (ONCE): from about 96
 // MiB on they have left the last-level cache (256 MB) since they were written,
 // and loading them there again only pushes out the rest.  Measured with inputs
 // that change from call to call, plain loads and once, tokens of 4096, top 2:
