@@ -26,13 +26,13 @@ __device__ __forceinline__ bool pair_held(int32_t row, int64_t R) { return (uint
 // Outputs are stored as used once ("nt"), so that they do not wait for the L2 to
 // make room, though the next call of a training step reads dY and dX_perm (whole
 // steps, kept and so: 1024 tokens, 16 experts 2048 x 1408, top 4: 533, 526 us; 8192,
-// 16 of them, top 2: 1212, 1201; 1024, 8 of 1024 x 512: 186, 186).  f32 rows of a large call are loaded so too (ONCE): from about 96
-// MiB on they have left the last-level cache (256 MB) since they were written,
-// and loading them there again only pushes out the rest.  Measured with inputs
-// that change from call to call, plain loads and once, tokens of 4096, top 2:
-// combine with dropout of 2048 tokens (64 MiB) 17.5, 19.5 us; 4096: 41, 35;
-// 8192: 77, 65; its gradient 22, 27; 51, 43; 94, 78.  bf16 rows are loaded
-// plainly (4096 tokens of 2048, top 4: 16.4 us, once 29).
+// 16 of them, top 2: 1212, 1201; 1024, 8 of 1024 x 512: 186, 186).  f32 rows of a
+// large call are loaded so too (ONCE): from about 96 MiB on they have left the
+// last-level cache (256 MB) since they were written, and loading them there again
+// only pushes out the rest.  Measured with inputs that change from call to call,
+// plain loads and once, tokens of 4096, top 2: combine with dropout of 2048 tokens
+// (64 MiB) 17.5, 19.5 us; 4096: 41, 35; 8192: 77, 65; its gradient 22, 27; 51, 43; 94,
+// 78.  bf16 rows are loaded plainly (4096 tokens of 2048, top 4: 16.4 us, once 29).
 template <bool ONCE>
 __device__ __forceinline__ float4 load4(const float* p) {
   f32x4_t v;
