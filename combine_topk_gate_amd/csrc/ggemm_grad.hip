@@ -842,23 +842,30 @@ static int64_t wave_tiles(const GradGemmArgs& a, int N) {
 // 14.4, 12.3; 100, 4 of 4096 x 576, top 1 (4096 terms): 32.9, 31.9.
 // bf16: a K step of 64 costs these about 0.2 us a CU (several waves at once) and a
 // wave alone 0.9, a tile four steps' time beside; the large tiles cost 15 us and
-// more but a fifth a step.  Measured (large tiles, these), top 2 of 8 experts, keep:
-// 256 tokens, 256 x 512 (1.5 tiles a CU of 4 steps): 13.1, 7.9; 2048 there (8.5):
-// 18.0, 19.6; 35, 3 of 3968 x 64 (8 tiles, 62 steps): 42, 12.7; 1000, 1024 x 1024 (8.8
-// a CU, 16): 34, 45.  Rows of layer 1: 256, 256 x 512: 14.5, 8.4; 2048 there: 25, 17;
-// 1000, 2048 x 512 (4.4, 32): 39, 34; 512, 16 of 1024 x 1024, top 4 (10, 16): 38, 48;
-// 6265, 44 of 3456 x 64 (3.4, 54): 90, 57; layer 0: 256, 256 x 512 (0.8, 16): 21, 9;
-// 1000, 1024 x 1024 (8.8, 32): 47, 58; 60, one of 448 x 8576 (14 tiles, 268): 34, 36
-// (the large tiles cut into parts).
+// more but a fifth a step, and rows' gradients cut the few of them that a small
+// problem has into parts.  Measured (large tiles, these) at t tiles a CU and s steps.
+// Rows, 8 experts of 512 columns, layer 1: t 1, s 8: 18, 8; 64: 29, 23; 128: 34, 40; t 2.5,
+// 16: 34, 19; 32: 31, 30; 64: 38, 53; t 6.5, 8: 29, 18; 32: 59, 45; t 12.5, 8: 30, 28; 16: 39,
+// 43; t 16.5, 4: 28, 28; 8: 32, 37; layer 0: t 2.5, 32: 30, 28; 64: 36, 52; t 8.5, 8: 20, 19; 16:
+// 28, 28; t 12.5, 8: 20, 23; 128 columns (of fewer than 256 a large tile is partly empty),
+// layer 1: t 1, 64: 36, 26; 128: 44, 47; t 4, 32: 54, 31; 64: 56, 55; t 8, 16: 38, 32; 32: 56, 53; t
+// 12, 8: 31, 31; 64 experts of 16 rows, layer 0: t 6, 8: 16, 18; t 12, 8: 19, 32; 58 of 6 rows, t
+// 9, 4: 22, 17.  So the limits are those of middling problems, and off by up to 40% at
+// t 2 to 3 with 64 steps and at t 12 with many experts.
+// Kept (no parts, so the large tiles are slow where they are few): 2 experts of 256
+// columns, 1024 rows, t 1: s 16: 29, 11; 128: 138, 45; 8 of 512 columns: t 1.5, 64: 65, 37;
+// t 2.5, 16: 30, 20; 128: 154, 117; t 4.5, 8: 22, 19; 32: 48, 47; 64: 82, 89; t 6.5, 4: 18, 17; 8: 23,
+// 23; 16: 31, 35; t 8.5, 1: 14.9, 14.9; 4: 18, 20; 17 of 3328 columns, 9 rows each, t 8.5, 3: 23, 16; 89 of
+// 576, 23 each, t 10.8, 1: 18.5, 15.4; of 128 columns: t 4, 128: 169, 126; t 6, 32: 49, 46; t 8, 16: 32, 36.
 static bool wave_rows(const GradGemmArgs& a, bool bf16, int N, int K, int cus) {
   const int64_t tiles = wave_tiles(a, N), steps = K / kBK;
   if (!bf16) return tiles <= 8 * cus && K <= 2048;
-  // (of fewer than 256 columns a large tile is partly empty)
   return tiles * (steps + 4) <= (N < 256 ? 256 : 170) * cus && steps <= 192;
 }
 static bool wave_keep(const GradGemmArgs& a, bool bf16, int cus) {
   const int64_t tiles = wave_tiles(a, a.F), steps = a.H / kBK;
-  return !bf16 || tiles <= cus || tiles * (steps + 4) <= 64 * cus;
+  // up to 4 1/4 tiles a CU whatever the steps, 6 1/4 for few of them or narrow products; more for the fewest
+  return !bf16 || 4 * tiles <= (steps <= 8 || a.F < 256 ? 25 : 17) * cus || tiles * (steps + 4) <= 64 * cus;
 }
 // Up to a tile a CU 8 waves share one, above 4 (8, 4): layer 0's rows above 11.8,
 // 13.1 us; 512 tokens there (320 tiles): 20.5, 18.8; kept, 21 rows, one of 2112 x 448:
