@@ -45,7 +45,9 @@
  *     in [0, E), and offsets must be the exclusive prefix sum of the counts
  *     of the same call sequence.  Violating these gives unspecified results
  *     (the kernels keep every memory access inside the caller's buffers: an
- *     out-of-range expert id or source block makes its pair a dropped one).
+ *     out-of-range expert id or source block makes its pair a dropped one, and
+ *     the grouped GEMMs keep their segments inside the rows whatever the
+ *     offsets say).
  *   - MOE_DEBUG_VALIDATE=1 in the environment makes every entry point check
  *     those device-resident inputs before it launches anything: it copies
  *     them to host memory (synchronising `stream`) and returns
