@@ -107,7 +107,9 @@ inline unsigned token_blocks(int64_t M, int tpt) {
 // weight, and only those held are gone through, in slot order (a share of an
 // expert-parallel layer holds few: 16 of 128 experts, 4096 tokens of 7168, 8 pairs
 // each, all gone through and so: combine with dropout 76, 52 us, its gradient 78,
-// 50, the dispatch's 41, 32).
+// 50, the dispatch's 41, 32).  A wave reads other lanes' pairs while some of its lanes
+// are past the row's end; the lanes that hold pairs (at most 16) never are, as a row
+// has a multiple of 16 groups of four columns.
 struct TokenPairs {
   int32_t row;  // of lane j
   float w;
